@@ -21,6 +21,12 @@ DSA_LAYER_FULL = 1
 DSA_IDX_ROPE_Q = 1 << 0
 DSA_IDX_ROPE_K = 1 << 1
 DSA_IDX_INDEPENDENT_ROWS = 1 << 2
+DSA_ROPE_SCALE_NONE, DSA_ROPE_SCALE_LINEAR, DSA_ROPE_SCALE_YARN = 0, 1, 2
+DSA_BF16, DSA_F32 = 0, 1
+DSA_ROPE_INTERLEAVED = 1 << 0
+DSA_ROPE_INVERSE = 1 << 1
+DSA_CACHE_BF16, DSA_CACHE_FP8 = 0, 1
+DSA_CACHE_ROPE = 1 << 8
 
 STATUS_NAMES = {0: "DSA_OK", 1: "DSA_ERR_ARG", 2: "DSA_ERR_SHAPE", 3: "DSA_ERR_NO_DONOR", 4: "DSA_ERR_UNSUPPORTED",
                 5: "DSA_ERR_CUDA", 6: "DSA_ERR_WORKSPACE", 7: "DSA_ERR_TIMEOUT", 8: "DSA_ERR_DEVICE"}
@@ -32,10 +38,12 @@ EXPORTED = ("dsa_status_string", "dsa_last_error", "dsa_donor_table", "dsa_rope_
             "dsa_indexer_topk_paged", "dsa_sparse_attn_paged", "dsa_indexer_projections", "dsa_sparse_attn_backward",
             "dsa_indexer_static_status", "dsa_profile_read", "dsa_debug_pipeline",
             "dsa_indexer_backward_workspace_size", "dsa_indexer_backward",
-            "dsa_sparse_attn_backward_workspace_size")
+            "dsa_sparse_attn_backward_workspace_size", "dsa_rope_table_scaled", "dsa_rope_apply",
+            "dsa_latent_cache_write", "dsa_latent_cache_read", "dsa_latent_attn_workspace_size",
+            "dsa_latent_attn_paged")
 
 PROFILE_KINDS = {0: "rope", 1: "ranges", 2: "indexer", 3: "select", 4: "attn_prep", 5: "attn", 6: "attn_bwd",
-                 7: "proj", 8: "indexer_bwd"}
+                 7: "proj", 8: "indexer_bwd", 9: "cache"}
 
 
 class DsaError(RuntimeError):
@@ -62,6 +70,28 @@ class ProfileRecord(C.Structure):
 class LayerIO(C.Structure):
     _fields_ = [("q_idx", C.c_void_p), ("k_idx", C.c_void_p), ("w", C.c_void_p), ("q", C.c_void_p),
                 ("kv", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p)]
+
+
+class RopeScaling(C.Structure):
+    """dsa_rope_scaling: a scaled RoPE table (see rope_scaling_linear and rope_scaling_yarn)."""
+    _fields_ = [("kind", C.c_int32), ("orig_len", C.c_int32), ("factor", C.c_double), ("beta_fast", C.c_double),
+                ("beta_slow", C.c_double), ("mscale", C.c_double)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("n_tokens", C.c_int32), ("n_heads", C.c_int32), ("rope_dim", C.c_int32), ("dtype", C.c_int32),
+                ("x_token_stride", C.c_int64), ("x_head_stride", C.c_int64), ("out_token_stride", C.c_int64),
+                ("out_head_stride", C.c_int64), ("flags", C.c_uint32)]
+
+
+class LatentCache(C.Structure):
+    """dsa_latent_cache (see latent_cache)."""
+    _fields_ = [("latent", C.c_void_p), ("scale", C.c_void_p), ("rope", C.c_void_p), ("n_rows", C.c_int32),
+                ("format", C.c_int32)]
+
+
+class CacheWriteDesc(C.Structure):
+    _fields_ = [("n_tokens", C.c_int32), ("flags", C.c_uint32), ("kv_stride", C.c_int64)]
 
 
 _lib: Optional[C.CDLL] = None
@@ -136,6 +166,18 @@ def lib() -> C.CDLL:
         L.dsa_mtp_indexshare_step.restype = st
         L.dsa_mtp_indexshare_step.argtypes = [P(IndexerDesc), P(AttnDesc), i32, P(LayerIO), vp, vp, vp, vp, vp, i32,
                                               vp, vp, sz, vp]
+        L.dsa_rope_table_scaled.restype = st
+        L.dsa_rope_table_scaled.argtypes = [C.c_double, i32, i32, P(RopeScaling), P(C.c_float)]
+        L.dsa_rope_apply.restype = st
+        L.dsa_rope_apply.argtypes = [P(RopeDesc), vp, vp, vp, i32, vp, vp, sz, vp]
+        L.dsa_latent_cache_write.restype = st
+        L.dsa_latent_cache_write.argtypes = [P(CacheWriteDesc), vp, vp, vp, vp, i32, P(LatentCache), vp, sz, vp]
+        L.dsa_latent_cache_read.restype = st
+        L.dsa_latent_cache_read.argtypes = [P(LatentCache), P(PagedCache), i32, vp, vp, i32, vp, sz, vp]
+        L.dsa_latent_attn_workspace_size.restype = st
+        L.dsa_latent_attn_workspace_size.argtypes = [P(AttnDesc), P(sz)]
+        L.dsa_latent_attn_paged.restype = st
+        L.dsa_latent_attn_paged.argtypes = [P(AttnDesc), vp, P(LatentCache), vp, P(PagedCache), vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -461,6 +503,162 @@ def dsa_sparse_attn_paged(desc: AttnDesc, q, kv_cache, idx, pages: PagedCache, o
     if ws is None:
         ws = torch.empty(dsa_sparse_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
     _check(lib().dsa_sparse_attn_paged(C.byref(desc), _ptr(q), _ptr(kv_cache), _ptr(idx), C.byref(pages), _ptr(out),
+                                       _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    return ws
+
+
+# ------------------------------------------------------------------------------ rotary positions
+
+def rope_scaling_linear(factor: float, mscale: float = 1.0) -> RopeScaling:
+    """Position interpolation: every frequency divided by factor."""
+    return RopeScaling(DSA_ROPE_SCALE_LINEAR, 0, float(factor), 0.0, 0.0, float(mscale))
+
+
+def rope_scaling_yarn(factor: float, orig_len: int, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                      mscale: float = 1.0) -> RopeScaling:
+    """YaRN: frequencies that turn often within orig_len kept, slow ones divided by factor."""
+    return RopeScaling(DSA_ROPE_SCALE_YARN, int(orig_len), float(factor), float(beta_fast), float(beta_slow),
+                       float(mscale))
+
+
+def dsa_rope_table_scaled(theta: float, rope_dim: int, n_pos: int, scaling: Optional[RopeScaling] = None) -> torch.Tensor:
+    """Host float32 tensor [n_pos, rope_dim/2, 2] of (cos, sin), scaled for long contexts."""
+    out = torch.empty((max(n_pos, 0), max(rope_dim // 2, 1), 2), dtype=torch.float32)
+    _check(lib().dsa_rope_table_scaled(float(theta), int(rope_dim), int(n_pos), C.byref(scaling) if scaling else None,
+                                       C.cast(out.data_ptr(), C.POINTER(C.c_float))))
+    return out
+
+
+def _heads_view(t: torch.Tensor, name: str):
+    """(token stride, head stride) of a [tokens, heads, rope_dim] view whose last dim is contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected a [tokens, heads, rope_dim] view, got {t.dim()} dims")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the rotary dims of a head must be contiguous")
+    return t.stride(0), t.stride(1)
+
+
+def rope_desc(x: torch.Tensor, out: torch.Tensor, flags: int = 0) -> RopeDesc:
+    """Descriptor for turning x into out, [tokens, heads, rope_dim] views (slices of wider heads are
+    fine; `out` may be `x`).  It holds for every pair of views of these shapes, strides and type."""
+    if x.shape != out.shape or x.dtype != out.dtype:
+        raise ValueError("x and out must have the same shape and dtype")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
+    xs, os_ = _heads_view(x, "x"), _heads_view(out, "out")
+    return RopeDesc(x.shape[0], x.shape[1], x.shape[2], DSA_F32 if x.dtype == torch.float32 else DSA_BF16, xs[0], xs[1],
+                    os_[0], os_[1], flags)
+
+
+def dsa_rope_apply(desc: RopeDesc, x, pos, rope_cs, out, ws=None, stream=None) -> torch.Tensor:
+    """out = x turned at pos (DSA_ROPE_INVERSE: by the negated angle, the gradient), [tokens, heads,
+    rope_dim] views as the descriptor was made for."""
+    dt = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16
+    shape = (desc.n_tokens, desc.n_heads, desc.rope_dim)
+    for t, st, name in ((x, (desc.x_token_stride, desc.x_head_stride), "x"),
+                        (out, (desc.out_token_stride, desc.out_head_stride), "out")):
+        if t.dtype != dt or t.shape != shape or not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA {dt} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+        if _heads_view(t, name) != st:
+            raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's {st}")
+    _want(pos, torch.int32, desc.n_tokens, "pos")
+    n_pos = _rope_rows(rope_cs, desc.rope_dim)
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=out.device)
+    _check(lib().dsa_rope_apply(C.byref(desc), x.data_ptr(), _ptr(pos), _ptr(rope_cs), n_pos, out.data_ptr(), _ptr(ws),
+                                ws.numel(), _stream(stream)))
+    return ws
+
+
+def _rope_rows(rope_cs: torch.Tensor, rope_dim: int) -> int:
+    """Positions of a (cos, sin) table for rope_dim rotary dims."""
+    if rope_cs.dtype != torch.float32 or rope_cs.dim() != 3 or rope_cs.shape[1:] != (rope_dim // 2, 2):
+        raise ValueError(f"rope_cs: expected a float32 [positions, {rope_dim // 2}, 2] tensor, got {rope_cs.dtype} "
+                         f"{tuple(rope_cs.shape)}")
+    return rope_cs.shape[0]
+
+
+# ------------------------------------------------------------------------------ latent cache
+
+def latent_cache(latent: torch.Tensor, scale: Optional[torch.Tensor] = None,
+                 rope: Optional[torch.Tensor] = None) -> LatentCache:
+    """A latent cache over the caller's tensors (kept alive by the caller): bf16 [n_rows, 576] alone,
+    or fp8: codes [n_rows, 512] (uint8 or float8_e4m3fn), scale uint8 [n_rows, 4], rope bf16 [n_rows, 64]."""
+    n = latent.shape[0]
+    if scale is None and rope is None:
+        if latent.dtype != torch.bfloat16 or latent.shape != (n, 576):
+            raise ValueError(f"latent: expected bf16 [n_rows, 576], got {latent.dtype} {tuple(latent.shape)}")
+        return LatentCache(_ptr(latent), None, None, n, DSA_CACHE_BF16)
+    if latent.dtype not in (torch.uint8, torch.float8_e4m3fn) or latent.shape != (n, 512):
+        raise ValueError(f"latent: expected e4m3 codes [n_rows, 512], got {latent.dtype} {tuple(latent.shape)}")
+    if scale is None or scale.dtype != torch.uint8 or scale.shape != (n, 4):
+        raise ValueError("scale: expected uint8 [n_rows, 4]")
+    if rope is None or rope.dtype != torch.bfloat16 or rope.shape != (n, 64):
+        raise ValueError("rope: expected bf16 [n_rows, 64]")
+    return LatentCache(_ptr(latent), _ptr(scale), _ptr(rope), n, DSA_CACHE_FP8)
+
+
+def cache_write_desc(kv: torch.Tensor, flags: int = 0) -> CacheWriteDesc:
+    """Descriptor for storing kv, a [tokens, 576] bf16 view with contiguous rows."""
+    if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != 576 or kv.stride(1) != 1:
+        raise ValueError("kv: expected a bf16 [tokens, 576] view with contiguous rows")
+    return CacheWriteDesc(kv.shape[0], flags, kv.stride(0) if kv.shape[0] > 1 else max(576, kv.stride(0)))
+
+
+def dsa_latent_cache_write(desc: CacheWriteDesc, kv, slot, pos, rope_cs, cache: LatentCache, ws=None,
+                           stream=None) -> torch.Tensor:
+    """Store kv's rows in cache rows slot (negative: none), turned at pos with DSA_CACHE_ROPE."""
+    n = desc.n_tokens
+    if kv.dtype != torch.bfloat16 or kv.shape != (n, 576) or kv.stride(1) != 1 or not kv.is_cuda:
+        raise ValueError(f"kv: expected a CUDA bf16 [{n}, 576] view with contiguous rows")
+    if n > 1 and kv.stride(0) != desc.kv_stride:
+        raise ValueError(f"kv: token stride {kv.stride(0)} is not the descriptor's {desc.kv_stride}")
+    _want(slot, torch.int32, n, "slot")
+    n_pos = 0
+    if desc.flags & DSA_CACHE_ROPE:
+        _want(pos, torch.int32, n, "pos")
+        n_pos = _rope_rows(rope_cs, 64)
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=kv.device)
+    _check(lib().dsa_latent_cache_write(C.byref(desc), kv.data_ptr(), _ptr(slot), _ptr(pos), _ptr(rope_cs), n_pos,
+                                        C.byref(cache), _ptr(ws), ws.numel(), _stream(stream)))
+    return ws
+
+
+def dsa_latent_cache_read(cache: LatentCache, pages: PagedCache, n_seq: int, row_start, kv_out, ws=None,
+                          stream=None) -> torch.Tensor:
+    """kv_out[row_start[t] + j] = row j of sequence t for every cached row of n_seq sequences, bf16."""
+    _paged_args(pages)
+    _want(row_start, torch.int32, n_seq, "row_start")
+    if kv_out.dtype != torch.bfloat16 or kv_out.dim() != 2 or kv_out.shape[1] != 576:
+        raise ValueError(f"kv_out: expected bf16 [rows, 576], got {kv_out.dtype} {tuple(kv_out.shape)}")
+    if ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=kv_out.device)
+    _check(lib().dsa_latent_cache_read(C.byref(cache), C.byref(pages), int(n_seq), _ptr(row_start), _ptr(kv_out),
+                                       kv_out.shape[0], _ptr(ws), ws.numel(), _stream(stream)))
+    return ws
+
+
+def dsa_latent_attn_workspace_size(desc: AttnDesc) -> int:
+    n = C.c_size_t(0)
+    _check(lib().dsa_latent_attn_workspace_size(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def dsa_latent_attn_paged(desc: AttnDesc, q, cache: LatentCache, idx, pages: PagedCache, out, lse=None, ws=None,
+                          stream=None) -> torch.Tensor:
+    """Latent attention of row t over its sequence's cached keys: all of them (idx None) or the
+    selected ones."""
+    n_q, H = desc.n_q, desc.n_heads
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    for t, dt, n, name in ((q, bf, n_q * H * desc.d_qk, "q"), (idx, i32, n_q * desc.topk, "idx"),
+                           (out, bf, n_q * H * desc.d_v, "out"), (lse, f32, n_q * H, "lse")):
+        if t is not None:
+            _want(t, dt, n, name)
+    _paged_args(pages)
+    if ws is None:
+        ws = torch.empty(dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
+    _check(lib().dsa_latent_attn_paged(C.byref(desc), _ptr(q), C.byref(cache), _ptr(idx), C.byref(pages), _ptr(out),
                                        _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
     return ws
 

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstring>
 #include <atomic>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <string>
@@ -791,6 +792,220 @@ dsa_status dsa_sparse_attn_paged(const dsa_attn_desc* desc, const void* q, const
   if ((s = check_pages(pages, desc->n_kv, &pg)) != DSA_OK) return s;
   return run_attn(desc, q, kv_cache, idx, nullptr, out, lse, ws, ws_bytes, static_cast<cudaStream_t>(stream), true,
                   nullptr, &pg);
+}
+
+dsa_status dsa_rope_table_scaled(double theta, int32_t rope_dim, int32_t n_pos, const dsa_rope_scaling* sc,
+                                 float* host_out) {
+  if (!sc) return dsa_rope_table(theta, rope_dim, n_pos, host_out);
+  if (!host_out || rope_dim < 0 || (rope_dim & 1) || n_pos < 1 || !(theta > 0.0) || !std::isfinite(theta))
+    return fail(DSA_ERR_ARG, "rope table: bad theta/rope_dim/n_pos or NULL output");
+  if (sc->kind < DSA_ROPE_SCALE_NONE || sc->kind > DSA_ROPE_SCALE_YARN)
+    return fail(DSA_ERR_ARG, "rope scaling kind %d", sc->kind);
+  if (!(sc->mscale > 0.0) || !std::isfinite(sc->mscale)) return fail(DSA_ERR_ARG, "rope scaling: mscale must be > 0");
+  if (sc->kind != DSA_ROPE_SCALE_NONE && (!(sc->factor >= 1.0) || !std::isfinite(sc->factor)))
+    return fail(DSA_ERR_ARG, "rope scaling: factor must be >= 1");
+  const int half = rope_dim / 2;
+  double lo = 0.0, hi = 0.0;
+  if (sc->kind == DSA_ROPE_SCALE_YARN) {
+    if (sc->orig_len < 1 || !(theta > 1.0) || !(sc->beta_slow > 0.0) || !(sc->beta_fast >= sc->beta_slow) ||
+        !std::isfinite(sc->beta_fast))
+      return fail(DSA_ERR_ARG, "YaRN scaling: needs orig_len >= 1, theta > 1 and beta_fast >= beta_slow > 0");
+    const auto dim_of = [&](double turns) {
+      return rope_dim * std::log(sc->orig_len / (turns * 6.283185307179586476925)) / (2.0 * std::log(theta));
+    };
+    lo = std::max(0.0, std::floor(dim_of(sc->beta_fast)));
+    hi = std::min(rope_dim - 1.0, std::ceil(dim_of(sc->beta_slow)));
+  }
+  std::unique_ptr<double[]> inv(new (std::nothrow) double[half > 0 ? half : 1]);
+  if (!inv) return fail(DSA_ERR_ARG, "rope table: out of host memory");
+  for (int i = 0; i < half; ++i) {
+    const double f = std::pow(theta, -2.0 * i / rope_dim);
+    double r = sc->kind == DSA_ROPE_SCALE_LINEAR ? 1.0 : 0.0;
+    if (sc->kind == DSA_ROPE_SCALE_YARN) r = hi > lo ? std::min(1.0, std::max(0.0, (i - lo) / (hi - lo))) : (i > lo ? 1.0 : 0.0);
+    inv[i] = r == 0.0 ? f : f * (1.0 - r) + f / sc->factor * r;
+  }
+  for (int64_t p = 0; p < n_pos; ++p) {
+    float* row = host_out + p * rope_dim;
+    for (int i = 0; i < half; ++i) {
+      const double a = static_cast<double>(p) * inv[i];
+      row[2 * i] = static_cast<float>(std::cos(a) * sc->mscale);
+      row[2 * i + 1] = static_cast<float>(std::sin(a) * sc->mscale);
+    }
+  }
+  return DSA_OK;
+}
+
+namespace {
+// Common to the cache calls: a workspace for the status header, cleared on the stream.
+dsa_status check_status_ws(const void* ws, size_t ws_bytes) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be non-NULL and 256-byte aligned");
+  if (ws_bytes < kAlign) return fail(DSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, kAlign);
+  return DSA_OK;
+}
+
+dsa_status check_cache(const dsa_latent_cache* c, LatentCache* out) {
+  if (!c) return fail(DSA_ERR_ARG, "latent cache is NULL");
+  if (c->format != DSA_CACHE_BF16 && c->format != DSA_CACHE_FP8) return fail(DSA_ERR_ARG, "latent cache format %d", c->format);
+  const bool fp8 = c->format == DSA_CACHE_FP8;
+  if (!c->latent || (fp8 && (!c->scale || !c->rope)))
+    return fail(DSA_ERR_ARG, "latent cache: latent (fp8: and scale, rope) must be non-NULL");
+  if (!aligned16(c->latent) || (fp8 && (!aligned16(c->scale) || !aligned16(c->rope))))
+    return fail(DSA_ERR_ARG, "latent cache arrays must be 16-byte aligned");
+  if (c->n_rows < kPageRows || c->n_rows % kPageRows)
+    return fail(DSA_ERR_SHAPE, "latent cache: n_rows %d must be whole pages of %d rows", c->n_rows, kPageRows);
+  *out = LatentCache{static_cast<uint8_t*>(c->latent), c->scale, static_cast<uint16_t*>(c->rope), c->n_rows, fp8};
+  return DSA_OK;
+}
+}  // namespace
+
+dsa_status dsa_rope_apply(const dsa_rope_desc* d, const void* x, const int32_t* pos, const float* rope_cs,
+                          int32_t rope_n_pos, void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!d) return fail(DSA_ERR_ARG, "rope descriptor is NULL");
+  if (d->n_tokens < 0 || d->n_heads < 1) return fail(DSA_ERR_ARG, "n_tokens must be >= 0 and n_heads >= 1");
+  if (d->rope_dim < 2 || d->rope_dim > 512 || (d->rope_dim & 1))
+    return fail(DSA_ERR_ARG, "rope_dim %d must be even and within 2..512", d->rope_dim);
+  if (d->dtype != DSA_BF16 && d->dtype != DSA_F32) return fail(DSA_ERR_ARG, "rope dtype %d", d->dtype);
+  if (d->flags & ~(DSA_ROPE_INTERLEAVED | DSA_ROPE_INVERSE)) return fail(DSA_ERR_ARG, "unknown rope flags 0x%x", d->flags);
+  if (d->x_token_stride < 0 || d->x_head_stride < 0 || d->out_token_stride < 0 || d->out_head_stride < 0)
+    return fail(DSA_ERR_ARG, "rope strides must be >= 0");
+  if ((d->n_tokens > 1 && d->out_token_stride < d->rope_dim) || (d->n_heads > 1 && d->out_head_stride < d->rope_dim))
+    return fail(DSA_ERR_ARG, "out's strides must be at least rope_dim");
+  if (static_cast<long long>(d->n_tokens) * d->n_heads > 0x7FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_tokens * n_heads exceeds the int32 range");
+  if (x == out && (d->x_token_stride != d->out_token_stride || d->x_head_stride != d->out_head_stride))
+    return fail(DSA_ERR_ARG, "in place, x and out need the same strides");
+  dsa_status s;
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  if (d->n_tokens == 0) return DSA_OK;
+  if (!x || !out || !pos || !rope_cs || rope_n_pos < 1) return fail(DSA_ERR_ARG, "x, pos, rope_cs and out must be non-NULL");
+  const uintptr_t el = d->dtype == DSA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % el || reinterpret_cast<uintptr_t>(out) % el)
+    return fail(DSA_ERR_ARG, "x and out must be aligned to their elements");
+  if (!aligned16(rope_cs)) return fail(DSA_ERR_ARG, "rope_cs must be 16-byte aligned");
+  if ((s = check_device()) != DSA_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
+  const RopeApply a{x, out, d->n_tokens, d->n_heads, d->rope_dim, d->x_token_stride, d->x_head_stride,
+                    d->out_token_stride, d->out_head_stride, d->dtype == DSA_F32,
+                    (d->flags & DSA_ROPE_INTERLEAVED) != 0, (d->flags & DSA_ROPE_INVERSE) != 0};
+  const int ps = prof_begin(kProfCache, st);
+  e = launch_rope_apply(a, pos, rope_cs, rope_n_pos, static_cast<uint32_t*>(ws), st);
+  prof_end(ps, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "rotary positions kernel");
+}
+
+dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* d, const void* kv, const int32_t* slot,
+                                  const int32_t* pos, const float* rope_cs, int32_t rope_n_pos,
+                                  const dsa_latent_cache* cache, void* ws, size_t ws_bytes, void* stream) {
+  if (!d) return fail(DSA_ERR_ARG, "cache write descriptor is NULL");
+  if (d->n_tokens < 0) return fail(DSA_ERR_ARG, "n_tokens must be >= 0");
+  if (d->flags & ~(DSA_CACHE_ROPE | DSA_ROPE_INTERLEAVED)) return fail(DSA_ERR_ARG, "unknown cache write flags 0x%x", d->flags);
+  if (d->kv_stride < 576 || d->kv_stride % 8)
+    return fail(DSA_ERR_ARG, "kv_stride %lld must be a multiple of 8, at least 576", static_cast<long long>(d->kv_stride));
+  dsa_status s;
+  LatentCache c;
+  if ((s = check_cache(cache, &c)) != DSA_OK) return s;
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  if (d->n_tokens == 0) return DSA_OK;
+  const bool rot = (d->flags & DSA_CACHE_ROPE) != 0;
+  if (!kv || !slot || (rot && (!pos || !rope_cs || rope_n_pos < 1)))
+    return fail(DSA_ERR_ARG, "kv, slot (DSA_CACHE_ROPE: and pos, rope_cs) must be non-NULL");
+  if (!aligned16(kv)) return fail(DSA_ERR_ARG, "kv must be 16-byte aligned");
+  if (rot && !aligned16(rope_cs)) return fail(DSA_ERR_ARG, "rope_cs must be 16-byte aligned");
+  if ((s = check_device()) != DSA_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
+  const int ps = prof_begin(kProfCache, st);
+  e = launch_cache_write(c, kv, d->kv_stride, slot, pos, rot ? rope_cs : nullptr, rope_n_pos, d->n_tokens,
+                         (d->flags & DSA_ROPE_INTERLEAVED) != 0, static_cast<uint32_t*>(ws), st);
+  prof_end(ps, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "cache write kernel");
+}
+
+dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_cache* pages, int32_t n_seq,
+                                 const int32_t* row_start, void* kv_out, int32_t n_out, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  dsa_status s;
+  LatentCache c;
+  if ((s = check_cache(cache, &c)) != DSA_OK) return s;
+  PagedRows pg;
+  if ((s = check_pages(pages, c.n_rows, &pg)) != DSA_OK) return s;
+  if (n_seq < 0 || n_out < 0) return fail(DSA_ERR_ARG, "n_seq and n_out must be >= 0");
+  if (static_cast<long long>(n_seq) * pg.max_pages > 0x7FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_seq * max_pages exceeds the int32 range");
+  if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  if (n_seq == 0) return DSA_OK;
+  if (!row_start || !kv_out) return fail(DSA_ERR_ARG, "row_start and kv_out must be non-NULL");
+  if (!aligned16(kv_out)) return fail(DSA_ERR_ARG, "kv_out must be 16-byte aligned");
+  if ((s = check_device()) != DSA_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
+  const int ps = prof_begin(kProfCache, st);
+  e = launch_cache_read(c, pg, n_seq, row_start, n_out, kv_out, static_cast<uint32_t*>(ws), st);
+  prof_end(ps, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "cache read kernel");
+}
+
+namespace {
+// desc->topk counts only where an index is given.
+dsa_attn_desc latent_desc(const dsa_attn_desc* d, bool selected) {
+  dsa_attn_desc c = *d;
+  if (!selected && c.topk < 1) c.topk = 1;
+  return c;
+}
+}  // namespace
+
+dsa_status dsa_latent_attn_workspace_size(const dsa_attn_desc* desc, size_t* bytes) {
+  if (!desc) return fail(DSA_ERR_ARG, "attention descriptor is NULL");
+  if (!bytes) return fail(DSA_ERR_ARG, "bytes is NULL");
+  const dsa_attn_desc d = latent_desc(desc, false);
+  dsa_status s = check_attn_desc(&d);
+  if (s != DSA_OK) return s;
+  // enough for either cache and either walk of this descriptor
+  *bytes = std::max(attn_ws_bytes(&d), kAlign + align_up(latent_attn_ws_bytes(d.n_q, d.n_heads)));
+  return DSA_OK;
+}
+
+dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
+                                 const int32_t* idx, const dsa_paged_cache* pages, void* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  if (!desc) return fail(DSA_ERR_ARG, "attention descriptor is NULL");
+  const dsa_attn_desc d = latent_desc(desc, idx != nullptr);
+  dsa_status s = check_attn_desc(&d);
+  if (s != DSA_OK) return s;
+  LatentCache c;
+  if ((s = check_cache(cache, &c)) != DSA_OK) return s;
+  PagedRows pg;
+  if ((s = check_pages(pages, d.n_kv, &pg)) != DSA_OK) return s;
+  if (c.n_rows != d.n_kv) return fail(DSA_ERR_SHAPE, "n_kv %d must equal the cache's n_rows %d", d.n_kv, c.n_rows);
+  if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
+  if (static_cast<long long>(d.n_q) * d.n_heads > 0x7FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_q * n_heads exceeds the int32 range");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (idx && !c.fp8)   // selected rows of a bf16 cache: the sparse kernel's gather walk
+    return run_attn(&d, q, c.latent, idx, nullptr, out, lse, ws, ws_bytes, st, true, nullptr, &pg);
+  if (d.n_q == 0) return DSA_OK;
+  if (!q || !out || !ws) return fail(DSA_ERR_ARG, "q, out and ws must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_ARG, "q and out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be 256-byte aligned");
+  if ((s = check_device()) != DSA_OK) return s;
+  const size_t need = kAlign + align_up(latent_attn_ws_bytes(d.n_q, d.n_heads));
+  if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "attention workspace too small: %zu < %zu bytes", ws_bytes, need);
+  CUtensorMap tkv, tq;
+  std::memset(&tkv, 0, sizeof(tkv));
+  if (!c.fp8 && (s = tmap_kv_tiles(&tkv, c.latent, static_cast<uint64_t>(c.n_rows))) != DSA_OK) return s;
+  if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
+                     static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)
+    return s;
+  cudaError_t e;
+  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
+  e = launch_latent_attn(c, tkv, tq, pg, idx, d.n_q, d.n_heads, d.topk, d.softmax_scale, out, lse,
+                         static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "latent attention kernel");
 }
 
 dsa_status dsa_indexer_projections(const dsa_proj_desc* d, const void* x, const void* q_latent, const void* wq_b,

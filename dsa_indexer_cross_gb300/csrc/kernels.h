@@ -221,6 +221,45 @@ cudaError_t launch_sparse_attn_bwd_dense(int hd, const CUtensorMap& tmap_kv, con
                                          const void* dout, float* dq, float* dkv, uint32_t* status, float* delta,
                                          void* scratch, cudaStream_t st);
 
+// ---------------------------------------------------------------------------- latent cache
+// out[t, h, :rope] = the rotary dims x[t, h, :rope] turned at pos[t] (strides in elements).
+struct RopeApply {
+  const void* x;
+  void* out;
+  int n_tokens, n_heads, rope;
+  long long x_tok, x_head, o_tok, o_head;
+  bool f32, interleaved, inverse;
+};
+cudaError_t launch_rope_apply(const RopeApply& a, const int32_t* pos, const float* cs, int n_pos, uint32_t* status,
+                              cudaStream_t st);
+
+// A latent cache: bf16 rows of 576 in latent, or (fp8) e4m3 codes [n_rows][512] in latent, scale
+// bytes [n_rows][4] and bf16 rotary dims [n_rows][64].
+struct LatentCache {
+  uint8_t* latent;
+  uint8_t* scale;
+  uint16_t* rope;
+  int n_rows;
+  bool fp8;
+};
+// Row kv + t * kv_stride -> cache row slot[t] (negative: not stored); cs != nullptr turns the last
+// 64 dims at pos[t].
+cudaError_t launch_cache_write(const LatentCache& c, const void* kv, long long kv_stride, const int32_t* slot,
+                               const int32_t* pos, const float* cs, int n_pos, int n_tokens, bool interleaved,
+                               uint32_t* status, cudaStream_t st);
+// Every row j < seq_len[t] of n_seq sequences -> out row row_start[t] + j, bf16.
+cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_seq, const int32_t* row_start, int n_out,
+                              void* out, uint32_t* status, cudaStream_t st);
+
+// Latent attention over a paged cache: every key of row t's sequence (idx == nullptr), or the
+// offsets in idx [n_q][topk] (fp8 cache).  tmap_kv: bf16 cache as 64-row tiles (boxes {64, 64, 9});
+// tmap_q: q as [n_q * n_heads][576], boxes {64, latent_attn_q_box_rows(n_heads)}.
+int latent_attn_q_box_rows(int n_heads);
+size_t latent_attn_ws_bytes(int n_q, int n_heads);
+cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_q,
+                               const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
+                               void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
+
 int device_sm_count();
 
 // ---------------------------------------------------------------------------- launch log
@@ -230,7 +269,7 @@ int device_sm_count();
 // do nothing.  prof_begin returns the record's slot (-1 when nothing is recorded).
 enum ProfKind : int {
   kProfRope = 0, kProfRanges = 1, kProfIndexer = 2, kProfSelect = 3, kProfAttnPrep = 4, kProfAttn = 5,
-  kProfAttnBwd = 6, kProfProj = 7, kProfIndexerBwd = 8
+  kProfAttnBwd = 6, kProfProj = 7, kProfIndexerBwd = 8, kProfCache = 9
 };
 int prof_begin(int kind, cudaStream_t st);
 void prof_end(int slot, cudaStream_t st);

@@ -1,0 +1,953 @@
+// Latent attention of one query row per sequence over a paged latent cache (bf16 or fp8): every
+// cached key of the sequence, or the keys an index row selects (fp8), on tcgen05.
+//
+//   o[t, h] = sum_j softmax_j(tau * q[t, h] . kv_j) * kv_j[:512]      kv_j: row j of sequence t
+//
+// All heads of a row read the same latent rows, so the work is a stream of rows with two small
+// products on top.  Formulation as in the sparse kernel: a CTA owns HB columns (heads) and walks
+// the rows in 64-row tiles, both products run with the rows on the M side,
+//     S^T[r, c]  = Rows[r, :576] . Q[c, :576]            M = 64 rows,   N = HB, K = 576
+//     O^T[d, c] += Rows[:, d]^T  . P^T[r, c]             M = 128 dims,  N = HB, K = 64
+// and a tile lies once in shared memory, as nine 64-dim blocks in the 128-byte swizzle, K-major
+// for the first product and MN-major for the second.  O^T (512 x HB fp32) stays in TMEM.
+//
+// Split over the length.  The tiles of all sequences form one line; each of the G groups of CTAs
+// (a group is one CTA per block of HB heads) takes an equal share of consecutive tiles, whatever
+// the lengths are: sequences that lie inside a share are finished there, the others leave
+// unnormalised partials (fp32 O, the max in use, both sums) that a second kernel joins.  The
+// lengths are device data: every CTA finds its share from a block scan over them.
+//
+// How rows arrive.  bf16: one 3-D TMA box per tile (half a page).  fp8: producer warps load codes
+// into registers one tile ahead, convert and store the bf16 tile; power-of-two scales make that
+// exact.  Rows past the sequence's end, or on a page outside the cache, are written as zeros
+// before the products (an uninitialised page may hold NaN, which a zero weight does not cancel).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kRows = 64;
+constexpr int kDqk = 576;
+constexpr int kDv = 512;
+constexpr int kKB = kDqk / 64;
+constexpr int kBlkBytes = kRows * 128;
+constexpr int kTileBytes = kKB * kBlkBytes;
+constexpr int kPrefetch = 4;           // tiles between a tile's L2 prefetch and its load
+constexpr int kMinTiles = 2;           // a share holds at least this many tiles
+
+template <int HB, bool FP8>
+struct LCfg {
+  static constexpr int Q_BYTES = HB * kDqk * 2;
+  static constexpr int DYN_SMEM = 1024 + 2 * kTileBytes + Q_BYTES;
+  static constexpr int SW = HB >= 32 ? 8 : 4;          // softmax warps
+  static constexpr int SOFT = 32 * SW;
+  static constexpr int NP = FP8 ? 4 : 1;               // producer warps
+  static constexpr int S_WARP = SW + NP;
+  static constexpr int PV_WARP = S_WARP + 1;
+  static constexpr int THREADS = 32 * (SW + NP + 2);
+  static constexpr int CW = HB / (SW / 4);             // columns per softmax warp
+  static constexpr int NR = CW / 8;
+  static constexpr uint32_t TMEM_COLS = 6 * HB <= 128 ? 128 : 6 * HB <= 256 ? 256 : 512;
+  static constexpr int S_COL = 4 * HB;
+  static_assert(HB % 16 == 0 && HB <= 64 && CW % 16 == 0, "columns");
+};
+
+struct LShared {
+  uint64_t full[2], empty[2];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, o_done[2], o_free, mma_done;
+  uint32_t tmem_base, abort_flag, soft_abort;
+  int row0, tile0;
+  long long wsum[32];
+  alignas(16) float red[4][64];
+  alignas(16) float red2[4][64];
+  alignas(16) float m_used[64];
+  alignas(16) float l_run[64];
+  alignas(16) float l_sum[64];
+  alignas(16) float alpha[64];
+};
+static_assert(LCfg<64, true>::DYN_SMEM + sizeof(LShared) <= 232448, "HB = 64 must fit in shared memory");
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.or.pred po, %2, %3, pi;\n selp.u32 %0, 1, 0, po;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ldg_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void lrow16(float (&r)[16], const float* p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+    r[4 * i] = v.x;
+    r[4 * i + 1] = v.y;
+    r[4 * i + 2] = v.z;
+    r[4 * i + 3] = v.w;
+  }
+}
+
+struct LArgs {
+  const uint8_t* latent;       // bf16 rows (unused by the kernel: TMA), or e4m3 codes
+  const uint8_t* scale;
+  const uint16_t* rope;
+  const int32_t* idx;          // selected offsets [n_q][topk], or nullptr
+  const int32_t* row_nt;       // SEL: 64-slot tiles of each row
+  PagedRows pg;
+  uint16_t* out;
+  float* lse;
+  int n_q, H, topk, n_grp, n_hb;
+  float scale_log2;
+  int2* start;                 // [n_grp + 1]: (row, tile) each group starts at; [n_grp].x = groups in use
+  float* part_o;               // [n_grp * 2][H][512]
+  float* part_m;               // [3][n_grp * 2][H]: max in use (log2), sum of the rounded weights, plain sum
+  uint32_t* status;
+  unsigned long long wait_ns;
+  int stop_after;
+};
+
+__device__ __forceinline__ int row_len(const PagedRows& pg, int row) {
+  return max(0, min(__ldg(pg.seq_len + row), pg.max_pages << kPageShift));
+}
+template <bool SEL>
+__device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
+  if constexpr (SEL) return __ldg(a.row_nt + row);
+  return (row_len(a.pg, row) + kRows - 1) / kRows;
+}
+
+// The segments (consecutive tiles of one row) of this CTA's share, in order.
+struct Seg {
+  int row, i0, n;
+  bool whole;        // the row's every tile
+};
+template <bool SEL>
+struct Walk {
+  const LArgs& a;
+  int row, tile;
+  long long left;
+  __device__ __forceinline__ Walk(const LArgs& args, int r, int t, long long n) : a(args), row(r), tile(t), left(n) {}
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (left <= 0) return false;
+    int T = row_tiles<SEL>(a, row);
+    while (T == 0) T = row_tiles<SEL>(a, ++row);
+    s.row = row;
+    s.i0 = tile;
+    s.n = static_cast<int>(min(static_cast<long long>(T - tile), left));
+    s.whole = tile == 0 && s.n == T;
+    left -= s.n;
+    ++row;
+    tile = 0;
+    return true;
+  }
+};
+
+// Block-table entries of one row, 32 pages at a time in the lanes of a warp (and the next 32).
+struct PageWindow {
+  const int32_t* bt;
+  int max_pages, base, cur, nxt;
+  __device__ __forceinline__ int load(int k) const {
+    const int p = k * 32 + static_cast<int>(threadIdx.x & 31);
+    return p < max_pages ? __ldg(bt + p) : -1;
+  }
+  __device__ __forceinline__ PageWindow(const PagedRows& pg, int row, int page)
+      : bt(pg.block_table + static_cast<size_t>(row) * pg.max_pages), max_pages(pg.max_pages), base(page >> 5) {
+    cur = load(base);
+    nxt = load(base + 1);
+  }
+  // page of logical page p, p within the current or the next 32; the whole warp calls it
+  __device__ __forceinline__ int get(int p) const { return __shfl_sync(0xffffffffu, (p >> 5) == base ? cur : nxt, p & 31); }
+  __device__ __forceinline__ void advance(int p) {
+    if ((p >> 5) != base) {
+      base = p >> 5;
+      cur = nxt;
+      nxt = load(base + 1);
+    }
+  }
+};
+
+template <int HB, bool FP8, bool SEL>
+__global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap tmap_kv, const __grid_constant__ CUtensorMap tmap_q,
+                       const __grid_constant__ LArgs a) {
+  using C = LCfg<HB, FP8>;
+  constexpr int NR = C::NR;
+  static_assert(FP8 || !SEL, "selected rows of a bf16 cache take the sparse kernel's gather walk");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ LShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sT = smem;                        // two tiles
+  uint8_t* sQ = smem + 2 * kTileBytes;       // HB x 576, nine blocks of HB x 128 B
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = blockIdx.x / a.n_hb, hb = blockIdx.x - grp * a.n_hb;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh.full[s], C::NP);
+      mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.s_full[s], 1);
+      mbar_init(&sh.s_empty[s], C::SW);
+      mbar_init(&sh.o_done[s], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.p_full, C::SW);
+    mbar_init(&sh.o_free, C::SW);
+    mbar_init(&sh.mma_done, 2);
+    sh.abort_flag = 0;
+    sh.soft_abort = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == C::PV_WARP) {
+    tmem_alloc(&sh.tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // this group's share of the line of tiles: block scan over the rows' tile counts
+  const int per = (a.n_q + C::THREADS - 1) / C::THREADS;
+  const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
+  long long mine = 0;
+  for (int r = ra; r < rb; ++r) {
+    mine += row_tiles<SEL>(a, r);
+    if (blockIdx.x == 0) {
+      const int want = __ldg(a.pg.seq_len + r);
+      if (want < 0 || want > (a.pg.max_pages << kPageShift)) {
+        atomicOr(a.status, DEV_ERR_RANGE);
+        atomicAdd(a.status + 1, 1u);
+      }
+    }
+  }
+  long long pre = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) sh.wsum[warp] = pre;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0;
+  pre -= mine;
+  for (int w = 0; w < C::THREADS / 32; ++w) {
+    if (w < warp) pre += sh.wsum[w];
+    total += sh.wsum[w];
+  }
+  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + kMinTiles - 1) / kMinTiles));
+  const long long first = grp < groups ? total * grp / groups : 0;
+  const long long share = grp < groups ? total * (grp + 1) / groups - first : 0;
+  if (share > 0 && pre <= first && first < pre + mine) {
+    long long at = pre;
+    int r = ra;
+    while (true) {
+      const int T = row_tiles<SEL>(a, r);
+      if (first < at + T) break;
+      at += T;
+      ++r;
+    }
+    sh.row0 = r;
+    sh.tile0 = static_cast<int>(first - at);
+    if (hb == 0) a.start[grp] = make_int2(r, static_cast<int>(first - at));
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.n_grp] = make_int2(groups, 0);
+  // rows without keys: zeros and -inf
+  for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
+    if (row_tiles<SEL>(a, t) != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.H * kDv);
+    for (int e = threadIdx.x; e < a.H * (kDv / 8); e += C::THREADS) o[e] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int h = threadIdx.x; h < a.H; h += C::THREADS) a.lse[static_cast<size_t>(t) * a.H + h] = -INFINITY;
+  }
+  __syncthreads();
+  const uint32_t tmem = sh.tmem_base;
+  Walk<SEL> walk(a, share > 0 ? sh.row0 : 0, share > 0 ? sh.tile0 : 0, share);
+  Seg sg;
+
+  // valid rows of tile i (absolute) of a row: past the length, or on a page outside the cache, none
+  auto tile_rows = [&](int len, int i, int page) -> int {
+    if (page < 0 || page >= a.pg.n_pages) return 0;
+    return max(0, min(kRows, len - i * kRows));
+  };
+
+  if (warp >= C::SW && warp < C::S_WARP) {
+    // ---------------------------------------------------------------- Q and the rows
+    const int pw = warp - C::SW;
+    uint32_t g = 0, it = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, a.status, a.wait_ns));
+    };
+    while (ok && walk.next(sg)) {
+      if (pw == 0) {
+        if (it > 0) ok = wait(&sh.q_empty, (it - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) {
+          const int qrow = sg.row * a.H + hb * HB;
+          mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
+#pragma unroll 1
+          for (int kb = 0; kb < kKB; ++kb) tma_load_2d(sQ + kb * (HB * 128), &tmap_q, &sh.q_full, kb * 64, qrow);
+        }
+        __syncwarp();
+      }
+      ++it;
+      if constexpr (!FP8) {
+        PageWindow win(a.pg, sg.row, sg.i0 >> 1);
+        const int last = sg.i0 + sg.n;
+        auto row_at = [&](int i, int page) { return (page << kPageShift) + (i & 1) * kRows; };
+        for (int i = sg.i0; i < last; ++i, ++g) {
+          win.advance(i >> 1);
+          const int page = win.get(i >> 1);
+          const bool bad = page < 0 || page >= a.pg.n_pages;
+          const int row = row_at(i, bad ? 0 : page);
+          if (hb == 0) {
+            // the tile kPrefetch ahead (at a segment's start, every tile up to it) comes to L2
+            // before its slot is free
+            for (int f = i == sg.i0 ? i + 1 : i + kPrefetch; f <= i + kPrefetch && f < last; ++f) {
+              const int fp = win.get(f >> 1);
+              if (lane == 0 && fp >= 0 && fp < a.pg.n_pages)
+                l2_prefetch(a.latent + static_cast<size_t>(row_at(f, fp)) * (kDqk * 2), kTileBytes);
+            }
+          }
+          if (bad && lane == 0 && hb == 0) {
+            atomicOr(a.status, DEV_ERR_BAD_INDEX);
+            atomicAdd(a.status + 1, 1u);
+          }
+          if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
+            ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
+            break;
+          }
+          if (g >= 2 && !(ok = wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.full[g & 1], kTileBytes);
+            tma_load_3d(sT + (g & 1) * kTileBytes, &tmap_kv, &sh.full[g & 1], 0, row, 0);
+          }
+          __syncwarp();
+        }
+      } else {
+        // warp pw converts row octets pw, pw + NP, ...; lane = (row of the octet, 16 codes of each
+        // 64-dim block).  Eight lanes of a store phase cover two rows x every other 16-byte
+        // chunk, which the swizzle spreads over all banks.
+        constexpr int K = 8 / C::NP;
+        const int c = lane & 3;
+        uint4 raw[K][8], rr[K][2];
+        uint32_t sc[K];
+        const int len = row_len(a.pg, sg.row);
+        const int last = sg.i0 + sg.n;
+        PageWindow win(a.pg, sg.row, SEL ? 0 : sg.i0 >> 1);
+        const int32_t* irow = SEL ? a.idx + static_cast<size_t>(sg.row) * a.topk : nullptr;
+        int jx[K], prow[K];
+        auto slot_idx = [&](int i) {       // SEL: this thread's offsets of tile i
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int s = i * kRows + 8 * (pw + C::NP * k) + (lane >> 2);
+            jx[k] = i < last && s < a.topk ? __ldg(irow + s) : -1;
+          }
+        };
+        auto resolve = [&](int i) {        // cache rows of tile i (-1: none)
+          if constexpr (SEL) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              const int j = jx[k];
+              const int page = j >= 0 && j < len ? __ldg(win.bt + (j >> kPageShift)) : -1;
+              const bool in = page >= 0 && page < a.pg.n_pages;
+              if (j >= 0 && !in && c == 0 && hb == 0) {
+                atomicOr(a.status, DEV_ERR_BAD_INDEX);
+                atomicAdd(a.status + 1, 1u);
+              }
+              prow[k] = in ? (page << kPageShift) + (j & (kPageRows - 1)) : -1;
+            }
+          } else {
+            int nv = 0, page = -1;
+            if (i < last) {
+              win.advance(i >> 1);
+              page = win.get(i >> 1);
+              nv = tile_rows(len, i, page);
+              if (nv == 0 && lane == 0 && pw == 0 && hb == 0) {
+                atomicOr(a.status, DEV_ERR_BAD_INDEX);
+                atomicAdd(a.status + 1, 1u);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              const int r = 8 * (pw + C::NP * k) + (lane >> 2);
+              prow[k] = r < nv ? (page << kPageShift) + (i & 1) * kRows + r : -1;
+            }
+          }
+        };
+        auto fetch = [&]() {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const bool in = prow[k] >= 0;
+            const size_t row = in ? prow[k] : 0;
+            const uint8_t* src = a.latent + row * kDv + c * 16;
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            sc[k] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row) : 0u;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) raw[k][b] = in ? ldg_once(src + b * 64) : z;
+            const uint16_t* rs = a.rope + row * 64 + c * 16;
+            rr[k][0] = in ? ldg_once(rs) : z;
+            rr[k][1] = in ? ldg_once(rs + 8) : z;
+          }
+        };
+        if constexpr (SEL) slot_idx(sg.i0);
+        resolve(sg.i0);
+        fetch();
+        if constexpr (SEL) slot_idx(sg.i0 + 1);
+        for (int i = sg.i0; i < last; ++i, ++g) {
+          if constexpr (!SEL) {
+            if (hb == 0 && pw == 0) {
+              for (int f = i == sg.i0 ? i + 2 : i + kPrefetch; f <= i + kPrefetch && f < last; ++f) {
+                const int fp = win.get(f >> 1);
+                if (lane == 0 && fp >= 0 && fp < a.pg.n_pages) {
+                  const size_t row = (static_cast<size_t>(fp) << kPageShift) + (f & 1) * kRows;
+                  l2_prefetch(a.latent + row * kDv, kRows * kDv);
+                  l2_prefetch(a.rope + row * 64, kRows * 128);
+                  l2_prefetch(a.scale + row * 4, kRows * 4);
+                }
+              }
+            }
+          }
+          if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
+            ok = false;   // test hook
+            break;
+          }
+          if (g >= 2 && !(ok = wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1))) break;
+          const uint32_t tile = smem_u32(sT + (g & 1) * kTileBytes);
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int r = 8 * (pw + C::NP * k) + (lane >> 2);
+            const uint32_t d0 = tile + r * 128 + (((2 * c) ^ (r & 7)) << 4);
+            const uint32_t d1 = tile + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const uint32_t m = fp8_mult((sc[k] >> (8 * (b >> 1))) & 0xFFu);
+              uint32_t o[8];
+              fp8x4_to_bf16(raw[k][b].x, m, o[0], o[1]);
+              fp8x4_to_bf16(raw[k][b].y, m, o[2], o[3]);
+              fp8x4_to_bf16(raw[k][b].z, m, o[4], o[5]);
+              fp8x4_to_bf16(raw[k][b].w, m, o[6], o[7]);
+              sts128(d0 + b * kBlkBytes, o[0], o[1], o[2], o[3]);
+              sts128(d1 + b * kBlkBytes, o[4], o[5], o[6], o[7]);
+            }
+            sts128(d0 + 8 * kBlkBytes, rr[k][0].x, rr[k][0].y, rr[k][0].z, rr[k][0].w);
+            sts128(d1 + 8 * kBlkBytes, rr[k][1].x, rr[k][1].y, rr[k][1].z, rr[k][1].w);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[g & 1]);
+          if (i + 1 < last) {
+            resolve(i + 1);
+            fetch();
+            if constexpr (SEL) slot_idx(i + 2);
+          }
+        }
+      }
+    }
+    // let every copy this CTA started land before its shared memory can be released
+    if (pw == 0 && lane == 0) {
+      if (it > 0) mbar_drain(&sh.q_full, (it - 1) & 1, 200000000ull);
+      if constexpr (!FP8)
+        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full[j & 1], (j >> 1) & 1, 200000000ull);
+    }
+  } else if (warp < C::SW) {
+    // ---------------------------------------------------------------- softmax + epilogue
+    constexpr int kSoft = C::SOFT;
+    const int tid = threadIdx.x;
+    const int qd = warp & 3;                       // TMEM lane quarter
+    const int c_off = (warp >> 2) * C::CW;         // this warp's columns: [c_off, c_off + CW)
+    const int r0 = qd * 16 + (lane >> 2);          // S^T rows held: r0 and r0 + 8
+    const int cq = 2 * (lane & 3);                 // column pair within each group of 8 columns
+    const uint32_t t_lane = static_cast<uint32_t>(qd * 32) << 16;
+    const int n_cols = min(HB, a.H - hb * HB);
+    // A failed (timed-out) wait is published through sh.soft_abort, written only before a
+    // named barrier and read right after it, so all softmax warps leave at the same point.
+    uint32_t g = 0;
+    bool stop = false;
+    while (!stop && walk.next(sg)) {
+      if (tid < HB) sh.m_used[tid] = -INFINITY;
+      float lp[2 * NR], lu[2 * NR];   // per column: sums of the rounded weights, and of the weights
+#pragma unroll
+      for (int c = 0; c < 2 * NR; ++c) lp[c] = lu[c] = 0.f;
+      named_bar_sync(1, kSoft);
+      const int len = row_len(a.pg, sg.row);
+      const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+      const int32_t* irow = SEL ? a.idx + static_cast<size_t>(sg.row) * a.topk : nullptr;
+      auto in_cache = [&](int j) {
+        if (j < 0 || j >= len) return false;
+        const int page = __ldg(bt + (j >> kPageShift));
+        return page >= 0 && page < a.pg.n_pages;
+      };
+      for (int n = 0; n < sg.n; ++n, ++g) {
+        const int i = sg.i0 + n;
+        const int sb = g & 1;
+        bool rv0, rv1;                 // rows r0 / r0 + 8 hold a key
+        if constexpr (SEL) {
+          const int s0 = i * kRows + r0, s1 = s0 + 8;
+          rv0 = s0 < a.topk && in_cache(__ldg(irow + s0));
+          rv1 = s1 < a.topk && in_cache(__ldg(irow + s1));
+        } else {
+          const int nv = tile_rows(len, i, __ldg(bt + (i >> 1)));
+          rv0 = r0 < nv;
+          rv1 = r0 + 8 < nv;
+        }
+        bool ok = mbar_wait_for(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, a.status, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        float sc[4 * NR];   // [4k + j]: j = 0,1 row r0 columns 8k+cq, +1;  j = 2,3 row r0 + 8
+        bool need = false;
+        if (ok) {
+          tc_fence_after();
+          uint32_t v[4 * NR];
+          tmem_ld_16x256b<NR>(tmem + t_lane + C::S_COL + sb * HB + c_off, v);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+#pragma unroll
+          for (int kk = 0; kk < NR; ++kk) {
+            const float2 mu = *reinterpret_cast<const float2*>(&sh.m_used[c_off + 8 * kk + cq]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bool valid = (j & 2) ? rv1 : rv0;
+              const float x = valid ? __uint_as_float(v[4 * kk + j]) * a.scale_log2 : -INFINITY;
+              sc[4 * kk + j] = x;
+              need |= x > ((j & 1) ? mu.y : mu.x) + 8.f;   // only a max that grew by > 2^8 forces a rescale
+            }
+          }
+        }
+        // one barrier-reduction per tile decides whether the slow path runs
+        if (!ok && lane == 0) sh.soft_abort = 1;
+        if (bar_or(1, kSoft, need || !ok)) {
+          if (ok) {
+#pragma unroll
+            for (int kk = 0; kk < NR; ++kk) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(sc[4 * kk + e], sc[4 * kk + 2 + e]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                if (lane < 4) sh.red[qd][c_off + 8 * kk + cq + e] = x;
+              }
+            }
+            // O^T may only be rescaled once the previous tile's PV has finished
+            if (n > 0) {
+              ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, a.status, a.wait_ns);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok && lane == 0) sh.soft_abort = 1;
+            }
+          }
+          named_bar_sync(1, kSoft);
+          stop = sh.soft_abort != 0;
+          if (!stop && tid < HB) {
+            const float m = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
+            float al = 1.f;
+            if (m > sh.m_used[tid] + 8.f) {
+              al = exp2f(sh.m_used[tid] - m);         // 0 when the old max is -inf
+              sh.m_used[tid] = m;
+            }
+            sh.alpha[tid] = al;
+          }
+          named_bar_sync(1, kSoft);
+          if (stop) break;
+          tc_fence_after();
+          bool any = false;
+#pragma unroll
+          for (int kk = 0; kk < NR; ++kk) {
+            const float2 al = *reinterpret_cast<const float2*>(&sh.alpha[c_off + 8 * kk + cq]);
+            lp[2 * kk] *= al.x;
+            lp[2 * kk + 1] *= al.y;
+            lu[2 * kk] *= al.x;
+            lu[2 * kk + 1] *= al.y;
+          }
+#pragma unroll
+          for (int c0 = 0; c0 < HB; c0 += 16) {
+            float ar[16];
+            lrow16(ar, &sh.alpha[c0]);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) any |= ar[c] != 1.f;
+          }
+          if (any && n > 0) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+#pragma unroll
+              for (int hw = 0; hw < C::CW / 16; ++hw) {
+                const int hh = c_off / 16 + hw;
+                uint32_t o[16];
+                tmem_ld16(tmem + t_lane + b * HB + hh * 16, o);
+                tmem_ld_wait();
+                float ar[16];
+                lrow16(ar, &sh.alpha[hh * 16]);
+#pragma unroll
+                for (int h = 0; h < 16; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * ar[h]);
+                tmem_st16(tmem + t_lane + b * HB + hh * 16, o);
+              }
+            }
+            tmem_st_wait();
+          }
+        }
+        // P = 2^(s - m), rounded to bf16 for the second product (at most 2^-9 of each weight, no
+        // bias), into the tile's rope block, which S^T no longer needs.  The output is divided by
+        // the sum of the rounded weights, so that they add up to one; the log-sum-exp takes the
+        // sum of the unrounded ones.
+        const uint32_t p_base = smem_u32(sT + sb * kTileBytes + (kKB - 1) * kBlkBytes);
+#pragma unroll
+        for (int kk = 0; kk < NR; ++kk) {
+          float2 mu = *reinterpret_cast<const float2*>(&sh.m_used[c_off + 8 * kk + cq]);
+          mu.x = mu.x == -INFINITY ? 0.f : mu.x;      // only masked entries so far: 2^(-inf - 0) = 0
+          mu.y = mu.y == -INFINITY ? 0.f : mu.y;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = r0 + 8 * h;
+            const float p0 = ex2f(sc[4 * kk + 2 * h] - mu.x);
+            const float p1 = ex2f(sc[4 * kk + 2 * h + 1] - mu.y);
+            const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+            const int chunk = c_off / 8 + kk;
+            sts32(p_base + r * 128 + ((chunk ^ (r & 7)) << 4) + cq * 2, *reinterpret_cast<const uint32_t*>(&pb));
+            lp[2 * kk] += __low2float(pb);
+            lp[2 * kk + 1] += __high2float(pb);
+            lu[2 * kk] += p0;
+            lu[2 * kk + 1] += p1;
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full);
+      }
+      if (stop) break;
+      // segment end: column sums over the 64 rows, then the output or a partial
+#pragma unroll
+      for (int kk = 0; kk < NR; ++kk) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = lp[2 * kk + e], y = lu[2 * kk + e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+          }
+          if (lane < 4) {
+            sh.red[qd][c_off + 8 * kk + cq + e] = x;
+            sh.red2[qd][c_off + 8 * kk + cq + e] = y;
+          }
+        }
+      }
+      bool ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, a.status, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) sh.soft_abort = 1;
+      named_bar_sync(1, kSoft);
+      stop = sh.soft_abort != 0;
+      if (tid < HB) {
+        sh.l_run[tid] = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
+        sh.l_sum[tid] = (sh.red2[0][tid] + sh.red2[1][tid]) + (sh.red2[2][tid] + sh.red2[3][tid]);
+      }
+      named_bar_sync(1, kSoft);
+      if (stop) break;
+      tc_fence_after();
+      const size_t pslot = static_cast<size_t>(grp) * 2 + (sg.i0 > 0 ? 0 : 1);
+#pragma unroll
+      for (int hw = 0; hw < C::CW / 16; ++hw) {
+        const int hh = c_off / 16 + hw;
+#pragma unroll
+        for (int b2 = 0; b2 < 4; b2 += 2) {
+          uint32_t o[2][16];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) tmem_ld16(tmem + t_lane + (b2 + b) * HB + hh * 16, o[b]);
+          tmem_ld_wait();
+          if (sg.whole) {
+            uint16_t* orow = a.out + (static_cast<size_t>(sg.row) * a.H + hb * HB) * kDv + qd * 32 + lane + b2 * 128;
+            float inv[16];
+            lrow16(inv, &sh.l_run[hh * 16]);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+              const int c = hh * 16 + h;
+              if (c >= n_cols) continue;
+              // a NaN sum stays NaN; a sum of zero (no key) gives zeros
+              const float iv = inv[h] == 0.f ? 0.f : 1.f / inv[h];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const __nv_bfloat16 ob = __float2bfloat16_rn(__uint_as_float(o[b][h]) * iv);
+                orow[static_cast<size_t>(c) * kDv + b * 128] = *reinterpret_cast<const uint16_t*>(&ob);
+              }
+            }
+          } else {
+            float* prow = a.part_o + (pslot * a.H + hb * HB) * kDv + qd * 32 + lane + b2 * 128;
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+              const int c = hh * 16 + h;
+              if (c >= n_cols) continue;
+#pragma unroll
+              for (int b = 0; b < 2; ++b) prow[static_cast<size_t>(c) * kDv + b * 128] = __uint_as_float(o[b][h]);
+            }
+          }
+        }
+      }
+      if (tid < n_cols) {
+        if (sg.whole) {
+          if (a.lse) {
+            const float l = sh.l_sum[tid];
+            a.lse[static_cast<size_t>(sg.row) * a.H + hb * HB + tid] =
+                l == 0.f ? -INFINITY : (sh.m_used[tid] + log2f(l)) * 0.69314718055994531f;
+          }
+        } else {
+          const size_t n = static_cast<size_t>(a.n_grp) * 2 * a.H, at = pslot * a.H + hb * HB + tid;
+          a.part_m[at] = sh.m_used[tid];
+          a.part_m[n + at] = sh.l_run[tid];
+          a.part_m[2 * n + at] = sh.l_sum[tid];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.o_free);
+      named_bar_sync(1, kSoft);        // per-column state may be reset now
+    }
+  } else {
+    // ---------------------------------------------------------------- MMA issuers
+    constexpr uint32_t id_qk = idesc_bf16_f32(64, HB, 0, 0);
+    constexpr uint32_t id_pv = idesc_bf16_f32(128, HB, 1, 1);
+    const uint32_t st0 = smem_u32(sT);
+    uint32_t g = 0, it = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, a.status, a.wait_ns));
+    };
+    const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    while (ok && walk.next(sg)) {
+      if (warp == C::S_WARP) {
+        const int len = row_len(a.pg, sg.row);
+        const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+        ok = wait(&sh.q_full, it & 1);
+        for (int n = 0; n < sg.n && ok; ++n, ++g) {
+          const int sb = g & 1;
+          int nv = kRows;
+          if constexpr (!FP8) nv = tile_rows(len, sg.i0 + n, __ldg(bt + ((sg.i0 + n) >> 1)));
+          if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
+          if (!(ok = wait(&sh.full[sb], (g >> 1) & 1))) break;
+          if constexpr (!FP8) {
+            if (nv < kRows) {
+              // rows without a key become zeros in all nine blocks (a swizzled row is one
+              // 128-byte line of its block)
+              for (int e = lane; e < (kRows - nv) * 8 * kKB; e += 32) {
+                const int kb = e / ((kRows - nv) * 8), w = e - kb * ((kRows - nv) * 8);
+                sts128(st0 + sb * kTileBytes + kb * kBlkBytes + nv * 128 + w * 16, 0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          tc_fence_after();
+          const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
+          const uint32_t d_s = tmem + C::S_COL + sb * HB;
+#pragma unroll
+          for (int kb = 0; kb < kKB; ++kb) {
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub)
+              umma_bf16_elect(d_s, da + static_cast<uint64_t>((kb * kBlkBytes + sub * 32) >> 4),
+                              dq0 + static_cast<uint64_t>((kb * HB * 128 + sub * 32) >> 4), id_qk, (kb | sub) ? 1u : 0u);
+          }
+          umma_commit_elect(&sh.s_full[sb]);
+        }
+        if (ok) umma_commit_elect(&sh.q_empty);
+      } else {
+        for (int n = 0; n < sg.n && ok; ++n, ++g) {
+          ok = wait(&sh.p_full, g & 1);
+          if (ok && n == 0 && it > 0) ok = wait(&sh.o_free, (it - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tb = st0 + (g & 1u) * kTileBytes;
+          const uint64_t dv = sdesc_sw128(tb, kBlkBytes, 1024);
+          const uint64_t dp = sdesc_sw128(tb + (kKB - 1) * kBlkBytes, kBlkBytes, 1024);
+          const uint32_t acc0 = n > 0 ? 1u : 0u;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int kq = 0; kq < kRows / 16; ++kq)
+              umma_bf16_elect(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes + kq * 2048) >> 4),
+                              dp + static_cast<uint64_t>((kq * 2048) >> 4), id_pv, kq > 0 ? 1u : acc0);
+          }
+          umma_commit_elect(&sh.empty[g & 1]);
+          umma_commit_elect(&sh.o_done[g & 1]);
+        }
+      }
+      ++it;
+    }
+    // every MMA this warp issued has completed before TMEM is released
+    umma_commit_elect(&sh.mma_done);
+    mbar_drain(&sh.mma_done, 0, 200000000ull);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::PV_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// Joins the partials of the rows that were split: block (b, h) takes the row that begins in group
+// b's share and goes on in the next ones, head h.  With M the largest of the partials' maxima m_s
+// and w_s = 2^(m_s - M): out = sum w_s O_s / sum w_s lr_s, lse = ln 2 (M + log2 sum w_s l_s).
+__global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ LArgs a) {
+  const int b = blockIdx.x, h = blockIdx.y;
+  const int groups = __ldg(&a.start[a.n_grp].x);
+  if (b + 1 >= groups) return;
+  const int2 s0 = a.start[b], s1 = a.start[b + 1];
+  if (s1.y == 0 || (s0.x == s1.x && s0.y > 0)) return;      // no row goes on, or it began before
+  const int row = s1.x;
+  int end = b + 2;                                          // groups b .. end - 1 hold the row
+  while (end < groups && a.start[end].x == row && a.start[end].y > 0) ++end;
+  const size_t n = static_cast<size_t>(a.n_grp) * 2 * a.H;
+  auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == b ? 1 : 0)) * a.H + h; };
+  float M = -INFINITY;
+  bool nan = false;
+  for (int c = b; c < end; ++c) {
+    const float m = a.part_m[slot(c)];
+    M = fmaxf(M, m);
+    nan |= m != m;
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lr = 0.f, ls = 0.f;
+  for (int c = b; c < end; ++c) {
+    const size_t at = slot(c);
+    const float m = a.part_m[at];
+    const float w = m == -INFINITY ? 0.f : exp2f(m - M);
+    const float4 o = reinterpret_cast<const float4*>(a.part_o + at * kDv)[threadIdx.x];
+    const float l1 = a.part_m[n + at];
+    // a partial whose sum is NaN (a NaN score) keeps its mark even where its max says nothing
+    if (l1 != l1) nan = true;
+    acc.x += w * o.x;
+    acc.y += w * o.y;
+    acc.z += w * o.z;
+    acc.w += w * o.w;
+    lr += w * l1;
+    ls += w * a.part_m[2 * n + at];
+  }
+  if (nan) lr = ls = __int_as_float(0x7FC00000);
+  const float inv = lr == 0.f ? 0.f : 1.f / lr;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const size_t orow = static_cast<size_t>(row) * a.H + h;
+  reinterpret_cast<uint2*>(a.out + orow * kDv)[threadIdx.x] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  if (a.lse && threadIdx.x == 0) a.lse[orow] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+}
+
+int head_block(int n_heads) { return n_heads <= 16 ? 16 : n_heads <= 32 ? 32 : 64; }
+
+struct Layout {
+  int n_hb, n_grp;
+  size_t off_start, off_m, off_o, total;
+};
+Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
+  Layout L{};
+  L.n_hb = (n_heads + head_block(n_heads) - 1) / head_block(n_heads);
+  const long long most = (static_cast<long long>(n_q) * row_tiles_max + kMinTiles - 1) / kMinTiles;
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 152;
+  L.n_grp = static_cast<int>(std::max(1LL, std::min<long long>(sms / L.n_hb, most)));
+  const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  size_t o = up(static_cast<size_t>(n_q) * sizeof(int32_t));           // row_nt (selected keys)
+  L.off_start = o;
+  o += up((static_cast<size_t>(L.n_grp) + 1) * sizeof(int2));
+  L.off_m = o;
+  o += up(static_cast<size_t>(L.n_grp) * 2 * n_heads * 3 * sizeof(float));
+  L.off_o = o;
+  o += L.n_grp > 1 ? static_cast<size_t>(L.n_grp) * 2 * n_heads * kDv * sizeof(float) : 0;
+  L.total = o;
+  return L;
+}
+
+template <int HB, bool FP8, bool SEL>
+cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
+  using C = LCfg<HB, FP8>;
+  cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, SEL>>(C::DYN_SMEM);
+  if (e != cudaSuccess) return e;
+  latent_attn_kernel<HB, FP8, SEL><<<a.n_grp * a.n_hb, C::THREADS, C::DYN_SMEM, st>>>(tkv, tq, a);
+  return cudaGetLastError();
+}
+template <int HB>
+cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
+  if (!fp8) return launch_t<HB, false, false>(tkv, tq, a, st);
+  return sel ? launch_t<HB, true, true>(tkv, tq, a, st) : launch_t<HB, true, false>(tkv, tq, a, st);
+}
+
+}  // namespace
+
+int latent_attn_q_box_rows(int n_heads) { return head_block(n_heads); }
+
+size_t latent_attn_ws_bytes(int n_q, int n_heads) {
+  // the most groups any block table can ask for
+  return latent_layout(n_q, n_heads, 1LL << 24).total;
+}
+
+cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_q,
+                               const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
+                               void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st) {
+  const bool sel = idx != nullptr;
+  const Layout L = latent_layout(n_q, n_heads, sel ? (topk + kRows - 1) / kRows : pg.max_pages * 2LL);
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  const PipelineDebug dbg = pipeline_debug();
+  LArgs a{};
+  a.latent = c.latent;
+  a.scale = c.scale;
+  a.rope = c.rope;
+  a.idx = idx;
+  a.row_nt = reinterpret_cast<int32_t*>(base);
+  a.pg = pg;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.n_q = n_q;
+  a.H = n_heads;
+  a.topk = topk;
+  a.n_grp = L.n_grp;
+  a.n_hb = L.n_hb;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.start = reinterpret_cast<int2*>(base + L.off_start);
+  a.part_m = reinterpret_cast<float*>(base + L.off_m);
+  a.part_o = reinterpret_cast<float*>(base + L.off_o);
+  a.status = status;
+  a.wait_ns = dbg.wait_ns;
+  a.stop_after = dbg.stop_after_tiles;
+  cudaError_t e;
+  if (sel) {
+    const int ps = prof_begin(kProfAttnPrep, st);
+    e = launch_row_tiles(idx, n_q, topk, reinterpret_cast<int32_t*>(base), st);
+    prof_end(ps, st);
+    if (e != cudaSuccess) return e;
+  }
+  const int ps = prof_begin(kProfAttn, st);
+  switch (head_block(n_heads)) {
+    case 16: e = launch_hb<16>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
+    case 32: e = launch_hb<32>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
+    default: e = launch_hb<64>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
+  }
+  if (e == cudaSuccess && L.n_grp > 1) {
+    latent_join_kernel<<<dim3(L.n_grp - 1, n_heads), 128, 0, st>>>(a);
+    e = cudaGetLastError();
+  }
+  prof_end(ps, st);
+  return e;
+}
+
+}  // namespace dsa

@@ -384,6 +384,147 @@ dsa_status dsa_sparse_attn_paged(const dsa_attn_desc* desc, const void* q, const
                                  const dsa_paged_cache* pages, void* out, float* lse, void* ws, size_t ws_bytes,
                                  void* stream);
 
+/* ------------------------------------------------------------------ rotary positions  */
+
+/* Scaling of a RoPE table beyond the positions a model was trained on.  The pages give the
+ * indexer's RoPE only; the scalings are the published ones (position interpolation; YaRN,
+ * "Efficient Context Window Extension of Large Language Models").
+ *   DSA_ROPE_SCALE_NONE    f_i = theta^(-2i/rope_dim)
+ *   DSA_ROPE_SCALE_LINEAR  f_i / factor
+ *   DSA_ROPE_SCALE_YARN    f_i (1 - r_i) + f_i / factor * r_i, with r_i = (i - lo) / (hi - lo) cut to
+ *                          [0, 1], lo = max(0, floor(d(beta_fast))), hi = min(rope_dim - 1,
+ *                          ceil(d(beta_slow))), d(b) = rope_dim ln(orig_len / (2 pi b)) / (2 ln theta)
+ *                          (hi = lo: r_i = 1 from i = lo + 1 on)
+ * Every cos and sin is multiplied by mscale (1: none; YaRN's usual 0.1 ln(factor) + 1 is the
+ * caller's to give). */
+#define DSA_ROPE_SCALE_NONE 0
+#define DSA_ROPE_SCALE_LINEAR 1
+#define DSA_ROPE_SCALE_YARN 2
+typedef struct dsa_rope_scaling {
+  int32_t kind;       /* DSA_ROPE_SCALE_*                                       */
+  int32_t orig_len;   /* YARN: positions the model was trained on, >= 1         */
+  double factor;      /* LINEAR, YARN: >= 1                                     */
+  double beta_fast;   /* YARN: turns over orig_len above which dims are kept    */
+  double beta_slow;   /* YARN: turns below which dims are interpolated; > 0     */
+  double mscale;      /* > 0                                                    */
+} dsa_rope_scaling;
+
+/* dsa_rope_table with a scaling (NULL: none, the same values as dsa_rope_table).  Host code; angles
+ * in float64.  Errors: DSA_ERR_ARG (those of dsa_rope_table; a kind or value out of range; YARN with
+ * theta <= 1 or beta_fast < beta_slow). */
+dsa_status dsa_rope_table_scaled(double theta, int32_t rope_dim, int32_t n_pos, const dsa_rope_scaling* scaling,
+                                 float* host_out);
+
+#define DSA_BF16 0
+#define DSA_F32 1
+#define DSA_ROPE_INTERLEAVED (1u << 0)   /* pairs (2i, 2i + 1); clear: (i, i + rope_dim / 2)          */
+#define DSA_ROPE_INVERSE (1u << 1)       /* turn by the negated angle: the rotation's gradient, for
+                                            d_x from d_out (mscale stays a factor of both)            */
+typedef struct dsa_rope_desc {
+  int32_t n_tokens;
+  int32_t n_heads;
+  int32_t rope_dim;          /* even, 2 .. 512                                                        */
+  int32_t dtype;             /* DSA_BF16 or DSA_F32, of x and out                                     */
+  int64_t x_token_stride;    /* strides in elements, >= 0; a head's rope_dim elements are contiguous  */
+  int64_t x_head_stride;
+  int64_t out_token_stride;
+  int64_t out_head_stride;
+  uint32_t flags;            /* DSA_ROPE_*                                                            */
+} dsa_rope_desc;
+
+/* Rotary positions of (a part of) every head: with c, s = rope_cs[pos[t]][i],
+ *   out[t, h, a_i] = x[t, h, a_i] c - x[t, h, b_i] s      out[t, h, b_i] = x[t, h, a_i] s + x[t, h, b_i] c
+ * over the pairs (a_i, b_i) of the layout, in fp32, rounded once.  x and out point at the rotary
+ * dims of head 0 of token 0 and are strided, so a projection's [n][H][128 + 64] rotary part goes
+ * straight into the absorbed query's [n][H][512 + 64] (dsa_sparse_attn takes q already rotated; [MB]
+ * qk_rope_head_dim commit: 64 rotary dims); only these dims are read and written.  out may be x with
+ * the same strides (in place); otherwise no element of out may be an element of x, nor may two of
+ * out's coincide.
+ *   pos int32 [n_tokens], each in [0, rope_n_pos); another one leaves its token's out as it was and is
+ *   flagged (DSA_ERR_DEVICE in the workspace status).  rope_cs f32 [rope_n_pos][rope_dim/2][2], 16-byte
+ *   aligned (dsa_rope_table, dsa_rope_table_scaled; device copy).  ws: at least 256 bytes.
+ * 16-byte vectors are used where addresses, strides and rope_dim allow, single pairs elsewhere.
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_tokens * n_heads beyond int32), DSA_ERR_WORKSPACE,
+ * DSA_ERR_CUDA. */
+dsa_status dsa_rope_apply(const dsa_rope_desc* desc, const void* x, const int32_t* pos, const float* rope_cs,
+                          int32_t rope_n_pos, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ latent cache ----- */
+
+/* The latent cache as it is written by dsa_latent_cache_write and read by dsa_latent_cache_read and
+ * dsa_latent_attn_paged: n_rows rows in pages of DSA_PAGE_ROWS (the layout of the paged calls above).
+ *   DSA_CACHE_BF16: latent bf16 [n_rows][576] (scale, rope NULL) -- what dsa_sparse_attn_paged reads.
+ *   DSA_CACHE_FP8:  latent e4m3 codes [n_rows][512], scale uint8 [n_rows][4], rope bf16 [n_rows][64]:
+ *     644 bytes a row instead of 1152.  Code c of dims [128 g, 128 g + 128) stands for
+ *     c * 2^(scale[g] - 127).  The exponent scale[g] - 127 is the smallest integer e with
+ *     amax <= 448 * 2^e, kept within [-100, 7]; codes are rounded to nearest even and saturate, so
+ *     a stored value is within 2^-4 of the value, or 2^-10 * 2^e near zero.  Powers of two make every
+ *     stored value exact in bf16.  A group holding a NaN or an infinity is stored as scale byte 255;
+ *     bytes above 134 read as NaN.
+ * All three arrays 16-byte aligned. */
+#define DSA_CACHE_BF16 0
+#define DSA_CACHE_FP8 1
+typedef struct dsa_latent_cache {
+  void* latent;
+  uint8_t* scale;
+  void* rope;
+  int32_t n_rows;     /* a multiple of DSA_PAGE_ROWS */
+  int32_t format;     /* DSA_CACHE_*                 */
+} dsa_latent_cache;
+
+#define DSA_CACHE_ROPE (1u << 8)   /* turn the last 64 dims at pos[t] before storing (with
+                                      DSA_ROPE_INTERLEAVED: that layout)                  */
+typedef struct dsa_cache_write_desc {
+  int32_t n_tokens;
+  uint32_t flags;       /* DSA_CACHE_ROPE, DSA_ROPE_INTERLEAVED                         */
+  int64_t kv_stride;    /* elements between tokens of kv: a multiple of 8, >= 576       */
+} dsa_cache_write_desc;
+
+/* Store kv[t] (bf16, 512 latent and 64 rotary dims) in cache row slot[t]; a negative slot stores
+ * nothing (a padded token).  Slots of one call must differ (two tokens with the same one leave a
+ * mixture of both in that row); rows without a token stay as they were.  With DSA_CACHE_ROPE the
+ * rotary dims are turned in fp32 and rounded once, as dsa_rope_apply does; pos and rope_cs (rope_dim
+ * 64) are then needed, else NULL.  A slot >= n_rows or a position outside the table stores nothing and
+ * is flagged (DSA_ERR_DEVICE).  ws: at least 256 bytes.
+ *   kv bf16, 16-byte aligned; slot int32 [n_tokens]; pos int32 [n_tokens].
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows not whole pages), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
+dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* desc, const void* kv, const int32_t* slot,
+                                  const int32_t* pos, const float* rope_cs, int32_t rope_n_pos,
+                                  const dsa_latent_cache* cache, void* ws, size_t ws_bytes, void* stream);
+
+/* Bring cached sequences back to contiguous bf16 rows (the kv that dsa_sparse_attn takes for their
+ * next prefill chunk): kv_out[row_start[t] + j] = row j of sequence t, for j < pages->seq_len[t],
+ * t < n_seq (block_table and seq_len hold n_seq rows).  Other rows of kv_out stay as they were;
+ * sequences whose output rows overlap leave a mixture.  A page outside the cache, or output rows
+ * outside [0, n_out), are skipped page by page and flagged; a length outside [0, max_pages *
+ * page_rows] is cut to it and flagged (DSA_ERR_DEVICE).  ws: at least 256 bytes.
+ *   row_start int32 [n_seq]; kv_out bf16 [n_out][576], 16-byte aligned.
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows != n_pages * page_rows, n_seq * max_pages beyond int32),
+ * DSA_ERR_UNSUPPORTED (page_rows), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
+dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_cache* pages, int32_t n_seq,
+                                 const int32_t* row_start, void* kv_out, int32_t n_out, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* Latent attention of one query row per block-table row over a paged latent cache, bf16 or fp8:
+ *   idx NULL: every logical key j < seq_len[t] (dense layers; prefixes no longer than index_topk,
+ *             where the selection is the whole prefix; verification of drafts as rows of their own,
+ *             each with its own length) -- desc->topk is not read;
+ *   idx given: the selected keys, as dsa_sparse_attn_paged, which serves a bf16 cache.
+ * o[t, h] = sum_j softmax_j(tau q[t, h] . kv_j) kv_j[:512] and its natural log-sum-exp, over the stored
+ * values; softmax weights are rounded to bf16 for the second product and divided by their own sum,
+ * lse sums the unrounded ones.  A row without keys gives o = 0 and lse = -inf.  Rows of a page past
+ * the sequence's end are never used, whatever they hold.  A page outside the cache, or (idx) an
+ * offset >= seq_len[t], is skipped and flagged; a length outside [0, max_pages * page_rows] is cut to
+ * it and flagged (DSA_ERR_DEVICE).  Results do not depend on the order in which CTAs run.
+ *   q bf16 [n_q][n_heads][576], out bf16 [n_q][n_heads][512], 16-byte aligned; lse f32 [n_q][n_heads]
+ *   or NULL; block_table and seq_len hold n_q rows; desc->n_kv == cache->n_rows.
+ * ws: dsa_latent_attn_workspace_size(desc) bytes.  Errors: those of dsa_sparse_attn_paged, DSA_ERR_ARG
+ * (the cache), DSA_ERR_SHAPE (n_q * n_heads beyond int32). */
+dsa_status dsa_latent_attn_workspace_size(const dsa_attn_desc* desc, size_t* bytes);
+dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
+                                 const int32_t* idx, const dsa_paged_cache* pages, void* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ MTP drafting ---- */
 
 /* One step of multi-step MTP drafting with IndexShare ([EX] "MTP path: IndexShare +
@@ -449,7 +590,8 @@ enum {
   DSA_PROF_ATTN = 5,          /* sparse attention kernel                                    */
   DSA_PROF_ATTN_BWD = 6,      /* sparse attention backward                                  */
   DSA_PROF_PROJ = 7,          /* indexer projections                                        */
-  DSA_PROF_INDEXER_BWD = 8    /* indexer backward                                           */
+  DSA_PROF_INDEXER_BWD = 8,   /* indexer backward                                           */
+  DSA_PROF_CACHE = 9          /* rotary positions, latent cache writing and reading         */
 };
 typedef struct dsa_profile_record {
   int32_t kind;   /* DSA_PROF_*                        */

@@ -1,0 +1,352 @@
+"""GPU tests of latent attention over a paged cache (dsa_latent_attn_paged) against float64, at the
+lengths, head counts and masks where it can go wrong.  Every unused cache row is NaN."""
+import numpy as np
+import pytest
+import torch
+
+import dsa_indexer_cross_gb300 as D
+from latent_cases import DEV, P, TAU, Paged, attend, check_rows, gen, i32, randn
+from oracle import latent_oracle as LO
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dsa_indexer_cross_gb300.build import build
+    build()
+    assert torch.cuda.is_available()
+
+
+def _dense(lens, H, fmt, seed=1, std=1.0, check=None):
+    pc = Paged(lens, fmt, seed=seed)
+    q = randn((len(lens), H, 576), gen(seed + 50), std)
+    out, lse, ws = attend(pc, q)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [pc.stored(t) if check is None or t in check else None for t in range(len(lens))])
+    return pc, q, out, lse
+
+
+EDGES = [0, 1, 2, 63, 64, 65, 127, 128, 129, 0, 191, 192, 193, 1000, 0]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H", [1, 3, 16, 17, 32, 33, 64, 65, 128])
+def test_every_key_at_edge_lengths(H, fmt):
+    _dense(EDGES, H, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,L", [(16, 1), (128, 64), (1, 700), (64, 9000), (128, 33333), (40, 20001)])
+def test_one_row_split_over_all_ctas(H, L, fmt):
+    _dense([L], H, fmt, seed=L)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_many_rows_and_uneven_lengths(fmt):
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 400, size=700).tolist()
+    lens[13], lens[500] = 12000, 7001
+    _dense(lens, 16, fmt, seed=9, check={0, 1, 12, 13, 14, 350, 499, 500, 501, 698, 699})
+
+
+def test_no_keys_at_all():
+    pc, q, out, lse = _dense([0, 0, 0], 24, "fp8")
+    assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+    desc = D.attn_desc(0, pc.n_pages * P, 16, 0, TAU)
+    e = torch.empty((0, 16, 576), dtype=torch.bfloat16, device=DEV)
+    D.dsa_latent_attn_paged(desc, e, pc.cache, None, pc.pages, torch.empty((0, 16, 512), dtype=torch.bfloat16, device=DEV))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_scores_that_keep_rising(fmt):
+    """Keys whose scores grow along the sequence: the running maximum moves in many tiles, in both
+    orders of the lengths, and weights underflow behind it."""
+    pc = Paged([2000, 900], fmt, seed=2)
+    q = randn((2, 33, 576), gen(3))
+    for t in range(2):
+        L = pc.lens[t]
+        ramp = torch.linspace(0.0, 30.0, L, device=DEV)[:, None]
+        if fmt == "bf16":
+            pc.kv[t] = (pc.kv[t].float() * 0.3 + ramp * q[t, 0].float() * (24.0 / 576)).to(torch.bfloat16)
+            pc.rows[pc.phys[t]] = pc.kv[t]
+        else:
+            from latent_cases import encode
+            kv = (pc.kv[t].float() * 0.3 + ramp * q[t, 0].float() * (24.0 / 576)).to(torch.bfloat16)
+            pc.codes[pc.phys[t]], pc.scale[pc.phys[t]] = encode(kv[:, :512])
+            pc.rope[pc.phys[t]] = kv[:, 512:]
+    out, lse, ws = attend(pc, q)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [pc.stored(0), pc.stored(1)])
+
+
+def test_fp8_equals_the_rows_read_back():
+    """Attention over the fp8 cache and over its rows read back into a bf16 cache: the same bits."""
+    lens = [5, 700, 0, 3000, 129]
+    pc = Paged(lens, "fp8", seed=6)
+    bf = Paged(lens, "bf16", seed=6)
+    start = np.concatenate([[0], np.cumsum(lens)[:-1]])
+    rows = torch.empty((sum(lens), 576), dtype=torch.bfloat16, device=DEV)
+    D.dsa_latent_cache_read(pc.cache, pc.pages, len(lens), i32(start), rows)
+    for t, L in enumerate(lens):
+        bf.rows[bf.phys[t]] = rows[start[t]:start[t] + L]
+    for H in (16, 128):
+        q = randn((len(lens), H, 576), gen(7))
+        a, b = attend(pc, q), attend(bf, q)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def _selection(lens, topk, seed, holes=False):
+    rng = np.random.default_rng(seed)
+    idx = np.full((len(lens), topk), -1, dtype=np.int32)
+    for t, L in enumerate(lens):
+        m = min(topk, L)
+        if holes:
+            m = m // 2
+        j = np.sort(rng.choice(L, size=m, replace=False)) if m else np.zeros(0, int)
+        if holes:      # unused slots anywhere, order arbitrary
+            at = rng.choice(topk, size=m, replace=False)
+            idx[t, at] = rng.permutation(j)
+        else:
+            idx[t, :m] = j
+    return idx
+
+
+@pytest.mark.parametrize("H", [1, 16, 33, 128])
+@pytest.mark.parametrize("topk,holes", [(1, False), (64, False), (100, True), (777, False), (2048, True)])
+def test_selected_keys_of_an_fp8_cache(H, topk, holes):
+    lens = [0, 1, 50, 64, 3000, 129, 0, 2048, 5000, 777]
+    pc = Paged(lens, "fp8", seed=topk)
+    q = randn((len(lens), H, 576), gen(topk + H))
+    idx = _selection(lens, topk, topk, holes)
+    out, lse, ws = attend(pc, q, i32(idx))
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [pc.stored(t)[idx[t][idx[t] >= 0]] for t in range(len(lens))])
+
+
+def test_selected_keys_of_a_bf16_cache_are_the_sparse_call():
+    lens = [900, 64, 3000]
+    pc = Paged(lens, "bf16", seed=3)
+    q = randn((3, 64, 576), gen(4))
+    idx = i32(_selection(lens, 256, 5))
+    out, lse, ws = attend(pc, q, idx)
+    assert D.dsa_workspace_status(ws) == 0
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    D.dsa_sparse_attn_paged(D.attn_desc(3, pc.n_pages * P, 64, 256, TAU), q, pc.rows, idx, pc.pages, o2, l2)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_whole_selection_is_every_key():
+    """An index row listing every key gives what the call without an index gives."""
+    lens = [300, 1024, 7]
+    pc = Paged(lens, "fp8", seed=12)
+    q = randn((3, 16, 576), gen(13))
+    idx = np.full((3, 1024), -1, dtype=np.int32)
+    for t, L in enumerate(lens):
+        idx[t, :L] = np.arange(L)
+    a, b = attend(pc, q), attend(pc, q, i32(idx))
+    kv = [pc.stored(t) for t in range(3)]
+    check_rows(a[0], a[1], q, kv)
+    check_rows(b[0], b[1], q, kv)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_pages_outside_the_cache_are_skipped_and_flagged(fmt):
+    pc = Paged([500, 128, 70], fmt, seed=5)
+    q = randn((3, 20, 576), gen(6))
+    bt = pc.bt.copy()
+    bt[0, 1], bt[1, 0] = pc.n_pages, -1
+    bt_d = i32(bt)
+    good = pc.pages
+    pc.pages = D.paged_cache(bt_d, pc.len_d, pc.n_pages)
+    out, lse, ws = attend(pc, q)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    k0 = pc.stored(0)
+    check_rows(out, lse, q, [np.concatenate([k0[:128], k0[256:]]), np.zeros((0, 576)), pc.stored(2)])
+    if fmt == "fp8":
+        idx = i32(np.array([[0, 130, 300, -1], [0, 1, 2, 3], [69, 70, 5, 100000]]))
+        out, lse, ws = attend(pc, q, idx, ws=ws)
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+        check_rows(out, lse, q, [k0[[0, 300]], np.zeros((0, 576)), pc.stored(2)[[69, 5]]])
+    # lengths outside the table are cut to it and flagged
+    pc.pages = good
+    full = Paged([256], fmt, seed=5, extra_cols=0)
+    ln = i32([300])
+    full.pages = D.paged_cache(full.bt_d, ln, full.n_pages)
+    out, lse, ws = attend(full, q[:1])
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+    check_rows(out, lse, q[:1], [full.stored(0)])
+    ln[0] = -1
+    out, lse, ws = attend(full, q[:1], ws=ws)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8 and torch.all(out == 0)
+
+
+def test_nan_and_infinity_in_a_used_row_reach_the_output():
+    pc = Paged([100, 100, 5000], "bf16", seed=1)
+    q = randn((3, 16, 576), gen(2))
+    pc.rows[pc.phys[1][50], 3] = float("nan")
+    pc.rows[pc.phys[2][4000], 3] = float("nan")
+    out, lse, _ = attend(pc, q)
+    check_rows(out, lse, q, [pc.stored(0), None, None])
+    assert torch.all(torch.isnan(out[1:])) and torch.all(torch.isnan(lse[1:]))
+
+
+def test_same_bits_every_time_without_lse_and_on_other_streams():
+    pc = Paged([3000, 77, 9000, 0, 640], "fp8", seed=21)
+    q = randn((5, 128, 576), gen(22))
+    ref, lse, _ = attend(pc, q)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for s in streams:                    # at the same time, a workspace each
+        with torch.cuda.stream(s):
+            got.append(attend(pc, q, lse=len(got) != 1))
+    torch.cuda.synchronize()
+    for o, l, _ in got:
+        assert torch.equal(o, ref) and (l is None or torch.equal(l, lse))
+
+
+def test_captured_call_follows_new_lengths_and_pages():
+    """Decode in a CUDA graph: the captured call reads lengths, pages and rows as they are at replay."""
+    pc = Paged([1, 500, 2000, 300], "fp8", seed=31, extra_cols=2)
+    q = randn((4, 64, 576), gen(32))
+    desc = D.attn_desc(4, pc.n_pages * P, 64, 0, TAU)
+    ws = torch.empty(D.dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=DEV)
+    out, lse, _ = attend(pc, q, ws=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            D.dsa_latent_attn_paged(desc, q, pc.cache, None, pc.pages, out, lse, ws=ws)
+    torch.cuda.synchronize()
+    for lens in ([1, 500, 2000, 300], [0, 1, 64, 2], [1, 130, 1999, 0], [1, 500, 1, 300]):
+        pc.len_d.copy_(i32(lens))
+        out.fill_(3.0)
+        graph.replay()
+        assert D.dsa_workspace_status(ws) == 0
+        check_rows(out, lse, q, [pc.stored(t)[:L] for t, L in enumerate(lens)])
+
+
+def test_rows_of_drafts_share_their_sequence():
+    """Verifying drafts: rows with the same pages and growing lengths, each causal."""
+    pc = Paged([1003], "bf16", seed=41)
+    bt = i32(np.repeat(pc.bt, 4, axis=0))
+    ln = i32([1000, 1001, 1002, 1003])
+    pc.pages = D.paged_cache(bt, ln, pc.n_pages)
+    q = randn((4, 16, 576), gen(42))
+    out, lse, ws = attend(pc, q)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [pc.stored(0)[:1000 + t] for t in range(4)])
+
+
+def test_long_cache_offsets_pass_32_bits():
+    """Rows whose byte and element offsets pass 2^31: the last pages of a 5 GB bf16 cache."""
+    n_pages = (1 << 31) // (P * 576) + 600           # 2^31 elements and more
+    rows = torch.full((n_pages * P, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    kv = randn((300, 576), gen(51))
+    bt = np.array([[n_pages - 1, 0, n_pages - 3]], dtype=np.int32)
+    for j, p in enumerate(bt[0]):
+        part = kv[j * P:(j + 1) * P]
+        rows[int(p) * P:int(p) * P + part.shape[0]] = part
+    bt_d, ln = i32(bt), i32([300])
+    q = randn((1, 128, 576), gen(52))
+    out = torch.empty((1, 128, 512), dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty((1, 128), device=DEV)
+    cache, pages = D.latent_cache(rows), D.paged_cache(bt_d, ln, n_pages)
+    ws = D.dsa_latent_attn_paged(D.attn_desc(1, n_pages * P, 128, 0, TAU), q, cache, None, pages, out, lse)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [kv.double().cpu().numpy()])
+    back = torch.empty_like(kv)
+    D.dsa_latent_cache_read(cache, pages, 1, i32([0]), back)
+    assert torch.equal(back, kv)
+    slot = i32([(n_pages - 2) * P + 5])
+    D.dsa_latent_cache_write(D.cache_write_desc(kv[:1]), kv[:1], slot, None, None, cache)
+    assert torch.equal(rows[(n_pages - 2) * P + 5], kv[0])
+
+
+def test_wait_that_runs_out_is_reported_and_the_next_call_is_clean():
+    for fmt in ("bf16", "fp8"):
+        pc = Paged([3000, 2000], fmt, seed=61)
+        q = randn((2, 64, 576), gen(62))
+        ref, lse, ws = attend(pc, q)
+        try:
+            D.dsa_debug_pipeline(stop_after_tiles=0, wait_ns=1_000_000)
+            attend(pc, q, ws=ws)
+            assert D.dsa_workspace_status(ws, raise_on_fault=False) & 1
+        finally:
+            D.dsa_debug_pipeline(-1, 0)
+        out, l2, _ = attend(pc, q, ws=ws)
+        assert D.dsa_workspace_status(ws) == 0
+        assert torch.equal(out, ref) and torch.equal(l2, lse)
+
+
+def test_a_decode_step_through_every_operator():
+    """Three decode steps as a server runs them: rotate the queries into the absorbed layout, write the
+    new rows rotated into their pages, attend over every key and over selected ones, and read the
+    sequences back for a prefill chunk."""
+    B, H, g = 6, 32, gen(71)
+    lens = np.array([0, 5, 127, 128, 600, 1500])
+    steps, cap = 3, 1500 + 3
+    cols = (cap + P - 1) // P
+    n_pages = B * cols + 1
+    bt = np.random.default_rng(7).permutation(n_pages)[:B * cols].reshape(B, cols).astype(np.int32)
+    bt_d, len_d = i32(bt), i32(lens)
+    codes = torch.full((n_pages * P, 512), 0x7F, dtype=torch.uint8, device=DEV)
+    scale = torch.full((n_pages * P, 4), 255, dtype=torch.uint8, device=DEV)
+    rope = torch.full((n_pages * P, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    cache, pages = D.latent_cache(codes, scale, rope), D.paged_cache(bt_d, len_d, n_pages)
+    tab = D.dsa_rope_table_scaled(1e4, 64, 2048, D.rope_scaling_yarn(4.0, 512)).to(DEV)
+    tab64 = tab.double().cpu().numpy()
+    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    hist = [[] for _ in range(B)]           # the rows each sequence was given, float64, unrotated
+
+    def slots(seqs, pos):
+        return i32(bt[seqs, pos // P].astype(np.int64) * P + pos % P)
+
+    def store(kv, seqs, pos):
+        D.dsa_latent_cache_write(D.cache_write_desc(kv, D.DSA_CACHE_ROPE | D.DSA_ROPE_INTERLEAVED), kv, slots(seqs, pos),
+                                 i32(pos), tab, cache, ws=ws)
+        assert D.dsa_workspace_status(ws) == 0
+        for r, t in zip(kv.double().cpu().numpy(), seqs):
+            hist[t].append(r)
+
+    for t in range(B):                       # the prompts
+        if lens[t]:
+            store(randn((int(lens[t]), 576), g), np.full(lens[t], t), np.arange(lens[t]))
+    for _ in range(steps):
+        store(randn((B, 576), g), np.arange(B), lens.copy())
+        lens += 1
+        len_d.copy_(i32(lens))
+        q = torch.empty((B, H, 576), dtype=torch.bfloat16, device=DEV)
+        q[..., :512] = randn((B, H, 512), g)
+        proj = randn((B, H, 192), g)
+        x, o = proj[..., 128:], q[..., 512:]
+        D.dsa_rope_apply(D.rope_desc(x, o, D.DSA_ROPE_INTERLEAVED), x, i32(lens - 1), tab, o, ws=ws)
+        turned = LO.rope(x.double().cpu().numpy(), tab64[lens - 1][:, None, :, 0], tab64[lens - 1][:, None, :, 1], True, False)
+        assert np.all(np.abs(o.double().cpu().numpy() - turned) <= 2.0 ** -7 * np.abs(turned) + 1e-5)
+        kv = []
+        for t in range(B):
+            h = np.stack(hist[t])
+            at = tab64[np.arange(lens[t])]
+            r = LO.rope(h[:, 512:], at[..., 0], at[..., 1], True, False)
+            c, s = LO.fp8_encode(h[:, :512])
+            ph = bt[t, np.arange(lens[t]) // P].astype(np.int64) * P + np.arange(lens[t]) % P
+            stored = rope[torch.as_tensor(ph, device=DEV)].double().cpu().numpy()
+            assert np.all(np.abs(stored - r) <= 2.0 ** -8 * np.abs(r) * (1 + 2.0 ** -7) + 2.0 ** -20)
+            kv.append(np.concatenate([LO.fp8_decode(c, s), stored], axis=1))
+        desc = D.attn_desc(B, n_pages * P, H, 100, TAU)
+        out = torch.empty((B, H, 512), dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty((B, H), device=DEV)
+        aws = D.dsa_latent_attn_paged(desc, q, cache, None, pages, out, lse)
+        assert D.dsa_workspace_status(aws) == 0
+        check_rows(out, lse, q, kv)
+        idx = _selection(lens, 100, int(lens[0]))
+        D.dsa_latent_attn_paged(desc, q, cache, i32(idx), pages, out, lse, ws=aws)
+        assert D.dsa_workspace_status(aws) == 0
+        check_rows(out, lse, q, [k[i[i >= 0]] for k, i in zip(kv, idx)])
+    start = np.concatenate([[0], np.cumsum(lens)[:-1]])
+    back = torch.empty((int(lens.sum()), 576), dtype=torch.bfloat16, device=DEV)
+    D.dsa_latent_cache_read(cache, pages, B, i32(start), back, ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    assert np.array_equal(back.double().cpu().numpy(), np.concatenate(kv))

@@ -1,0 +1,256 @@
+"""GPU tests of rotary positions and of the latent cache's writing and reading back, against the
+float64 definitions in oracle/latent_oracle.py.
+
+Tolerances.  A rotation is two fp32 products and a sum: |error| <= 2^-23 (|a c| + |b s|) + half a step
+of the output type (2^-8 of the value for bf16, 2^-24 for fp32).  Codes, scale bytes and rows read
+back are exact."""
+import numpy as np
+import pytest
+import torch
+
+import dsa_indexer_cross_gb300 as D
+from latent_cases import DEV, P, Paged, encode, gen, i32, randn
+from oracle import latent_oracle as LO
+
+pytestmark = pytest.mark.gpu
+THETA = 8e6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dsa_indexer_cross_gb300.build import build
+    build()
+    assert torch.cuda.is_available()
+
+
+def _check_turned(got, x, cs, inter, inverse, eps_half):
+    c, s = cs[..., 0], cs[..., 1]
+    want = LO.rope(x, c, s, inter, inverse)
+    mag = LO.rope(np.abs(x), np.abs(c), np.abs(s), inter, False)      # upper pair: |a||c| - |b||s|; use the sum
+    half = x.shape[-1] // 2
+    both = np.empty_like(mag)
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+        both[..., a] = np.abs(x[..., a] * c[..., i]) + np.abs(x[..., b] * s[..., i])
+        both[..., b] = np.abs(x[..., a] * s[..., i]) + np.abs(x[..., b] * c[..., i])
+    tol = 2.0 ** -23 * both + eps_half * np.abs(want) * (1 + 2.0 ** -7) + 1e-38
+    assert np.all(np.abs(got - want) <= tol), float(np.max(np.abs(got - want) / tol))
+
+
+# (tokens, heads, width in, offset in, width out, offset out, rope): vector paths, and every reason
+# to leave them (odd widths, unaligned offsets, rope not a multiple of the vector)
+ROPE_SHAPES = [(1, 1, 64, 0, 64, 0, 64), (3, 128, 192, 128, 576, 512, 64), (257, 5, 576, 512, 192, 128, 64),
+               (70, 4, 128, 64, 64, 0, 64), (9, 3, 66, 2, 70, 6, 64), (5, 2, 21, 1, 33, 3, 18), (4, 7, 2, 0, 2, 0, 2),
+               (33, 1, 40, 8, 24, 8, 16), (2, 3, 512, 0, 512, 0, 512), (6, 2, 104, 0, 104, 0, 100)]
+
+
+@pytest.mark.parametrize("dtype,eps_half", [(torch.bfloat16, 2.0 ** -8), (torch.float32, 2.0 ** -24)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("shape", ROPE_SHAPES)
+def test_rope_apply(shape, inter, inverse, dtype, eps_half):
+    n, h, wi, oi, wo, oo, r = shape
+    g = gen(n * 31 + h)
+    x = torch.randn((n, h, wi), generator=g, device=DEV).to(dtype)
+    out = torch.randn((n, h, wo), generator=g, device=DEV).to(dtype)
+    before = out.clone()
+    tab = D.dsa_rope_table(THETA, r, 3000).to(DEV)
+    pos = torch.randint(0, 3000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    pos[0] = 2999
+    xv, ov = x[..., oi:oi + r], out[..., oo:oo + r]
+    flags = (D.DSA_ROPE_INTERLEAVED if inter else 0) | (D.DSA_ROPE_INVERSE if inverse else 0)
+    ws = D.dsa_rope_apply(D.rope_desc(xv, ov, flags), xv, pos, tab, ov)
+    assert D.dsa_workspace_status(ws) == 0
+    cs = tab.double().cpu().numpy()[pos.cpu().numpy()][:, None]
+    _check_turned(ov.double().cpu().numpy(), xv.double().cpu().numpy(), cs, inter, inverse, eps_half)
+    before[..., oo:oo + r] = ov
+    assert torch.equal(before, out)                  # the other dims stay as they were
+    # in place gives the same bits
+    y = x.clone()
+    yv = y[..., oi:oi + r]
+    D.dsa_rope_apply(D.rope_desc(yv, yv, flags), yv, pos, tab, yv)
+    assert torch.equal(yv, ov)
+
+
+def test_rope_is_undone_by_its_inverse_and_is_its_own_gradient():
+    g = gen(5)
+    n, h = 40, 6
+    x, y = (torch.randn((n, h, 64), generator=g, device=DEV) for _ in range(2))
+    tab = D.dsa_rope_table_scaled(1e4, 64, 5000, D.rope_scaling_yarn(40.0, 4096)).to(DEV)
+    pos = torch.randint(0, 5000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    for flag in (0, D.DSA_ROPE_INTERLEAVED):
+        fx, back, gy = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+        D.dsa_rope_apply(D.rope_desc(x, fx, flag), x, pos, tab, fx)
+        inv = D.rope_desc(x, fx, flag | D.DSA_ROPE_INVERSE)
+        D.dsa_rope_apply(inv, fx, pos, tab, back)
+        # two rotations, each off by 2^-23 (|a| + |b|) + 2^-24, of values of at most |x| sqrt 2; the
+        # table's c^2 + s^2 is within 2^-22 of one
+        assert float((back - x).abs().max()) <= 2.0 ** -20 * float(x.abs().max())
+        D.dsa_rope_apply(inv, y, pos, tab, gy)
+        # the gradient of sum(y * rope(x)): central differences of a linear map are exact up to rounding
+        lhs, rhs = (fx.double() * y.double()).sum(), (x.double() * gy.double()).sum()
+        assert abs(float(lhs - rhs)) <= 2.0 ** -22 * float((fx.double().abs() * y.double().abs()).sum() * 4)
+        e = torch.zeros_like(x)
+        e[3, 2, 10] = 0.5
+        up, dn = torch.empty_like(x), torch.empty_like(x)
+        D.dsa_rope_apply(D.rope_desc(x, fx, flag), x + e, pos, tab, up)
+        D.dsa_rope_apply(D.rope_desc(x, fx, flag), x - e, pos, tab, dn)
+        slope = float(((up.double() - dn.double()) * y.double()).sum())
+        # two pairs' differences of values rounded to 2^-24 of at most 8
+        assert abs(slope - float(gy[3, 2, 10])) <= 2.0 ** -18 * (1 + float(y[3, 2].abs().max()))
+
+
+def test_rope_skips_and_flags_positions_outside_the_table():
+    x = torch.ones((4, 2, 64), device=DEV)
+    out = torch.full_like(x, 9.0)
+    tab = D.dsa_rope_table(THETA, 64, 10).to(DEV)
+    ws = D.dsa_rope_apply(D.rope_desc(x, out), x, i32([0, 10, -1, 3]), tab, out)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    assert torch.all(out[1:3] == 9.0) and torch.equal(out[0], x[0]) and not torch.any(out[3] == 9.0)
+    ws = D.dsa_rope_apply(D.rope_desc(x, out), x, i32([0, 9, 1, 3]), tab, out, ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    e = torch.empty((0, 2, 64), device=DEV)
+    D.dsa_rope_apply(D.rope_desc(e, e), e, i32([]), tab, e)
+
+
+def _write(kv, slot, fmt, n_pages, pos=None, tab=None, flags=0):
+    n_rows = n_pages * P
+    if fmt == "bf16":
+        bufs = [torch.full((n_rows, 576), 5.0, dtype=torch.bfloat16, device=DEV)]
+    else:
+        bufs = [torch.full((n_rows, 512), 0x31, dtype=torch.uint8, device=DEV),
+                torch.full((n_rows, 4), 99, dtype=torch.uint8, device=DEV),
+                torch.full((n_rows, 64), 5.0, dtype=torch.bfloat16, device=DEV)]
+    ws = D.dsa_latent_cache_write(D.cache_write_desc(kv, flags), kv, slot, pos, tab, D.latent_cache(*bufs))
+    return bufs, D.dsa_workspace_status(ws, raise_on_fault=False)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,stride,rot", [(1, 576, None), (7, 576, False), (129, 640, True), (300, 576, None), (64, 1152, False)])
+def test_cache_write(fmt, n, stride, rot):
+    """rot: None = stored as given, else turned in the half (False) or interleaved (True) layout."""
+    g = gen(n)
+    kv = randn((n, stride), g)[:, :576]
+    kv = kv * (10.0 ** torch.randint(-6, 5, (n, 1), generator=g, device=DEV)).to(torch.bfloat16)
+    kv = torch.nn.functional.pad(kv, (0, stride - 576))[:, :576]
+    assert n == 1 or kv.stride(0) == stride
+    n_pages = (n + P - 1) // P + 2
+    slot = torch.randperm(n_pages * P, generator=g, device=DEV)[:n].to(torch.int32)
+    if n > 5:
+        slot[2], slot[n - 1] = -1, -5
+    tab = D.dsa_rope_table(THETA, 64, 4000).to(DEV)
+    pos = torch.randint(0, 4000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    flags = 0 if rot is None else D.DSA_CACHE_ROPE | (D.DSA_ROPE_INTERLEAVED if rot else 0)
+    bufs, bits = _write(kv, slot, fmt, n_pages, pos if flags else None, tab if flags else None, flags)
+    assert bits == 0
+    keep = (slot >= 0).cpu().numpy()
+    at = slot.cpu().numpy()[keep].astype(np.int64)
+    x = kv.double().cpu().numpy()[keep]
+    rope = (bufs[0][:, 512:] if fmt == "bf16" else bufs[2]).double().cpu().numpy()
+    if rot is None:
+        assert np.array_equal(rope[at], x[:, 512:])
+    else:
+        _check_turned(rope[at], x[:, 512:], tab.double().cpu().numpy()[pos.cpu().numpy()[keep]], rot, False, 2.0 ** -8)
+    if fmt == "bf16":
+        assert np.array_equal(bufs[0][:, :512].double().cpu().numpy()[at], x[:, :512])
+    else:
+        codes, scale = LO.fp8_encode(x[:, :512])
+        assert np.array_equal(bufs[1].cpu().numpy()[at], scale)
+        assert np.array_equal(bufs[0].cpu().numpy()[at], codes)
+        c2, s2 = encode(kv[torch.as_tensor(keep, device=DEV)][:, :512])      # the helper the other tests use
+        assert np.array_equal(c2.cpu().numpy(), codes) and np.array_equal(s2.cpu().numpy(), scale)
+    other = np.ones(n_pages * P, dtype=bool)
+    other[at] = False
+    for b, v in zip(bufs, (5.0,) if fmt == "bf16" else (0x31, 99, 5.0)):
+        assert np.all(b.double().cpu().numpy()[other] == v)
+
+
+def test_cache_write_special_values():
+    kv = torch.zeros((8, 576), dtype=torch.bfloat16, device=DEV)
+    kv[0, 5] = float("inf")               # group 0 of token 0 becomes NaN, the others are zero
+    kv[1, 200] = float("nan")
+    kv[2, :] = 3.0e38                     # saturates
+    kv[3, :] = 2.0 ** -133                # the smallest bf16
+    kv[4, 0], kv[4, 1] = 448.0, 449.0     # scale borders
+    kv[5, 0] = 450.0
+    kv[6, 0], kv[6, 1], kv[6, 2] = 1.0, 2.0 ** -17, -(2.0 ** -19)      # subnormal codes and ties
+    kv[7, 512] = float("nan")             # the rotary dims are stored as they are
+    bufs, bits = _write(kv, i32(np.arange(8)), "fp8", 1)
+    assert bits == 0
+    x = kv.double().cpu().numpy()[:, :512]
+    codes, scale = LO.fp8_encode(x)
+    assert np.array_equal(bufs[1].cpu().numpy()[:8], scale)
+    assert np.array_equal(bufs[0].cpu().numpy()[:8], codes)
+    assert torch.isnan(bufs[2][7, 0])
+    out = torch.zeros((8, 576), dtype=torch.bfloat16, device=DEV)
+    bt, ln = i32([[0]]), i32([8])
+    D.dsa_latent_cache_read(D.latent_cache(*bufs), D.paged_cache(bt, ln, 1), 1, i32([0]), out)
+    y = out.double().cpu().numpy()[:, :512]
+    assert np.all(np.isnan(y[0, :128])) and np.all(y[0, 128:] == 0) and np.all(np.isnan(y[1, 128:256]))
+    assert np.all(y[2] == 57344.0) and np.all(y[3] == 0.0)
+
+
+def test_cache_write_skips_and_flags_bad_slots_and_positions():
+    g = gen(1)
+    kv = randn((4, 576), g)
+    tab = D.dsa_rope_table(THETA, 64, 10).to(DEV)
+    bufs, bits = _write(kv, i32([0, 128, 2, 3]), "bf16", 1, i32([0, 1, 10, -1]), tab, D.DSA_CACHE_ROPE)
+    assert bits == 2
+    assert torch.all(bufs[0][1:] == 5.0) and torch.equal(bufs[0][0, :512], kv[0, :512])
+
+
+def test_every_code_and_scale_reads_back_exactly():
+    """All 256 codes under every scale byte; the stored value is exact in bf16 wherever it is within
+    bf16's range."""
+    codes = torch.arange(512, device=DEV).remainder(256).to(torch.uint8).expand(256, 512).contiguous()
+    scale = torch.arange(256, device=DEV).to(torch.uint8)[:, None].expand(256, 4).contiguous()
+    rope = randn((256, 64), gen(2))
+    out = torch.zeros((256, 576), dtype=torch.bfloat16, device=DEV)
+    bt, ln = i32([[1, 0]]), i32([256])
+    D.dsa_latent_cache_read(D.latent_cache(codes, scale, rope), D.paged_cache(bt, ln, 2), 1, i32([0]), out)
+    back = torch.cat([out[128:], out[:128]])
+    assert torch.equal(back[:, 512:], rope)
+    got = back[:, :512].double().cpu().numpy()
+    for b in range(256):
+        if b > 134:
+            assert np.all(np.isnan(got[b]))
+            continue
+        want = LO.e4m3_values()[codes[b].cpu().numpy()] * 2.0 ** (b - 127)
+        fin = np.isfinite(want)                       # the writer never stores the NaN codes under these bytes
+        big = np.abs(want) >= 2.0 ** -126             # below, bf16's own subnormals
+        assert np.array_equal(got[b][fin & big], want[fin & big])
+        assert np.all(np.abs(got[b][fin] - want[fin]) <= 2.0 ** -134)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens", [[1], [0, 128, 129, 0, 1], [300, 1000, 127, 64], [0]])
+def test_cache_read(fmt, lens):
+    pc = Paged(lens, fmt, seed=sum(lens))
+    start = np.concatenate([[0], np.cumsum(lens)[:-1]]) + 3            # rows before and behind stay
+    start[-1] += 2
+    total = sum(lens) + 9
+    out = torch.full((total, 576), 4.0, dtype=torch.bfloat16, device=DEV)
+    ws = D.dsa_latent_cache_read(pc.cache, pc.pages, len(lens), i32(start), out)
+    assert D.dsa_workspace_status(ws) == 0
+    want = np.full((total, 576), 4.0)
+    for t, L in enumerate(lens):
+        want[start[t]:start[t] + L] = pc.stored(t)
+    assert np.array_equal(out.double().cpu().numpy(), want)
+
+
+def test_cache_read_skips_and_flags():
+    pc = Paged([200, 130, 5], "fp8", seed=8)
+    bt = pc.bt.copy()
+    bt[0, 1] = pc.n_pages                       # a page outside the cache: its rows are skipped
+    out = torch.full((400, 576), 4.0, dtype=torch.bfloat16, device=DEV)
+    bt_d = i32(bt)
+    start = i32([0, 272, 399])                  # sequence 1's second page and sequence 2 do not fit
+    ws = D.dsa_latent_cache_read(pc.cache, D.paged_cache(bt_d, pc.len_d, pc.n_pages), 3, start, out)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    o = out.double().cpu().numpy()
+    assert np.array_equal(o[:128], pc.stored(0)[:128]) and np.all(o[128:272] == 4.0)
+    assert np.array_equal(o[272:400], pc.stored(1)[:128])
+    # lengths outside the table are cut and flagged
+    ln = i32([-3, 100000, 5])
+    ws = D.dsa_latent_cache_read(pc.cache, D.paged_cache(pc.bt_d, ln, pc.n_pages), 1, i32([0]), out, ws=ws)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8

@@ -1,0 +1,240 @@
+"""Host-side checks of the latent cache's operators: RoPE table scalings, refused arguments, and the
+float64 definitions the GPU tests compare with.  Nothing here launches a kernel."""
+import ctypes as C
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import dsa_indexer_cross_gb300 as D
+from dsa_indexer_cross_gb300 import _lib
+from oracle import latent_oracle as LO
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dsa_indexer_cross_gb300.build import build
+    build()
+
+
+@pytest.mark.parametrize("kind,kw", [
+    ("none", {}), ("linear", dict(factor=4.0)), ("linear", dict(factor=1.0)),
+    ("yarn", dict(factor=40.0, orig_len=4096, beta_fast=32.0, beta_slow=1.0)),
+    ("yarn", dict(factor=8.0, orig_len=32768, beta_fast=16.0, beta_slow=2.0)),
+    ("yarn", dict(factor=2.0, orig_len=7, beta_fast=1.0, beta_slow=1.0)),
+])
+@pytest.mark.parametrize("theta,dim,mscale", [(1e4, 64, 1.0), (8e6, 64, 1.1386294), (1e4, 6, 0.5)])
+def test_scaled_rope_table(kind, kw, theta, dim, mscale):
+    f = LO.rope_frequencies(theta, dim, kind, **kw)
+    sc = {"none": lambda: D.RopeScaling(D.DSA_ROPE_SCALE_NONE, 0, 0.0, 0.0, 0.0, mscale),
+          "linear": lambda: D.rope_scaling_linear(mscale=mscale, **kw),
+          "yarn": lambda: D.rope_scaling_yarn(mscale=mscale, **kw)}[kind]()
+    n = 70000
+    tab = D.dsa_rope_table_scaled(theta, dim, n, sc).double().numpy()
+    for p in (0, 1, 77, 65536, n - 1):
+        # float64 angles differ by a few units of their last place; the table is rounded to 32 bits
+        tol = 2.0 ** -24 * mscale + 8 * 2.0 ** -52 * max(1.0, p)
+        assert np.all(np.abs(tab[p, :, 0] - mscale * np.cos(p * f)) <= tol)
+        assert np.all(np.abs(tab[p, :, 1] - mscale * np.sin(p * f)) <= tol)
+
+
+def test_unscaled_table_is_the_plain_table():
+    assert torch.equal(D.dsa_rope_table_scaled(8e6, 64, 1000), D.dsa_rope_table(8e6, 64, 1000))
+    none = D.RopeScaling(D.DSA_ROPE_SCALE_NONE, 0, 0.0, 0.0, 0.0, 1.0)
+    assert torch.equal(D.dsa_rope_table_scaled(8e6, 64, 1000, none), D.dsa_rope_table(8e6, 64, 1000))
+
+
+def test_yarn_keeps_fast_dims_and_interpolates_slow_ones():
+    f0, f = LO.rope_frequencies(1e4, 64), LO.rope_frequencies(1e4, 64, "yarn", 16.0, 4096)
+    assert f[0] == f0[0] and f[-1] == pytest.approx(f0[-1] / 16.0, rel=1e-12)
+    assert np.all(np.diff(f / f0) <= 1e-15)
+
+
+@pytest.mark.parametrize("bad", [dict(kind=3), dict(kind=-1), dict(mscale=0.0), dict(mscale=math.nan),
+                                 dict(factor=0.5), dict(orig_len=0), dict(beta_slow=0.0), dict(beta_fast=0.5)])
+def test_bad_scalings_are_refused(bad):
+    a = dict(kind=2, orig_len=4096, factor=4.0, beta_fast=32.0, beta_slow=1.0, mscale=1.0)
+    a.update(bad)
+    with pytest.raises(D.DsaError) as e:
+        D.dsa_rope_table_scaled(1e4, 64, 16, D.RopeScaling(*a.values()))
+    assert e.value.name == "DSA_ERR_ARG"
+
+
+def test_yarn_needs_a_base_above_one():
+    with pytest.raises(D.DsaError):
+        D.dsa_rope_table_scaled(1.0, 64, 16, D.rope_scaling_yarn(4.0, 4096))
+
+
+# ------------------------------------------------------------------ the definitions themselves
+
+def test_fp8_definition_matches_torch_and_rounds_within_half_a_step():
+    v = LO.e4m3_values()
+    t = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(v[~np.isnan(v)], t[~np.isnan(v)]) and np.array_equal(np.isnan(v), np.isnan(t))
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn((6, 512), generator=g) * torch.tensor([1e-30, 1e-3, 1.0, 30.0, 5e4, 3e38])[:, None]).to(torch.bfloat16)
+    x64 = x.double().numpy()
+    codes, scale = LO.fp8_encode(x64)
+    y = LO.fp8_decode(codes, scale)
+    e = scale.astype(np.float64).repeat(128, axis=1) - 127
+    # a group in which a draw passed bf16's range holds an infinity and is stored as NaN
+    finite = np.isfinite(x64).reshape(6, 4, 128).all(axis=2)
+    assert np.array_equal(scale == 255, ~finite) and np.all(np.isnan(y[~finite.repeat(128, axis=1)]))
+    ok = finite.repeat(128, axis=1)
+    inside = (np.abs(x64) <= 448.0 * 2.0 ** 7) & ok
+    err = np.abs(y - x64)
+    assert np.all(err[inside] <= np.maximum(np.abs(x64) * 2.0 ** -4, 2.0 ** -10 * 2.0 ** e)[inside])
+    assert np.all(np.abs(y[~inside & ok]) == 448.0 * 2.0 ** 7) and (~inside & ok).any()
+
+
+def test_rope_definition_inverse_and_adjoint():
+    rng = np.random.default_rng(0)
+    x, y = rng.standard_normal((5, 8)), rng.standard_normal((5, 8))
+    a = rng.standard_normal((5, 4))
+    for inter in (False, True):
+        fwd = LO.rope(x, np.cos(a), np.sin(a), inter, False)
+        assert np.allclose(LO.rope(fwd, np.cos(a), np.sin(a), inter, True), x, atol=1e-14)
+        # the inverse is the transpose, so it is the rotation's gradient
+        assert np.sum(fwd * y) == pytest.approx(np.sum(x * LO.rope(y, np.cos(a), np.sin(a), inter, True)), abs=1e-12)
+
+
+# ------------------------------------------------------------------ refused arguments
+
+def _status(fn, *args):
+    st = fn(*args)
+    return _lib.STATUS_NAMES[st], D.lib().dsa_last_error().decode()
+
+
+WS = 0x100000
+
+
+def _rope(**kw):
+    a = dict(n_tokens=4, n_heads=2, rope_dim=64, dtype=0, x_token_stride=128, x_head_stride=64, out_token_stride=128,
+             out_head_stride=64, flags=0)
+    a.update(kw)
+    return _lib.RopeDesc(*a.values())
+
+
+@pytest.mark.parametrize("kw,name", [
+    (dict(n_tokens=-1), "DSA_ERR_ARG"), (dict(n_heads=0), "DSA_ERR_ARG"), (dict(rope_dim=3), "DSA_ERR_ARG"),
+    (dict(rope_dim=0), "DSA_ERR_ARG"), (dict(rope_dim=514), "DSA_ERR_ARG"), (dict(dtype=2), "DSA_ERR_ARG"),
+    (dict(flags=4), "DSA_ERR_ARG"), (dict(x_token_stride=-1), "DSA_ERR_ARG"), (dict(out_head_stride=32), "DSA_ERR_ARG"),
+    (dict(out_token_stride=0), "DSA_ERR_ARG"), (dict(n_tokens=1 << 30, n_heads=4), "DSA_ERR_SHAPE"),
+])
+def test_rope_descriptors_refused(kw, name):
+    d = _rope(**kw)
+    assert _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x4000, WS, 256, None)[0] == name
+
+
+@pytest.mark.parametrize("x,pos,cs,n_pos,out,ws,ws_bytes,name", [
+    (None, 0x2000, 0x3000, 8, 0x4000, WS, 256, "DSA_ERR_ARG"), (0x1000, None, 0x3000, 8, 0x4000, WS, 256, "DSA_ERR_ARG"),
+    (0x1000, 0x2000, None, 8, 0x4000, WS, 256, "DSA_ERR_ARG"), (0x1000, 0x2000, 0x3000, 0, 0x4000, WS, 256, "DSA_ERR_ARG"),
+    (0x1000, 0x2000, 0x3000, 8, None, WS, 256, "DSA_ERR_ARG"), (0x1001, 0x2000, 0x3000, 8, 0x4000, WS, 256, "DSA_ERR_ARG"),
+    (0x1000, 0x2000, 0x3004, 8, 0x4000, WS, 256, "DSA_ERR_ARG"), (0x1000, 0x2000, 0x3000, 8, 0x4000, None, 256, "DSA_ERR_ARG"),
+    (0x1000, 0x2000, 0x3000, 8, 0x4000, WS + 16, 256, "DSA_ERR_ARG"), (0x1000, 0x2000, 0x3000, 8, 0x4000, WS, 255, "DSA_ERR_WORKSPACE"),
+])
+def test_rope_pointers_refused(x, pos, cs, n_pos, out, ws, ws_bytes, name):
+    d = _rope()
+    assert _status(D.lib().dsa_rope_apply, C.byref(d), x, pos, cs, n_pos, out, ws, ws_bytes, None)[0] == name
+
+
+def test_rope_in_place_needs_equal_strides():
+    d = _rope(out_token_stride=192)
+    assert _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x1000, WS, 256, None)[0] == "DSA_ERR_ARG"
+
+
+def _cache(**kw):
+    a = dict(latent=0x10000, scale=0x20000, rope=0x30000, n_rows=256, format=1)
+    a.update(kw)
+    return _lib.LatentCache(*a.values())
+
+
+BAD_CACHES = [
+    (dict(format=2), "DSA_ERR_ARG"), (dict(latent=None), "DSA_ERR_ARG"), (dict(scale=None), "DSA_ERR_ARG"),
+    (dict(rope=None), "DSA_ERR_ARG"), (dict(latent=0x10008), "DSA_ERR_ARG"), (dict(scale=0x20004), "DSA_ERR_ARG"),
+    (dict(n_rows=0), "DSA_ERR_SHAPE"), (dict(n_rows=200), "DSA_ERR_SHAPE"),
+]
+
+
+@pytest.mark.parametrize("kw,name", BAD_CACHES)
+def test_bad_caches_refused_everywhere(kw, name):
+    c = _cache(**kw)
+    w = _lib.CacheWriteDesc(4, 0, 576)
+    p = _lib.PagedCache(0x40000, 0x50000, 2, max(1, c.n_rows // 128), 128)
+    a = D.attn_desc(2, c.n_rows, 16, 0, 0.04)
+    L = D.lib()
+    assert _status(L.dsa_latent_cache_write, C.byref(w), 0x1000, 0x2000, None, None, 0, C.byref(c), WS, 256, None)[0] == name
+    assert _status(L.dsa_latent_cache_read, C.byref(c), C.byref(p), 2, 0x2000, 0x3000, 10, WS, 256, None)[0] == name
+    assert _status(L.dsa_latent_attn_paged, C.byref(a), 0x1000, C.byref(c), None, C.byref(p), 0x2000, None, WS, 1 << 40,
+                   None)[0] == name
+
+
+@pytest.mark.parametrize("desc,kv,slot,pos,cs,n_pos,name", [
+    ((-1, 0, 576), 0x1000, 0x2000, None, None, 0, "DSA_ERR_ARG"), ((4, 0, 575), 0x1000, 0x2000, None, None, 0, "DSA_ERR_ARG"),
+    ((4, 0, 580), 0x1000, 0x2000, None, None, 0, "DSA_ERR_ARG"), ((4, 2, 576), 0x1000, 0x2000, None, None, 0, "DSA_ERR_ARG"),
+    ((4, 0, 576), None, 0x2000, None, None, 0, "DSA_ERR_ARG"), ((4, 0, 576), 0x1000, None, None, None, 0, "DSA_ERR_ARG"),
+    ((4, 0, 576), 0x1008, 0x2000, None, None, 0, "DSA_ERR_ARG"), ((4, 256, 576), 0x1000, 0x2000, None, 0x4000, 8, "DSA_ERR_ARG"),
+    ((4, 256, 576), 0x1000, 0x2000, 0x3000, None, 8, "DSA_ERR_ARG"), ((4, 256, 576), 0x1000, 0x2000, 0x3000, 0x4000, 0, "DSA_ERR_ARG"),
+])
+def test_cache_write_refused(desc, kv, slot, pos, cs, n_pos, name):
+    d, c = _lib.CacheWriteDesc(*desc), _cache()
+    assert _status(D.lib().dsa_latent_cache_write, C.byref(d), kv, slot, pos, cs, n_pos, C.byref(c), WS, 256, None)[0] == name
+
+
+@pytest.mark.parametrize("pages,n_seq,start,out,n_out,name", [
+    ((0x4000, 0x5000, 2, 2, 64), 1, 0x2000, 0x3000, 9, "DSA_ERR_UNSUPPORTED"),
+    ((0x4000, 0x5000, 2, 3, 128), 1, 0x2000, 0x3000, 9, "DSA_ERR_SHAPE"),
+    ((None, 0x5000, 2, 2, 128), 1, 0x2000, 0x3000, 9, "DSA_ERR_ARG"),
+    ((0x4000, 0x5000, 0, 2, 128), 1, 0x2000, 0x3000, 9, "DSA_ERR_ARG"),
+    ((0x4000, 0x5000, 1 << 20, 2, 128), 1 << 20, 0x2000, 0x3000, 9, "DSA_ERR_SHAPE"),
+    ((0x4000, 0x5000, 1 << 25, 2, 128), 1, 0x2000, 0x3000, 9, "DSA_ERR_SHAPE"),
+    ((0x4000, 0x5000, 2, 2, 128), -1, 0x2000, 0x3000, 9, "DSA_ERR_ARG"),
+    ((0x4000, 0x5000, 2, 2, 128), 1, None, 0x3000, 9, "DSA_ERR_ARG"),
+    ((0x4000, 0x5000, 2, 2, 128), 1, 0x2000, 0x3008, 9, "DSA_ERR_ARG"),
+])
+def test_cache_read_refused(pages, n_seq, start, out, n_out, name):
+    c, p = _cache(), _lib.PagedCache(*pages)
+    assert _status(D.lib().dsa_latent_cache_read, C.byref(c), C.byref(p), n_seq, start, out, n_out, WS, 256, None)[0] == name
+
+
+@pytest.mark.parametrize("kw,idx,name", [
+    (dict(n_heads=129), None, "DSA_ERR_UNSUPPORTED"), (dict(d_qk=192), None, "DSA_ERR_UNSUPPORTED"),
+    (dict(n_kv=128), None, "DSA_ERR_SHAPE"), (dict(softmax_scale=0.0), None, "DSA_ERR_ARG"),
+    (dict(topk=0), 0x6000, "DSA_ERR_ARG"), (dict(flags=1), None, "DSA_ERR_ARG"), (dict(n_q=-1), None, "DSA_ERR_ARG"),
+    (dict(n_q=1 << 25, n_heads=128), None, "DSA_ERR_SHAPE"),
+])
+def test_latent_attention_refused(kw, idx, name):
+    a = dict(n_q=2, n_kv=256, n_heads=16, d_qk=576, d_v=512, topk=8, softmax_scale=0.04, flags=0)
+    a.update(kw)
+    d, c, p = _lib.AttnDesc(*a.values()), _cache(), _lib.PagedCache(0x4000, 0x5000, 2, 2, 128)
+    got = _status(D.lib().dsa_latent_attn_paged, C.byref(d), 0x1000, C.byref(c), idx, C.byref(p), 0x2000, None, WS, 1 << 40, None)
+    assert got[0] == name
+
+
+def test_latent_attention_workspace():
+    a = D.attn_desc(64, 1 << 20, 128, 0, 0.04)
+    n = D.dsa_latent_attn_workspace_size(a)
+    assert n % 256 == 0 and n > 152 * 128 * 2048       # the partial outputs of a fully split call
+    assert n < 64 << 20
+    with pytest.raises(D.DsaError):
+        D.dsa_latent_attn_workspace_size(D.attn_desc(64, 1 << 20, 0, 0, 0.04))
+
+
+def test_binding_checks_views():
+    x = torch.zeros((3, 2, 192), dtype=torch.bfloat16)
+    o = torch.zeros((3, 2, 576), dtype=torch.bfloat16)
+    d = D.rope_desc(x[..., 128:], o[..., 512:])
+    assert (d.x_token_stride, d.x_head_stride, d.out_token_stride, d.out_head_stride) == (384, 192, 1152, 576)
+    with pytest.raises(ValueError):
+        D.rope_desc(x, o)
+    with pytest.raises(ValueError):
+        D.rope_desc(x.half(), x.half())
+    with pytest.raises(ValueError):
+        D.rope_desc(x.transpose(1, 2)[:, :2], x.transpose(1, 2)[:, :2])
+    with pytest.raises(ValueError):      # host tensors are refused before their address is used
+        D.dsa_rope_apply(d, x[..., 128:], torch.zeros(3, dtype=torch.int32), D.dsa_rope_table(1e4, 64, 4), o[..., 512:])
+    with pytest.raises(ValueError):
+        D.cache_write_desc(torch.zeros((4, 640), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        D.latent_cache(torch.zeros((128, 512), dtype=torch.bfloat16))
