@@ -209,9 +209,23 @@ def _want(t: torch.Tensor, dtype, numel: int, name: str) -> None:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:      # the handle alone: a Stream object costs as much as a small launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _arg(t: torch.Tensor, dtype, numel: int, name: str) -> int:
+    """_want and _ptr in one, for the calls of a few microseconds."""
+    if t.dtype is not dtype or t.numel() < numel:
+        _want(t, dtype, numel, name)
+    if not t.is_cuda or not t.is_contiguous():
+        return _ptr(t)
+    return t.data_ptr()
+
+
+def _on_current_device(t: torch.Tensor) -> None:
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
 
 
 def _u8(types: Sequence[int]):
@@ -550,32 +564,40 @@ def rope_desc(x: torch.Tensor, out: torch.Tensor, flags: int = 0) -> RopeDesc:
                     os_[0], os_[1], flags)
 
 
+def _rope_view(t: torch.Tensor, desc: RopeDesc, token: int, head: int, name: str) -> int:
+    dt = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16
+    shape = (desc.n_tokens, desc.n_heads, desc.rope_dim)
+    if t.dtype is not dt or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA {dt} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    if t.stride() != (token, head, 1) and _heads_view(t, name) != (token, head):
+        raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's {(token, head)}")
+    return t.data_ptr()
+
+
 def dsa_rope_apply(desc: RopeDesc, x, pos, rope_cs, out, ws=None, stream=None) -> torch.Tensor:
     """out = x turned at pos (DSA_ROPE_INVERSE: by the negated angle, the gradient), [tokens, heads,
     rope_dim] views as the descriptor was made for."""
-    dt = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16
-    shape = (desc.n_tokens, desc.n_heads, desc.rope_dim)
-    for t, st, name in ((x, (desc.x_token_stride, desc.x_head_stride), "x"),
-                        (out, (desc.out_token_stride, desc.out_head_stride), "out")):
-        if t.dtype != dt or t.shape != shape or not t.is_cuda:
-            raise ValueError(f"{name}: expected a CUDA {dt} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-        if _heads_view(t, name) != st:
-            raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's {st}")
-    _want(pos, torch.int32, desc.n_tokens, "pos")
+    px = _rope_view(x, desc, desc.x_token_stride, desc.x_head_stride, "x")
+    po = _rope_view(out, desc, desc.out_token_stride, desc.out_head_stride, "out")
+    _on_current_device(out)
     n_pos = _rope_rows(rope_cs, desc.rope_dim)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=out.device)
-    _check(lib().dsa_rope_apply(C.byref(desc), x.data_ptr(), _ptr(pos), _ptr(rope_cs), n_pos, out.data_ptr(), _ptr(ws),
-                                ws.numel(), _stream(stream)))
+    st = (_lib or lib()).dsa_rope_apply(desc, px, _arg(pos, torch.int32, desc.n_tokens, "pos"), _ptr(rope_cs), n_pos, po,
+                                        _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
     return ws
 
 
 def _rope_rows(rope_cs: torch.Tensor, rope_dim: int) -> int:
     """Positions of a (cos, sin) table for rope_dim rotary dims."""
-    if rope_cs.dtype != torch.float32 or rope_cs.dim() != 3 or rope_cs.shape[1:] != (rope_dim // 2, 2):
+    s = rope_cs.shape
+    if rope_cs.dtype is not torch.float32 or len(s) != 3 or s[1] != rope_dim // 2 or s[2] != 2:
         raise ValueError(f"rope_cs: expected a float32 [positions, {rope_dim // 2}, 2] tensor, got {rope_cs.dtype} "
-                         f"{tuple(rope_cs.shape)}")
-    return rope_cs.shape[0]
+                         f"{tuple(s)}")
+    return s[0]
 
 
 # ------------------------------------------------------------------------------ latent cache
@@ -609,19 +631,22 @@ def dsa_latent_cache_write(desc: CacheWriteDesc, kv, slot, pos, rope_cs, cache: 
                            stream=None) -> torch.Tensor:
     """Store kv's rows in cache rows slot (negative: none), turned at pos with DSA_CACHE_ROPE."""
     n = desc.n_tokens
-    if kv.dtype != torch.bfloat16 or kv.shape != (n, 576) or kv.stride(1) != 1 or not kv.is_cuda:
+    if kv.dtype is not torch.bfloat16 or kv.shape != (n, 576) or not kv.is_cuda or kv.stride(1) != 1:
         raise ValueError(f"kv: expected a CUDA bf16 [{n}, 576] view with contiguous rows")
     if n > 1 and kv.stride(0) != desc.kv_stride:
         raise ValueError(f"kv: token stride {kv.stride(0)} is not the descriptor's {desc.kv_stride}")
-    _want(slot, torch.int32, n, "slot")
-    n_pos = 0
+    _on_current_device(kv)
+    n_pos, p_pos, p_cs = 0, None, None
     if desc.flags & DSA_CACHE_ROPE:
-        _want(pos, torch.int32, n, "pos")
-        n_pos = _rope_rows(rope_cs, 64)
+        p_pos = _arg(pos, torch.int32, n, "pos")
+        n_pos, p_cs = _rope_rows(rope_cs, 64), _ptr(rope_cs)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=kv.device)
-    _check(lib().dsa_latent_cache_write(C.byref(desc), kv.data_ptr(), _ptr(slot), _ptr(pos), _ptr(rope_cs), n_pos,
-                                        C.byref(cache), _ptr(ws), ws.numel(), _stream(stream)))
+    st = (_lib or lib()).dsa_latent_cache_write(desc, kv.data_ptr(), _arg(slot, torch.int32, n, "slot"), p_pos, p_cs,
+                                                n_pos, cache, _arg(ws, torch.uint8, 0, "ws"), ws.numel(),
+                                                _stream(stream))
+    if st:
+        _check(st)
     return ws
 
 
@@ -629,13 +654,17 @@ def dsa_latent_cache_read(cache: LatentCache, pages: PagedCache, n_seq: int, row
                           stream=None) -> torch.Tensor:
     """kv_out[row_start[t] + j] = row j of sequence t for every cached row of n_seq sequences, bf16."""
     _paged_args(pages)
-    _want(row_start, torch.int32, n_seq, "row_start")
-    if kv_out.dtype != torch.bfloat16 or kv_out.dim() != 2 or kv_out.shape[1] != 576:
-        raise ValueError(f"kv_out: expected bf16 [rows, 576], got {kv_out.dtype} {tuple(kv_out.shape)}")
+    s = kv_out.shape
+    if len(s) != 2 or s[1] != 576:
+        raise ValueError(f"kv_out: expected bf16 [rows, 576], got {kv_out.dtype} {tuple(s)}")
+    p_out = _arg(kv_out, torch.bfloat16, 0, "kv_out")
+    _on_current_device(kv_out)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=kv_out.device)
-    _check(lib().dsa_latent_cache_read(C.byref(cache), C.byref(pages), int(n_seq), _ptr(row_start), _ptr(kv_out),
-                                       kv_out.shape[0], _ptr(ws), ws.numel(), _stream(stream)))
+    st = (_lib or lib()).dsa_latent_cache_read(cache, pages, n_seq, _arg(row_start, torch.int32, n_seq, "row_start"),
+                                               p_out, s[0], _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
     return ws
 
 
@@ -649,17 +678,18 @@ def dsa_latent_attn_paged(desc: AttnDesc, q, cache: LatentCache, idx, pages: Pag
                           stream=None) -> torch.Tensor:
     """Latent attention of row t over its sequence's cached keys: all of them (idx None) or the
     selected ones."""
-    n_q, H = desc.n_q, desc.n_heads
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    for t, dt, n, name in ((q, bf, n_q * H * desc.d_qk, "q"), (idx, i32, n_q * desc.topk, "idx"),
-                           (out, bf, n_q * H * desc.d_v, "out"), (lse, f32, n_q * H, "lse")):
-        if t is not None:
-            _want(t, dt, n, name)
+    n = desc.n_q * desc.n_heads
+    p_q, p_out = _arg(q, torch.bfloat16, n * desc.d_qk, "q"), _arg(out, torch.bfloat16, n * desc.d_v, "out")
+    p_idx = None if idx is None else _arg(idx, torch.int32, desc.n_q * desc.topk, "idx")
+    p_lse = None if lse is None else _arg(lse, torch.float32, n, "lse")
+    _on_current_device(q)
     _paged_args(pages)
     if ws is None:
         ws = torch.empty(dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
-    _check(lib().dsa_latent_attn_paged(C.byref(desc), _ptr(q), C.byref(cache), _ptr(idx), C.byref(pages), _ptr(out),
-                                       _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+    st = (_lib or lib()).dsa_latent_attn_paged(desc, p_q, cache, p_idx, pages, p_out, p_lse,
+                                               _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
     return ws
 
 

@@ -162,12 +162,13 @@ dsa_status tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
 // {64, 64, 9} is a whole 64-row tile, landing in shared memory as nine 64-row x 128-byte
 // blocks (128-byte swizzle), the layout the attention kernel reads.  One copy per tile keeps
 // the TMA unit far busier than nine per-block copies.
-dsa_status tmap_kv_tiles(CUtensorMap* m, const void* base, uint64_t rows) {
+dsa_status tmap_kv_tiles(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows = 64,
+                         uint32_t box_blocks = 9) {
   auto fn = encode_fn();
   if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[3] = {64, rows, 9};
   cuuint64_t strides[2] = {576 * 2, 64 * 2};
-  cuuint32_t box[3] = {64, 64, 9};
+  cuuint32_t box[3] = {64, box_rows, box_blocks};
   cuuint32_t es[3] = {1, 1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -836,7 +837,7 @@ dsa_status dsa_rope_table_scaled(double theta, int32_t rope_dim, int32_t n_pos, 
 }
 
 namespace {
-// Common to the cache calls: a workspace for the status header, cleared on the stream.
+// Common to the cache calls: a workspace for the status header (the launchers clear or write it).
 dsa_status check_status_ws(const void* ws, size_t ws_bytes) {
   if (!ws || reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be non-NULL and 256-byte aligned");
   if (ws_bytes < kAlign) return fail(DSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, kAlign);
@@ -884,13 +885,11 @@ dsa_status dsa_rope_apply(const dsa_rope_desc* d, const void* x, const int32_t* 
   if (!aligned16(rope_cs)) return fail(DSA_ERR_ARG, "rope_cs must be 16-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
   const RopeApply a{x, out, d->n_tokens, d->n_heads, d->rope_dim, d->x_token_stride, d->x_head_stride,
                     d->out_token_stride, d->out_head_stride, d->dtype == DSA_F32,
                     (d->flags & DSA_ROPE_INTERLEAVED) != 0, (d->flags & DSA_ROPE_INVERSE) != 0};
   const int ps = prof_begin(kProfCache, st);
-  e = launch_rope_apply(a, pos, rope_cs, rope_n_pos, static_cast<uint32_t*>(ws), st);
+  const cudaError_t e = launch_rope_apply(a, pos, rope_cs, rope_n_pos, static_cast<uint32_t*>(ws), st);
   prof_end(ps, st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "rotary positions kernel");
 }
@@ -915,10 +914,8 @@ dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* d, const void* kv,
   if (rot && !aligned16(rope_cs)) return fail(DSA_ERR_ARG, "rope_cs must be 16-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
   const int ps = prof_begin(kProfCache, st);
-  e = launch_cache_write(c, kv, d->kv_stride, slot, pos, rot ? rope_cs : nullptr, rope_n_pos, d->n_tokens,
+  const cudaError_t e = launch_cache_write(c, kv, d->kv_stride, slot, pos, rot ? rope_cs : nullptr, rope_n_pos, d->n_tokens,
                          (d->flags & DSA_ROPE_INTERLEAVED) != 0, static_cast<uint32_t*>(ws), st);
   prof_end(ps, st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "cache write kernel");
@@ -933,8 +930,8 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
   PagedRows pg;
   if ((s = check_pages(pages, c.n_rows, &pg)) != DSA_OK) return s;
   if (n_seq < 0 || n_out < 0) return fail(DSA_ERR_ARG, "n_seq and n_out must be >= 0");
-  if (static_cast<long long>(n_seq) * pg.max_pages > 0x7FFFFFFFLL)
-    return fail(DSA_ERR_SHAPE, "n_seq * max_pages exceeds the int32 range");
+  if (static_cast<long long>(n_seq) * pg.max_pages > 0x1FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_seq * max_pages exceeds 2^29 - 1");
   if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
   if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
   if (n_seq == 0) return DSA_OK;
@@ -942,10 +939,8 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
   if (!aligned16(kv_out)) return fail(DSA_ERR_ARG, "kv_out must be 16-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
   const int ps = prof_begin(kProfCache, st);
-  e = launch_cache_read(c, pg, n_seq, row_start, n_out, kv_out, static_cast<uint32_t*>(ws), st);
+  const cudaError_t e = launch_cache_read(c, pg, n_seq, row_start, n_out, kv_out, static_cast<uint32_t*>(ws), st);
   prof_end(ps, st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "cache read kernel");
 }
@@ -995,15 +990,19 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   if ((s = check_device()) != DSA_OK) return s;
   const size_t need = kAlign + align_up(latent_attn_ws_bytes(d.n_q, d.n_heads));
   if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "attention workspace too small: %zu < %zu bytes", ws_bytes, need);
-  CUtensorMap tkv, tq;
+  CUtensorMap tkv, tv, tq;
   std::memset(&tkv, 0, sizeof(tkv));
-  if (!c.fp8 && (s = tmap_kv_tiles(&tkv, c.latent, static_cast<uint64_t>(c.n_rows))) != DSA_OK) return s;
+  std::memset(&tv, 0, sizeof(tv));
+  if (!c.fp8) {
+    const bool pair = d.n_heads > 64;
+    const uint64_t rows = static_cast<uint64_t>(c.n_rows);
+    if ((s = tmap_kv_tiles(&tkv, c.latent, rows, pair ? 32 : 64)) != DSA_OK) return s;
+    if (pair && (s = tmap_kv_tiles(&tv, c.latent, rows, 64, 4)) != DSA_OK) return s;
+  }
   if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
                      static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)
     return s;
-  cudaError_t e;
-  if ((e = cudaMemsetAsync(ws, 0, kAlign, st)) != cudaSuccess) return cuda_fail(e, "clear status");
-  e = launch_latent_attn(c, tkv, tq, pg, idx, d.n_q, d.n_heads, d.topk, d.softmax_scale, out, lse,
+  const cudaError_t e = launch_latent_attn(c, tkv, tv, tq, pg, idx, d.n_q, d.n_heads, d.topk, d.softmax_scale, out, lse,
                          static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "latent attention kernel");
 }

@@ -33,14 +33,18 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Four codes (one word) -> four bf16 values (two words), times the group's multiplier.  A code's
-// four exponent and three mantissa bits, moved to the low end of bf16's exponent field and the
-// high end of its mantissa, are the code's value times 2^-120 (an e4m3 subnormal becomes a bf16
-// subnormal); the multiply is exact.
+// Four codes (one word) -> four bf16 values (two words), times the group's multiplier.  A byte
+// permute sign-extends two codes to 16 bits; shifted left by four and masked, a code's exponent and
+// mantissa bits lie at the low end of bf16's exponent field and the high end of its mantissa, its
+// sign at the top: the code's value times 2^-120 (an e4m3 subnormal becomes a bf16 subnormal).  The
+// multiply is exact.  Two integer-pipe instructions a pair (the shift is a multiply-add): the
+// integer pipe runs at half rate and bounds a conversion that masks sign and magnitude apart.
 __device__ __forceinline__ void fp8x4_to_bf16(uint32_t w, uint32_t mult, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);   // code << 8 in each half
-  lo = bf16x2_mul((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), mult);
-  hi = bf16x2_mul((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), mult);
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(b) : "r"(w));
+  lo = bf16x2_mul((a * 16u) & 0x87F087F0u, mult);
+  hi = bf16x2_mul((b * 16u) & 0x87F087F0u, mult);
 }
 
 // Scale byte of a group whose largest |value| has the bf16 bits `top` (sign cleared; NaN and

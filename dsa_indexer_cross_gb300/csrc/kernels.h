@@ -252,12 +252,13 @@ cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_s
                               void* out, uint32_t* status, cudaStream_t st);
 
 // Latent attention over a paged cache: every key of row t's sequence (idx == nullptr), or the
-// offsets in idx [n_q][topk] (fp8 cache).  tmap_kv: bf16 cache as 64-row tiles (boxes {64, 64, 9});
+// offsets in idx [n_q][topk] (fp8 cache).  A bf16 cache is read through tmap_kv: up to 64 heads as
+// 64-row tiles (boxes {64, 64, 9}); above, boxes {64, 32, 9} in tmap_kv and {64, 64, 4} in tmap_v.
 // tmap_q: q as [n_q * n_heads][576], boxes {64, latent_attn_q_box_rows(n_heads)}.
 int latent_attn_q_box_rows(int n_heads);
 size_t latent_attn_ws_bytes(int n_q, int n_heads);
-cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_q,
-                               const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
+cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
+                               const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
                                void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
 
 int device_sm_count();

@@ -25,21 +25,13 @@
 
 #include <algorithm>
 
-#include "fp8.cuh"
-#include "kernels.h"
-#include "ptx.cuh"
+#include "latent_attn.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kRows = 64;
-constexpr int kDqk = 576;
-constexpr int kDv = 512;
-constexpr int kKB = kDqk / 64;
 constexpr int kBlkBytes = kRows * 128;
 constexpr int kTileBytes = kKB * kBlkBytes;
-constexpr int kPrefetch = 4;           // tiles between a tile's L2 prefetch and its load
-constexpr int kMinTiles = 2;           // a share holds at least this many tiles
 
 template <int HB, bool FP8>
 struct LCfg {
@@ -47,10 +39,16 @@ struct LCfg {
   static constexpr int DYN_SMEM = 1024 + 2 * kTileBytes + Q_BYTES;
   static constexpr int SW = HB >= 32 ? 8 : 4;          // softmax warps
   static constexpr int SOFT = 32 * SW;
-  static constexpr int NP = FP8 ? 4 : 1;               // producer warps
+  static constexpr int NP = FP8 ? 8 : 1;               // producer warps
   static constexpr int S_WARP = SW + NP;
   static constexpr int PV_WARP = S_WARP + 1;
-  static constexpr int THREADS = 32 * (SW + NP + 2);
+  // fp8 with eight softmax warps: two idle warps complete the MMA warps' warpgroup, and the
+  // producers' two tiles of codes in registers (96 a thread at launch) are paid for by that
+  // warpgroup: 8 * 96 + 8 * 120 + 4 * 48 = 20 * 96.
+  static constexpr bool REG_SPLIT = FP8 && SW == 8;
+  static constexpr int REG_LAUNCH = 96, REG_PROD = 120, REG_MMA = 48;
+  static constexpr int THREADS = 32 * (SW + NP + (REG_SPLIT ? 4 : 2));
+  static_assert(!REG_SPLIT || 8 * REG_LAUNCH + 8 * REG_PROD + 4 * REG_MMA <= 20 * REG_LAUNCH, "register split");
   static constexpr int CW = HB / (SW / 4);             // columns per softmax warp
   static constexpr int NR = CW / 8;
   static constexpr uint32_t TMEM_COLS = 6 * HB <= 128 ? 128 : 6 * HB <= 256 ? 256 : 512;
@@ -62,8 +60,8 @@ struct LShared {
   uint64_t full[2], empty[2];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, o_done[2], o_free, mma_done;
   uint32_t tmem_base, abort_flag, soft_abort;
-  int row0, tile0;
-  long long wsum[32];
+  CtaFaults faults;
+  Share share;
   alignas(16) float red[4][64];
   alignas(16) float red2[4][64];
   alignas(16) float m_used[64];
@@ -72,125 +70,6 @@ struct LShared {
   alignas(16) float alpha[64];
 };
 static_assert(LCfg<64, true>::DYN_SMEM + sizeof(LShared) <= 232448, "HB = 64 must fit in shared memory");
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.or.pred po, %2, %3, pi;\n selp.u32 %0, 1, 0, po;\n}\n"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 ldg_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void lrow16(float (&r)[16], const float* p) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
-    r[4 * i] = v.x;
-    r[4 * i + 1] = v.y;
-    r[4 * i + 2] = v.z;
-    r[4 * i + 3] = v.w;
-  }
-}
-
-struct LArgs {
-  const uint8_t* latent;       // bf16 rows (unused by the kernel: TMA), or e4m3 codes
-  const uint8_t* scale;
-  const uint16_t* rope;
-  const int32_t* idx;          // selected offsets [n_q][topk], or nullptr
-  const int32_t* row_nt;       // SEL: 64-slot tiles of each row
-  PagedRows pg;
-  uint16_t* out;
-  float* lse;
-  int n_q, H, topk, n_grp, n_hb;
-  float scale_log2;
-  int2* start;                 // [n_grp + 1]: (row, tile) each group starts at; [n_grp].x = groups in use
-  float* part_o;               // [n_grp * 2][H][512]
-  float* part_m;               // [3][n_grp * 2][H]: max in use (log2), sum of the rounded weights, plain sum
-  uint32_t* status;
-  unsigned long long wait_ns;
-  int stop_after;
-};
-
-__device__ __forceinline__ int row_len(const PagedRows& pg, int row) {
-  return max(0, min(__ldg(pg.seq_len + row), pg.max_pages << kPageShift));
-}
-template <bool SEL>
-__device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
-  if constexpr (SEL) return __ldg(a.row_nt + row);
-  return (row_len(a.pg, row) + kRows - 1) / kRows;
-}
-
-// The segments (consecutive tiles of one row) of this CTA's share, in order.
-struct Seg {
-  int row, i0, n;
-  bool whole;        // the row's every tile
-};
-template <bool SEL>
-struct Walk {
-  const LArgs& a;
-  int row, tile;
-  long long left;
-  __device__ __forceinline__ Walk(const LArgs& args, int r, int t, long long n) : a(args), row(r), tile(t), left(n) {}
-  __device__ __forceinline__ bool next(Seg& s) {
-    if (left <= 0) return false;
-    int T = row_tiles<SEL>(a, row);
-    while (T == 0) T = row_tiles<SEL>(a, ++row);
-    s.row = row;
-    s.i0 = tile;
-    s.n = static_cast<int>(min(static_cast<long long>(T - tile), left));
-    s.whole = tile == 0 && s.n == T;
-    left -= s.n;
-    ++row;
-    tile = 0;
-    return true;
-  }
-};
-
-// Block-table entries of one row, 32 pages at a time in the lanes of a warp (and the next 32).
-struct PageWindow {
-  const int32_t* bt;
-  int max_pages, base, cur, nxt;
-  __device__ __forceinline__ int load(int k) const {
-    const int p = k * 32 + static_cast<int>(threadIdx.x & 31);
-    return p < max_pages ? __ldg(bt + p) : -1;
-  }
-  __device__ __forceinline__ PageWindow(const PagedRows& pg, int row, int page)
-      : bt(pg.block_table + static_cast<size_t>(row) * pg.max_pages), max_pages(pg.max_pages), base(page >> 5) {
-    cur = load(base);
-    nxt = load(base + 1);
-  }
-  // page of logical page p, p within the current or the next 32; the whole warp calls it
-  __device__ __forceinline__ int get(int p) const { return __shfl_sync(0xffffffffu, (p >> 5) == base ? cur : nxt, p & 31); }
-  __device__ __forceinline__ void advance(int p) {
-    if ((p >> 5) != base) {
-      base = p >> 5;
-      cur = nxt;
-      nxt = load(base + 1);
-    }
-  }
-};
 
 template <int HB, bool FP8, bool SEL>
 __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
@@ -209,7 +88,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.full[s], C::NP);
+      mbar_init(&sh.full[s], FP8 ? 33 * C::NP : 1);      // fp8: each warp, and each thread's copies
       mbar_init(&sh.empty[s], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], C::SW);
@@ -222,6 +101,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     mbar_init(&sh.mma_done, 2);
     sh.abort_flag = 0;
     sh.soft_abort = 0;
+    sh.faults.bits = sh.faults.count = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -229,84 +109,26 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     tmem_alloc(&sh.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
-  // this group's share of the line of tiles: block scan over the rows' tile counts
-  const int per = (a.n_q + C::THREADS - 1) / C::THREADS;
-  const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
-  long long mine = 0;
-  for (int r = ra; r < rb; ++r) {
-    mine += row_tiles<SEL>(a, r);
-    if (blockIdx.x == 0) {
-      const int want = __ldg(a.pg.seq_len + r);
-      if (want < 0 || want > (a.pg.max_pages << kPageShift)) {
-        atomicOr(a.status, DEV_ERR_RANGE);
-        atomicAdd(a.status + 1, 1u);
-      }
-    }
-  }
-  long long pre = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += v;
-  }
-  if (lane == 31) sh.wsum[warp] = pre;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  long long total = 0;
-  pre -= mine;
-  for (int w = 0; w < C::THREADS / 32; ++w) {
-    if (w < warp) pre += sh.wsum[w];
-    total += sh.wsum[w];
-  }
-  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + kMinTiles - 1) / kMinTiles));
-  const long long first = grp < groups ? total * grp / groups : 0;
-  const long long share = grp < groups ? total * (grp + 1) / groups - first : 0;
-  if (share > 0 && pre <= first && first < pre + mine) {
-    long long at = pre;
-    int r = ra;
-    while (true) {
-      const int T = row_tiles<SEL>(a, r);
-      if (first < at + T) break;
-      at += T;
-      ++r;
-    }
-    sh.row0 = r;
-    sh.tile0 = static_cast<int>(first - at);
-    if (hb == 0) a.start[grp] = make_int2(r, static_cast<int>(first - at));
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.n_grp] = make_int2(groups, 0);
-  // rows without keys: zeros and -inf
-  for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
-    if (row_tiles<SEL>(a, t) != 0) continue;
-    uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.H * kDv);
-    for (int e = threadIdx.x; e < a.H * (kDv / 8); e += C::THREADS) o[e] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int h = threadIdx.x; h < a.H; h += C::THREADS) a.lse[static_cast<size_t>(t) * a.H + h] = -INFINITY;
-  }
+  if constexpr (SEL) grid_wait();        // the tile counts of the selections
+  grid_trigger();
+  const long long share = find_share<SEL, C::THREADS>(a, grp, hb == 0, sh.share, sh.faults);
   __syncthreads();
   const uint32_t tmem = sh.tmem_base;
-  Walk<SEL> walk(a, share > 0 ? sh.row0 : 0, share > 0 ? sh.tile0 : 0, share);
-  Seg sg;
-
-  // valid rows of tile i (absolute) of a row: past the length, or on a page outside the cache, none
-  auto tile_rows = [&](int len, int i, int page) -> int {
-    if (page < 0 || page >= a.pg.n_pages) return 0;
-    return max(0, min(kRows, len - i * kRows));
-  };
+  Walk<SEL> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
+  Seg sg{};
 
   if (warp >= C::SW && warp < C::S_WARP) {
     // ---------------------------------------------------------------- Q and the rows
+    if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REG_PROD>();
     const int pw = warp - C::SW;
     uint32_t g = 0, it = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, a.status, a.wait_ns));
+      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
     };
-    while (ok && walk.next(sg)) {
+    auto load_q = [&]() -> bool {      // warp 0: the segment's HB rows of q, once the previous ones are read
       if (pw == 0) {
-        if (it > 0) ok = wait(&sh.q_empty, (it - 1) & 1);
-        if (!ok) break;
+        if (it > 0 && !wait(&sh.q_empty, (it - 1) & 1)) return false;
         if (lane == 0) {
           const int qrow = sg.row * a.H + hb * HB;
           mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
@@ -316,28 +138,18 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         __syncwarp();
       }
       ++it;
-      if constexpr (!FP8) {
-        PageWindow win(a.pg, sg.row, sg.i0 >> 1);
-        const int last = sg.i0 + sg.n;
-        auto row_at = [&](int i, int page) { return (page << kPageShift) + (i & 1) * kRows; };
-        for (int i = sg.i0; i < last; ++i, ++g) {
-          win.advance(i >> 1);
-          const int page = win.get(i >> 1);
+      return true;
+    };
+    if constexpr (!FP8) {
+      while (ok && walk.next(sg)) {
+        if (!(ok = load_q())) break;
+        const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+        int ahead = __ldg(bt + (sg.i0 >> 1));
+        for (int n = 0; n < sg.n; ++n, ++g) {
+          const int i = sg.i0 + n, page = ahead;
+          if (n + 1 < sg.n) ahead = __ldg(bt + ((i + 1) >> 1));
           const bool bad = page < 0 || page >= a.pg.n_pages;
-          const int row = row_at(i, bad ? 0 : page);
-          if (hb == 0) {
-            // the tile kPrefetch ahead (at a segment's start, every tile up to it) comes to L2
-            // before its slot is free
-            for (int f = i == sg.i0 ? i + 1 : i + kPrefetch; f <= i + kPrefetch && f < last; ++f) {
-              const int fp = win.get(f >> 1);
-              if (lane == 0 && fp >= 0 && fp < a.pg.n_pages)
-                l2_prefetch(a.latent + static_cast<size_t>(row_at(f, fp)) * (kDqk * 2), kTileBytes);
-            }
-          }
-          if (bad && lane == 0 && hb == 0) {
-            atomicOr(a.status, DEV_ERR_BAD_INDEX);
-            atomicAdd(a.status + 1, 1u);
-          }
+          if (bad && lane == 0 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
           if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
             ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
             break;
@@ -345,129 +157,108 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           if (g >= 2 && !(ok = wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&sh.full[g & 1], kTileBytes);
-            tma_load_3d(sT + (g & 1) * kTileBytes, &tmap_kv, &sh.full[g & 1], 0, row, 0);
+            tma_load_3d(sT + (g & 1) * kTileBytes, &tmap_kv, &sh.full[g & 1], 0,
+                        bad ? 0 : (page << kPageShift) + (i & 1) * kRows, 0);
           }
           __syncwarp();
-        }
-      } else {
-        // warp pw converts row octets pw, pw + NP, ...; lane = (row of the octet, 16 codes of each
-        // 64-dim block).  Eight lanes of a store phase cover two rows x every other 16-byte
-        // chunk, which the swizzle spreads over all banks.
-        constexpr int K = 8 / C::NP;
-        const int c = lane & 3;
-        uint4 raw[K][8], rr[K][2];
-        uint32_t sc[K];
-        const int len = row_len(a.pg, sg.row);
-        const int last = sg.i0 + sg.n;
-        PageWindow win(a.pg, sg.row, SEL ? 0 : sg.i0 >> 1);
-        const int32_t* irow = SEL ? a.idx + static_cast<size_t>(sg.row) * a.topk : nullptr;
-        int jx[K], prow[K];
-        auto slot_idx = [&](int i) {       // SEL: this thread's offsets of tile i
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            const int s = i * kRows + 8 * (pw + C::NP * k) + (lane >> 2);
-            jx[k] = i < last && s < a.topk ? __ldg(irow + s) : -1;
-          }
-        };
-        auto resolve = [&](int i) {        // cache rows of tile i (-1: none)
-          if constexpr (SEL) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-              const int j = jx[k];
-              const int page = j >= 0 && j < len ? __ldg(win.bt + (j >> kPageShift)) : -1;
-              const bool in = page >= 0 && page < a.pg.n_pages;
-              if (j >= 0 && !in && c == 0 && hb == 0) {
-                atomicOr(a.status, DEV_ERR_BAD_INDEX);
-                atomicAdd(a.status + 1, 1u);
-              }
-              prow[k] = in ? (page << kPageShift) + (j & (kPageRows - 1)) : -1;
-            }
-          } else {
-            int nv = 0, page = -1;
-            if (i < last) {
-              win.advance(i >> 1);
-              page = win.get(i >> 1);
-              nv = tile_rows(len, i, page);
-              if (nv == 0 && lane == 0 && pw == 0 && hb == 0) {
-                atomicOr(a.status, DEV_ERR_BAD_INDEX);
-                atomicAdd(a.status + 1, 1u);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-              const int r = 8 * (pw + C::NP * k) + (lane >> 2);
-              prow[k] = r < nv ? (page << kPageShift) + (i & 1) * kRows + r : -1;
-            }
-          }
-        };
-        auto fetch = [&]() {
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            const bool in = prow[k] >= 0;
-            const size_t row = in ? prow[k] : 0;
-            const uint8_t* src = a.latent + row * kDv + c * 16;
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            sc[k] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row) : 0u;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) raw[k][b] = in ? ldg_once(src + b * 64) : z;
-            const uint16_t* rs = a.rope + row * 64 + c * 16;
-            rr[k][0] = in ? ldg_once(rs) : z;
-            rr[k][1] = in ? ldg_once(rs + 8) : z;
-          }
-        };
-        if constexpr (SEL) slot_idx(sg.i0);
-        resolve(sg.i0);
-        fetch();
-        if constexpr (SEL) slot_idx(sg.i0 + 1);
-        for (int i = sg.i0; i < last; ++i, ++g) {
-          if constexpr (!SEL) {
-            if (hb == 0 && pw == 0) {
-              for (int f = i == sg.i0 ? i + 2 : i + kPrefetch; f <= i + kPrefetch && f < last; ++f) {
-                const int fp = win.get(f >> 1);
-                if (lane == 0 && fp >= 0 && fp < a.pg.n_pages) {
-                  const size_t row = (static_cast<size_t>(fp) << kPageShift) + (f & 1) * kRows;
-                  l2_prefetch(a.latent + row * kDv, kRows * kDv);
-                  l2_prefetch(a.rope + row * 64, kRows * 128);
-                  l2_prefetch(a.scale + row * 4, kRows * 4);
-                }
-              }
-            }
-          }
-          if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
-            ok = false;   // test hook
-            break;
-          }
-          if (g >= 2 && !(ok = wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1))) break;
-          const uint32_t tile = smem_u32(sT + (g & 1) * kTileBytes);
-#pragma unroll
-          for (int k = 0; k < K; ++k) {
-            const int r = 8 * (pw + C::NP * k) + (lane >> 2);
-            const uint32_t d0 = tile + r * 128 + (((2 * c) ^ (r & 7)) << 4);
-            const uint32_t d1 = tile + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4);
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              const uint32_t m = fp8_mult((sc[k] >> (8 * (b >> 1))) & 0xFFu);
-              uint32_t o[8];
-              fp8x4_to_bf16(raw[k][b].x, m, o[0], o[1]);
-              fp8x4_to_bf16(raw[k][b].y, m, o[2], o[3]);
-              fp8x4_to_bf16(raw[k][b].z, m, o[4], o[5]);
-              fp8x4_to_bf16(raw[k][b].w, m, o[6], o[7]);
-              sts128(d0 + b * kBlkBytes, o[0], o[1], o[2], o[3]);
-              sts128(d1 + b * kBlkBytes, o[4], o[5], o[6], o[7]);
-            }
-            sts128(d0 + 8 * kBlkBytes, rr[k][0].x, rr[k][0].y, rr[k][0].z, rr[k][0].w);
-            sts128(d1 + 8 * kBlkBytes, rr[k][1].x, rr[k][1].y, rr[k][1].z, rr[k][1].w);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[g & 1]);
-          if (i + 1 < last) {
-            resolve(i + 1);
-            fetch();
-            if constexpr (SEL) slot_idx(i + 2);
-          }
         }
       }
+    }
+    if constexpr (FP8) {
+      // Warp pw converts the eight rows [8 pw, 8 pw + 8) of every tile; lane = (row, 16 codes of each
+      // 64-dim block).  Eight lanes of a store phase cover two rows x every other 16-byte chunk,
+      // which the swizzle spreads over all banks.  Codes are two tiles ahead in registers, and what
+      // it takes to find them is fetched ahead of that, one step a tile and across segments: the
+      // offset (four tiles ahead), its page (three), its codes (two).  The rotary dims, which need
+      // no conversion, are copied when the slot is free, out of L2.
+      const int r = 8 * pw + (lane >> 2), c = lane & 3;
+      uint4 raw[2][8];
+      uint32_t sc[2];
+      int at[2];                             // cache row of each set's tile, -1: zeros
+      Walk<SEL> aw(walk);
+      Seg as;
+      int ai = 0;
+      bool alive = aw.next(as);
+      int j1 = -1, row1 = 0, len1 = 0;       // offset known
+      int j2 = -1, page2 = -1;               // page known
+      bool past2 = false;
+      auto offset_step = [&]() {
+        j1 = -1;
+        if (!alive) return;
+        row1 = as.row;
+        const int s = (as.i0 + ai) * kRows + r;
+        j1 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row1) * a.topk + s) : -1;
+        len1 = row_len(a.pg, row1);
+        if (++ai == as.n) {
+          ai = 0;
+          alive = aw.next(as);
+        }
+      };
+      auto page_step = [&]() {       // (loads only: nothing here waits for them)
+        j2 = j1;
+        past2 = j1 >= len1;
+        page2 = -1;
+        if (j1 >= 0 && !past2)
+          page2 = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
+      };
+      auto fetch_step = [&](uint4 (&w)[8], uint32_t& scale, int& row_at) {
+        const bool in = static_cast<uint32_t>(page2) < static_cast<uint32_t>(a.pg.n_pages);
+        // a key on a page outside the cache, or (selected) past the end; the tile tail is neither
+        if (!in && j2 >= 0 && (SEL || (!past2 && r == 0)) && c == 0 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+        row_at = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : -1;
+        const size_t row = in ? row_at : 0;      // a row of the cache in any case: no branch around the loads
+        const uint8_t* src = a.latent + row * kDv + c * 16;
+        scale = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) w[b] = ldg_once(src + b * 64);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + row * 64));
+      };
+      offset_step();
+      page_step();
+      offset_step();
+      fetch_step(raw[0], sc[0], at[0]);
+      page_step();
+      offset_step();
+      fetch_step(raw[1], sc[1], at[1]);
+      page_step();
+      offset_step();
+      // one tile: registers -> the bf16 tile, then the registers' next fetch
+      auto tile_step = [&](uint4 (&w)[8], uint32_t& scale, int& row_at) -> bool {
+        if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
+        if (g >= 2 && !wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1)) return false;
+        const uint32_t tile = smem_u32(sT + (g & 1) * kTileBytes);
+        const uint32_t d0 = tile + r * 128 + (((2 * c) ^ (r & 7)) << 4);
+        const uint32_t d1 = tile + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4);
+        const uint16_t* rs = a.rope + static_cast<size_t>(max(row_at, 0)) * 64 + c * 16;
+        cp_async_16_zfill(d0 + 8 * kBlkBytes, rs, row_at >= 0);
+        cp_async_16_zfill(d1 + 8 * kBlkBytes, rs + 8, row_at >= 0);
+        cp_async_mbar_arrive(&sh.full[g & 1]);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          // a row without a key: times zero
+          const uint32_t m = row_at >= 0 ? fp8_mult((scale >> (8 * (b >> 1))) & 0xFFu) : 0u;
+          uint32_t o[8];
+          fp8x4_to_bf16(w[b].x, m, o[0], o[1]);
+          fp8x4_to_bf16(w[b].y, m, o[2], o[3]);
+          fp8x4_to_bf16(w[b].z, m, o[4], o[5]);
+          fp8x4_to_bf16(w[b].w, m, o[6], o[7]);
+          sts128(d0 + b * kBlkBytes, o[0], o[1], o[2], o[3]);
+          sts128(d1 + b * kBlkBytes, o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[g & 1]);
+        fetch_step(w, scale, row_at);
+        page_step();
+        offset_step();
+        ++g;
+        return true;
+      };
+      while (ok && walk.next(sg)) {
+        ok = load_q();
+        for (int n = 0; n < sg.n && ok; ++n) ok = (g & 1) ? tile_step(raw[1], sc[1], at[1]) : tile_step(raw[0], sc[0], at[0]);
+      }
+      cp_async_wait<0>();
     }
     // let every copy this CTA started land before its shared memory can be released
     if (pw == 0 && lane == 0) {
@@ -512,11 +303,11 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           rv0 = s0 < a.topk && in_cache(__ldg(irow + s0));
           rv1 = s1 < a.topk && in_cache(__ldg(irow + s1));
         } else {
-          const int nv = tile_rows(len, i, __ldg(bt + (i >> 1)));
+          const int nv = tile_rows(a, len, i, __ldg(bt + (i >> 1)));
           rv0 = r0 < nv;
           rv1 = r0 + 8 < nv;
         }
-        bool ok = mbar_wait_for(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, a.status, a.wait_ns);
+        bool ok = mbar_wait_for(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         float sc[4 * NR];   // [4k + j]: j = 0,1 row r0 columns 8k+cq, +1;  j = 2,3 row r0 + 8
         bool need = false;
@@ -557,7 +348,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             }
             // O^T may only be rescaled once the previous tile's PV has finished
             if (n > 0) {
-              ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, a.status, a.wait_ns);
+              ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok && lane == 0) sh.soft_abort = 1;
             }
@@ -658,7 +449,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           }
         }
       }
-      bool ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, a.status, a.wait_ns);
+      bool ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) sh.soft_abort = 1;
       named_bar_sync(1, kSoft);
@@ -728,17 +519,19 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       named_bar_sync(1, kSoft);        // per-column state may be reset now
     }
   } else {
-    // ---------------------------------------------------------------- MMA issuers
+    // ---------------------------------------------------------------- MMA issuers (and idle warps)
+    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REG_MMA>();
+    const bool issuer = warp <= C::PV_WARP;
     constexpr uint32_t id_qk = idesc_bf16_f32(64, HB, 0, 0);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, HB, 1, 1);
     const uint32_t st0 = smem_u32(sT);
     uint32_t g = 0, it = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, a.status, a.wait_ns));
+      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
     };
     const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    while (ok && walk.next(sg)) {
+    while (issuer && ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
         const int len = row_len(a.pg, sg.row);
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
@@ -746,9 +539,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           int nv = kRows;
-          if constexpr (!FP8) nv = tile_rows(len, sg.i0 + n, __ldg(bt + ((sg.i0 + n) >> 1)));
+          if constexpr (!FP8) nv = tile_rows(a, len, sg.i0 + n, __ldg(bt + ((sg.i0 + n) >> 1)));
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
           if (!(ok = wait(&sh.full[sb], (g >> 1) & 1))) break;
+          if constexpr (FP8) fence_proxy_async_smem();       // the rotary dims' cp.async copies
           if constexpr (!FP8) {
             if (nv < kRows) {
               // rows without a key become zeros in all nine blocks (a swizzled row is one
@@ -765,18 +559,16 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
           const uint32_t d_s = tmem + C::S_COL + sb * HB;
 #pragma unroll
-          for (int kb = 0; kb < kKB; ++kb) {
-#pragma unroll
-            for (int sub = 0; sub < 4; ++sub)
-              umma_bf16_elect(d_s, da + static_cast<uint64_t>((kb * kBlkBytes + sub * 32) >> 4),
-                              dq0 + static_cast<uint64_t>((kb * HB * 128 + sub * 32) >> 4), id_qk, (kb | sub) ? 1u : 0u);
-          }
+          for (int kb = 0; kb < kKB; ++kb)
+            umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
+                                     dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
           umma_commit_elect(&sh.s_full[sb]);
         }
         if (ok) umma_commit_elect(&sh.q_empty);
       } else {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           ok = wait(&sh.p_full, g & 1);
+          if constexpr (FP8) fence_proxy_async_smem();
           if (ok && n == 0 && it > 0) ok = wait(&sh.o_free, (it - 1) & 1);
           if (!ok) break;
           tc_fence_after();
@@ -785,12 +577,9 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           const uint64_t dp = sdesc_sw128(tb + (kKB - 1) * kBlkBytes, kBlkBytes, 1024);
           const uint32_t acc0 = n > 0 ? 1u : 0u;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int kq = 0; kq < kRows / 16; ++kq)
-              umma_bf16_elect(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes + kq * 2048) >> 4),
-                              dp + static_cast<uint64_t>((kq * 2048) >> 4), id_pv, kq > 0 ? 1u : acc0);
-          }
+          for (int b = 0; b < 4; ++b)      // four K steps of 16 rows (2048 B)
+            umma_bf16_x4_elect<128, 128>(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes) >> 4), dp, id_pv,
+                                         acc0);
           umma_commit_elect(&sh.empty[g & 1]);
           umma_commit_elect(&sh.o_done[g & 1]);
         }
@@ -798,12 +587,43 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       ++it;
     }
     // every MMA this warp issued has completed before TMEM is released
-    umma_commit_elect(&sh.mma_done);
-    mbar_drain(&sh.mma_done, 0, 200000000ull);
+    if (issuer) {
+      umma_commit_elect(&sh.mma_done);
+      mbar_drain(&sh.mma_done, 0, 200000000ull);
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == C::PV_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (threadIdx.x == 0) publish_faults(a, sh.faults);
+}
+
+// row_nt[t] = number of 64-slot tiles up to the last slot of idx row t holding an index >= 0; one
+// warp per row.
+__global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __restrict__ idx, int n_q, int topk,
+                                                             int32_t* __restrict__ row_nt) {
+  grid_trigger();
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= n_q) return;
+  const int32_t* irow = idx + static_cast<size_t>(t) * topk;
+  int last = -1;
+  if ((topk & 3) == 0 && (reinterpret_cast<uintptr_t>(idx) & 15) == 0) {
+    const int4* v = reinterpret_cast<const int4*>(irow);
+#pragma unroll 8
+    for (int s = lane; s < topk / 4; s += 32) {
+      const int4 q = __ldg(v + s);
+      if (q.x >= 0) last = 4 * s;
+      if (q.y >= 0) last = 4 * s + 1;
+      if (q.z >= 0) last = 4 * s + 2;
+      if (q.w >= 0) last = 4 * s + 3;
+    }
+  } else {
+#pragma unroll 8
+    for (int s = lane; s < topk; s += 32)
+      if (__ldg(irow + s) >= 0) last = s;
+  }
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0) row_nt[t] = (last + kRows) / kRows;
 }
 
 // Joins the partials of the rows that were split: block (b, h) takes the row that begins in group
@@ -811,6 +631,20 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 // and w_s = 2^(m_s - M): out = sum w_s O_s / sum w_s lr_s, lse = ln 2 (M + log2 sum w_s l_s).
 __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ LArgs a) {
   const int b = blockIdx.x, h = blockIdx.y;
+  grid_wait();
+  if (b == 0 && h == 0 && threadIdx.x < 32) {
+    uint32_t bits = 0, count = 0;
+    for (int i = threadIdx.x; i < a.n_cta; i += 32) {
+      bits |= a.err[2 * i];
+      count += a.err[2 * i + 1];
+    }
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (threadIdx.x == 0) {
+      a.status[0] = bits;
+      a.status[1] = count;
+    }
+  }
   const int groups = __ldg(&a.start[a.n_grp].x);
   if (b + 1 >= groups) return;
   const int2 s0 = a.start[b], s1 = a.start[b + 1];
@@ -857,7 +691,7 @@ int head_block(int n_heads) { return n_heads <= 16 ? 16 : n_heads <= 32 ? 32 : 6
 
 struct Layout {
   int n_hb, n_grp;
-  size_t off_start, off_m, off_o, total;
+  size_t off_err, off_start, off_m, off_o, total;
 };
 Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
   Layout L{};
@@ -868,6 +702,8 @@ Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
   L.n_grp = static_cast<int>(std::max(1LL, std::min<long long>(sms / L.n_hb, most)));
   const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t o = up(static_cast<size_t>(n_q) * sizeof(int32_t));           // row_nt (selected keys)
+  L.off_err = o;
+  o += up(static_cast<size_t>(L.n_grp) * L.n_hb * 2 * sizeof(uint32_t));
   L.off_start = o;
   o += up((static_cast<size_t>(L.n_grp) + 1) * sizeof(int2));
   L.off_m = o;
@@ -883,8 +719,16 @@ cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs&
   using C = LCfg<HB, FP8>;
   cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, SEL>>(C::DYN_SMEM);
   if (e != cudaSuccess) return e;
-  latent_attn_kernel<HB, FP8, SEL><<<a.n_grp * a.n_hb, C::THREADS, C::DYN_SMEM, st>>>(tkv, tq, a);
-  return cudaGetLastError();
+  if constexpr (C::REG_SPLIT) {
+    // the producers' setmaxnreg.inc waits for registers the block must hold from launch: refuse a
+    // build whose count would leave it waiting (looked up once)
+    static const int regs = [] {
+      cudaFuncAttributes fa{};
+      return cudaFuncGetAttributes(&fa, latent_attn_kernel<HB, FP8, SEL>) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < C::REG_LAUNCH) return cudaErrorInvalidConfiguration;
+  }
+  return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, SEL, 1, tkv, tq, a);
 }
 template <int HB>
 cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
@@ -901,8 +745,8 @@ size_t latent_attn_ws_bytes(int n_q, int n_heads) {
   return latent_layout(n_q, n_heads, 1LL << 24).total;
 }
 
-cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_q,
-                               const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
+cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
+                               const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
                                void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st) {
   const bool sel = idx != nullptr;
   const Layout L = latent_layout(n_q, n_heads, sel ? (topk + kRows - 1) / kRows : pg.max_pages * 2LL);
@@ -922,6 +766,8 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   a.topk = topk;
   a.n_grp = L.n_grp;
   a.n_hb = L.n_hb;
+  a.n_cta = L.n_grp * L.n_hb;
+  a.err = reinterpret_cast<uint32_t*>(base + L.off_err);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.start = reinterpret_cast<int2*>(base + L.off_start);
   a.part_m = reinterpret_cast<float*>(base + L.off_m);
@@ -932,20 +778,21 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   cudaError_t e;
   if (sel) {
     const int ps = prof_begin(kProfAttnPrep, st);
-    e = launch_row_tiles(idx, n_q, topk, reinterpret_cast<int32_t*>(base), st);
+    selected_tiles_kernel<<<(n_q + 3) / 4, 128, 0, st>>>(idx, n_q, topk, reinterpret_cast<int32_t*>(base));
+    e = cudaGetLastError();
     prof_end(ps, st);
     if (e != cudaSuccess) return e;
   }
   const int ps = prof_begin(kProfAttn, st);
-  switch (head_block(n_heads)) {
+  if (L.n_hb == 2) {
+    e = launch_latent_pair(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st);
+  } else switch (head_block(n_heads)) {
     case 16: e = launch_hb<16>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
     case 32: e = launch_hb<32>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
     default: e = launch_hb<64>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
   }
-  if (e == cudaSuccess && L.n_grp > 1) {
-    latent_join_kernel<<<dim3(L.n_grp - 1, n_heads), 128, 0, st>>>(a);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && a.n_cta > 1)
+    e = launch_pdl(latent_join_kernel, L.n_grp > 1 ? dim3(L.n_grp - 1, n_heads) : dim3(1, 1), 128, 0, st, true, 1, a);
   prof_end(ps, st);
   return e;
 }

@@ -1,0 +1,235 @@
+// Shared by the latent attention kernels: arguments, the split of the work over the cache's length,
+// and small helpers.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "fp8.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace dsa {
+
+constexpr int kRows = 64;              // latent rows per tile
+constexpr int kDqk = 576;
+constexpr int kDv = 512;
+constexpr int kKB = kDqk / 64;         // 64-dim blocks per row
+constexpr int kMinTiles = 2;           // a share holds at least this many tiles
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Programmatic dependent launch: let the next kernel's blocks be scheduled; wait for the previous
+// kernel's memory.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n bar.red.or.pred po, %2, %3, pi;\n selp.u32 %0, 1, 0, po;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ldg_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void lrow16(float (&r)[16], const float* p) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+    r[4 * i] = v.x;
+    r[4 * i + 1] = v.y;
+    r[4 * i + 2] = v.z;
+    r[4 * i + 3] = v.w;
+  }
+}
+
+struct LArgs {
+  const uint8_t* latent;       // bf16 rows (unused by the kernel: TMA), or e4m3 codes
+  const uint8_t* scale;
+  const uint16_t* rope;
+  const int32_t* idx;          // selected offsets [n_q][topk], or nullptr
+  const int32_t* row_nt;       // SEL: 64-slot tiles of each row
+  PagedRows pg;
+  uint16_t* out;
+  float* lse;
+  int n_q, H, topk, n_grp, n_hb;
+  float scale_log2;
+  int2* start;                 // [n_grp + 1]: (row, tile) each group starts at; [n_grp].x = groups in use
+  float* part_o;               // [n_grp * 2][H][512]
+  float* part_m;               // [3][n_grp * 2][H]: max in use (log2), sum of the rounded weights, plain sum
+  uint32_t* status;
+  uint32_t* err;               // [CTAs][2]: error bits, bad-index count
+  int n_cta;
+  unsigned long long wait_ns;
+  int stop_after;
+};
+
+__device__ __forceinline__ int row_len(const PagedRows& pg, int row) {
+  return max(0, min(__ldg(pg.seq_len + row), pg.max_pages << kPageShift));
+}
+template <bool SEL>
+__device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
+  if constexpr (SEL) return __ldg(a.row_nt + row);
+  return (row_len(a.pg, row) + kRows - 1) / kRows;
+}
+
+// The segments (consecutive tiles of one row) of this CTA's share, in order.
+struct Seg {
+  int row, i0, n;
+  bool whole;        // the row's every tile
+};
+template <bool SEL>
+struct Walk {
+  const LArgs& a;
+  int row, tile;
+  long long left;
+  __device__ __forceinline__ Walk(const LArgs& args, int r, int t, long long n) : a(args), row(r), tile(t), left(n) {}
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (left <= 0) return false;
+    int T = row_tiles<SEL>(a, row);
+    while (T == 0) T = row_tiles<SEL>(a, ++row);
+    s.row = row;
+    s.i0 = tile;
+    s.n = static_cast<int>(min(static_cast<long long>(T - tile), left));
+    s.whole = tile == 0 && s.n == T;
+    left -= s.n;
+    ++row;
+    tile = 0;
+    return true;
+  }
+};
+
+// Faults are collected per CTA; the CTAs' words are put together by the join kernel (or, when
+// there is one CTA, written as they are), so no clearing pass runs before the kernel.
+struct CtaFaults {
+  uint32_t bits, count;
+};
+__device__ __forceinline__ void report(CtaFaults& f, uint32_t bits) {
+  atomicOr(&f.bits, bits);
+  atomicAdd(&f.count, 1u);
+}
+__device__ __forceinline__ void publish_faults(const LArgs& a, const CtaFaults& f) {
+  uint32_t* w = gridDim.x == 1 ? a.status : a.err + 2 * blockIdx.x;
+  w[0] = f.bits;
+  w[1] = f.count;
+}
+
+// The share of group `grp`: a block scan over the rows' tile counts (the whole block calls it, with
+// a block-wide barrier inside and one needed behind it before row0 / tile0 are read).
+struct Share {
+  long long wsum[32];
+  int row0, tile0;
+};
+template <bool SEL, int THREADS>
+__device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool writes_start, Share& sh, CtaFaults& faults) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (a.n_q + THREADS - 1) / THREADS;
+  const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
+  long long mine = 0;
+  bool bad_len = false;
+  for (int r = ra; r < rb; ++r) {
+    mine += row_tiles<SEL>(a, r);
+    if (blockIdx.x == 0) {
+      const int want = __ldg(a.pg.seq_len + r);
+      if (want < 0 || want > (a.pg.max_pages << kPageShift)) bad_len = true;
+    }
+  }
+  long long pre = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) sh.wsum[warp] = pre;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (bad_len) report(faults, DEV_ERR_RANGE);
+  long long total = 0;
+  pre -= mine;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) pre += sh.wsum[w];
+    total += sh.wsum[w];
+  }
+  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + kMinTiles - 1) / kMinTiles));
+  const long long first = grp < groups ? total * grp / groups : 0;
+  const long long share = grp < groups ? total * (grp + 1) / groups - first : 0;
+  if (share > 0 && pre <= first && first < pre + mine) {
+    long long at = pre;
+    int r = ra;
+    while (true) {
+      const int T = row_tiles<SEL>(a, r);
+      if (first < at + T) break;
+      at += T;
+      ++r;
+    }
+    sh.row0 = r;
+    sh.tile0 = static_cast<int>(first - at);
+    if (writes_start) a.start[grp] = make_int2(r, static_cast<int>(first - at));
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.n_grp] = make_int2(groups, 0);
+  // rows without keys: zeros and -inf
+  for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
+    if (row_tiles<SEL>(a, t) != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.H * kDv);
+    for (int e = threadIdx.x; e < a.H * (kDv / 8); e += THREADS) o[e] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int h = threadIdx.x; h < a.H; h += THREADS) a.lse[static_cast<size_t>(t) * a.H + h] = -INFINITY;
+  }
+  return share;
+}
+
+// Valid rows of tile i of a row of `len` keys: none on a page outside the cache.
+__device__ __forceinline__ int tile_rows(const LArgs& a, int len, int i, int page) {
+  if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pg.n_pages)) return 0;
+  return max(0, min(kRows, len - i * kRows));
+}
+
+// A launch that may overlap the end of the previous kernel on the stream (which the kernel waits for
+// itself, grid_wait) when `after` is set; cluster > 1: clusters of that many CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool after, int cluster,
+                       A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (after) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The CTA-pair kernel for 65 .. 128 heads (latent_pair.cu).  tmap_s / tmap_v: a bf16 cache in boxes
+// {64, 32, 9} and {64, 64, 4}.
+cudaError_t launch_latent_pair(bool fp8, bool sel, const CUtensorMap& tmap_s, const CUtensorMap& tmap_v,
+                               const CUtensorMap& tmap_q, const LArgs& a, cudaStream_t st);
+
+}  // namespace dsa

@@ -65,6 +65,41 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   b = v;
 }
 
+// ---------------------------------------------------------------------------- status
+// Small calls (at most kSoleMost items to check) have no clearing pass before the kernel, which
+// costs as much as the kernel: block 0 checks every item and writes the status words itself, and
+// nothing else touches them.  Larger calls clear them first, and each block reports its own.
+constexpr int kSoleMost = 4096;
+
+__device__ __forceinline__ void report(uint32_t* status, bool sole, uint32_t bits) {
+  if (sole) return;
+  atomicOr(status, bits);
+  atomicAdd(status + 1, 1u);
+}
+// Block 0 of a call that writes the status words itself: check(i) gives item i's error bits.
+template <typename F>
+__device__ __forceinline__ void sole_status(uint32_t* status, int n, F check) {
+  __shared__ uint32_t s_bits, s_count;
+  if (threadIdx.x == 0) s_bits = s_count = 0u;
+  __syncthreads();
+  uint32_t bits = 0, count = 0;
+#pragma unroll 16
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint32_t e = check(i);
+    bits |= e;
+    count += e ? 1u : 0u;
+  }
+  if (bits) {
+    atomicOr(&s_bits, bits);
+    atomicAdd(&s_count, count);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    status[0] = s_bits;
+    status[1] = s_count;
+  }
+}
+
 // ---------------------------------------------------------------------------- rotary positions
 // A thread turns one 16-byte vector (interleaved: its own pairs) or one vector of each half
 // (half layout) of up to U heads of one token, so the token's (cos, sin) are loaded once for U
@@ -75,20 +110,22 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
                                                       const float2* __restrict__ cs, int n_pos, uint32_t n_items,
                                                       int n_heads, int head_groups, int rope, long long x_tok,
                                                       long long x_head, long long o_tok, long long o_head, float sgn,
-                                                      uint32_t* status) {
+                                                      uint32_t* status, int sole) {
   using E = Elem<T>;
   constexpr int V = E::VEC;
   constexpr int NP = INTER ? V / 2 : V;          // pairs of one head in this thread
+  if (sole && blockIdx.x == 0)
+    sole_status(status, sole, [&](int t) {
+      const int p = __ldg(pos + t);
+      return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
+    });
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t nv = static_cast<uint32_t>(rope) / (INTER ? V : 2 * V);
   const uint32_t v = item % nv, hg = (item / nv) % head_groups, t = item / (nv * head_groups);
   const int p = __ldg(pos + t);
   if (p < 0 || p >= n_pos) {
-    if (v == 0 && hg == 0) {
-      atomicOr(status, DEV_ERR_BAD_INDEX);
-      atomicAdd(status + 1, 1u);
-    }
+    if (v == 0 && hg == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
     return;
   }
   const T* xt = x + static_cast<long long>(t) * x_tok + v * V;
@@ -140,18 +177,21 @@ template <typename T, bool INTER>
 __global__ void __launch_bounds__(256) rope_apply_pair(const T* x, T* out, const int32_t* __restrict__ pos,
                                                        const float2* __restrict__ cs, int n_pos, uint32_t n_items,
                                                        int n_heads, int rope, long long x_tok, long long x_head,
-                                                       long long o_tok, long long o_head, float sgn, uint32_t* status) {
+                                                       long long o_tok, long long o_head, float sgn, uint32_t* status,
+                                                       int sole) {
   using E = Elem<T>;
+  if (sole && blockIdx.x == 0)
+    sole_status(status, sole, [&](int t) {
+      const int p = __ldg(pos + t);
+      return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
+    });
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t half = static_cast<uint32_t>(rope) / 2;
   const uint32_t i = item % half, h = (item / half) % n_heads, t = item / (half * n_heads);
   const int p = __ldg(pos + t);
   if (p < 0 || p >= n_pos) {
-    if (i == 0 && h == 0) {
-      atomicOr(status, DEV_ERR_BAD_INDEX);
-      atomicAdd(status + 1, 1u);
-    }
+    if (i == 0 && h == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
     return;
   }
   const uint32_t ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + half;
@@ -220,7 +260,14 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const uint16_t* __rest
                                                           const float2* __restrict__ cs, int n_pos, int n_tokens,
                                                           int n_rows, bool inter, uint8_t* __restrict__ latent,
                                                           uint8_t* __restrict__ scale, uint16_t* __restrict__ rope,
-                                                          uint32_t* status) {
+                                                          uint32_t* status, int sole) {
+  if (sole && blockIdx.x == 0)
+    sole_status(status, sole, [&](int i) {
+      const int s = __ldg(slot + i);
+      if (s < 0) return 0u;
+      const int p = ROT ? __ldg(pos + i) : 0;
+      return s >= n_rows || (ROT && (p < 0 || p >= n_pos)) ? DEV_ERR_BAD_INDEX : 0u;
+    });
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (t >= n_tokens) return;
@@ -232,10 +279,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const uint16_t* __rest
   if constexpr (ROT) p = __ldg(pos + t);
   if (s < 0) return;
   if (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) {
-    if (lane == 0) {
-      atomicOr(status, DEV_ERR_BAD_INDEX);
-      atomicAdd(status + 1, 1u);
-    }
+    if (lane == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
     return;
   }
   const uint4 turned = rope_vec<ROT>(r, lane, inter, cs + static_cast<size_t>(p) * (kRope / 2));
@@ -277,33 +321,38 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const uint16_t* __rest
 }
 
 // ---------------------------------------------------------------------------- reading rows back
-// One block per (sequence, page): its valid rows go to out rows row_start[t] + j.  A warp takes
-// four rows at a time, all their loads before the first store.
+// One block per kReadRows rows of a (sequence, page): its valid rows go to out rows row_start[t] + j.
+// A warp takes four rows, all their loads before the first store.
+constexpr int kReadRows = 32;
+constexpr int kReadSplit = kPageRows / kReadRows;
 template <bool FP8>
 __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restrict__ latent,
                                                          const uint8_t* __restrict__ scale,
                                                          const uint16_t* __restrict__ rope, const PagedRows pg,
                                                          const int32_t* __restrict__ row_start, int n_out,
-                                                         uint16_t* __restrict__ out, uint32_t* status) {
-  const int t = blockIdx.x / pg.max_pages, pl = blockIdx.x % pg.max_pages;
-  const int want = __ldg(pg.seq_len + t);
+                                                         uint16_t* __restrict__ out, uint32_t* status, int sole) {
   const int cap = pg.max_pages << kPageShift;
-  if (pl == 0 && threadIdx.x == 0 && (want < 0 || want > cap)) {
-    atomicOr(status, DEV_ERR_RANGE);
-    atomicAdd(status + 1, 1u);
-  }
-  const int n = min(want < cap ? want - (pl << kPageShift) : cap - (pl << kPageShift), kPageRows);
-  if (n <= 0) return;
-  const int page = __ldg(pg.block_table + static_cast<size_t>(t) * pg.max_pages + pl);
-  const long long o0 = static_cast<long long>(__ldg(row_start + t)) + (pl << kPageShift);
-  if (page < 0 || page >= pg.n_pages || o0 < 0 || o0 + n > n_out) {
-    if (threadIdx.x == 0) {
-      atomicOr(status, DEV_ERR_BAD_INDEX);
-      atomicAdd(status + 1, 1u);
-    }
-    return;
-  }
-  const size_t row0 = static_cast<size_t>(page) << kPageShift;
+  // valid rows of a page, its physical page and its first output row; the error bits, if any
+  auto place = [&](int blk, int& n, int& page, long long& o0) -> uint32_t {
+    const int t = blk / pg.max_pages, pl = blk % pg.max_pages;
+    const int want = __ldg(pg.seq_len + t);
+    const uint32_t range = pl == 0 && (want < 0 || want > cap) ? DEV_ERR_RANGE : 0u;
+    n = min(min(want, cap) - (pl << kPageShift), kPageRows);
+    if (n <= 0) return range;
+    page = __ldg(pg.block_table + static_cast<size_t>(t) * pg.max_pages + pl);
+    o0 = static_cast<long long>(__ldg(row_start + t)) + (pl << kPageShift);
+    return range | (page < 0 || page >= pg.n_pages || o0 < 0 || o0 + n > n_out ? DEV_ERR_BAD_INDEX : 0u);
+  };
+  int n = 0, page = 0;
+  long long o0 = 0;
+  if (sole && blockIdx.x == 0) sole_status(status, sole, [&](int b) { return place(b, n, page, o0); });
+  const uint32_t err = place(blockIdx.x / kReadSplit, n, page, o0);
+  const int part = blockIdx.x % kReadSplit * kReadRows;
+  if (err && part == 0 && threadIdx.x == 0) report(status, sole != 0, err);
+  n = min(n - part, kReadRows);
+  if (n <= 0 || (err & DEV_ERR_BAD_INDEX)) return;
+  o0 += part;
+  const size_t row0 = (static_cast<size_t>(page) << kPageShift) + part;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint4* dst = reinterpret_cast<uint4*>(out + static_cast<size_t>(o0) * kRow);
   if constexpr (!FP8) {
@@ -320,7 +369,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restri
         if (e + 256 * k < total) dst[e + 256 * k] = v[k];
     }
   } else {
-    for (int r0 = warp * 4; r0 < n; r0 += 32) {
+    const int r0 = warp * 4;
+    static_assert(kReadRows == 32, "eight warps of four rows");
+    if (r0 < n) {
       uint2 c[4][2];
       uint32_t sc[4];
 #pragma unroll
@@ -365,6 +416,9 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
   // thread indices are 32-bit: larger problems go in several launches
   const int most = static_cast<int>(std::max(1LL, std::min<long long>(a.n_tokens, 0x7FFFFF00LL / per)));
   const float sgn = a.inverse ? -1.f : 1.f;
+  const int sole = a.n_tokens <= kSoleMost ? a.n_tokens : 0;
+  cudaError_t e = sole ? cudaSuccess : cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
+  if (e != cudaSuccess) return e;
   for (int t0 = 0; t0 < a.n_tokens; t0 += most) {
     const int n = std::min(most, a.n_tokens - t0);
     const uint32_t items = static_cast<uint32_t>(per * n);
@@ -374,11 +428,11 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
     const float2* c2 = reinterpret_cast<const float2*>(cs);
     if (vec)
       rope_apply_vec<T, INTER, U><<<grid, 256, 0, st>>>(x, out, pos + t0, c2, n_pos, items, a.n_heads, groups, a.rope,
-                                                        a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status);
+                                                        a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole);
     else
       rope_apply_pair<T, INTER><<<grid, 256, 0, st>>>(x, out, pos + t0, c2, n_pos, items, a.n_heads, a.rope, a.x_tok,
-                                                      a.x_head, a.o_tok, a.o_head, sgn, status);
-    const cudaError_t e = cudaGetLastError();
+                                                      a.x_head, a.o_tok, a.o_head, sgn, status, sole);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (n == a.n_tokens) break;      // also keeps t0 + most inside int
   }
@@ -400,10 +454,15 @@ cudaError_t launch_cache_write(const LatentCache& c, const void* kv, long long k
                                const int32_t* pos, const float* cs, int n_pos, int n_tokens, bool interleaved,
                                uint32_t* status, cudaStream_t st) {
   const unsigned grid = (static_cast<unsigned>(n_tokens) + 7) / 8;
+  const int sole = n_tokens <= kSoleMost ? n_tokens : 0;
+  if (!sole) {
+    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
+    if (e != cudaSuccess) return e;
+  }
   const auto go = [&](auto kern) {
     kern<<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(kv), kv_stride, slot, pos,
                                reinterpret_cast<const float2*>(cs), n_pos, n_tokens, c.n_rows, interleaved, c.latent,
-                               c.scale, c.rope, status);
+                               c.scale, c.rope, status, sole);
     return cudaGetLastError();
   };
   if (c.fp8) return cs ? go(cache_write_kernel<true, true>) : go(cache_write_kernel<true, false>);
@@ -412,13 +471,19 @@ cudaError_t launch_cache_write(const LatentCache& c, const void* kv, long long k
 
 cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_seq, const int32_t* row_start, int n_out,
                               void* out, uint32_t* status, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(n_seq) * static_cast<unsigned>(pg.max_pages);
+  const unsigned n_pg = static_cast<unsigned>(n_seq) * static_cast<unsigned>(pg.max_pages);   // < 2^29: the ABI's check
+  const unsigned grid = n_pg * kReadSplit;
+  const int sole = n_pg <= kSoleMost ? static_cast<int>(n_pg) : 0;
+  if (!sole) {
+    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
+    if (e != cudaSuccess) return e;
+  }
   if (c.fp8)
     cache_read_kernel<true><<<grid, 256, 0, st>>>(c.latent, c.scale, c.rope, pg, row_start, n_out,
-                                                  static_cast<uint16_t*>(out), status);
+                                                  static_cast<uint16_t*>(out), status, sole);
   else
     cache_read_kernel<false><<<grid, 256, 0, st>>>(c.latent, c.scale, c.rope, pg, row_start, n_out,
-                                                   static_cast<uint16_t*>(out), status);
+                                                   static_cast<uint16_t*>(out), status, sole);
   return cudaGetLastError();
 }
 

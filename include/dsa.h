@@ -499,7 +499,7 @@ dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* desc, const void* 
  * outside [0, n_out), are skipped page by page and flagged; a length outside [0, max_pages *
  * page_rows] is cut to it and flagged (DSA_ERR_DEVICE).  ws: at least 256 bytes.
  *   row_start int32 [n_seq]; kv_out bf16 [n_out][576], 16-byte aligned.
- * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows != n_pages * page_rows, n_seq * max_pages beyond int32),
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows != n_pages * page_rows, n_seq * max_pages >= 2^29),
  * DSA_ERR_UNSUPPORTED (page_rows), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
 dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_cache* pages, int32_t n_seq,
                                  const int32_t* row_start, void* kv_out, int32_t n_out, void* ws, size_t ws_bytes,
