@@ -42,11 +42,10 @@ struct LCfg {
   static constexpr int NP = FP8 ? 8 : 1;               // producer warps
   static constexpr int S_WARP = SW + NP;
   static constexpr int PV_WARP = S_WARP + 1;
-  // fp8 with eight softmax warps: two idle warps complete the MMA warps' warpgroup, and the
-  // producers' two tiles of codes in registers (96 a thread at launch) are paid for by that
-  // warpgroup: 8 * 96 + 8 * 120 + 4 * 48 = 20 * 96.
+  // fp8 with eight softmax warps: two idle warps complete the MMA warps' warpgroup, which pays for
+  // the producers' codes in registers: 8 * 96 + 8 * 112 + 4 * 64 = 20 * 96.
   static constexpr bool REG_SPLIT = FP8 && SW == 8;
-  static constexpr int REG_LAUNCH = 96, REG_PROD = 120, REG_MMA = 48;
+  static constexpr int REG_LAUNCH = 96, REG_PROD = 112, REG_MMA = 64;
   static constexpr int THREADS = 32 * (SW + NP + (REG_SPLIT ? 4 : 2));
   static_assert(!REG_SPLIT || 8 * REG_LAUNCH + 8 * REG_PROD + 4 * REG_MMA <= 20 * REG_LAUNCH, "register split");
   static constexpr int CW = HB / (SW / 4);             // columns per softmax warp
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.full[s], FP8 ? 33 * C::NP : 1);      // fp8: each warp, and each thread's copies
+      mbar_init(&sh.full[s], FP8 ? 33 * (C::NP / 2) : 1);      // fp8: each warp of the group, and each thread's copies
       mbar_init(&sh.empty[s], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], C::SW);
@@ -121,28 +120,13 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     // ---------------------------------------------------------------- Q and the rows
     if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REG_PROD>();
     const int pw = warp - C::SW;
-    uint32_t g = 0, it = 0;
+    uint32_t g = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
     };
-    auto load_q = [&]() -> bool {      // warp 0: the segment's HB rows of q, once the previous ones are read
-      if (pw == 0) {
-        if (it > 0 && !wait(&sh.q_empty, (it - 1) & 1)) return false;
-        if (lane == 0) {
-          const int qrow = sg.row * a.H + hb * HB;
-          mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
-#pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb) tma_load_2d(sQ + kb * (HB * 128), &tmap_q, &sh.q_full, kb * 64, qrow);
-        }
-        __syncwarp();
-      }
-      ++it;
-      return true;
-    };
     if constexpr (!FP8) {
       while (ok && walk.next(sg)) {
-        if (!(ok = load_q())) break;
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
         int ahead = __ldg(bt + (sg.i0 >> 1));
         for (int n = 0; n < sg.n; ++n, ++g) {
@@ -165,105 +149,127 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       }
     }
     if constexpr (FP8) {
-      // Warp pw converts the eight rows [8 pw, 8 pw + 8) of every tile; lane = (row, 16 codes of each
-      // 64-dim block).  Eight lanes of a store phase cover two rows x every other 16-byte chunk,
-      // which the swizzle spreads over all banks.  Codes are two tiles ahead in registers, and what
-      // it takes to find them is fetched ahead of that, one step a tile and across segments: the
-      // offset (four tiles ahead), its page (three), its codes (two).  The rotary dims, which need
-      // no conversion, are copied when the slot is free, out of L2.
-      const int r = 8 * pw + (lane >> 2), c = lane & 3;
-      uint4 raw[2][8];
-      uint32_t sc[2];
-      int at[2];                             // cache row of each set's tile, -1: zeros
+      // Two groups of four warps take the tiles in turn, so one group's loads are in flight while the
+      // other converts; a warp takes sixteen rows of its group's tiles.  (One group with two tiles in
+      // flight per warp was slower: a wait for any result also waited for the other tile's loads.)
+      // A load instruction takes 256 bytes of two rows, whole 128-byte lines; eight lanes of a store
+      // phase cover two rows x every other 16-byte chunk, which the swizzle spreads over all banks.
+      // Lane l looks after row l & 15: its offset is found two of the group's tiles ahead, its page
+      // one, its codes as soon as the registers are free, across segments.  The rotary dims, which
+      // need no conversion, are copied when the slot is free, out of L2.
+      const uint32_t turn = pw >> 2;                                      // tiles with g & 1 == turn, in slot `turn`
+      const int row_base = 16 * (pw & 3), my_row = row_base + (lane & 15);
+      const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4 (+ 4), row parity
+      uint4 w[16];
+      uint32_t sc = 0;                       // scale word and cache row (-1: zeros) of row lane & 15
+      int at = -1;
       Walk<SEL> aw(walk);
       Seg as;
       int ai = 0;
       bool alive = aw.next(as);
+      int len0 = alive ? row_len(a.pg, as.row) : 0;
       int j1 = -1, row1 = 0, len1 = 0;       // offset known
       int j2 = -1, page2 = -1;               // page known
       bool past2 = false;
+      auto advance = [&]() {
+        if (alive && ++ai == as.n) {
+          ai = 0;
+          alive = aw.next(as);
+          if (alive) len0 = row_len(a.pg, as.row);
+        }
+      };
       auto offset_step = [&]() {
         j1 = -1;
         if (!alive) return;
         row1 = as.row;
-        const int s = (as.i0 + ai) * kRows + r;
+        len1 = len0;
+        const int s = (as.i0 + ai) * kRows + my_row;
         j1 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row1) * a.topk + s) : -1;
-        len1 = row_len(a.pg, row1);
-        if (++ai == as.n) {
-          ai = 0;
-          alive = aw.next(as);
-        }
+        advance();
+        advance();
       };
-      auto page_step = [&]() {       // (loads only: nothing here waits for them)
+      auto page_step = [&]() {
         j2 = j1;
         past2 = j1 >= len1;
         page2 = -1;
         if (j1 >= 0 && !past2)
           page2 = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
       };
-      auto fetch_step = [&](uint4 (&w)[8], uint32_t& scale, int& row_at) {
+      auto fetch_step = [&]() {
         const bool in = static_cast<uint32_t>(page2) < static_cast<uint32_t>(a.pg.n_pages);
-        // a key on a page outside the cache, or (selected) past the end; the tile tail is neither
-        if (!in && j2 >= 0 && (SEL || (!past2 && r == 0)) && c == 0 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
-        row_at = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : -1;
-        const size_t row = in ? row_at : 0;      // a row of the cache in any case: no branch around the loads
-        const uint8_t* src = a.latent + row * kDv + c * 16;
-        scale = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row);
+        // a key on a page outside the cache, or (selected) past the end; the tile's tail is neither
+        if (!in && j2 >= 0 && (SEL || (!past2 && my_row == 0)) && lane < 16 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+        at = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : -1;
+        const int safe = max(at, 0);           // a row of the cache in any case: no branch around the loads
+        int from[8];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) w[b] = ldg_once(src + b * 64);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + row * 64));
+        for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, safe, 2 * k + par);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint8_t* src = a.latent + static_cast<size_t>(from[k]) * kDv + blk4 * 64 + c * 16;
+          w[2 * k] = ldg_once(src);
+          w[2 * k + 1] = ldg_once(src + 256);
+        }
+        sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + safe);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(safe) * 64));
       };
+      if (turn) advance();
       offset_step();
       page_step();
       offset_step();
-      fetch_step(raw[0], sc[0], at[0]);
+      fetch_step();
       page_step();
       offset_step();
-      fetch_step(raw[1], sc[1], at[1]);
-      page_step();
-      offset_step();
+      const uint32_t tile = smem_u32(sT + turn * kTileBytes);
       // one tile: registers -> the bf16 tile, then the registers' next fetch
-      auto tile_step = [&](uint4 (&w)[8], uint32_t& scale, int& row_at) -> bool {
+      auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
-        if (g >= 2 && !wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1)) return false;
-        const uint32_t tile = smem_u32(sT + (g & 1) * kTileBytes);
-        const uint32_t d0 = tile + r * 128 + (((2 * c) ^ (r & 7)) << 4);
-        const uint32_t d1 = tile + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4);
-        const uint16_t* rs = a.rope + static_cast<size_t>(max(row_at, 0)) * 64 + c * 16;
-        cp_async_16_zfill(d0 + 8 * kBlkBytes, rs, row_at >= 0);
-        cp_async_16_zfill(d1 + 8 * kBlkBytes, rs + 8, row_at >= 0);
-        cp_async_mbar_arrive(&sh.full[g & 1]);
+        if (g >= 2 && !wait(&sh.empty[turn], ((g >> 1) - 1) & 1)) return false;
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          // a row without a key: times zero
-          const uint32_t m = row_at >= 0 ? fp8_mult((scale >> (8 * (b >> 1))) & 0xFFu) : 0u;
-          uint32_t o[8];
-          fp8x4_to_bf16(w[b].x, m, o[0], o[1]);
-          fp8x4_to_bf16(w[b].y, m, o[2], o[3]);
-          fp8x4_to_bf16(w[b].z, m, o[4], o[5]);
-          fp8x4_to_bf16(w[b].w, m, o[6], o[7]);
-          sts128(d0 + b * kBlkBytes, o[0], o[1], o[2], o[3]);
-          sts128(d1 + b * kBlkBytes, o[4], o[5], o[6], o[7]);
+        for (int k = 0; k < 4; ++k) {
+          const int q = 4 * k + (lane >> 3), r = row_base + q;            // row, 16-byte chunk lane & 7
+          const int from = __shfl_sync(0xffffffffu, at, q);
+          cp_async_16_zfill(tile + 8 * kBlkBytes + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+                            a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
+        }
+        cp_async_mbar_arrive(&sh.full[turn]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = row_base + 2 * k + par;
+          const uint32_t rsc = __shfl_sync(0xffffffffu, sc, 2 * k + par);
+          const bool in = __shfl_sync(0xffffffffu, at, 2 * k + par) >= 0;
+          const uint32_t ch0 = ((2 * c) ^ (r & 7)) << 4, ch1 = ((2 * c + 1) ^ (r & 7)) << 4;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // a row without a key: times zero
+            const uint32_t m = in ? fp8_mult((rsc >> (16 * h + 8 * (blk4 >> 1))) & 0xFFu) : 0u;
+            const uint4 v = w[2 * k + h];
+            uint32_t o[8];
+            fp8x4_to_bf16(v.x, m, o[0], o[1]);
+            fp8x4_to_bf16(v.y, m, o[2], o[3]);
+            fp8x4_to_bf16(v.z, m, o[4], o[5]);
+            fp8x4_to_bf16(v.w, m, o[6], o[7]);
+            const uint32_t d = tile + (4 * h + blk4) * kBlkBytes + r * 128;
+            sts128(d + ch0, o[0], o[1], o[2], o[3]);
+            sts128(d + ch1, o[4], o[5], o[6], o[7]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[g & 1]);
-        fetch_step(w, scale, row_at);
+        if (lane == 0) mbar_arrive(&sh.full[turn]);
+        fetch_step();
         page_step();
         offset_step();
-        ++g;
         return true;
       };
-      while (ok && walk.next(sg)) {
-        ok = load_q();
-        for (int n = 0; n < sg.n && ok; ++n) ok = (g & 1) ? tile_step(raw[1], sc[1], at[1]) : tile_step(raw[0], sc[0], at[0]);
-      }
+      while (ok && walk.next(sg))
+        for (int n = 0; n < sg.n && ok; ++n, ++g)
+          if ((g & 1) == turn) ok = tile_step();
       cp_async_wait<0>();
     }
     // let every copy this CTA started land before its shared memory can be released
-    if (pw == 0 && lane == 0) {
-      if (it > 0) mbar_drain(&sh.q_full, (it - 1) & 1, 200000000ull);
-      if constexpr (!FP8)
+    if constexpr (!FP8) {
+      if (lane == 0)
         for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full[j & 1], (j >> 1) & 1, 200000000ull);
     }
   } else if (warp < C::SW) {
@@ -535,7 +541,17 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       if (warp == C::S_WARP) {
         const int len = row_len(a.pg, sg.row);
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+        // the segment's HB rows of q, once the previous ones have been read
+        if (it > 0 && !(ok = wait(&sh.q_empty, (it - 1) & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
+#pragma unroll 1
+          for (int kb = 0; kb < kKB; ++kb)
+            tma_load_2d(sQ + kb * (HB * 128), &tmap_q, &sh.q_full, kb * 64, sg.row * a.H + hb * HB);
+        }
+        __syncwarp();
         ok = wait(&sh.q_full, it & 1);
+        if (!ok && lane == 0) mbar_drain(&sh.q_full, it & 1, 200000000ull);   // the copy lands before we leave
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           int nv = kRows;

@@ -47,10 +47,10 @@ struct PCfg {
   static constexpr int NP = FP8 ? 8 : 2;         // converters, or the TMA warp and the one behind it
   static constexpr int S_WARP = kSW + NP;
   static constexpr int PV_WARP = S_WARP + 1;
-  // fp8: two idle warps complete the MMA warps' warpgroup, which pays for the converters' two tiles of
-  // codes in registers: 8 * 96 + 8 * 120 + 4 * 48 = 20 * 96.
+  // fp8: two idle warps complete the MMA warps' warpgroup, which pays for the converters' codes in
+  // registers: 8 * 96 + 8 * 112 + 4 * 64 = 20 * 96.
   static constexpr bool REG_SPLIT = FP8;
-  static constexpr int REG_LAUNCH = 96, REG_PROD = 120, REG_MMA = 48;
+  static constexpr int REG_LAUNCH = 96, REG_PROD = 112, REG_MMA = 64;
   static constexpr int THREADS = 32 * (PV_WARP + (REG_SPLIT ? 3 : 1));
   static_assert(8 * REG_LAUNCH + 8 * REG_PROD + 4 * REG_MMA <= 20 * REG_LAUNCH, "register split");
 };
@@ -77,36 +77,15 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on the leader's copy of `bar`.
+// Arrive on the leader's copy of `bar`.  What the arrival publishes lies in this CTA's own shared
+// memory and TMEM and is read there by this SM's tensor core, so the order within the CTA is enough
+// (fence.proxy.async, tcgen05 fences and the CTA-scope release before it); a cluster-scope release took
+// about 1100 cycles on the path from one tile to the next.
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}\n" ::"r"(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(
           smem_u32(bar))
       : "memory");
-}
-// Bounded wait that also sees what the other CTA's arrivals released.
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                             uint32_t* bits, unsigned long long limit_ns) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > limit_ns) {
-      *abort_flag = 1u;
-      atomicOr(bits, DEV_ERR_TIMEOUT);
-      return false;
-    }
-  }
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
@@ -160,7 +139,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.ready[s], FP8 ? 2 * C::NP : 2);
+      mbar_init(&sh.ready[s], FP8 ? C::NP : 2);      // fp8: a group's four warps in each CTA
       mbar_init(&sh.empty[s], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], 2 * kSW);
@@ -193,32 +172,32 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   Walk<SEL> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, wait_cluster(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
+    return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
+  };
+
+  // S warps: this CTA's 64 heads of a segment's row, once the previous ones have been read
+  auto load_q = [&](uint32_t it) -> bool {
+    if (it > 0 && !wait(&sh.q_empty, (it - 1) & 1)) return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&sh.q_full, kQBytes);
+#pragma unroll 1
+      for (int kb = 0; kb < kKB; ++kb)
+        tma_load_2d(sQ + kb * (kHeads * 128), &tmap_q, &sh.q_full, kb * 64, sg.row * a.H + static_cast<int>(rank) * kHeads);
+    }
+    __syncwarp();
+    const bool ok = wait(&sh.q_full, it & 1);
+    if (!ok && lane == 0) mbar_drain(&sh.q_full, it & 1, 200000000ull);   // the copy lands before we leave
+    return ok;
   };
 
   if (warp >= kSW && warp < C::S_WARP) {
-    // ---------------------------------------------------------------- Q and the rows
+    // ---------------------------------------------------------------- the rows
     if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REG_PROD>();
     const int pw = warp - kSW;
-    uint32_t g = 0, it = 0;
+    uint32_t g = 0;
     bool ok = true;
-    auto load_q = [&]() -> bool {        // warp 0: this CTA's 64 heads of the segment's row
-      if (pw == 0) {
-        if (it > 0 && !wait(&sh.q_empty, (it - 1) & 1)) return false;
-        if (lane == 0) {
-          const int qrow = sg.row * a.H + static_cast<int>(rank) * kHeads;
-          mbar_arrive_expect_tx(&sh.q_full, kQBytes);
-#pragma unroll 1
-          for (int kb = 0; kb < kKB; ++kb) tma_load_2d(sQ + kb * (kHeads * 128), &tmap_q, &sh.q_full, kb * 64, qrow);
-        }
-        __syncwarp();
-      }
-      ++it;
-      return true;
-    };
     if constexpr (!FP8) {
       while (ok && walk.next(sg)) {
-        if (!(ok = load_q())) break;
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
         const int len = row_len(a.pg, sg.row);
         int ahead = __ldg(bt + (sg.i0 >> 1));
@@ -263,128 +242,133 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         }
       }
     } else {
-      // Warp pw takes row octet pw & 3 of the CTA's own keys and of the other 32, and 64-dim blocks
-      // 2 (pw >> 2), + 1 of its own and of the other dims: own keys x own dims go to both parts, own
-      // keys x other dims to the S part, other keys x own dims to the V part.  Lane = (row, 16 codes
-      // of a block); the steps ahead are those of the one-CTA kernel.
-      const int oct = pw & 3, vb0 = 2 * (pw >> 2), c = lane & 3;
-      const int own = 8 * oct + (lane >> 2);                              // row of the S part
-      const int key[2] = {32 * static_cast<int>(rank) + own, 32 * (1 - static_cast<int>(rank)) + own};
-      const int own_blk = 4 * static_cast<int>(rank), oth_blk = 4 - own_blk;
-      struct Set {
-        uint4 w[6], rope;
-        uint32_t sc[2];
-        int at[2];
-      } set[2];
+      // Two groups of four warps take the tiles in turn (latent_attn.cu).  A warp takes eight of the
+      // CTA's own keys (rows 8 (pw & 3) .. of the S part) and eight of the other 32: own keys x own dims
+      // go to both parts, own keys x other dims to the S part, other keys x own dims to the V part.
+      // Lane l looks after row l & 15 (own 0 .. 7, other 8 .. 15).
+      const uint32_t turn = pw >> 2;                                      // tiles with g & 1 == turn, in slot `turn`
+      const int rank_i = static_cast<int>(rank), row_base = 8 * (pw & 3);
+      const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4, row parity
+      const int my_key = (((lane & 8) != 0) == (rank_i != 0) ? 0 : 32) + row_base + (lane & 7);
+      uint4 w[12], rp[2];
+      uint32_t sc = 0;                       // scale word and cache row (-1: zeros) of row lane & 15
+      int at = -1;
       Walk<SEL> aw(walk);
       Seg as;
       int ai = 0;
       bool alive = aw.next(as);
-      int j1[2] = {-1, -1}, row1 = 0, len1 = 0;
-      int j2[2] = {-1, -1}, page2[2] = {-1, -1};
-      bool past2[2] = {false, false};
-      auto offset_step = [&]() {
-        j1[0] = j1[1] = -1;
-        if (!alive) return;
-        row1 = as.row;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int s = (as.i0 + ai) * kRows + key[k];
-          j1[k] = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row1) * a.topk + s) : -1;
-        }
-        len1 = row_len(a.pg, row1);
-        if (++ai == as.n) {
+      int len0 = alive ? row_len(a.pg, as.row) : 0;
+      int j1 = -1, row1 = 0, len1 = 0;       // offset known
+      int j2 = -1, page2 = -1;               // page known
+      bool past2 = false;
+      auto advance = [&]() {
+        if (alive && ++ai == as.n) {
           ai = 0;
           alive = aw.next(as);
+          if (alive) len0 = row_len(a.pg, as.row);
         }
+      };
+      auto offset_step = [&]() {
+        j1 = -1;
+        if (!alive) return;
+        row1 = as.row;
+        len1 = len0;
+        const int s = (as.i0 + ai) * kRows + my_key;
+        j1 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row1) * a.topk + s) : -1;
+        advance();
+        advance();
       };
       auto page_step = [&]() {
+        j2 = j1;
+        past2 = j1 >= len1;
+        page2 = -1;
+        if (j1 >= 0 && !past2)
+          page2 = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
+      };
+      auto fetch_step = [&]() {
+        const bool in = static_cast<uint32_t>(page2) < static_cast<uint32_t>(a.pg.n_pages);
+        // a key on a page outside the cache, or (selected) past the end; the tile's tail is neither
+        if (!in && j2 >= 0 && (SEL || (!past2 && my_key == 0)) && lane < 16 && rank == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+        at = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : -1;
+        const int safe = max(at, 0);           // a row of the cache in any case: no branch around the loads
+        const int off = blk4 * 64 + c * 16;
+        int from[8], rf[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          j2[k] = j1[k];
-          past2[k] = j1[k] >= len1;
-          page2[k] = -1;
-          if (j1[k] >= 0 && !past2[k])
-            page2[k] = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1[k] >> kPageShift));
-        }
-      };
-      auto fetch_step = [&](Set& x) {
+        for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, safe, 2 * k + par);   // own 0 .. 3, other 4 .. 7
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const bool in = static_cast<uint32_t>(page2[k]) < static_cast<uint32_t>(a.pg.n_pages);
-          if (!in && j2[k] >= 0 && (SEL || (!past2[k] && key[k] == 0)) && c == 0 && rank == 0 && pw < 4)
-            report(sh.faults, DEV_ERR_BAD_INDEX);
-          x.at[k] = in ? (page2[k] << kPageShift) + (j2[k] & (kPageRows - 1)) : -1;
-          const size_t row = in ? x.at[k] : 0;
-          const uint8_t* src = a.latent + row * kDv + c * 16;
-          x.sc[k] = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row);
-          x.w[4 * k] = ldg_once(src + (own_blk + vb0) * 64);
-          x.w[4 * k + 1] = ldg_once(src + (own_blk + vb0 + 1) * 64);
-          if (k == 0) {
-            x.w[2] = ldg_once(src + (oth_blk + vb0) * 64);
-            x.w[3] = ldg_once(src + (oth_blk + vb0 + 1) * 64);
-            x.rope = ldg_once(a.rope + row * 64 + (2 * vb0 + c) * 8);
-          }
+        for (int k = 0; k < 2; ++k) rf[k] = __shfl_sync(0xffffffffu, safe, 4 * k + (lane >> 3));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint8_t* own = a.latent + static_cast<size_t>(from[k]) * kDv + off;
+          const uint8_t* oth = a.latent + static_cast<size_t>(from[4 + k]) * kDv + off;
+          w[k] = ldg_once(own + 256 * rank_i);
+          w[4 + k] = ldg_once(own + 256 * (1 - rank_i));
+          w[8 + k] = ldg_once(oth + 256 * rank_i);
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rp[k] = ldg_once(a.rope + static_cast<size_t>(rf[k]) * 64 + (lane & 7) * 8);
+        sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + safe);
       };
-      auto convert = [&](const uint4& w, uint32_t m, uint32_t (&o)[8]) {
-        fp8x4_to_bf16(w.x, m, o[0], o[1]);
-        fp8x4_to_bf16(w.y, m, o[2], o[3]);
-        fp8x4_to_bf16(w.z, m, o[4], o[5]);
-        fp8x4_to_bf16(w.w, m, o[6], o[7]);
-      };
+      if (turn) advance();
       offset_step();
       page_step();
       offset_step();
-      fetch_step(set[0]);
+      fetch_step();
       page_step();
       offset_step();
-      fetch_step(set[1]);
-      page_step();
-      offset_step();
-      const uint32_t ch0 = ((2 * c) ^ (own & 7)) << 4, ch1 = ((2 * c + 1) ^ (own & 7)) << 4;   // key & 7 == own & 7
-      auto tile_step = [&](Set& x) -> bool {
+      const uint32_t sp = smem_u32(smem + kOffStage + turn * kStage), vp = sp + kSBytes;
+      auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
-        if (g >= 2 && !wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1)) return false;
-        const uint32_t sp = smem_u32(smem + kOffStage + (g & 1) * kStage) + own * 128;
-        const uint32_t vp = smem_u32(smem + kOffStage + (g & 1) * kStage + kSBytes);
+        if (g >= 2 && !wait(&sh.empty[turn], ((g >> 1) - 1) & 1)) return false;
 #pragma unroll
-        for (int e = 0; e < 6; ++e) {
-          const int k = e >= 4;                                            // 0, 1: own x own; 2, 3: own x other dims
-          const int blk = (e == 2 || e == 3 ? oth_blk : own_blk) + vb0 + (e & 1);
-          const uint32_t m = x.at[k] >= 0 ? fp8_mult((x.sc[k] >> (8 * (blk >> 1))) & 0xFFu) : 0u;
+        for (int e = 0; e < 12; ++e) {
+          const int k = e & 3;
+          const int r = row_base + 2 * k + par;                           // row of the S part, or of its half of the V part
+          const int half = e >= 4 && e < 8 ? 1 - rank_i : rank_i;
+          const int src = (e >= 8 ? 8 : 0) + 2 * k + par;
+          const uint32_t rsc = __shfl_sync(0xffffffffu, sc, src);
+          const bool in = __shfl_sync(0xffffffffu, at, src) >= 0;
+          // dims block 4 half + blk4; a row without a key: times zero
+          const uint32_t m = in ? fp8_mult((rsc >> (16 * half + 8 * (blk4 >> 1))) & 0xFFu) : 0u;
+          const uint32_t ch0 = ((2 * c) ^ (r & 7)) << 4, ch1 = ((2 * c + 1) ^ (r & 7)) << 4;
           uint32_t o[8];
-          convert(x.w[e], m, o);
-          if (e < 4) {
-            sts128(sp + blk * kSBlk + ch0, o[0], o[1], o[2], o[3]);
-            sts128(sp + blk * kSBlk + ch1, o[4], o[5], o[6], o[7]);
+          fp8x4_to_bf16(w[e].x, m, o[0], o[1]);
+          fp8x4_to_bf16(w[e].y, m, o[2], o[3]);
+          fp8x4_to_bf16(w[e].z, m, o[4], o[5]);
+          fp8x4_to_bf16(w[e].w, m, o[6], o[7]);
+          if (e < 8) {
+            const uint32_t d = sp + (4 * half + blk4) * kSBlk + r * 128;
+            sts128(d + ch0, o[0], o[1], o[2], o[3]);
+            sts128(d + ch1, o[4], o[5], o[6], o[7]);
           }
-          if (e < 2 || e >= 4) {
-            const uint32_t d = vp + (vb0 + (e & 1)) * kVBlk + key[k] * 128;
+          if (e < 4 || e >= 8) {
+            const int key = (e >= 8 ? 32 * (1 - rank_i) : 32 * rank_i) + r;   // key & 7 == r & 7
+            const uint32_t d = vp + blk4 * kVBlk + key * 128;
             sts128(d + ch0, o[0], o[1], o[2], o[3]);
             sts128(d + ch1, o[4], o[5], o[6], o[7]);
           }
         }
-        const uint4 z = x.at[0] >= 0 ? x.rope : make_uint4(0, 0, 0, 0);
-        sts128(sp + 8 * kSBlk + (((2 * vb0 + c) ^ (own & 7)) << 4), z.x, z.y, z.z, z.w);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int q = 4 * k + (lane >> 3), r = row_base + q;
+          const uint4 z = __shfl_sync(0xffffffffu, at, q) >= 0 ? rp[k] : make_uint4(0, 0, 0, 0);
+          sts128(sp + 8 * kSBlk + r * 128 + (((lane & 7) ^ (r & 7)) << 4), z.x, z.y, z.z, z.w);
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_leader(&sh.ready[g & 1]);
-        fetch_step(x);
+        if (lane == 0) arrive_leader(&sh.ready[turn]);
+        fetch_step();
         page_step();
         offset_step();
-        ++g;
         return true;
       };
-      while (ok && walk.next(sg)) {
-        ok = load_q();
-        for (int n = 0; n < sg.n && ok; ++n) ok = (g & 1) ? tile_step(set[1]) : tile_step(set[0]);
-      }
+      while (ok && walk.next(sg))
+        for (int n = 0; n < sg.n && ok; ++n, ++g)
+          if ((g & 1) == turn) ok = tile_step();
     }
     // let every copy this CTA started land before its shared memory can be released
-    if (pw == 0 && lane == 0) {
-      if (it > 0) mbar_drain(&sh.q_full, (it - 1) & 1, 200000000ull);
-      if constexpr (!FP8)
+    if constexpr (!FP8) {
+      if (pw == 0 && lane == 0)
         for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full[j & 1], (j >> 1) & 1, 200000000ull);
     }
   } else if (warp < kSW) {
@@ -561,7 +545,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     if (warp == C::S_WARP) {
       uint32_t it = 0;
       while (walk.next(sg)) {
-        if (!wait(&sh.q_full, it & 1)) break;
+        if (!load_q(it)) break;
         if (lane == 0) arrive_leader(&sh.q_ready);
         ++it;
       }
@@ -577,7 +561,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
     while (issuer && ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
-        ok = wait(&sh.q_full, it & 1) && wait(&sh.q_ready, it & 1);
+        ok = load_q(it) && wait(&sh.q_ready, it & 1);
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
