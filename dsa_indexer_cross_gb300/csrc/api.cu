@@ -993,11 +993,13 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   CUtensorMap tkv, tv, tq;
   std::memset(&tkv, 0, sizeof(tkv));
   std::memset(&tv, 0, sizeof(tv));
-  if (!c.fp8) {
-    const bool pair = d.n_heads > 64;
-    const uint64_t rows = static_cast<uint64_t>(c.n_rows);
-    if ((s = tmap_kv_tiles(&tkv, c.latent, rows, pair ? 32 : 64)) != DSA_OK) return s;
-    if (pair && (s = tmap_kv_tiles(&tv, c.latent, rows, 64, 4)) != DSA_OK) return s;
+  const LatentRing ring = latent_attn_ring(d.n_q, d.n_heads, pg, idx != nullptr, d.topk);
+  const bool pair = ring.rows > 0;
+  if (!c.fp8 || pair) {
+    const void* rows = c.fp8 ? static_cast<const uint8_t*>(ws) + kAlign + ring.offset : c.latent;
+    const uint64_t n = static_cast<uint64_t>(c.fp8 ? ring.rows : c.n_rows);
+    if ((s = tmap_kv_tiles(&tkv, rows, n, pair ? 32 : 64)) != DSA_OK) return s;
+    if (pair && (s = tmap_kv_tiles(&tv, rows, n, 64, 4)) != DSA_OK) return s;
   }
   if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
                      static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)

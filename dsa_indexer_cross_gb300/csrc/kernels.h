@@ -255,6 +255,14 @@ cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_s
 // offsets in idx [n_q][topk] (fp8 cache).  A bf16 cache is read through tmap_kv: up to 64 heads as
 // 64-row tiles (boxes {64, 64, 9}); above, boxes {64, 32, 9} in tmap_kv and {64, 64, 4} in tmap_v.
 // tmap_q: q as [n_q * n_heads][576], boxes {64, latent_attn_q_box_rows(n_heads)}.
+// For more than 64 heads an fp8 cache's tiles go through a ring of kRing bf16 tiles per CTA pair in the
+// scratch (offset and rows of that array: latent_attn_ring), which the two maps then cover instead.
+constexpr int kRing = 8;
+struct LatentRing {
+  size_t offset;
+  int rows;            // 0: none
+};
+LatentRing latent_attn_ring(int n_q, int n_heads, const PagedRows& pg, bool selected, int topk);
 int latent_attn_q_box_rows(int n_heads);
 size_t latent_attn_ws_bytes(int n_q, int n_heads);
 cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,

@@ -37,17 +37,12 @@ template <int HB, bool FP8>
 struct LCfg {
   static constexpr int Q_BYTES = HB * kDqk * 2;
   static constexpr int DYN_SMEM = 1024 + 2 * kTileBytes + Q_BYTES;
-  static constexpr int SW = HB >= 32 ? 8 : 4;          // softmax warps
+  static constexpr int SW = HB >= 32 && !FP8 ? 8 : 4;  // softmax warps (fp8: four, which leaves the converters 128 registers)
   static constexpr int SOFT = 32 * SW;
   static constexpr int NP = FP8 ? 8 : 1;               // producer warps
   static constexpr int S_WARP = SW + NP;
   static constexpr int PV_WARP = S_WARP + 1;
-  // fp8 with eight softmax warps: two idle warps complete the MMA warps' warpgroup, which pays for
-  // the producers' codes in registers: 8 * 96 + 8 * 112 + 4 * 64 = 20 * 96.
-  static constexpr bool REG_SPLIT = FP8 && SW == 8;
-  static constexpr int REG_LAUNCH = 96, REG_PROD = 112, REG_MMA = 64;
-  static constexpr int THREADS = 32 * (SW + NP + (REG_SPLIT ? 4 : 2));
-  static_assert(!REG_SPLIT || 8 * REG_LAUNCH + 8 * REG_PROD + 4 * REG_MMA <= 20 * REG_LAUNCH, "register split");
+  static constexpr int THREADS = 32 * (SW + NP + 2);
   static constexpr int CW = HB / (SW / 4);             // columns per softmax warp
   static constexpr int NR = CW / 8;
   static constexpr uint32_t TMEM_COLS = 6 * HB <= 128 ? 128 : 6 * HB <= 256 ? 256 : 512;
@@ -57,7 +52,9 @@ struct LCfg {
 
 struct LShared {
   uint64_t full[2], empty[2];
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, o_done[2], o_free, mma_done;
+  // [2]: by tile parity.  (One p_full for all tiles would not do: the softmax may be two tiles ahead of
+  // the PV warp's look, and a barrier two phases on reads as not yet complete.)
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free, mma_done;
   uint32_t tmem_base, abort_flag, soft_abort;
   CtaFaults faults;
   Share share;
@@ -91,11 +88,11 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       mbar_init(&sh.empty[s], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], C::SW);
+      mbar_init(&sh.p_full[s], C::SW);
       mbar_init(&sh.o_done[s], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
-    mbar_init(&sh.p_full, C::SW);
     mbar_init(&sh.o_free, C::SW);
     mbar_init(&sh.mma_done, 2);
     sh.abort_flag = 0;
@@ -118,12 +115,11 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 
   if (warp >= C::SW && warp < C::S_WARP) {
     // ---------------------------------------------------------------- Q and the rows
-    if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REG_PROD>();
     const int pw = warp - C::SW;
     uint32_t g = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
     };
     if constexpr (!FP8) {
       while (ok && walk.next(sg)) {
@@ -161,14 +157,14 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       const int row_base = 16 * (pw & 3), my_row = row_base + (lane & 15);
       const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4 (+ 4), row parity
       uint4 w[16];
-      uint32_t sc = 0;                       // scale word and cache row (-1: zeros) of row lane & 15
-      int at = -1;
+      uint32_t sc = 0;                       // scale word of row lane & 15
+      int at = -1;                           // its cache row (-1: zeros)
       Walk<SEL> aw(walk);
       Seg as;
       int ai = 0;
       bool alive = aw.next(as);
       int len0 = alive ? row_len(a.pg, as.row) : 0;
-      int j1 = -1, row1 = 0, len1 = 0;       // offset known
+      int j1 = -1, row1 = 0, len1 = 0;       // offset of row lane & 15 known
       int j2 = -1, page2 = -1;               // page known
       bool past2 = false;
       auto advance = [&]() {
@@ -178,13 +174,17 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           if (alive) len0 = row_len(a.pg, as.row);
         }
       };
+      int j0 = -1, row0 = 0, lenx = 0;       // the offset after that, found while w holds nothing
       auto offset_step = [&]() {
-        j1 = -1;
+        j1 = j0;         // (asked for a tile ago)
+        row1 = row0;
+        len1 = lenx;
+        j0 = -1;
         if (!alive) return;
-        row1 = as.row;
-        len1 = len0;
+        row0 = as.row;
+        lenx = len0;
         const int s = (as.i0 + ai) * kRows + my_row;
-        j1 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row1) * a.topk + s) : -1;
+        j0 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row0) * a.topk + s) : -1;
         advance();
         advance();
       };
@@ -192,53 +192,69 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         j2 = j1;
         past2 = j1 >= len1;
         page2 = -1;
-        if (j1 >= 0 && !past2)
+        // (unselected: the page of a row past the end is still the tile's page)
+        if (j1 >= 0 && (!SEL || !past2))
           page2 = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
       };
       auto fetch_step = [&]() {
         const bool in = static_cast<uint32_t>(page2) < static_cast<uint32_t>(a.pg.n_pages);
         // a key on a page outside the cache, or (selected) past the end; the tile's tail is neither
-        if (!in && j2 >= 0 && (SEL || (!past2 && my_row == 0)) && lane < 16 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
-        at = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : -1;
-        const int safe = max(at, 0);           // a row of the cache in any case: no branch around the loads
-        int from[8];
+        if (!in && j2 >= 0 && (SEL || my_row == 0) && lane < 16 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+        const int row = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : 0;   // a row of the cache in any case
+        at = in && !past2 ? row : -1;
+        const int off = blk4 * 64 + c * 16;
+        if constexpr (SEL) {
+          int from[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, safe, 2 * k + par);
+          for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, row, 2 * k + par);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint8_t* src = a.latent + static_cast<size_t>(from[k]) * kDv + blk4 * 64 + c * 16;
-          w[2 * k] = ldg_once(src);
-          w[2 * k + 1] = ldg_once(src + 256);
+          for (int k = 0; k < 8; ++k) {
+            const uint8_t* src = a.latent + static_cast<size_t>(from[k]) * kDv + off;
+            w[2 * k] = ldg_once(src);
+            w[2 * k + 1] = ldg_once(src + 256);
+          }
+        } else {
+          // the tile's rows follow one another (rows past the end lie in the same page)
+          const uint8_t* src = a.latent + static_cast<size_t>(row + (in ? par - (lane & 15) : par)) * kDv + off;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            w[2 * k] = ldg_once(src + 2 * k * kDv);
+            w[2 * k + 1] = ldg_once(src + 2 * k * kDv + 256);
+          }
         }
-        sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + safe);
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(safe) * 64));
+        sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(row) * 64));
       };
       if (turn) advance();
+      offset_step();
       offset_step();
       page_step();
       offset_step();
       fetch_step();
       page_step();
-      offset_step();
       const uint32_t tile = smem_u32(sT + turn * kTileBytes);
+      // the lane's line of row par in block blk4, swizzled for chunk 2 c; row 2 k + par's lies 256 k on, its
+      // swizzle differs by 2 k (mod 8)
+      const uint32_t lane_line = tile + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
       // one tile: registers -> the bf16 tile, then the registers' next fetch
       auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
         if (g >= 2 && !wait(&sh.empty[turn], ((g >> 1) - 1) & 1)) return false;
+        const uint32_t rl = opaque(tile) + 8 * kBlkBytes + row_base * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int q = 4 * k + (lane >> 3), r = row_base + q;            // row, 16-byte chunk lane & 7
+          const int q = 4 * k + (lane >> 3);                              // row, 16-byte chunk lane & 7
           const int from = __shfl_sync(0xffffffffu, at, q);
-          cp_async_16_zfill(tile + 8 * kBlkBytes + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
+          cp_async_16_zfill(rl + q * 128 + (((lane & 7) ^ (q & 7)) << 4),
                             a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
         }
         cp_async_mbar_arrive(&sh.full[turn]);
+        const uint32_t line = opaque(lane_line);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int r = row_base + 2 * k + par;
           const uint32_t rsc = __shfl_sync(0xffffffffu, sc, 2 * k + par);
           const bool in = __shfl_sync(0xffffffffu, at, 2 * k + par) >= 0;
-          const uint32_t ch0 = ((2 * c) ^ (r & 7)) << 4, ch1 = ((2 * c + 1) ^ (r & 7)) << 4;
+          const uint32_t d = line ^ (static_cast<uint32_t>((2 * k) & 7) << 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // a row without a key: times zero
@@ -249,22 +265,19 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             fp8x4_to_bf16(v.y, m, o[2], o[3]);
             fp8x4_to_bf16(v.z, m, o[4], o[5]);
             fp8x4_to_bf16(v.w, m, o[6], o[7]);
-            const uint32_t d = tile + (4 * h + blk4) * kBlkBytes + r * 128;
-            sts128(d + ch0, o[0], o[1], o[2], o[3]);
-            sts128(d + ch1, o[4], o[5], o[6], o[7]);
+            sts128(d + 256 * k + 4 * h * kBlkBytes, o[0], o[1], o[2], o[3]);
+            sts128((d ^ 16u) + 256 * k + 4 * h * kBlkBytes, o[4], o[5], o[6], o[7]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full[turn]);
+        offset_step();
         fetch_step();
         page_step();
-        offset_step();
         return true;
       };
-      while (ok && walk.next(sg))
-        for (int n = 0; n < sg.n && ok; ++n, ++g)
-          if ((g & 1) == turn) ok = tile_step();
+      for (g = turn; ok && g < static_cast<uint32_t>(share); g += 2) ok = tile_step();
       cp_async_wait<0>();
     }
     // let every copy this CTA started land before its shared memory can be released
@@ -313,7 +326,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           rv0 = r0 < nv;
           rv1 = r0 + 8 < nv;
         }
-        bool ok = mbar_wait_for(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
+        bool ok = wait_bar(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         float sc[4 * NR];   // [4k + j]: j = 0,1 row r0 columns 8k+cq, +1;  j = 2,3 row r0 + 8
         bool need = false;
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             }
             // O^T may only be rescaled once the previous tile's PV has finished
             if (n > 0) {
-              ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
+              ok = wait_bar(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok && lane == 0) sh.soft_abort = 1;
             }
@@ -390,9 +403,9 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             for (int c = 0; c < 16; ++c) any |= ar[c] != 1.f;
           }
           if (any && n > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-#pragma unroll
+#pragma unroll 1
               for (int hw = 0; hw < C::CW / 16; ++hw) {
                 const int hh = c_off / 16 + hw;
                 uint32_t o[16];
@@ -435,7 +448,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full);
+        if (lane == 0) mbar_arrive(&sh.p_full[sb]);
       }
       if (stop) break;
       // segment end: column sums over the 64 rows, then the output or a partial
@@ -455,7 +468,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           }
         }
       }
-      bool ok = mbar_wait_for(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
+      bool ok = wait_bar(&sh.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) sh.soft_abort = 1;
       named_bar_sync(1, kSoft);
@@ -468,10 +481,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       if (stop) break;
       tc_fence_after();
       const size_t pslot = static_cast<size_t>(grp) * 2 + (sg.i0 > 0 ? 0 : 1);
-#pragma unroll
+#pragma unroll 1
       for (int hw = 0; hw < C::CW / 16; ++hw) {
         const int hh = c_off / 16 + hw;
-#pragma unroll
+#pragma unroll 1
         for (int b2 = 0; b2 < 4; b2 += 2) {
           uint32_t o[2][16];
 #pragma unroll
@@ -525,19 +538,17 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       named_bar_sync(1, kSoft);        // per-column state may be reset now
     }
   } else {
-    // ---------------------------------------------------------------- MMA issuers (and idle warps)
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REG_MMA>();
-    const bool issuer = warp <= C::PV_WARP;
+    // ---------------------------------------------------------------- MMA issuers
     constexpr uint32_t id_qk = idesc_bf16_f32(64, HB, 0, 0);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, HB, 1, 1);
     const uint32_t st0 = smem_u32(sT);
     uint32_t g = 0, it = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
+      return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
     };
     const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    while (issuer && ok && walk.next(sg)) {
+    while (ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
         const int len = row_len(a.pg, sg.row);
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
@@ -574,7 +585,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           tc_fence_after();
           const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
           const uint32_t d_s = tmem + C::S_COL + sb * HB;
-#pragma unroll
+          // (fp8: rolled, for the instruction cache)
+#pragma unroll FP8 ? 1 : kKB
           for (int kb = 0; kb < kKB; ++kb)
             umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
                                      dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
@@ -583,7 +595,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         if (ok) umma_commit_elect(&sh.q_empty);
       } else {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
-          ok = wait(&sh.p_full, g & 1);
+          ok = wait(&sh.p_full[g & 1], (g >> 1) & 1);
           if constexpr (FP8) fence_proxy_async_smem();
           if (ok && n == 0 && it > 0) ok = wait(&sh.o_free, (it - 1) & 1);
           if (!ok) break;
@@ -592,7 +604,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           const uint64_t dv = sdesc_sw128(tb, kBlkBytes, 1024);
           const uint64_t dp = sdesc_sw128(tb + (kKB - 1) * kBlkBytes, kBlkBytes, 1024);
           const uint32_t acc0 = n > 0 ? 1u : 0u;
-#pragma unroll
+#pragma unroll FP8 ? 1 : 4
           for (int b = 0; b < 4; ++b)      // four K steps of 16 rows (2048 B)
             umma_bf16_x4_elect<128, 128>(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes) >> 4), dp, id_pv,
                                          acc0);
@@ -603,10 +615,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       ++it;
     }
     // every MMA this warp issued has completed before TMEM is released
-    if (issuer) {
-      umma_commit_elect(&sh.mma_done);
-      mbar_drain(&sh.mma_done, 0, 200000000ull);
-    }
+    umma_commit_elect(&sh.mma_done);
+    mbar_drain(&sh.mma_done, 0, 200000000ull);
   }
   tc_fence_before();
   __syncthreads();
@@ -707,7 +717,7 @@ int head_block(int n_heads) { return n_heads <= 16 ? 16 : n_heads <= 32 ? 32 : 6
 
 struct Layout {
   int n_hb, n_grp;
-  size_t off_err, off_start, off_m, off_o, total;
+  size_t off_err, off_start, off_m, off_ring, off_o, total;
 };
 Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
   Layout L{};
@@ -724,6 +734,8 @@ Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
   o += up((static_cast<size_t>(L.n_grp) + 1) * sizeof(int2));
   L.off_m = o;
   o += up(static_cast<size_t>(L.n_grp) * 2 * n_heads * 3 * sizeof(float));
+  L.off_ring = o;
+  if (L.n_hb == 2) o += up(static_cast<size_t>(L.n_grp) * kRing * kRows * kDqk * sizeof(uint16_t));
   L.off_o = o;
   o += L.n_grp > 1 ? static_cast<size_t>(L.n_grp) * 2 * n_heads * kDv * sizeof(float) : 0;
   L.total = o;
@@ -735,15 +747,6 @@ cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs&
   using C = LCfg<HB, FP8>;
   cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, SEL>>(C::DYN_SMEM);
   if (e != cudaSuccess) return e;
-  if constexpr (C::REG_SPLIT) {
-    // the producers' setmaxnreg.inc waits for registers the block must hold from launch: refuse a
-    // build whose count would leave it waiting (looked up once)
-    static const int regs = [] {
-      cudaFuncAttributes fa{};
-      return cudaFuncGetAttributes(&fa, latent_attn_kernel<HB, FP8, SEL>) == cudaSuccess ? fa.numRegs : 0;
-    }();
-    if (regs < C::REG_LAUNCH) return cudaErrorInvalidConfiguration;
-  }
   return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, SEL, 1, tkv, tq, a);
 }
 template <int HB>
@@ -753,6 +756,17 @@ cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensor
 }
 
 }  // namespace
+
+namespace {
+long long row_tiles_max(const PagedRows& pg, bool selected, int topk) {
+  return selected ? (topk + kRows - 1) / kRows : pg.max_pages * 2LL;
+}
+}  // namespace
+
+LatentRing latent_attn_ring(int n_q, int n_heads, const PagedRows& pg, bool selected, int topk) {
+  const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, selected, topk));
+  return LatentRing{L.off_ring, L.n_hb == 2 ? L.n_grp * kRing * kRows : 0};
+}
 
 int latent_attn_q_box_rows(int n_heads) { return head_block(n_heads); }
 
@@ -765,7 +779,7 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
                                const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
                                void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st) {
   const bool sel = idx != nullptr;
-  const Layout L = latent_layout(n_q, n_heads, sel ? (topk + kRows - 1) / kRows : pg.max_pages * 2LL);
+  const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, sel, topk));
   uint8_t* base = static_cast<uint8_t*>(scratch);
   const PipelineDebug dbg = pipeline_debug();
   LArgs a{};
@@ -787,6 +801,7 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   a.scale_log2 = scale * 1.4426950408889634f;
   a.start = reinterpret_cast<int2*>(base + L.off_start);
   a.part_m = reinterpret_cast<float*>(base + L.off_m);
+  a.ring = reinterpret_cast<uint16_t*>(base + L.off_ring);
   a.part_o = reinterpret_cast<float*>(base + L.off_o);
   a.status = status;
   a.wait_ns = dbg.wait_ns;

@@ -47,6 +47,13 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
                : "l"(p));
   return v;
 }
+// x, as a value the compiler cannot carry around a loop (addresses derived from it are formed where they
+// are used instead of being held in registers).
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  uint32_t y;
+  asm volatile("mov.u32 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ void lrow16(float (&r)[16], const float* p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -70,6 +77,7 @@ struct LArgs {
   int n_q, H, topk, n_grp, n_hb;
   float scale_log2;
   int2* start;                 // [n_grp + 1]: (row, tile) each group starts at; [n_grp].x = groups in use
+  uint16_t* ring;              // fp8, CTA pairs: [n_grp][kRing][64][576] bf16
   float* part_o;               // [n_grp * 2][H][512]
   float* part_m;               // [3][n_grp * 2][H]: max in use (log2), sum of the rounded weights, plain sum
   uint32_t* status;
@@ -102,6 +110,7 @@ struct Walk {
   __device__ __forceinline__ bool next(Seg& s) {
     if (left <= 0) return false;
     int T = row_tiles<SEL>(a, row);
+#pragma unroll 1
     while (T == 0) T = row_tiles<SEL>(a, ++row);
     s.row = row;
     s.i0 = tile;
@@ -142,6 +151,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
   const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
   long long mine = 0;
   bool bad_len = false;
+#pragma unroll 1
   for (int r = ra; r < rb; ++r) {
     mine += row_tiles<SEL>(a, r);
     if (blockIdx.x == 0) {
@@ -162,6 +172,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
   if (bad_len) report(faults, DEV_ERR_RANGE);
   long long total = 0;
   pre -= mine;
+#pragma unroll 1
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) pre += sh.wsum[w];
     total += sh.wsum[w];
@@ -184,14 +195,36 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.n_grp] = make_int2(groups, 0);
   // rows without keys: zeros and -inf
+#pragma unroll 1
   for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
     if (row_tiles<SEL>(a, t) != 0) continue;
     uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.H * kDv);
+#pragma unroll 1
     for (int e = threadIdx.x; e < a.H * (kDv / 8); e += THREADS) o[e] = make_uint4(0, 0, 0, 0);
     if (a.lse)
       for (int h = threadIdx.x; h < a.H; h += THREADS) a.lse[static_cast<size_t>(t) * a.H + h] = -INFINITY;
   }
   return share;
+}
+
+// Bounded mbarrier wait, as mbar_wait_for, but out of line behind the first try: the warp roles' code
+// together has to stay in the instruction caches, and the waits are most of its copies.
+static __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* bits,
+                                       unsigned long long limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort_flag = 1u;
+      atomicOr(bits, DEV_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag, uint32_t* bits,
+                                         unsigned long long limit_ns) {
+  return mbar_try_wait(bar, parity) || wait_more(bar, parity, abort_flag, bits, limit_ns);
 }
 
 // Valid rows of tile i of a row of `len` keys: none on a page outside the cache.

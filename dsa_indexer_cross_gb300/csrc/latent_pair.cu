@@ -16,7 +16,10 @@
 //   S part: its 32 keys, all 576 dims   (nine 64-dim blocks of 32 rows x 128 B)
 //   V part: all 64 keys, its 256 dims   (four 64-dim blocks of 64 rows x 128 B)
 // The two overlap in the values of its keys and dims, which lie in both: each part needs the same place
-// in both CTAs (a descriptor holds for the pair) and its own row order.
+// in both CTAs (a descriptor holds for the pair) and its own row order.  They are filled and freed
+// apart: the S part of tile g + 2 as soon as S(g) is complete, the V part once PV(g) is, so the way
+// of a tile from its rows to its product does not limit how often one begins (one barrier for both
+// parts: 1487 us where the two take MEAS_BF16, 64 rows of 8K to 131K keys, 128 heads, bf16).
 //
 // TMEM.  An M = 128 accumulator of a pair has head h of each CTA in lane h for the first half of the
 // columns and in lane 64 + h for the second half: O is 2 x 128 columns, S 32 columns, double-buffered.
@@ -40,24 +43,27 @@ constexpr int kPBytes = kHeads * kRows * 2;
 constexpr int kOffStage = kQBytes, kOffP = kQBytes + 2 * kStage, kOffShared = kOffP + 2 * kPBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 256;                       // O: columns 0 .. 255
+
 constexpr int kSW = 8, kSoft = 256;              // softmax warps, threads
+constexpr int kKT = 16, kOC = 128;               // keys of a tile, O columns per softmax thread
+constexpr int kConv = 8;                         // fp8: converter warps = tiles of the ring (kRing)
+static_assert(kConv == kRing, "a converter warp for each tile of the ring");
 
 template <bool FP8>
 struct PCfg {
-  static constexpr int NP = FP8 ? 8 : 2;         // converters, or the TMA warp and the one behind it
-  static constexpr int S_WARP = kSW + NP;
+  static constexpr int COPY = kSW;               // the TMA warp and the one behind it, for each part (fp8: for both)
+  static constexpr int CONV = COPY + (FP8 ? 2 : 4);
+  static constexpr int S_WARP = CONV + (FP8 ? kConv : 0);
   static constexpr int PV_WARP = S_WARP + 1;
-  // fp8: two idle warps complete the MMA warps' warpgroup, which pays for the converters' codes in
-  // registers: 8 * 96 + 8 * 112 + 4 * 64 = 20 * 96.
-  static constexpr bool REG_SPLIT = FP8;
-  static constexpr int REG_LAUNCH = 96, REG_PROD = 112, REG_MMA = 64;
-  static constexpr int THREADS = 32 * (PV_WARP + (REG_SPLIT ? 3 : 1));
-  static_assert(8 * REG_LAUNCH + 8 * REG_PROD + 4 * REG_MMA <= 20 * REG_LAUNCH, "register split");
+  static constexpr int THREADS = 32 * (PV_WARP + 1);
 };
 
 struct PShared {
-  uint64_t full[2], ready[2], empty[2], q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free,
-      mma_done;
+  // [2]: by tile parity.  full_*: copies have landed (this CTA); ready_*, s_empty, p_full, o_free, q_ready:
+  // the leader's, both CTAs arrive; s_full, o_done, q_empty: S, PV, all of a segment's S complete (both CTAs)
+  uint64_t full_s[2], full_v[2], ready_s[2], ready_v[2], q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2],
+      o_done[2], o_free, mma_done;
+  uint64_t ring_full[kRing], ring_empty[kRing];   // fp8: both CTAs arrive on each CTA's
   uint32_t tmem_base, abort_flag, soft_abort;
   CtaFaults faults;
   Share share;
@@ -77,15 +83,22 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on the leader's copy of `bar`.  What the arrival publishes lies in this CTA's own shared
+// Arrive on the copy of `bar` in the pair's CTA `rank` (0: the leader).  What the arrival publishes lies in this CTA's own shared
 // memory and TMEM and is read there by this SM's tensor core, so the order within the CTA is enough
 // (fence.proxy.async, tcgen05 fences and the CTA-scope release before it); a cluster-scope release took
 // about 1100 cycles on the path from one tile to the next.
-__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+__device__ __forceinline__ void arrive_cta(uint64_t* bar, uint32_t rank) {
   asm volatile(
-      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(
-          smem_u32(bar))
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(rank)
       : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+__device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
@@ -138,13 +151,18 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.ready[s], FP8 ? C::NP : 2);      // fp8: a group's four warps in each CTA
-      mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.full_s[s], 1);
+      mbar_init(&sh.full_v[s], 1);
+      mbar_init(&sh.ready_s[s], 2);
+      mbar_init(&sh.ready_v[s], 2);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], 2 * kSW);
       mbar_init(&sh.p_full[s], 2 * kSW);
       mbar_init(&sh.o_done[s], 1);
+    }
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&sh.ring_full[s], 2);    // the CTAs' converters
+      mbar_init(&sh.ring_empty[s], 3);   // its rows read: both of this CTA's parts, the other's V part
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_ready, 1);
@@ -172,7 +190,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   Walk<SEL> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_for(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
   };
 
   // S warps: this CTA's 64 heads of a segment's row, once the previous ones have been read
@@ -190,195 +208,179 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     return ok;
   };
 
-  if (warp >= kSW && warp < C::S_WARP) {
+  if (warp >= C::COPY && warp < C::CONV) {
     // ---------------------------------------------------------------- the rows
-    if constexpr (C::REG_SPLIT) setmaxnreg_inc<C::REG_PROD>();
-    const int pw = warp - kSW;
-    uint32_t g = 0;
+    // The first warp copies, the second, behind it, writes zeros for rows without a key (of the V part:
+    // a masked score may come from anything, a zero weight does not cancel a NaN) and tells the
+    // leader.  bf16: two warps for the S part, two for the V part; fp8: one pair for both, in turn.
+    const int pw = warp - C::COPY;
+    const bool copies = (pw & 1) == 0;
+    const int part0 = FP8 ? 0 : pw >> 1, part1 = FP8 ? 2 : part0 + 1;   // 0: S part, 1: V part
+    uint32_t g = 0, slot = 0, lap = 0;       // slot, lap: the tile's place in the ring
     bool ok = true;
-    if constexpr (!FP8) {
-      while (ok && walk.next(sg)) {
-        const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
-        const int len = row_len(a.pg, sg.row);
-        int ahead = __ldg(bt + (sg.i0 >> 1));
-        for (int n = 0; n < sg.n; ++n, ++g) {
-          const int i = sg.i0 + n, page = ahead;
-          if (n + 1 < sg.n) ahead = __ldg(bt + ((i + 1) >> 1));
-          const int nv = tile_rows(a, len, i, page);
-          uint8_t* st = smem + kOffStage + (g & 1) * kStage;
-          if (pw == 0) {
-            if (nv == 0 && lane == 0 && rank == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
-            if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
-              ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
-              break;
-            }
-            if (g >= 2 && !(ok = wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1))) break;
+    while (ok && walk.next(sg)) {
+      const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+      const int len = row_len(a.pg, sg.row);
+      int ahead = FP8 ? 0 : __ldg(bt + (sg.i0 >> 1));
+      for (int n = 0; n < sg.n && ok; ++n, ++g) {
+        const int i = sg.i0 + n, page = ahead, sb = g & 1;
+        if (!FP8 && n + 1 < sg.n) ahead = __ldg(bt + ((i + 1) >> 1));
+        const int nv = FP8 ? kRows : tile_rows(a, len, i, page);
+        if (copies) {
+          if (nv == 0 && lane == 0 && rank == 0 && part0 == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+          if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
+            ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
+            break;
+          }
+          if constexpr (FP8) {
+            if (!(ok = wait(&sh.ring_full[slot], lap & 1))) break;
+          }
+        }
+#pragma unroll 1
+        for (int part = part0; part < part1 && ok; ++part) {
+          uint64_t* full = part ? &sh.full_v[sb] : &sh.full_s[sb];
+          uint8_t* st = smem + kOffStage + sb * kStage + (part ? kSBytes : 0);
+          if (copies) {
+            if (g >= 2 && !(ok = wait(part ? &sh.o_done[sb] : &sh.s_full[sb], ((g >> 1) - 1) & 1))) break;
             if (lane == 0) {
-              const int row = nv == 0 ? 0 : (page << kPageShift) + (i & 1) * kRows;
-              mbar_arrive_expect_tx(&sh.full[g & 1], kStage);
-              tma_load_3d(st, &tmap_s, &sh.full[g & 1], 0, row + 32 * static_cast<int>(rank), 0);
-              tma_load_3d(st + kSBytes, &tmap_v, &sh.full[g & 1], 0, row, 4 * static_cast<int>(rank));
+              int row = nv == 0 ? 0 : (page << kPageShift) + (i & 1) * kRows;
+              if constexpr (FP8) {
+                row = (grp * kRing + static_cast<int>(slot)) * kRows;
+                fence_proxy_async_global();    // the converters' stores, before the copies that read them
+              }
+              mbar_arrive_expect_tx(full, part ? kVBytes : kSBytes);
+              if (part)
+                tma_load_3d(st, &tmap_v, full, 0, row, 4 * static_cast<int>(rank));
+              else
+                tma_load_3d(st, &tmap_s, full, 0, row + 32 * static_cast<int>(rank), 0);
             }
             __syncwarp();
           } else {
-            // the warp behind the copies: zeros for rows without a key, then the leader may read
-            if (!(ok = wait(&sh.full[g & 1], (g >> 1) & 1))) break;
-            if (nv < kRows) {
-              const uint32_t sp = smem_u32(st), vp = sp + kSBytes;
-              const int s0 = max(0, min(32, nv - 32 * static_cast<int>(rank)));
-              for (int e = lane; e < (32 - s0) * 8 * kKB; e += 32) {
-                const int kb = e / ((32 - s0) * 8), w = e - kb * ((32 - s0) * 8);
-                sts128(sp + kb * kSBlk + s0 * 128 + w * 16, 0u, 0u, 0u, 0u);
-              }
-              for (int e = lane; e < (kRows - nv) * 8 * 4; e += 32) {
-                const int vb = e / ((kRows - nv) * 8), w = e - vb * ((kRows - nv) * 8);
-                sts128(vp + vb * kVBlk + nv * 128 + w * 16, 0u, 0u, 0u, 0u);
-              }
+            if (!(ok = wait(full, (g >> 1) & 1))) break;
+            if (!FP8 && part && nv < kRows) {
+              const int each = (kRows - nv) * 8;                          // 16-byte pieces of one block
+              for (int e = lane; e < each * 4; e += 32)
+                sts128(smem_u32(st) + (e / each) * kVBlk + nv * 128 + (e % each) * 16, 0u, 0u, 0u, 0u);
               fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) arrive_leader(&sh.ready[g & 1]);
+            if (lane == 0) {
+              arrive_cta(part ? &sh.ready_v[sb] : &sh.ready_s[sb], 0);
+              if constexpr (FP8) {
+                arrive_cta(&sh.ring_empty[slot], rank);
+                if (part) arrive_cta(&sh.ring_empty[slot], rank ^ 1u);
+              }
+            }
           }
+        }
+        if (++slot == kRing) {
+          slot = 0;
+          ++lap;
         }
       }
-    } else {
-      // Two groups of four warps take the tiles in turn (latent_attn.cu).  A warp takes eight of the
-      // CTA's own keys (rows 8 (pw & 3) .. of the S part) and eight of the other 32: own keys x own dims
-      // go to both parts, own keys x other dims to the S part, other keys x own dims to the V part.
-      // Lane l looks after row l & 15 (own 0 .. 7, other 8 .. 15).
-      const uint32_t turn = pw >> 2;                                      // tiles with g & 1 == turn, in slot `turn`
-      const int rank_i = static_cast<int>(rank), row_base = 8 * (pw & 3);
-      const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4, row parity
-      const int my_key = (((lane & 8) != 0) == (rank_i != 0) ? 0 : 32) + row_base + (lane & 7);
-      uint4 w[12], rp[2];
-      uint32_t sc = 0;                       // scale word and cache row (-1: zeros) of row lane & 15
-      int at = -1;
-      Walk<SEL> aw(walk);
-      Seg as;
-      int ai = 0;
-      bool alive = aw.next(as);
-      int len0 = alive ? row_len(a.pg, as.row) : 0;
-      int j1 = -1, row1 = 0, len1 = 0;       // offset known
-      int j2 = -1, page2 = -1;               // page known
-      bool past2 = false;
-      auto advance = [&]() {
-        if (alive && ++ai == as.n) {
-          ai = 0;
-          alive = aw.next(as);
-          if (alive) len0 = row_len(a.pg, as.row);
-        }
-      };
-      auto offset_step = [&]() {
-        j1 = -1;
-        if (!alive) return;
-        row1 = as.row;
-        len1 = len0;
-        const int s = (as.i0 + ai) * kRows + my_key;
-        j1 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row1) * a.topk + s) : -1;
-        advance();
-        advance();
-      };
-      auto page_step = [&]() {
-        j2 = j1;
-        past2 = j1 >= len1;
-        page2 = -1;
-        if (j1 >= 0 && !past2)
-          page2 = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
-      };
-      auto fetch_step = [&]() {
-        const bool in = static_cast<uint32_t>(page2) < static_cast<uint32_t>(a.pg.n_pages);
-        // a key on a page outside the cache, or (selected) past the end; the tile's tail is neither
-        if (!in && j2 >= 0 && (SEL || (!past2 && my_key == 0)) && lane < 16 && rank == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
-        at = in ? (page2 << kPageShift) + (j2 & (kPageRows - 1)) : -1;
-        const int safe = max(at, 0);           // a row of the cache in any case: no branch around the loads
-        const int off = blk4 * 64 + c * 16;
-        int from[8], rf[2];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) from[k] = __shfl_sync(0xffffffffu, safe, 2 * k + par);   // own 0 .. 3, other 4 .. 7
-#pragma unroll
-        for (int k = 0; k < 2; ++k) rf[k] = __shfl_sync(0xffffffffu, safe, 4 * k + (lane >> 3));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint8_t* own = a.latent + static_cast<size_t>(from[k]) * kDv + off;
-          const uint8_t* oth = a.latent + static_cast<size_t>(from[4 + k]) * kDv + off;
-          w[k] = ldg_once(own + 256 * rank_i);
-          w[4 + k] = ldg_once(own + 256 * (1 - rank_i));
-          w[8 + k] = ldg_once(oth + 256 * rank_i);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) rp[k] = ldg_once(a.rope + static_cast<size_t>(rf[k]) * 64 + (lane & 7) * 8);
-        sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + safe);
-      };
-      if (turn) advance();
-      offset_step();
-      page_step();
-      offset_step();
-      fetch_step();
-      page_step();
-      offset_step();
-      const uint32_t sp = smem_u32(smem + kOffStage + turn * kStage), vp = sp + kSBytes;
-      auto tile_step = [&]() -> bool {
-        if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
-        if (g >= 2 && !wait(&sh.empty[turn], ((g >> 1) - 1) & 1)) return false;
-#pragma unroll
-        for (int e = 0; e < 12; ++e) {
-          const int k = e & 3;
-          const int r = row_base + 2 * k + par;                           // row of the S part, or of its half of the V part
-          const int half = e >= 4 && e < 8 ? 1 - rank_i : rank_i;
-          const int src = (e >= 8 ? 8 : 0) + 2 * k + par;
-          const uint32_t rsc = __shfl_sync(0xffffffffu, sc, src);
-          const bool in = __shfl_sync(0xffffffffu, at, src) >= 0;
-          // dims block 4 half + blk4; a row without a key: times zero
-          const uint32_t m = in ? fp8_mult((rsc >> (16 * half + 8 * (blk4 >> 1))) & 0xFFu) : 0u;
-          const uint32_t ch0 = ((2 * c) ^ (r & 7)) << 4, ch1 = ((2 * c + 1) ^ (r & 7)) << 4;
-          uint32_t o[8];
-          fp8x4_to_bf16(w[e].x, m, o[0], o[1]);
-          fp8x4_to_bf16(w[e].y, m, o[2], o[3]);
-          fp8x4_to_bf16(w[e].z, m, o[4], o[5]);
-          fp8x4_to_bf16(w[e].w, m, o[6], o[7]);
-          if (e < 8) {
-            const uint32_t d = sp + (4 * half + blk4) * kSBlk + r * 128;
-            sts128(d + ch0, o[0], o[1], o[2], o[3]);
-            sts128(d + ch1, o[4], o[5], o[6], o[7]);
-          }
-          if (e < 4 || e >= 8) {
-            const int key = (e >= 8 ? 32 * (1 - rank_i) : 32 * rank_i) + r;   // key & 7 == r & 7
-            const uint32_t d = vp + blk4 * kVBlk + key * 128;
-            sts128(d + ch0, o[0], o[1], o[2], o[3]);
-            sts128(d + ch1, o[4], o[5], o[6], o[7]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int q = 4 * k + (lane >> 3), r = row_base + q;
-          const uint4 z = __shfl_sync(0xffffffffu, at, q) >= 0 ? rp[k] : make_uint4(0, 0, 0, 0);
-          sts128(sp + 8 * kSBlk + r * 128 + (((lane & 7) ^ (r & 7)) << 4), z.x, z.y, z.z, z.w);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_leader(&sh.ready[turn]);
-        fetch_step();
-        page_step();
-        offset_step();
-        return true;
-      };
-      while (ok && walk.next(sg))
-        for (int n = 0; n < sg.n && ok; ++n, ++g)
-          if ((g & 1) == turn) ok = tile_step();
     }
-    // let every copy this CTA started land before its shared memory can be released
-    if constexpr (!FP8) {
-      if (pw == 0 && lane == 0)
-        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full[j & 1], (j >> 1) & 1, 200000000ull);
+    // let every copy this CTA started land before its shared memory can be released (one more wait than
+    // copies where the last tile's were not both started: bounded)
+    if (copies && lane == 0)
+      for (int part = part0; part < part1; ++part)
+        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j)
+          mbar_drain(part ? &sh.full_v[j & 1] : &sh.full_s[j & 1], (j >> 1) & 1, 200000000ull);
+  } else if (FP8 && warp >= C::CONV && warp < C::S_WARP) {
+    // ---------------------------------------------------------------- fp8: codes -> bf16 rows in the ring
+    // Warp w converts the CTA's 32 keys of tiles w, w + kRing, ...: lane l looks up key l of the next tile
+    // (offset, page) while this one is converted, eight rows at a time, a lane taking 16 codes (32 bytes
+    // out) of each.  The loops stay rolled: the roles' code together has to stay in the instruction
+    // caches (all 32 rows unrolled: 4826 us where this takes MEAS_FP8).
+    const uint32_t slot = warp - C::CONV;
+    uint16_t* ring = a.ring + (static_cast<size_t>(grp * kRing + slot) * kRows + 32 * rank) * kDqk;
+    Walk<SEL> aw(walk);
+    Seg as;
+    int ai = 0;
+    bool alive = aw.next(as), ok = true;
+    auto advance = [&](int by) {
+      for (ai += by; alive && ai >= as.n;) {
+        ai -= as.n;
+        alive = aw.next(as);
+      }
+    };
+    int j = -1, len = 0, page = -1;          // lane's key of the tile at ai
+    auto find_offset = [&]() {
+      j = -1;
+      if (!alive) return;
+      len = row_len(a.pg, as.row);
+      const int s = (as.i0 + ai) * kRows + 32 * static_cast<int>(rank) + lane;
+      j = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(as.row) * a.topk + s) : -1;
+    };
+    auto find_page = [&]() {
+      page = -1;
+      if (j >= 0 && j < len)
+        page = __ldg(a.pg.block_table + static_cast<size_t>(as.row) * a.pg.max_pages + (j >> kPageShift));
+    };
+    auto cache_row = [&]() -> int {          // -1: no key
+      const bool in = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pg.n_pages);
+      // a key on a page outside the cache, or a selected one past the end (the tile's tail is neither)
+      if (!in && (SEL ? j >= 0 : j >= 0 && j < len && lane == 0 && rank == 0)) report(sh.faults, DEV_ERR_BAD_INDEX);
+      return in ? (page << kPageShift) + (j & (kPageRows - 1)) : -1;
+    };
+    advance(static_cast<int>(slot));
+    find_offset();
+    find_page();
+    uint32_t lap = 0;
+    for (uint32_t t = slot; ok && t < static_cast<uint32_t>(share); t += kRing, ++lap) {
+      if (a.stop_after >= 0 && t >= static_cast<uint32_t>(a.stop_after)) break;   // test hook
+      const int at = cache_row();
+      const uint32_t sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + max(at, 0));
+      advance(kRing);
+      find_offset();
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint4 w[8], rope[2];
+        int row[8], rr[2];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) row[k] = __shfl_sync(0xffffffffu, at, 8 * q + k);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rr[k] = __shfl_sync(0xffffffffu, at, 8 * q + 4 * k + (lane >> 3));
+        // (rows without a key read a row of the cache all the same: no branch around the loads)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = ldg_once(a.latent + static_cast<size_t>(max(row[k], 0)) * kDv + lane * 16);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rope[k] = ldg_once(a.rope + static_cast<size_t>(max(rr[k], 0)) * 64 + (lane & 7) * 8);
+        if (q == 0) {
+          find_page();
+          if (lap > 0 && !(ok = wait(&sh.ring_empty[slot], (lap - 1) & 1))) break;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t rsc = __shfl_sync(0xffffffffu, sc, 8 * q + k);
+          const uint32_t m = row[k] >= 0 ? fp8_mult((rsc >> (8 * (lane >> 3))) & 0xFFu) : 0u;   // no key: times zero
+          uint32_t o[8];
+          fp8x4_to_bf16(w[k].x, m, o[0], o[1]);
+          fp8x4_to_bf16(w[k].y, m, o[2], o[3]);
+          fp8x4_to_bf16(w[k].z, m, o[4], o[5]);
+          fp8x4_to_bf16(w[k].w, m, o[6], o[7]);
+          stg256(ring + (8 * q + k) * kDqk + lane * 16, o);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(ring + (8 * q + 4 * k + (lane >> 3)) * kDqk + kDv + (lane & 7) * 8) =
+              rr[k] >= 0 ? rope[k] : make_uint4(0, 0, 0, 0);
+      }
+      if (!ok) break;
+      // the rows are visible to both CTAs' copies before they are told
+      __threadfence();
+      fence_proxy_async_global();
+      __syncwarp();
+      if (lane < 2) arrive_cta(&sh.ring_full[slot], lane);
     }
   } else if (warp < kSW) {
     // ---------------------------------------------------------------- softmax + epilogue
     const int qd = warp & 3, cw = warp >> 2;
     const int head = (qd & 1) * 32 + lane;                       // of this CTA's 64
-    const int kbase = (qd >> 1) * 32 + cw * 16;                  // this thread's keys of a tile
+    const int kbase = (qd >> 1) * 32 + cw * kKT;               // this thread's keys of a tile
     const int part = (qd >> 1) * 2 + cw;
     const uint32_t t_lane = static_cast<uint32_t>(qd * 32) << 16;
     const int ghead = static_cast<int>(rank) * kHeads + head;
+    constexpr uint32_t kAll = 0xFFFFu;
     uint32_t g = 0;
     bool stop = false;
     while (!stop && walk.next(sg)) {
@@ -391,35 +393,35 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         const int sb = g & 1;
         uint32_t mask;                                           // bit c: key kbase + c holds a key
         if constexpr (SEL) {
-          const int s = i * kRows + kbase + (lane & 15);
+          const int s = i * kRows + kbase + (lane & (kKT - 1));
           const int j = s < a.topk ? __ldg(irow + s) : -1;
           bool v = j >= 0 && j < len;
           if (v) v = static_cast<uint32_t>(__ldg(bt + (j >> kPageShift))) < static_cast<uint32_t>(a.pg.n_pages);
-          mask = __ballot_sync(0xffffffffu, v) & 0xFFFFu;
+          mask = __ballot_sync(0xffffffffu, v) & kAll;
         } else {
-          const int nv = max(0, min(16, tile_rows(a, len, i, __ldg(bt + (i >> 1))) - kbase));
-          mask = (1u << nv) - 1u;
+          const int nv = tile_rows(a, len, i, __ldg(bt + (i >> 1))) - kbase;
+          mask = nv >= kKT ? kAll : nv <= 0 ? 0u : (1u << nv) - 1u;
         }
         bool ok = wait(&sh.s_full[sb], (g >> 1) & 1);
-        float x[16];
+        float x[kKT];
         float mx = -INFINITY;
         if (ok) {
           tc_fence_after();
-          uint32_t v[16];
+          uint32_t v[kKT];
           tmem_ld16(tmem + t_lane + kSCol + sb * 32 + cw * 16, v);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_leader(&sh.s_empty[sb]);
-          if (mask == 0xFFFFu) {
+          if (lane == 0) arrive_cta(&sh.s_empty[sb], 0);
+          if (mask == kAll) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(v[c]) * a.scale_log2;
+            for (int c = 0; c < kKT; ++c) x[c] = __uint_as_float(v[c]) * a.scale_log2;
           } else {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) x[c] = (mask >> c) & 1u ? __uint_as_float(v[c]) * a.scale_log2 : -INFINITY;
+            for (int c = 0; c < kKT; ++c) x[c] = (mask >> c) & 1u ? __uint_as_float(v[c]) * a.scale_log2 : -INFINITY;
           }
 #pragma unroll
-          for (int c = 0; c < 16; ++c) mx = fmaxf(mx, x[c]);
+          for (int c = 0; c < kKT; ++c) mx = fmaxf(mx, x[c]);
         }
         // the maximum in use follows only when it is outgrown by 2^8 (exact either way)
         if (!ok && lane == 0) sh.soft_abort = 1;
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           lu *= al;
           if (n > 0 && __any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll 2
-            for (int b = 0; b < 8; ++b) {
+            for (int b = 0; b < kOC / 16; ++b) {
               uint32_t o[16];
               tmem_ld16(tmem + t_lane + cw * 128 + b * 16, o);
               tmem_ld_wait();
@@ -459,9 +461,9 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         // P = 2^(s - m), rounded to bf16 (at most 2^-9 of each weight, no bias); the output is divided by
         // the sum of the rounded weights, the log-sum-exp takes the sum of the unrounded ones
         const float ms = m_used == -INFINITY ? 0.f : m_used;     // only masked entries so far: 2^(-inf - 0) = 0
-        uint32_t pk[8];
+        uint32_t pk[kKT / 2];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kKT / 2; ++c) {
           const float p0 = ex2f(x[2 * c] - ms), p1 = ex2f(x[2 * c + 1] - ms);
           const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
           pk[c] = *reinterpret_cast<const uint32_t*>(&pb);
@@ -474,12 +476,13 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           if (!ok && lane == 0) sh.soft_abort = 1;               // seen at the next barrier
         }
         const uint32_t prow = smem_u32(smem + kOffP + sb * kPBytes) + head * 128;
-        sts128(prow + (((kbase / 8) ^ (head & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
-        sts128(prow + (((kbase / 8 + 1) ^ (head & 7)) << 4), pk[4], pk[5], pk[6], pk[7]);
+#pragma unroll
+        for (int c = 0; c < kKT / 8; ++c)
+          sts128(prow + (((kbase / 8 + c) ^ (head & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(&sh.p_full[sb]);
+        if (lane == 0) arrive_cta(&sh.p_full[sb], 0);
       }
       if (stop) break;
       // segment end
@@ -494,13 +497,13 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       named_bar_sync(1, kSoft);                                  // red may be written again
       if (stop) break;
       tc_fence_after();
-      const int dim0 = (qd >> 1) * 256 + cw * 128;               // this thread's 128 dims
+      const int dim0 = (qd >> 1) * 256 + cw * 128;               // this thread's OC dims
       const size_t pslot = static_cast<size_t>(grp) * 2 + (sg.i0 > 0 ? 0 : 1);
       const float inv = l == 0.f ? 0.f : 1.f / l;                // a NaN sum stays NaN; no key: zeros
       uint16_t* orow = a.out + (static_cast<size_t>(sg.row) * a.H + ghead) * kDv + dim0;
       float* prow = a.part_o + (pslot * a.H + ghead) * kDv + dim0;
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < kOC / 32; ++b) {
         uint32_t o[32];
         tmem_ld32(tmem + t_lane + cw * 128 + b * 32, o);
         tmem_ld_wait();
@@ -537,38 +540,37 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_leader(&sh.o_free);
+      if (lane == 0) arrive_cta(&sh.o_free, 0);
     }
   } else if (rank != 0) {
     // ---------------------------------------------------------------- the peer: tell the leader of its Q
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REG_MMA>();
     if (warp == C::S_WARP) {
       uint32_t it = 0;
       while (walk.next(sg)) {
         if (!load_q(it)) break;
-        if (lane == 0) arrive_leader(&sh.q_ready);
+        if (lane == 0) arrive_cta(&sh.q_ready, 0);
         ++it;
       }
     }
   } else {
-    // ---------------------------------------------------------------- MMA issuers (and idle warps)
-    if constexpr (C::REG_SPLIT) setmaxnreg_dec<C::REG_MMA>();
-    const bool issuer = warp <= C::PV_WARP;
+    // ---------------------------------------------------------------- MMA issuers
     constexpr uint32_t id_qk = idesc_bf16_f32(128, kRows, 0, 0);
     constexpr uint32_t id_pv = idesc_bf16_f32(128, 256, 0, 1);
     uint32_t g = 0, it = 0;
     bool ok = true;
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    while (issuer && ok && walk.next(sg)) {
+    while (ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
         ok = load_q(it) && wait(&sh.q_ready, it & 1);
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
-          if (!(ok = wait(&sh.ready[sb], (g >> 1) & 1))) break;
+          if (!(ok = wait(&sh.ready_s[sb], (g >> 1) & 1))) break;
           tc_fence_after();
           const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
-#pragma unroll
+          // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
+          // too slowly for the tensor core: 1913 us where the loop took 1465)
+#pragma unroll FP8 ? 1 : kKB
           for (int kb = 0; kb < kKB; ++kb)
             umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),
                                      dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
@@ -578,27 +580,24 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       } else {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
-          ok = wait(&sh.p_full[sb], (g >> 1) & 1);
+          ok = wait(&sh.ready_v[sb], (g >> 1) & 1) && wait(&sh.p_full[sb], (g >> 1) & 1);
           if (ok && n == 0 && it > 0) ok = wait(&sh.o_free, (it - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t dp = sdesc_sw128(smem_u32(smem + kOffP + sb * kPBytes), 16, 1024);
           const uint64_t dv = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage + kSBytes), kVBlk, 1024);
-#pragma unroll
+#pragma unroll FP8 ? 1 : 2
           for (int h = 0; h < 2; ++h)
             umma_pair_x4_elect<2, 128>(tmem + h * 128, dp, dv + static_cast<uint64_t>((2 * h * kVBlk) >> 4), id_pv,
                                        n > 0 ? 1u : 0u);
-          commit_pair_elect(&sh.empty[sb]);
           commit_pair_elect(&sh.o_done[sb]);
         }
       }
       ++it;
     }
     // every product this warp issued has completed before TMEM is released
-    if (issuer) {
-      commit_pair_elect(&sh.mma_done);
-      mbar_drain(&sh.mma_done, 0, 200000000ull);
-    }
+    commit_pair_elect(&sh.mma_done);
+    mbar_drain(&sh.mma_done, 0, 200000000ull);
   }
   tc_fence_before();
   __syncthreads();
@@ -612,14 +611,6 @@ template <bool FP8, bool SEL>
 cudaError_t launch_t(const CUtensorMap& ts, const CUtensorMap& tv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
   cudaError_t e = smem_attr_once<latent_pair_kernel<FP8, SEL>>(kDynSmem);
   if (e != cudaSuccess) return e;
-  if constexpr (PCfg<FP8>::REG_SPLIT) {
-    // as in the one-CTA kernel: refuse a build whose setmaxnreg.inc could not be granted
-    static const int regs = [] {
-      cudaFuncAttributes fa{};
-      return cudaFuncGetAttributes(&fa, latent_pair_kernel<FP8, SEL>) == cudaSuccess ? fa.numRegs : 0;
-    }();
-    if (regs < PCfg<FP8>::REG_LAUNCH) return cudaErrorInvalidConfiguration;
-  }
   return launch_pdl(latent_pair_kernel<FP8, SEL>, dim3(a.n_cta), PCfg<FP8>::THREADS, kDynSmem, st, SEL, 2, ts, tv, tq, a);
 }
 
