@@ -101,6 +101,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmap_q);
+    if constexpr (!FP8) tma_prefetch_desc(&tmap_kv);
+  }
   if (warp == C::PV_WARP) {
     tmem_alloc(&sh.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
@@ -572,11 +576,13 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           if constexpr (FP8) fence_proxy_async_smem();       // the rotary dims' cp.async copies
           if constexpr (!FP8) {
             if (nv < kRows) {
-              // rows without a key become zeros in all nine blocks (a swizzled row is one
-              // 128-byte line of its block)
-              for (int e = lane; e < (kRows - nv) * 8 * kKB; e += 32) {
-                const int kb = e / ((kRows - nv) * 8), w = e - kb * ((kRows - nv) * 8);
-                sts128(st0 + sb * kTileBytes + kb * kBlkBytes + nv * 128 + w * 16, 0u, 0u, 0u, 0u);
+              // rows without a key become zeros in the eight blocks of latent dims (a swizzled row is one
+              // 128-byte line of its block; their rotary dims only reach masked scores)
+#pragma unroll 1
+              for (int kb = 0; kb < kKB - 1; ++kb) {
+                const uint32_t blk = st0 + sb * kTileBytes + kb * kBlkBytes;
+#pragma unroll 1
+                for (uint32_t o = nv * 128 + lane * 16; o < kBlkBytes; o += 512) sts128(blk + o, 0u, 0u, 0u, 0u);
               }
               fence_proxy_async_smem();
               __syncwarp();
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
           const uint32_t d_s = tmem + C::S_COL + sb * HB;
           // (fp8: rolled, for the instruction cache)
-#pragma unroll FP8 ? 1 : kKB
+#pragma unroll FP8 ? 1 : 3
           for (int kb = 0; kb < kKB; ++kb)
             umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
                                      dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           const uint64_t dv = sdesc_sw128(tb, kBlkBytes, 1024);
           const uint64_t dp = sdesc_sw128(tb + (kKB - 1) * kBlkBytes, kBlkBytes, 1024);
           const uint32_t acc0 = n > 0 ? 1u : 0u;
-#pragma unroll FP8 ? 1 : 4
+#pragma unroll FP8 ? 1 : 2
           for (int b = 0; b < 4; ++b)      // four K steps of 16 rows (2048 B)
             umma_bf16_x4_elect<128, 128>(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes) >> 4), dp, id_pv,
                                          acc0);
@@ -652,13 +658,24 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
   if (lane == 0) row_nt[t] = (last + kRows) / kRows;
 }
 
-// Joins the partials of the rows that were split: block (b, h) takes the row that begins in group
-// b's share and goes on in the next ones, head h.  With M the largest of the partials' maxima m_s
-// and w_s = 2^(m_s - M): out = sum w_s O_s / sum w_s lr_s, lse = ln 2 (M + log2 sum w_s l_s).
-__global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ LArgs a) {
-  const int b = blockIdx.x, h = blockIdx.y;
+// Joins the partials of the rows that were split: block (b, y) takes the row that begins in group b's
+// share and goes on in the next ones (by_row: row b, where there are fewer rows than groups), HPB heads, 8 / HPB warps a head; a warp takes every (8 / HPB)-th
+// partial, a lane 16 dims, and the warps' sums meet in shared memory.  With M the largest of the
+// partials' maxima m_s and w_s = 2^(m_s - M): out = sum w_s O_s / sum w_s lr_s,
+// lse = ln 2 (M + log2 sum w_s l_s).  The order of the sums is fixed.  Few rows, each in many partials,
+// take one head a block (eight warps on one row of 100K keys in 76 partials, 128 heads: MEAS_JOIN_A us,
+// one warp a head 56); many rows, most in two or three, take eight (75 rows: MEAS_JOIN_B us, two heads a
+// block 19).
+template <int HPB>
+__global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LArgs a, bool by_row) {
+  constexpr int kJoinWarps = 8 / HPB;
+  __shared__ float4 sum[HPB][kJoinWarps > 1 ? kJoinWarps - 1 : 1][kJoinWarps > 1 ? kDv / 4 : 1];
+  __shared__ float sl[HPB][kJoinWarps][2];
+  const int lane = threadIdx.x & 31;
+  const int hw = (threadIdx.x >> 5) / kJoinWarps, w = (threadIdx.x >> 5) % kJoinWarps;
+  const int h = blockIdx.y * HPB + hw;
   grid_wait();
-  if (b == 0 && h == 0 && threadIdx.x < 32) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
     uint32_t bits = 0, count = 0;
     for (int i = threadIdx.x; i < a.n_cta; i += 32) {
       bits |= a.err[2 * i];
@@ -672,45 +689,95 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
     }
   }
   const int groups = __ldg(&a.start[a.n_grp].x);
-  if (b + 1 >= groups) return;
+  int b = blockIdx.x;
+  if (by_row) {                                             // the last group that starts at or before the row
+    int below = 0;
+    for (int c = lane; c < groups; c += 32) below += a.start[c].x < b || (a.start[c].x == b && a.start[c].y == 0);
+    b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(below))) - 1;
+  }
+  if (b < 0 || b + 1 >= groups) return;
   const int2 s0 = a.start[b], s1 = a.start[b + 1];
+  if (by_row && s1.x != static_cast<int>(blockIdx.x)) return;
   if (s1.y == 0 || (s0.x == s1.x && s0.y > 0)) return;      // no row goes on, or it began before
   const int row = s1.x;
   int end = b + 2;                                          // groups b .. end - 1 hold the row
-  while (end < groups && a.start[end].x == row && a.start[end].y > 0) ++end;
+  while (end < groups) {                                    // (32 at a time)
+    const int c = end + lane;
+    const int2 s = c < groups ? a.start[c] : make_int2(-1, 0);
+    const uint32_t on = __ballot_sync(0xffffffffu, s.x == row && s.y > 0);
+    end += on == 0xFFFFFFFFu ? 32 : __ffs(static_cast<int>(~on)) - 1;
+    if (on != 0xFFFFFFFFu) break;
+  }
   const size_t n = static_cast<size_t>(a.n_grp) * 2 * a.H;
   auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == b ? 1 : 0)) * a.H + h; };
+  const bool live = h < a.H;
   float M = -INFINITY;
-  bool nan = false;
-  for (int c = b; c < end; ++c) {
-    const float m = a.part_m[slot(c)];
-    M = fmaxf(M, m);
-    nan |= m != m;
+  if (live) {
+    for (int c = b + lane; c < end; c += 32) M = fmaxf(M, a.part_m[slot(c)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   float lr = 0.f, ls = 0.f;
-  for (int c = b; c < end; ++c) {
-    const size_t at = slot(c);
-    const float m = a.part_m[at];
-    const float w = m == -INFINITY ? 0.f : exp2f(m - M);
-    const float4 o = reinterpret_cast<const float4*>(a.part_o + at * kDv)[threadIdx.x];
-    const float l1 = a.part_m[n + at];
-    // a partial whose sum is NaN (a NaN score) keeps its mark even where its max says nothing
-    if (l1 != l1) nan = true;
-    acc.x += w * o.x;
-    acc.y += w * o.y;
-    acc.z += w * o.z;
-    acc.w += w * o.w;
-    lr += w * l1;
-    ls += w * a.part_m[2 * n + at];
+  if (live) {
+#pragma unroll 3
+    for (int c = b + w; c < end; c += kJoinWarps) {
+      const size_t at = slot(c);
+      const float m = __ldg(a.part_m + at), l1 = __ldg(a.part_m + n + at), l2 = __ldg(a.part_m + 2 * n + at);
+      const float4* src = reinterpret_cast<const float4*>(a.part_o + at * kDv) + lane;
+      float4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __ldg(src + 32 * k);
+      // a partial without a key weighs nothing; one whose sum is NaN (a NaN score) makes the row NaN
+      // even where its maximum says nothing
+      const float f = m == -INFINITY ? (l1 == l1 ? 0.f : l1) : exp2f(m - M);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[k].x += f * o[k].x;
+        acc[k].y += f * o[k].y;
+        acc[k].z += f * o[k].z;
+        acc[k].w += f * o[k].w;
+      }
+      lr += f * l1;
+      ls += f * l2;
+    }
   }
-  if (nan) lr = ls = __int_as_float(0x7FC00000);
+  if (w > 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[hw][w - 1][lane + 32 * k] = acc[k];
+  }
+  if (lane == 0) {
+    sl[hw][w][0] = lr;
+    sl[hw][w][1] = ls;
+  }
+  __syncthreads();
+  if (w > 0 || !live) return;
+  lr = ls = 0.f;
+#pragma unroll
+  for (int v = 0; v < kJoinWarps; ++v) {
+    lr += sl[hw][v][0];
+    ls += sl[hw][v][1];
+  }
   const float inv = lr == 0.f ? 0.f : 1.f / lr;
-  const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   const size_t orow = static_cast<size_t>(row) * a.H + h;
-  reinterpret_cast<uint2*>(a.out + orow * kDv)[threadIdx.x] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  if (a.lse && threadIdx.x == 0) a.lse[orow] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int v = 0; v < kJoinWarps - 1; ++v) {
+      const float4 o = sum[hw][v][lane + 32 * k];
+      acc[k].x += o.x;
+      acc[k].y += o.y;
+      acc[k].z += o.z;
+      acc[k].w += o.w;
+    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
+    reinterpret_cast<uint2*>(a.out + orow * kDv)[lane + 32 * k] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  }
+  if (a.lse && lane == 0) a.lse[orow] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
 }
 
 int head_block(int n_heads) { return n_heads <= 16 ? 16 : n_heads <= 32 ? 32 : 64; }
@@ -822,8 +889,12 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
     case 32: e = launch_hb<32>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
     default: e = launch_hb<64>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
   }
-  if (e == cudaSuccess && a.n_cta > 1)
-    e = launch_pdl(latent_join_kernel, L.n_grp > 1 ? dim3(L.n_grp - 1, n_heads) : dim3(1, 1), 128, 0, st, true, 1, a);
+  if (e == cudaSuccess && a.n_cta > 1) {
+    const int hpb = 2LL * n_q <= L.n_grp ? 1 : 8;
+    const bool by_row = n_q < L.n_grp;
+    const dim3 grid = L.n_grp > 1 ? dim3(std::min(n_q, L.n_grp - 1), (n_heads + hpb - 1) / hpb) : dim3(1, 1);
+    e = launch_pdl(hpb == 1 ? latent_join_kernel<1> : latent_join_kernel<8>, grid, 256, 0, st, true, 1, a, by_row);
+  }
   prof_end(ps, st);
   return e;
 }

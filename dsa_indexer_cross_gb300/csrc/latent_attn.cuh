@@ -14,7 +14,11 @@ constexpr int kRows = 64;              // latent rows per tile
 constexpr int kDqk = 576;
 constexpr int kDv = 512;
 constexpr int kKB = kDqk / 64;         // 64-dim blocks per row
-constexpr int kMinTiles = 2;           // a share holds at least this many tiles
+// A share holds at least this many tiles.  A tile costs a CTA about a microsecond, a partial the join
+// about 0.1: 20000 keys, 16 heads, 23 us with shares of 4 or more and 27 with 2, while short rows want
+// them split (1000 keys: 14.6 with 2, 16.6 with 4; 4000 keys, 64 heads, fp8: 20.7 and 22.9).
+constexpr int kMinTiles = 2;
+__device__ __forceinline__ int min_share(long long total) { return total > 128 ? 4 : kMinTiles; }
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -46,6 +50,11 @@ __device__ __forceinline__ uint4 ldg_once(const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+__device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 // x, as a value the compiler cannot carry around a loop (addresses derived from it are formed where they
 // are used instead of being held in registers).
@@ -177,7 +186,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
     if (w < warp) pre += sh.wsum[w];
     total += sh.wsum[w];
   }
-  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + kMinTiles - 1) / kMinTiles));
+  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + min_share(total) - 1) / min_share(total)));
   const long long first = grp < groups ? total * grp / groups : 0;
   const long long share = grp < groups ? total * (grp + 1) / groups - first : 0;
   if (share > 0 && pre <= first && first < pre + mine) {

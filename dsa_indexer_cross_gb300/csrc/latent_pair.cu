@@ -95,11 +95,6 @@ __device__ __forceinline__ void arrive_cta(uint64_t* bar, uint32_t rank) {
       : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
-__device__ __forceinline__ void stg256(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
                : "memory");
@@ -174,6 +169,11 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     sh.faults.bits = sh.faults.count = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_desc(&tmap_q);
+    tma_prefetch_desc(&tmap_s);
+    tma_prefetch_desc(&tmap_v);
   }
   if (warp == C::PV_WARP) {
     tmem_alloc_pair(&sh.tmem_base, kTmemCols);
@@ -258,9 +258,11 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           } else {
             if (!(ok = wait(full, (g >> 1) & 1))) break;
             if (!FP8 && part && nv < kRows) {
-              const int each = (kRows - nv) * 8;                          // 16-byte pieces of one block
-              for (int e = lane; e < each * 4; e += 32)
-                sts128(smem_u32(st) + (e / each) * kVBlk + nv * 128 + (e % each) * 16, 0u, 0u, 0u, 0u);
+#pragma unroll 1
+              for (int vb = 0; vb < 4; ++vb) {
+#pragma unroll 1
+                for (uint32_t o = nv * 128 + lane * 16; o < kVBlk; o += 512) sts128(smem_u32(st) + vb * kVBlk + o, 0u, 0u, 0u, 0u);
+              }
               fence_proxy_async_smem();
             }
             __syncwarp();
@@ -508,22 +510,24 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         tmem_ld32(tmem + t_lane + cw * 128 + b * 32, o);
         tmem_ld_wait();
         if (ghead >= a.H) continue;
+        // a lane's dims are 32-byte pieces of its head's row
         if (sg.whole) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t w[4];
+          for (int v = 0; v < 2; ++v) {
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 ob = __floats2bfloat162_rn(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                                              __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+            for (int e = 0; e < 8; ++e) {
+              const __nv_bfloat162 ob = __floats2bfloat162_rn(__uint_as_float(o[16 * v + 2 * e]) * inv,
+                                                              __uint_as_float(o[16 * v + 2 * e + 1]) * inv);
               w[e] = *reinterpret_cast<const uint32_t*>(&ob);
             }
-            reinterpret_cast<uint4*>(orow + b * 32)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+            // (out is 16-byte aligned)
+            reinterpret_cast<uint4*>(orow + b * 32)[2 * v] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(orow + b * 32)[2 * v + 1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
         } else {
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            reinterpret_cast<uint4*>(prow + b * 32)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          for (int v = 0; v < 4; ++v) stg256(prow + b * 32 + 8 * v, o + 8 * v);
         }
       }
       if (part == 0 && ghead < a.H) {
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
           // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
           // too slowly for the tensor core: 1913 us where the loop took 1465)
-#pragma unroll FP8 ? 1 : kKB
+#pragma unroll FP8 ? 1 : 3
           for (int kb = 0; kb < kKB; ++kb)
             umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),
                                      dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
