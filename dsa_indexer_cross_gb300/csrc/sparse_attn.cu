@@ -97,7 +97,9 @@ struct ACfg {
 // Per-column softmax state lives in shared memory (uniform across the softmax threads).
 struct AShared {
   uint64_t full[2], empty[2];   // per tile slot set (nine 64-dim blocks)
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, o_done[2], o_free;   // o_done[g & 1]: PV(g) complete
+  // p_full, o_done: [g & 1].  (One p_full for all tiles would not do: the softmax may be two tiles ahead
+  // of the PV warp's look, and a barrier two phases on reads as not yet complete.)
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free;   // o_done[g & 1]: PV(g) complete
   uint64_t mma_done;            // both MMA warps' last commits: nothing of theirs in flight
   uint32_t tmem_base, abort_flag, soft_abort;
   uint32_t prod_ok;
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__(ACfg<HB, HD>::THREADS, 1)
       mbar_init(&sh.s_full[b], 1);
       mbar_init(&sh.s_empty[b], C::SW);   // one arrive per softmax warp
     }
-    mbar_init(&sh.p_full, C::SW);
+    mbar_init(&sh.p_full[0], C::SW);
+    mbar_init(&sh.p_full[1], C::SW);
     mbar_init(&sh.o_done[0], 1);
     mbar_init(&sh.o_done[1], 1);
     mbar_init(&sh.o_free, C::SW);
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(ACfg<HB, HD>::THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full);
+        if (lane == 0) mbar_arrive(&sh.p_full[g & 1]);
       }
       if (stop) break;
       // item end: column sums over the 64 rows, then O^T / l -> out
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(ACfg<HB, HD>::THREADS, 1)
         // O^T += V^T P^T: A = the tile's value blocks (MN-major, 64-dim blocks one slot
         // apart), B = P^T in the rope block (MN-major)
         for (int i = 0; i < I.nt && ok; ++i, ++g) {
-          ok = wait(&sh.p_full, g & 1);
+          ok = wait(&sh.p_full[g & 1], (g >> 1) & 1);
           if constexpr (!DENSE && kCpBlocks > 0) fence_proxy_async_smem();   // V blocks written by cp.async
           if (ok && i == 0 && it > 0) ok = wait(&sh.o_free, (it - 1) & 1);
           if (!ok) break;
