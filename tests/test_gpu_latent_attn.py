@@ -350,3 +350,26 @@ def test_a_decode_step_through_every_operator():
     D.dsa_latent_cache_read(cache, pages, B, i32(start), back, ws=ws)
     assert D.dsa_workspace_status(ws) == 0
     assert np.array_equal(back.double().cpu().numpy(), np.concatenate(kv))
+
+
+def test_random_shapes_one_after_another():
+    """Calls of ever new shapes, each kernel's code cold now and then: no wait runs out, whatever the order
+    in which the warps get going."""
+    rng = np.random.default_rng(77)
+    for it in range(90):
+        H = int(rng.choice([1, 16, 24, 40, 64, 100, 128]))
+        fmt = "fp8" if it % 3 else "bf16"
+        lens = rng.integers(0, 1200, size=int(rng.integers(1, 9))).tolist()
+        pc = Paged(lens, fmt, seed=it)
+        q = randn((len(lens), H, 576), gen(it))
+        idx = None
+        if fmt == "fp8" and it % 2:
+            idx = i32(_selection(lens, 200, it))
+        out, lse, ws = attend(pc, q, idx)
+        assert D.dsa_workspace_status(ws) == 0, (it, H, fmt, lens)
+        if it % 10 == 0:
+            rows = [pc.stored(t) for t in range(len(lens))]
+            if idx is not None:
+                sel = idx.cpu().numpy()
+                rows = [r[s[s >= 0]] for r, s in zip(rows, sel)]
+            check_rows(out, lse, q, rows)
