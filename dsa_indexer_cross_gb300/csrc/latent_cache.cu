@@ -114,7 +114,8 @@ __device__ __forceinline__ void sole_status(uint32_t* status, int n, F check) {
 // A thread turns one 16-byte vector (interleaved: its own pairs) or one vector of each half
 // (half layout) of up to U heads of one token, so the token's (cos, sin) are loaded once for U
 // heads and U independent loads are in flight.  Neighbouring threads take neighbouring
-// vectors, then neighbouring heads.
+// vectors, then neighbouring heads.  The input is read once (ld.cs: 22.6 us against 24.6 at 8000
+// tokens of 64 heads, 133 MB); U = 2 and 8 and smaller blocks measured the same.
 template <typename T, bool INTER, int U>
 __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const int32_t* __restrict__ pos,
                                                       const float2* __restrict__ cs, int n_pos, uint32_t n_items,
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
   for (int u = 0; u < U; ++u) {
     const int h = static_cast<int>(hg) + u * head_groups;
     if (h < n_heads) {
-      a[u] = *reinterpret_cast<const uint4*>(xt + h * x_head);
-      if constexpr (!INTER) b[u] = *reinterpret_cast<const uint4*>(xt + h * x_head + half);
+      a[u] = __ldcs(reinterpret_cast<const uint4*>(xt + h * x_head));
+      if constexpr (!INTER) b[u] = __ldcs(reinterpret_cast<const uint4*>(xt + h * x_head + half));
     }
   }
   float c[NP], s[NP];
