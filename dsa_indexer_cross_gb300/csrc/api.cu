@@ -998,8 +998,8 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   if (!c.fp8 || pair) {
     const void* rows = c.fp8 ? static_cast<const uint8_t*>(ws) + kAlign + ring.offset : c.latent;
     const uint64_t n = static_cast<uint64_t>(c.fp8 ? ring.rows : c.n_rows);
-    if ((s = tmap_kv_tiles(&tkv, rows, n, pair ? 32 : 64)) != DSA_OK) return s;
-    if (pair && (s = tmap_kv_tiles(&tv, rows, n, 64, 4)) != DSA_OK) return s;
+    if ((s = tmap_kv_tiles(&tkv, rows, n, pair ? 32 : 64, pair ? 9 : 1)) != DSA_OK) return s;
+    if ((s = tmap_kv_tiles(&tv, rows, n, 64, 4)) != DSA_OK) return s;
   }
   if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
                      static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)

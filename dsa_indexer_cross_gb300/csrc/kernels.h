@@ -252,8 +252,8 @@ cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_s
                               void* out, uint32_t* status, cudaStream_t st);
 
 // Latent attention over a paged cache: every key of row t's sequence (idx == nullptr), or the
-// offsets in idx [n_q][topk] (fp8 cache).  A bf16 cache is read through tmap_kv: up to 64 heads as
-// 64-row tiles (boxes {64, 64, 9}); above, boxes {64, 32, 9} in tmap_kv and {64, 64, 4} in tmap_v.
+// offsets in idx [n_q][topk] (fp8 cache).  A bf16 cache is read through tmap_v, boxes {64, 64, 4},
+// and tmap_kv, boxes {64, 64, 1} (up to 64 heads) or {64, 32, 9}.
 // tmap_q: q as [n_q * n_heads][576], boxes {64, latent_attn_q_box_rows(n_heads)}.
 // For more than 64 heads an fp8 cache's tiles go through a ring of kRing bf16 tiles per CTA pair in the
 // scratch (offset and rows of that array: latent_attn_ring), which the two maps then cover instead.

@@ -51,7 +51,7 @@ struct LCfg {
 };
 
 struct LShared {
-  uint64_t full[2], empty[2];
+  uint64_t full[2][2], empty[2][2];   // by tile parity and half: latent dims 0 .. 255; 256 .. 511 and the rotary dims
   // [2]: by tile parity.  (One p_full for all tiles would not do: the softmax may be two tiles ahead of
   // the PV warp's look, and a barrier two phases on reads as not yet complete.)
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free, mma_done;
@@ -69,7 +69,8 @@ static_assert(LCfg<64, true>::DYN_SMEM + sizeof(LShared) <= 232448, "HB = 64 mus
 
 template <int HB, bool FP8, bool SEL>
 __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap tmap_kv, const __grid_constant__ CUtensorMap tmap_q,
+    latent_attn_kernel(const __grid_constant__ CUtensorMap tmap_kv, const __grid_constant__ CUtensorMap tmap_v,
+                       const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ LArgs a) {
   using C = LCfg<HB, FP8>;
   constexpr int NR = C::NR;
@@ -84,8 +85,11 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.full[s], FP8 ? 33 * (C::NP / 2) : 1);      // fp8: each warp of the group, and each thread's copies
-      mbar_init(&sh.empty[s], 1);
+      // fp8: each warp of the group (second half: and each thread's copies)
+      mbar_init(&sh.full[s][0], FP8 ? C::NP / 2 : 1);
+      mbar_init(&sh.full[s][1], FP8 ? 33 * (C::NP / 2) : 1);
+      mbar_init(&sh.empty[s][0], 1);
+      mbar_init(&sh.empty[s][1], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], C::SW);
       mbar_init(&sh.p_full[s], C::SW);
@@ -103,7 +107,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
   }
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmap_q);
-    if constexpr (!FP8) tma_prefetch_desc(&tmap_kv);
+    if constexpr (!FP8) {
+      tma_prefetch_desc(&tmap_kv);
+      tma_prefetch_desc(&tmap_v);
+    }
   }
   if (warp == C::PV_WARP) {
     tmem_alloc(&sh.tmem_base, C::TMEM_COLS);
@@ -138,12 +145,19 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
             break;
           }
-          if (g >= 2 && !(ok = wait(&sh.empty[g & 1], ((g >> 1) - 1) & 1))) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sh.full[g & 1], kTileBytes);
-            tma_load_3d(sT + (g & 1) * kTileBytes, &tmap_kv, &sh.full[g & 1], 0,
-                        bad ? 0 : (page << kPageShift) + (i & 1) * kRows, 0);
+          uint8_t* st = sT + (g & 1) * kTileBytes;
+          const int row = bad ? 0 : (page << kPageShift) + (i & 1) * kRows;
+#pragma unroll 1
+          for (int h = 0; h < 2 && ok; ++h) {
+            uint64_t* full = &sh.full[g & 1][h];
+            if (g >= 2) ok = wait(&sh.empty[g & 1][h], ((g >> 1) - 1) & 1);
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(full, (4 + h) * kBlkBytes);
+              tma_load_3d(st + 4 * h * kBlkBytes, &tmap_v, full, 0, row, 4 * h);
+              if (h) tma_load_3d(st + 8 * kBlkBytes, &tmap_kv, full, 0, row, 8);
+            }
           }
+          if (!ok) break;
           __syncwarp();
         }
       }
@@ -243,26 +257,34 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       // one tile: registers -> the bf16 tile, then the registers' next fetch
       auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
-        if (g >= 2 && !wait(&sh.empty[turn], ((g >> 1) - 1) & 1)) return false;
-        const uint32_t rl = opaque(tile) + 8 * kBlkBytes + row_base * 128;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int q = 4 * k + (lane >> 3);                              // row, 16-byte chunk lane & 7
-          const int from = __shfl_sync(0xffffffffu, at, q);
-          cp_async_16_zfill(rl + q * 128 + (((lane & 7) ^ (q & 7)) << 4),
-                            a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
-        }
-        cp_async_mbar_arrive(&sh.full[turn]);
         const uint32_t line = opaque(lane_line);
+        uint32_t rsc[8];                     // scale words of this lane's rows; all ones: no key
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t rsc = __shfl_sync(0xffffffffu, sc, 2 * k + par);
-          const bool in = __shfl_sync(0xffffffffu, at, 2 * k + par) >= 0;
-          const uint32_t d = line ^ (static_cast<uint32_t>((2 * k) & 7) << 4);
+          rsc[k] = __shfl_sync(0xffffffffu, sc, 2 * k + par);
+          if (__shfl_sync(0xffffffffu, at, 2 * k + par) < 0) rsc[k] = 0xFFFFFFFFu;
+        }
+        // half by half: the first product starts on the first while the second is converted, and the
+        // previous tile's second product leaves the first half before it is done with the other
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          if (g >= 2 && !wait(&sh.empty[turn][h], ((g >> 1) - 1) & 1)) return false;
+          if (h == 1) {
+            const uint32_t rl = opaque(tile) + 8 * kBlkBytes + row_base * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int q = 4 * k + (lane >> 3);                          // row, 16-byte chunk lane & 7
+              const int from = __shfl_sync(0xffffffffu, at, q);
+              cp_async_16_zfill(rl + q * 128 + (((lane & 7) ^ (q & 7)) << 4),
+                                a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
+            }
+            cp_async_mbar_arrive(&sh.full[turn][1]);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t d = line ^ (static_cast<uint32_t>((2 * k) & 7) << 4);
             // a row without a key: times zero
-            const uint32_t m = in ? fp8_mult((rsc >> (16 * h + 8 * (blk4 >> 1))) & 0xFFu) : 0u;
+            const uint32_t m = rsc[k] == 0xFFFFFFFFu ? 0u : fp8_mult((rsc[k] >> (16 * h + 8 * (blk4 >> 1))) & 0xFFu);
             const uint4 v = w[2 * k + h];
             uint32_t o[8];
             fp8x4_to_bf16(v.x, m, o[0], o[1]);
@@ -272,10 +294,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             sts128(d + 256 * k + 4 * h * kBlkBytes, o[0], o[1], o[2], o[3]);
             sts128((d ^ 16u) + 256 * k + 4 * h * kBlkBytes, o[4], o[5], o[6], o[7]);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[turn][h]);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[turn]);
         offset_step();
         fetch_step();
         page_step();
@@ -287,7 +309,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     // let every copy this CTA started land before its shared memory can be released
     if constexpr (!FP8) {
       if (lane == 0)
-        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full[j & 1], (j >> 1) & 1, 200000000ull);
+        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j)
+          for (int h = 0; h < 2; ++h) mbar_drain(&sh.full[j & 1][h], (j >> 1) & 1, 200000000ull);
     }
   } else if (warp < C::SW) {
     // ---------------------------------------------------------------- softmax + epilogue
@@ -572,14 +595,18 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           int nv = kRows;
           if constexpr (!FP8) nv = tile_rows(a, len, sg.i0 + n, __ldg(bt + ((sg.i0 + n) >> 1)));
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
-          if (!(ok = wait(&sh.full[sb], (g >> 1) & 1))) break;
-          if constexpr (FP8) fence_proxy_async_smem();       // the rotary dims' cp.async copies
-          if constexpr (!FP8) {
-            if (nv < kRows) {
-              // rows without a key become zeros in the eight blocks of latent dims (a swizzled row is one
-              // 128-byte line of its block; their rotary dims only reach masked scores)
+          const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
+          const uint32_t d_s = tmem + C::S_COL + sb * HB;
+#pragma unroll
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (!(ok = wait(&sh.full[sb][h], (g >> 1) & 1))) break;
+            if constexpr (FP8) {
+              fence_proxy_async_smem();        // the rotary dims' cp.async copies
+            } else if (nv < kRows) {
+              // rows without a key become zeros in the blocks of latent dims (a swizzled row is one 128-byte
+              // line of its block; their rotary dims only reach masked scores)
 #pragma unroll 1
-              for (int kb = 0; kb < kKB - 1; ++kb) {
+              for (int kb = 4 * h; kb < 4 * h + 4; ++kb) {
                 const uint32_t blk = st0 + sb * kTileBytes + kb * kBlkBytes;
 #pragma unroll 1
                 for (uint32_t o = nv * 128 + lane * 16; o < kBlkBytes; o += 512) sts128(blk + o, 0u, 0u, 0u, 0u);
@@ -587,15 +614,14 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
+            tc_fence_after();
+            // (fp8: rolled, for the instruction cache)
+#pragma unroll FP8 ? 1 : 5
+            for (int kb = 4 * h; kb < 4 + 5 * h; ++kb)
+              umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
+                                       dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
           }
-          tc_fence_after();
-          const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
-          const uint32_t d_s = tmem + C::S_COL + sb * HB;
-          // (fp8: rolled, for the instruction cache)
-#pragma unroll FP8 ? 1 : 3
-          for (int kb = 0; kb < kKB; ++kb)
-            umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
-                                     dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
+          if (!ok) break;
           umma_commit_elect(&sh.s_full[sb]);
         }
         if (ok) umma_commit_elect(&sh.q_empty);
@@ -610,11 +636,13 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           const uint64_t dv = sdesc_sw128(tb, kBlkBytes, 1024);
           const uint64_t dp = sdesc_sw128(tb + (kKB - 1) * kBlkBytes, kBlkBytes, 1024);
           const uint32_t acc0 = n > 0 ? 1u : 0u;
-#pragma unroll FP8 ? 1 : 2
-          for (int b = 0; b < 4; ++b)      // four K steps of 16 rows (2048 B)
+#pragma unroll FP8 ? 1 : 4
+          for (int b = 0; b < 4; ++b) {    // four K steps of 16 rows (2048 B)
             umma_bf16_x4_elect<128, 128>(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes) >> 4), dp, id_pv,
                                          acc0);
-          umma_commit_elect(&sh.empty[g & 1]);
+            if (b == 1) umma_commit_elect(&sh.empty[g & 1][0]);
+          }
+          umma_commit_elect(&sh.empty[g & 1][1]);
           umma_commit_elect(&sh.o_done[g & 1]);
         }
       }
@@ -810,16 +838,18 @@ Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
 }
 
 template <int HB, bool FP8, bool SEL>
-cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
+cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq, const LArgs& a,
+                     cudaStream_t st) {
   using C = LCfg<HB, FP8>;
   cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, SEL>>(C::DYN_SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, SEL, 1, tkv, tq, a);
+  return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, SEL, 1, tkv, tv, tq, a);
 }
 template <int HB>
-cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
-  if (!fp8) return launch_t<HB, false, false>(tkv, tq, a, st);
-  return sel ? launch_t<HB, true, true>(tkv, tq, a, st) : launch_t<HB, true, false>(tkv, tq, a, st);
+cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq,
+                      const LArgs& a, cudaStream_t st) {
+  if (!fp8) return launch_t<HB, false, false>(tkv, tv, tq, a, st);
+  return sel ? launch_t<HB, true, true>(tkv, tv, tq, a, st) : launch_t<HB, true, false>(tkv, tv, tq, a, st);
 }
 
 }  // namespace
@@ -885,12 +915,12 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   if (L.n_hb == 2) {
     e = launch_latent_pair(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st);
   } else switch (head_block(n_heads)) {
-    case 16: e = launch_hb<16>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
-    case 32: e = launch_hb<32>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
-    default: e = launch_hb<64>(c.fp8, sel, tmap_kv, tmap_q, a, st); break;
+    case 16: e = launch_hb<16>(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st); break;
+    case 32: e = launch_hb<32>(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st); break;
+    default: e = launch_hb<64>(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st); break;
   }
   if (e == cudaSuccess && a.n_cta > 1) {
-    const int hpb = 2LL * n_q <= L.n_grp ? 1 : 8;
+    const int hpb = 8LL * n_q <= L.n_grp ? 1 : 8;      // eight partials a row and more, or fewer
     const bool by_row = n_q < L.n_grp;
     const dim3 grid = L.n_grp > 1 ? dim3(std::min(n_q, L.n_grp - 1), (n_heads + hpb - 1) / hpb) : dim3(1, 1);
     e = launch_pdl(hpb == 1 ? latent_join_kernel<1> : latent_join_kernel<8>, grid, 256, 0, st, true, 1, a, by_row);

@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
           // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
           // too slowly for the tensor core: 1913 us where the loop took 1465)
-#pragma unroll FP8 ? 1 : 3
+#pragma unroll FP8 ? 1 : kKB
           for (int kb = 0; kb < kKB; ++kb)
             umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),
                                      dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
