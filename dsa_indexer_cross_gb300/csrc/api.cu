@@ -873,6 +873,12 @@ dsa_status dsa_rope_apply(const dsa_rope_desc* d, const void* x, const int32_t* 
     return fail(DSA_ERR_ARG, "out's strides must be at least rope_dim");
   if (static_cast<long long>(d->n_tokens) * d->n_heads > 0x7FFFFFFFLL)
     return fail(DSA_ERR_SHAPE, "n_tokens * n_heads exceeds the int32 range");
+  if (static_cast<long long>(d->n_heads) * (d->rope_dim / 2) > kRopeMostPairs)
+    return fail(DSA_ERR_SHAPE, "n_heads * rope_dim / 2 exceeds %lld", kRopeMostPairs);
+  if (d->n_tokens > 1 && d->n_heads > 1 &&
+      d->out_head_stride > (d->out_token_stride - d->rope_dim) / (d->n_heads - 1) &&
+      d->out_token_stride > (d->out_head_stride - d->rope_dim) / (d->n_tokens - 1))
+    return fail(DSA_ERR_ARG, "out's heads must lie within a token's stride, or its tokens within a head's");
   if (x == out && (d->x_token_stride != d->out_token_stride || d->x_head_stride != d->out_head_stride))
     return fail(DSA_ERR_ARG, "in place, x and out need the same strides");
   dsa_status s;
@@ -980,6 +986,7 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
   if (static_cast<long long>(d.n_q) * d.n_heads > 0x7FFFFFFFLL)
     return fail(DSA_ERR_SHAPE, "n_q * n_heads exceeds the int32 range");
+  if (idx && d.topk > (1 << 30)) return fail(DSA_ERR_SHAPE, "topk %d exceeds 2^30", d.topk);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (idx && !c.fp8)   // selected rows of a bf16 cache: the sparse kernel's gather walk
     return run_attn(&d, q, c.latent, idx, nullptr, out, lse, ws, ws_bytes, st, true, nullptr, &pg);

@@ -222,7 +222,9 @@ cudaError_t launch_sparse_attn_bwd_dense(int hd, const CUtensorMap& tmap_kv, con
                                          void* scratch, cudaStream_t st);
 
 // ---------------------------------------------------------------------------- latent cache
-// out[t, h, :rope] = the rotary dims x[t, h, :rope] turned at pos[t] (strides in elements).
+// out[t, h, :rope] = the rotary dims x[t, h, :rope] turned at pos[t] (strides in elements).  One launch
+// turns at most kRopeMostPairs pairs (32-bit thread numbers); a token's fit into one.
+constexpr long long kRopeMostPairs = 0x7FFFFF00LL;
 struct RopeApply {
   const void* x;
   void* out;
@@ -266,8 +268,8 @@ LatentRing latent_attn_ring(int n_q, int n_heads, const PagedRows& pg, bool sele
 int latent_attn_q_box_rows(int n_heads);
 size_t latent_attn_ws_bytes(int n_q, int n_heads);
 cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
-                               const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
-                               void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
+                               const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads,
+                               int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
 
 int device_sm_count();
 

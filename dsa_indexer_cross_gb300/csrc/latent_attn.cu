@@ -1,5 +1,6 @@
 // Latent attention of one query row per sequence over a paged latent cache (bf16 or fp8): every
-// cached key of the sequence, or the keys an index row selects (fp8), on tcgen05.
+// cached key of the sequence, or the keys an index row selects (fp8), on tcgen05.  The kernel here
+// serves up to 64 heads, latent_pair.cu's 65 to 128; split, join and launch are common.
 //
 //   o[t, h] = sum_j softmax_j(tau * q[t, h] . kv_j) * kv_j[:512]      kv_j: row j of sequence t
 //
@@ -17,10 +18,19 @@
 // unnormalised partials (fp32 O, the max in use, both sums) that a second kernel joins.  The
 // lengths are device data: every CTA finds its share from a block scan over them.
 //
-// How rows arrive.  bf16: one 3-D TMA box per tile (half a page).  fp8: producer warps load codes
-// into registers one tile ahead, convert and store the bf16 tile; power-of-two scales make that
-// exact.  Rows past the sequence's end, or on a page outside the cache, are written as zeros
-// before the products (an uninitialised page may hold NaN, which a zero weight does not cancel).
+// How rows arrive.  bf16: TMA boxes of half a page's rows.  fp8: eight converter warps load codes into
+// registers up to two tiles ahead and store the bf16 tile; power-of-two scales make that exact.  Either
+// way a tile is filled and freed in two halves (latent dims 0 .. 255; the rest and the rotary dims), so
+// the first product starts on one while the other is on its way (16 heads, fp8: 800 -> 747 us; bf16 and
+// 64 heads the same).  Rows past the sequence's end, or on a page outside the cache, are written as
+// zeros before the products (an uninitialised page may hold NaN, which a zero weight does not cancel).
+//
+// What bounds it (64 rows of 8K to 131K keys, 4.8M in all; a copy moves 6.78 TB/s here).  bf16 reads
+// 5.6 GB: 803 us at 16 and 32 heads, 860 at 64 (6.9 and 6.5 TB/s): HBM.  fp8 reads 3.1 GB: 749 us at 16
+// heads, 808 at 32, 1022 at 64 (4.1, 3.8, 3.0 TB/s): the way of a tile from codes through registers and
+// shared memory to its products, whose operand reads and the converters' writes share the SM's
+// shared-memory bandwidth.  Selected keys (2048 of each row): 45 us at 16 heads, 70 at 64: the gathers'
+// latency, the partials and their join.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,7 +47,8 @@ template <int HB, bool FP8>
 struct LCfg {
   static constexpr int Q_BYTES = HB * kDqk * 2;
   static constexpr int DYN_SMEM = 1024 + 2 * kTileBytes + Q_BYTES;
-  static constexpr int SW = HB >= 32 && !FP8 ? 8 : 4;  // softmax warps (fp8: four, which leaves the converters 128 registers)
+  // softmax warps (fp8: four, which leaves the converters 128 registers)
+  static constexpr int SW = HB >= 32 && !FP8 ? 8 : 4;
   static constexpr int SOFT = 32 * SW;
   static constexpr int NP = FP8 ? 8 : 1;               // producer warps
   static constexpr int S_WARP = SW + NP;
@@ -136,7 +147,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       while (ok && walk.next(sg)) {
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
         int ahead = __ldg(bt + (sg.i0 >> 1));
-        for (int n = 0; n < sg.n; ++n, ++g) {
+        for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int i = sg.i0 + n, page = ahead;
           if (n + 1 < sg.n) ahead = __ldg(bt + ((i + 1) >> 1));
           const bool bad = page < 0 || page >= a.pg.n_pages;
@@ -157,7 +168,6 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
               if (h) tma_load_3d(st + 8 * kBlkBytes, &tmap_kv, full, 0, row, 8);
             }
           }
-          if (!ok) break;
           __syncwarp();
         }
       }
@@ -253,7 +263,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       const uint32_t tile = smem_u32(sT + turn * kTileBytes);
       // the lane's line of row par in block blk4, swizzled for chunk 2 c; row 2 k + par's lies 256 k on, its
       // swizzle differs by 2 k (mod 8)
-      const uint32_t lane_line = tile + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
+      const uint32_t lane_line =
+          tile + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
       // one tile: registers -> the bf16 tile, then the registers' next fetch
       auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
@@ -306,7 +317,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       for (g = turn; ok && g < static_cast<uint32_t>(share); g += 2) ok = tile_step();
       cp_async_wait<0>();
     }
-    // let every copy this CTA started land before its shared memory can be released
+    // let every copy this CTA started land before its shared memory can be released (a wait that ran out
+    // between a tile's halves leaves one more wait here than copies: bounded)
     if constexpr (!FP8) {
       if (lane == 0)
         for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j)
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             tmem_st_wait();
           }
         }
-        // P = 2^(s - m), rounded to bf16 for the second product (at most 2^-9 of each weight, no
+        // P = 2^(s - m), rounded to bf16 for the second product (at most 2^-8 of each weight, no
         // bias), into the tile's rope block, which S^T no longer needs.  The output is divided by
         // the sum of the rounded weights, so that they add up to one; the log-sum-exp takes the
         // sum of the unrounded ones.
@@ -687,13 +699,12 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
 }
 
 // Joins the partials of the rows that were split: block (b, y) takes the row that begins in group b's
-// share and goes on in the next ones (by_row: row b, where there are fewer rows than groups), HPB heads, 8 / HPB warps a head; a warp takes every (8 / HPB)-th
-// partial, a lane 16 dims, and the warps' sums meet in shared memory.  With M the largest of the
+// share and goes on in the next ones (by_row: row b, where there are fewer rows than groups), HPB heads,
+// 8 / HPB warps a head; a warp takes every (8 / HPB)-th partial, a lane 16 dims, and the warps' sums meet in shared memory.  With M the largest of the
 // partials' maxima m_s and w_s = 2^(m_s - M): out = sum w_s O_s / sum w_s lr_s,
 // lse = ln 2 (M + log2 sum w_s l_s).  The order of the sums is fixed.  Few rows, each in many partials,
-// take one head a block (eight warps on one row of 100K keys in 76 partials, 128 heads: MEAS_JOIN_A us,
-// one warp a head 56); many rows, most in two or three, take eight (75 rows: MEAS_JOIN_B us, two heads a
-// block 19).
+// take one head a block (eight warps on one row of 100K keys in 76 partials, 128 heads: 17 us, one
+// warp a head 56); many rows, most in two or three, take eight (75 rows: 12 us, two heads a block 19).
 template <int HPB>
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LArgs a, bool by_row) {
   constexpr int kJoinWarps = 8 / HPB;
@@ -873,8 +884,8 @@ size_t latent_attn_ws_bytes(int n_q, int n_heads) {
 }
 
 cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
-                               const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads, int topk, float scale,
-                               void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st) {
+                               const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads,
+                               int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st) {
   const bool sel = idx != nullptr;
   const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, sel, topk));
   uint8_t* base = static_cast<uint8_t*>(scratch);

@@ -423,9 +423,9 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
   const int groups = vec ? (a.n_heads + U - 1) / U : a.n_heads;
   const long long per = static_cast<long long>(groups) * (vec ? a.rope / (INTER ? V : 2 * V) : a.rope / 2);
   // thread indices are 32-bit: larger problems go in several launches
-  const int most = static_cast<int>(std::max(1LL, std::min<long long>(a.n_tokens, 0x7FFFFF00LL / per)));
+  const int most = static_cast<int>(std::max(1LL, std::min<long long>(a.n_tokens, kRopeMostPairs / per)));
   const float sgn = a.inverse ? -1.f : 1.f;
-  const int sole = a.n_tokens <= kSoleMostRope ? a.n_tokens : 0;
+  const int sole = a.n_tokens <= std::min(kSoleMostRope, most) ? a.n_tokens : 0;      // (one launch)
   cudaError_t e = sole ? cudaSuccess : cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
   if (e != cudaSuccess) return e;
   for (int t0 = 0; t0 < a.n_tokens; t0 += most) {

@@ -9,8 +9,8 @@
 //     S[h, r]  = Q[h, :576] . Rows[r, :576]      M = 2 x 64 heads, N = 64 rows (32 from each CTA), K = 576
 //     O[h, d] += P[h, r] . Rows[r, d]            M = 2 x 64 heads, N = 256 dims (128 from each CTA) twice,
 //                                                K = 64 rows
-// Per 64-row tile a CTA's operand reads fall from 240 KB to 156 KB, the rows that it converts or loads
-// from 72 KB to 68 KB (written) and 41 KB to 29 KB (fp8 codes read).
+// Per 64-row tile a CTA's operand reads fall from 240 KB to 156 KB, the rows that it loads from 72 KB to
+// 68 KB, the fp8 rows that it converts from 64 to 32.
 //
 // Shared memory of a tile in CTA r (its dims: [256 r, 256 r + 256), its keys: rows 32 r .. 32 r + 31):
 //   S part: its 32 keys, all 576 dims   (nine 64-dim blocks of 32 rows x 128 B)
@@ -19,12 +19,23 @@
 // in both CTAs (a descriptor holds for the pair) and its own row order.  They are filled and freed
 // apart: the S part of tile g + 2 as soon as S(g) is complete, the V part once PV(g) is, so the way
 // of a tile from its rows to its product does not limit how often one begins (one barrier for both
-// parts: 1487 us where the two take MEAS_BF16, 64 rows of 8K to 131K keys, 128 heads, bf16).
+// parts: 1487 us where the two take 1116, 64 rows of 8K to 131K keys, 128 heads, bf16).
 //
 // TMEM.  An M = 128 accumulator of a pair has head h of each CTA in lane h for the first half of the
 // columns and in lane 64 + h for the second half: O is 2 x 128 columns, S 32 columns, double-buffered.
 // A softmax thread owns one head and 16 of a tile's 64 keys, so the running maximum is a register and
 // the slow path (a maximum that grew by more than 2^8) exchanges four values a head.
+//
+// fp8.  The two parts of a tile overlap, so converting into shared memory would convert (or write) the
+// overlap twice.  Instead each CTA converts its 32 keys once, whole rows, into a ring of bf16 tiles in the
+// workspace that stays in L2 (kRing tiles a pair, 0.6 MB; 45 MB in all), and both CTAs' TMA boxes pick
+// their parts from there as they do from a bf16 cache (1900 us and more where converters wrote the parts
+// into shared memory).
+//
+// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1116 us, 1202 TFLOP/s of a measured
+// 1924 and 5.0 TB/s of 6.78: operand reads from shared memory next to the copies' writes.  fp8: 1441 us,
+// 932 TFLOP/s, 2.2 TB/s: the same, and the converters' loads and stores through L1.  (Scoring two tiles
+// with one N = 128 product: bf16 1653, fp8 2008 us.)
 //
 // The leader (the pair's even CTA) issues every product; the peer's warps signal its barriers.  Every
 // wait is bounded; the CTAs leave together (a cluster barrier behind the last wait), so no signal goes
@@ -83,10 +94,11 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrive on the copy of `bar` in the pair's CTA `rank` (0: the leader).  What the arrival publishes lies in this CTA's own shared
-// memory and TMEM and is read there by this SM's tensor core, so the order within the CTA is enough
-// (fence.proxy.async, tcgen05 fences and the CTA-scope release before it); a cluster-scope release took
-// about 1100 cycles on the path from one tile to the next.
+// Arrive on the copy of `bar` in the pair's CTA `rank` (0: the leader).  What the arrival publishes lies in
+// this CTA's own shared memory and TMEM and is read there by this SM's tensor core, so the order within
+// the CTA is enough (fence.proxy.async, tcgen05 fences and the CTA-scope release before it); a
+// cluster-scope release took about 1100 cycles on the path from one tile to the next.  (The ring's rows in
+// global memory are fenced at GPU scope by their writers.)
 __device__ __forceinline__ void arrive_cta(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n mbarrier.arrive.shared::cluster.b64 _, [a];\n}\n" ::"r"(
@@ -292,7 +304,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     // Warp w converts the CTA's 32 keys of tiles w, w + kRing, ...: lane l looks up key l of the next tile
     // (offset, page) while this one is converted, eight rows at a time, a lane taking 16 codes (32 bytes
     // out) of each.  The loops stay rolled: the roles' code together has to stay in the instruction
-    // caches (all 32 rows unrolled: 4826 us where this takes MEAS_FP8).
+    // caches (all 32 rows unrolled: 4826 us where this takes 1441).
     const uint32_t slot = warp - C::CONV;
     uint16_t* ring = a.ring + (static_cast<size_t>(grp * kRing + slot) * kRows + 32 * rank) * kDqk;
     Walk<SEL> aw(walk);
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
             tmem_st_wait();
           }
         }
-        // P = 2^(s - m), rounded to bf16 (at most 2^-9 of each weight, no bias); the output is divided by
+        // P = 2^(s - m), rounded to bf16 (at most 2^-8 of each weight, no bias); the output is divided by
         // the sum of the rounded weights, the log-sum-exp takes the sum of the unrounded ones
         const float ms = m_used == -INFINITY ? 0.f : m_used;     // only masked entries so far: 2^(-inf - 0) = 0
         uint32_t pk[kKT / 2];
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           tc_fence_after();
           const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
           // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
-          // too slowly for the tensor core: 1913 us where the loop took 1465)
+          // too slowly for the tensor core: 1913 us where the loop takes 1441)
 #pragma unroll FP8 ? 1 : kKB
           for (int kb = 0; kb < kKB; ++kb)
             umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),

@@ -438,14 +438,14 @@ typedef struct dsa_rope_desc {
  * dims of head 0 of token 0 and are strided, so a projection's [n][H][128 + 64] rotary part goes
  * straight into the absorbed query's [n][H][512 + 64] (dsa_sparse_attn takes q already rotated; [MB]
  * qk_rope_head_dim commit: 64 rotary dims); only these dims are read and written.  out may be x with
- * the same strides (in place); otherwise no element of out may be an element of x, nor may two of
- * out's coincide.
+ * the same strides (in place); otherwise no element of out may be an element of x.  out's heads lie
+ * within a token's stride, or its tokens within a head's.
  *   pos int32 [n_tokens], each in [0, rope_n_pos); another one leaves its token's out as it was and is
  *   flagged (DSA_ERR_DEVICE in the workspace status).  rope_cs f32 [rope_n_pos][rope_dim/2][2], 16-byte
  *   aligned (dsa_rope_table, dsa_rope_table_scaled; device copy).  ws: at least 256 bytes.
  * 16-byte vectors are used where addresses, strides and rope_dim allow, single pairs elsewhere.
- * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_tokens * n_heads beyond int32), DSA_ERR_WORKSPACE,
- * DSA_ERR_CUDA. */
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_tokens * n_heads beyond int32, n_heads * rope_dim / 2 beyond
+ * 2^31 - 256), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
 dsa_status dsa_rope_apply(const dsa_rope_desc* desc, const void* x, const int32_t* pos, const float* rope_cs,
                           int32_t rope_n_pos, void* out, void* ws, size_t ws_bytes, void* stream);
 
@@ -460,7 +460,8 @@ dsa_status dsa_rope_apply(const dsa_rope_desc* desc, const void* x, const int32_
  *     amax <= 448 * 2^e, kept within [-100, 7]; codes are rounded to nearest even and saturate, so
  *     a stored value is within 2^-4 of the value, or 2^-10 * 2^e near zero.  Powers of two make every
  *     stored value exact in bf16.  A group holding a NaN or an infinity is stored as scale byte 255;
- *     bytes above 134 read as NaN.
+ *     bytes above 134 read as NaN.  Writing stores no NaN codes (0x7F, 0xFF); under a scale byte up to
+ *     134 they read as +-480 * 2^(scale[g] - 127).
  * All three arrays 16-byte aligned. */
 #define DSA_CACHE_BF16 0
 #define DSA_CACHE_FP8 1
@@ -519,7 +520,7 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
  *   q bf16 [n_q][n_heads][576], out bf16 [n_q][n_heads][512], 16-byte aligned; lse f32 [n_q][n_heads]
  *   or NULL; block_table and seq_len hold n_q rows; desc->n_kv == cache->n_rows.
  * ws: dsa_latent_attn_workspace_size(desc) bytes.  Errors: those of dsa_sparse_attn_paged, DSA_ERR_ARG
- * (the cache), DSA_ERR_SHAPE (n_q * n_heads beyond int32). */
+ * (the cache), DSA_ERR_SHAPE (n_q * n_heads beyond int32, topk beyond 2^30). */
 dsa_status dsa_latent_attn_workspace_size(const dsa_attn_desc* desc, size_t* bytes);
 dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
                                  const int32_t* idx, const dsa_paged_cache* pages, void* out, float* lse, void* ws,

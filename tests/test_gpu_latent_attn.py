@@ -228,6 +228,62 @@ def test_captured_call_follows_new_lengths_and_pages():
         check_rows(out, lse, q, [pc.stored(t)[:L] for t, L in enumerate(lens)])
 
 
+@pytest.mark.parametrize("H,fmt", [(16, "fp8"), (64, "fp8"), (128, "fp8"), (128, "bf16")])
+def test_two_captured_graphs_share_a_workspace(H, fmt):
+    """Graphs of two shapes, one over every key and one over selected ones, replayed in turn on one
+    stream with one workspace, and between eager calls on it."""
+    pa, pb = Paged([700, 3, 2100], fmt, seed=33), Paged([90, 1500, 0, 64, 800], fmt, seed=34)
+    qa, qb = randn((3, H, 576), gen(35)), randn((5, H, 576), gen(36))
+    sel = i32(_selection(pb.lens, 150, 3))
+    need = max(D.dsa_latent_attn_workspace_size(D.attn_desc(n, pc.n_pages * P, H, k, TAU))
+               for n, pc, k in ((3, pa, 0), (5, pb, 150)))
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    calls = [(pa, qa, None), (pb, qb, sel)]
+    want = [attend(*c, ws=ws) for c in calls]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    with torch.cuda.stream(s):
+        for pc, q, idx in calls:
+            graphs.append(torch.cuda.CUDAGraph())
+            desc = D.attn_desc(q.shape[0], pc.n_pages * P, H, 0 if idx is None else idx.shape[1], TAU)
+            out, lse = torch.empty_like(want[len(outs)][0]), torch.empty_like(want[len(outs)][1])
+            outs.append((out, lse))
+            with torch.cuda.graph(graphs[-1], stream=s):
+                D.dsa_latent_attn_paged(desc, q, pc.cache, idx, pc.pages, out, lse, ws=ws)
+        for turn in range(6):
+            for gr, (o, l), w, c in zip(graphs, outs, want, calls):
+                o.fill_(3.0)
+                l.fill_(3.0)
+                gr.replay()
+                if turn & 1:
+                    again = attend(*c, ws=ws)
+                    assert torch.equal(again[0], w[0])
+                assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+        assert D.dsa_workspace_status(ws) == 0
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("H,fmt,sel", [(16, "bf16", False), (128, "bf16", False), (16, "fp8", True), (128, "fp8", True),
+                                       (128, "fp8", False)])
+@pytest.mark.parametrize("stop", [1, 3])
+def test_waits_that_run_out_in_mid_sequence(H, fmt, sel, stop):
+    """The feed stops after a tile or three of each CTA: reported, and the next call is clean."""
+    pc = Paged([30000, 20000], fmt, seed=63)
+    q = randn((2, H, 576), gen(64))
+    idx = i32(_selection(pc.lens, 12000, 5)) if sel else None
+    ref, lse, ws = attend(pc, q, idx)
+    try:
+        D.dsa_debug_pipeline(stop_after_tiles=stop, wait_ns=1_000_000)
+        attend(pc, q, idx, ws=ws)
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) & 1
+    finally:
+        D.dsa_debug_pipeline(-1, 0)
+    out, l2, _ = attend(pc, q, idx, ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    assert torch.equal(out, ref) and torch.equal(l2, lse)
+
+
 def test_rows_of_drafts_share_their_sequence():
     """Verifying drafts: rows with the same pages and growing lengths, each causal."""
     pc = Paged([1003], "bf16", seed=41)

@@ -113,6 +113,28 @@ def test_rope_skips_and_flags_positions_outside_the_table():
     D.dsa_rope_apply(D.rope_desc(e, e), e, i32([]), tab, e)
 
 
+@pytest.mark.parametrize("rope,offset", [(512, 0), (510, 1)])
+def test_rope_of_more_pairs_than_one_launch_turns(rope, offset):
+    """2^31 pairs and more of few tokens (odd widths: one a thread): several launches, one status.  x is
+    one token's heads for all (a stride of zero); a token outside the table lies in the last launch."""
+    n, h = 260, 32768 + 700
+    g = gen(77)
+    x = torch.randn((h, 512), generator=g, device=DEV).to(torch.bfloat16)[:, offset:offset + rope].expand(n, h, rope)
+    out = torch.full((n, h, 512), 3.0, dtype=torch.bfloat16, device=DEV)
+    ov = out[..., offset:offset + rope]
+    tab = D.dsa_rope_table(THETA, rope, 50).to(DEV)
+    pos = torch.randint(0, 50, (n,), generator=g, device=DEV, dtype=torch.int32)
+    pos[258] = 50
+    ws = D.dsa_rope_apply(D.rope_desc(x, ov), x, pos, tab, ov)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    for t in (0, 100, 255, 256, 257, 259):
+        hs = torch.tensor([0, 1, h // 2, h - 1], device=DEV)
+        cs = tab.double().cpu().numpy()[int(pos[t])][None]
+        _check_turned(ov[t, hs].double().cpu().numpy(), x[t, hs].double().cpu().numpy(), cs, False, False, 2.0 ** -8)
+    assert torch.all(out[258] == 3.0)
+    assert torch.all(out[..., :offset] == 3.0) and torch.all(out[..., offset + rope:] == 3.0)
+
+
 def _write(kv, slot, fmt, n_pages, pos=None, tab=None, flags=0):
     n_rows = n_pages * P
     if fmt == "bf16":

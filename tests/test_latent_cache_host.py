@@ -144,6 +144,35 @@ def test_rope_in_place_needs_equal_strides():
     assert _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x1000, WS, 256, None)[0] == "DSA_ERR_ARG"
 
 
+@pytest.mark.parametrize("kw", [dict(out_token_stride=64), dict(out_head_stride=65, out_token_stride=128),
+                                dict(n_heads=3), dict(out_head_stride=255, out_token_stride=64)])
+def test_rope_refuses_an_out_whose_heads_overlap(kw):
+    d = _rope(**kw)
+    st, msg = _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x4000, WS, 256, None)
+    assert st == "DSA_ERR_ARG" and "out's heads" in msg
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(out_head_stride=256, out_token_stride=64), dict(n_heads=1, out_head_stride=0),
+                                dict(n_tokens=1, out_token_stride=0), dict(out_token_stride=1 << 62, n_heads=1 << 20)])
+def test_rope_accepts_token_and_head_major_outs(kw):
+    """(refused for the missing workspace, which is looked at after the strides)"""
+    d = _rope(**kw)
+    st, msg = _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x4000, None, 256, None)
+    assert st == "DSA_ERR_ARG" and "workspace" in msg
+
+
+def test_rope_refuses_more_pairs_of_a_token_than_a_launch_turns():
+    d = _rope(n_tokens=1, n_heads=1 << 27, rope_dim=64)
+    assert _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x4000, WS, 256, None)[0] == "DSA_ERR_SHAPE"
+
+
+def test_latent_attention_refuses_a_selection_beyond_int32_tiles():
+    d = _lib.AttnDesc(2, 256, 16, 576, 512, (1 << 30) + 1, 0.04, 0)
+    c, p = _cache(), _lib.PagedCache(0x4000, 0x5000, 2, 2, 128)
+    got = _status(D.lib().dsa_latent_attn_paged, C.byref(d), 0x1000, C.byref(c), 0x6000, C.byref(p), 0x2000, None, WS, 1 << 40, None)
+    assert got[0] == "DSA_ERR_SHAPE"
+
+
 def _cache(**kw):
     a = dict(latent=0x10000, scale=0x20000, rope=0x30000, n_rows=256, format=1)
     a.update(kw)
