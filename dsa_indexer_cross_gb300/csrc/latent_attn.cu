@@ -670,19 +670,21 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
   if (threadIdx.x == 0) publish_faults(a, sh.faults);
 }
 
-// row_nt[t] = number of 64-slot tiles up to the last slot of idx row t holding an index >= 0; one
-// warp per row.
-__global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __restrict__ idx, int n_q, int topk,
+// row_nt[t] = number of 64-slot tiles up to the last slot of idx row t holding an index >= 0; a block
+// a row (2048 slots: one round of loads).
+__global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __restrict__ idx, int topk,
                                                              int32_t* __restrict__ row_nt) {
+  __shared__ int top;
   grid_trigger();
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (t >= n_q) return;
+  const int t = blockIdx.x;
   const int32_t* irow = idx + static_cast<size_t>(t) * topk;
+  if (threadIdx.x == 0) top = -1;
+  __syncthreads();
   int last = -1;
   if ((topk & 3) == 0 && (reinterpret_cast<uintptr_t>(idx) & 15) == 0) {
     const int4* v = reinterpret_cast<const int4*>(irow);
-#pragma unroll 8
-    for (int s = lane; s < topk / 4; s += 32) {
+#pragma unroll 4
+    for (int s = threadIdx.x; s < topk / 4; s += 128) {
       const int4 q = __ldg(v + s);
       if (q.x >= 0) last = 4 * s;
       if (q.y >= 0) last = 4 * s + 1;
@@ -690,114 +692,146 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
       if (q.w >= 0) last = 4 * s + 3;
     }
   } else {
-#pragma unroll 8
-    for (int s = lane; s < topk; s += 32)
+#pragma unroll 4
+    for (int s = threadIdx.x; s < topk; s += 128)
       if (__ldg(irow + s) >= 0) last = s;
   }
   last = __reduce_max_sync(0xffffffffu, last);
-  if (lane == 0) row_nt[t] = (last + kRows) / kRows;
+  if ((threadIdx.x & 31) == 0 && last >= 0) atomicMax(&top, last);
+  __syncthreads();
+  if (threadIdx.x == 0) row_nt[t] = (top + kRows) / kRows;
 }
 
 // Joins the partials of the rows that were split: block (b, y) takes the row that begins in group b's
 // share and goes on in the next ones (by_row: row b, where there are fewer rows than groups), HPB heads,
-// 8 / HPB warps a head; a warp takes every (8 / HPB)-th partial, a lane 16 dims, and the warps' sums meet in shared memory.  With M the largest of the
-// partials' maxima m_s and w_s = 2^(m_s - M): out = sum w_s O_s / sum w_s lr_s,
-// lse = ln 2 (M + log2 sum w_s l_s).  The order of the sums is fixed.  Few rows, each in many partials,
-// take one head a block (eight warps on one row of 100K keys in 76 partials, 128 heads: 17 us, one
-// warp a head 56); many rows, most in two or three, take eight (75 rows: 12 us, two heads a block 19).
+// 8 / HPB warps a head; a warp takes every (8 / HPB)-th partial, a lane 16 dims, and the warps' sums meet
+// in shared memory.  With M the largest of the partials' maxima m_s and w_s = 2^(m_s - M):
+// out = sum w_s O_s / sum w_s lr_s, lse = ln 2 (M + log2 sum w_s l_s).  The order of the sums is fixed.
+// Latency bounds it, so two round trips is all there is: every group's start, then the partials' maxima
+// and sums and the first O rows together.  One block more puts the CTAs' fault words into the status.
+// Few rows, each in many partials, take one head a block (eight warps on one row of 100K keys in 76
+// partials, 128 heads: MEAS_JOIN_A us, one warp a head 56); many rows, most in two or three, take eight
+// (75 rows: MEAS_JOIN_B us, two heads a block 19).
 template <int HPB>
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LArgs a, bool by_row) {
   constexpr int kJoinWarps = 8 / HPB;
+  constexpr int kAhead = 3;                      // O rows in flight per warp
+  constexpr int kLaneGroups = kMostGroups / 32;
   __shared__ float4 sum[HPB][kJoinWarps > 1 ? kJoinWarps - 1 : 1][kJoinWarps > 1 ? kDv / 4 : 1];
-  __shared__ float sl[HPB][kJoinWarps][2];
-  const int lane = threadIdx.x & 31;
-  const int hw = (threadIdx.x >> 5) / kJoinWarps, w = (threadIdx.x >> 5) % kJoinWarps;
+  __shared__ float weight[8][kMostGroups];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hw = warp / kJoinWarps, w = warp % kJoinWarps;
   const int h = blockIdx.y * HPB + hw;
   grid_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+  if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y != 0 || warp != 0) return;
     uint32_t bits = 0, count = 0;
-    for (int i = threadIdx.x; i < a.n_cta; i += 32) {
+#pragma unroll 5
+    for (int i = lane; i < a.n_cta; i += 32) {
       bits |= a.err[2 * i];
       count += a.err[2 * i + 1];
     }
     bits = __reduce_or_sync(0xffffffffu, bits);
     count = __reduce_add_sync(0xffffffffu, count);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       a.status[0] = bits;
       a.status[1] = count;
     }
+    return;
   }
-  const int groups = __ldg(&a.start[a.n_grp].x);
-  int b = blockIdx.x;
-  if (by_row) {                                             // the last group that starts at or before the row
-    int below = 0;
-    for (int c = lane; c < groups; c += 32) below += a.start[c].x < b || (a.start[c].x == b && a.start[c].y == 0);
-    b = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(below))) - 1;
+  int2 st[kLaneGroups];
+#pragma unroll
+  for (int k = 0; k < kLaneGroups; ++k)
+    st[k] = lane + 32 * k < a.n_grp ? a.start[lane + 32 * k] : make_int2(0x7FFFFFFF, 0);
+  int row = blockIdx.x;
+  if (!by_row) {
+    const int2 s0 = a.start[blockIdx.x], s1 = a.start[blockIdx.x + 1];
+    if (s1.x == 0x7FFFFFFF || s1.y == 0 || (s0.x == s1.x && s0.y > 0)) return;   // no row goes on, or it began before
+    row = s1.x;
   }
-  if (b < 0 || b + 1 >= groups) return;
-  const int2 s0 = a.start[b], s1 = a.start[b + 1];
-  if (by_row && s1.x != static_cast<int>(blockIdx.x)) return;
-  if (s1.y == 0 || (s0.x == s1.x && s0.y > 0)) return;      // no row goes on, or it began before
-  const int row = s1.x;
-  int end = b + 2;                                          // groups b .. end - 1 hold the row
-  while (end < groups) {                                    // (32 at a time)
-    const int c = end + lane;
-    const int2 s = c < groups ? a.start[c] : make_int2(-1, 0);
-    const uint32_t on = __ballot_sync(0xffffffffu, s.x == row && s.y > 0);
-    end += on == 0xFFFFFFFFu ? 32 : __ffs(static_cast<int>(~on)) - 1;
-    if (on != 0xFFFFFFFFu) break;
+  // the row's groups: from the last that starts at its first tile or before, to the last that starts in it
+  uint32_t below = 0;
+#pragma unroll
+  for (int k = 0; k < kLaneGroups; ++k) {
+    below += st[k].x < row || (st[k].x == row && st[k].y == 0) ? 1u : 0u;
+    below += st[k].x <= row ? 0x10000u : 0u;
   }
+  below = __reduce_add_sync(0xffffffffu, below);
+  const int b = static_cast<int>(below & 0xFFFFu) - 1, end = static_cast<int>(below >> 16);
+  if (b < 0 || end - b < 2) return;                         // not split
   const size_t n = static_cast<size_t>(a.n_grp) * 2 * a.H;
   auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == b ? 1 : 0)) * a.H + h; };
   const bool live = h < a.H;
-  float M = -INFINITY;
-  if (live) {
-    for (int c = b + lane; c < end; c += 32) M = fmaxf(M, a.part_m[slot(c)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  }
+  float M = -INFINITY, lr = 0.f, ls = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float lr = 0.f, ls = 0.f;
   if (live) {
-#pragma unroll 3
-    for (int c = b + w; c < end; c += kJoinWarps) {
-      const size_t at = slot(c);
-      const float m = __ldg(a.part_m + at), l1 = __ldg(a.part_m + n + at), l2 = __ldg(a.part_m + 2 * n + at);
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + at * kDv) + lane;
-      float4 o[4];
+    float m[kLaneGroups], l1[kLaneGroups], l2[kLaneGroups];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __ldg(src + 32 * k);
-      // a partial without a key weighs nothing; one whose sum is NaN (a NaN score) makes the row NaN
-      // even where its maximum says nothing
-      const float f = m == -INFINITY ? (l1 == l1 ? 0.f : l1) : exp2f(m - M);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[k].x += f * o[k].x;
-        acc[k].y += f * o[k].y;
-        acc[k].z += f * o[k].z;
-        acc[k].w += f * o[k].w;
+    for (int k = 0; k < kLaneGroups; ++k) {
+      const int c = b + lane + 32 * k;
+      m[k] = -INFINITY;
+      l1[k] = l2[k] = 0.f;
+      if (c < end) {
+        m[k] = __ldg(a.part_m + slot(c));
+        l1[k] = __ldg(a.part_m + n + slot(c));
+        l2[k] = __ldg(a.part_m + 2 * n + slot(c));
       }
-      lr += f * l1;
-      ls += f * l2;
+    }
+#pragma unroll 1
+    for (int c0 = b + w; c0 < end; c0 += kAhead * kJoinWarps) {
+      float4 o[kAhead][4];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + u * kJoinWarps;
+        if (c < end) {
+          const float4* src = reinterpret_cast<const float4*>(a.part_o + slot(c) * kDv) + lane;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[u][k] = __ldg(src + 32 * k);
+        }
+      }
+      if (c0 == b + w) {
+        // (while the rows are on their way)  A partial without a key weighs nothing; one whose sum is NaN
+        // (a NaN score) makes the row NaN even where its maximum says nothing.
+#pragma unroll
+        for (int k = 0; k < kLaneGroups; ++k) M = fmaxf(M, m[k]);
+#pragma unroll
+        for (int e = 16; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, e));
+#pragma unroll
+        for (int k = 0; k < kLaneGroups; ++k) {
+          const float f = m[k] == -INFINITY ? (l1[k] == l1[k] ? 0.f : l1[k]) : exp2f(m[k] - M);
+          weight[warp][lane + 32 * k] = f;
+          lr += f * l1[k];
+          ls += f * l2[k];
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int c = c0 + u * kJoinWarps;
+        if (c >= end) break;
+        const float f = weight[warp][c - b];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[k].x += f * o[u][k].x;
+          acc[k].y += f * o[u][k].y;
+          acc[k].z += f * o[u][k].z;
+          acc[k].w += f * o[u][k].w;
+        }
+      }
     }
   }
   if (w > 0) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[hw][w - 1][lane + 32 * k] = acc[k];
   }
-  if (lane == 0) {
-    sl[hw][w][0] = lr;
-    sl[hw][w][1] = ls;
-  }
   __syncthreads();
   if (w > 0 || !live) return;
-  lr = ls = 0.f;
 #pragma unroll
-  for (int v = 0; v < kJoinWarps; ++v) {
-    lr += sl[hw][v][0];
-    ls += sl[hw][v][1];
+  for (int e = 16; e > 0; e >>= 1) {
+    lr += __shfl_xor_sync(0xffffffffu, lr, e);
+    ls += __shfl_xor_sync(0xffffffffu, ls, e);
   }
   const float inv = lr == 0.f ? 0.f : 1.f / lr;
   const size_t orow = static_cast<size_t>(row) * a.H + h;
@@ -831,13 +865,13 @@ Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
   const long long most = (static_cast<long long>(n_q) * row_tiles_max + kMinTiles - 1) / kMinTiles;
   int sms = device_sm_count();
   if (sms <= 0) sms = 152;
-  L.n_grp = static_cast<int>(std::max(1LL, std::min<long long>(sms / L.n_hb, most)));
+  L.n_grp = static_cast<int>(std::max(1LL, std::min<long long>(std::min(sms / L.n_hb, kMostGroups), most)));
   const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t o = up(static_cast<size_t>(n_q) * sizeof(int32_t));           // row_nt (selected keys)
   L.off_err = o;
   o += up(static_cast<size_t>(L.n_grp) * L.n_hb * 2 * sizeof(uint32_t));
   L.off_start = o;
-  o += up((static_cast<size_t>(L.n_grp) + 1) * sizeof(int2));
+  o += up(static_cast<size_t>(L.n_grp) * sizeof(int2));
   L.off_m = o;
   o += up(static_cast<size_t>(L.n_grp) * 2 * n_heads * 3 * sizeof(float));
   L.off_ring = o;
@@ -917,7 +951,7 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   cudaError_t e;
   if (sel) {
     const int ps = prof_begin(kProfAttnPrep, st);
-    selected_tiles_kernel<<<(n_q + 3) / 4, 128, 0, st>>>(idx, n_q, topk, reinterpret_cast<int32_t*>(base));
+    selected_tiles_kernel<<<n_q, 128, 0, st>>>(idx, topk, reinterpret_cast<int32_t*>(base));
     e = cudaGetLastError();
     prof_end(ps, st);
     if (e != cudaSuccess) return e;
@@ -933,7 +967,7 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   if (e == cudaSuccess && a.n_cta > 1) {
     const int hpb = 8LL * n_q <= L.n_grp ? 1 : 8;      // eight partials a row and more, or fewer
     const bool by_row = n_q < L.n_grp;
-    const dim3 grid = L.n_grp > 1 ? dim3(std::min(n_q, L.n_grp - 1), (n_heads + hpb - 1) / hpb) : dim3(1, 1);
+    const dim3 grid(std::min(n_q, L.n_grp - 1) + 1, (n_heads + hpb - 1) / hpb);
     e = launch_pdl(hpb == 1 ? latent_join_kernel<1> : latent_join_kernel<8>, grid, 256, 0, st, true, 1, a, by_row);
   }
   prof_end(ps, st);

@@ -18,6 +18,7 @@ constexpr int kKB = kDqk / 64;         // 64-dim blocks per row
 // about 0.1: 20000 keys, 16 heads, 23 us with shares of 4 or more and 27 with 2, while short rows want
 // them split (1000 keys: 14.6 with 2, 16.6 with 4; 4000 keys, 64 heads, fp8: 20.7 and 22.9).
 constexpr int kMinTiles = 2;
+constexpr int kMostGroups = 160;       // groups of CTAs (the join holds five per lane)
 __device__ __forceinline__ int min_share(long long total) { return total > 128 ? 4 : kMinTiles; }
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -85,7 +86,7 @@ struct LArgs {
   float* lse;
   int n_q, H, topk, n_grp, n_hb;
   float scale_log2;
-  int2* start;                 // [n_grp + 1]: (row, tile) each group starts at; [n_grp].x = groups in use
+  int2* start;                 // [n_grp]: (row, tile) each group starts at; groups without a share: row INT_MAX
   uint16_t* ring;              // fp8, CTA pairs: [n_grp][kRing][64][576] bf16
   float* part_o;               // [n_grp * 2][H][512]
   float* part_m;               // [3][n_grp * 2][H]: max in use (log2), sum of the rounded weights, plain sum
@@ -104,6 +105,13 @@ __device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
   if constexpr (SEL) return __ldg(a.row_nt + row);
   return (row_len(a.pg, row) + kRows - 1) / kRows;
 }
+
+// Splitting rows evenly costs writing and joining partials; a CTA pair per row costs the tiles that the
+// longest row has above the even share.  128 heads, 64 rows of 8 selected tiles over 76 pairs: 54.8 us
+// split, 40.9 whole; of 32 tiles, 87.8 and 78.6; 48 rows of 32 (12 above the share), 76.8 and 75.3; 20 rows
+// of 16 (12 above it), 41.9 and 46.4.  Single CTAs, whose partials are smaller, gain nothing (64 heads, 128
+// rows of 32: 112 and 118).  Extra tiles that are taken:
+__device__ __forceinline__ int whole_row_extra(int groups) { return groups / 9; }
 
 // The segments (consecutive tiles of one row) of this CTA's share, in order.
 struct Seg {
@@ -151,6 +159,7 @@ __device__ __forceinline__ void publish_faults(const LArgs& a, const CtaFaults& 
 // a block-wide barrier inside and one needed behind it before row0 / tile0 are read).
 struct Share {
   long long wsum[32];
+  int wmax[32];
   int row0, tile0;
 };
 template <bool SEL, int THREADS>
@@ -159,10 +168,13 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
   const int per = (a.n_q + THREADS - 1) / THREADS;
   const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
   long long mine = 0;
+  int tallest = 0;
   bool bad_len = false;
 #pragma unroll 1
   for (int r = ra; r < rb; ++r) {
-    mine += row_tiles<SEL>(a, r);
+    const int T = row_tiles<SEL>(a, r);
+    mine += T;
+    tallest = max(tallest, T);
     if (blockIdx.x == 0) {
       const int want = __ldg(a.pg.seq_len + r);
       if (want < 0 || want > (a.pg.max_pages << kPageShift)) bad_len = true;
@@ -175,6 +187,8 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
     if (lane >= o) pre += v;
   }
   if (lane == 31) sh.wsum[warp] = pre;
+  tallest = __reduce_max_sync(0xffffffffu, tallest);
+  if (lane == 0) sh.wmax[warp] = tallest;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -185,24 +199,37 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) pre += sh.wsum[w];
     total += sh.wsum[w];
+    tallest = max(tallest, sh.wmax[w]);
   }
-  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + min_share(total) - 1) / min_share(total)));
-  const long long first = grp < groups ? total * grp / groups : 0;
-  const long long share = grp < groups ? total * (grp + 1) / groups - first : 0;
-  if (share > 0 && pre <= first && first < pre + mine) {
-    long long at = pre;
-    int r = ra;
-    while (true) {
-      const int T = row_tiles<SEL>(a, r);
-      if (first < at + T) break;
-      at += T;
-      ++r;
+  int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + min_share(total) - 1) / min_share(total)));
+  const bool by_row = a.n_hb == 2 && a.n_q <= a.n_grp && tallest <= total / max(groups, 1) + whole_row_extra(groups);
+  if (by_row) groups = a.n_q;
+  long long share = 0;
+  if (by_row) {
+    share = grp < groups ? row_tiles<SEL>(a, grp) : 0;
+    if (threadIdx.x == 0 && grp < groups) {
+      sh.row0 = grp;
+      sh.tile0 = 0;
+      if (writes_start) a.start[grp] = make_int2(grp, 0);
     }
-    sh.row0 = r;
-    sh.tile0 = static_cast<int>(first - at);
-    if (writes_start) a.start[grp] = make_int2(r, static_cast<int>(first - at));
+  } else {
+    const long long first = grp < groups ? total * grp / groups : 0;
+    share = grp < groups ? total * (grp + 1) / groups - first : 0;
+    if (share > 0 && pre <= first && first < pre + mine) {
+      long long at = pre;
+      int r = ra;
+      while (true) {
+        const int T = row_tiles<SEL>(a, r);
+        if (first < at + T) break;
+        at += T;
+        ++r;
+      }
+      sh.row0 = r;
+      sh.tile0 = static_cast<int>(first - at);
+      if (writes_start) a.start[grp] = make_int2(r, static_cast<int>(first - at));
+    }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.start[a.n_grp] = make_int2(groups, 0);
+  if (writes_start && threadIdx.x == 0 && grp >= groups) a.start[grp] = make_int2(0x7FFFFFFF, 0);
   // rows without keys: zeros and -inf
 #pragma unroll 1
   for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
