@@ -67,6 +67,7 @@ struct LShared {
   // the PV warp's look, and a barrier two phases on reads as not yet complete.)
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free, mma_done;
   uint32_t tmem_base, abort_flag, soft_abort;
+  uint32_t keys[2][4];                // SEL, by tile parity and sixteen rows: those that hold a key
   CtaFaults faults;
   Share share;
   alignas(16) float red[4][64];
@@ -290,6 +291,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
                                 a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
             }
             cp_async_mbar_arrive(&sh.full[turn][1]);
+            if constexpr (SEL) {
+              const uint32_t keys = __ballot_sync(0xffffffffu, at >= 0) & 0xFFFFu;
+              if (lane == 0) sh.keys[turn][pw & 3] = keys;
+            }
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -346,26 +351,24 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       named_bar_sync(1, kSoft);
       const int len = row_len(a.pg, sg.row);
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
-      const int32_t* irow = SEL ? a.idx + static_cast<size_t>(sg.row) * a.topk : nullptr;
-      auto in_cache = [&](int j) {
-        if (j < 0 || j >= len) return false;
-        const int page = __ldg(bt + (j >> kPageShift));
-        return page >= 0 && page < a.pg.n_pages;
-      };
       for (int n = 0; n < sg.n; ++n, ++g) {
         const int i = sg.i0 + n;
         const int sb = g & 1;
         bool rv0, rv1;                 // rows r0 / r0 + 8 hold a key
-        if constexpr (SEL) {
-          const int s0 = i * kRows + r0, s1 = s0 + 8;
-          rv0 = s0 < a.topk && in_cache(__ldg(irow + s0));
-          rv1 = s1 < a.topk && in_cache(__ldg(irow + s1));
-        } else {
+        if constexpr (!SEL) {
           const int nv = tile_rows(a, len, i, __ldg(bt + (i >> 1)));
           rv0 = r0 < nv;
           rv1 = r0 + 8 < nv;
         }
         bool ok = wait_bar(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
+        if constexpr (SEL) {
+          // (long complete: S took the tile.  Looking the rows up here once more, two loads one after the other,
+          // held up the tiles: 64 heads, 128 selections of 2048, 112 us where this takes 99.)
+          ok = ok && wait_bar(&sh.full[sb][1], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
+          const uint32_t keys = sh.keys[sb][qd] >> (lane >> 2);
+          rv0 = keys & 1u;
+          rv1 = keys & 0x100u;
+        }
         ok = __all_sync(0xffffffffu, ok);
         float sc[4 * NR];   // [4k + j]: j = 0,1 row r0 columns 8k+cq, +1;  j = 2,3 row r0 + 8
         bool need = false;
