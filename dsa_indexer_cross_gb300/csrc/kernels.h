@@ -222,6 +222,33 @@ cudaError_t launch_sparse_attn_bwd_dense(int hd, const CUtensorMap& tmap_kv, con
                                          void* scratch, cudaStream_t st);
 
 // ---------------------------------------------------------------------------- latent cache
+// A launch that may overlap the end of the previous kernel on the stream (which the kernel waits for
+// itself, grid_wait) when `after` is set; cluster > 1: clusters of that many CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool after, int cluster,
+                       A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2] = {};
+  int n = 0;
+  if (after) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // out[t, h, :rope] = the rotary dims x[t, h, :rope] turned at pos[t] (strides in elements).  One launch
 // turns at most kRopeMostPairs pairs (32-bit thread numbers); a token's fit into one.
 constexpr long long kRopeMostPairs = 0x7FFFFF00LL;

@@ -26,10 +26,6 @@ __device__ __forceinline__ float ex2f(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Programmatic dependent launch: let the next kernel's blocks be scheduled; wait for the previous
-// kernel's memory.
-__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t n, bool p) {
   uint32_t r;
   asm volatile(
@@ -267,33 +263,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 __device__ __forceinline__ int tile_rows(const LArgs& a, int len, int i, int page) {
   if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.pg.n_pages)) return 0;
   return max(0, min(kRows, len - i * kRows));
-}
-
-// A launch that may overlap the end of the previous kernel on the stream (which the kernel waits for
-// itself, grid_wait) when `after` is set; cluster > 1: clusters of that many CTAs.
-template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool after, int cluster,
-                       A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2] = {};
-  int n = 0;
-  if (after) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = cluster;
-    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // The CTA-pair kernel for 65 .. 128 heads (latent_pair.cu).  tmap_s / tmap_v: a bf16 cache in boxes

@@ -69,14 +69,24 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // Small calls have no clearing pass before the kernel, which costs as much as the kernel itself (and 2
 // of 27 us at 8000 tokens of 64 heads): block 0 checks every item and writes the status words, and
 // nothing else touches them.  Larger calls (block 0's checks would outlast the other blocks' copies:
-// 41 us for 32768 tokens written, 16 with the clearing pass) clear them first, and each block reports
-// its own.
+// 41 us for 32768 tokens written, 16 with the clearing pass) are launched behind a kernel that clears
+// them without waiting for it (the same tokens behind a memset: CLEAR_MEAS); only a block that reports
+// waits, and block 0, so that the call does not end before the clearing has.
 constexpr int kSoleMostRope = 16384, kSoleMostWrite = 4096, kSoleMostPages = 4096;
 
 __device__ __forceinline__ void report(uint32_t* status, bool sole, uint32_t bits) {
   if (sole) return;
+  grid_wait();
   atomicOr(status, bits);
   atomicAdd(status + 1, 1u);
+}
+__global__ void clear_status_kernel(uint32_t* status) {
+  grid_trigger();
+  status[threadIdx.x] = 0u;
+}
+cudaError_t clear_status(uint32_t* status, cudaStream_t st) {
+  clear_status_kernel<<<1, 2, 0, st>>>(status);
+  return cudaGetLastError();
 }
 // Block 0 of a call that writes the status words itself: check(i) gives item i's error bits.
 template <typename F>
@@ -125,11 +135,15 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
   using E = Elem<T>;
   constexpr int V = E::VEC;
   constexpr int NP = INTER ? V / 2 : V;          // pairs of one head in this thread
-  if (sole && blockIdx.x == 0)
-    sole_status(status, sole, [&](int t) {
-      const int p = __ldg(pos + t);
-      return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
-    });
+  if (blockIdx.x == 0) {
+    if (sole)
+      sole_status(status, sole, [&](int t) {
+        const int p = __ldg(pos + t);
+        return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
+      });
+    else
+      grid_wait();
+  }
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t nv = static_cast<uint32_t>(rope) / (INTER ? V : 2 * V);
@@ -191,11 +205,15 @@ __global__ void __launch_bounds__(256) rope_apply_pair(const T* x, T* out, const
                                                        long long o_tok, long long o_head, float sgn, uint32_t* status,
                                                        int sole) {
   using E = Elem<T>;
-  if (sole && blockIdx.x == 0)
-    sole_status(status, sole, [&](int t) {
-      const int p = __ldg(pos + t);
-      return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
-    });
+  if (blockIdx.x == 0) {
+    if (sole)
+      sole_status(status, sole, [&](int t) {
+        const int p = __ldg(pos + t);
+        return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
+      });
+    else
+      grid_wait();
+  }
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t half = static_cast<uint32_t>(rope) / 2;
@@ -261,42 +279,54 @@ __device__ __forceinline__ uint4 rope_vec(uint4 v, int lane, bool inter, const f
   }
 }
 
-// One warp per token.  Lane l holds the row's 16-byte vectors l and l + 32 (dims 8l.. and
-// 256 + 8l..): 16 lanes make a scale group, and every load and store instruction covers whole
-// consecutive lines.
+// Eight tokens a block.  Warps 0-7 take one token's latent dims each: lane l holds the row's 16-byte
+// vectors l and l + 32 (dims 8l.. and 256 + 8l..), 16 lanes make a scale group, and every load and store
+// instruction covers whole consecutive lines.  Warps 8-9 take the rotary dims of four tokens each, so the
+// turn's chain of loads (position, table row) holds up no latent dims (WRITE_MEAS).
 template <bool FP8, bool ROT>
-__global__ void __launch_bounds__(256) cache_write_kernel(const uint16_t* __restrict__ kv, long long kv_stride,
+__global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __restrict__ kv, long long kv_stride,
                                                           const int32_t* __restrict__ slot,
                                                           const int32_t* __restrict__ pos,
                                                           const float2* __restrict__ cs, int n_pos, int n_tokens,
                                                           int n_rows, bool inter, uint8_t* __restrict__ latent,
                                                           uint8_t* __restrict__ scale, uint16_t* __restrict__ rope,
                                                           uint32_t* status, int sole) {
-  if (sole && blockIdx.x == 0)
-    sole_status(status, sole, [&](int i) {
-      const int s = __ldg(slot + i), p = ROT ? __ldg(pos + i) : 0;
-      return s >= 0 && (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) ? DEV_ERR_BAD_INDEX : 0u;
-    });
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= n_tokens) return;
-  const uint4* src = reinterpret_cast<const uint4*>(kv + static_cast<long long>(t) * kv_stride);
-  const uint4 a = __ldg(src + lane), b = __ldg(src + 32 + lane);
-  const uint4 r = __ldg(src + 64 + (lane & 7));
-  const int s = __ldg(slot + t);
-  int p = 0;
-  if constexpr (ROT) p = __ldg(pos + t);
-  if (s < 0) return;
-  if (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) {
-    if (lane == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
+  if (blockIdx.x == 0) {
+    if (sole)
+      sole_status(status, sole, [&](int i) {
+        const int s = __ldg(slot + i), p = ROT ? __ldg(pos + i) : 0;
+        return s >= 0 && (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) ? DEV_ERR_BAD_INDEX : 0u;
+      });
+    else
+      grid_wait();
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool turns = warp >= 8;
+  const int t = blockIdx.x * 8 + (turns ? 4 * (warp - 8) + (lane >> 3) : warp);
+  const int tt = min(t, n_tokens - 1);
+  const uint4* src = reinterpret_cast<const uint4*>(kv + static_cast<long long>(tt) * kv_stride);
+  const uint4 a = __ldg(src + (turns ? 64 + (lane & 7) : lane));
+  uint4 b;
+  if (!turns) b = __ldg(src + 32 + lane);
+  const int s = t < n_tokens ? __ldg(slot + tt) : -1;
+  const int p = ROT ? __ldg(pos + tt) : 0;
+  const bool bad = s >= n_rows || (ROT && (p < 0 || p >= n_pos)), stored = s >= 0 && !bad;
+  if (turns) {
+    const uint4 turned = rope_vec<ROT>(a, lane, inter, cs + static_cast<size_t>(stored ? p : 0) * (kRope / 2));
+    if (!stored) return;
+    uint16_t* row = FP8 ? rope + static_cast<size_t>(s) * kRope
+                        : reinterpret_cast<uint16_t*>(latent) + static_cast<size_t>(s) * kRow + kLat;
+    reinterpret_cast<uint4*>(row)[lane & 7] = turned;
     return;
   }
-  const uint4 turned = rope_vec<ROT>(r, lane, inter, cs + static_cast<size_t>(p) * (kRope / 2));
+  if (!stored) {
+    if (s >= 0 && lane == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
+    return;
+  }
   if constexpr (!FP8) {
     uint4* dst = reinterpret_cast<uint4*>(latent) + static_cast<size_t>(s) * (kRow / 8);
     dst[lane] = a;
     dst[32 + lane] = b;
-    if (lane < 8) dst[64 + lane] = turned;
   } else {
     uint32_t sb[2];
     uint2 codes[2];
@@ -325,7 +355,6 @@ __global__ void __launch_bounds__(256) cache_write_kernel(const uint16_t* __rest
     const uint32_t b1 = __shfl_sync(0xffffffffu, sb[0], 16), b3 = __shfl_sync(0xffffffffu, sb[1], 16);
     if (lane == 0)
       *reinterpret_cast<uint32_t*>(scale + static_cast<size_t>(s) * 4) = sb[0] | (b1 << 8) | (sb[1] << 16) | (b3 << 24);
-    if (lane < 8) reinterpret_cast<uint4*>(rope + static_cast<size_t>(s) * kRope)[lane] = turned;
   }
 }
 
@@ -354,7 +383,12 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restri
   };
   int n = 0, page = 0;
   long long o0 = 0;
-  if (sole && blockIdx.x == 0) sole_status(status, sole, [&](int b) { return place(b, n, page, o0); });
+  if (blockIdx.x == 0) {
+    if (sole)
+      sole_status(status, sole, [&](int b) { return place(b, n, page, o0); });
+    else
+      grid_wait();
+  }
   const uint32_t err = place(blockIdx.x / kReadSplit, n, page, o0);
   const int part = blockIdx.x % kReadSplit * kReadRows;
   if (err && part == 0 && threadIdx.x == 0) report(status, sole != 0, err);
@@ -426,7 +460,7 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
   const int most = static_cast<int>(std::max(1LL, std::min<long long>(a.n_tokens, kRopeMostPairs / per)));
   const float sgn = a.inverse ? -1.f : 1.f;
   const int sole = a.n_tokens <= std::min(kSoleMostRope, most) ? a.n_tokens : 0;      // (one launch)
-  cudaError_t e = sole ? cudaSuccess : cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
+  cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
   if (e != cudaSuccess) return e;
   for (int t0 = 0; t0 < a.n_tokens; t0 += most) {
     const int n = std::min(most, a.n_tokens - t0);
@@ -435,13 +469,11 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
     const T* x = static_cast<const T*>(a.x) + t0 * a.x_tok;
     T* out = static_cast<T*>(a.out) + t0 * a.o_tok;
     const float2* c2 = reinterpret_cast<const float2*>(cs);
-    if (vec)
-      rope_apply_vec<T, INTER, U><<<grid, 256, 0, st>>>(x, out, pos + t0, c2, n_pos, items, a.n_heads, groups, a.rope,
-                                                        a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole);
-    else
-      rope_apply_pair<T, INTER><<<grid, 256, 0, st>>>(x, out, pos + t0, c2, n_pos, items, a.n_heads, a.rope, a.x_tok,
-                                                      a.x_head, a.o_tok, a.o_head, sgn, status, sole);
-    e = cudaGetLastError();
+    const bool after = !sole && t0 == 0;       // (the clearing kernel)
+    e = vec ? launch_pdl(rope_apply_vec<T, INTER, U>, dim3(grid), 256, 0, st, after, 1, x, out, pos + t0, c2, n_pos, items,
+                         a.n_heads, groups, a.rope, a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole)
+            : launch_pdl(rope_apply_pair<T, INTER>, dim3(grid), 256, 0, st, after, 1, x, out, pos + t0, c2, n_pos, items,
+                         a.n_heads, a.rope, a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole);
     if (e != cudaSuccess) return e;
     if (n == a.n_tokens) break;      // also keeps t0 + most inside int
   }
@@ -464,15 +496,12 @@ cudaError_t launch_cache_write(const LatentCache& c, const void* kv, long long k
                                uint32_t* status, cudaStream_t st) {
   const unsigned grid = (static_cast<unsigned>(n_tokens) + 7) / 8;
   const int sole = n_tokens <= kSoleMostWrite ? n_tokens : 0;
-  if (!sole) {
-    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
+  if (e != cudaSuccess) return e;
   const auto go = [&](auto kern) {
-    kern<<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(kv), kv_stride, slot, pos,
-                               reinterpret_cast<const float2*>(cs), n_pos, n_tokens, c.n_rows, interleaved, c.latent,
-                               c.scale, c.rope, status, sole);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(grid), 320, 0, st, !sole, 1, static_cast<const uint16_t*>(kv), kv_stride, slot, pos,
+                      reinterpret_cast<const float2*>(cs), n_pos, n_tokens, c.n_rows, interleaved, c.latent, c.scale,
+                      c.rope, status, sole);
   };
   if (c.fp8) return cs ? go(cache_write_kernel<true, true>) : go(cache_write_kernel<true, false>);
   return cs ? go(cache_write_kernel<false, true>) : go(cache_write_kernel<false, false>);
@@ -483,17 +512,10 @@ cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_s
   const unsigned n_pg = static_cast<unsigned>(n_seq) * static_cast<unsigned>(pg.max_pages);   // < 2^29: the ABI's check
   const unsigned grid = n_pg * kReadSplit;
   const int sole = n_pg <= kSoleMostPages ? static_cast<int>(n_pg) : 0;
-  if (!sole) {
-    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(WsHeader), st);
-    if (e != cudaSuccess) return e;
-  }
-  if (c.fp8)
-    cache_read_kernel<true><<<grid, 256, 0, st>>>(c.latent, c.scale, c.rope, pg, row_start, n_out,
-                                                  static_cast<uint16_t*>(out), status, sole);
-  else
-    cache_read_kernel<false><<<grid, 256, 0, st>>>(c.latent, c.scale, c.rope, pg, row_start, n_out,
-                                                   static_cast<uint16_t*>(out), status, sole);
-  return cudaGetLastError();
+  const cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(c.fp8 ? cache_read_kernel<true> : cache_read_kernel<false>, dim3(grid), 256, 0, st, !sole, 1, c.latent,
+                    c.scale, c.rope, pg, row_start, n_out, static_cast<uint16_t*>(out), status, sole);
 }
 
 }  // namespace dsa
