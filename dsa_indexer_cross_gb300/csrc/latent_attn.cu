@@ -26,10 +26,10 @@
 // zeros before the products (an uninitialised page may hold NaN, which a zero weight does not cancel).
 //
 // What bounds it (64 rows of 8K to 131K keys, 4.8M in all; a copy moves 6.78 TB/s here).  bf16 reads
-// 5.6 GB: 803 us at 16 and 32 heads, 860 at 64 (6.9 and 6.5 TB/s): HBM.  fp8 reads 3.1 GB: 749 us at 16
-// heads, 808 at 32, 1022 at 64 (4.1, 3.8, 3.0 TB/s): the way of a tile from codes through registers and
+// 5.6 GB: 803 us at 16 and 32 heads, 860 at 64 (6.9 and 6.5 TB/s): HBM.  fp8 reads 3.1 GB: 743 us at 16
+// heads, 800 at 32, 1019 at 64 (4.2, 3.9, 3.1 TB/s): the way of a tile from codes through registers and
 // shared memory to its products, whose operand reads and the converters' writes share the SM's
-// shared-memory bandwidth.  Selected keys (2048 of each row): 45 us at 16 heads, 70 at 64: the gathers'
+// shared-memory bandwidth.  Selected keys (2048 of each row): 41 us at 16 heads, 63 at 64: the gathers'
 // latency, the partials and their join.
 #include <cuda_bf16.h>
 
@@ -713,8 +713,8 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
 // Latency bounds it, so two round trips is all there is: every group's start, then the partials' maxima
 // and sums and the first O rows together.  One block more puts the CTAs' fault words into the status.
 // Few rows, each in many partials, take one head a block (eight warps on one row of 100K keys in 76
-// partials, 128 heads: MEAS_JOIN_A us, one warp a head 56); many rows, most in two or three, take eight
-// (75 rows: MEAS_JOIN_B us, two heads a block 19).
+// partials, 128 heads: 10 us; 17 with a load of the starts, of the maxima and of the rows behind one
+// another; one warp a head 56); many rows, most in two or three, take eight (48 rows, 16 heads: 7 us, 12).
 template <int HPB>
 __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant__ LArgs a, bool by_row) {
   constexpr int kJoinWarps = 8 / HPB;

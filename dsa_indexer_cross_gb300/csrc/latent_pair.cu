@@ -33,8 +33,8 @@
 // into shared memory).
 //
 // What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1116 us, 1202 TFLOP/s of a measured
-// 1924 and 5.0 TB/s of 6.78: operand reads from shared memory next to the copies' writes.  fp8: 1441 us,
-// 932 TFLOP/s, 2.2 TB/s: the same, and the converters' loads and stores through L1.  (Scoring two tiles
+// 1924 and 5.0 TB/s of 6.78: operand reads from shared memory next to the copies' writes.  fp8: 1447 us,
+// 927 TFLOP/s, 2.2 TB/s: the same, and the converters' loads and stores through L1.  (Scoring two tiles
 // with one N = 128 product: bf16 1653, fp8 2008 us.)
 //
 // The leader (the pair's even CTA) issues every product; the peer's warps signal its barriers.  Every
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     // out) of each.  The first kRing tiles are spread instead, eight rows of four tiles a warp: the first
     // tile is there after one round of loads, not four (four selections of 2048: 30.8 -> 27.3 us).  The
     // loops stay rolled: the roles' code together has to stay in the instruction caches (all 32 rows
-    // unrolled: 4826 us where this takes 1441).
+    // unrolled: 4826 us where this takes 1447).
     const uint32_t slot = warp - C::CONV;
     uint16_t* ring = a.ring + (static_cast<size_t>(grp * kRing) * kRows + 32 * rank) * kDqk;
     const uint32_t quarter = slot & 3, first = slot >> 2;      // spread: these rows of tiles first, first + 2, ...
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           tc_fence_after();
           const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
           // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
-          // too slowly for the tensor core: 1913 us where the loop takes 1441)
+          // too slowly for the tensor core: 1913 us where the loop takes 1447)
 #pragma unroll FP8 ? 1 : kKB
           for (int kb = 0; kb < kKB; ++kb)
             umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),
