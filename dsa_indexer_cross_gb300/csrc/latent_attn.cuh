@@ -14,12 +14,12 @@ constexpr int kRows = 64;              // latent rows per tile
 constexpr int kDqk = 576;
 constexpr int kDv = 512;
 constexpr int kKB = kDqk / 64;         // 64-dim blocks per row
-// A share holds at least this many tiles.  A tile costs a CTA about a microsecond, a partial the join
-// about 0.1: 20000 keys, 16 heads, 23 us with shares of 4 or more and 27 with 2, while short rows want
-// them split (1000 keys: 14.6 with 2, 16.6 with 4; 4000 keys, 64 heads, fp8: 20.7 and 22.9).
+// A share holds at least this many tiles, four where two would leave the rows in more than 64 partials each.
+// One row of 1000, 8000, 12000, 20000 keys, 16 heads: 13.6, 14.8, 16.7, 20.8 us with shares of two or more,
+// 15.6, 16.8, 16.8, 18.8 with four; eight rows of 2500: 16.7 and 18.7; 4000 keys, 64 heads, fp8: 20.9 and 22.9.
 constexpr int kMinTiles = 2;
 constexpr int kMostGroups = 160;       // groups of CTAs (the join holds five per lane)
-__device__ __forceinline__ int min_share(long long total) { return total > 128 ? 4 : kMinTiles; }
+__device__ __forceinline__ int min_share(long long total, int n_q) { return total > 128LL * n_q ? 4 : kMinTiles; }
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -197,7 +197,8 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
     total += sh.wsum[w];
     tallest = max(tallest, sh.wmax[w]);
   }
-  int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + min_share(total) - 1) / min_share(total)));
+  const int least = min_share(total, a.n_q);
+  int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + least - 1) / least));
   const bool by_row = a.n_hb == 2 && a.n_q <= a.n_grp && tallest <= total / max(groups, 1) + whole_row_extra(groups);
   if (by_row) groups = a.n_q;
   long long share = 0;
