@@ -1,6 +1,6 @@
 """GB300-native DSA lightning indexer + causal top-k, IndexShare layer loop and sparse MLA
-attention, and the paged latent cache with the attention that reads it.  The compute runs in libdsa.so (hand-written sm_103a kernels behind a C ABI,
-include/dsa.h); this package is its ctypes binding plus seeded input generators.
+attention, and the paged latent cache with the attention that reads it.  The compute runs in
+libdsa.so (hand-written sm_103a kernels behind a C ABI, include/dsa.h); this package is its ctypes binding plus seeded input generators.
 """
 from ._lib import (AttnDesc, DsaError, IndexCache, IndexerDesc, LayerIO, PagedCache, DSA_IDX_INDEPENDENT_ROWS,
                    DSA_IDX_ROPE_K, DSA_PAGE_ROWS, ProjDesc, dsa_indexer_projections, dsa_indexer_topk_paged,

@@ -208,24 +208,28 @@ def _want(t: torch.Tensor, dtype, numel: int, name: str) -> None:
         raise ValueError(f"{name}: needs at least {numel} elements, has {t.numel()}")
 
 
+# (None in a torch without CUDA, whose calls never get here)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:      # the handle alone: a Stream object costs as much as a small launch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _arg(t: torch.Tensor, dtype, numel: int, name: str) -> int:
     """_want and _ptr in one, for the calls of a few microseconds."""
-    if t.dtype is not dtype or t.numel() < numel:
-        _want(t, dtype, numel, name)
-    if not t.is_cuda or not t.is_contiguous():
-        return _ptr(t)
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() >= numel and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _want(t, dtype, numel, name)
+    return _ptr(t)
 
 
 def _on_current_device(t: torch.Tensor) -> None:
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    if t.get_device() != _device():
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{_device()}")
 
 
 def _u8(types: Sequence[int]):
@@ -564,9 +568,7 @@ def rope_desc(x: torch.Tensor, out: torch.Tensor, flags: int = 0) -> RopeDesc:
                     os_[0], os_[1], flags)
 
 
-def _rope_view(t: torch.Tensor, desc: RopeDesc, token: int, head: int, name: str) -> int:
-    dt = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16
-    shape = (desc.n_tokens, desc.n_heads, desc.rope_dim)
+def _rope_view(t: torch.Tensor, dt, shape: tuple, token: int, head: int, name: str) -> int:
     if t.dtype is not dt or t.shape != shape or not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA {dt} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
@@ -578,13 +580,15 @@ def _rope_view(t: torch.Tensor, desc: RopeDesc, token: int, head: int, name: str
 def dsa_rope_apply(desc: RopeDesc, x, pos, rope_cs, out, ws=None, stream=None) -> torch.Tensor:
     """out = x turned at pos (DSA_ROPE_INVERSE: by the negated angle, the gradient), [tokens, heads,
     rope_dim] views as the descriptor was made for."""
-    px = _rope_view(x, desc, desc.x_token_stride, desc.x_head_stride, "x")
-    po = _rope_view(out, desc, desc.out_token_stride, desc.out_head_stride, "out")
+    n, r = desc.n_tokens, desc.rope_dim
+    dt, shape = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16, (n, desc.n_heads, r)
+    px = _rope_view(x, dt, shape, desc.x_token_stride, desc.x_head_stride, "x")
+    po = _rope_view(out, dt, shape, desc.out_token_stride, desc.out_head_stride, "out")
     _on_current_device(out)
-    n_pos = _rope_rows(rope_cs, desc.rope_dim)
+    n_pos = _rope_rows(rope_cs, r)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=out.device)
-    st = (_lib or lib()).dsa_rope_apply(desc, px, _arg(pos, torch.int32, desc.n_tokens, "pos"), _ptr(rope_cs), n_pos, po,
+    st = (_lib or lib()).dsa_rope_apply(desc, px, _arg(pos, torch.int32, n, "pos"), _ptr(rope_cs), n_pos, po,
                                         _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
     if st:
         _check(st)
