@@ -50,6 +50,25 @@ def test_many_rows_and_uneven_lengths(fmt):
     _dense(lens, 16, fmt, seed=9, check={0, 1, 12, 13, 14, 350, 499, 500, 501, 698, 699})
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens", [[500] * 20 + [510, 0, 450], [64] * 70, [40] * 76, [65] * 77, [1000, 1000, 1001],
+                                  [0, 0, 3000, 2900, 0, 3100] * 6])
+def test_rows_of_nearly_equal_length(lens, fmt):
+    """The pair kernel takes whole rows where the longest is near the even share."""
+    _dense(lens, 100, fmt, seed=len(lens))
+
+
+@pytest.mark.parametrize("n,topk", [(9, 512), (64, 512), (30, 1000), (77, 130)])
+def test_selections_of_equal_size(n, topk):
+    lens = [topk + 300 * (t % 5) for t in range(n)]
+    pc = Paged(lens, "fp8", seed=n)
+    q = randn((n, 128, 576), gen(n))
+    idx = _selection(lens, topk, n)
+    out, lse, ws = attend(pc, q, i32(idx))
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [pc.stored(t)[idx[t]] if t % 7 in (0, 3) else None for t in range(n)])
+
+
 def test_no_keys_at_all():
     pc, q, out, lse = _dense([0, 0, 0], 24, "fp8")
     assert torch.all(out == 0) and torch.all(lse == -float("inf"))

@@ -276,3 +276,135 @@ def test_cache_read_skips_and_flags():
     ln = i32([-3, 100000, 5])
     ws = D.dsa_latent_cache_read(pc.cache, D.paged_cache(pc.bt_d, ln, pc.n_pages), 1, i32([0]), out, ws=ws)
     assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+
+
+def _dirty():
+    """A workspace as an earlier call may have left it."""
+    return torch.full((256,), 0xFF, dtype=torch.uint8, device=DEV)
+
+
+def test_large_rotations_equal_small_ones_and_flag():
+    """Calls whose status words are cleared before the kernel, against calls of a few thousand tokens."""
+    n, g = 40000, gen(91)
+    x = torch.randn((n, 2, 64), generator=g, device=DEV)
+    tab = D.dsa_rope_table(THETA, 64, 3000).to(DEV)
+    pos = torch.randint(0, 3000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    out, ref = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+    ws = _dirty()
+    for bad in (None, 0, n - 1, 17001):
+        p = pos.clone()
+        if bad is not None:
+            p[bad] = 3000
+        D.dsa_rope_apply(D.rope_desc(x, out), x, p, tab, out, ws=ws)
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) == (0 if bad is None else 2)
+    out.fill_(9.0)
+    pos[17001] = -1
+    D.dsa_rope_apply(D.rope_desc(x, out), x, pos, tab, out, ws=ws)
+    for i in range(0, n, 4000):
+        D.dsa_rope_apply(D.rope_desc(x[i:i + 4000], ref[i:i + 4000]), x[i:i + 4000], pos[i:i + 4000], tab, ref[i:i + 4000])
+    assert torch.equal(out, ref) and torch.all(out[17001] == 9.0)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_large_writes_equal_small_ones_and_flag(fmt):
+    n, g = 9001, gen(92)
+    kv = randn((n, 576), g)
+    n_pages = n // P + 3
+    slot = torch.randperm(n_pages * P, generator=g, device=DEV)[:n].to(torch.int32)
+    slot[5], slot[8000], slot[n - 1], slot[7777] = n_pages * P, -1, 1 << 30, -9
+    tab = D.dsa_rope_table(THETA, 64, 500).to(DEV)
+    pos = torch.randint(0, 500, (n,), generator=g, device=DEV, dtype=torch.int32)
+    pos[8000], pos[4000] = 500, -1                     # the first is a token without a slot
+    got, bits = _write(kv, slot, fmt, n_pages, pos, tab, D.DSA_CACHE_ROPE)
+    assert bits == 2
+    ref, _ = _write(kv[:1], slot[:1], fmt, n_pages, pos[:1], tab, D.DSA_CACHE_ROPE)
+    cache = D.latent_cache(*ref)
+    for i in range(0, n, 1000):
+        k = kv[i:i + 1000]
+        D.dsa_latent_cache_write(D.cache_write_desc(k, D.DSA_CACHE_ROPE), k, slot[i:i + 1000], pos[i:i + 1000], tab, cache)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    ws = _dirty()
+    slot[5] = slot[n - 1] = slot[4000] = -1
+    D.dsa_latent_cache_write(D.cache_write_desc(kv, D.DSA_CACHE_ROPE), kv, slot, pos, tab, D.latent_cache(*got), ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_large_reads_flag_and_skip():
+    """More pages than one block checks: two sequences of 2300, of two pages each, share the cache's."""
+    pc = Paged([200, 256], "fp8", seed=93)
+    m = 2300
+    bt, ln = np.repeat(pc.bt[:, :2], m // 2, axis=0), np.repeat([200, 256], m // 2)
+    start = np.concatenate([[0], np.cumsum(ln)[:-1]])
+    out = torch.full((int(ln.sum()), 576), 4.0, dtype=torch.bfloat16, device=DEV)
+    ws = _dirty()
+    bt_d, ln_d = i32(bt), i32(ln)
+    D.dsa_latent_cache_read(pc.cache, D.paged_cache(bt_d, ln_d, pc.n_pages), m, i32(start), out, ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    a, b = (torch.as_tensor(pc.stored(t), device=DEV).to(torch.bfloat16) for t in (0, 1))
+    want = torch.cat([a.repeat(m // 2, 1), b.repeat(m // 2, 1)])
+    assert torch.equal(out, want)
+    bt[m - 1, 1] = pc.n_pages
+    out.fill_(4.0)
+    bt_d = i32(bt)
+    D.dsa_latent_cache_read(pc.cache, D.paged_cache(bt_d, ln_d, pc.n_pages), m, i32(start), out, ws=ws)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    want[-128:] = 4.0
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n", [50, 9000])
+def test_captured_cache_calls_follow_new_data(n):
+    """Rotate, write and read back in a CUDA graph, small and large (with a clearing kernel), replayed on new
+    positions, slots and lengths."""
+    g = gen(94)
+    src = randn((n, 576), g)
+    kv = torch.zeros_like(src)
+    n_pages = (n + P - 1) // P
+    cols = 45
+    n_seq = n_pages * (100 if n > 4096 else 1)          # many rows of the same few sequences, mostly empty
+    rows = torch.zeros((n_pages * P, 576), dtype=torch.bfloat16, device=DEV)
+    back = torch.zeros((n_pages * P, 576), dtype=torch.bfloat16, device=DEV)
+    tab = D.dsa_rope_table(THETA, 64, 100).to(DEV)
+    pos = torch.zeros(n, dtype=torch.int32, device=DEV)
+    slot = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    bt = torch.zeros((n_seq, cols), dtype=torch.int32, device=DEV)
+    bt[:n_pages, 0] = torch.arange(n_pages, device=DEV)
+    ln = torch.zeros(n_seq, dtype=torch.int32, device=DEV)
+    start = torch.zeros(n_seq, dtype=torch.int32, device=DEV)
+    start[:n_pages] = torch.arange(n_pages, device=DEV) * P
+    cache, pages = D.latent_cache(rows), D.paged_cache(bt, ln, n_pages)
+    ws = [torch.zeros(256, dtype=torch.uint8, device=DEV) for _ in range(3)]
+    xv, ov = src[:, None, 512:], kv[:, None, 512:]
+
+    def step():
+        D.dsa_rope_apply(D.rope_desc(xv, ov), xv, pos, tab, ov, ws=ws[0])
+        D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, slot, None, None, cache, ws=ws[1])
+        D.dsa_latent_cache_read(cache, pages, n_seq, start, back, ws=ws[2])
+    kv[:, :512] = src[:, :512]
+    step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    torch.cuda.synchronize()
+    for it in range(3):
+        pos.copy_(torch.randint(0, 100, (n,), generator=g, device=DEV))
+        if it == 1:
+            pos[n - 1] = 100
+        slot.copy_(torch.randperm(n_pages * P, generator=g, device=DEV)[:n])
+        ln[:n_pages] = P
+        back.zero_()
+        graph.replay()
+        bits = [D.dsa_workspace_status(w, raise_on_fault=False) for w in ws]
+        assert bits == [2 if it == 1 else 0, 0, 0]
+        assert torch.equal(back, rows)
+        assert torch.equal(rows[slot.long()], kv)
+        ref = torch.zeros_like(kv)
+        m = n - 1 if it == 1 else n
+        for i in range(0, m, 1000):
+            j = min(m, i + 1000)
+            D.dsa_rope_apply(D.rope_desc(xv[i:j], ref[i:j, None, 512:]), xv[i:j], pos[i:j], tab, ref[i:j, None, 512:])
+        assert torch.equal(kv[:m, 512:], ref[:m, 512:])
