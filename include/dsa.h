@@ -487,7 +487,7 @@ typedef struct dsa_cache_write_desc {
  * rotary dims are turned in fp32 and rounded once, as dsa_rope_apply does; pos and rope_cs (rope_dim
  * 64) are then needed, else NULL.  A slot >= n_rows or a position outside the table stores nothing and
  * is flagged (DSA_ERR_DEVICE).  ws: at least 256 bytes.
- *   kv bf16, 16-byte aligned; slot int32 [n_tokens]; pos int32 [n_tokens].
+ *   kv bf16, 16-byte aligned, no part of the cache; slot int32 [n_tokens]; pos int32 [n_tokens].
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows not whole pages), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
 dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* desc, const void* kv, const int32_t* slot,
                                   const int32_t* pos, const float* rope_cs, int32_t rope_n_pos,
@@ -513,10 +513,12 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
  *   idx given: the selected keys, as dsa_sparse_attn_paged, which serves a bf16 cache.
  * o[t, h] = sum_j softmax_j(tau q[t, h] . kv_j) kv_j[:512] and its natural log-sum-exp, over the stored
  * values; softmax weights are rounded to bf16 for the second product and divided by their own sum,
- * lse sums the unrounded ones.  A row without keys gives o = 0 and lse = -inf.  Rows of a page past
- * the sequence's end are never used, whatever they hold.  A page outside the cache, or (idx) an
- * offset >= seq_len[t], is skipped and flagged; a length outside [0, max_pages * page_rows] is cut to
- * it and flagged (DSA_ERR_DEVICE).  Results do not depend on the order in which CTAs run.
+ * lse sums the unrounded ones (selected keys of a bf16 cache: the results are dsa_sparse_attn_paged's,
+ * whose lse sums the rounded weights, within 2^-8 of it).  A row without keys gives o = 0 and
+ * lse = -inf.  Rows of a page past the sequence's end are never used, whatever they hold.  A page
+ * outside the cache, or (idx) an offset >= seq_len[t], is skipped and flagged; a length outside
+ * [0, max_pages * page_rows] is cut to it and flagged (DSA_ERR_DEVICE).  A key listed twice counts
+ * twice.  Results do not depend on the order in which CTAs run.
  *   q bf16 [n_q][n_heads][576], out bf16 [n_q][n_heads][512], 16-byte aligned; lse f32 [n_q][n_heads]
  *   or NULL; block_table and seq_len hold n_q rows; desc->n_kv == cache->n_rows.
  * ws: dsa_latent_attn_workspace_size(desc) bytes.  Errors: those of dsa_sparse_attn_paged, DSA_ERR_ARG
