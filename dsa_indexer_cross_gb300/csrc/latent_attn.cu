@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     tmem_alloc(&sh.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
-  if constexpr (SEL) grid_wait();        // the tile counts of the selections
   grid_trigger();
+  grid_wait();
   const long long share = find_share<SEL, C::THREADS>(a, grp, hb == 0, sh.share, sh.faults);
   __syncthreads();
   const uint32_t tmem = sh.tmem_base;
@@ -679,6 +679,7 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
                                                              int32_t* __restrict__ row_nt) {
   __shared__ int top;
   grid_trigger();
+  grid_wait();
   const int t = blockIdx.x;
   const int32_t* irow = idx + static_cast<size_t>(t) * topk;
   if (threadIdx.x == 0) top = -1;
@@ -725,6 +726,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hw = warp / kJoinWarps, w = warp % kJoinWarps;
   const int h = blockIdx.y * HPB + hw;
+  grid_trigger();
   grid_wait();
   if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y != 0 || warp != 0) return;
@@ -891,7 +893,7 @@ cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tv, const CUtens
   using C = LCfg<HB, FP8>;
   cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, SEL>>(C::DYN_SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, SEL, 1, tkv, tv, tq, a);
+  return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, 1, tkv, tv, tq, a);
 }
 template <int HB>
 cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq,
@@ -954,8 +956,7 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   cudaError_t e;
   if (sel) {
     const int ps = prof_begin(kProfAttnPrep, st);
-    selected_tiles_kernel<<<n_q, 128, 0, st>>>(idx, topk, reinterpret_cast<int32_t*>(base));
-    e = cudaGetLastError();
+    e = launch_pdl(selected_tiles_kernel, dim3(n_q), 128, 0, st, 1, idx, topk, reinterpret_cast<int32_t*>(base));
     prof_end(ps, st);
     if (e != cudaSuccess) return e;
   }
@@ -971,7 +972,7 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
     const int hpb = 8LL * n_q <= L.n_grp ? 1 : 8;      // eight partials a row and more, or fewer
     const bool by_row = n_q < L.n_grp;
     const dim3 grid(std::min(n_q, L.n_grp - 1) + 1, (n_heads + hpb - 1) / hpb);
-    e = launch_pdl(hpb == 1 ? latent_join_kernel<1> : latent_join_kernel<8>, grid, 256, 0, st, true, 1, a, by_row);
+    e = launch_pdl(hpb == 1 ? latent_join_kernel<1> : latent_join_kernel<8>, grid, 256, 0, st, 1, a, by_row);
   }
   prof_end(ps, st);
   return e;

@@ -70,24 +70,22 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // of 27 us at 8000 tokens of 64 heads): block 0 checks every item and writes the status words, and
 // nothing else touches them.  Larger calls (block 0's checks would outlast the other blocks' copies:
 // 41 us for 32768 tokens written, 16 with the clearing pass) are launched behind a kernel that clears
-// them without waiting for it, about 2 us less than behind a memset; only a block that reports waits, and
-// block 0, so that the call does not end before the clearing has.  (Always clearing costs small calls a
-// launch: one head of 2048 tokens 6.7 -> 8.6 us.)
+// them, about 2 us less than a memset.  (Always clearing costs small calls a launch: one head of 2048
+// tokens 6.7 -> 8.6 us.)
 constexpr int kSoleMostRope = 16384, kSoleMostWrite = 4096, kSoleMostPages = 4096;
 
 __device__ __forceinline__ void report(uint32_t* status, bool sole, uint32_t bits) {
   if (sole) return;
-  grid_wait();
   atomicOr(status, bits);
   atomicAdd(status + 1, 1u);
 }
 __global__ void clear_status_kernel(uint32_t* status) {
   grid_trigger();
+  grid_wait();
   status[threadIdx.x] = 0u;
 }
 cudaError_t clear_status(uint32_t* status, cudaStream_t st) {
-  clear_status_kernel<<<1, 2, 0, st>>>(status);
-  return cudaGetLastError();
+  return launch_pdl(clear_status_kernel, dim3(1), 2, 0, st, 1, status);
 }
 // Block 0 of a call that writes the status words itself: check(i) gives item i's error bits.
 template <typename F>
@@ -136,15 +134,13 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
   using E = Elem<T>;
   constexpr int V = E::VEC;
   constexpr int NP = INTER ? V / 2 : V;          // pairs of one head in this thread
-  if (blockIdx.x == 0) {
-    if (sole)
-      sole_status(status, sole, [&](int t) {
-        const int p = __ldg(pos + t);
-        return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
-      });
-    else
-      grid_wait();
-  }
+  grid_trigger();
+  grid_wait();
+  if (sole && blockIdx.x == 0)
+    sole_status(status, sole, [&](int t) {
+      const int p = __ldg(pos + t);
+      return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
+    });
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t nv = static_cast<uint32_t>(rope) / (INTER ? V : 2 * V);
@@ -206,15 +202,13 @@ __global__ void __launch_bounds__(256) rope_apply_pair(const T* x, T* out, const
                                                        long long o_tok, long long o_head, float sgn, uint32_t* status,
                                                        int sole) {
   using E = Elem<T>;
-  if (blockIdx.x == 0) {
-    if (sole)
-      sole_status(status, sole, [&](int t) {
-        const int p = __ldg(pos + t);
-        return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
-      });
-    else
-      grid_wait();
-  }
+  grid_trigger();
+  grid_wait();
+  if (sole && blockIdx.x == 0)
+    sole_status(status, sole, [&](int t) {
+      const int p = __ldg(pos + t);
+      return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
+    });
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t half = static_cast<uint32_t>(rope) / 2;
@@ -298,15 +292,13 @@ __global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __rest
                                                           int n_rows, bool inter, uint8_t* __restrict__ latent,
                                                           uint8_t* __restrict__ scale, uint16_t* __restrict__ rope,
                                                           uint32_t* status, int sole) {
-  if (blockIdx.x == 0) {
-    if (sole)
-      sole_status(status, sole, [&](int i) {
-        const int s = __ldg(slot + i), p = ROT ? __ldg(pos + i) : 0;
-        return s >= 0 && (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) ? DEV_ERR_BAD_INDEX : 0u;
-      });
-    else
-      grid_wait();
-  }
+  grid_trigger();
+  grid_wait();
+  if (sole && blockIdx.x == 0)
+    sole_status(status, sole, [&](int i) {
+      const int s = __ldg(slot + i), p = ROT ? __ldg(pos + i) : 0;
+      return s >= 0 && (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) ? DEV_ERR_BAD_INDEX : 0u;
+    });
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool turns = warp >= 8;
   const int t = blockIdx.x * 8 + (turns ? 4 * (warp - 8) + (lane >> 3) : warp);
@@ -393,12 +385,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restri
   };
   int n = 0, page = 0;
   long long o0 = 0;
-  if (blockIdx.x == 0) {
-    if (sole)
-      sole_status(status, sole, [&](int b) { return place(b, n, page, o0); });
-    else
-      grid_wait();
-  }
+  grid_trigger();
+  grid_wait();
+  if (sole && blockIdx.x == 0) sole_status(status, sole, [&](int b) { return place(b, n, page, o0); });
   const uint32_t err = place(blockIdx.x / kReadSplit, n, page, o0);
   const int part = blockIdx.x % kReadSplit * kReadRows;
   if (err && part == 0 && threadIdx.x == 0) report(status, sole != 0, err);
@@ -479,10 +468,9 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
     const T* x = static_cast<const T*>(a.x) + t0 * a.x_tok;
     T* out = static_cast<T*>(a.out) + t0 * a.o_tok;
     const float2* c2 = reinterpret_cast<const float2*>(cs);
-    const bool after = !sole && t0 == 0;       // (the clearing kernel)
-    e = vec ? launch_pdl(rope_apply_vec<T, INTER, U>, dim3(grid), 256, 0, st, after, 1, x, out, pos + t0, c2, n_pos, items,
+    e = vec ? launch_pdl(rope_apply_vec<T, INTER, U>, dim3(grid), 256, 0, st, 1, x, out, pos + t0, c2, n_pos, items,
                          a.n_heads, groups, a.rope, a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole)
-            : launch_pdl(rope_apply_pair<T, INTER>, dim3(grid), 256, 0, st, after, 1, x, out, pos + t0, c2, n_pos, items,
+            : launch_pdl(rope_apply_pair<T, INTER>, dim3(grid), 256, 0, st, 1, x, out, pos + t0, c2, n_pos, items,
                          a.n_heads, a.rope, a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole);
     if (e != cudaSuccess) return e;
     if (n == a.n_tokens) break;      // also keeps t0 + most inside int
@@ -509,7 +497,7 @@ cudaError_t launch_cache_write(const LatentCache& c, const void* kv, long long k
   const cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
   if (e != cudaSuccess) return e;
   const auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(grid), 320, 0, st, !sole, 1, static_cast<const uint16_t*>(kv), kv_stride, slot, pos,
+    return launch_pdl(kern, dim3(grid), 320, 0, st, 1, static_cast<const uint16_t*>(kv), kv_stride, slot, pos,
                       reinterpret_cast<const float2*>(cs), n_pos, n_tokens, c.n_rows, interleaved, c.latent, c.scale,
                       c.rope, status, sole);
   };
@@ -524,7 +512,7 @@ cudaError_t launch_cache_read(const LatentCache& c, const PagedRows& pg, int n_s
   const int sole = n_pg <= kSoleMostPages ? static_cast<int>(n_pg) : 0;
   const cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(c.fp8 ? cache_read_kernel<true> : cache_read_kernel<false>, dim3(grid), 256, 0, st, !sole, 1, c.latent,
+  return launch_pdl(c.fp8 ? cache_read_kernel<true> : cache_read_kernel<false>, dim3(grid), 256, 0, st, 1, c.latent,
                     c.scale, c.rope, pg, row_start, n_out, static_cast<uint16_t*>(out), status, sole);
 }
 

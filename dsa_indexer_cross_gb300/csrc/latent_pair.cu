@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     tmem_alloc_pair(&sh.tmem_base, kTmemCols);
     tmem_relinquish_pair();
   }
-  if constexpr (SEL) grid_wait();        // the tile counts of the selections
   grid_trigger();
+  grid_wait();
   const long long share = find_share<SEL, C::THREADS>(a, grp, rank == 0, sh.share, sh.faults);
   __syncthreads();
   tc_fence_before();
@@ -644,7 +644,7 @@ template <bool FP8, bool SEL>
 cudaError_t launch_t(const CUtensorMap& ts, const CUtensorMap& tv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
   cudaError_t e = smem_attr_once<latent_pair_kernel<FP8, SEL>>(kDynSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_pair_kernel<FP8, SEL>, dim3(a.n_cta), PCfg<FP8>::THREADS, kDynSmem, st, SEL, 2, ts, tv, tq, a);
+  return launch_pdl(latent_pair_kernel<FP8, SEL>, dim3(a.n_cta), PCfg<FP8>::THREADS, kDynSmem, st, 2, ts, tv, tq, a);
 }
 
 }  // namespace

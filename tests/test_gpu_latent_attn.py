@@ -427,6 +427,95 @@ def test_a_decode_step_through_every_operator():
     assert np.array_equal(back.double().cpu().numpy(), np.concatenate(kv))
 
 
+@pytest.mark.parametrize("H,fmt,sel", [(16, "bf16", False), (16, "fp8", True), (64, "fp8", False), (128, "bf16", False),
+                                       (128, "fp8", False), (128, "fp8", True)])
+def test_calls_in_a_row_see_what_the_one_before_wrote(H, fmt, sel):
+    """Attention right behind the writing of its rows, queries, lengths and selection, without a
+    synchronisation, gives what it gives alone; so does a torch operation right behind it."""
+    lens, g = [130, 700, 64, 1500, 1], gen(97)
+    pc = Paged(lens, fmt, seed=98)
+    slot = torch.cat([p.to(torch.int32) for p in pc.phys])
+    n, turns = slot.numel(), 12
+    kvs, qs = [randn((n, 576), g) for _ in range(turns)], [randn((5, H, 576), g) for _ in range(turns)]
+    ids = [i32(_selection(lens, 200, it)) for it in range(turns)]
+    kv, q, idx = torch.zeros_like(kvs[0]), torch.zeros_like(qs[0]), torch.zeros_like(ids[0])
+    ln = pc.len_d.clone()
+    desc = D.attn_desc(5, pc.n_pages * P, H, 200 if sel else 0, TAU)
+    ws, w1 = torch.empty(D.dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=DEV), torch.zeros(256, dtype=torch.uint8, device=DEV)
+    out, lse = torch.zeros((5, H, 512), dtype=torch.bfloat16, device=DEV), torch.zeros((5, H), device=DEV)
+
+    def run(it, wait):
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        kv.copy_(kvs[it])
+        sync()
+        D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, slot, None, None, pc.cache, ws=w1)
+        sync()
+        q.copy_(qs[it])
+        idx.copy_(ids[it])
+        pc.len_d.copy_(ln - (it % 3) * (ln > 2))
+        sync()
+        D.dsa_latent_attn_paged(desc, q, pc.cache, idx if sel else None, pc.pages, out, lse, ws=ws)
+        sync()
+        return out.clone(), lse.clone()
+    want = [run(it, True) for it in range(turns)]
+    for _ in range(4):
+        for (o, l), (a, b) in zip(want, [run(it, False) for it in range(turns)]):
+            assert torch.equal(o, a) and torch.equal(l, b)
+
+
+@pytest.mark.parametrize("H,fmt,sel", [(16, "bf16", False), (64, "fp8", True), (128, "fp8", False)])
+def test_captured_with_copies_and_a_second_stream(H, fmt, sel):
+    """A graph of memory copies, the operators and two branches: writing and attention on one stream, the
+    rotation of another tensor on a second one, joined by events."""
+    lens, g = [130, 700, 64, 1500, 1], gen(99)
+    pc = Paged(lens, fmt, seed=100)
+    slot = torch.cat([p.to(torch.int32) for p in pc.phys])
+    n = slot.numel()
+    kv_in, q_in = torch.zeros((n, 576), dtype=torch.bfloat16, device=DEV), torch.zeros((5, H, 576), dtype=torch.bfloat16, device=DEV)
+    kv, q = torch.zeros_like(kv_in), torch.zeros_like(q_in)
+    idx = i32(_selection(lens, 200, 6)) if sel else None
+    desc = D.attn_desc(5, pc.n_pages * P, H, 200 if sel else 0, TAU)
+    ws, w1, w2 = (torch.zeros(k, dtype=torch.uint8, device=DEV) for k in (D.dsa_latent_attn_workspace_size(desc), 256, 256))
+    out, lse = torch.zeros((5, H, 512), dtype=torch.bfloat16, device=DEV), torch.zeros((5, H), device=DEV)
+    got, turned = torch.zeros_like(out), torch.zeros((5, H, 64), dtype=torch.bfloat16, device=DEV)
+    tab, pos = D.dsa_rope_table(1e4, 64, 100).to(DEV), i32([0, 7, 99, 31, 5])
+    qv = q[..., 512:]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(sync):
+        kv.copy_(kv_in)
+        q.copy_(q_in)
+        sync()
+        e = torch.cuda.Event()
+        e.record()
+        with torch.cuda.stream(s2):
+            s2.wait_event(e)
+            D.dsa_rope_apply(D.rope_desc(qv, turned), qv, pos, tab, turned, ws=w2)
+            done = torch.cuda.Event()
+            done.record()
+        D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, slot, None, None, pc.cache, ws=w1)
+        sync()
+        D.dsa_latent_attn_paged(desc, q, pc.cache, idx, pc.pages, out, lse, ws=ws)
+        sync()
+        torch.cuda.current_stream().wait_event(done)
+        got.copy_(out)
+    with torch.cuda.stream(s1):
+        step(torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s1):
+            step(lambda: None)
+        for it in range(6):
+            kv_in.copy_(randn((n, 576), g))
+            q_in.copy_(randn((5, H, 576), g))
+            graph.replay()
+            a = got.clone(), lse.clone(), turned.clone()
+            step(torch.cuda.synchronize)
+            torch.cuda.synchronize()
+            assert torch.equal(a[0], got) and torch.equal(a[1], lse) and torch.equal(a[2], turned)
+    assert D.dsa_workspace_status(ws) == 0
+
+
 def test_random_shapes_one_after_another():
     """Calls of ever new shapes, each kernel's code cold now and then: no wait runs out, whatever the order
     in which the warps get going."""

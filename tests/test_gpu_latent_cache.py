@@ -408,3 +408,39 @@ def test_captured_cache_calls_follow_new_data(n):
             j = min(m, i + 1000)
             D.dsa_rope_apply(D.rope_desc(xv[i:j], ref[i:j, None, 512:]), xv[i:j], pos[i:j], tab, ref[i:j, None, 512:])
         assert torch.equal(kv[:m, 512:], ref[:m, 512:])
+
+
+@pytest.mark.parametrize("n", [1, 200, 4000, 20000])
+def test_calls_in_a_row_see_what_the_one_before_wrote(n):
+    """No call starts on its data before the call (or the torch operation) ahead of it on the stream has
+    ended, although its blocks may be scheduled earlier: torch copies, rotates, writes, reads back and turns
+    back, many times over the same buffers without a synchronisation."""
+    g, turns = gen(95), 40
+    src = randn((turns, n, 576), g) if n < 10000 else None
+    n_pages = (n + P - 1) // P
+    tab = D.dsa_rope_table(THETA, 64, 64).to(DEV)
+    pos = torch.randint(0, 64, (n,), generator=g, device=DEV, dtype=torch.int32)
+    rows = torch.zeros((n_pages * P, 576), dtype=torch.bfloat16, device=DEV)
+    kv, back = torch.zeros((n, 576), dtype=torch.bfloat16, device=DEV), torch.zeros((n, 576), dtype=torch.bfloat16, device=DEV)
+    slot = i32(np.random.default_rng(1).permutation(n_pages)[np.arange(n) // P] * P + np.arange(n) % P)
+    bt = (slot[::P] // P)[None].contiguous()
+    cache, pages = D.latent_cache(rows), D.paged_cache(bt, i32([n]), n_pages)
+    ln, start = i32([n]), i32([0])
+    pages = D.paged_cache(bt, ln, n_pages)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    kr, br = kv[:, None, 512:], back[:, None, 512:]
+    want, sums = [], []
+    for it in range(turns):
+        x = src[it] if src is not None else randn((n, 576), g)
+        want.append(x.float().abs().sum(dim=1)[:: max(1, n // 100)])
+        kv.copy_(x)
+        D.dsa_rope_apply(D.rope_desc(kr, kr), kr, pos, tab, kr, ws=ws)
+        D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, slot, None, None, cache, ws=ws)
+        D.dsa_latent_cache_read(cache, pages, 1, start, back, ws=ws)
+        D.dsa_rope_apply(D.rope_desc(br, br, D.DSA_ROPE_INVERSE), br, pos, tab, br, ws=ws)
+        sums.append(back.float().abs().sum(dim=1)[:: max(1, n // 100)])
+    assert D.dsa_workspace_status(ws) == 0
+    for a, b in zip(want, sums):
+        # the 64 rotary dims are rounded twice, by at most 2^-8 of a pair's length each (1.5 of the value's
+        # sum over a pair at most); sums of 576 terms in fp32
+        assert torch.all((a - b).abs() <= a * (2 * 2.0 ** -8 * 1.5 + 576 * 2.0 ** -23))
