@@ -1,6 +1,6 @@
 // Rotary positions of strided heads, and the paged latent cache's writing and reading back.
 // All three move data once and compute next to nothing: HBM bandwidth bounds them at size, a
-// launch's latency when small (64 tokens written 2.1 us in a graph, 64 tokens of 128 heads turned 2.1).
+// launch's latency when small (64 tokens written 1.7 us in a graph, 64 tokens of 128 heads turned 2.0).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -123,8 +123,8 @@ __device__ __forceinline__ void sole_status(uint32_t* status, int n, F check) {
 // A thread turns one 16-byte vector (interleaved: its own pairs) or one vector of each half
 // (half layout) of up to U heads of one token, so the token's (cos, sin) are loaded once for U
 // heads and U independent loads are in flight.  Neighbouring threads take neighbouring
-// vectors, then neighbouring heads.  The input is read once (ld.cs: 22.6 us against 24.6 at 8000
-// tokens of 64 heads, 133 MB); U = 2 and 8 and smaller blocks measured the same.
+// vectors, then neighbouring heads.  The input is read once (ld.cs: 2 of 26 us at 8000 tokens
+// of 64 heads, 133 MB, which take 23.5 in a graph: 5.7 TB/s); U = 2 and 8 and smaller blocks measured the same.
 template <typename T, bool INTER, int U>
 __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const int32_t* __restrict__ pos,
                                                       const float2* __restrict__ cs, int n_pos, uint32_t n_items,
@@ -282,8 +282,8 @@ __device__ __forceinline__ uint32_t abs_max(const uint4& v) {
 // vectors l and l + 32 (dims 8l.. and 256 + 8l..), 16 lanes make a scale group, and every load and store
 // instruction covers whole consecutive lines.  Warps 8-9 take the rotary dims of four tokens each, so the
 // turn's chain of loads (position, table row) holds up no latent dims, and is not done four times over: 60000
-// tokens to fp8, 124 MB, 24 us (5.1 TB/s of a copy's 6.8), where one warp a token took 31, and two or four
-// tokens a warp 37 and 46; 32768 tokens 14.4 us.
+// tokens to fp8, 124 MB, 24 us, where one warp a token took 31, and two or four tokens a warp 37 and 46;
+// 32768 tokens, 67 MB, 11.5 us in a graph (5.9 TB/s of a copy's 6.8).
 template <bool FP8, bool ROT>
 __global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __restrict__ kv, long long kv_stride,
                                                           const int32_t* __restrict__ slot,
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __rest
 // ---------------------------------------------------------------------------- reading rows back
 // One block per kReadRows rows of a (sequence, page): its valid rows go to out rows row_start[t] + j.
 // A warp takes four rows, all their loads before the first store.  1.08 M rows of fp8, 1.9 GB moved:
-// 289 us, 6.7 TB/s, what a copy reaches.
+// 286 us, 6.8 TB/s, what a copy reaches.
 constexpr int kReadRows = 32;
 constexpr int kReadSplit = kPageRows / kReadRows;
 template <bool FP8>
