@@ -26,8 +26,8 @@
 // zeros before the products (an uninitialised page may hold NaN, which a zero weight does not cancel).
 //
 // What bounds it (64 rows of 8K to 131K keys, 4.8M in all; a copy moves 6.78 TB/s here).  bf16 reads
-// 5.6 GB: 803 us at 16 and 32 heads, 860 at 64 (6.9 and 6.5 TB/s): HBM.  fp8 reads 3.1 GB: 743 us at 16
-// heads, 800 at 32, 1019 at 64 (4.2, 3.9, 3.1 TB/s): the way of a tile from codes through registers and
+// 5.6 GB: 803 us at 16 and 32 heads, 860 at 64 (6.9 and 6.5 TB/s): HBM.  fp8 reads 3.1 GB: 727 us at 16
+// heads, 800 at 32, 1036 at 64 (4.3, 3.9, 3.0 TB/s): the way of a tile from codes through registers and
 // shared memory to its products, whose operand reads and the converters' writes share the SM's
 // shared-memory bandwidth.  Selected keys (2048 of each row): 41 us at 16 heads, 63 at 64: the gathers'
 // latency, the partials and their join.
@@ -131,7 +131,9 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
   grid_trigger();
   grid_wait();
   const long long share = find_share<SEL, C::THREADS>(a, grp, hb == 0, sh.share, sh.faults);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   Walk<SEL> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
@@ -516,7 +518,9 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       named_bar_sync(1, kSoft);
       stop = sh.soft_abort != 0;
       if (tid < HB) {
-        sh.l_run[tid] = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
+        const float l = (sh.red[0][tid] + sh.red[1][tid]) + (sh.red[2][tid] + sh.red[3][tid]);
+        sh.l_run[tid] = l;
+        sh.alpha[tid] = l == 0.f ? 0.f : 1.f / l;   // a NaN sum stays NaN; a sum of zero (no key) gives zeros
         sh.l_sum[tid] = (sh.red2[0][tid] + sh.red2[1][tid]) + (sh.red2[2][tid] + sh.red2[3][tid]);
       }
       named_bar_sync(1, kSoft);
@@ -535,16 +539,14 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           if (sg.whole) {
             uint16_t* orow = a.out + (static_cast<size_t>(sg.row) * a.H + hb * HB) * kDv + qd * 32 + lane + b2 * 128;
             float inv[16];
-            lrow16(inv, &sh.l_run[hh * 16]);
+            lrow16(inv, &sh.alpha[hh * 16]);
 #pragma unroll
             for (int h = 0; h < 16; ++h) {
               const int c = hh * 16 + h;
               if (c >= n_cols) continue;
-              // a NaN sum stays NaN; a sum of zero (no key) gives zeros
-              const float iv = inv[h] == 0.f ? 0.f : 1.f / inv[h];
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
-                const __nv_bfloat16 ob = __float2bfloat16_rn(__uint_as_float(o[b][h]) * iv);
+                const __nv_bfloat16 ob = __float2bfloat16_rn(__uint_as_float(o[b][h]) * inv[h]);
                 orow[static_cast<size_t>(c) * kDv + b * 128] = *reinterpret_cast<const uint16_t*>(&ob);
               }
             }

@@ -20,6 +20,14 @@ constexpr int kKB = kDqk / 64;         // 64-dim blocks per row
 constexpr int kMinTiles = 2;
 constexpr int kMostGroups = 160;       // groups of CTAs (the join holds five per lane)
 __device__ __forceinline__ int min_share(long long total, int n_q) { return total > 128LL * n_q ? 4 : kMinTiles; }
+// The first tile of group g's share, g <= groups <= kMostGroups: total * g / groups, to the nearest 2^s tiles
+// below where that passes 32 bits (a 64-bit division takes hundreds of cycles on every call's way).
+__device__ __forceinline__ long long share_start(long long total, int g, int groups) {
+  if (g == groups) return total;
+  const int s = max(0, 40 - __clzll(total));           // total >> s < 2^24
+  return static_cast<long long>(static_cast<uint32_t>(total >> s) * static_cast<uint32_t>(g) / static_cast<uint32_t>(groups))
+         << s;
+}
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -151,79 +159,121 @@ __device__ __forceinline__ void publish_faults(const LArgs& a, const CtaFaults& 
   w[1] = f.count;
 }
 
-// The share of group `grp`: a block scan over the rows' tile counts (the whole block calls it, with
-// a block-wide barrier inside and one needed behind it before row0 / tile0 are read).
+// The share of group `grp`: a scan over the rows' tile counts (the whole block calls it; a block-wide barrier
+// is needed behind it before row0 / tile0 are read).
 struct Share {
   long long wsum[32];
   int wmax[32];
   int row0, tile0;
 };
+// Groups in use, and whether they take a row each.
+__device__ __forceinline__ int share_groups(const LArgs& a, long long total, int tallest, bool& by_row) {
+  const int groups =
+      static_cast<int>(min(static_cast<long long>(a.n_grp), min_share(total, a.n_q) == 4 ? (total + 3) >> 2 : (total + 1) >> 1));
+  by_row = a.n_hb == 2 && a.n_q <= a.n_grp &&
+           tallest <= share_start(total, 1, max(groups, 1)) + whole_row_extra(groups);
+  return by_row ? a.n_q : groups;
+}
+__device__ __forceinline__ bool bad_length(const LArgs& a, int row) {
+  const int want = __ldg(a.pg.seq_len + row);
+  return want < 0 || want > (a.pg.max_pages << kPageShift);
+}
 template <bool SEL, int THREADS>
 __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool writes_start, Share& sh, CtaFaults& faults) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (a.n_q + THREADS - 1) / THREADS;
-  const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
-  long long mine = 0;
-  int tallest = 0;
-  bool bad_len = false;
-#pragma unroll 1
-  for (int r = ra; r < rb; ++r) {
-    const int T = row_tiles<SEL>(a, r);
-    mine += T;
-    tallest = max(tallest, T);
-    if (blockIdx.x == 0) {
-      const int want = __ldg(a.pg.seq_len + r);
-      if (want < 0 || want > (a.pg.max_pages << kPageShift)) bad_len = true;
-    }
-  }
-  long long pre = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += v;
-  }
-  if (lane == 31) sh.wsum[warp] = pre;
-  tallest = __reduce_max_sync(0xffffffffu, tallest);
-  if (lane == 0) sh.wmax[warp] = tallest;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (bad_len) report(faults, DEV_ERR_RANGE);
-  long long total = 0;
-  pre -= mine;
-#pragma unroll 1
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) pre += sh.wsum[w];
-    total += sh.wsum[w];
-    tallest = max(tallest, sh.wmax[w]);
-  }
-  const int least = min_share(total, a.n_q);
-  int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), (total + least - 1) / least));
-  const bool by_row = a.n_hb == 2 && a.n_q <= a.n_grp && tallest <= total / max(groups, 1) + whole_row_extra(groups);
-  if (by_row) groups = a.n_q;
   long long share = 0;
-  if (by_row) {
-    share = grp < groups ? row_tiles<SEL>(a, grp) : 0;
-    if (threadIdx.x == 0 && grp < groups) {
-      sh.row0 = grp;
-      sh.tile0 = 0;
-      if (writes_start) a.start[grp] = make_int2(grp, 0);
+  int groups;
+  if (a.n_q <= 32) {
+    // A row a lane, each warp for itself: no barrier, no trip through shared memory (300 keys, 16 heads: 11.6 ->
+    // 10.8 us).
+    const int T = lane < a.n_q ? row_tiles<SEL>(a, lane) : 0;
+    const uint32_t total = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(T));     // 32 x 2^25 at most
+    bool by_row;
+    groups = share_groups(a, total, __reduce_max_sync(0xffffffffu, T), by_row);
+    uint32_t pre = T;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += v;
+    }
+    pre -= T;
+    int row0 = grp, tile0 = 0;
+    if (grp < groups) {
+      if (by_row) {
+        share = __shfl_sync(0xffffffffu, T, grp);
+      } else {
+        const uint32_t first = static_cast<uint32_t>(share_start(total, grp, groups));
+        share = share_start(total, grp + 1, groups) - first;
+        row0 = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, pre <= first && first < pre + T))) - 1;
+        tile0 = static_cast<int>(first - __shfl_sync(0xffffffffu, pre, row0));
+      }
+    }
+    if (threadIdx.x == 0) {
+      sh.row0 = row0;
+      sh.tile0 = tile0;
+      if (writes_start && grp < groups) a.start[grp] = make_int2(row0, tile0);
+    }
+    if (blockIdx.x == 0 && warp == 0) {
+      __syncwarp();        // (thread 0 has set faults)
+      if (lane < a.n_q && bad_length(a, lane)) report(faults, DEV_ERR_RANGE);
     }
   } else {
-    const long long first = grp < groups ? total * grp / groups : 0;
-    share = grp < groups ? total * (grp + 1) / groups - first : 0;
-    if (share > 0 && pre <= first && first < pre + mine) {
-      long long at = pre;
-      int r = ra;
-      while (true) {
-        const int T = row_tiles<SEL>(a, r);
-        if (first < at + T) break;
-        at += T;
-        ++r;
+    const int per = (a.n_q + THREADS - 1) / THREADS;
+    const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
+    long long mine = 0;
+    int tallest = 0;
+    bool bad_len = false;
+#pragma unroll 1
+    for (int r = ra; r < rb; ++r) {
+      const int T = row_tiles<SEL>(a, r);
+      mine += T;
+      tallest = max(tallest, T);
+      if (blockIdx.x == 0 && bad_length(a, r)) bad_len = true;
+    }
+    long long pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += v;
+    }
+    if (lane == 31) sh.wsum[warp] = pre;
+    tallest = __reduce_max_sync(0xffffffffu, tallest);
+    if (lane == 0) sh.wmax[warp] = tallest;
+    __syncthreads();
+    if (bad_len) report(faults, DEV_ERR_RANGE);
+    long long total = 0;
+    pre -= mine;
+#pragma unroll 1
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) pre += sh.wsum[w];
+      total += sh.wsum[w];
+      tallest = max(tallest, sh.wmax[w]);
+    }
+    bool by_row;
+    groups = share_groups(a, total, tallest, by_row);
+    if (by_row) {
+      share = grp < groups ? row_tiles<SEL>(a, grp) : 0;
+      if (threadIdx.x == 0 && grp < groups) {
+        sh.row0 = grp;
+        sh.tile0 = 0;
+        if (writes_start) a.start[grp] = make_int2(grp, 0);
       }
-      sh.row0 = r;
-      sh.tile0 = static_cast<int>(first - at);
-      if (writes_start) a.start[grp] = make_int2(r, static_cast<int>(first - at));
+    } else {
+      const long long first = grp < groups ? share_start(total, grp, groups) : 0;
+      share = grp < groups ? share_start(total, grp + 1, groups) - first : 0;
+      if (share > 0 && pre <= first && first < pre + mine) {
+        long long at = pre;
+        int r = ra;
+        while (true) {
+          const int T = row_tiles<SEL>(a, r);
+          if (first < at + T) break;
+          at += T;
+          ++r;
+        }
+        sh.row0 = r;
+        sh.tile0 = static_cast<int>(first - at);
+        if (writes_start) a.start[grp] = make_int2(r, static_cast<int>(first - at));
+      }
     }
   }
   if (writes_start && threadIdx.x == 0 && grp >= groups) a.start[grp] = make_int2(0x7FFFFFFF, 0);

@@ -19,7 +19,7 @@
 // in both CTAs (a descriptor holds for the pair) and its own row order.  They are filled and freed
 // apart: the S part of tile g + 2 as soon as S(g) is complete, the V part once PV(g) is, so the way
 // of a tile from its rows to its product does not limit how often one begins (one barrier for both
-// parts: 1487 us where the two take 1116, 64 rows of 8K to 131K keys, 128 heads, bf16).
+// parts: 1487 us where the two take 1102, 64 rows of 8K to 131K keys, 128 heads, bf16).
 //
 // TMEM.  An M = 128 accumulator of a pair has head h of each CTA in lane h for the first half of the
 // columns and in lane 64 + h for the second half: O is 2 x 128 columns, S 32 columns, double-buffered.
@@ -32,9 +32,9 @@
 // their parts from there as they do from a bf16 cache (1900 us and more where converters wrote the parts
 // into shared memory).
 //
-// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1116 us, 1202 TFLOP/s of a measured
-// 1924 and 5.0 TB/s of 6.78: operand reads from shared memory next to the copies' writes.  fp8: 1447 us,
-// 927 TFLOP/s, 2.2 TB/s: the same, and the converters' loads and stores through L1.  (Scoring two tiles
+// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1102 us, 1217 TFLOP/s of a measured
+// 1924 and 5.1 TB/s of 6.78: operand reads from shared memory next to the copies' writes.  fp8: 1473 us,
+// 911 TFLOP/s, 2.1 TB/s: the same, and the converters' loads and stores through L1.  (Scoring two tiles
 // with one N = 128 product: bf16 1653, fp8 2008 us.)
 //
 // The leader (the pair's even CTA) issues every product; the peer's warps signal its barriers.  Every
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     // out) of each.  The first kRing tiles are spread instead, eight rows of four tiles a warp: the first
     // tile is there after one round of loads, not four (four selections of 2048: 30.8 -> 27.3 us).  The
     // loops stay rolled: the roles' code together has to stay in the instruction caches (all 32 rows
-    // unrolled: 4826 us where this takes 1447).
+    // unrolled: 4826 us where this takes 1473).
     const uint32_t slot = warp - C::CONV;
     uint16_t* ring = a.ring + (static_cast<size_t>(grp * kRing) * kRows + 32 * rank) * kDqk;
     const uint32_t quarter = slot & 3, first = slot >> 2;      // spread: these rows of tiles first, first + 2, ...
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           tc_fence_after();
           const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
           // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
-          // too slowly for the tensor core: 1913 us where the loop takes 1447)
+          // too slowly for the tensor core: 1913 us where the loop takes 1473)
 #pragma unroll FP8 ? 1 : kKB
           for (int kb = 0; kb < kKB; ++kb)
             umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),
