@@ -168,8 +168,8 @@ struct Share {
 };
 // Groups in use, and whether they take a row each.
 __device__ __forceinline__ int share_groups(const LArgs& a, long long total, int tallest, bool& by_row) {
-  const int groups =
-      static_cast<int>(min(static_cast<long long>(a.n_grp), min_share(total, a.n_q) == 4 ? (total + 3) >> 2 : (total + 1) >> 1));
+  const long long most = min_share(total, a.n_q) == 4 ? (total + 3) >> 2 : (total + 1) >> 1;
+  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), most));
   by_row = a.n_hb == 2 && a.n_q <= a.n_grp &&
            tallest <= share_start(total, 1, max(groups, 1)) + whole_row_extra(groups);
   return by_row ? a.n_q : groups;
