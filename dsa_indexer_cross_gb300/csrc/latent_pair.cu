@@ -38,8 +38,10 @@
 // with one N = 128 product: bf16 1653, fp8 2008 us.)
 //
 // The leader (the pair's even CTA) issues every product; the peer's warps signal its barriers.  Every
-// wait is bounded; the CTAs leave together (a cluster barrier behind the last wait), so no signal goes
-// to a CTA that has left.
+// wait is bounded.  The CTAs leave together (a cluster barrier behind the last wait), so no thread
+// signals a CTA that has left.  The leader's commits arrive in both CTAs by themselves, which no barrier
+// between threads orders: each CTA waits for the last of them, mma_done, on its own copy before it leaves,
+// and none is issued that nobody waits for (q_empty behind the last segment).
 #include "latent_attn.cuh"
 
 namespace dsa {
@@ -71,7 +73,8 @@ struct PCfg {
 
 struct PShared {
   // [2]: by tile parity.  full_*: copies have landed (this CTA); ready_*, s_empty, p_full, o_free, q_ready:
-  // the leader's, both CTAs arrive; s_full, o_done, q_empty: S, PV, all of a segment's S complete (both CTAs)
+  // the leader's, both CTAs arrive; s_full, o_done, q_empty: S, PV, all of a segment's S complete (both CTAs;
+  // q_empty where a segment follows); mma_done: every product complete (both CTAs)
   uint64_t full_s[2], full_v[2], ready_s[2], ready_v[2], q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2],
       o_done[2], o_free, mma_done;
   uint64_t ring_full[kRing], ring_empty[kRing];   // fp8: both CTAs arrive on each CTA's
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
                                      dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
           commit_pair_elect(&sh.s_full[sb]);
         }
-        if (ok) commit_pair_elect(&sh.q_empty);
+        if (ok && walk.left > 0) commit_pair_elect(&sh.q_empty);
       } else {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
@@ -635,7 +638,10 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) publish_faults(a, sh.faults);
-  cluster_sync_all();                    // neither CTA signals, reads or is read any more
+  cluster_sync_all();                    // no thread of either CTA signals, reads or is read any more
+  // The leader has issued every commit and seen its own copy of mma_done.  The peer's shared memory may only be
+  // given up when its copy is there too: both issuing warps' last commit, behind all others of theirs.
+  if (rank != 0 && threadIdx.x == 0) mbar_drain(&sh.mma_done, 0, 200000000ull);
   tc_fence_after();
   if (warp == C::PV_WARP) tmem_dealloc_pair(tmem, kTmemCols);
 }

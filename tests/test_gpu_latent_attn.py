@@ -537,3 +537,82 @@ def test_random_shapes_one_after_another():
                 sel = idx.cpu().numpy()
                 rows = [r[s[s >= 0]] for r, s in zip(rows, sel)]
             check_rows(out, lse, q, rows)
+
+
+class _Calls:
+    """Attention calls of different shapes and data on one workspace, to be issued directly behind one
+    another: every tensor is made beforehand."""
+
+    def __init__(self, H, fmt, sel, seed):
+        rng = np.random.default_rng(seed)
+        shapes = [rng.integers(0, 300, size=200).tolist(), [64] * 310, [5000, 3], rng.integers(0, 2000, size=31).tolist(),
+                  [1], [130] * 77, [0, 9000, 0, 700, 64, 1]]
+        self.calls, need = [], 0
+        for i, lens in enumerate(shapes):
+            pc = Paged(lens, fmt, seed=seed + i)
+            n, k = len(lens), 150 if sel else 0
+            desc = D.attn_desc(n, pc.n_pages * P, H, k, TAU)
+            q = randn((n, H, 576), gen(seed + 20 + i))
+            idx = i32(_selection(lens, k, seed + i)) if sel else None
+            out = torch.empty((n, H, 512), dtype=torch.bfloat16, device=DEV)
+            lse = torch.empty((n, H), device=DEV)
+            need = max(need, D.dsa_latent_attn_workspace_size(desc))
+            self.calls.append((desc, q, pc, idx, out, lse))
+        self.ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+
+    def run(self, after=lambda: None):
+        for desc, q, pc, idx, out, lse in self.calls:
+            D.dsa_latent_attn_paged(desc, q, pc.cache, idx, pc.pages, out, lse, ws=self.ws)
+            after()
+
+    def results(self):
+        return [(out.clone(), lse.clone()) for *_, out, lse in self.calls]
+
+    def forget(self):
+        for *_, out, lse in self.calls:
+            out.fill_(7.0)
+            lse.fill_(7.0)
+
+    def check(self, want):
+        for (o, l), (a, b) in zip(want, self.results()):
+            assert torch.equal(o, a) and torch.equal(l, b)
+
+
+def _alone_and_in_a_row(c):
+    """The results of synchronised calls, of calls without a synchronisation, and of a captured graph."""
+    def check_status():
+        assert D.dsa_workspace_status(c.ws) == 0
+    c.run(check_status)                       # (dsa_workspace_status synchronises)
+    want = c.results()
+    for desc, q, pc, idx, out, lse in c.calls:
+        at = [0, len(pc.lens) - 1]
+        kv = [None] * len(pc.lens)
+        for t in at:
+            kv[t] = pc.stored(t) if idx is None else pc.stored(t)[[j for j in idx[t].tolist() if j >= 0]]
+        check_rows(out, lse, q, kv)
+    for _ in range(10):
+        c.forget()
+        for _ in range(3):
+            c.run()
+        c.check(want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            c.run()
+            c.run()
+        for _ in range(10):
+            c.forget()
+            graph.replay()
+            graph.replay()
+            c.check(want)
+    torch.cuda.synchronize()
+    check_status()
+
+
+@pytest.mark.parametrize("H,fmt,sel", [(100, "bf16", False), (128, "bf16", False), (100, "fp8", True), (128, "fp8", False)])
+def test_pairs_take_over_the_shared_memory_of_the_call_before(H, fmt, sel):
+    """Calls of the pair kernel directly behind one another, a pair walking from no row to many: nothing of
+    the call before (copies, commits to the peer's barriers) may reach the shared memory of the next one."""
+    _alone_and_in_a_row(_Calls(H, fmt, sel, 500 + H))
