@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     if constexpr (!FP8) {
       while (ok && walk.next(sg)) {
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
-        int ahead = __ldg(bt + (sg.i0 >> 1));
+        int ahead = gload(bt + (sg.i0 >> 1));
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int i = sg.i0 + n, page = ahead;
-          if (n + 1 < sg.n) ahead = __ldg(bt + ((i + 1) >> 1));
+          if (n + 1 < sg.n) ahead = gload(bt + ((i + 1) >> 1));
           const bool bad = page < 0 || page >= a.pg.n_pages;
           if (bad && lane == 0 && hb == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
           if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         row0 = as.row;
         lenx = len0;
         const int s = (as.i0 + ai) * kRows + my_row;
-        j0 = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(row0) * a.topk + s) : -1;
+        j0 = !SEL ? s : s < a.topk ? gload(a.idx + static_cast<size_t>(row0) * a.topk + s) : -1;
         advance();
         advance();
       };
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         page2 = -1;
         // (unselected: the page of a row past the end is still the tile's page)
         if (j1 >= 0 && (!SEL || !past2))
-          page2 = __ldg(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
+          page2 = gload(a.pg.block_table + static_cast<size_t>(row1) * a.pg.max_pages + (j1 >> kPageShift));
       };
       auto fetch_step = [&]() {
         const bool in = static_cast<uint32_t>(page2) < static_cast<uint32_t>(a.pg.n_pages);
@@ -241,19 +241,19 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint8_t* src = a.latent + static_cast<size_t>(from[k]) * kDv + off;
-            w[2 * k] = ldg_once(src);
-            w[2 * k + 1] = ldg_once(src + 256);
+            w[2 * k] = gload_once(src);
+            w[2 * k + 1] = gload_once(src + 256);
           }
         } else {
           // the tile's rows follow one another (rows past the end lie in the same page)
           const uint8_t* src = a.latent + static_cast<size_t>(row + (in ? par - (lane & 15) : par)) * kDv + off;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            w[2 * k] = ldg_once(src + 2 * k * kDv);
-            w[2 * k + 1] = ldg_once(src + 2 * k * kDv + 256);
+            w[2 * k] = gload_once(src + 2 * k * kDv);
+            w[2 * k + 1] = gload_once(src + 2 * k * kDv + 256);
           }
         }
-        sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + row);
+        sc = gload(reinterpret_cast<const uint32_t*>(a.scale) + row);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(row) * 64));
       };
       if (turn) advance();
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         const int sb = g & 1;
         bool rv0, rv1;                 // rows r0 / r0 + 8 hold a key
         if constexpr (!SEL) {
-          const int nv = tile_rows(a, len, i, __ldg(bt + (i >> 1)));
+          const int nv = tile_rows(a, len, i, gload(bt + (i >> 1)));
           rv0 = r0 < nv;
           rv1 = r0 + 8 < nv;
         }
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           int nv = kRows;
-          if constexpr (!FP8) nv = tile_rows(a, len, sg.i0 + n, __ldg(bt + ((sg.i0 + n) >> 1)));
+          if constexpr (!FP8) nv = tile_rows(a, len, sg.i0 + n, gload(bt + ((sg.i0 + n) >> 1)));
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
           const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
           const uint32_t d_s = tmem + C::S_COL + sb * HB;
@@ -677,8 +677,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 
 // row_nt[t] = number of 64-slot tiles up to the last slot of idx row t holding an index >= 0; a block
 // a row (2048 slots: one round of loads).
-__global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __restrict__ idx, int topk,
-                                                             int32_t* __restrict__ row_nt) {
+__global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* idx, int topk, int32_t* row_nt) {
   __shared__ int top;
   grid_trigger();
   grid_wait();
@@ -691,7 +690,7 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
     const int4* v = reinterpret_cast<const int4*>(irow);
 #pragma unroll 4
     for (int s = threadIdx.x; s < topk / 4; s += 128) {
-      const int4 q = __ldg(v + s);
+      const int4 q = gload(v + s);
       if (q.x >= 0) last = 4 * s;
       if (q.y >= 0) last = 4 * s + 1;
       if (q.z >= 0) last = 4 * s + 2;
@@ -700,7 +699,7 @@ __global__ void __launch_bounds__(128) selected_tiles_kernel(const int32_t* __re
   } else {
 #pragma unroll 4
     for (int s = threadIdx.x; s < topk; s += 128)
-      if (__ldg(irow + s) >= 0) last = s;
+      if (gload(irow + s) >= 0) last = s;
   }
   last = __reduce_max_sync(0xffffffffu, last);
   if ((threadIdx.x & 31) == 0 && last >= 0) atomicMax(&top, last);
@@ -781,9 +780,9 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
       m[k] = -INFINITY;
       l1[k] = l2[k] = 0.f;
       if (c < end) {
-        m[k] = __ldg(a.part_m + slot(c));
-        l1[k] = __ldg(a.part_m + n + slot(c));
-        l2[k] = __ldg(a.part_m + 2 * n + slot(c));
+        m[k] = gload(a.part_m + slot(c));
+        l1[k] = gload(a.part_m + n + slot(c));
+        l2[k] = gload(a.part_m + 2 * n + slot(c));
       }
     }
 #pragma unroll 1
@@ -795,7 +794,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
         if (c < end) {
           const float4* src = reinterpret_cast<const float4*>(a.part_o + slot(c) * kDv) + lane;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[u][k] = __ldg(src + 32 * k);
+          for (int k = 0; k < 4; ++k) o[u][k] = gload(src + 32 * k);
         }
       }
       if (c0 == b + w) {

@@ -49,9 +49,10 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint4 ldg_once(const void* p) {
+// gload of what is read once.
+__device__ __forceinline__ uint4 gload_once(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -102,11 +103,11 @@ struct LArgs {
 };
 
 __device__ __forceinline__ int row_len(const PagedRows& pg, int row) {
-  return max(0, min(__ldg(pg.seq_len + row), pg.max_pages << kPageShift));
+  return max(0, min(gload(pg.seq_len + row), pg.max_pages << kPageShift));
 }
 template <bool SEL>
 __device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
-  if constexpr (SEL) return __ldg(a.row_nt + row);
+  if constexpr (SEL) return gload(a.row_nt + row);
   return (row_len(a.pg, row) + kRows - 1) / kRows;
 }
 
@@ -175,7 +176,7 @@ __device__ __forceinline__ int share_groups(const LArgs& a, long long total, int
   return by_row ? a.n_q : groups;
 }
 __device__ __forceinline__ bool bad_length(const LArgs& a, int row) {
-  const int want = __ldg(a.pg.seq_len + row);
+  const int want = gload(a.pg.seq_len + row);
   return want < 0 || want > (a.pg.max_pages << kPageShift);
 }
 template <bool SEL, int THREADS>

@@ -126,11 +126,10 @@ __device__ __forceinline__ void sole_status(uint32_t* status, int n, F check) {
 // vectors, then neighbouring heads.  The input is read once (ld.cs: 2 of 26 us at 8000 tokens
 // of 64 heads, 133 MB, which take 23.5 in a graph: 5.7 TB/s); U = 2 and 8 and smaller blocks measured the same.
 template <typename T, bool INTER, int U>
-__global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const int32_t* __restrict__ pos,
-                                                      const float2* __restrict__ cs, int n_pos, uint32_t n_items,
-                                                      int n_heads, int head_groups, int rope, long long x_tok,
-                                                      long long x_head, long long o_tok, long long o_head, float sgn,
-                                                      uint32_t* status, int sole) {
+__global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const int32_t* pos, const float2* cs,
+                                                      int n_pos, uint32_t n_items, int n_heads, int head_groups,
+                                                      int rope, long long x_tok, long long x_head, long long o_tok,
+                                                      long long o_head, float sgn, uint32_t* status, int sole) {
   using E = Elem<T>;
   constexpr int V = E::VEC;
   constexpr int NP = INTER ? V / 2 : V;          // pairs of one head in this thread
@@ -138,14 +137,14 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
   grid_wait();
   if (sole && blockIdx.x == 0)
     sole_status(status, sole, [&](int t) {
-      const int p = __ldg(pos + t);
+      const int p = gload(pos + t);
       return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
     });
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t nv = static_cast<uint32_t>(rope) / (INTER ? V : 2 * V);
   const uint32_t v = item % nv, hg = (item / nv) % head_groups, t = item / (nv * head_groups);
-  const int p = __ldg(pos + t);
+  const int p = gload(pos + t);
   if (p < 0 || p >= n_pos) {
     if (v == 0 && hg == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
     return;
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
   const float4* ct = reinterpret_cast<const float4*>(cs + static_cast<size_t>(p) * half + v * NP);
 #pragma unroll
   for (int i = 0; i < NP / 2; ++i) {
-    const float4 q = __ldg(ct + i);
+    const float4 q = gload(ct + i);
     c[2 * i] = q.x;
     s[2 * i] = q.y * sgn;
     c[2 * i + 1] = q.z;
@@ -196,24 +195,23 @@ __global__ void __launch_bounds__(256) rope_apply_vec(const T* x, T* out, const 
 
 // Any width, stride and alignment: one pair per thread.
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(256) rope_apply_pair(const T* x, T* out, const int32_t* __restrict__ pos,
-                                                       const float2* __restrict__ cs, int n_pos, uint32_t n_items,
-                                                       int n_heads, int rope, long long x_tok, long long x_head,
-                                                       long long o_tok, long long o_head, float sgn, uint32_t* status,
-                                                       int sole) {
+__global__ void __launch_bounds__(256) rope_apply_pair(const T* x, T* out, const int32_t* pos, const float2* cs,
+                                                       int n_pos, uint32_t n_items, int n_heads, int rope,
+                                                       long long x_tok, long long x_head, long long o_tok,
+                                                       long long o_head, float sgn, uint32_t* status, int sole) {
   using E = Elem<T>;
   grid_trigger();
   grid_wait();
   if (sole && blockIdx.x == 0)
     sole_status(status, sole, [&](int t) {
-      const int p = __ldg(pos + t);
+      const int p = gload(pos + t);
       return p < 0 || p >= n_pos ? DEV_ERR_BAD_INDEX : 0u;
     });
   const uint32_t item = blockIdx.x * blockDim.x + threadIdx.x;
   if (item >= n_items) return;
   const uint32_t half = static_cast<uint32_t>(rope) / 2;
   const uint32_t i = item % half, h = (item / half) % n_heads, t = item / (half * n_heads);
-  const int p = __ldg(pos + t);
+  const int p = gload(pos + t);
   if (p < 0 || p >= n_pos) {
     if (i == 0 && h == 0) report(status, sole != 0, DEV_ERR_BAD_INDEX);
     return;
@@ -222,7 +220,7 @@ __global__ void __launch_bounds__(256) rope_apply_pair(const T* x, T* out, const
   const T* xr = x + static_cast<long long>(t) * x_tok + static_cast<long long>(h) * x_head;
   T* orow = out + static_cast<long long>(t) * o_tok + static_cast<long long>(h) * o_head;
   float a = E::load(xr + ia), b = E::load(xr + ib);
-  const float2 q = __ldg(cs + static_cast<size_t>(p) * half + i);
+  const float2 q = gload(cs + static_cast<size_t>(p) * half + i);
   turn(a, b, q.x, q.y * sgn);
   E::store(orow + ia, a);
   E::store(orow + ib, b);
@@ -249,7 +247,7 @@ __device__ __forceinline__ uint4 rope_vec(uint4 v, int lane, bool inter, const f
       const float4* ct = reinterpret_cast<const float4*>(cs_row + l * 4);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 q = __ldg(ct + i);
+        const float4 q = gload(ct + i);
         turn(f[4 * i], f[4 * i + 1], q.x, q.y);
         turn(f[4 * i + 2], f[4 * i + 3], q.z, q.w);
       }
@@ -260,7 +258,7 @@ __device__ __forceinline__ uint4 rope_vec(uint4 v, int lane, bool inter, const f
       const bool second = l >= 4;          // f is the second half's vector, g the first's
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 q = __ldg(ct + i);
+        const float4 q = gload(ct + i);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float c = e ? q.z : q.x, s = e ? q.w : q.y;
@@ -285,18 +283,16 @@ __device__ __forceinline__ uint32_t abs_max(const uint4& v) {
 // tokens to fp8, 124 MB, 24 us, where one warp a token took 31, and two or four tokens a warp 37 and 46;
 // 32768 tokens, 67 MB, 11.5 us in a graph (5.9 TB/s of a copy's 6.8).
 template <bool FP8, bool ROT>
-__global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __restrict__ kv, long long kv_stride,
-                                                          const int32_t* __restrict__ slot,
-                                                          const int32_t* __restrict__ pos,
-                                                          const float2* __restrict__ cs, int n_pos, int n_tokens,
-                                                          int n_rows, bool inter, uint8_t* __restrict__ latent,
-                                                          uint8_t* __restrict__ scale, uint16_t* __restrict__ rope,
+__global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* kv, long long kv_stride,
+                                                          const int32_t* slot, const int32_t* pos, const float2* cs,
+                                                          int n_pos, int n_tokens, int n_rows, bool inter,
+                                                          uint8_t* latent, uint8_t* scale, uint16_t* rope,
                                                           uint32_t* status, int sole) {
   grid_trigger();
   grid_wait();
   if (sole && blockIdx.x == 0)
     sole_status(status, sole, [&](int i) {
-      const int s = __ldg(slot + i), p = ROT ? __ldg(pos + i) : 0;
+      const int s = gload(slot + i), p = ROT ? gload(pos + i) : 0;
       return s >= 0 && (s >= n_rows || (ROT && (p < 0 || p >= n_pos))) ? DEV_ERR_BAD_INDEX : 0u;
     });
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -305,12 +301,12 @@ __global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __rest
   const int tt = min(t, n_tokens - 1);
   const uint4* src = reinterpret_cast<const uint4*>(kv + static_cast<long long>(tt) * kv_stride);
   // (fp8: marked as read once, 32768 tokens 15.3 -> 14.4 us; to bf16 16.4 -> 17.0)
-  const auto load = [](const uint4* q) { return FP8 ? __ldcs(q) : __ldg(q); };
+  const auto load = [](const uint4* q) { return FP8 ? __ldcs(q) : gload(q); };
   const uint4 a = load(src + (turns ? 64 + (lane & 7) : lane));
   uint4 b;
   if (!turns) b = load(src + 32 + lane);
-  const int s = t < n_tokens ? __ldg(slot + tt) : -1;
-  const int p = ROT ? __ldg(pos + tt) : 0;
+  const int s = t < n_tokens ? gload(slot + tt) : -1;
+  const int p = ROT ? gload(pos + tt) : 0;
   const bool bad = s >= n_rows || (ROT && (p < 0 || p >= n_pos)), stored = s >= 0 && !bad;
   if (turns) {
     const uint4 turned = rope_vec<ROT>(a, lane, inter, cs + static_cast<size_t>(stored ? p : 0) * (kRope / 2));
@@ -366,21 +362,20 @@ __global__ void __launch_bounds__(320) cache_write_kernel(const uint16_t* __rest
 constexpr int kReadRows = 32;
 constexpr int kReadSplit = kPageRows / kReadRows;
 template <bool FP8>
-__global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restrict__ latent,
-                                                         const uint8_t* __restrict__ scale,
-                                                         const uint16_t* __restrict__ rope, const PagedRows pg,
-                                                         const int32_t* __restrict__ row_start, int n_out,
-                                                         uint16_t* __restrict__ out, uint32_t* status, int sole) {
+__global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* latent, const uint8_t* scale,
+                                                         const uint16_t* rope, const PagedRows pg,
+                                                         const int32_t* row_start, int n_out, uint16_t* out,
+                                                         uint32_t* status, int sole) {
   const int cap = pg.max_pages << kPageShift;
   // valid rows of a page, its physical page and its first output row; the error bits, if any
   auto place = [&](int blk, int& n, int& page, long long& o0) -> uint32_t {
     const int t = blk / pg.max_pages, pl = blk % pg.max_pages;
-    const int want = __ldg(pg.seq_len + t);
+    const int want = gload(pg.seq_len + t);
     const uint32_t range = pl == 0 && (want < 0 || want > cap) ? DEV_ERR_RANGE : 0u;
     n = min(min(want, cap) - (pl << kPageShift), kPageRows);
     if (n <= 0) return range;
-    page = __ldg(pg.block_table + static_cast<size_t>(t) * pg.max_pages + pl);
-    o0 = static_cast<long long>(__ldg(row_start + t)) + (pl << kPageShift);
+    page = gload(pg.block_table + static_cast<size_t>(t) * pg.max_pages + pl);
+    o0 = static_cast<long long>(gload(row_start + t)) + (pl << kPageShift);
     return range | (page < 0 || page >= pg.n_pages || o0 < 0 || o0 + n > n_out ? DEV_ERR_BAD_INDEX : 0u);
   };
   int n = 0, page = 0;
@@ -405,7 +400,7 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restri
       uint4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (e + 256 * k < total) v[k] = __ldg(src + e + 256 * k);
+        if (e + 256 * k < total) v[k] = gload(src + e + 256 * k);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (e + 256 * k < total) dst[e + 256 * k] = v[k];
@@ -420,12 +415,12 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const uint8_t* __restri
       for (int k = 0; k < 4; ++k) {
         const size_t row = row0 + min(r0 + k, n - 1);
         const uint2* src = reinterpret_cast<const uint2*>(latent + row * kLat);
-        c[k][0] = __ldg(src + lane);
-        c[k][1] = __ldg(src + 32 + lane);
-        sc[k] = __ldg(reinterpret_cast<const uint32_t*>(scale) + row);
+        c[k][0] = gload(src + lane);
+        c[k][1] = gload(src + 32 + lane);
+        sc[k] = gload(reinterpret_cast<const uint32_t*>(scale) + row);
       }
       const int rr = r0 + (lane >> 3);        // the four rows' rotary dims, eight lanes each
-      const uint4 rv = __ldg(reinterpret_cast<const uint4*>(rope + (row0 + min(rr, n - 1)) * kRope) + (lane & 7));
+      const uint4 rv = gload(reinterpret_cast<const uint4*>(rope + (row0 + min(rr, n - 1)) * kRope) + (lane & 7));
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (r0 + k >= n) continue;

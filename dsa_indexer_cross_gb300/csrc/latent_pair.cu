@@ -243,10 +243,10 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     while (ok && walk.next(sg)) {
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
       const int len = row_len(a.pg, sg.row);
-      int ahead = FP8 ? 0 : __ldg(bt + (sg.i0 >> 1));
+      int ahead = FP8 ? 0 : gload(bt + (sg.i0 >> 1));
       for (int n = 0; n < sg.n && ok; ++n, ++g) {
         const int i = sg.i0 + n, page = ahead, sb = g & 1;
-        if (!FP8 && n + 1 < sg.n) ahead = __ldg(bt + ((i + 1) >> 1));
+        if (!FP8 && n + 1 < sg.n) ahead = gload(bt + ((i + 1) >> 1));
         const int nv = FP8 ? kRows : tile_rows(a, len, i, page);
         if (copies) {
           if (nv == 0 && lane == 0 && rank == 0 && part0 == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
@@ -337,12 +337,12 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       if (!alive) return;
       len = row_len(a.pg, as.row);
       const int s = (as.i0 + ai) * kRows + static_cast<int>(32 * rank + my_row);
-      j = !SEL ? s : s < a.topk ? __ldg(a.idx + static_cast<size_t>(as.row) * a.topk + s) : -1;
+      j = !SEL ? s : s < a.topk ? gload(a.idx + static_cast<size_t>(as.row) * a.topk + s) : -1;
     };
     auto find_page = [&]() {
       page = -1;
       if (j >= 0 && j < len)
-        page = __ldg(a.pg.block_table + static_cast<size_t>(as.row) * a.pg.max_pages + (j >> kPageShift));
+        page = gload(a.pg.block_table + static_cast<size_t>(as.row) * a.pg.max_pages + (j >> kPageShift));
     };
     auto cache_row = [&]() -> int {          // -1: no key
       const bool in = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pg.n_pages);
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     find_page();
     for (uint32_t lap = 0, t = slot; ok && (lap == 0 || t < n_tiles); t += kRing, ++lap) {
       const int at = cache_row();
-      const uint32_t sc = __ldg(reinterpret_cast<const uint32_t*>(a.scale) + max(at, 0));
+      const uint32_t sc = gload(reinterpret_cast<const uint32_t*>(a.scale) + max(at, 0));
       advance(static_cast<int>(t + kRing - my_tile));
       my_tile = t + kRing;
       my_row = lane;
@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         for (int k = 0; k < 2; ++k) rr[k] = __shfl_sync(0xffffffffu, at, 8 * q + 4 * k + (lane >> 3));
         // (rows without a key read a row of the cache all the same: no branch around the loads)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = ldg_once(a.latent + static_cast<size_t>(max(row[k], 0)) * kDv + lane * 16);
+        for (int k = 0; k < 8; ++k) w[k] = gload_once(a.latent + static_cast<size_t>(max(row[k], 0)) * kDv + lane * 16);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) rope[k] = ldg_once(a.rope + static_cast<size_t>(max(rr[k], 0)) * 64 + (lane & 7) * 8);
+        for (int k = 0; k < 2; ++k) rope[k] = gload_once(a.rope + static_cast<size_t>(max(rr[k], 0)) * 64 + (lane & 7) * 8);
         if (q == 0) {
           find_page();
           if (lap > 0 && !(ok = wait(&sh.ring_empty[slot], (lap - 1) & 1))) break;
@@ -428,12 +428,12 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         uint32_t mask;                                           // bit c: key kbase + c holds a key
         if constexpr (SEL) {
           const int s = i * kRows + kbase + (lane & (kKT - 1));
-          const int j = s < a.topk ? __ldg(irow + s) : -1;
+          const int j = s < a.topk ? gload(irow + s) : -1;
           bool v = j >= 0 && j < len;
-          if (v) v = static_cast<uint32_t>(__ldg(bt + (j >> kPageShift))) < static_cast<uint32_t>(a.pg.n_pages);
+          if (v) v = static_cast<uint32_t>(gload(bt + (j >> kPageShift))) < static_cast<uint32_t>(a.pg.n_pages);
           mask = __ballot_sync(0xffffffffu, v) & kAll;
         } else {
-          const int nv = tile_rows(a, len, i, __ldg(bt + (i >> 1))) - kbase;
+          const int nv = tile_rows(a, len, i, gload(bt + (i >> 1))) - kbase;
           mask = nv >= kKT ? kAll : nv <= 0 ? 0u : (1u << nv) - 1u;
         }
         bool ok = wait(&sh.s_full[sb], (g >> 1) & 1);

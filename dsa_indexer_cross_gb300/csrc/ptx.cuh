@@ -331,5 +331,13 @@ __device__ __forceinline__ float key_float(uint32_t k) {
 // kernel's memory.
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// How such a kernel reads global memory: with ordinary loads behind grid_wait.  It is resident while the
+// kernel before still writes, so nothing that a kernel or a copy may have written (which is every argument
+// of a call and all of its workspace) is read-only for its lifetime, as the non-coherent loads (__ldg, .nc,
+// and what the compiler makes of const __restrict__ pointers) ask for; those may also be moved above grid_wait.
+template <typename T>
+__device__ __forceinline__ T gload(const T* p) {
+  return *p;
+}
 
 }  // namespace dsa

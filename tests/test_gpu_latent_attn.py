@@ -616,3 +616,64 @@ def test_pairs_take_over_the_shared_memory_of_the_call_before(H, fmt, sel):
     """Calls of the pair kernel directly behind one another, a pair walking from no row to many: nothing of
     the call before (copies, commits to the peer's barriers) may reach the shared memory of the next one."""
     _alone_and_in_a_row(_Calls(H, fmt, sel, 500 + H))
+
+
+@pytest.mark.parametrize("H,fmt,sel", [(16, "bf16", False), (16, "fp8", True), (64, "fp8", False), (64, "fp8", True),
+                                       (128, "fp8", False), (128, "fp8", True), (128, "bf16", False)])
+def test_attention_calls_right_behind_one_another(H, fmt, sel):
+    """Split calls with different queries, lengths and selections on one workspace, no other operation
+    between them: partials, starts, tile counts and the ring are the call's own, never the one's before."""
+    _alone_and_in_a_row(_Calls(H, fmt, sel, 700 + H))
+
+
+@pytest.mark.parametrize("H,fmt,sel", [(16, "bf16", False), (16, "fp8", False), (64, "fp8", True), (128, "bf16", False),
+                                       (128, "fp8", False), (128, "fp8", True)])
+def test_attention_right_behind_the_writing_of_its_rows(H, fmt, sel):
+    """Turns of rotation into q, writing every cached row and attention, with nothing between them and ever
+    other data: the bits of synchronised turns, eagerly and captured."""
+    lens, g, turns = [130, 700, 64, 1500, 1, 4000], gen(197), 5
+    pc = Paged(lens, fmt, seed=198)
+    slot = torch.cat([p.to(torch.int32) for p in pc.phys])
+    n, B = slot.numel(), len(lens)
+    kvs = [randn((n, 576), g) for _ in range(turns)]
+    src = [randn((B, H, 576), g) for _ in range(turns)]
+    ids = [i32(_selection(lens, 200, it)) if sel else None for it in range(turns)]
+    q = src[0].clone()
+    tab, pos = D.dsa_rope_table(1e4, 64, 100).to(DEV), i32([0, 7, 99, 31, 5, 60])
+    desc = D.attn_desc(B, pc.n_pages * P, H, 200 if sel else 0, TAU)
+    ws, w1, w2 = (torch.zeros(k, dtype=torch.uint8, device=DEV) for k in (D.dsa_latent_attn_workspace_size(desc), 256, 256))
+    outs = [(torch.zeros((B, H, 512), dtype=torch.bfloat16, device=DEV), torch.zeros((B, H), device=DEV)) for _ in range(turns)]
+
+    def run(sync):
+        for it in range(turns):
+            x, y = src[it][..., 512:], q[..., 512:]
+            D.dsa_rope_apply(D.rope_desc(x, y), x, pos, tab, y, ws=w2)
+            sync()
+            D.dsa_latent_cache_write(D.cache_write_desc(kvs[it]), kvs[it], slot, None, None, pc.cache, ws=w1)
+            sync()
+            D.dsa_latent_attn_paged(desc, q, pc.cache, ids[it], pc.pages, *outs[it], ws=ws)
+            sync()
+
+    run(torch.cuda.synchronize)
+    want = [(o.clone(), l.clone()) for o, l in outs]
+    assert not torch.equal(want[0][0], want[1][0])
+
+    def check():
+        for (o, l), (a, b) in zip(want, outs):
+            assert torch.equal(o, a) and torch.equal(l, b)
+            a.fill_(7.0)
+            b.fill_(7.0)
+    for _ in range(10):
+        run(lambda: None)
+        check()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            run(lambda: None)
+        for _ in range(10):
+            graph.replay()
+            check()
+    torch.cuda.synchronize()
+    assert all(D.dsa_workspace_status(w) == 0 for w in (ws, w1, w2))

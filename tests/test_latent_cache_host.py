@@ -267,3 +267,15 @@ def test_binding_checks_views():
         D.cache_write_desc(torch.zeros((4, 640), dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         D.latent_cache(torch.zeros((128, 512), dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("name", ["latent_cache.cu", "latent_attn.cu", "latent_attn.cuh", "latent_pair.cu", "fp8.cuh"])
+def test_overlapped_kernels_read_memory_with_ordinary_loads(name):
+    """Every kernel of these files is resident while the one before it still writes, so none of what it
+    reads is read-only for its lifetime: no non-coherent load, and no const pointer that the compiler may
+    read with one."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(_lib.__file__), "csrc", name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.search(r"__ldg\b|\.nc\b|__restrict__|ld\.global\.nc", code)
