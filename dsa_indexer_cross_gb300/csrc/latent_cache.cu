@@ -456,8 +456,8 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
   const int sole = a.n_tokens <= std::min(kSoleMostRope, most) ? a.n_tokens : 0;      // (one launch)
   cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
   if (e != cudaSuccess) return e;
-  for (int t0 = 0; t0 < a.n_tokens; t0 += most) {
-    const int n = std::min(most, a.n_tokens - t0);
+  for (long long t0 = 0; t0 < a.n_tokens; t0 += most) {      // (t0 + most may pass 32 bits)
+    const int n = static_cast<int>(std::min<long long>(most, a.n_tokens - t0));
     const uint32_t items = static_cast<uint32_t>(per * n);
     const unsigned grid = (items + 255) / 256;
     const T* x = static_cast<const T*>(a.x) + t0 * a.x_tok;
@@ -468,7 +468,6 @@ cudaError_t launch_rope_t(const RopeApply& a, const int32_t* pos, const float* c
             : launch_pdl(rope_apply_pair<T, INTER>, dim3(grid), 256, 0, st, 1, x, out, pos + t0, c2, n_pos, items,
                          a.n_heads, a.rope, a.x_tok, a.x_head, a.o_tok, a.o_head, sgn, status, sole);
     if (e != cudaSuccess) return e;
-    if (n == a.n_tokens) break;      // also keeps t0 + most inside int
   }
   return cudaSuccess;
 }

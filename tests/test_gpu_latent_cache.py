@@ -444,3 +444,27 @@ def test_calls_in_a_row_see_what_the_one_before_wrote(n):
         # the 64 rotary dims are rounded twice, by at most 2^-8 of a pair's length each (1.5 of the value's
         # sum over a pair at most); sums of 576 terms in fp32
         assert torch.all((a - b).abs() <= a * (2 * 2.0 ** -8 * 1.5 + 576 * 2.0 ** -23))
+
+
+def test_rope_of_as_many_tokens_as_an_int_holds():
+    """2^31 - 1 tokens of one head and one pair: two launches, the second of 255 tokens, and no third."""
+    n, g = (1 << 31) - 1, gen(78)
+    x = randn((1, 1, 2), g).expand(n, 1, 2)
+    out = torch.full((n + 64, 1, 2), 3.0, dtype=torch.bfloat16, device=DEV)
+    ov = out[:n]
+    tab = D.dsa_rope_table(THETA, 2, 50).to(DEV)
+    pos = torch.zeros(n, dtype=torch.int32, device=DEV)
+    at = [0, 1, 12345, (1 << 30) + 7, n - 256, n - 255, n - 254, n - 2, n - 1]
+    pos[at] = i32([3, 49, 7, 11, 5, 6, 8, 50, 9])
+    ws = D.dsa_rope_apply(D.rope_desc(x, ov), x, pos, tab, ov)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    p64 = pos[at].cpu().numpy()
+    keep = p64 < 50
+    cs = tab.double().cpu().numpy()[p64[keep]][:, None]
+    got = ov[at].double().cpu().numpy()[keep]
+    _check_turned(got, np.broadcast_to(x[0].double().cpu().numpy(), got.shape), cs, False, False, 2.0 ** -8)
+    assert torch.all(out[n - 2] == 3.0) and torch.all(out[n:] == 3.0)
+    out[at] = x[at]                           # everywhere else: a turn by nothing
+    flat = out[:n].view(torch.int32).view(-1)
+    step = 1 << 28
+    assert all(torch.all(flat[i:i + step] == flat[0]) for i in range(0, n, step))
