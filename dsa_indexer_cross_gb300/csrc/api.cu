@@ -73,6 +73,14 @@ dsa_status check_device() {
   return DSA_OK;
 }
 
+// A call without rows does one thing: it clears the status words, as every call that takes a workspace
+// does (without one there are none).
+dsa_status empty_call(void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (!ws || ws_bytes < kAlign) return DSA_OK;
+  const cudaError_t e = cudaMemsetAsync(ws, 0, kAlign, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "clear status");
+}
+
 // ------------------------------------------------------------------ phase profiling
 // Five events per device bracket the four phases of an indexer call while profiling is on.
 std::atomic<int> g_profile{0};
@@ -291,7 +299,7 @@ dsa_status run_indexer(const dsa_indexer_desc* d, const void* q_idx, const void*
                        size_t ws_bytes, cudaStream_t st, bool clear_status, const PagedRows* pg = nullptr) {
   dsa_status s = check_indexer_desc(d);
   if (s != DSA_OK) return s;
-  if (d->n_q == 0) return DSA_OK;
+  if (d->n_q == 0) return clear_status ? empty_call(ws, ws_bytes, st) : DSA_OK;
   const bool rq = (d->flags & DSA_IDX_ROPE_Q) && d->rope_dim > 0;
   const bool rk = (d->flags & DSA_IDX_ROPE_K) && d->rope_dim > 0;
   if (!q_idx || !k_idx || !w || (!ks && !pg) || !ke || !idx_out || !ws)
@@ -421,7 +429,7 @@ dsa_status run_attn(const dsa_attn_desc* d, const void* q, const void* kv, const
                     uint32_t* status_override = nullptr, const PagedRows* pg = nullptr, bool reuse_prepass = false) {
   dsa_status s = check_attn_desc(d);
   if (s != DSA_OK) return s;
-  if (d->n_q == 0) return DSA_OK;
+  if (d->n_q == 0) return clear_status ? empty_call(ws, ws_bytes, st) : DSA_OK;
   if (!q || !kv || !idx || (!ks && !pg) || !out || !ws)
     return fail(DSA_ERR_ARG, "q, kv, idx, ks, out and ws must be non-NULL");
   if (!aligned16(q) || !aligned16(kv) || !aligned16(out)) return fail(DSA_ERR_ARG, "q, kv and out must be 16-byte aligned");
@@ -883,7 +891,7 @@ dsa_status dsa_rope_apply(const dsa_rope_desc* d, const void* x, const int32_t* 
     return fail(DSA_ERR_ARG, "in place, x and out need the same strides");
   dsa_status s;
   if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
-  if (d->n_tokens == 0) return DSA_OK;
+  if (d->n_tokens == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
   if (!x || !out || !pos || !rope_cs || rope_n_pos < 1) return fail(DSA_ERR_ARG, "x, pos, rope_cs and out must be non-NULL");
   const uintptr_t el = d->dtype == DSA_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(x) % el || reinterpret_cast<uintptr_t>(out) % el)
@@ -912,7 +920,7 @@ dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* d, const void* kv,
   LatentCache c;
   if ((s = check_cache(cache, &c)) != DSA_OK) return s;
   if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
-  if (d->n_tokens == 0) return DSA_OK;
+  if (d->n_tokens == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
   const bool rot = (d->flags & DSA_CACHE_ROPE) != 0;
   if (!kv || !slot || (rot && (!pos || !rope_cs || rope_n_pos < 1)))
     return fail(DSA_ERR_ARG, "kv, slot (DSA_CACHE_ROPE: and pos, rope_cs) must be non-NULL");
@@ -940,7 +948,7 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
     return fail(DSA_ERR_SHAPE, "n_seq * max_pages exceeds 2^29 - 1");
   if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
   if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
-  if (n_seq == 0) return DSA_OK;
+  if (n_seq == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
   if (!row_start || !kv_out) return fail(DSA_ERR_ARG, "row_start and kv_out must be non-NULL");
   if (!aligned16(kv_out)) return fail(DSA_ERR_ARG, "kv_out must be 16-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
@@ -990,7 +998,7 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (idx && !c.fp8)   // selected rows of a bf16 cache: the sparse kernel's gather walk
     return run_attn(&d, q, c.latent, idx, nullptr, out, lse, ws, ws_bytes, st, true, nullptr, &pg);
-  if (d.n_q == 0) return DSA_OK;
+  if (d.n_q == 0) return empty_call(ws, ws_bytes, st);
   if (!q || !out || !ws) return fail(DSA_ERR_ARG, "q, out and ws must be non-NULL");
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_ARG, "q and out must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be 256-byte aligned");
@@ -1034,7 +1042,7 @@ dsa_status dsa_indexer_projections(const dsa_proj_desc* d, const void* x, const 
     return fail(DSA_ERR_ARG, "bf16 tensors must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be 256-byte aligned");
   if (ws_bytes < kAlign) return fail(DSA_ERR_WORKSPACE, "projection workspace too small: %zu < %zu bytes", ws_bytes, kAlign);
-  if (d->n_tokens == 0) return DSA_OK;
+  if (d->n_tokens == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
   dsa_status s;
   if ((s = check_device()) != DSA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

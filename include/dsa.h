@@ -557,7 +557,7 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
 /* Synchronise `stream`, read the device status word of workspace `ws`, and map it:
  * DSA_OK, DSA_ERR_TIMEOUT (a pipeline wait hit its bound) or DSA_ERR_DEVICE (bad index,
  * range or overflow).  The raw bits are stored in *device_bits when it is not NULL.
- * The word is cleared at the start of every call that takes the workspace. */
+ * The word is cleared at the start of every call that takes the workspace, of one without rows too. */
 dsa_status dsa_workspace_status(const void* ws, void* stream, uint32_t* device_bits);
 
 /* ------------------------------------------------------------------ profiling ------- */

@@ -468,3 +468,47 @@ def test_rope_of_as_many_tokens_as_an_int_holds():
     flat = out[:n].view(torch.int32).view(-1)
     step = 1 << 28
     assert all(torch.all(flat[i:i + step] == flat[0]) for i in range(0, n, step))
+
+
+def _empty_calls():
+    """(name, call with a workspace) of every call that takes rows, without any."""
+    bf, f32, i32_ = torch.bfloat16, torch.float32, torch.int32
+    some = lambda dt, *s: torch.zeros(s, dtype=dt, device=DEV)  # noqa: E731
+    rows, codes = some(bf, P, 576), some(torch.uint8, P, 512)
+    bt, ln = some(i32_, 1, 1), some(i32_, 1)
+    pages = D.paged_cache(bt, ln, 1)
+    c16, c8 = D.latent_cache(rows), D.latent_cache(codes, some(torch.uint8, P, 4), some(bf, P, 64))
+    tab, x = some(f32, 4, 32, 2), some(bf, 0, 2, 64)
+    q, out, idx, pos = some(bf, 0, 16, 576), some(bf, 0, 16, 512), some(i32_, 0, 8), some(i32_, 0)
+    kv = some(bf, 0, 576)
+    ad, ad0 = D.attn_desc(0, P, 16, 8, 0.04), D.attn_desc(0, P, 16, 0, 0.04)
+    nd = D.indexer_desc(0, P, 64, 128, 64, 8, P, D.DSA_IDX_ROPE_Q | D.DSA_IDX_ROPE_K)
+    npd = D.indexer_desc(0, P, 64, 128, 64, 8, P, D.DSA_IDX_ROPE_Q | D.DSA_IDX_INDEPENDENT_ROWS)
+    pd = D.ProjDesc(0, 64, 64, 64, 128, 1e-6)
+    one = some(bf, 64 * 128 * 64)
+    of = some(f32, 64 * 64)
+    qi, ki, w = some(bf, 0, 64, 128), some(bf, P, 128), some(f32, 0, 64)
+    keep = (rows, codes, bt, ln, c16, c8)
+    return keep, [
+        ("rope", lambda ws: D.dsa_rope_apply(D.rope_desc(x, x), x, pos, tab, x, ws=ws)),
+        ("write", lambda ws: D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, pos, None, None, c8, ws=ws)),
+        ("read", lambda ws: D.dsa_latent_cache_read(c8, pages, 0, pos, rows, ws=ws)),
+        ("every key", lambda ws: D.dsa_latent_attn_paged(ad0, q, c8, None, pages, out, ws=ws)),
+        ("selected, fp8", lambda ws: D.dsa_latent_attn_paged(ad, q, c8, idx, pages, out, ws=ws)),
+        ("selected, bf16", lambda ws: D.dsa_latent_attn_paged(ad, q, c16, idx, pages, out, ws=ws)),
+        ("sparse", lambda ws: D.dsa_sparse_attn(ad, q, rows, idx, pos, out, ws=ws)),
+        ("sparse, paged", lambda ws: D.dsa_sparse_attn_paged(ad, q, rows, idx, pages, out, ws=ws)),
+        ("indexer", lambda ws: D.dsa_indexer_topk(nd, qi, ki, w, pos, some(i32_, P), pos, pos, tab, idx, ws=ws)),
+        ("indexer, paged", lambda ws: D.dsa_indexer_topk_paged(npd, qi, ki, w, pos, pages, tab, idx, ws=ws)),
+        ("projections", lambda ws: D.dsa_indexer_projections(pd, one, one, one, one, of, of, one, one, one, of, ws=ws)),
+    ]
+
+
+def test_calls_without_rows_clear_the_status():
+    """A reused workspace holds the faults of the call before, a new one whatever its memory held."""
+    keep, calls = _empty_calls()
+    for name, call in calls:
+        ws = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device=DEV)
+        call(ws)
+        assert D.dsa_workspace_status(ws) == 0, name
+        assert torch.all(ws[256:] == 0xFF), name
