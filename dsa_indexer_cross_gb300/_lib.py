@@ -486,8 +486,8 @@ def paged_cache(block_table: torch.Tensor, seq_len: torch.Tensor, n_pages: int) 
     return PagedCache(_ptr(block_table), _ptr(seq_len), block_table.shape[1], n_pages, DSA_PAGE_ROWS)
 
 
-def _paged_args(pages: PagedCache) -> None:
-    if not pages.block_table or not pages.seq_len:
+def _paged_args(pages: PagedCache, rows: int) -> None:
+    if rows and not (pages.block_table and pages.seq_len):      # (an empty tensor has no address)
         raise ValueError("paged cache: block_table and seq_len must be set")
 
 
@@ -500,7 +500,7 @@ def dsa_indexer_topk_paged(desc: IndexerDesc, q_idx, k_cache, w, q_pos, pages: P
                            (idx_out, i32, n_q * k, "idx_out"), (score_out, f32, n_q * k, "score_out")):
         if t is not None:
             _want(t, dt, n, name)
-    _paged_args(pages)
+    _paged_args(pages, n_q)
     if ws is None:
         ws = torch.empty(dsa_indexer_workspace_size(desc), dtype=torch.uint8, device=q_idx.device)
     n_pos = rope_cs.shape[0] if rope_cs is not None else 0
@@ -517,7 +517,7 @@ def dsa_sparse_attn_paged(desc: AttnDesc, q, kv_cache, idx, pages: PagedCache, o
                            (idx, i32, n_q * k, "idx"), (out, bf, n_q * H * desc.d_v, "out"), (lse, f32, n_q * H, "lse")):
         if t is not None:
             _want(t, dt, n, name)
-    _paged_args(pages)
+    _paged_args(pages, n_q)
     if ws is None:
         ws = torch.empty(dsa_sparse_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
     _check(lib().dsa_sparse_attn_paged(C.byref(desc), _ptr(q), _ptr(kv_cache), _ptr(idx), C.byref(pages), _ptr(out),
@@ -657,7 +657,7 @@ def dsa_latent_cache_write(desc: CacheWriteDesc, kv, slot, pos, rope_cs, cache: 
 def dsa_latent_cache_read(cache: LatentCache, pages: PagedCache, n_seq: int, row_start, kv_out, ws=None,
                           stream=None) -> torch.Tensor:
     """kv_out[row_start[t] + j] = row j of sequence t for every cached row of n_seq sequences, bf16."""
-    _paged_args(pages)
+    _paged_args(pages, n_seq)
     s = kv_out.shape
     if len(s) != 2 or s[1] != 576:
         raise ValueError(f"kv_out: expected bf16 [rows, 576], got {kv_out.dtype} {tuple(s)}")
@@ -687,7 +687,7 @@ def dsa_latent_attn_paged(desc: AttnDesc, q, cache: LatentCache, idx, pages: Pag
     p_idx = None if idx is None else _arg(idx, torch.int32, desc.n_q * desc.topk, "idx")
     p_lse = None if lse is None else _arg(lse, torch.float32, n, "lse")
     _on_current_device(q)
-    _paged_args(pages)
+    _paged_args(pages, desc.n_q)
     if ws is None:
         ws = torch.empty(dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
     st = (_lib or lib()).dsa_latent_attn_paged(desc, p_q, cache, p_idx, pages, p_out, p_lse,

@@ -758,8 +758,10 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
 }
 
 namespace {
-dsa_status check_pages(const dsa_paged_cache* pc, int32_t n_kv, PagedRows* pg) {
-  if (!pc || !pc->block_table || !pc->seq_len) return fail(DSA_ERR_ARG, "paged cache: block_table and seq_len must be non-NULL");
+// rows: of the tables that the call reads; tables without any may be NULL (an empty tensor's address).
+dsa_status check_pages(const dsa_paged_cache* pc, int32_t n_kv, int32_t rows, PagedRows* pg) {
+  if (!pc || (rows != 0 && (!pc->block_table || !pc->seq_len)))
+    return fail(DSA_ERR_ARG, "paged cache: block_table and seq_len must be non-NULL");
   if (pc->page_rows != kPageRows)
     return fail(DSA_ERR_UNSUPPORTED, "page_rows %d: this library supports %d-row pages", pc->page_rows, kPageRows);
   if (pc->max_pages < 1 || pc->n_pages < 1) return fail(DSA_ERR_ARG, "max_pages and n_pages must be >= 1");
@@ -781,7 +783,7 @@ dsa_status dsa_indexer_topk_paged(const dsa_indexer_desc* desc, const void* q_id
   dsa_status s = check_indexer_desc(desc);
   if (s != DSA_OK) return s;
   PagedRows pg;
-  if ((s = check_pages(pages, desc->n_kv, &pg)) != DSA_OK) return s;
+  if ((s = check_pages(pages, desc->n_kv, desc->n_q, &pg)) != DSA_OK) return s;
   if (!(desc->flags & DSA_IDX_INDEPENDENT_ROWS) || (desc->flags & DSA_IDX_ROPE_K))
     return fail(DSA_ERR_ARG, "a paged key cache needs DSA_IDX_INDEPENDENT_ROWS and a pre-rotated cache (no DSA_IDX_ROPE_K)");
   if (desc->n_heads != 64)
@@ -798,7 +800,7 @@ dsa_status dsa_sparse_attn_paged(const dsa_attn_desc* desc, const void* q, const
   dsa_status s = check_attn_desc(desc);
   if (s != DSA_OK) return s;
   PagedRows pg;
-  if ((s = check_pages(pages, desc->n_kv, &pg)) != DSA_OK) return s;
+  if ((s = check_pages(pages, desc->n_kv, desc->n_q, &pg)) != DSA_OK) return s;
   return run_attn(desc, q, kv_cache, idx, nullptr, out, lse, ws, ws_bytes, static_cast<cudaStream_t>(stream), true,
                   nullptr, &pg);
 }
@@ -942,14 +944,14 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
   LatentCache c;
   if ((s = check_cache(cache, &c)) != DSA_OK) return s;
   PagedRows pg;
-  if ((s = check_pages(pages, c.n_rows, &pg)) != DSA_OK) return s;
+  if ((s = check_pages(pages, c.n_rows, n_seq, &pg)) != DSA_OK) return s;
   if (n_seq < 0 || n_out < 0) return fail(DSA_ERR_ARG, "n_seq and n_out must be >= 0");
   if (static_cast<long long>(n_seq) * pg.max_pages > 0x1FFFFFFFLL)
     return fail(DSA_ERR_SHAPE, "n_seq * max_pages exceeds 2^29 - 1");
   if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
   if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
   if (n_seq == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
-  if (!row_start || !kv_out) return fail(DSA_ERR_ARG, "row_start and kv_out must be non-NULL");
+  if (!row_start || (!kv_out && n_out > 0)) return fail(DSA_ERR_ARG, "row_start and kv_out must be non-NULL");
   if (!aligned16(kv_out)) return fail(DSA_ERR_ARG, "kv_out must be 16-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -989,7 +991,7 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   LatentCache c;
   if ((s = check_cache(cache, &c)) != DSA_OK) return s;
   PagedRows pg;
-  if ((s = check_pages(pages, d.n_kv, &pg)) != DSA_OK) return s;
+  if ((s = check_pages(pages, d.n_kv, d.n_q, &pg)) != DSA_OK) return s;
   if (c.n_rows != d.n_kv) return fail(DSA_ERR_SHAPE, "n_kv %d must equal the cache's n_rows %d", d.n_kv, c.n_rows);
   if (pg.max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
   if (static_cast<long long>(d.n_q) * d.n_heads > 0x7FFFFFFFLL)

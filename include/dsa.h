@@ -353,7 +353,8 @@ dsa_status dsa_indexer_backward(const dsa_indexer_desc* desc, const void* q_idx,
  * logical key j (j < seq_len[t]) sits at cache row
  *   block_table[t * max_pages + j / page_rows] * page_rows + j % page_rows.
  * All arrays are device memory owned by the caller.  page_rows must be DSA_PAGE_ROWS (one
- * 128-key indexer tile per page, so every tile is one TMA box). */
+ * 128-key indexer tile per page, so every tile is one TMA box).  A call without rows may leave
+ * block_table and seq_len NULL. */
 #define DSA_PAGE_ROWS 128
 typedef struct dsa_paged_cache {
   const int32_t* block_table; /* [n_q][max_pages] int32 physical page ids                    */
@@ -499,7 +500,7 @@ dsa_status dsa_latent_cache_write(const dsa_cache_write_desc* desc, const void* 
  * sequences whose output rows overlap leave a mixture.  A page outside the cache, or output rows
  * outside [0, n_out), are skipped page by page and flagged; a length outside [0, max_pages *
  * page_rows] is cut to it and flagged (DSA_ERR_DEVICE).  ws: at least 256 bytes.
- *   row_start int32 [n_seq]; kv_out bf16 [n_out][576], 16-byte aligned.
+ *   row_start int32 [n_seq]; kv_out bf16 [n_out][576], 16-byte aligned (n_out 0: may be NULL).
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows != n_pages * page_rows, n_seq * max_pages >= 2^29),
  * DSA_ERR_UNSUPPORTED (page_rows), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
 dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_cache* pages, int32_t n_seq,

@@ -512,3 +512,26 @@ def test_calls_without_rows_clear_the_status():
         call(ws)
         assert D.dsa_workspace_status(ws) == 0, name
         assert torch.all(ws[256:] == 0xFF), name
+
+
+def test_empty_batches_and_outputs_made_of_empty_tensors():
+    c = D.latent_cache(torch.zeros((2 * P, 576), dtype=torch.bfloat16, device=DEV))
+    e = lambda dt, *s: torch.empty(s, dtype=dt, device=DEV)  # noqa: E731
+    none = D.paged_cache(e(torch.int32, 0, 5), e(torch.int32, 0), 2)
+    q, out = e(torch.bfloat16, 0, 16, 576), e(torch.bfloat16, 0, 16, 512)
+    ws = D.dsa_latent_attn_paged(D.attn_desc(0, 2 * P, 16, 0, 0.04), q, c, None, none, out)
+    assert D.dsa_workspace_status(ws) == 0
+    ws = D.dsa_sparse_attn_paged(D.attn_desc(0, 2 * P, 16, 4, 0.04), q, torch.zeros((2 * P, 576), dtype=torch.bfloat16, device=DEV),
+                                 e(torch.int32, 0, 4), none, out)
+    assert D.dsa_workspace_status(ws) == 0
+    back = e(torch.bfloat16, 0, 576)
+    ws = D.dsa_latent_cache_read(c, none, 0, e(torch.int32, 0), back)
+    assert D.dsa_workspace_status(ws) == 0
+    # sequences that are all empty have no output rows; a row without room is flagged
+    bt, ln = i32([[0], [1]]), i32([0, 0])
+    pages = D.paged_cache(bt, ln, 2)
+    ws = D.dsa_latent_cache_read(c, pages, 2, i32([0, 0]), back)
+    assert D.dsa_workspace_status(ws) == 0
+    ln[1] = 1
+    ws = D.dsa_latent_cache_read(c, pages, 2, i32([0, 0]), back, ws=ws)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2

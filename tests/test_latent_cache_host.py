@@ -279,3 +279,20 @@ def test_overlapped_kernels_read_memory_with_ordinary_loads(name):
     with open(os.path.join(os.path.dirname(_lib.__file__), "csrc", name)) as f:
         code = re.sub(r"//[^\n]*", "", f.read())
     assert not re.search(r"__ldg\b|\.nc\b|__restrict__|ld\.global\.nc", code)
+
+
+def test_an_empty_batch_needs_no_tables():
+    """(the address of an empty tensor is NULL)"""
+    L, c = D.lib(), _cache()
+    p = _lib.PagedCache(None, None, 2, 2, 128)
+    d = D.attn_desc(0, 256, 16, 8, 0.04)
+    for idx in (None, 0x6000):
+        assert _status(L.dsa_latent_attn_paged, C.byref(d), None, C.byref(c), idx, C.byref(p), None, None, None, 0, None)[0] == "DSA_OK"
+    assert _status(L.dsa_sparse_attn_paged, C.byref(d), None, None, None, C.byref(p), None, None, None, 0, None)[0] == "DSA_OK"
+    n = D.indexer_desc(0, 256, 64, 128, 64, 8, 256, D.DSA_IDX_ROPE_Q | D.DSA_IDX_INDEPENDENT_ROWS)
+    assert _status(L.dsa_indexer_topk_paged, C.byref(n), None, None, None, None, C.byref(p), None, 0, None, None, None, 0, None)[0] == "DSA_OK"
+    d = D.attn_desc(2, 256, 16, 8, 0.04)
+    assert _status(L.dsa_latent_attn_paged, C.byref(d), 0x1000, C.byref(c), None, C.byref(p), 0x2000, None, WS, 1 << 40, None)[0] == "DSA_ERR_ARG"
+    with pytest.raises(ValueError, match="must be set"):
+        _lib._paged_args(p, 1)
+    _lib._paged_args(p, 0)
