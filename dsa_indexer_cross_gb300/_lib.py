@@ -88,6 +88,7 @@ class LatentCache(C.Structure):
     """dsa_latent_cache (see latent_cache)."""
     _fields_ = [("latent", C.c_void_p), ("scale", C.c_void_p), ("rope", C.c_void_p), ("n_rows", C.c_int32),
                 ("format", C.c_int32)]
+    device = None       # ordinal of the tensors' device, where latent_cache made it
 
 
 class CacheWriteDesc(C.Structure):
@@ -219,17 +220,35 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _arg(t: torch.Tensor, dtype, numel: int, name: str) -> int:
-    """_want and _ptr in one, for the calls of a few microseconds."""
-    if t.dtype is dtype and t.numel() >= numel and t.is_cuda and t.is_contiguous():
+def _arg(t: torch.Tensor, dtype, numel: int, name: str, dev: int) -> int:
+    """_want and _ptr in one, on device `dev`, for the calls of a few microseconds."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
         return t.data_ptr()
     _want(t, dtype, numel, name)
-    return _ptr(t)
+    _ptr(t)
+    raise ValueError(f"{name} is on {t.device}, but the call's other tensors are on cuda:{dev}")
 
 
-def _on_current_device(t: torch.Tensor) -> None:
-    if t.get_device() != _device():
-        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{_device()}")
+def _current_device(t: torch.Tensor, name: str, *handles) -> int:
+    """The current device, which holds `t` and the tensors of the cache and page-table handles."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: tensors passed to libdsa must be CUDA tensors (device memory)")
+    if dev != _device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_device()}")
+    for h in handles:
+        if h.device is not None and h.device != dev:
+            raise ValueError(f"{name} is on {t.device}, but the {type(h).__name__}'s tensors are on cuda:{h.device}")
+    return dev
+
+
+def _one_device(*tensors) -> int:
+    """The ordinal of the device that holds every tensor of a handle."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"a handle's tensors must be on one device, not {tensors[0].device} and {t.device}")
+    return dev
 
 
 def _u8(types: Sequence[int]):
@@ -479,14 +498,25 @@ class PagedCache(C.Structure):
     block_table[t, j // page_rows] * page_rows + j % page_rows, valid for j < seq_len[t]."""
     _fields_ = [("block_table", C.c_void_p), ("seq_len", C.c_void_p), ("max_pages", C.c_int32),
                 ("n_pages", C.c_int32), ("page_rows", C.c_int32)]
+    rows = device = None       # rows that both tables have, their device's ordinal, where paged_cache made it
 
 
 def paged_cache(block_table: torch.Tensor, seq_len: torch.Tensor, n_pages: int) -> PagedCache:
-    """block_table: int32 [n_q, max_pages] device tensor; seq_len: int32 [n_q] (kept alive by the caller)."""
-    return PagedCache(_ptr(block_table), _ptr(seq_len), block_table.shape[1], n_pages, DSA_PAGE_ROWS)
+    """block_table: int32 [n_q, max_pages] device tensor; seq_len: int32 [n_q] (kept alive by the caller).
+    Calls of at most as many rows as the shorter of the two has."""
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: expected [rows, max_pages], got {block_table.dim()} dims")
+    _want(block_table, torch.int32, 0, "block_table")
+    _want(seq_len, torch.int32, 0, "seq_len")
+    pages = PagedCache(_ptr(block_table), _ptr(seq_len), block_table.shape[1], n_pages, DSA_PAGE_ROWS)
+    pages.rows = min(block_table.shape[0], seq_len.numel())
+    pages.device = _one_device(block_table, seq_len)
+    return pages
 
 
 def _paged_args(pages: PagedCache, rows: int) -> None:
+    if pages.rows is not None and rows > pages.rows:
+        raise ValueError(f"paged cache: a call of {rows} rows, block_table and seq_len have {pages.rows}")
     if rows and not (pages.block_table and pages.seq_len):      # (an empty tensor has no address)
         raise ValueError("paged cache: block_table and seq_len must be set")
 
@@ -568,10 +598,10 @@ def rope_desc(x: torch.Tensor, out: torch.Tensor, flags: int = 0) -> RopeDesc:
                     os_[0], os_[1], flags)
 
 
-def _rope_view(t: torch.Tensor, dt, shape: tuple, token: int, head: int, name: str) -> int:
-    if t.dtype is not dt or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA {dt} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
+def _rope_view(t: torch.Tensor, dt, shape: tuple, token: int, head: int, name: str, dev: int) -> int:
+    if t.dtype is not dt or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a {dt} tensor of shape {shape} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
     if t.stride() != (token, head, 1) and _heads_view(t, name) != (token, head):
         raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's {(token, head)}")
     return t.data_ptr()
@@ -582,14 +612,15 @@ def dsa_rope_apply(desc: RopeDesc, x, pos, rope_cs, out, ws=None, stream=None) -
     rope_dim] views as the descriptor was made for."""
     n, r = desc.n_tokens, desc.rope_dim
     dt, shape = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16, (n, desc.n_heads, r)
-    px = _rope_view(x, dt, shape, desc.x_token_stride, desc.x_head_stride, "x")
-    po = _rope_view(out, dt, shape, desc.out_token_stride, desc.out_head_stride, "out")
-    _on_current_device(out)
+    dev = _current_device(out, "out")
+    px = _rope_view(x, dt, shape, desc.x_token_stride, desc.x_head_stride, "x", dev)
+    po = _rope_view(out, dt, shape, desc.out_token_stride, desc.out_head_stride, "out", dev)
     n_pos = _rope_rows(rope_cs, r)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=out.device)
-    st = (_lib or lib()).dsa_rope_apply(desc, px, _arg(pos, torch.int32, n, "pos"), _ptr(rope_cs), n_pos, po,
-                                        _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+    st = (_lib or lib()).dsa_rope_apply(desc, px, _arg(pos, torch.int32, n, "pos", dev),
+                                        _arg(rope_cs, torch.float32, 0, "rope_cs", dev), n_pos, po,
+                                        _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
         _check(st)
     return ws
@@ -614,14 +645,18 @@ def latent_cache(latent: torch.Tensor, scale: Optional[torch.Tensor] = None,
     if scale is None and rope is None:
         if latent.dtype != torch.bfloat16 or latent.shape != (n, 576):
             raise ValueError(f"latent: expected bf16 [n_rows, 576], got {latent.dtype} {tuple(latent.shape)}")
-        return LatentCache(_ptr(latent), None, None, n, DSA_CACHE_BF16)
+        cache = LatentCache(_ptr(latent), None, None, n, DSA_CACHE_BF16)
+        cache.device = latent.get_device()
+        return cache
     if latent.dtype not in (torch.uint8, torch.float8_e4m3fn) or latent.shape != (n, 512):
         raise ValueError(f"latent: expected e4m3 codes [n_rows, 512], got {latent.dtype} {tuple(latent.shape)}")
     if scale is None or scale.dtype != torch.uint8 or scale.shape != (n, 4):
         raise ValueError("scale: expected uint8 [n_rows, 4]")
     if rope is None or rope.dtype != torch.bfloat16 or rope.shape != (n, 64):
         raise ValueError("rope: expected bf16 [n_rows, 64]")
-    return LatentCache(_ptr(latent), _ptr(scale), _ptr(rope), n, DSA_CACHE_FP8)
+    cache = LatentCache(_ptr(latent), _ptr(scale), _ptr(rope), n, DSA_CACHE_FP8)
+    cache.device = _one_device(latent, scale, rope)
+    return cache
 
 
 def cache_write_desc(kv: torch.Tensor, flags: int = 0) -> CacheWriteDesc:
@@ -635,19 +670,19 @@ def dsa_latent_cache_write(desc: CacheWriteDesc, kv, slot, pos, rope_cs, cache: 
                            stream=None) -> torch.Tensor:
     """Store kv's rows in cache rows slot (negative: none), turned at pos with DSA_CACHE_ROPE."""
     n = desc.n_tokens
-    if kv.dtype is not torch.bfloat16 or kv.shape != (n, 576) or not kv.is_cuda or kv.stride(1) != 1:
-        raise ValueError(f"kv: expected a CUDA bf16 [{n}, 576] view with contiguous rows")
+    if kv.dtype is not torch.bfloat16 or kv.shape != (n, 576) or kv.stride(1) != 1:
+        raise ValueError(f"kv: expected a bf16 [{n}, 576] view with contiguous rows")
     if n > 1 and kv.stride(0) != desc.kv_stride:
         raise ValueError(f"kv: token stride {kv.stride(0)} is not the descriptor's {desc.kv_stride}")
-    _on_current_device(kv)
+    dev = _current_device(kv, "kv", cache)
     n_pos, p_pos, p_cs = 0, None, None
     if desc.flags & DSA_CACHE_ROPE:
-        p_pos = _arg(pos, torch.int32, n, "pos")
-        n_pos, p_cs = _rope_rows(rope_cs, 64), _ptr(rope_cs)
+        p_pos = _arg(pos, torch.int32, n, "pos", dev)
+        n_pos, p_cs = _rope_rows(rope_cs, 64), _arg(rope_cs, torch.float32, 0, "rope_cs", dev)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=kv.device)
-    st = (_lib or lib()).dsa_latent_cache_write(desc, kv.data_ptr(), _arg(slot, torch.int32, n, "slot"), p_pos, p_cs,
-                                                n_pos, cache, _arg(ws, torch.uint8, 0, "ws"), ws.numel(),
+    st = (_lib or lib()).dsa_latent_cache_write(desc, kv.data_ptr(), _arg(slot, torch.int32, n, "slot", dev), p_pos,
+                                                p_cs, n_pos, cache, _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(),
                                                 _stream(stream))
     if st:
         _check(st)
@@ -661,12 +696,13 @@ def dsa_latent_cache_read(cache: LatentCache, pages: PagedCache, n_seq: int, row
     s = kv_out.shape
     if len(s) != 2 or s[1] != 576:
         raise ValueError(f"kv_out: expected bf16 [rows, 576], got {kv_out.dtype} {tuple(s)}")
-    p_out = _arg(kv_out, torch.bfloat16, 0, "kv_out")
-    _on_current_device(kv_out)
+    dev = _current_device(kv_out, "kv_out", cache, pages)
+    p_out = _arg(kv_out, torch.bfloat16, 0, "kv_out", dev)
     if ws is None:
         ws = torch.empty(256, dtype=torch.uint8, device=kv_out.device)
-    st = (_lib or lib()).dsa_latent_cache_read(cache, pages, n_seq, _arg(row_start, torch.int32, n_seq, "row_start"),
-                                               p_out, s[0], _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+    st = (_lib or lib()).dsa_latent_cache_read(cache, pages, n_seq,
+                                               _arg(row_start, torch.int32, n_seq, "row_start", dev), p_out, s[0],
+                                               _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
         _check(st)
     return ws
@@ -683,15 +719,15 @@ def dsa_latent_attn_paged(desc: AttnDesc, q, cache: LatentCache, idx, pages: Pag
     """Latent attention of row t over its sequence's cached keys: all of them (idx None) or the
     selected ones."""
     n = desc.n_q * desc.n_heads
-    p_q, p_out = _arg(q, torch.bfloat16, n * desc.d_qk, "q"), _arg(out, torch.bfloat16, n * desc.d_v, "out")
-    p_idx = None if idx is None else _arg(idx, torch.int32, desc.n_q * desc.topk, "idx")
-    p_lse = None if lse is None else _arg(lse, torch.float32, n, "lse")
-    _on_current_device(q)
+    dev = _current_device(q, "q", cache, pages)
+    p_q, p_out = _arg(q, torch.bfloat16, n * desc.d_qk, "q", dev), _arg(out, torch.bfloat16, n * desc.d_v, "out", dev)
+    p_idx = None if idx is None else _arg(idx, torch.int32, desc.n_q * desc.topk, "idx", dev)
+    p_lse = None if lse is None else _arg(lse, torch.float32, n, "lse", dev)
     _paged_args(pages, desc.n_q)
     if ws is None:
         ws = torch.empty(dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
     st = (_lib or lib()).dsa_latent_attn_paged(desc, p_q, cache, p_idx, pages, p_out, p_lse,
-                                               _arg(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+                                               _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
         _check(st)
     return ws

@@ -296,3 +296,72 @@ def test_an_empty_batch_needs_no_tables():
     with pytest.raises(ValueError, match="must be set"):
         _lib._paged_args(p, 1)
     _lib._paged_args(p, 0)
+
+
+class _Placed:
+    """As much of a tensor as the binding looks at, on a device of choice."""
+
+    def __init__(self, t, dev):
+        self.t, self.dev, self.is_cuda, self.dtype, self.device = t, dev, True, t.dtype, f"cuda:{dev}"
+
+    def get_device(self):
+        return self.dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_page_tables_are_checked_before_a_kernel_reads_them():
+    z = lambda dt, *s: _Placed(torch.zeros(s, dtype=dt), 0)  # noqa: E731
+    i32 = torch.int32
+    for bt, ln in ((z(torch.int64, 3, 4), z(i32, 3)), (z(i32, 3, 4), z(torch.int64, 3)), (z(i32, 12), z(i32, 3))):
+        with pytest.raises(ValueError, match="block_table|seq_len"):
+            D.paged_cache(bt, ln, 9)
+    with pytest.raises(ValueError, match="CUDA"):
+        D.paged_cache(torch.zeros((3, 4), dtype=i32), torch.zeros(3, dtype=i32), 9)
+    with pytest.raises(ValueError, match="one device"):
+        D.paged_cache(z(i32, 3, 4), _Placed(torch.zeros(3, dtype=i32), 1), 9)
+    for n_table, n_len in ((3, 5), (5, 3)):
+        pages = D.paged_cache(z(i32, n_table, 4), z(i32, n_len), 9)
+        assert (pages.rows, pages.device, pages.max_pages) == (3, 0, 4)
+        _lib._paged_args(pages, 3)
+        with pytest.raises(ValueError, match="a call of 4 rows"):
+            _lib._paged_args(pages, 4)
+    # a handle made by hand says nothing of its rows
+    _lib._paged_args(_lib.PagedCache(0x4000, 0x5000, 2, 2, 128), 1 << 20)
+
+
+def test_every_tensor_of_a_call_is_on_the_current_device(monkeypatch):
+    bf, i32, u8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+    monkeypatch.setattr(_lib, "_device", lambda: 0)
+    at = lambda t, here: _Placed(t, 0 if here else 1)  # noqa: E731
+    tab, ws = torch.zeros((4, 32, 2)), torch.zeros(256, dtype=u8)
+    attn = dict(q=torch.zeros((2, 16, 576), dtype=bf), rows=torch.zeros((256, 576), dtype=bf), idx=torch.zeros((2, 8), dtype=i32),
+                bt=torch.zeros((2, 2), dtype=i32), ln=torch.zeros(2, dtype=i32), out=torch.zeros((2, 16, 512), dtype=bf),
+                lse=torch.zeros((2, 16)), ws=ws)
+    read = dict(rows=attn["rows"], bt=attn["bt"], ln=attn["ln"], start=torch.zeros(2, dtype=i32), out=torch.zeros((9, 576), dtype=bf), ws=ws)
+    write = dict(kv=torch.zeros((2, 576), dtype=bf), slot=torch.zeros(2, dtype=i32), pos=torch.zeros(2, dtype=i32), tab=tab,
+                 codes=torch.zeros((256, 512), dtype=u8), scale=torch.zeros((256, 4), dtype=u8), rope=torch.zeros((256, 64), dtype=bf), ws=ws)
+    rope = dict(x=torch.zeros((2, 3, 64)), pos=write["pos"], tab=tab, out=torch.zeros((2, 3, 64)), ws=ws)
+
+    def call_attn(q, rows, idx, bt, ln, out, lse, ws):
+        D.dsa_latent_attn_paged(D.attn_desc(2, 256, 16, 8, 0.04), q, D.latent_cache(rows), idx, D.paged_cache(bt, ln, 2), out, lse, ws=ws)
+
+    def call_read(rows, bt, ln, start, out, ws):
+        D.dsa_latent_cache_read(D.latent_cache(rows), D.paged_cache(bt, ln, 2), 2, start, out, ws=ws)
+
+    def call_write(kv, slot, pos, tab, codes, scale, rope, ws):
+        D.dsa_latent_cache_write(D.cache_write_desc(kv, D.DSA_CACHE_ROPE), kv, slot, pos, tab, D.latent_cache(codes, scale, rope), ws=ws)
+
+    def call_rope(x, pos, tab, out, ws):
+        D.dsa_rope_apply(D.rope_desc(x, out), x, pos, tab, out, ws=ws)
+    reached = []
+    monkeypatch.setattr(_lib, "_stream", lambda s: reached.append(1) or (_ for _ in ()).throw(StopIteration))
+    for call, tensors in ((call_attn, attn), (call_read, read), (call_write, write), (call_rope, rope)):
+        with pytest.raises((StopIteration, RuntimeError)):       # all in place: as far as the launch
+            call(**{k: at(t, True) for k, t in tensors.items()})
+        assert reached.pop()
+        for other in tensors:
+            with pytest.raises(ValueError, match="cuda:1"):
+                call(**{k: at(t, k != other) for k, t in tensors.items()})
+            assert not reached
