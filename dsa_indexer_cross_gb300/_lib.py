@@ -602,8 +602,10 @@ def _rope_view(t: torch.Tensor, dt, shape: tuple, token: int, head: int, name: s
     if t.dtype is not dt or t.shape != shape or t.get_device() != dev:
         raise ValueError(f"{name}: expected a {dt} tensor of shape {shape} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
-    if t.stride() != (token, head, 1) and _heads_view(t, name) != (token, head):
-        raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's {(token, head)}")
+    if t.stride() != (token, head, 1):
+        s = _heads_view(t, name)        # (of one token or one head, the stride is never used)
+        if (shape[0] > 1 and s[0] != token) or (shape[1] > 1 and s[1] != head):
+            raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's {(token, head)}")
     return t.data_ptr()
 
 
@@ -663,7 +665,7 @@ def cache_write_desc(kv: torch.Tensor, flags: int = 0) -> CacheWriteDesc:
     """Descriptor for storing kv, a [tokens, 576] bf16 view with contiguous rows."""
     if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != 576 or kv.stride(1) != 1:
         raise ValueError("kv: expected a bf16 [tokens, 576] view with contiguous rows")
-    return CacheWriteDesc(kv.shape[0], flags, kv.stride(0) if kv.shape[0] > 1 else max(576, kv.stride(0)))
+    return CacheWriteDesc(kv.shape[0], flags, kv.stride(0) if kv.shape[0] > 1 else 576)
 
 
 def dsa_latent_cache_write(desc: CacheWriteDesc, kv, slot, pos, rope_cs, cache: LatentCache, ws=None,

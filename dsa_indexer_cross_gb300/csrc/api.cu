@@ -869,9 +869,13 @@ dsa_status check_cache(const dsa_latent_cache* c, LatentCache* out) {
 }
 }  // namespace
 
-dsa_status dsa_rope_apply(const dsa_rope_desc* d, const void* x, const int32_t* pos, const float* rope_cs,
+dsa_status dsa_rope_apply(const dsa_rope_desc* desc, const void* x, const int32_t* pos, const float* rope_cs,
                           int32_t rope_n_pos, void* out, void* ws, size_t ws_bytes, void* stream) {
-  if (!d) return fail(DSA_ERR_ARG, "rope descriptor is NULL");
+  if (!desc) return fail(DSA_ERR_ARG, "rope descriptor is NULL");
+  dsa_rope_desc given = *desc;
+  if (given.n_tokens == 1) given.x_token_stride = given.out_token_stride = 0;      // never used, so not looked at
+  if (given.n_heads == 1) given.x_head_stride = given.out_head_stride = 0;
+  const dsa_rope_desc* d = &given;
   if (d->n_tokens < 0 || d->n_heads < 1) return fail(DSA_ERR_ARG, "n_tokens must be >= 0 and n_heads >= 1");
   if (d->rope_dim < 2 || d->rope_dim > 512 || (d->rope_dim & 1))
     return fail(DSA_ERR_ARG, "rope_dim %d must be even and within 2..512", d->rope_dim);

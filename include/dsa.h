@@ -426,7 +426,8 @@ typedef struct dsa_rope_desc {
   int32_t n_heads;
   int32_t rope_dim;          /* even, 2 .. 512                                                        */
   int32_t dtype;             /* DSA_BF16 or DSA_F32, of x and out                                     */
-  int64_t x_token_stride;    /* strides in elements, >= 0; a head's rope_dim elements are contiguous  */
+  int64_t x_token_stride;    /* strides in elements, >= 0 (of one token or one head: any, not used); a
+                                head's rope_dim elements are contiguous                               */
   int64_t x_head_stride;
   int64_t out_token_stride;
   int64_t out_head_stride;

@@ -535,3 +535,22 @@ def test_empty_batches_and_outputs_made_of_empty_tensors():
     ln[1] = 1
     ws = D.dsa_latent_cache_read(c, pages, 2, i32([0, 0]), back, ws=ws)
     assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_a_single_row_cut_from_odd_rows(fmt):
+    """One token of a tensor whose rows are not a multiple of eight elements apart, and one head of it turned
+    in place through views of different strides: what the same values in plain tensors give."""
+    buf = randn((7, 1001), gen(81))
+    kv = torch.as_strided(buf, (1, 576), (1001, 1), 8)      # 16-byte aligned
+    tab, slot, pos = D.dsa_rope_table(THETA, 64, 50).to(DEV), i32([3]), i32([17])
+    got, bits = _write(kv, slot, fmt, 1, pos, tab, D.DSA_CACHE_ROPE)
+    want, _ = _write(kv.clone(), slot, fmt, 1, pos, tab, D.DSA_CACHE_ROPE)
+    assert bits == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+    x = torch.as_strided(buf, (1, 1, 64), (1001, 3, 1), 16)
+    y = torch.as_strided(buf, (1, 1, 64), (5, 77, 1), 16)
+    ref = torch.empty((1, 1, 64), dtype=torch.bfloat16, device=DEV)
+    plain = x.clone()
+    D.dsa_rope_apply(D.rope_desc(plain, ref), plain, pos, tab, ref)
+    ws = D.dsa_rope_apply(D.rope_desc(x, y), y, pos, tab, x)
+    assert D.dsa_workspace_status(ws) == 0 and torch.equal(x, ref)

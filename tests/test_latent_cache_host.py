@@ -365,3 +365,29 @@ def test_every_tensor_of_a_call_is_on_the_current_device(monkeypatch):
             with pytest.raises(ValueError, match="cuda:1"):
                 call(**{k: at(t, k != other) for k, t in tensors.items()})
             assert not reached
+
+
+def test_strides_of_a_single_token_or_head_are_not_looked_at():
+    """Views of one row carry whatever stride they were cut with."""
+    one = torch.zeros((5, 1001), dtype=torch.bfloat16)[2:3, :576]
+    for kv, stride in ((one, 576), (one[:0], 576), (torch.zeros((1, 2000), dtype=torch.bfloat16)[:, :576], 576),
+                       (torch.zeros((2, 640), dtype=torch.bfloat16)[:, :576], 640)):
+        assert D.cache_write_desc(kv).kv_stride == stride
+    d = _rope(n_tokens=1, x_token_stride=7, out_token_stride=192)            # in place: the missing workspace is met
+    st, msg = _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x1000, None, 256, None)
+    assert st == "DSA_ERR_ARG" and "workspace" in msg
+    d = _rope(n_heads=1, x_head_stride=-3, out_head_stride=1)
+    st, msg = _status(D.lib().dsa_rope_apply, C.byref(d), 0x1000, 0x2000, 0x3000, 8, 0x1000, None, 256, None)
+    assert st == "DSA_ERR_ARG" and "workspace" in msg
+    bf, x = torch.bfloat16, torch.zeros((4, 3, 64))
+    for t, ok in ((x, True), (torch.zeros((4, 9, 64))[:, ::3], False), (torch.zeros((4, 3, 70))[..., :64], False)):
+        try:
+            _lib._rope_view(_Placed(t, 0), torch.float32, (4, 3, 64), 192, 64, "x", 0)
+            assert ok
+        except ValueError as e:
+            assert not ok and "strides" in str(e)
+    head = torch.zeros((4, 9, 64), dtype=bf)[:, 4:5]
+    _lib._rope_view(_Placed(head, 0), bf, (4, 1, 64), 576, 1234, "x", 0)
+    _lib._rope_view(_Placed(head[1:2], 0), bf, (1, 1, 64), 1, 1234, "x", 0)
+    with pytest.raises(ValueError, match="strides"):
+        _lib._rope_view(_Placed(head, 0), bf, (4, 1, 64), 64, 64, "x", 0)
