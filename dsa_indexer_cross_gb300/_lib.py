@@ -220,6 +220,19 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call, out of the memory of the stream that runs it: the allocator hands memory on
+    in the order of one stream's work, so another stream's block may be written, or given away, while this call
+    is still to use it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _arg(t: torch.Tensor, dtype, numel: int, name: str, dev: int) -> int:
     """_want and _ptr in one, on device `dev`, for the calls of a few microseconds."""
     if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
@@ -310,7 +323,7 @@ def dsa_indexer_topk(desc: IndexerDesc, q_idx, k_idx, w, q_pos, k_pos, ks, ke, r
                      ws=None, stream=None) -> torch.Tensor:
     _indexer_args(desc, q_idx, k_idx, w, q_pos, k_pos, ks, ke, rope_cs, idx_out, score_out)
     if ws is None:
-        ws = torch.empty(dsa_indexer_workspace_size(desc), dtype=torch.uint8, device=idx_out.device)
+        ws = _workspace(dsa_indexer_workspace_size(desc), idx_out.device, stream)
     n_pos = rope_cs.shape[0] if rope_cs is not None else 0
     _check(lib().dsa_indexer_topk(C.byref(desc), _ptr(q_idx), _ptr(k_idx), _ptr(w), _ptr(q_pos), _ptr(k_pos),
                                   _ptr(ks), _ptr(ke), _ptr(rope_cs), n_pos, _ptr(idx_out), _ptr(score_out),
@@ -345,7 +358,7 @@ def dsa_indexer_backward(desc: IndexerDesc, q_idx, k_idx, w, q_pos, k_pos, ks, k
                        (dw, n_q * H, "dw")):
         _want(t, f32, n, name)
     if ws is None:
-        ws = torch.empty(dsa_indexer_backward_workspace_size(desc), dtype=torch.uint8, device=dq_idx.device)
+        ws = _workspace(dsa_indexer_backward_workspace_size(desc), dq_idx.device, stream)
     n_pos = rope_cs.shape[0] if rope_cs is not None else 0
     _check(lib().dsa_indexer_backward(C.byref(desc), _ptr(q_idx), _ptr(k_idx), _ptr(w), _ptr(q_pos), _ptr(k_pos),
                                       _ptr(ks), _ptr(ke), _ptr(rope_cs), n_pos, _ptr(idx), _ptr(d_score),
@@ -373,7 +386,7 @@ def dsa_sparse_attn(desc: AttnDesc, q, kv, idx, ks, out, lse=None, ws=None, stre
         if t is not None:
             _want(t, dt, n, name)
     if ws is None:
-        ws = torch.empty(dsa_sparse_attn_workspace_size(desc), dtype=torch.uint8, device=out.device)
+        ws = _workspace(dsa_sparse_attn_workspace_size(desc), out.device, stream)
     _check(lib().dsa_sparse_attn(C.byref(desc), _ptr(q), _ptr(kv), _ptr(idx), _ptr(ks), _ptr(out), _ptr(lse),
                                  _ptr(ws), ws.numel(), _stream(stream)))
     return ws
@@ -437,7 +450,7 @@ def indexshare_layers_forward(idesc: IndexerDesc, adesc: AttnDesc, indexer_types
         io[l] = LayerIO(_ptr(L.get("q_idx")), _ptr(L.get("k_idx")), _ptr(L.get("w")), _ptr(L["q"]), _ptr(L["kv"]),
                         _ptr(L["out"]), _ptr(L.get("lse")))
     if ws is None:
-        ws = torch.empty(dsa_layers_workspace_size(idesc, adesc), dtype=torch.uint8, device=layers[0]["q"].device)
+        ws = _workspace(dsa_layers_workspace_size(idesc, adesc), layers[0]["q"].device, stream)
     n_pos = rope_cs.shape[0] if rope_cs is not None else 0
     _check(lib().indexshare_layers_forward(C.byref(idesc), C.byref(adesc), len(types), _u8(types), io, _ptr(ks),
                                            _ptr(ke), _ptr(q_pos), _ptr(k_pos), _ptr(rope_cs), n_pos, cache.handle,
@@ -461,7 +474,7 @@ def dsa_sparse_attn_backward(desc: AttnDesc, q, kv, idx, ks, out, lse, d_out, dq
                            (dkv, f32, n_kv * desc.d_qk, "dkv")):
         _want(t, dt, n, name)
     if ws is None:
-        ws = torch.empty(dsa_sparse_attn_backward_workspace_size(desc), dtype=torch.uint8, device=q.device)
+        ws = _workspace(dsa_sparse_attn_backward_workspace_size(desc), q.device, stream)
     _check(lib().dsa_sparse_attn_backward(C.byref(desc), _ptr(q), _ptr(kv), _ptr(idx), _ptr(ks), _ptr(out), _ptr(lse),
                                           _ptr(d_out), _ptr(dq), _ptr(dkv), _ptr(ws), ws.numel(), _stream(stream)))
     return ws
@@ -483,7 +496,7 @@ def dsa_indexer_projections(desc: "ProjDesc", x, q_latent, wq_b, wk, k_norm_w, k
                            (k_idx, bf, T * d, "k_idx"), (w, f32, T * H, "w")):
         _want(t, dt, n, name)
     if ws is None:
-        ws = torch.zeros(256, dtype=torch.uint8, device=x.device)
+        ws = _workspace(256, x.device, stream)
     _check(lib().dsa_indexer_projections(C.byref(desc), _ptr(x), _ptr(q_latent), _ptr(wq_b), _ptr(wk), _ptr(k_norm_w),
                                          _ptr(k_norm_b), _ptr(weights_proj), _ptr(q_idx), _ptr(k_idx), _ptr(w),
                                          _ptr(ws), ws.numel(), _stream(stream)))
@@ -532,7 +545,7 @@ def dsa_indexer_topk_paged(desc: IndexerDesc, q_idx, k_cache, w, q_pos, pages: P
             _want(t, dt, n, name)
     _paged_args(pages, n_q)
     if ws is None:
-        ws = torch.empty(dsa_indexer_workspace_size(desc), dtype=torch.uint8, device=q_idx.device)
+        ws = _workspace(dsa_indexer_workspace_size(desc), q_idx.device, stream)
     n_pos = rope_cs.shape[0] if rope_cs is not None else 0
     _check(lib().dsa_indexer_topk_paged(C.byref(desc), _ptr(q_idx), _ptr(k_cache), _ptr(w), _ptr(q_pos),
                                         C.byref(pages), _ptr(rope_cs), n_pos, _ptr(idx_out), _ptr(score_out),
@@ -549,7 +562,7 @@ def dsa_sparse_attn_paged(desc: AttnDesc, q, kv_cache, idx, pages: PagedCache, o
             _want(t, dt, n, name)
     _paged_args(pages, n_q)
     if ws is None:
-        ws = torch.empty(dsa_sparse_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
+        ws = _workspace(dsa_sparse_attn_workspace_size(desc), q.device, stream)
     _check(lib().dsa_sparse_attn_paged(C.byref(desc), _ptr(q), _ptr(kv_cache), _ptr(idx), C.byref(pages), _ptr(out),
                                        _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
     return ws
@@ -619,7 +632,7 @@ def dsa_rope_apply(desc: RopeDesc, x, pos, rope_cs, out, ws=None, stream=None) -
     po = _rope_view(out, dt, shape, desc.out_token_stride, desc.out_head_stride, "out", dev)
     n_pos = _rope_rows(rope_cs, r)
     if ws is None:
-        ws = torch.empty(256, dtype=torch.uint8, device=out.device)
+        ws = _workspace(256, out.device, stream)
     st = (_lib or lib()).dsa_rope_apply(desc, px, _arg(pos, torch.int32, n, "pos", dev),
                                         _arg(rope_cs, torch.float32, 0, "rope_cs", dev), n_pos, po,
                                         _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
@@ -682,7 +695,7 @@ def dsa_latent_cache_write(desc: CacheWriteDesc, kv, slot, pos, rope_cs, cache: 
         p_pos = _arg(pos, torch.int32, n, "pos", dev)
         n_pos, p_cs = _rope_rows(rope_cs, 64), _arg(rope_cs, torch.float32, 0, "rope_cs", dev)
     if ws is None:
-        ws = torch.empty(256, dtype=torch.uint8, device=kv.device)
+        ws = _workspace(256, kv.device, stream)
     st = (_lib or lib()).dsa_latent_cache_write(desc, kv.data_ptr(), _arg(slot, torch.int32, n, "slot", dev), p_pos,
                                                 p_cs, n_pos, cache, _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(),
                                                 _stream(stream))
@@ -701,7 +714,7 @@ def dsa_latent_cache_read(cache: LatentCache, pages: PagedCache, n_seq: int, row
     dev = _current_device(kv_out, "kv_out", cache, pages)
     p_out = _arg(kv_out, torch.bfloat16, 0, "kv_out", dev)
     if ws is None:
-        ws = torch.empty(256, dtype=torch.uint8, device=kv_out.device)
+        ws = _workspace(256, kv_out.device, stream)
     st = (_lib or lib()).dsa_latent_cache_read(cache, pages, n_seq,
                                                _arg(row_start, torch.int32, n_seq, "row_start", dev), p_out, s[0],
                                                _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
@@ -727,7 +740,7 @@ def dsa_latent_attn_paged(desc: AttnDesc, q, cache: LatentCache, idx, pages: Pag
     p_lse = None if lse is None else _arg(lse, torch.float32, n, "lse", dev)
     _paged_args(pages, desc.n_q)
     if ws is None:
-        ws = torch.empty(dsa_latent_attn_workspace_size(desc), dtype=torch.uint8, device=q.device)
+        ws = _workspace(dsa_latent_attn_workspace_size(desc), q.device, stream)
     st = (_lib or lib()).dsa_latent_attn_paged(desc, p_q, cache, p_idx, pages, p_out, p_lse,
                                                _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
@@ -755,7 +768,7 @@ def dsa_mtp_indexshare_step(idesc: IndexerDesc, adesc: AttnDesc, step: int, laye
     io = LayerIO(_ptr(L.get("q_idx")), _ptr(L.get("k_idx")), _ptr(L.get("w")), _ptr(L["q"]), _ptr(L["kv"]),
                  _ptr(L["out"]), _ptr(L.get("lse")))
     if ws is None:
-        ws = torch.empty(dsa_layers_workspace_size(idesc, adesc), dtype=torch.uint8, device=L["q"].device)
+        ws = _workspace(dsa_layers_workspace_size(idesc, adesc), L["q"].device, stream)
     n_pos = rope_cs.shape[0] if rope_cs is not None else 0
     _check(lib().dsa_mtp_indexshare_step(C.byref(idesc), C.byref(adesc), int(step), C.byref(io), _ptr(ks), _ptr(ke),
                                          _ptr(q_pos), _ptr(k_pos), _ptr(rope_cs), n_pos, _ptr(mtp_idx), _ptr(ws),

@@ -554,3 +554,40 @@ def test_a_single_row_cut_from_odd_rows(fmt):
     D.dsa_rope_apply(D.rope_desc(plain, ref), plain, pos, tab, ref)
     ws = D.dsa_rope_apply(D.rope_desc(x, y), y, pos, tab, x)
     assert D.dsa_workspace_status(ws) == 0 and torch.equal(x, ref)
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "default"])
+def test_a_workspace_made_for_a_call_on_another_stream(how):
+    """It comes from that stream's memory: what is freed on the current stream, whose work may still use it, is
+    not taken, and the workspace, freed before its call has run, is not given to the current stream."""
+    s = torch.cuda.Stream()
+    given = {"stream": s, "handle": s.cuda_stream, "default": 0}[how]
+    here = torch.cuda.Stream()                # the current stream
+    g = gen(83)
+    x, out = torch.randn((4, 2, 64), generator=g, device=DEV), torch.zeros((4, 2, 64), device=DEV)
+    tab, pos = D.dsa_rope_table(THETA, 64, 10).to(DEV), i32([0, 1, 2, 3])
+    cache = D.latent_cache(torch.zeros((P, 576), dtype=torch.bfloat16, device=DEV))
+    kv, slot = randn((4, 576), g), i32([5, 6, 7, 8])
+    back = torch.zeros((P, 576), dtype=torch.bfloat16, device=DEV)
+    bt, ln, start = i32([[0]]), i32([9]), i32([0])
+    pages = D.paged_cache(bt, ln, 1)
+    q, o = randn((1, 16, 576), g), torch.zeros((1, 16, 512), dtype=torch.bfloat16, device=DEV)
+    calls = [lambda: D.dsa_rope_apply(D.rope_desc(x, out), x, pos, tab, out, stream=given),
+             lambda: D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, slot, None, None, cache, stream=given),
+             lambda: D.dsa_latent_cache_read(cache, pages, 1, start, back, stream=given),
+             lambda: D.dsa_latent_attn_paged(D.attn_desc(1, P, 16, 0, 0.04), q, cache, None, pages, o, stream=given)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(here):
+        for call in calls:
+            freed = [torch.empty(256, dtype=torch.uint8, device=DEV) for _ in range(4)]
+            taken = {t.data_ptr() for t in freed}
+            del freed
+            ws = call()
+            assert ws.data_ptr() not in taken
+            size, at = ws.numel(), ws.data_ptr()
+            del ws
+            new = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(8)]
+            assert at not in {t.data_ptr() for t in new}
+            del new
+    torch.cuda.synchronize()
+    assert torch.equal(back[5:9], kv)
