@@ -517,7 +517,9 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
  * values; softmax weights are rounded to bf16 for the second product and divided by their own sum,
  * lse sums the unrounded ones (selected keys of a bf16 cache: the results are dsa_sparse_attn_paged's,
  * whose lse sums the rounded weights, within 2^-8 of it).  A row without keys gives o = 0 and
- * lse = -inf.  Rows of a page past the sequence's end are never used, whatever they hold.  A page
+ * lse = -inf.  A NaN or +inf score makes its head's o and lse NaN; a score of -inf weighs zero (a head
+ * without any other: o = 0, lse = -inf), and a value only shows under it where zero times it is NaN.
+ * Rows of a page past the sequence's end are never used, whatever they hold.  A page
  * outside the cache, or (idx) an offset >= seq_len[t], is skipped and flagged; a length outside
  * [0, max_pages * page_rows] is cut to it and flagged (DSA_ERR_DEVICE).  A key listed twice counts
  * twice.  Results do not depend on the order in which CTAs run.

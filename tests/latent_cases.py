@@ -129,3 +129,29 @@ def check_rows(out, lse, q, rows_kv, tau=TAU, heads=None):
         if l64 is not None:
             lt = eps[:, 0] + 2.0 ** -20 * np.maximum(1.0, np.abs(l))
             assert np.all(np.abs(l64[t] - l) <= lt), (t, float(np.max(np.abs(l64[t] - l) / lt)))
+
+
+def check_exceptional(out, lse, q, rows_kv, tau=TAU):
+    """As check_rows, where rows may hold infinities and NaN, and never passing a NaN that the formula does
+    not give.  A head with a NaN or +inf score is NaN throughout.  A score of -inf weighs zero, so its row only
+    shows in the dims where zero times its value is NaN; everywhere else the result is finite and within
+    check_rows' bound over the other keys (without any: zeros, and a log-sum-exp of -inf)."""
+    u = 2.0 ** -8
+    q64, o64, l64 = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for t, kv in enumerate(rows_kv):
+        with np.errstate(invalid="ignore"):
+            s = tau * (q64[t] @ kv.T)
+            nan_dims = np.isnan(kv[:, :512] * 0.0)
+        for h in range(q.shape[1]):
+            got, l = o64[t, h], l64[t, h]
+            if np.any(np.isnan(s[h]) | (s[h] == np.inf)):
+                assert np.all(np.isnan(got)) and np.isnan(l), (t, h)
+                continue
+            used = s[h] > -np.inf
+            shown = nan_dims[~used].any(axis=0)
+            assert np.array_equal(np.isnan(got), shown), (t, h)
+            o, ref, A, B = (x[0] for x in LO.latent_attn_row(q64[t, h:h + 1], kv[used], tau))
+            eps = (576 * 2.0 ** -23 + 2.0 ** -20) * max(B, 1.0)
+            tol = u * np.abs(o) + (u * (1 + 2 * u) + 2 * eps + 2.0 ** -13) * (A + np.abs(o))
+            assert np.all(np.abs(got - o)[~shown] <= tol[~shown]), (t, h)
+            assert l == ref if not used.any() else abs(l - ref) <= eps + 2.0 ** -20 * max(1.0, abs(ref)), (t, h)

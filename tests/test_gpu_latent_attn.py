@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import dsa_indexer_cross_gb300 as D
-from latent_cases import DEV, P, TAU, Paged, attend, check_rows, gen, i32, randn
+from latent_cases import DEV, P, TAU, Paged, attend, check_exceptional, check_rows, gen, i32, randn
 from oracle import latent_oracle as LO
 
 pytestmark = pytest.mark.gpu
@@ -677,3 +677,88 @@ def test_attention_right_behind_the_writing_of_its_rows(H, fmt, sel):
             check()
     torch.cuda.synchronize()
     assert all(D.dsa_workspace_status(w) == 0 for w in (ws, w1, w2))
+
+
+@pytest.mark.parametrize("H,fmt,sel", [(1, "bf16", False), (16, "bf16", False), (64, "bf16", False), (128, "bf16", False),
+                                       (16, "fp8", False), (64, "fp8", False), (100, "fp8", False), (16, "fp8", True),
+                                       (40, "fp8", True), (128, "fp8", True)])
+def test_infinities_and_nan_in_used_rows(H, fmt, sel):
+    """Scores of plus and minus infinity (an infinite rotary dim: the query's sign decides), a NaN in the
+    rotary and in the latent dims, infinite values (fp8: a group stored as NaN), in the first tile, in the last
+    and in the middle of a split row, as the only key, and (selected) in a row that is not selected."""
+    lens = [100, 700, 5000, 300, 1, 1, 9000, 64, 65, 2000]
+    pc = Paged(lens, fmt, seed=H)
+    q = randn((len(lens), H, 576), gen(H + 1))
+    inf, nan = float("inf"), float("nan")
+
+    def poke(t, j, dim, value):
+        if fmt == "bf16":
+            pc.rows[pc.phys[t][j], dim] = value
+            pc.kv[t][j, dim] = value
+        elif dim >= 512:
+            pc.rope[pc.phys[t][j], dim - 512] = value
+        else:
+            pc.codes[pc.phys[t][j], dim // 128 * 128:dim // 128 * 128 + 128] = 0x7F
+            pc.scale[pc.phys[t][j], dim // 128] = 255
+    pokes = [(0, 5, 520, inf), (1, 300, 575, -inf), (1, 699, 512, inf), (2, 4000, 530, nan), (3, 299, 17, inf),
+             (4, 0, 540, inf), (5, 0, 100, nan), (6, 8999, 515, inf), (8, 64, 513, -inf), (9, 1000, 300, nan)]
+    for p in pokes:
+        poke(*p)
+    idx = None
+    rows = [pc.stored(t) for t in range(len(lens))]
+    if sel:
+        idx = _selection(lens, 200, H)
+        for t, j, _, _ in pokes:
+            if t == 9:
+                idx[t, idx[t] == j] = 999                      # not selected: its NaN stays out
+            elif not np.any(idx[t] == j):
+                idx[t, 7] = j
+        rows = [r[i[i >= 0]] for r, i in zip(rows, idx)]
+        assert np.all(np.isfinite(rows[9]))
+        idx = i32(idx)
+    out, lse, ws = attend(pc, q, idx)
+    assert D.dsa_workspace_status(ws) == 0
+    check_exceptional(out, lse, q, rows)
+
+
+@pytest.mark.parametrize("H,fmt", [(16, "bf16"), (33, "fp8"), (64, "bf16"), (100, "bf16"), (128, "fp8")])
+def test_nothing_of_an_unused_row_shows(H, fmt):
+    """Every cache row past a sequence's end, and every row of a page outside the cache's used ones, is NaN:
+    all results are finite."""
+    pc = Paged(EDGES + [4000, 20000], fmt, seed=H + 3)
+    q = randn((len(pc.lens), H, 576), gen(H + 4))
+    cases = [None] + ([i32(_selection(pc.lens, 300, H, holes=True))] if fmt == "fp8" else [])
+    for idx in cases:
+        out, lse, ws = attend(pc, q, idx)
+        assert D.dsa_workspace_status(ws) == 0
+        assert torch.all(torch.isfinite(out)) and not torch.any(torch.isnan(lse))
+        rows = [pc.stored(t) for t in range(len(pc.lens))]
+        if idx is not None:
+            rows = [r[i[i >= 0]] for r, i in zip(rows, idx.cpu().numpy())]
+        check_exceptional(out, lse, q, rows)
+
+
+@pytest.mark.parametrize("H,fmt", [(16, "bf16"), (16, "fp8"), (128, "bf16"), (128, "fp8")])
+def test_nothing_shows_in_place_of_a_page_outside_the_cache(H, fmt):
+    """The skipped keys count as absent even where the page that is read in their place holds NaN."""
+    pc = Paged([500, 130], fmt, seed=71)
+    spare = sorted(set(range(pc.n_pages)) - set(pc.bt[pc.bt >= 0].tolist()))
+    bt = pc.bt.copy()
+    if 0 not in spare:                            # page 0, unused, becomes one of NaN
+        bt[pc.bt == 0] = spare[0]
+        old, new = slice(0, P), slice(spare[0] * P, spare[0] * P + P)
+        for b in ((pc.rows,) if fmt == "bf16" else (pc.codes, pc.scale, pc.rope)):
+            kept = b[new].clone()
+            b[new] = b[old]
+            b[old] = kept
+        for t, L in enumerate(pc.lens):
+            j = np.arange(L)
+            pc.phys[t] = torch.as_tensor(bt[t, j // P].astype(np.int64) * P + j % P, device=DEV)
+    rows = [pc.stored(t) for t in range(2)]
+    bt[0, 2], bt[1, 1] = pc.n_pages + 3, -9
+    bt_d = i32(bt)
+    pc.pages = D.paged_cache(bt_d, pc.len_d, pc.n_pages)
+    q = randn((2, H, 576), gen(72))
+    out, lse, ws = attend(pc, q)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    check_exceptional(out, lse, q, [np.concatenate([rows[0][:256], rows[0][384:]]), rows[1][:128]])
