@@ -221,7 +221,7 @@ def roofline_numbers(w, geo):
 # launch is too long for a full-set capture) and is scaled by the 4096 / 608 units: each
 # group streams the same chunks, so the traffic grows with the number of groups.
 MEASURED_TRAFFIC = {
-    ("indexer", "chunk_1m"): ((1.030887e9 + 0.616833e9) * 4096 / 608, ("indexer.cu", "api.cu"), "bb0d03ae38582e47",
+    ("indexer", "chunk_1m"): ((1.032803e9 + 0.618241e9) * 4096 / 608, ("indexer.cu", "api.cu"), "729cbe79662d58bf",
                               "profiles/indexer_chunk_1m.md (608-query slice, scaled by 4096/608)"),
 }
 

@@ -26,10 +26,12 @@
 // zeros before the products (an uninitialised page may hold NaN, which a zero weight does not cancel).
 //
 // What bounds it (64 rows of 8K to 131K keys, 4.8M in all; a copy moves 6.78 TB/s here).  bf16 reads
-// 5.6 GB: 803 us at 16 and 32 heads, 860 at 64 (6.9 and 6.5 TB/s): HBM.  fp8 reads 3.1 GB: 727 us at 16
-// heads, 800 at 32, 1036 at 64 (4.3, 3.9, 3.0 TB/s): the way of a tile from codes through registers and
-// shared memory to its products, whose operand reads and the converters' writes share the SM's
-// shared-memory bandwidth.  Selected keys (2048 of each row): 41 us at 16 heads, 63 at 64: the gathers'
+// 5.6 GB: 797 us at 16 heads, 803 at 32, 875 at 64 (7.0, 6.9 and 6.4 TB/s): HBM.  fp8 reads 3.1 GB: 729 us at
+// 16 heads, 800 at 32, 1051 at 64 (4.3, 3.9, 3.0 TB/s): no one unit.  At 64 heads L1 and shared memory are at
+// 43 % of their rate, the tensor pipe at 37, DRAM at 32; the operand reads and the converters' writes of its
+// tiles (312 KB, at 128 bytes a clock) would take some 630 us.  What is left is the way of a tile from codes
+// through registers and shared memory to its two products, with two tiles under way; how much of it each step
+// takes has not been measured.  Selected keys (2048 of each row): 39 us at 16 heads, 61 at 64: the gathers'
 // latency, the partials and their join.
 #include <cuda_bf16.h>
 

@@ -114,8 +114,10 @@ __device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
 // Splitting rows evenly costs writing and joining partials; a CTA pair per row costs the tiles that the
 // longest row has above the even share.  128 heads, 64 rows of 8 selected tiles over 76 pairs: 54.8 us
 // split, 40.9 whole; of 32 tiles, 87.8 and 78.6; 48 rows of 32 (12 above the share), 76.8 and 75.3; 20 rows
-// of 16 (12 above it), 41.9 and 46.4.  Single CTAs, whose partials are smaller, gain nothing (64 heads, 128
-// rows of 32: 112 and 118).  Extra tiles that are taken:
+// of 16 (12 above it), 41.9 and 46.4.  Up to 8 extra tiles are taken at 76 pairs, where all of this was
+// measured; 12 gain or lose with the rows' length.  Fewer groups, whose partials are fewer, take fewer in
+// proportion (not measured).  Single CTAs, whose partials are smaller, gain nothing (64 heads, 128 rows of 32:
+// 112 and 118).  Extra tiles that are taken:
 __device__ __forceinline__ int whole_row_extra(int groups) { return groups / 9; }
 
 // The segments (consecutive tiles of one row) of this CTA's share, in order.

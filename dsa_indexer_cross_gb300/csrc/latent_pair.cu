@@ -3,7 +3,7 @@
 // the split over the length.
 //
 // Why a pair.  At these head counts the products, not the cache's bytes, are the larger part, and what
-// bounds them is shared-memory bandwidth (128 bytes a clock): one CTA's transposed products read each
+// they take most of is shared-memory bandwidth (128 bytes a clock): one CTA's transposed products read each
 // row's 64-dim blocks once per M tile against only 64 columns.  Here the heads are on M, 64 in each
 // CTA, and the tensor cores take half of the other operand from each CTA's shared memory:
 //     S[h, r]  = Q[h, :576] . Rows[r, :576]      M = 2 x 64 heads, N = 64 rows (32 from each CTA), K = 576
@@ -32,10 +32,13 @@
 // their parts from there as they do from a bf16 cache (1900 us and more where converters wrote the parts
 // into shared memory).
 //
-// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1102 us, 1217 TFLOP/s of a measured
-// 1924 and 5.1 TB/s of 6.78: operand reads from shared memory next to the copies' writes.  fp8: 1473 us,
-// 911 TFLOP/s, 2.1 TB/s: the same, and the converters' loads and stores through L1.  (Scoring two tiles
-// with one N = 128 product: bf16 1653, fp8 2008 us.)
+// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1102 to 1126 us, 1192 TFLOP/s of a measured
+// 1924 and 4.9 TB/s of 6.78: operand reads and copies (224 KB a tile, at 128 bytes a clock) would take 80 %
+// of that, though the counter of L1 and shared memory stands at 51 %, the tensor pipe at 44, DRAM at 54.
+// fp8: 1470 us, 913 TFLOP/s, 2.1 TB/s: the same tiles, with the converters' loads and stores through L1 on
+// top (53 %, 33, 24).  No unit is full in either: the rest is the chain from a tile's rows to S, softmax, P and
+// the second product, two tiles under way, whose steps have not been measured apart.  (Scoring two tiles with
+// one N = 128 product: bf16 1653, fp8 2008 us.)
 //
 // The leader (the pair's even CTA) issues every product; the peer's warps signal its barriers.  Every
 // wait is bounded.  The CTAs leave together (a cluster barrier behind the last wait), so no thread

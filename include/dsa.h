@@ -525,8 +525,9 @@ dsa_status dsa_latent_cache_read(const dsa_latent_cache* cache, const dsa_paged_
  * twice.  Results do not depend on the order in which CTAs run.
  *   q bf16 [n_q][n_heads][576], out bf16 [n_q][n_heads][512], 16-byte aligned; lse f32 [n_q][n_heads]
  *   or NULL; block_table and seq_len hold n_q rows; desc->n_kv == cache->n_rows.
- * ws: dsa_latent_attn_workspace_size(desc) bytes.  Errors: those of dsa_sparse_attn_paged, DSA_ERR_ARG
- * (the cache), DSA_ERR_SHAPE (n_q * n_heads beyond int32, topk beyond 2^30). */
+ * ws: dsa_latent_attn_workspace_size(desc) bytes, enough for either cache, with or without idx, and for any
+ * lengths: up to 40 MB for 64 heads and fewer and 85 MB beyond, little of it by n_q.
+ * Errors: those of dsa_sparse_attn_paged, DSA_ERR_ARG (the cache), DSA_ERR_SHAPE (n_q * n_heads beyond int32, topk beyond 2^30). */
 dsa_status dsa_latent_attn_workspace_size(const dsa_attn_desc* desc, size_t* bytes);
 dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
                                  const int32_t* idx, const dsa_paged_cache* pages, void* out, float* lse, void* ws,
