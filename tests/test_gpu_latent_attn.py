@@ -762,3 +762,50 @@ def test_nothing_shows_in_place_of_a_page_outside_the_cache(H, fmt):
     out, lse, ws = attend(pc, q)
     assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
     check_exceptional(out, lse, q, [np.concatenate([rows[0][:256], rows[0][384:]]), rows[1][:128]])
+
+
+def test_long_fp8_cache_offsets_pass_32_bits():
+    """Codes whose offsets pass 2^31, at the end of a 2.2 GB array, through every fp8 path."""
+    n_pages = (1 << 31) // (P * 512) + 40
+    codes = torch.full((n_pages * P, 512), 0x7F, dtype=torch.uint8, device=DEV)
+    scale = torch.full((n_pages * P, 4), 255, dtype=torch.uint8, device=DEV)
+    rope = torch.full((n_pages * P, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    cache = D.latent_cache(codes, scale, rope)
+    kv, L = randn((300, 576), gen(151)), 300
+    bt = np.array([[n_pages - 1, 0, n_pages - 3]], dtype=np.int32)
+    j = np.arange(L)
+    slot = i32(bt[0, j // P].astype(np.int64) * P + j % P)
+    ws = D.dsa_latent_cache_write(D.cache_write_desc(kv), kv, slot, None, None, cache)
+    assert D.dsa_workspace_status(ws) == 0
+    at = slot.long()
+    x = kv.double().cpu().numpy()
+    c, s = LO.fp8_encode(x[:, :512])
+    assert np.array_equal(codes[at].cpu().numpy(), c) and np.array_equal(scale[at].cpu().numpy(), s)
+    stored = np.concatenate([LO.fp8_decode(c, s), x[:, 512:]], axis=1)
+    bt_d, ln = i32(bt), i32([L])
+    pages = D.paged_cache(bt_d, ln, n_pages)
+    back = torch.empty_like(kv)
+    D.dsa_latent_cache_read(cache, pages, 1, i32([0]), back)
+    assert np.array_equal(back.double().cpu().numpy(), stored)
+    for H in (16, 128):
+        q = randn((1, H, 576), gen(152))
+        for pick in (None, [299, 0, 130, 257, 256, 127, 128]):
+            idx = None if pick is None else i32([pick])
+            out = torch.empty((1, H, 512), dtype=torch.bfloat16, device=DEV)
+            lse = torch.empty((1, H), device=DEV)
+            desc = D.attn_desc(1, n_pages * P, H, 0 if pick is None else len(pick), TAU)
+            ws = D.dsa_latent_attn_paged(desc, q, cache, idx, pages, out, lse)
+            assert D.dsa_workspace_status(ws) == 0
+            check_exceptional(out, lse, q, [stored if pick is None else stored[pick]])
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_a_key_listed_twice_counts_twice(H):
+    pc = Paged([400, 90], "fp8", seed=161)
+    q = randn((2, H, 576), gen(162))
+    idx = np.full((2, 130), -1, dtype=np.int32)
+    idx[0, :129] = np.repeat(np.arange(43) * 9, 3)
+    idx[1, 5:] = 77
+    out, lse, ws = attend(pc, q, i32(idx))
+    assert D.dsa_workspace_status(ws) == 0
+    check_exceptional(out, lse, q, [pc.stored(t)[idx[t][idx[t] >= 0]] for t in range(2)])
