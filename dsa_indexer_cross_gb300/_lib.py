@@ -40,10 +40,10 @@ EXPORTED = ("dsa_status_string", "dsa_last_error", "dsa_donor_table", "dsa_rope_
             "dsa_indexer_backward_workspace_size", "dsa_indexer_backward",
             "dsa_sparse_attn_backward_workspace_size", "dsa_rope_table_scaled", "dsa_rope_apply",
             "dsa_latent_cache_write", "dsa_latent_cache_read", "dsa_latent_attn_workspace_size",
-            "dsa_latent_attn_paged")
+            "dsa_latent_attn_paged", "dsa_mtp_verify")
 
 PROFILE_KINDS = {0: "rope", 1: "ranges", 2: "indexer", 3: "select", 4: "attn_prep", 5: "attn", 6: "attn_bwd",
-                 7: "proj", 8: "indexer_bwd", 9: "cache"}
+                 7: "proj", 8: "indexer_bwd", 9: "cache", 10: "verify"}
 
 
 class DsaError(RuntimeError):
@@ -93,6 +93,11 @@ class LatentCache(C.Structure):
 
 class CacheWriteDesc(C.Structure):
     _fields_ = [("n_tokens", C.c_int32), ("flags", C.c_uint32), ("kv_stride", C.c_int64)]
+
+
+class VerifyDesc(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("n_draft", C.c_int32), ("vocab", C.c_int32), ("dtype", C.c_int32),
+                ("target_stride", C.c_int64), ("draft_stride", C.c_int64)]
 
 
 _lib: Optional[C.CDLL] = None
@@ -179,6 +184,8 @@ def lib() -> C.CDLL:
         L.dsa_latent_attn_workspace_size.argtypes = [P(AttnDesc), P(sz)]
         L.dsa_latent_attn_paged.restype = st
         L.dsa_latent_attn_paged.argtypes = [P(AttnDesc), vp, P(LatentCache), vp, P(PagedCache), vp, vp, vp, sz, vp]
+        L.dsa_mtp_verify.restype = st
+        L.dsa_mtp_verify.argtypes = [P(VerifyDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -773,6 +780,68 @@ def dsa_mtp_indexshare_step(idesc: IndexerDesc, adesc: AttnDesc, step: int, laye
     _check(lib().dsa_mtp_indexshare_step(C.byref(idesc), C.byref(adesc), int(step), C.byref(io), _ptr(ks), _ptr(ke),
                                          _ptr(q_pos), _ptr(k_pos), _ptr(rope_cs), n_pos, _ptr(mtp_idx), _ptr(ws),
                                          ws.numel(), _stream(stream)))
+    return ws
+
+
+# ------------------------------------------------------------------------------ draft verification
+
+def _vocab_rows(t: torch.Tensor, n: int, m: int, vocab: int, dt, name: str) -> int:
+    """Elements between the vocabulary rows of a [n, m, vocab] view whose rows are equally far apart."""
+    if t.dtype is not dt or t.shape != (n, m, vocab):
+        raise ValueError(f"{name}: expected a {dt} view of shape {(n, m, vocab)}, got {t.dtype} {tuple(t.shape)}")
+    s = t.stride()
+    if vocab > 1 and s[2] != 1:
+        raise ValueError(f"{name}: a row's probabilities must be contiguous")
+    row = s[1] if m > 1 else s[0] if n > 1 else vocab
+    if n > 1 and m > 1 and s[0] != m * row:
+        raise ValueError(f"{name}: rows must be equally far apart, strides are {s}")
+    return row
+
+
+def verify_desc(target: torch.Tensor, draft: Optional[torch.Tensor] = None) -> VerifyDesc:
+    """Descriptor for verifying drafts against target [sequences, drafts + 1, vocab], with the draft's
+    probabilities [sequences, drafts, vocab] or without; fp32 or bf16 views whose rows are equally far apart.
+    It holds for every pair of views of these shapes, strides and type."""
+    if target.dim() != 3 or target.shape[1] < 1:
+        raise ValueError(f"target: expected [sequences, drafts + 1, vocab], got {tuple(target.shape)}")
+    if target.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"target: expected torch.bfloat16 or torch.float32, got {target.dtype}")
+    n, m, v = target.shape
+    row = _vocab_rows(target, n, m, v, target.dtype, "target")
+    drow = _vocab_rows(draft, n, m - 1, v, target.dtype, "draft") if draft is not None else 0
+    return VerifyDesc(n, m - 1, v, DSA_F32 if target.dtype == torch.float32 else DSA_BF16, row, drow)
+
+
+def dsa_mtp_verify(desc: VerifyDesc, target, draft, tokens, draft_len, u_accept, u_sample, tokens_out, n_accepted,
+                   ws=None, stream=None) -> torch.Tensor:
+    """tokens_out[t] = the drafts of sequence t that are taken, the token drawn behind them, then -1;
+    n_accepted[t] = how many were taken.  draft None: drafts without probabilities; draft_len None: all of them."""
+    n, d, v = desc.n_seq, desc.n_draft, desc.vocab
+    dt = torch.float32 if desc.dtype == DSA_F32 else torch.bfloat16
+    dev = _current_device(target, "target")
+    views = [(target, d + 1, desc.target_stride, "target")]
+    if draft is not None and d > 0:
+        views.append((draft, d, desc.draft_stride, "draft"))
+    for t, m, row, name in views:
+        if _vocab_rows(t, n, m, v, dt, name) != row:
+            if n * m > 1:
+                raise ValueError(f"{name}: strides {t.stride()} are not the descriptor's ({row} between rows)")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, but the call's other tensors are on cuda:{dev}")
+    i32, f32 = torch.int32, torch.float32
+    p_tok = p_u = None
+    if d > 0:
+        p_tok, p_u = _arg(tokens, i32, n * d, "tokens", dev), _arg(u_accept, f32, n * d, "u_accept", dev)
+    p_len = None if draft_len is None else _arg(draft_len, i32, n, "draft_len", dev)
+    if ws is None:
+        ws = _workspace(256, target.device, stream)
+    st = (_lib or lib()).dsa_mtp_verify(desc, target.data_ptr(), draft.data_ptr() if draft is not None else None, p_tok,
+                                        p_len, p_u, _arg(u_sample, f32, n, "u_sample", dev),
+                                        _arg(tokens_out, i32, n * (d + 1), "tokens_out", dev),
+                                        _arg(n_accepted, i32, n, "n_accepted", dev),
+                                        _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
     return ws
 
 

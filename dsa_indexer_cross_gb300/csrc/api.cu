@@ -1030,6 +1030,36 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "latent attention kernel");
 }
 
+dsa_status dsa_mtp_verify(const dsa_verify_desc* d, const void* target, const void* draft, const int32_t* tokens,
+                          const int32_t* draft_len, const float* u_accept, const float* u_sample, int32_t* tokens_out,
+                          int32_t* n_accepted, void* ws, size_t ws_bytes, void* stream) {
+  if (!d) return fail(DSA_ERR_ARG, "verify descriptor is NULL");
+  if (d->n_seq < 0 || d->n_draft < 0 || d->vocab < 1) return fail(DSA_ERR_ARG, "n_seq and n_draft must be >= 0, vocab >= 1");
+  if (d->dtype != DSA_BF16 && d->dtype != DSA_F32) return fail(DSA_ERR_ARG, "verify dtype %d", d->dtype);
+  if (d->vocab > (1 << 30)) return fail(DSA_ERR_SHAPE, "vocab %d exceeds 2^30", d->vocab);
+  if (static_cast<long long>(d->n_seq) * (d->n_draft + 1LL) > 0x7FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_seq * (n_draft + 1) exceeds the int32 range");
+  if (d->target_stride < d->vocab || (draft && d->draft_stride < d->vocab))
+    return fail(DSA_ERR_ARG, "target_stride and draft_stride must be at least vocab");
+  dsa_status s;
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  if (d->n_seq == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
+  if (!target || !u_sample || !tokens_out || !n_accepted || (d->n_draft > 0 && (!tokens || !u_accept)))
+    return fail(DSA_ERR_ARG, "target, tokens, u_accept, u_sample, tokens_out and n_accepted must be non-NULL");
+  const uintptr_t el = d->dtype == DSA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(target) % el || reinterpret_cast<uintptr_t>(draft) % el)
+    return fail(DSA_ERR_ARG, "target and draft must be aligned to their elements");
+  if ((s = check_device()) != DSA_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // (without drafts there is no draft distribution to take off)
+  const Verify a{target, d->n_draft > 0 ? draft : nullptr, tokens, draft_len, u_accept, u_sample, tokens_out, n_accepted,
+                 d->target_stride, d->draft_stride, d->n_seq, d->n_draft, d->vocab};
+  const int ps = prof_begin(kProfVerify, st);
+  const cudaError_t e = launch_verify(a, d->dtype == DSA_F32, static_cast<uint32_t*>(ws), st);
+  prof_end(ps, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "verification kernel");
+}
+
 dsa_status dsa_indexer_projections(const dsa_proj_desc* d, const void* x, const void* q_latent, const void* wq_b,
                                    const void* wk, const float* k_norm_w, const float* k_norm_b,
                                    const void* weights_proj, void* q_idx, void* k_idx, float* w, void* ws,

@@ -299,6 +299,23 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
                                const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads,
                                int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
 
+// ---------------------------------------------------------------------------- draft verification
+// Drafts taken, and the token drawn behind them, of every sequence (strides in elements between vocabulary
+// rows; draft NULL: drafts without probabilities; draft_len NULL: n_draft each).
+struct Verify {
+  const void* target;
+  const void* draft;
+  const int32_t* tokens;
+  const int32_t* draft_len;
+  const float* u_accept;
+  const float* u_sample;
+  int32_t* tokens_out;
+  int32_t* n_accepted;
+  long long target_stride, draft_stride;
+  int n_seq, n_draft, vocab;
+};
+cudaError_t launch_verify(const Verify& a, bool f32, uint32_t* status, cudaStream_t st);
+
 int device_sm_count();
 
 // ---------------------------------------------------------------------------- launch log
@@ -308,7 +325,7 @@ int device_sm_count();
 // do nothing.  prof_begin returns the record's slot (-1 when nothing is recorded).
 enum ProfKind : int {
   kProfRope = 0, kProfRanges = 1, kProfIndexer = 2, kProfSelect = 3, kProfAttnPrep = 4, kProfAttn = 5,
-  kProfAttnBwd = 6, kProfProj = 7, kProfIndexerBwd = 8, kProfCache = 9
+  kProfAttnBwd = 6, kProfProj = 7, kProfIndexerBwd = 8, kProfCache = 9, kProfVerify = 10
 };
 int prof_begin(int kind, cudaStream_t st);
 void prof_end(int slot, cudaStream_t st);

@@ -8,6 +8,7 @@
 #include "fp8.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "status.cuh"
 
 namespace dsa {
 namespace {
@@ -73,51 +74,6 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // them, about 2 us less than a memset.  (Always clearing costs small calls a launch: one head of 2048
 // tokens 6.7 -> 8.6 us.)
 constexpr int kSoleMostRope = 16384, kSoleMostWrite = 4096, kSoleMostPages = 4096;
-
-__device__ __forceinline__ void report(uint32_t* status, bool sole, uint32_t bits) {
-  if (sole) return;
-  atomicOr(status, bits);
-  atomicAdd(status + 1, 1u);
-}
-__global__ void clear_status_kernel(uint32_t* status) {
-  grid_trigger();
-  grid_wait();
-  status[threadIdx.x] = 0u;
-}
-cudaError_t clear_status(uint32_t* status, cudaStream_t st) {
-  return launch_pdl(clear_status_kernel, dim3(1), 2, 0, st, 1, status);
-}
-// Block 0 of a call that writes the status words itself: check(i) gives item i's error bits.
-template <typename F>
-__device__ __forceinline__ void sole_status(uint32_t* status, int n, F check) {
-  __shared__ uint32_t s_bits, s_count;
-  if (threadIdx.x == 0) s_bits = s_count = 0u;
-  __syncthreads();
-  uint32_t bits = 0, count = 0;
-  int i = threadIdx.x;
-  for (; i + 7 * static_cast<int>(blockDim.x) < n; i += 8 * blockDim.x) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {        // (eight items' loads in flight)
-      const uint32_t e = check(i + u * blockDim.x);
-      bits |= e;
-      count += e ? 1u : 0u;
-    }
-  }
-  for (; i < n; i += blockDim.x) {
-    const uint32_t e = check(i);
-    bits |= e;
-    count += e ? 1u : 0u;
-  }
-  if (bits) {
-    atomicOr(&s_bits, bits);
-    atomicAdd(&s_count, count);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    status[0] = s_bits;
-    status[1] = s_count;
-  }
-}
 
 // ---------------------------------------------------------------------------- rotary positions
 // A thread turns one 16-byte vector (interleaved: its own pairs) or one vector of each half

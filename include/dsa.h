@@ -557,6 +557,47 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
                                    const int32_t* q_pos, const int32_t* k_pos, const float* rope_cs,
                                    int32_t rope_n_pos, int32_t* mtp_idx, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ draft verification */
+
+/* Verification of drafted tokens against the target model's probabilities, from given uniform numbers
+ * (the pages name the MTP path's acceptance length, not its rule; this is the published one of
+ * speculative sampling).  Sequence t drafted tokens x_0 .. x_{n-1}, n = draft_len[t], from distributions
+ * q_0 .. q_{n-1}; p_0 .. p_n are the target's at the same places.  With u_i = u_accept[t][i],
+ *   a = the first i < n where u_i q_i(x_i) < p_i(x_i) does not hold, n where it always does;
+ *   r = max(p_a - q_a, 0) where a < n, p_n where a = n;
+ *   y = the lowest v with sum_{w <= v} r(w) > u_sample[t] sum_w r(w)
+ * tokens_out[t] = x_0 .. x_{a-1}, y, then -1 up to n_draft + 1; n_accepted[t] = a.  For u uniform on
+ * [0, 1) and x_i drawn from q_i, the tokens follow the target's distribution.  draft NULL: drafts without
+ * probabilities (looked up, or a greedy draft): q_i is one at x_i, zero elsewhere.
+ * The products are compared exactly; the sums and u_sample times the last are as good as double
+ * precision, in an order that does not change from call to call.  Only the rows p_a and q_a are read whole.
+ * Where r has no weight (q_a covers p_a), y is drawn from p_a instead; where that has none either, or a
+ * sum is infinite, y = -1.  A NaN or negative difference weighs nothing; a u_sample outside [0, 1)
+ * draws the first or the last token of any weight (NaN: the first).
+ * A length outside [0, n_draft] is cut to it and flagged, a drafted token outside [0, vocab) is refused
+ * as a draft that is not taken (without draft probabilities nothing is then taken off p_a) and flagged
+ * (DSA_ERR_DEVICE).
+ *   target [n_seq][n_draft + 1] rows of vocab probabilities, target_stride elements apart; draft
+ *   [n_seq][n_draft] rows, draft_stride apart; both of dtype, finite and >= 0, aligned to their elements
+ *   (rows on 16-byte boundaries, or target and draft rows equally far behind one, are read in vectors).
+ *   tokens int32 [n_seq][n_draft], draft_len int32 [n_seq] (NULL: n_draft each), u_accept f32
+ *   [n_seq][n_draft], u_sample f32 [n_seq]; tokens_out int32 [n_seq][n_draft + 1], n_accepted int32
+ *   [n_seq].  Entries past a sequence's length are not read.  n_draft = 0: tokens and u_accept may be NULL.
+ * ws: at least 256 bytes.  Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_seq * (n_draft + 1) beyond int32, vocab
+ * beyond 2^30), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
+typedef struct dsa_verify_desc {
+  int32_t n_seq;
+  int32_t n_draft;          /* drafts of a sequence, at most; >= 0          */
+  int32_t vocab;
+  int32_t dtype;            /* DSA_BF16 or DSA_F32                          */
+  int64_t target_stride;    /* >= vocab                                     */
+  int64_t draft_stride;     /* >= vocab (draft NULL: not looked at)         */
+} dsa_verify_desc;
+
+dsa_status dsa_mtp_verify(const dsa_verify_desc* desc, const void* target, const void* draft, const int32_t* tokens,
+                          const int32_t* draft_len, const float* u_accept, const float* u_sample, int32_t* tokens_out,
+                          int32_t* n_accepted, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ device status ---- */
 
 /* Synchronise `stream`, read the device status word of workspace `ws`, and map it:
@@ -599,7 +640,8 @@ enum {
   DSA_PROF_ATTN_BWD = 6,      /* sparse attention backward                                  */
   DSA_PROF_PROJ = 7,          /* indexer projections                                        */
   DSA_PROF_INDEXER_BWD = 8,   /* indexer backward                                           */
-  DSA_PROF_CACHE = 9          /* rotary positions, latent cache writing and reading         */
+  DSA_PROF_CACHE = 9,         /* rotary positions, latent cache writing and reading         */
+  DSA_PROF_VERIFY = 10        /* draft verification                                         */
 };
 typedef struct dsa_profile_record {
   int32_t kind;   /* DSA_PROF_*                        */
