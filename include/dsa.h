@@ -569,8 +569,8 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
  * tokens_out[t] = x_0 .. x_{a-1}, y, then -1 up to n_draft + 1; n_accepted[t] = a.  For u uniform on
  * [0, 1) and x_i drawn from q_i, the tokens follow the target's distribution.  draft NULL: drafts without
  * probabilities (looked up, or a greedy draft): q_i is one at x_i, zero elsewhere.
- * The products are compared exactly; the sums and u_sample times the last are as good as double
- * precision, in an order that does not change from call to call.  Only the rows p_a and q_a are read whole.
+ * The products are compared exactly; the sums and u_sample times the last are good to some 2^-45
+ *, in an order that does not change from call to call.  Only the rows p_a and q_a are read whole.
  * Where r has no weight (q_a covers p_a), y is drawn from p_a instead; where that has none either, or a
  * sum is infinite, y = -1.  A NaN or negative difference weighs nothing; a u_sample outside [0, 1)
  * draws the first or the last token of any weight (NaN: the first).
