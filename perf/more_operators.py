@@ -337,7 +337,7 @@ def _plan(s):
         return desc, cache, pages, _handle(D, s["to"]), D.paged_cache(s["to_bt"], s["to_len"], s["to_pages"]), ws
     desc = D.attn_desc(s["seqs"], s["n_pages"] * PAGE, s["heads"], 0, TAU)
     if s["op"] == "shared":
-        groups = D.shared_rows(s["start"], s["prefix"], s["rows"])
+        groups = D.shared_rows(s["start"], s["prefix"], max(len(lens) for _, lens in s["plan_groups"]))
         ws = torch.empty(D.dsa_latent_attn_shared_workspace_size(desc, groups), dtype=torch.uint8, device=DEV)
         return desc, cache, groups, pages, ws
     ws = torch.empty(D.dsa_latent_key_weights_workspace_size(desc, pages), dtype=torch.uint8, device=DEV)
