@@ -20,7 +20,8 @@ from ._lib import (AttnDesc, DsaError, IndexCache, IndexerDesc, LayerIO, PagedCa
                    dsa_latent_cache_read, dsa_latent_cache_write, dsa_rope_apply,
                    dsa_rope_table_scaled, latent_cache, rope_desc, rope_scaling_linear,
                    rope_scaling_yarn,
-                   VerifyDesc, dsa_mtp_verify, verify_desc)
+                   VerifyDesc, dsa_mtp_verify, verify_desc,
+                   SharedRows, dsa_latent_attn_shared, dsa_latent_attn_shared_workspace_size, shared_rows)
 
 __all__ = ["AttnDesc", "DsaError", "IndexCache", "IndexerDesc", "LayerIO", "PagedCache", "DSA_PAGE_ROWS",
            "dsa_indexer_topk_paged", "dsa_sparse_attn_paged", "paged_cache", "ProjDesc", "dsa_indexer_projections", "dsa_sparse_attn_backward",
@@ -34,4 +35,5 @@ __all__ = ["AttnDesc", "DsaError", "IndexCache", "IndexerDesc", "LayerIO", "Page
            "DSA_ROPE_SCALE_LINEAR", "DSA_ROPE_SCALE_NONE", "DSA_ROPE_SCALE_YARN", "cache_write_desc",
            "dsa_latent_attn_paged", "dsa_latent_attn_workspace_size", "dsa_latent_cache_read",
            "dsa_latent_cache_write", "dsa_rope_apply", "dsa_rope_table_scaled", "latent_cache", "rope_desc",
-           "rope_scaling_linear", "rope_scaling_yarn", "VerifyDesc", "dsa_mtp_verify", "verify_desc"]
+           "rope_scaling_linear", "rope_scaling_yarn", "VerifyDesc", "dsa_mtp_verify", "verify_desc",
+           "SharedRows", "dsa_latent_attn_shared", "dsa_latent_attn_shared_workspace_size", "shared_rows"]

@@ -40,7 +40,8 @@ EXPORTED = ("dsa_status_string", "dsa_last_error", "dsa_donor_table", "dsa_rope_
             "dsa_indexer_backward_workspace_size", "dsa_indexer_backward",
             "dsa_sparse_attn_backward_workspace_size", "dsa_rope_table_scaled", "dsa_rope_apply",
             "dsa_latent_cache_write", "dsa_latent_cache_read", "dsa_latent_attn_workspace_size",
-            "dsa_latent_attn_paged", "dsa_mtp_verify")
+            "dsa_latent_attn_paged", "dsa_mtp_verify", "dsa_latent_attn_shared_workspace_size",
+            "dsa_latent_attn_shared")
 
 PROFILE_KINDS = {0: "rope", 1: "ranges", 2: "indexer", 3: "select", 4: "attn_prep", 5: "attn", 6: "attn_bwd",
                  7: "proj", 8: "indexer_bwd", 9: "cache", 10: "verify"}
@@ -93,6 +94,13 @@ class LatentCache(C.Structure):
 
 class CacheWriteDesc(C.Structure):
     _fields_ = [("n_tokens", C.c_int32), ("flags", C.c_uint32), ("kv_stride", C.c_int64)]
+
+
+class SharedRows(C.Structure):
+    """dsa_shared_rows (see shared_rows)."""
+    _fields_ = [("group_start", C.c_void_p), ("prefix_len", C.c_void_p), ("n_groups", C.c_int32),
+                ("max_rows", C.c_int32)]
+    device = None       # ordinal of the tensors' device, where shared_rows made it
 
 
 class VerifyDesc(C.Structure):
@@ -184,6 +192,11 @@ def lib() -> C.CDLL:
         L.dsa_latent_attn_workspace_size.argtypes = [P(AttnDesc), P(sz)]
         L.dsa_latent_attn_paged.restype = st
         L.dsa_latent_attn_paged.argtypes = [P(AttnDesc), vp, P(LatentCache), vp, P(PagedCache), vp, vp, vp, sz, vp]
+        L.dsa_latent_attn_shared_workspace_size.restype = st
+        L.dsa_latent_attn_shared_workspace_size.argtypes = [P(AttnDesc), P(SharedRows), P(sz)]
+        L.dsa_latent_attn_shared.restype = st
+        L.dsa_latent_attn_shared.argtypes = [P(AttnDesc), vp, P(LatentCache), P(SharedRows), P(PagedCache), vp, vp, vp, sz,
+                                             vp]
         L.dsa_mtp_verify.restype = st
         L.dsa_mtp_verify.argtypes = [P(VerifyDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         _lib = L
@@ -750,6 +763,42 @@ def dsa_latent_attn_paged(desc: AttnDesc, q, cache: LatentCache, idx, pages: Pag
         ws = _workspace(dsa_latent_attn_workspace_size(desc), q.device, stream)
     st = (_lib or lib()).dsa_latent_attn_paged(desc, p_q, cache, p_idx, pages, p_out, p_lse,
                                                _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
+    return ws
+
+
+def shared_rows(group_start: torch.Tensor, prefix_len: torch.Tensor, max_rows: int) -> SharedRows:
+    """Groups of rows that share a prefix: rows [group_start[g], group_start[g + 1]) their first prefix_len[g]
+    keys.  int32 device tensors of groups + 1 and of groups entries (kept alive by the caller); max_rows: rows of
+    the largest group, or about."""
+    n = prefix_len.numel()
+    _want(group_start, torch.int32, n + 1, "group_start")
+    _want(prefix_len, torch.int32, 0, "prefix_len")
+    rows = SharedRows(_ptr(group_start), _ptr(prefix_len), n, max_rows)
+    rows.device = _one_device(group_start, prefix_len)
+    return rows
+
+
+def dsa_latent_attn_shared_workspace_size(desc: AttnDesc, groups: SharedRows) -> int:
+    n = C.c_size_t(0)
+    _check(lib().dsa_latent_attn_shared_workspace_size(C.byref(desc), C.byref(groups), C.byref(n)))
+    return n.value
+
+
+def dsa_latent_attn_shared(desc: AttnDesc, q, cache: LatentCache, groups: SharedRows, pages: PagedCache, out, lse=None,
+                           ws=None, stream=None) -> torch.Tensor:
+    """Latent attention of row t over its sequence's cached keys, the keys that a group's rows share walked once
+    for all of them."""
+    n = desc.n_q * desc.n_heads
+    dev = _current_device(q, "q", cache, groups, pages)
+    p_q, p_out = _arg(q, torch.bfloat16, n * desc.d_qk, "q", dev), _arg(out, torch.bfloat16, n * desc.d_v, "out", dev)
+    p_lse = None if lse is None else _arg(lse, torch.float32, n, "lse", dev)
+    _paged_args(pages, desc.n_q)
+    if ws is None:
+        ws = _workspace(dsa_latent_attn_shared_workspace_size(desc, groups), q.device, stream)
+    st = (_lib or lib()).dsa_latent_attn_shared(desc, p_q, cache, groups, pages, p_out, p_lse,
+                                                _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
         _check(st)
     return ws

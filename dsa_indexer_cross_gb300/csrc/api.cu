@@ -1030,6 +1030,83 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "latent attention kernel");
 }
 
+namespace {
+// What the calls over a whole paged latent cache check of their descriptor, cache and tables.
+dsa_status check_latent(const dsa_attn_desc* desc, const dsa_latent_cache* cache, const dsa_paged_cache* pages,
+                        dsa_attn_desc* d, LatentCache* c, PagedRows* pg) {
+  if (!desc) return fail(DSA_ERR_ARG, "attention descriptor is NULL");
+  *d = latent_desc(desc, false);
+  dsa_status s = check_attn_desc(d);
+  if (s != DSA_OK) return s;
+  if ((s = check_cache(cache, c)) != DSA_OK) return s;
+  if ((s = check_pages(pages, d->n_kv, d->n_q, pg)) != DSA_OK) return s;
+  if (c->n_rows != d->n_kv) return fail(DSA_ERR_SHAPE, "n_kv %d must equal the cache's n_rows %d", d->n_kv, c->n_rows);
+  if (pg->max_pages > 0x7FFFFFFF / kPageRows) return fail(DSA_ERR_SHAPE, "max_pages * page_rows exceeds the int32 range");
+  if (static_cast<long long>(d->n_q) * d->n_heads > 0x7FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_q * n_heads exceeds the int32 range");
+  return DSA_OK;
+}
+// The groups, apart from their device arrays.
+dsa_status check_groups(const dsa_shared_rows* g) {
+  if (!g) return fail(DSA_ERR_ARG, "shared rows are NULL");
+  if (g->n_groups < 0 || g->max_rows < 1) return fail(DSA_ERR_ARG, "n_groups must be >= 0 and max_rows >= 1");
+  if (g->n_groups > (1 << 24)) return fail(DSA_ERR_SHAPE, "n_groups %d exceeds 2^24", g->n_groups);
+  return DSA_OK;
+}
+}  // namespace
+
+dsa_status dsa_latent_attn_shared_workspace_size(const dsa_attn_desc* desc, const dsa_shared_rows* groups, size_t* bytes) {
+  if (!desc) return fail(DSA_ERR_ARG, "attention descriptor is NULL");
+  if (!bytes) return fail(DSA_ERR_ARG, "bytes is NULL");
+  const dsa_attn_desc d = latent_desc(desc, false);
+  dsa_status s = check_attn_desc(&d);
+  if (s != DSA_OK || (s = check_groups(groups)) != DSA_OK) return s;
+  if (static_cast<long long>(d.n_q) * d.n_heads > 0x7FFFFFFFLL)
+    return fail(DSA_ERR_SHAPE, "n_q * n_heads exceeds the int32 range");
+  *bytes = kAlign + align_up(latent_shared_ws_bytes(d.n_q, d.n_heads, groups->n_groups, groups->max_rows));
+  return DSA_OK;
+}
+
+dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
+                                  const dsa_shared_rows* groups, const dsa_paged_cache* pages, void* out, float* lse,
+                                  void* ws, size_t ws_bytes, void* stream) {
+  dsa_attn_desc d;
+  LatentCache c;
+  PagedRows pg;
+  dsa_status s = check_latent(desc, cache, pages, &d, &c, &pg);
+  if (s != DSA_OK || (s = check_groups(groups)) != DSA_OK) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d.n_q == 0) return empty_call(ws, ws_bytes, st);
+  if (!q || !out || !ws || (groups->n_groups > 0 && (!groups->group_start || !groups->prefix_len)))
+    return fail(DSA_ERR_ARG, "q, group_start, prefix_len, out and ws must be non-NULL");
+  if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_ARG, "q and out must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be 256-byte aligned");
+  if ((s = check_device()) != DSA_OK) return s;
+  const size_t need = kAlign + align_up(latent_shared_ws_bytes(d.n_q, d.n_heads, groups->n_groups, groups->max_rows));
+  if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "shared attention workspace too small: %zu < %zu bytes", ws_bytes, need);
+  const SharedWalks walks = latent_shared_walks(d.n_q, d.n_heads, groups->n_groups, groups->max_rows);
+  CUtensorMap tkv[2], tv[2], tq[2];
+  std::memset(tkv, 0, sizeof(tkv));
+  std::memset(tv, 0, sizeof(tv));
+  std::memset(tq, 0, sizeof(tq));
+  for (int k = 0; k < walks.n; ++k) {
+    const bool pair = walks.pair[k];
+    if (!c.fp8 || pair) {
+      const void* rows = c.fp8 ? static_cast<const uint8_t*>(ws) + kAlign + walks.ring_offset[k] : c.latent;
+      const uint64_t n = static_cast<uint64_t>(c.fp8 ? walks.ring_rows[k] : c.n_rows);
+      if ((s = tmap_kv_tiles(&tkv[k], rows, n, pair ? 32 : 64, pair ? 9 : 1)) != DSA_OK) return s;
+      if ((s = tmap_kv_tiles(&tv[k], rows, n, 64, 4)) != DSA_OK) return s;
+    }
+    if ((s = tmap_bf16(&tq[k], q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads, static_cast<uint32_t>(walks.q_rows[k]))) !=
+        DSA_OK)
+      return s;
+  }
+  const SharedRows rows{groups->group_start, groups->prefix_len, groups->n_groups, groups->max_rows};
+  const cudaError_t e = launch_latent_shared(c, tkv, tv, tq, pg, rows, d.n_q, d.n_heads, d.softmax_scale, out, lse,
+                                             static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "shared-prefix attention kernel");
+}
+
 dsa_status dsa_mtp_verify(const dsa_verify_desc* d, const void* target, const void* draft, const int32_t* tokens,
                           const int32_t* draft_len, const float* u_accept, const float* u_sample, int32_t* tokens_out,
                           int32_t* n_accepted, void* ws, size_t ws_bytes, void* stream) {

@@ -299,6 +299,29 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
                                const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads,
                                int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
 
+// Rows that share prefixes: group g's are [start[g], start[g + 1]), their common keys [0, prefix[g]); max_rows: a
+// group's rows, at most or thereabouts (it chooses the kernels).
+struct SharedRows {
+  const int32_t* start;
+  const int32_t* prefix;
+  int n_groups, max_rows;
+};
+// The walks (kernel launches) of such a call: whether a walk takes CTA pairs, the box height of its tmap_q, and
+// (pairs) its ring in the scratch; a bf16 cache's maps are as for launch_latent_attn.
+struct SharedWalks {
+  int n;
+  bool pair[2];
+  int q_rows[2];
+  size_t ring_offset[2];
+  int ring_rows[2];
+};
+SharedWalks latent_shared_walks(int n_q, int n_heads, int n_groups, int max_rows);
+size_t latent_shared_ws_bytes(int n_q, int n_heads, int n_groups, int max_rows);
+cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_kv, const CUtensorMap* tmap_v,
+                                 const CUtensorMap* tmap_q, const PagedRows& pg, const SharedRows& groups, int n_q,
+                                 int n_heads, float scale, void* out, float* lse, uint32_t* status, void* scratch,
+                                 cudaStream_t st);
+
 // ---------------------------------------------------------------------------- draft verification
 // Drafts taken, and the token drawn behind them, of every sequence (strides in elements between vocabulary
 // rows; draft NULL: drafts without probabilities; draft_len NULL: n_draft each).

@@ -45,12 +45,13 @@ namespace {
 constexpr int kBlkBytes = kRows * 128;
 constexpr int kTileBytes = kKB * kBlkBytes;
 
-template <int HB, bool FP8>
+template <int HB, bool FP8, bool WEIGHTS = false>
 struct LCfg {
   static constexpr int Q_BYTES = HB * kDqk * 2;
   static constexpr int DYN_SMEM = 1024 + 2 * kTileBytes + Q_BYTES;
-  // softmax warps (fp8: four, which leaves the converters 128 registers)
-  static constexpr int SW = HB >= 32 && !FP8 ? 8 : 4;
+  // softmax warps (fp8: four, which leaves the converters 128 registers; the keys' weights: each key's
+  // columns in one warp)
+  static constexpr int SW = HB >= 32 && !FP8 && !WEIGHTS ? 8 : 4;
   static constexpr int SOFT = 32 * SW;
   static constexpr int NP = FP8 ? 8 : 1;               // producer warps
   static constexpr int S_WARP = SW + NP;
@@ -81,12 +82,13 @@ struct LShared {
 };
 static_assert(LCfg<64, true>::DYN_SMEM + sizeof(LShared) <= 232448, "HB = 64 must fit in shared memory");
 
-template <int HB, bool FP8, bool SEL>
-__global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
+template <int HB, bool FP8, int MODE>
+__global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap tmap_kv, const __grid_constant__ CUtensorMap tmap_v,
                        const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ LArgs a) {
-  using C = LCfg<HB, FP8>;
+  using C = LCfg<HB, FP8, MODE == kWeights>;
+  constexpr bool SEL = MODE == kSelected;
   constexpr int NR = C::NR;
   static_assert(FP8 || !SEL, "selected rows of a bf16 cache take the sparse kernel's gather walk");
   extern __shared__ uint8_t smem_raw[];
@@ -132,12 +134,12 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
   }
   grid_trigger();
   grid_wait();
-  const long long share = find_share<SEL, C::THREADS>(a, grp, hb == 0, sh.share, sh.faults);
+  const long long share = find_share<MODE, C::THREADS>(a, grp, hb == 0 && MODE != kWeights, sh.share, sh.faults);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  Walk<SEL> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
+  Walk<MODE> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
 
   if (warp >= C::SW && warp < C::S_WARP) {
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       uint4 w[16];
       uint32_t sc = 0;                       // scale word of row lane & 15
       int at = -1;                           // its cache row (-1: zeros)
-      Walk<SEL> aw(walk);
+      Walk<MODE> aw(walk);
       Seg as;
       int ai = 0;
       bool alive = aw.next(as);
@@ -333,7 +335,60 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j)
           for (int h = 0; h < 2; ++h) mbar_drain(&sh.full[j & 1][h], (j >> 1) & 1, 200000000ull);
     }
-  } else if (warp < C::SW) {
+  } else if (MODE == kWeights && warp < C::SW) {
+    // ---------------------------------------------------------------- the keys' weights
+    // A warp takes sixteen keys of a tile with all of the CTA's columns: a thread holds two keys, two of
+    // every eight columns, and four lanes' sums meet by shuffles.
+    const int r0 = warp * 16 + (lane >> 2), cq = 2 * (lane & 3);
+    const int my_key = r0 + ((lane & 1) << 3);           // lanes 0 and 1 of four write the two
+    const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t g = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int len = row_len(a.pg, sg.row);
+      const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+      // log-sum-exps in log2; +inf, which weighs nothing, for columns past the last head and for heads
+      // without any key
+      float lse2[2 * NR];
+#pragma unroll
+      for (int c = 0; c < 2 * NR; ++c) {
+        const int h = hb * HB + 8 * (c >> 1) + cq + (c & 1);
+        const float l = h < a.H ? gload(a.lse_in + sg.col0 + h) * 1.4426950408889634f : INFINITY;
+        lse2[c] = l == -INFINITY ? INFINITY : l;
+      }
+      const size_t base = static_cast<size_t>(sg.row) * a.w_stride;
+      float* to = a.n_hb == 1 ? a.w_out + base : a.w_part + static_cast<size_t>(hb) * a.n_q * a.w_stride + base;
+      const float* from = a.n_hb == 1 && a.w_in ? a.w_in + base : nullptr;
+      for (int n = 0; n < sg.n; ++n, ++g) {
+        const int i = sg.i0 + n, sb = g & 1;
+        const int nv = tile_rows(a, len, i, gload(bt + (i >> 1)));
+        const bool mine = (lane & 2) == 0 && my_key < nv;
+        const size_t at = static_cast<size_t>(i) * kRows + my_key;
+        const float before = mine && from ? gload(from + at) : 0.f;
+        ok = wait_bar(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tc_fence_after();
+        uint32_t v[4 * NR];
+        tmem_ld_16x256b<NR>(tmem + t_lane + C::S_COL + sb * HB, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2 * NR; ++c) {
+          x += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + (c & 1)]), a.scale_log2, -lse2[c]));
+          y += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + 2 + (c & 1)]), a.scale_log2, -lse2[c]));
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          x += __shfl_xor_sync(0xffffffffu, x, o);
+          y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        if (mine) to[at] = before + (lane & 1 ? y : x);
+      }
+    }
+  } else if (MODE != kWeights && warp < C::SW) {
     // ---------------------------------------------------------------- softmax + epilogue
     constexpr int kSoft = C::SOFT;
     const int tid = threadIdx.x;
@@ -342,12 +397,13 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
     const int r0 = qd * 16 + (lane >> 2);          // S^T rows held: r0 and r0 + 8
     const int cq = 2 * (lane & 3);                 // column pair within each group of 8 columns
     const uint32_t t_lane = static_cast<uint32_t>(qd * 32) << 16;
-    const int n_cols = min(HB, a.H - hb * HB);
+    int n_cols = min(HB, a.H - hb * HB);
     // A failed (timed-out) wait is published through sh.soft_abort, written only before a
     // named barrier and read right after it, so all softmax warps leave at the same point.
     uint32_t g = 0;
     bool stop = false;
     while (!stop && walk.next(sg)) {
+      if constexpr (MODE == kItems) n_cols = min(HB, columns<MODE>(sg));
       if (tid < HB) sh.m_used[tid] = -INFINITY;
       float lp[2 * NR], lu[2 * NR];   // per column: sums of the rounded weights, and of the weights
 #pragma unroll
@@ -528,7 +584,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
       named_bar_sync(1, kSoft);
       if (stop) break;
       tc_fence_after();
-      const size_t pslot = static_cast<size_t>(grp) * 2 + (sg.i0 > 0 ? 0 : 1);
+      const Partial<MODE> to(a, sg, grp);
+      const bool direct = writes_out<MODE>(sg);
 #pragma unroll 1
       for (int hw = 0; hw < C::CW / 16; ++hw) {
         const int hh = c_off / 16 + hw;
@@ -538,8 +595,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
 #pragma unroll
           for (int b = 0; b < 2; ++b) tmem_ld16(tmem + t_lane + (b2 + b) * HB + hh * 16, o[b]);
           tmem_ld_wait();
-          if (sg.whole) {
-            uint16_t* orow = a.out + (static_cast<size_t>(sg.row) * a.H + hb * HB) * kDv + qd * 32 + lane + b2 * 128;
+          if (direct) {
+            uint16_t* orow = a.out + (static_cast<size_t>(sg.col0) + hb * HB) * kDv + qd * 32 + lane + b2 * 128;
             float inv[16];
             lrow16(inv, &sh.alpha[hh * 16]);
 #pragma unroll
@@ -553,7 +610,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
               }
             }
           } else {
-            float* prow = a.part_o + (pslot * a.H + hb * HB) * kDv + qd * 32 + lane + b2 * 128;
+            float* prow = to.o + static_cast<size_t>(hb * HB) * kDv + qd * 32 + lane + b2 * 128;
 #pragma unroll
             for (int h = 0; h < 16; ++h) {
               const int c = hh * 16 + h;
@@ -565,17 +622,17 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
         }
       }
       if (tid < n_cols) {
-        if (sg.whole) {
+        if (direct) {
           if (a.lse) {
             const float l = sh.l_sum[tid];
-            a.lse[static_cast<size_t>(sg.row) * a.H + hb * HB + tid] =
+            a.lse[static_cast<size_t>(sg.col0) + hb * HB + tid] =
                 l == 0.f ? -INFINITY : (sh.m_used[tid] + log2f(l)) * 0.69314718055994531f;
           }
         } else {
-          const size_t n = static_cast<size_t>(a.n_grp) * 2 * a.H, at = pslot * a.H + hb * HB + tid;
-          a.part_m[at] = sh.m_used[tid];
-          a.part_m[n + at] = sh.l_run[tid];
-          a.part_m[2 * n + at] = sh.l_sum[tid];
+          float* at = to.m + hb * HB + tid;
+          at[0] = sh.m_used[tid];
+          at[to.step] = sh.l_run[tid];
+          at[2 * to.step] = sh.l_sum[tid];
         }
       }
       tc_fence_before();
@@ -604,7 +661,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
           mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
 #pragma unroll 1
           for (int kb = 0; kb < kKB; ++kb)
-            tma_load_2d(sQ + kb * (HB * 128), &tmap_q, &sh.q_full, kb * 64, sg.row * a.H + hb * HB);
+            tma_load_2d(sQ + kb * (HB * 128), &tmap_q, &sh.q_full, kb * 64, sg.col0 + hb * HB);
         }
         __syncwarp();
         ok = wait(&sh.q_full, it & 1);
@@ -639,12 +696,13 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
             for (int kb = 4 * h; kb < 4 + 5 * h; ++kb)
               umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
                                        dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
+            if constexpr (MODE == kWeights) umma_commit_elect(&sh.empty[sb][h]);      // no second product
           }
           if (!ok) break;
           umma_commit_elect(&sh.s_full[sb]);
         }
         if (ok) umma_commit_elect(&sh.q_empty);
-      } else {
+      } else if constexpr (MODE != kWeights) {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           ok = wait(&sh.p_full[g & 1], (g >> 1) & 1);
           if constexpr (FP8) fence_proxy_async_smem();
@@ -674,7 +732,16 @@ __global__ void __launch_bounds__(LCfg<HB, FP8>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == C::PV_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
-  if (threadIdx.x == 0) publish_faults(a, sh.faults);
+  if (threadIdx.x == 0) {
+    if constexpr (MODE == kWeights) {         // (the words are cleared before the kernel)
+      if (sh.faults.bits) {
+        atomicOr(a.status, sh.faults.bits);
+        atomicAdd(a.status + 1, sh.faults.count);
+      }
+    } else {
+      publish_faults<MODE>(a, sh.faults);
+    }
+  }
 }
 
 // row_nt[t] = number of 64-slot tiles up to the last slot of idx row t holding an index >= 0; a block
@@ -861,8 +928,6 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
   if (a.lse && lane == 0) a.lse[orow] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
 }
 
-int head_block(int n_heads) { return n_heads <= 16 ? 16 : n_heads <= 32 ? 32 : 64; }
-
 struct Layout {
   int n_hb, n_grp;
   size_t off_err, off_start, off_m, off_ring, off_o, total;
@@ -890,22 +955,38 @@ Layout latent_layout(int n_q, int n_heads, long long row_tiles_max) {
   return L;
 }
 
-template <int HB, bool FP8, bool SEL>
+template <int HB, bool FP8, int MODE>
 cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq, const LArgs& a,
                      cudaStream_t st) {
-  using C = LCfg<HB, FP8>;
-  cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, SEL>>(C::DYN_SMEM);
+  using C = LCfg<HB, FP8, MODE == kWeights>;
+  cudaError_t e = smem_attr_once<latent_attn_kernel<HB, FP8, MODE>>(C::DYN_SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_attn_kernel<HB, FP8, SEL>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, 1, tkv, tv, tq, a);
+  return launch_pdl(latent_attn_kernel<HB, FP8, MODE>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, 1, tkv, tv, tq, a);
 }
 template <int HB>
-cudaError_t launch_hb(bool fp8, bool sel, const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq,
+cudaError_t launch_hb(bool fp8, int mode, const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq,
                       const LArgs& a, cudaStream_t st) {
-  if (!fp8) return launch_t<HB, false, false>(tkv, tv, tq, a, st);
-  return sel ? launch_t<HB, true, true>(tkv, tv, tq, a, st) : launch_t<HB, true, false>(tkv, tv, tq, a, st);
+  switch (mode) {
+    case kItems: return fp8 ? launch_t<HB, true, kItems>(tkv, tv, tq, a, st) : launch_t<HB, false, kItems>(tkv, tv, tq, a, st);
+    case kWeights:
+      return fp8 ? launch_t<HB, true, kWeights>(tkv, tv, tq, a, st) : launch_t<HB, false, kWeights>(tkv, tv, tq, a, st);
+    default: break;
+  }
+  if (!fp8) return launch_t<HB, false, kEvery>(tkv, tv, tq, a, st);
+  return mode == kSelected ? launch_t<HB, true, kSelected>(tkv, tv, tq, a, st)
+                           : launch_t<HB, true, kEvery>(tkv, tv, tq, a, st);
 }
 
 }  // namespace
+
+cudaError_t launch_latent_single(int hb, bool fp8, int mode, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
+                                 const CUtensorMap& tmap_q, const LArgs& a, cudaStream_t st) {
+  switch (hb) {
+    case 16: return launch_hb<16>(fp8, mode, tmap_kv, tmap_v, tmap_q, a, st);
+    case 32: return launch_hb<32>(fp8, mode, tmap_kv, tmap_v, tmap_q, a, st);
+    default: return launch_hb<64>(fp8, mode, tmap_kv, tmap_v, tmap_q, a, st);
+  }
+}
 
 namespace {
 long long row_tiles_max(const PagedRows& pg, bool selected, int topk) {
@@ -965,11 +1046,9 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   }
   const int ps = prof_begin(kProfAttn, st);
   if (L.n_hb == 2) {
-    e = launch_latent_pair(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st);
-  } else switch (head_block(n_heads)) {
-    case 16: e = launch_hb<16>(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st); break;
-    case 32: e = launch_hb<32>(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st); break;
-    default: e = launch_hb<64>(c.fp8, sel, tmap_kv, tmap_v, tmap_q, a, st); break;
+    e = launch_latent_pair(c.fp8, sel ? kSelected : kEvery, tmap_kv, tmap_v, tmap_q, a, st);
+  } else {
+    e = launch_latent_single(head_block(n_heads), c.fp8, sel ? kSelected : kEvery, tmap_kv, tmap_v, tmap_q, a, st);
   }
   if (e == cudaSuccess && a.n_cta > 1) {
     const int hpb = 8LL * n_q <= L.n_grp ? 1 : 8;      // eight partials a row and more, or fewer

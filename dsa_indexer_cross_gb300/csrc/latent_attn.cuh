@@ -80,12 +80,25 @@ __device__ __forceinline__ void lrow16(float (&r)[16], const float* p) {
   }
 }
 
+// What a row of the line is: a query row with every key of its sequence, or with its selected ones; an item of a
+// shared-prefix call (latent_shared.cu): some columns, (row, head) pairs that follow one another in q, over some
+// tiles of one row's table; a query row whose keys' weights are wanted.
+enum WalkMode : int { kEvery = 0, kSelected = 1, kItems = 2, kWeights = 3 };
+
+// An item: {first column, columns | flags, table row, first tile}.
+constexpr int kItemSole = 1 << 16;     // nothing else adds to its columns
+constexpr int kItemOwn = 1 << 17;      // a row's own keys (clear: a group's prefix)
+
 struct LArgs {
   const uint8_t* latent;       // bf16 rows (unused by the kernel: TMA), or e4m3 codes
   const uint8_t* scale;
   const uint16_t* rope;
   const int32_t* idx;          // selected offsets [n_q][topk], or nullptr
-  const int32_t* row_nt;       // SEL: 64-slot tiles of each row
+  const int32_t* row_nt;       // selected keys: 64-slot tiles of each row; items: tiles of each
+  const int4* items;           // kItems, and how many there are
+  const int32_t* n_items;
+  float* whole_o;              // kItems: an item that one share holds, by column: [prefix, own][n_q * H][512]
+  float* whole_m;              // [prefix, own][3][n_q * H], as part_m
   PagedRows pg;
   uint16_t* out;
   float* lse;
@@ -93,8 +106,14 @@ struct LArgs {
   float scale_log2;
   int2* start;                 // [n_grp]: (row, tile) each group starts at; groups without a share: row INT_MAX
   uint16_t* ring;              // fp8, CTA pairs: [n_grp][kRing][64][576] bf16
-  float* part_o;               // [n_grp * 2][H][512]
+  float* part_o;               // [n_grp * 2][H][512]        (kItems: part_cols columns for H)
   float* part_m;               // [3][n_grp * 2][H]: max in use (log2), sum of the rounded weights, plain sum
+  int part_cols;
+  const float* lse_in;         // kWeights: [n_q][H]
+  const float* w_in;           // [n_q] rows w_stride apart; nullptr: zeros
+  float* w_out;
+  float* w_part;               // two blocks of heads: [2][n_q] rows w_stride apart
+  long long w_stride;
   uint32_t* status;
   uint32_t* err;               // [CTAs][2]: error bits, bad-index count
   int n_cta;
@@ -105,9 +124,9 @@ struct LArgs {
 __device__ __forceinline__ int row_len(const PagedRows& pg, int row) {
   return max(0, min(gload(pg.seq_len + row), pg.max_pages << kPageShift));
 }
-template <bool SEL>
+template <int MODE>
 __device__ __forceinline__ int row_tiles(const LArgs& a, int row) {
-  if constexpr (SEL) return gload(a.row_nt + row);
+  if constexpr (MODE == kSelected || MODE == kItems) return gload(a.row_nt + row);
   return (row_len(a.pg, row) + kRows - 1) / kRows;
 }
 
@@ -122,10 +141,12 @@ __device__ __forceinline__ int whole_row_extra(int groups) { return groups / 9; 
 
 // The segments (consecutive tiles of one row) of this CTA's share, in order.
 struct Seg {
-  int row, i0, n;
+  int row, i0, n;    // row: of the block table; i0: its tile
+  bool begins;       // with the row's first tile
   bool whole;        // the row's every tile
+  int col0, ncol;    // columns of q and out; kItems: ncol with the item's flags
 };
-template <bool SEL>
+template <int MODE>
 struct Walk {
   const LArgs& a;
   int row, tile;
@@ -133,19 +154,59 @@ struct Walk {
   __device__ __forceinline__ Walk(const LArgs& args, int r, int t, long long n) : a(args), row(r), tile(t), left(n) {}
   __device__ __forceinline__ bool next(Seg& s) {
     if (left <= 0) return false;
-    int T = row_tiles<SEL>(a, row);
+    int T = row_tiles<MODE>(a, row);
 #pragma unroll 1
-    while (T == 0) T = row_tiles<SEL>(a, ++row);
+    while (T == 0) T = row_tiles<MODE>(a, ++row);
     s.row = row;
     s.i0 = tile;
     s.n = static_cast<int>(min(static_cast<long long>(T - tile), left));
+    s.begins = tile == 0;
     s.whole = tile == 0 && s.n == T;
+    if constexpr (MODE == kItems) {
+      const int4 it = gload(a.items + row);
+      s.col0 = it.x;
+      s.ncol = it.y;
+      s.row = it.z;
+      s.i0 += it.w;
+    } else {
+      s.col0 = row * a.H;
+      s.ncol = a.H;
+    }
     left -= s.n;
     ++row;
     tile = 0;
     return true;
   }
 };
+// Where a segment's unnormalised columns go (the first of `cols`), and where its three numbers a column:
+// at m[0], m[step] and m[2 step].
+template <int MODE>
+struct Partial {
+  float *o, *m;
+  size_t step;
+  __device__ __forceinline__ Partial(const LArgs& a, const Seg& s, int grp) {
+    const int cols = MODE == kItems ? a.part_cols : a.H;
+    if (MODE == kItems && s.whole) {
+      const size_t all = static_cast<size_t>(a.n_q) * a.H, own = s.ncol & kItemOwn ? 1 : 0;
+      o = a.whole_o + (own * all + s.col0) * kDv;
+      m = a.whole_m + own * 3 * all + s.col0;
+      step = all;
+    } else {
+      const size_t slot = static_cast<size_t>(grp) * 2 + (s.begins ? 1 : 0);
+      o = a.part_o + slot * cols * kDv;
+      m = a.part_m + slot * cols;
+      step = static_cast<size_t>(a.n_grp) * 2 * cols;
+    }
+  }
+};
+template <int MODE>
+__device__ __forceinline__ bool writes_out(const Seg& s) {
+  return s.whole && (MODE != kItems || (s.ncol & kItemSole));
+}
+template <int MODE>
+__device__ __forceinline__ int columns(const Seg& s) {
+  return MODE == kItems ? s.ncol & 0xFFFF : s.ncol;
+}
 
 // Faults are collected per CTA; the CTAs' words are put together by the join kernel (or, when
 // there is one CTA, written as they are), so no clearing pass runs before the kernel.
@@ -156,8 +217,9 @@ __device__ __forceinline__ void report(CtaFaults& f, uint32_t bits) {
   atomicOr(&f.bits, bits);
   atomicAdd(&f.count, 1u);
 }
+template <int MODE>
 __device__ __forceinline__ void publish_faults(const LArgs& a, const CtaFaults& f) {
-  uint32_t* w = gridDim.x == 1 ? a.status : a.err + 2 * blockIdx.x;
+  uint32_t* w = MODE != kItems && gridDim.x == 1 ? a.status : a.err + 2 * blockIdx.x;
   w[0] = f.bits;
   w[1] = f.count;
 }
@@ -170,29 +232,31 @@ struct Share {
   int row0, tile0;
 };
 // Groups in use, and whether they take a row each.
-__device__ __forceinline__ int share_groups(const LArgs& a, long long total, int tallest, bool& by_row) {
-  const long long most = min_share(total, a.n_q) == 4 ? (total + 3) >> 2 : (total + 1) >> 1;
+template <int MODE>
+__device__ __forceinline__ int share_groups(const LArgs& a, int n_rows, long long total, int tallest, bool& by_row) {
+  const long long most = min_share(total, n_rows) == 4 ? (total + 3) >> 2 : (total + 1) >> 1;
   const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), most));
-  by_row = a.n_hb == 2 && a.n_q <= a.n_grp &&
+  by_row = MODE != kWeights && a.n_hb == 2 && n_rows <= a.n_grp &&
            tallest <= share_start(total, 1, max(groups, 1)) + whole_row_extra(groups);
-  return by_row ? a.n_q : groups;
+  return by_row ? n_rows : groups;
 }
 __device__ __forceinline__ bool bad_length(const LArgs& a, int row) {
   const int want = gload(a.pg.seq_len + row);
   return want < 0 || want > (a.pg.max_pages << kPageShift);
 }
-template <bool SEL, int THREADS>
+template <int MODE, int THREADS>
 __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool writes_start, Share& sh, CtaFaults& faults) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long share = 0;
   int groups;
-  if (a.n_q <= 32) {
+  const int n_rows = MODE == kItems ? gload(a.n_items) : a.n_q;
+  if (n_rows <= 32) {
     // A row a lane, each warp for itself: no barrier, no trip through shared memory (300 keys, 16 heads: 11.6 ->
     // 10.8 us).
-    const int T = lane < a.n_q ? row_tiles<SEL>(a, lane) : 0;
+    const int T = lane < n_rows ? row_tiles<MODE>(a, lane) : 0;
     const uint32_t total = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(T));     // 32 x 2^25 at most
     bool by_row;
-    groups = share_groups(a, total, __reduce_max_sync(0xffffffffu, T), by_row);
+    groups = share_groups<MODE>(a, n_rows, total, __reduce_max_sync(0xffffffffu, T), by_row);
     uint32_t pre = T;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -216,22 +280,22 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
       sh.tile0 = tile0;
       if (writes_start && grp < groups) a.start[grp] = make_int2(row0, tile0);
     }
-    if (blockIdx.x == 0 && warp == 0) {
+    if (MODE != kItems && blockIdx.x == 0 && warp == 0) {
       __syncwarp();        // (thread 0 has set faults)
       if (lane < a.n_q && bad_length(a, lane)) report(faults, DEV_ERR_RANGE);
     }
   } else {
-    const int per = (a.n_q + THREADS - 1) / THREADS;
-    const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
+    const int per = (n_rows + THREADS - 1) / THREADS;
+    const int ra = min(n_rows, static_cast<int>(threadIdx.x) * per), rb = min(n_rows, ra + per);
     long long mine = 0;
     int tallest = 0;
     bool bad_len = false;
 #pragma unroll 1
     for (int r = ra; r < rb; ++r) {
-      const int T = row_tiles<SEL>(a, r);
+      const int T = row_tiles<MODE>(a, r);
       mine += T;
       tallest = max(tallest, T);
-      if (blockIdx.x == 0 && bad_length(a, r)) bad_len = true;
+      if (MODE != kItems && blockIdx.x == 0 && bad_length(a, r)) bad_len = true;
     }
     long long pre = mine;
 #pragma unroll
@@ -253,9 +317,9 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
       tallest = max(tallest, sh.wmax[w]);
     }
     bool by_row;
-    groups = share_groups(a, total, tallest, by_row);
+    groups = share_groups<MODE>(a, n_rows, total, tallest, by_row);
     if (by_row) {
-      share = grp < groups ? row_tiles<SEL>(a, grp) : 0;
+      share = grp < groups ? row_tiles<MODE>(a, grp) : 0;
       if (threadIdx.x == 0 && grp < groups) {
         sh.row0 = grp;
         sh.tile0 = 0;
@@ -268,7 +332,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
         long long at = pre;
         int r = ra;
         while (true) {
-          const int T = row_tiles<SEL>(a, r);
+          const int T = row_tiles<MODE>(a, r);
           if (first < at + T) break;
           at += T;
           ++r;
@@ -280,15 +344,17 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
     }
   }
   if (writes_start && threadIdx.x == 0 && grp >= groups) a.start[grp] = make_int2(0x7FFFFFFF, 0);
-  // rows without keys: zeros and -inf
+  // rows without keys: zeros and -inf (of items: the join's)
+  if constexpr (MODE == kEvery || MODE == kSelected) {
 #pragma unroll 1
-  for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
-    if (row_tiles<SEL>(a, t) != 0) continue;
-    uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.H * kDv);
+    for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
+      if (row_tiles<MODE>(a, t) != 0) continue;
+      uint4* o = reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.H * kDv);
 #pragma unroll 1
-    for (int e = threadIdx.x; e < a.H * (kDv / 8); e += THREADS) o[e] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int h = threadIdx.x; h < a.H; h += THREADS) a.lse[static_cast<size_t>(t) * a.H + h] = -INFINITY;
+      for (int e = threadIdx.x; e < a.H * (kDv / 8); e += THREADS) o[e] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int h = threadIdx.x; h < a.H; h += THREADS) a.lse[static_cast<size_t>(t) * a.H + h] = -INFINITY;
+    }
   }
   return share;
 }
@@ -319,9 +385,16 @@ __device__ __forceinline__ int tile_rows(const LArgs& a, int len, int i, int pag
   return max(0, min(kRows, len - i * kRows));
 }
 
+// Columns of a CTA of the kernel for up to 64 heads.
+inline int head_block(int n_heads) { return n_heads <= 16 ? 16 : n_heads <= 32 ? 32 : 64; }
+// That kernel, with hb columns a CTA (latent_attn.cu).  tmap_kv / tmap_v: a bf16 cache in boxes {64, 64, 1}
+// and {64, 64, 4}.
+cudaError_t launch_latent_single(int hb, bool fp8, int mode, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
+                                 const CUtensorMap& tmap_q, const LArgs& a, cudaStream_t st);
+
 // The CTA-pair kernel for 65 .. 128 heads (latent_pair.cu).  tmap_s / tmap_v: a bf16 cache in boxes
 // {64, 32, 9} and {64, 64, 4}.
-cudaError_t launch_latent_pair(bool fp8, bool sel, const CUtensorMap& tmap_s, const CUtensorMap& tmap_v,
+cudaError_t launch_latent_pair(bool fp8, int mode, const CUtensorMap& tmap_s, const CUtensorMap& tmap_v,
                                const CUtensorMap& tmap_q, const LArgs& a, cudaStream_t st);
 
 }  // namespace dsa

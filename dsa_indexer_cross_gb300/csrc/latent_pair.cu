@@ -157,11 +157,12 @@ __device__ __forceinline__ void commit_pair_elect(uint64_t* bar) {
 }
 
 // ------------------------------------------------------------------------------- the kernel
-template <bool FP8, bool SEL>
+template <bool FP8, int MODE>
 __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     latent_pair_kernel(const __grid_constant__ CUtensorMap tmap_s, const __grid_constant__ CUtensorMap tmap_v,
                        const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ LArgs a) {
   using C = PCfg<FP8>;
+  constexpr bool SEL = MODE == kSelected;
   extern __shared__ __align__(1024) uint8_t smem[];
   PShared& sh = *reinterpret_cast<PShared*>(smem + kOffShared);
   uint8_t* sQ = smem;
@@ -206,13 +207,13 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   }
   grid_trigger();
   grid_wait();
-  const long long share = find_share<SEL, C::THREADS>(a, grp, rank == 0, sh.share, sh.faults);
+  const long long share = find_share<MODE, C::THREADS>(a, grp, rank == 0, sh.share, sh.faults);
   __syncthreads();
   tc_fence_before();
   cluster_sync_all();                    // barriers and TMEM of both CTAs are there
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
-  Walk<SEL> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
+  Walk<MODE> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       mbar_arrive_expect_tx(&sh.q_full, kQBytes);
 #pragma unroll 1
       for (int kb = 0; kb < kKB; ++kb)
-        tma_load_2d(sQ + kb * (kHeads * 128), &tmap_q, &sh.q_full, kb * 64, sg.row * a.H + static_cast<int>(rank) * kHeads);
+        tma_load_2d(sQ + kb * (kHeads * 128), &tmap_q, &sh.q_full, kb * 64, sg.col0 + static_cast<int>(rank) * kHeads);
     }
     __syncwarp();
     const bool ok = wait(&sh.q_full, it & 1);
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     uint16_t* ring = a.ring + (static_cast<size_t>(grp * kRing) * kRows + 32 * rank) * kDqk;
     const uint32_t quarter = slot & 3, first = slot >> 2;      // spread: these rows of tiles first, first + 2, ...
     uint32_t my_row = 8 * quarter + (lane & 7), my_tile = first + 2 * (lane >> 3);
-    Walk<SEL> aw(walk);
+    Walk<MODE> aw(walk);
     Seg as;
     int ai = 0;
     bool alive = aw.next(as), ok = true;
@@ -535,18 +536,20 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       if (stop) break;
       tc_fence_after();
       const int dim0 = (qd >> 1) * 256 + cw * 128;               // this thread's OC dims
-      const size_t pslot = static_cast<size_t>(grp) * 2 + (sg.i0 > 0 ? 0 : 1);
+      const Partial<MODE> to(a, sg, grp);
+      const bool direct = writes_out<MODE>(sg);
+      const bool live = ghead < columns<MODE>(sg);
       const float inv = l == 0.f ? 0.f : 1.f / l;                // a NaN sum stays NaN; no key: zeros
-      uint16_t* orow = a.out + (static_cast<size_t>(sg.row) * a.H + ghead) * kDv + dim0;
-      float* prow = a.part_o + (pslot * a.H + ghead) * kDv + dim0;
+      uint16_t* orow = a.out + (static_cast<size_t>(sg.col0) + ghead) * kDv + dim0;
+      float* prow = to.o + static_cast<size_t>(ghead) * kDv + dim0;
 #pragma unroll 1
       for (int b = 0; b < kOC / 32; ++b) {
         uint32_t o[32];
         tmem_ld32(tmem + t_lane + cw * 128 + b * 32, o);
         tmem_ld_wait();
-        if (ghead >= a.H) continue;
+        if (!live) continue;
         // a lane's dims are 32-byte pieces of its head's row
-        if (sg.whole) {
+        if (direct) {
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             uint32_t w[8];
@@ -565,16 +568,15 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           for (int v = 0; v < 4; ++v) stg256(prow + b * 32 + 8 * v, o + 8 * v);
         }
       }
-      if (part == 0 && ghead < a.H) {
-        if (sg.whole) {
+      if (part == 0 && live) {
+        if (direct) {
           if (a.lse)
-            a.lse[static_cast<size_t>(sg.row) * a.H + ghead] =
+            a.lse[static_cast<size_t>(sg.col0) + ghead] =
                 l2 == 0.f ? -INFINITY : (m_used + log2f(l2)) * 0.69314718055994531f;
         } else {
-          const size_t n = static_cast<size_t>(a.n_grp) * 2 * a.H, at = pslot * a.H + ghead;
-          a.part_m[at] = m_used;
-          a.part_m[n + at] = l;
-          a.part_m[2 * n + at] = l2;
+          to.m[ghead] = m_used;
+          to.m[to.step + ghead] = l;
+          to.m[2 * to.step + ghead] = l2;
         }
       }
       tc_fence_before();
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) publish_faults(a, sh.faults);
+  if (threadIdx.x == 0) publish_faults<MODE>(a, sh.faults);
   cluster_sync_all();                    // no thread of either CTA signals, reads or is read any more
   // The leader has issued every commit and seen its own copy of mma_done.  The peer's shared memory may only be
   // given up when its copy is there too: both issuing warps' last commit, behind all others of theirs.
@@ -649,19 +651,22 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   if (warp == C::PV_WARP) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-template <bool FP8, bool SEL>
+template <bool FP8, int MODE>
 cudaError_t launch_t(const CUtensorMap& ts, const CUtensorMap& tv, const CUtensorMap& tq, const LArgs& a, cudaStream_t st) {
-  cudaError_t e = smem_attr_once<latent_pair_kernel<FP8, SEL>>(kDynSmem);
+  cudaError_t e = smem_attr_once<latent_pair_kernel<FP8, MODE>>(kDynSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(latent_pair_kernel<FP8, SEL>, dim3(a.n_cta), PCfg<FP8>::THREADS, kDynSmem, st, 2, ts, tv, tq, a);
+  return launch_pdl(latent_pair_kernel<FP8, MODE>, dim3(a.n_cta), PCfg<FP8>::THREADS, kDynSmem, st, 2, ts, tv, tq, a);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_pair(bool fp8, bool sel, const CUtensorMap& tmap_s, const CUtensorMap& tmap_v,
+cudaError_t launch_latent_pair(bool fp8, int mode, const CUtensorMap& tmap_s, const CUtensorMap& tmap_v,
                                const CUtensorMap& tmap_q, const LArgs& a, cudaStream_t st) {
-  if (!fp8) return launch_t<false, false>(tmap_s, tmap_v, tmap_q, a, st);
-  return sel ? launch_t<true, true>(tmap_s, tmap_v, tmap_q, a, st) : launch_t<true, false>(tmap_s, tmap_v, tmap_q, a, st);
+  if (mode == kItems)
+    return fp8 ? launch_t<true, kItems>(tmap_s, tmap_v, tmap_q, a, st) : launch_t<false, kItems>(tmap_s, tmap_v, tmap_q, a, st);
+  if (!fp8) return launch_t<false, kEvery>(tmap_s, tmap_v, tmap_q, a, st);
+  return mode == kSelected ? launch_t<true, kSelected>(tmap_s, tmap_v, tmap_q, a, st)
+                           : launch_t<true, kEvery>(tmap_s, tmap_v, tmap_q, a, st);
 }
 
 }  // namespace dsa

@@ -1,0 +1,231 @@
+"""GPU tests of latent attention over shared prefixes (dsa_latent_attn_shared) against float64: every row is
+its own attention over all of its keys, whatever is shared.  Every unused cache row is NaN."""
+import numpy as np
+import pytest
+import torch
+
+import dsa_indexer_cross_gb300 as D
+from latent_cases import DEV, P, TAU, check_exceptional, check_rows, gen, i32, randn
+from shared_cases import SharedPaged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dsa_indexer_cross_gb300.build import build
+    build()
+    assert torch.cuda.is_available()
+
+
+def _check(groups, H, fmt, seed=1, check=None, bits=0, **kw):
+    sp = SharedPaged(groups, fmt, seed=seed)
+    q = randn((len(sp.lens), H, 576), gen(seed + 50))
+    out, lse, ws = sp.attend(q, **kw)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == bits
+    check_rows(out, lse, q, [sp.stored(t) if check is None or t in check else None for t in range(len(sp.lens))])
+    return sp, q, out, lse
+
+
+MIXED = [
+    (0, [70], False), (300, [300, 301, 450, 0, 1, 299, 600], False), (128, [128, 128], False), (63, [64, 65, 90], False),
+    (1000, [1200], False), (640, [650, 640, 1000], False), (500, [501, 502, 503, 504], True), (0, [5, 0, 200], False),
+    (129, [0, 0, 0], False), (2000, [100, 200, 300, 2100], False), (64, [64, 64, 64], True), (256, [], False), (192, [193, 250], False)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H", [1, 3, 8, 16, 17, 32, 33, 64, 65, 100, 128])
+def test_groups_of_every_kind(H, fmt):
+    _check(MIXED, H, fmt, seed=H)
+
+
+@pytest.mark.parametrize("max_rows", [1, 2, 4, 1000])
+@pytest.mark.parametrize("H", [5, 16, 64, 100])
+def test_the_hint_only_chooses_kernels(H, max_rows):
+    _check(MIXED, H, "fp8", seed=3, max_rows=max_rows)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("rows,H,prefix", [(4, 16, 5000), (48, 16, 8000), (2, 1, 700), (8, 64, 20000), (16, 100, 6000),
+                                           (3, 128, 3000), (70, 3, 12345), (130, 8, 1000), (2, 16, 129)])
+def test_one_group(rows, H, prefix, fmt):
+    rng = np.random.default_rng(rows)
+    lens = (prefix + rng.integers(0, 700, rows)).tolist()
+    _check([(prefix, lens, False)], H, fmt, seed=rows, check=set(range(0, rows, max(1, rows // 6))))
+    _check([(prefix, [prefix + 1 + i for i in range(rows)], True)], H, fmt, seed=rows + 1,
+           check=set(range(0, rows, max(1, rows // 6))))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_many_groups_and_rows(fmt):
+    rng = np.random.default_rng(7)
+    groups = []
+    for _ in range(1200):
+        p = int(rng.integers(0, 400))
+        groups.append((p, (p + rng.integers(0, 90, int(rng.integers(0, 4)))).tolist(), bool(rng.random() < 0.3)))
+    n = sum(len(g[1]) for g in groups)
+    for H in (4, 40):
+        _check(groups, H, fmt, seed=H, check=set(range(0, n, 97)) | {0, n - 1})
+
+
+def test_rows_outside_the_groups():
+    sp = SharedPaged(MIXED, "bf16", seed=5)
+    q = randn((len(sp.lens), 16, 576), gen(9))
+    out, lse, ws = sp.attend(q, start=sp.start_d[3:8].contiguous(), prefix=sp.prefix_d[3:7].contiguous())
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [sp.stored(t) for t in range(len(sp.lens))])
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    out, lse, ws = sp.attend(q, start=torch.zeros(1, dtype=torch.int32, device=DEV), prefix=e, max_rows=1)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [sp.stored(t) for t in range(len(sp.lens))])
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+def test_equals_the_unshared_call(H):
+    """Same inputs, same roundings of the weights, other sums: within both calls' bounds of float64; and with no
+    group at all each row is walked as there."""
+    sp = SharedPaged([(900, [900 + 37 * i for i in range(9)], False)], "fp8", seed=2)
+    q = randn((9, H, 576), gen(3))
+    out, lse, _ = sp.attend(q)
+    desc = D.attn_desc(9, sp.n_pages * P, H, 0, TAU)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    D.dsa_latent_attn_paged(desc, q, sp.cache, None, sp.pages, o2, l2)
+    check_rows(out, lse, q, [sp.stored(t) for t in range(9)])
+    assert torch.all((lse - l2).abs() <= 2.0 ** -12)
+    assert torch.all((out.float() - o2.float()).abs() <= 2.0 ** -6)
+
+
+@pytest.mark.parametrize("H", [8, 40, 100])
+def test_bad_groups_pages_and_lengths(H):
+    sp = SharedPaged(MIXED, "bf16", seed=6)
+    n = len(sp.lens)
+    q = randn((n, H, 576), gen(8))
+    want = [sp.stored(t) for t in range(n)]
+    for bad in ([0, 5, 4] + sp.start[3:], [-1] + sp.start[1:], sp.start[:-1] + [n + 1], [n] + sp.start[1:]):
+        out, lse, ws = sp.attend(q, start=i32(bad))
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+        check_rows(out, lse, q, want)
+    pre = list(sp.prefix)
+    pre[1] = -3
+    out, lse, ws = sp.attend(q, prefix=i32(pre))
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+    check_rows(out, lse, q, want)
+    # lengths beyond the table are cut to it, negative ones are empty
+    lens = sp.len_d.clone()
+    t0 = sp.start[4]
+    sp.len_d[t0] = -1
+    out, lse, ws = sp.attend(q)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+    check_rows(out, lse, q, [w if t != t0 else w[:0] for t, w in enumerate(want)])
+    sp.len_d.copy_(lens)
+    # a page outside the cache, in a prefix that several rows walk: its keys are left out of all of them
+    g = 5                                     # prefix 640, lengths 650, 640, 1000
+    rows = list(range(sp.start[g], sp.start[g + 1]))
+    keep = sp.bt_d.clone()
+    for r in rows:
+        sp.bt_d[r, 1] = sp.n_pages
+    out, lse, ws = sp.attend(q)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    check_rows(out, lse, q, [np.concatenate([w[:P], w[2 * P:]]) if t in rows else w for t, w in enumerate(want)])
+    sp.bt_d.copy_(keep)
+    out, lse, ws = sp.attend(q)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H", [16, 100])
+def test_infinities_and_nan_stay_with_their_rows(H, fmt):
+    groups = [(400, [400, 520, 70, 0, 410], False), (200, [201, 202, 203], True)]
+    sp = SharedPaged(groups, fmt, seed=4)
+    q = randn((len(sp.lens), H, 576), gen(5))
+    # an own key of row 1, and one of the last draft, are NaN or infinite; row 4's own key is -inf in a rotary dim
+    def row(t, j):
+        return int(sp.bt[t, j // P]) * P + j % P
+    store = sp.rows if fmt == "bf16" else sp.rope
+    off = 512 if fmt == "bf16" else 0
+    store[row(1, 500), off + 3] = float("nan")
+    store[row(7, 202), off + 5] = float("inf")
+    store[row(4, 405), off + 1] = -float("inf")
+    out, lse, ws = sp.attend(q)
+    assert D.dsa_workspace_status(ws) == 0
+    check_exceptional(out, lse, q, [sp.stored(t) for t in range(len(sp.lens))])
+    assert torch.all(torch.isnan(out[1])) and torch.all(torch.isfinite(out[0])) and torch.all(torch.isfinite(out[5:7]))
+
+
+def test_two_streams_graphs_and_a_shared_workspace():
+    sps = [SharedPaged([(700, [700 + 11 * i for i in range(6)], False)], "fp8", seed=s) for s in (1, 2)]
+    H = 24
+    qs = [randn((6, H, 576), gen(s + 20)) for s in (1, 2)]
+    want = [tuple(x.clone() for x in sp.attend(q)[:2]) for sp, q in zip(sps, qs)]
+    streams = [torch.cuda.Stream() for _ in sps]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got.append((k, sps[k].attend(qs[k])))
+    torch.cuda.synchronize()
+    for k, (out, lse, _) in got:
+        assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+    # captured, two calls on one workspace, then other queries and lengths in place
+    sp, q = sps[0], qs[0].clone()
+    ws = sp.attend(q)[2]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a = sp.attend(q, ws=ws)
+        b = sp.attend(q, ws=ws)
+    q.copy_(qs[1])
+    sp.len_d[2] = 300                       # shorter than the prefix now
+    g.replay()
+    torch.cuda.synchronize()
+    assert D.dsa_workspace_status(ws) == 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    kv = [sp.stored(t)[:300] if t == 2 else sp.stored(t) for t in range(6)]
+    check_rows(a[0], a[1], q, kv)
+
+
+def test_without_lse_and_empty_calls():
+    sp = SharedPaged([(300, [310, 400], False)], "bf16", seed=1)
+    q = randn((2, 16, 576), gen(2))
+    out, lse, ws = sp.attend(q)
+    o2, none, _ = sp.attend(q, lse=False)
+    assert none is None and torch.equal(out, o2)
+    e = torch.empty((0, 16, 576), dtype=torch.bfloat16, device=DEV)
+    desc = D.attn_desc(0, sp.n_pages * P, 16, 0, TAU)
+    groups = D.shared_rows(torch.zeros(1, dtype=torch.int32, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV), 1)
+    ws.fill_(255)
+    D.dsa_latent_attn_shared(desc, e, sp.cache, groups, sp.pages, torch.empty((0, 16, 512), dtype=torch.bfloat16, device=DEV), ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    sp = SharedPaged([(300, [0, 0, 0], False)], "bf16", seed=1)
+    out, lse, ws = sp.attend(randn((3, 16, 576), gen(2)))
+    assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+
+
+def test_results_repeat():
+    sp = SharedPaged([(3000, [3000 + 100 * i for i in range(20)], False), (500, [600] * 5, False)], "fp8", seed=1)
+    for H in (16, 64, 128):
+        q = randn((25, H, 576), gen(H))
+        out, lse, _ = sp.attend(q)
+        for _ in range(4):
+            o2, l2, _ = sp.attend(q)
+            assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("H", [8, 40, 100])
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_a_wait_that_runs_out_is_reported(H, fmt):
+    """The rows' producers stop at the start (a test hook; a share may hold no more than two tiles); the waits behind
+    them run out after a millisecond."""
+    sp = SharedPaged([(9000, [9000 + 50 * i for i in range(6)], False)], fmt, seed=3)
+    q = randn((6, H, 576), gen(4))
+    ref = sp.attend(q)
+    D.dsa_debug_pipeline(0, 1_000_000)
+    try:
+        _, _, ws = sp.attend(q, ws=ref[2])
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) & 1
+    finally:
+        D.dsa_debug_pipeline(-1, 0)
+    out, lse, ws = sp.attend(q, ws=ref[2])
+    assert D.dsa_workspace_status(ws) == 0
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
