@@ -321,7 +321,7 @@ def _prepare_verify(s, g):
 
 
 def _handle(D, c):
-    return D.latent_cache(c["rows"]) if "rows" in c else D.latent_cache(c["codes"], c["scale"], c["rope"])
+    return D.latent_cache(c["codes"], c["scale"], c["rope"]) if "codes" in c else D.latent_cache(c["rows"])
 
 
 def _plan(s):
