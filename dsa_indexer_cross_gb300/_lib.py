@@ -41,7 +41,7 @@ EXPORTED = ("dsa_status_string", "dsa_last_error", "dsa_donor_table", "dsa_rope_
             "dsa_sparse_attn_backward_workspace_size", "dsa_rope_table_scaled", "dsa_rope_apply",
             "dsa_latent_cache_write", "dsa_latent_cache_read", "dsa_latent_attn_workspace_size",
             "dsa_latent_attn_paged", "dsa_mtp_verify", "dsa_latent_attn_shared_workspace_size",
-            "dsa_latent_attn_shared")
+            "dsa_latent_attn_shared", "dsa_latent_key_weights_workspace_size", "dsa_latent_key_weights")
 
 PROFILE_KINDS = {0: "rope", 1: "ranges", 2: "indexer", 3: "select", 4: "attn_prep", 5: "attn", 6: "attn_bwd",
                  7: "proj", 8: "indexer_bwd", 9: "cache", 10: "verify"}
@@ -196,6 +196,11 @@ def lib() -> C.CDLL:
         L.dsa_latent_attn_shared_workspace_size.argtypes = [P(AttnDesc), P(SharedRows), P(sz)]
         L.dsa_latent_attn_shared.restype = st
         L.dsa_latent_attn_shared.argtypes = [P(AttnDesc), vp, P(LatentCache), P(SharedRows), P(PagedCache), vp, vp, vp, sz,
+                                             vp]
+        L.dsa_latent_key_weights_workspace_size.restype = st
+        L.dsa_latent_key_weights_workspace_size.argtypes = [P(AttnDesc), P(PagedCache), P(sz)]
+        L.dsa_latent_key_weights.restype = st
+        L.dsa_latent_key_weights.argtypes = [P(AttnDesc), vp, P(LatentCache), P(PagedCache), vp, vp, vp, C.c_int64, vp, sz,
                                              vp]
         L.dsa_mtp_verify.restype = st
         L.dsa_mtp_verify.argtypes = [P(VerifyDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -799,6 +804,44 @@ def dsa_latent_attn_shared(desc: AttnDesc, q, cache: LatentCache, groups: Shared
         ws = _workspace(dsa_latent_attn_shared_workspace_size(desc, groups), q.device, stream)
     st = (_lib or lib()).dsa_latent_attn_shared(desc, p_q, cache, groups, pages, p_out, p_lse,
                                                 _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
+    return ws
+
+
+def dsa_latent_key_weights_workspace_size(desc: AttnDesc, pages: PagedCache) -> int:
+    n = C.c_size_t(0)
+    _check(lib().dsa_latent_key_weights_workspace_size(C.byref(desc), C.byref(pages), C.byref(n)))
+    return n.value
+
+
+def _weight_rows(t: torch.Tensor, rows: int, width: int, name: str, dev: int) -> int:
+    """Elements between the rows of a float32 [rows or more, width or more] view with contiguous rows."""
+    if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[0] < rows or t.shape[1] < width or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a float32 view of at least {(rows, width)} on cuda:{dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.stride(0) if rows > 1 else max(width, t.shape[1])
+
+
+def dsa_latent_key_weights(desc: AttnDesc, q, cache: LatentCache, pages: PagedCache, lse, weight_in, weight_out,
+                           ws=None, stream=None) -> torch.Tensor:
+    """weight_out[t, j] = weight_in[t, j] (None: zeros) + the attention weights of key j over row t's heads.
+    weight_in and weight_out: float32 [rows, max_pages * 128 or more] of the same row stride, or the same tensor."""
+    n, width = desc.n_q, pages.max_pages * DSA_PAGE_ROWS
+    dev = _current_device(q, "q", cache, pages)
+    p_q, p_lse = (_arg(q, torch.bfloat16, n * desc.n_heads * desc.d_qk, "q", dev),
+                  _arg(lse, torch.float32, n * desc.n_heads, "lse", dev))
+    stride = _weight_rows(weight_out, n, width, "weight_out", dev)
+    if weight_in is not None and _weight_rows(weight_in, n, width, "weight_in", dev) != stride and n > 1:
+        raise ValueError("weight_in and weight_out must have the same row stride")
+    _paged_args(pages, n)
+    if ws is None:
+        ws = _workspace(dsa_latent_key_weights_workspace_size(desc, pages), q.device, stream)
+    st = (_lib or lib()).dsa_latent_key_weights(desc, p_q, cache, pages, p_lse,
+                                                None if weight_in is None else weight_in.data_ptr(), weight_out.data_ptr(),
+                                                stride, _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
         _check(st)
     return ws

@@ -38,6 +38,7 @@
 #include <algorithm>
 
 #include "latent_attn.cuh"
+#include "status.cuh"
 
 namespace dsa {
 namespace {
@@ -356,9 +357,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         const float l = h < a.H ? gload(a.lse_in + sg.col0 + h) * 1.4426950408889634f : INFINITY;
         lse2[c] = l == -INFINITY ? INFINITY : l;
       }
-      const size_t base = static_cast<size_t>(sg.row) * a.w_stride;
-      float* to = a.n_hb == 1 ? a.w_out + base : a.w_part + static_cast<size_t>(hb) * a.n_q * a.w_stride + base;
-      const float* from = a.n_hb == 1 && a.w_in ? a.w_in + base : nullptr;
+      float* to = a.n_hb == 1 ? a.w_out + sg.row * a.w_stride : a.w_part + (static_cast<long long>(hb) * a.n_q + sg.row) * a.w_pitch;
+      const float* from = a.n_hb == 1 && a.w_in ? a.w_in + sg.row * a.w_stride : nullptr;
       for (int n = 0; n < sg.n; ++n, ++g) {
         const int i = sg.i0 + n, sb = g & 1;
         const int nv = tile_rows(a, len, i, gload(bt + (i >> 1)));
@@ -1000,6 +1000,73 @@ LatentRing latent_attn_ring(int n_q, int n_heads, const PagedRows& pg, bool sele
 }
 
 int latent_attn_q_box_rows(int n_heads) { return head_block(n_heads); }
+
+namespace {
+// More than 64 heads are two blocks of columns on two CTAs; their sums are put together here, in one order.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) weights_sum_kernel(const __grid_constant__ LArgs a, int per_row) {
+  grid_trigger();
+  grid_wait();
+  const int t = blockIdx.x / per_row;
+  const int len = row_len(a.pg, t);
+  const int j0 = (blockIdx.x - t * per_row) * (4 * kSumThreads) + static_cast<int>(threadIdx.x);
+  const float* part = a.w_part + t * a.w_pitch;
+  float x[4], y[4], z[4];
+  bool in[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int j = j0 + u * kSumThreads;
+    in[u] = j < len && static_cast<uint32_t>(gload(a.pg.block_table + static_cast<size_t>(t) * a.pg.max_pages +
+                                                   (j >> kPageShift))) < static_cast<uint32_t>(a.pg.n_pages);
+    if (!in[u]) continue;
+    x[u] = gload(part + j);
+    y[u] = gload(part + static_cast<long long>(a.n_q) * a.w_pitch + j);
+    z[u] = a.w_in ? gload(a.w_in + t * a.w_stride + j) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (in[u]) a.w_out[t * a.w_stride + j0 + u * kSumThreads] = z[u] + (x[u] + y[u]);
+}
+}  // namespace
+
+size_t key_weights_ws_bytes(int n_q, int n_heads, int max_pages) {
+  return n_heads > 64 ? static_cast<size_t>(2) * n_q * max_pages * kPageRows * sizeof(float) : 0;
+}
+
+cudaError_t launch_key_weights(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
+                               const CUtensorMap& tmap_q, const PagedRows& pg, int n_q, int n_heads, float scale,
+                               const float* lse, const float* w_in, float* w_out, long long w_stride, uint32_t* status,
+                               void* scratch, cudaStream_t st) {
+  const PipelineDebug dbg = pipeline_debug();
+  const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, false, 0));
+  LArgs a{};
+  a.latent = c.latent;
+  a.scale = c.scale;
+  a.rope = c.rope;
+  a.pg = pg;
+  a.n_q = n_q;
+  a.H = n_heads;
+  a.n_grp = L.n_grp;
+  a.n_hb = L.n_hb;
+  a.n_cta = L.n_grp * L.n_hb;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.lse_in = lse;
+  a.w_in = w_in;
+  a.w_out = w_out;
+  a.w_part = static_cast<float*>(scratch);
+  a.w_stride = w_stride;
+  a.w_pitch = static_cast<long long>(pg.max_pages) * kPageRows;
+  a.status = status;
+  a.wait_ns = dbg.wait_ns;
+  a.stop_after = dbg.stop_after_tiles;
+  cudaError_t e = clear_status(status, st);
+  if (e == cudaSuccess) e = launch_latent_single(head_block(n_heads), c.fp8, kWeights, tmap_kv, tmap_v, tmap_q, a, st);
+  if (e == cudaSuccess && L.n_hb == 2) {
+    const int per_row = static_cast<int>((a.w_pitch + 4 * kSumThreads - 1) / (4 * kSumThreads));
+    e = launch_pdl(weights_sum_kernel, dim3(static_cast<unsigned>(n_q) * per_row), kSumThreads, 0, st, 1, a, per_row);
+  }
+  return e;
+}
 
 size_t latent_attn_ws_bytes(int n_q, int n_heads) {
   // the most groups any block table can ask for

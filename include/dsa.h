@@ -560,6 +560,24 @@ dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, cons
                                   const dsa_shared_rows* groups, const dsa_paged_cache* pages, void* out, float* lse,
                                   void* ws, size_t ws_bytes, void* stream);
 
+/* The attention weight that each cached key receives from one query row per block-table row, added to what
+ * it has received so far (what dsa_latent_cache_evict chooses by):
+ *   weight_out[t][j] = weight_in[t][j] + sum_h exp(tau q[t, h] . kv_j - lse[t, h])        j < seq_len[t]
+ * with the log-sum-exp that the attention of these rows gave (dsa_latent_attn_paged over every key, or
+ * dsa_latent_attn_shared; over selected keys the others' weights are what they would have been).  Scores and sums in fp32.
+ * A head whose lse is -inf (no key) weighs nothing.  A NaN score or lse makes the key's weight NaN.
+ *   lse f32 [n_q][n_heads]; weight_in, weight_out f32 rows weight_stride >= max_pages * page_rows elements
+ *   apart; weight_in NULL: zeros; it may be weight_out (in place), otherwise the two do not overlap.
+ * Elements of weight_out behind a sequence's keys, and those of keys on a page outside the cache (flagged), stay
+ * as they were.  desc->topk is not read; desc->n_kv == cache->n_rows.
+ * ws: dsa_latent_key_weights_workspace_size bytes: 256, and beyond 64 heads 8 bytes for each row and key of
+ * the table.  Errors: those of dsa_latent_attn_paged, DSA_ERR_ARG (weight_stride), DSA_ERR_SHAPE (n_q * max_pages
+ * beyond 2^29 - 1). */
+dsa_status dsa_latent_key_weights_workspace_size(const dsa_attn_desc* desc, const dsa_paged_cache* pages, size_t* bytes);
+dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
+                                  const dsa_paged_cache* pages, const float* lse, const float* weight_in,
+                                  float* weight_out, int64_t weight_stride, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ MTP drafting ---- */
 
 /* One step of multi-step MTP drafting with IndexShare ([EX] "MTP path: IndexShare +
