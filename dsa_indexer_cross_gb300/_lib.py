@@ -41,7 +41,8 @@ EXPORTED = ("dsa_status_string", "dsa_last_error", "dsa_donor_table", "dsa_rope_
             "dsa_sparse_attn_backward_workspace_size", "dsa_rope_table_scaled", "dsa_rope_apply",
             "dsa_latent_cache_write", "dsa_latent_cache_read", "dsa_latent_attn_workspace_size",
             "dsa_latent_attn_paged", "dsa_mtp_verify", "dsa_latent_attn_shared_workspace_size",
-            "dsa_latent_attn_shared", "dsa_latent_key_weights_workspace_size", "dsa_latent_key_weights")
+            "dsa_latent_attn_shared", "dsa_latent_key_weights_workspace_size", "dsa_latent_key_weights",
+            "dsa_latent_cache_evict_workspace_size", "dsa_latent_cache_evict")
 
 PROFILE_KINDS = {0: "rope", 1: "ranges", 2: "indexer", 3: "select", 4: "attn_prep", 5: "attn", 6: "attn_bwd",
                  7: "proj", 8: "indexer_bwd", 9: "cache", 10: "verify"}
@@ -101,6 +102,10 @@ class SharedRows(C.Structure):
     _fields_ = [("group_start", C.c_void_p), ("prefix_len", C.c_void_p), ("n_groups", C.c_int32),
                 ("max_rows", C.c_int32)]
     device = None       # ordinal of the tensors' device, where shared_rows made it
+
+
+class EvictDesc(C.Structure):
+    _fields_ = [("n_seq", C.c_int32), ("n_keep", C.c_int32), ("n_first", C.c_int32), ("n_last", C.c_int32)]
 
 
 class VerifyDesc(C.Structure):
@@ -202,6 +207,11 @@ def lib() -> C.CDLL:
         L.dsa_latent_key_weights.restype = st
         L.dsa_latent_key_weights.argtypes = [P(AttnDesc), vp, P(LatentCache), P(PagedCache), vp, vp, vp, C.c_int64, vp, sz,
                                              vp]
+        L.dsa_latent_cache_evict_workspace_size.restype = st
+        L.dsa_latent_cache_evict_workspace_size.argtypes = [P(EvictDesc), P(sz)]
+        L.dsa_latent_cache_evict.restype = st
+        L.dsa_latent_cache_evict.argtypes = [P(EvictDesc), P(LatentCache), P(PagedCache), vp, C.c_int64, P(LatentCache),
+                                             P(PagedCache), vp, vp, C.c_int64, vp, vp, sz, vp]
         L.dsa_mtp_verify.restype = st
         L.dsa_mtp_verify.argtypes = [P(VerifyDesc), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         _lib = L
@@ -842,6 +852,40 @@ def dsa_latent_key_weights(desc: AttnDesc, q, cache: LatentCache, pages: PagedCa
     st = (_lib or lib()).dsa_latent_key_weights(desc, p_q, cache, pages, p_lse,
                                                 None if weight_in is None else weight_in.data_ptr(), weight_out.data_ptr(),
                                                 stride, _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
+    if st:
+        _check(st)
+    return ws
+
+
+def evict_desc(n_seq: int, n_keep: int, n_first: int = 0, n_last: int = 0) -> EvictDesc:
+    """n_keep keys of each longer sequence stay: the first n_first, the last n_last, the heaviest between."""
+    return EvictDesc(n_seq, n_keep, n_first, n_last)
+
+
+def dsa_latent_cache_evict_workspace_size(desc: EvictDesc) -> int:
+    n = C.c_size_t(0)
+    _check(lib().dsa_latent_cache_evict_workspace_size(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def dsa_latent_cache_evict(desc: EvictDesc, cache: LatentCache, pages: PagedCache, weight, to: LatentCache,
+                           to_pages: PagedCache, kept, weight_out, new_len, ws=None, stream=None) -> torch.Tensor:
+    """The heaviest keys of each sequence of `pages`, in order, copied to the rows of `to_pages`; kept[t]: their old
+    positions, weight_out[t] (or None): their weights, new_len[t]: their number (to_pages' seq_len may be passed)."""
+    n = desc.n_seq
+    dev = _current_device(kept, "kept", cache, pages, to, to_pages)
+    _paged_args(pages, n)
+    _paged_args(to_pages, n)
+    width = pages.max_pages * DSA_PAGE_ROWS
+    stride = _weight_rows(weight, n, width, "weight", dev)
+    out_stride = _weight_rows(weight_out, n, min(desc.n_keep, width), "weight_out", dev) if weight_out is not None else 0
+    if ws is None:
+        ws = _workspace(dsa_latent_cache_evict_workspace_size(desc), kept.device, stream)
+    st = (_lib or lib()).dsa_latent_cache_evict(desc, cache, pages, weight.data_ptr(), stride, to, to_pages,
+                                                _arg(kept, torch.int32, n * desc.n_keep, "kept", dev),
+                                                None if weight_out is None else weight_out.data_ptr(), out_stride,
+                                                _arg(new_len, torch.int32, n, "new_len", dev),
+                                                _arg(ws, torch.uint8, 0, "ws", dev), ws.numel(), _stream(stream))
     if st:
         _check(st)
     return ws

@@ -1155,6 +1155,75 @@ dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, cons
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "key weights kernel");
 }
 
+namespace {
+dsa_status check_evict_desc(const dsa_evict_desc* d) {
+  if (!d) return fail(DSA_ERR_ARG, "evict descriptor is NULL");
+  if (d->n_seq < 0 || d->n_keep < 1 || d->n_first < 0 || d->n_last < 0)
+    return fail(DSA_ERR_ARG, "n_seq, n_first and n_last must be >= 0, n_keep >= 1");
+  if (static_cast<long long>(d->n_first) + d->n_last > d->n_keep)
+    return fail(DSA_ERR_ARG, "n_first %d and n_last %d exceed n_keep %d", d->n_first, d->n_last, d->n_keep);
+  return DSA_OK;
+}
+}  // namespace
+
+dsa_status dsa_latent_cache_evict_workspace_size(const dsa_evict_desc* desc, size_t* bytes) {
+  const dsa_status s = check_evict_desc(desc);
+  if (s != DSA_OK) return s;
+  if (!bytes) return fail(DSA_ERR_ARG, "bytes is NULL");
+  *bytes = kAlign;
+  return DSA_OK;
+}
+
+dsa_status dsa_latent_cache_evict(const dsa_evict_desc* d, const dsa_latent_cache* from, const dsa_paged_cache* from_pages,
+                                  const float* weight, int64_t weight_stride, const dsa_latent_cache* to,
+                                  const dsa_paged_cache* to_pages, int32_t* kept, float* weight_out,
+                                  int64_t weight_out_stride, int32_t* new_len, void* ws, size_t ws_bytes, void* stream) {
+  dsa_status s = check_evict_desc(d);
+  if (s != DSA_OK) return s;
+  LatentCache src, dst;
+  if ((s = check_cache(from, &src)) != DSA_OK || (s = check_cache(to, &dst)) != DSA_OK) return s;
+  if (src.fp8 != dst.fp8) return fail(DSA_ERR_ARG, "both caches must have the same format");
+  Evict a{};
+  if ((s = check_pages(from_pages, src.n_rows, d->n_seq, &a.from)) != DSA_OK) return s;
+  if (!to_pages || (d->n_seq != 0 && !to_pages->block_table)) return fail(DSA_ERR_ARG, "to_pages: block_table must be non-NULL");
+  dsa_paged_cache target = *to_pages;
+  target.seq_len = target.block_table;             // not read, so it may be NULL
+  if ((s = check_pages(&target, dst.n_rows, d->n_seq, &a.to)) != DSA_OK) return s;
+  a.to.seq_len = nullptr;
+  if (a.from.max_pages > (1 << 30) / kPageRows || d->n_keep > (1 << 30))
+    return fail(DSA_ERR_SHAPE, "max_pages * page_rows and n_keep may be up to 2^30");
+  const long long rows = std::min<long long>(d->n_keep, static_cast<long long>(a.from.max_pages) * kPageRows);
+  if (rows > static_cast<long long>(a.to.max_pages) * kPageRows)
+    return fail(DSA_ERR_SHAPE, "to_pages has room for %lld keys of a sequence, %lld may stay",
+                static_cast<long long>(a.to.max_pages) * kPageRows, rows);
+  if (d->n_seq * ((rows + 63) / 64) > 0x1FFFFFFFLL) return fail(DSA_ERR_SHAPE, "n_seq * n_keep / 64 exceeds 2^29 - 1");
+  if (weight_stride < static_cast<long long>(a.from.max_pages) * kPageRows)
+    return fail(DSA_ERR_ARG, "weight_stride %lld must be at least max_pages * page_rows", static_cast<long long>(weight_stride));
+  if (weight_out && weight_out_stride < rows)
+    return fail(DSA_ERR_ARG, "weight_out_stride %lld must be at least %lld", static_cast<long long>(weight_out_stride), rows);
+  if ((s = check_status_ws(ws, ws_bytes)) != DSA_OK) return s;
+  if (d->n_seq == 0) return empty_call(ws, ws_bytes, static_cast<cudaStream_t>(stream));
+  if (!weight || !kept || !new_len) return fail(DSA_ERR_ARG, "weight, kept and new_len must be non-NULL");
+  if (weight_out == weight) return fail(DSA_ERR_ARG, "weight_out must not be weight");
+  if (new_len == from_pages->seq_len) return fail(DSA_ERR_ARG, "new_len must not be from_pages' seq_len");
+  if ((s = check_device()) != DSA_OK) return s;
+  a.weight = weight;
+  a.weight_out = weight_out;
+  a.weight_stride = weight_stride;
+  a.weight_out_stride = weight_out_stride;
+  a.kept = kept;
+  a.new_len = new_len;
+  a.n_seq = d->n_seq;
+  a.n_keep = d->n_keep;
+  a.n_first = d->n_first;
+  a.n_last = d->n_last;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int ps = prof_begin(kProfCache, st);
+  const cudaError_t e = launch_evict(a, src, dst, static_cast<uint32_t*>(ws), st);
+  prof_end(ps, st);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "eviction kernel");
+}
+
 dsa_status dsa_mtp_verify(const dsa_verify_desc* d, const void* target, const void* draft, const int32_t* tokens,
                           const int32_t* draft_len, const float* u_accept, const float* u_sample, int32_t* tokens_out,
                           int32_t* n_accepted, void* ws, size_t ws_bytes, void* stream) {

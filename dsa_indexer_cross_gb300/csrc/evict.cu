@@ -1,0 +1,290 @@
+// Eviction from a paged latent cache: the keys that stay, chosen by the attention weight they have received,
+// and the copy of their rows to other pages.
+//
+// A sequence of L keys that is longer than n_keep keeps its first n_first, its last n_last and, of the keys
+// between, the K = n_keep - n_first - n_last heaviest (ties: the lower position), all in order.
+//
+// Choosing.  A cluster of CTAs takes a sequence, each warp a run of consecutive keys.  The K-th heaviest
+// weight is found by a radix select on order-preserving 32-bit keys, 11, 11 and 10 bits at a time: a histogram
+// per CTA, summed over the cluster through distributed shared memory, one bin of which goes on.  Then each warp
+// counts the keys above and at the limit, a scan over the cluster's warps says where its own go, and it writes
+// them in order by ballots.  The weights are read four more times, out of L2.
+//
+// Copying.  A warp takes eight rows; HBM bounds it.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "status.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostCtas = 8;
+constexpr int kBins = 2048;
+
+// Larger weights have larger keys, -0 that of 0; a NaN has the smallest.
+__device__ __forceinline__ uint32_t weight_key(float w) { return w == w ? float_key(w) : 0u; }
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t load_cta(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.u32 %0, [a];\n}\n"
+               : "=r"(v)
+               : "r"(smem_u32(p)), "r"(rank)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_cta(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.u32 [a], %2;\n}\n" ::"r"(smem_u32(p)),
+               "r"(rank), "r"(v)
+               : "memory");
+}
+
+struct Smem {
+  uint32_t mine[kBins];              // this CTA's histogram
+  uint32_t all[kBins];               // the cluster's
+  uint32_t above[kMostCtas * kWarps], at[kMostCtas * kWarps];      // of each warp of the cluster
+  uint32_t warp_sum[kWarps];
+  uint32_t bin, before;              // the limit's bin, and the entries above it
+};
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ uint32_t warp_incl(uint32_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ Evict e, int n_cta, uint32_t* status) {
+  __shared__ Smem sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x / n_cta, rank = blockIdx.x - t * n_cta;
+  grid_trigger();
+  grid_wait();
+  const int want = gload(e.from.seq_len + t);
+  const int L = max(0, min(want, e.from.max_pages << kPageShift));
+  const int n = min(L, e.n_keep);
+  const float* w = e.weight + t * e.weight_stride;
+  float* w_out = e.weight_out ? e.weight_out + t * e.weight_out_stride : nullptr;
+  int32_t* kept = e.kept + static_cast<long long>(t) * e.n_keep;
+  if (rank == 0 && threadIdx.x == 0) {
+    if (want != L) report(status, false, DEV_ERR_RANGE);
+    e.new_len[t] = n;
+  }
+  const int stride = n_cta * kThreads, me = rank * kThreads + static_cast<int>(threadIdx.x);
+  const auto keep = [&](int place, int j) {
+    kept[place] = j;
+    if (w_out) w_out[place] = gload(w + j);
+  };
+  // those that stay in any case, and the unused end of kept
+  const bool all = L <= e.n_keep;
+  const int head = all ? L : e.n_first, tail = all ? 0 : e.n_last;
+  for (int i = me; i < head; i += stride) keep(i, i);
+  for (int i = me; i < tail; i += stride) keep(n - tail + i, L - tail + i);
+  for (int i = n + me; i < e.n_keep; i += stride) kept[i] = -1;
+  const int K = n - head - tail;
+  if (K == 0) return;                                          // (the whole cluster)
+
+  // the warp's run [lo, hi) of the keys between
+  const int from = head, to = L - tail;
+  const int run = (to - from + n_cta * kWarps - 1) / (n_cta * kWarps);
+  const int lo = min(to, from + (rank * kWarps + warp) * run), hi = min(to, lo + run);
+  uint32_t limit = 0;                // bits of the limit found so far
+  uint32_t need = static_cast<uint32_t>(K);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bits = pass == 2 ? 10 : 11;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) sh.mine[b] = 0;
+    __syncthreads();
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int j0 = lo + lane; j0 < hi; j0 += 32 * U) {
+      float x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = j0 + 32 * u < hi ? gload(w + j0 + 32 * u) : 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t key = weight_key(x[u]);
+        const bool in = j0 + 32 * u < hi && (pass == 0 || (key >> (shift + bits)) == limit);
+        if (in) atomicAdd(&sh.mine[(key >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+    }
+    cluster_sync_all();
+    // a part of the bins each, summed over the cluster, to every CTA
+    const int part = kBins / n_cta + 1;
+    for (int b = rank * part + static_cast<int>(threadIdx.x); b < min(kBins, (rank + 1) * part); b += kThreads) {
+      uint32_t s = 0;
+      for (int c = 0; c < n_cta; ++c) s += load_cta(&sh.mine[b], c);
+      for (int c = 0; c < n_cta; ++c) store_cta(&sh.all[b], c, s);
+    }
+    cluster_sync_all();
+    // the bin that holds the need-th entry from above: thread i takes the four bins from the top
+    constexpr int PER = kBins / kThreads;
+    uint32_t c[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      c[i] = sh.all[kBins - 1 - (static_cast<int>(threadIdx.x) * PER + i)];
+      sum += c[i];
+    }
+    const uint32_t incl = warp_incl(sum);
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    const uint32_t warps = warp_incl(lane < kWarps ? sh.warp_sum[lane] : 0u);
+    uint32_t before = __shfl_sync(0xffffffffu, warps, max(warp - 1, 0));
+    before = (warp ? before : 0u) + incl - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (before < need && need <= before + c[i]) {
+        sh.bin = kBins - 1 - (static_cast<uint32_t>(threadIdx.x) * PER + i);
+        sh.before = before;
+      }
+      before += c[i];
+    }
+    __syncthreads();
+    limit = (limit << bits) | sh.bin;
+    need -= sh.before;
+  }
+  // limit: the K-th heaviest weight; need: how many of that weight stay
+  uint32_t above = 0, at = 0;
+#pragma unroll 4
+  for (int j = lo + lane; j < hi; j += 32) {
+    const uint32_t key = weight_key(gload(w + j));
+    above += key > limit ? 1u : 0u;
+    at += key == limit ? 1u : 0u;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  at = __reduce_add_sync(0xffffffffu, at);
+  if (lane < n_cta) {
+    store_cta(&sh.above[rank * kWarps + warp], lane, above);
+    store_cta(&sh.at[rank * kWarps + warp], lane, at);
+  }
+  cluster_sync_all();
+  // what the warps before this one hold
+  uint32_t above_before = 0, at_before = 0;
+  for (int g = lane; g < rank * kWarps + warp; g += 32) {
+    above_before += sh.above[g];
+    at_before += sh.at[g];
+  }
+  above_before = __reduce_add_sync(0xffffffffu, above_before);
+  at_before = __reduce_add_sync(0xffffffffu, at_before);
+#pragma unroll 2
+  for (int j0 = lo; j0 < hi; j0 += 32) {
+    const int j = j0 + lane;
+    const float x = j < hi ? gload(w + j) : 0.f;
+    const uint32_t key = weight_key(x);
+    const uint32_t a = __ballot_sync(0xffffffffu, j < hi && key > limit), q = __ballot_sync(0xffffffffu, j < hi && key == limit);
+    const uint32_t lower = (1u << lane) - 1u;
+    const uint32_t at_here = at_before + __popc(q & lower);
+    const bool stays = ((a >> lane) & 1u) || (((q >> lane) & 1u) && at_here < need);
+    if (stays) {
+      const int place = from + static_cast<int>(above_before + __popc(a & lower) + min(at_here, need));
+      kept[place] = j;
+      if (w_out) w_out[place] = x;
+    }
+    above_before += __popc(a);
+    at_before += __popc(q);
+  }
+}
+
+// Eight rows a warp: lane l looks row l & 7 up, a trip each for its place and its page, then all rows' loads are in
+// flight before the first store.
+constexpr int kCopyRows = 8;
+template <bool FP8>
+__global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__ Evict e, const LatentCache src,
+                                                         const LatentCache dst, int per_seq, uint32_t* status) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_trigger();
+  grid_wait();
+  const int t = blockIdx.x / per_seq;
+  const int i0 = ((blockIdx.x - t * per_seq) * 8 + warp) * kCopyRows;
+  const int n = gload(e.new_len + t);
+  if (i0 >= n) return;
+  const int i = i0 + (lane & (kCopyRows - 1));
+  int from = -1, to = -1;
+  if (i < n) {
+    const int j = gload(e.kept + static_cast<long long>(t) * e.n_keep + i);
+    const int to_page = gload(e.to.block_table + static_cast<long long>(t) * e.to.max_pages + (i >> kPageShift));
+    const int page = gload(e.from.block_table + static_cast<long long>(t) * e.from.max_pages + (j >> kPageShift));
+    if (static_cast<uint32_t>(page) < static_cast<uint32_t>(e.from.n_pages) &&
+        static_cast<uint32_t>(to_page) < static_cast<uint32_t>(e.to.n_pages)) {
+      from = (page << kPageShift) + (j & (kPageRows - 1));
+      to = (to_page << kPageShift) + (i & (kPageRows - 1));
+    } else if (lane < kCopyRows) {
+      report(status, false, DEV_ERR_BAD_INDEX);
+    }
+  }
+  if constexpr (FP8) {
+    uint4 v[kCopyRows], r[kCopyRows / 4];
+    uint32_t sc = 0;
+#pragma unroll
+    for (int k = 0; k < kCopyRows; ++k) {
+      const int row = __shfl_sync(0xffffffffu, from, k);
+      if (row >= 0) v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 512) + lane);
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyRows / 4; ++k) {
+      const int row = __shfl_sync(0xffffffffu, from, 4 * k + (lane >> 3));
+      if (row >= 0) r[k] = gload(reinterpret_cast<const uint4*>(src.rope + static_cast<size_t>(row) * 64) + (lane & 7));
+    }
+    if (lane < kCopyRows && from >= 0) sc = gload(reinterpret_cast<const uint32_t*>(src.scale) + from);
+#pragma unroll
+    for (int k = 0; k < kCopyRows; ++k) {
+      const int row = __shfl_sync(0xffffffffu, to, k);
+      if (row >= 0) reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 512)[lane] = v[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyRows / 4; ++k) {
+      const int row = __shfl_sync(0xffffffffu, to, 4 * k + (lane >> 3));
+      if (row >= 0) reinterpret_cast<uint4*>(dst.rope + static_cast<size_t>(row) * 64)[lane & 7] = r[k];
+    }
+    if (lane < kCopyRows && to >= 0) reinterpret_cast<uint32_t*>(dst.scale)[to] = sc;
+  } else {
+    // 72 vectors a row
+    constexpr int kVec = 72, kAll = kCopyRows * kVec / 32;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint4 v[kAll / 2];
+#pragma unroll
+      for (int k = 0; k < kAll / 2; ++k) {
+        const int x = (h * (kAll / 2) + k) * 32 + lane, row = __shfl_sync(0xffffffffu, from, x / kVec);
+        if (row >= 0) v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 1152) + x % kVec);
+      }
+#pragma unroll
+      for (int k = 0; k < kAll / 2; ++k) {
+        const int x = (h * (kAll / 2) + k) * 32 + lane, row = __shfl_sync(0xffffffffu, to, x / kVec);
+        if (row >= 0) reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 1152)[x % kVec] = v[k];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const Evict& a, const LatentCache& src, const LatentCache& dst, uint32_t* status, cudaStream_t st) {
+  cudaError_t e = clear_status(status, st);
+  if (e != cudaSuccess) return e;
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 152;
+  const int ctas = std::max(1, std::min(kMostCtas, 2 * sms / std::max(1, std::min(a.n_seq, 2 * sms))));
+  e = launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(ctas)), kThreads, 0, st, ctas, a,
+                 ctas, status);
+  if (e != cudaSuccess) return e;
+  const int rows = std::min(a.n_keep, a.from.max_pages * kPageRows);
+  const int per_seq = (rows + 8 * kCopyRows - 1) / (8 * kCopyRows);
+  return launch_pdl(src.fp8 ? evict_copy_kernel<true> : evict_copy_kernel<false>,
+                    dim3(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(per_seq)), 256, 0, st, 1, a, src, dst, per_seq,
+                    status);
+}
+
+}  // namespace dsa

@@ -331,6 +331,20 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
                                  int n_heads, float scale, void* out, float* lse, uint32_t* status, void* scratch,
                                  cudaStream_t st);
 
+// ---------------------------------------------------------------------------- eviction
+// Positions that stay (kept [n_seq][n_keep]), their weights and number, and their rows copied from one cache's
+// pages to another's; strides in elements.
+struct Evict {
+  PagedRows from, to;          // (to.seq_len is not read)
+  const float* weight;
+  float* weight_out;           // or nullptr
+  long long weight_stride, weight_out_stride;
+  int32_t* kept;
+  int32_t* new_len;
+  int n_seq, n_keep, n_first, n_last;
+};
+cudaError_t launch_evict(const Evict& a, const LatentCache& src, const LatentCache& dst, uint32_t* status, cudaStream_t st);
+
 // ---------------------------------------------------------------------------- draft verification
 // Drafts taken, and the token drawn behind them, of every sequence (strides in elements between vocabulary
 // rows; draft NULL: drafts without probabilities; draft_len NULL: n_draft each).

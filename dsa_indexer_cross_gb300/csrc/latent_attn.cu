@@ -1008,14 +1008,14 @@ __global__ void __launch_bounds__(kSumThreads) weights_sum_kernel(const __grid_c
   grid_trigger();
   grid_wait();
   const int t = blockIdx.x / per_row;
-  const int len = row_len(a.pg, t);
-  const int j0 = (blockIdx.x - t * per_row) * (4 * kSumThreads) + static_cast<int>(threadIdx.x);
+  const uint32_t len = static_cast<uint32_t>(row_len(a.pg, t));
+  const uint32_t j0 = (blockIdx.x - static_cast<uint32_t>(t) * per_row) * (4 * kSumThreads) + threadIdx.x;
   const float* part = a.w_part + t * a.w_pitch;
   float x[4], y[4], z[4];
   bool in[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const int j = j0 + u * kSumThreads;
+    const uint32_t j = j0 + u * kSumThreads;
     in[u] = j < len && static_cast<uint32_t>(gload(a.pg.block_table + static_cast<size_t>(t) * a.pg.max_pages +
                                                    (j >> kPageShift))) < static_cast<uint32_t>(a.pg.n_pages);
     if (!in[u]) continue;

@@ -578,6 +578,39 @@ dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, cons
                                   const dsa_paged_cache* pages, const float* lse, const float* weight_in,
                                   float* weight_out, int64_t weight_stride, void* ws, size_t ws_bytes, void* stream);
 
+/* Eviction by accumulated attention weight: sequences of more than n_keep keys keep the first n_first, the last
+ * n_last and the heaviest of the keys between, n_keep in all (ties: the lower position; a NaN weighs least);
+ * shorter ones keep everything.  The kept rows are copied, in order, to the pages of `to`: key i of
+ * sequence t is then what key kept[t][i] was.  Nothing of `from` is written, so pages that sequences share
+ * stay valid for the others, and the caller frees what it no longer needs.
+ *   kept int32 [n_seq][n_keep]: old positions, ascending, then -1; new_len int32 [n_seq]: keys that stay (it may
+ *   be the seq_len of to_pages, which this call does not read, so that to_pages then describes the result).
+ *   weight f32, rows weight_stride >= from_pages->max_pages * page_rows apart; weight_out f32 or NULL, rows
+ *   weight_out_stride apart (at least the smaller of n_keep and from's keys): the kept keys' weights, in
+ *   order; elements behind them stay as they were.
+ *   from, to: of one format, the same arrays or others; no page of to_pages is a page of from_pages or of
+ *   another sequence of to_pages (the rows of such a page become a mixture).  to_pages needs room for what may
+ *   stay: the smaller of n_keep and from_pages' max_pages * page_rows.  Rows of `to` that nothing is copied to
+ *   stay as they were.  Rotary dims are copied as they are: keys keep the positions they were turned at.
+ * A length outside [0, max_pages * page_rows] is cut to it and flagged; a row from or to a page outside its
+ * cache is not copied and flagged (DSA_ERR_DEVICE).  ws: dsa_latent_cache_evict_workspace_size bytes (256).
+ * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows != n_pages * page_rows; no room in to_pages; max_pages * page_rows or
+ * n_keep beyond 2^30, n_seq * n_keep / 64 beyond 2^29), DSA_ERR_UNSUPPORTED (page_rows), DSA_ERR_WORKSPACE,
+ * DSA_ERR_CUDA. */
+typedef struct dsa_evict_desc {
+  int32_t n_seq;
+  int32_t n_keep;     /* >= 1                          */
+  int32_t n_first;    /* n_first + n_last <= n_keep    */
+  int32_t n_last;
+} dsa_evict_desc;
+
+dsa_status dsa_latent_cache_evict_workspace_size(const dsa_evict_desc* desc, size_t* bytes);
+dsa_status dsa_latent_cache_evict(const dsa_evict_desc* desc, const dsa_latent_cache* from,
+                                  const dsa_paged_cache* from_pages, const float* weight, int64_t weight_stride,
+                                  const dsa_latent_cache* to, const dsa_paged_cache* to_pages, int32_t* kept,
+                                  float* weight_out, int64_t weight_out_stride, int32_t* new_len, void* ws,
+                                  size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ MTP drafting ---- */
 
 /* One step of multi-step MTP drafting with IndexShare ([EX] "MTP path: IndexShare +
