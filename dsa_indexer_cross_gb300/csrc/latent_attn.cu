@@ -586,6 +586,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       tc_fence_after();
       const Partial<MODE> to(a, sg, grp);
       const bool direct = writes_out<MODE>(sg);
+      if (tid == 0) note_piece<MODE>(a, sg, grp);
 #pragma unroll 1
       for (int hw = 0; hw < C::CW / 16; ++hw) {
         const int hh = c_off / 16 + hw;
@@ -629,10 +630,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
                 l == 0.f ? -INFINITY : (sh.m_used[tid] + log2f(l)) * 0.69314718055994531f;
           }
         } else {
-          float* at = to.m + hb * HB + tid;
-          at[0] = sh.m_used[tid];
-          at[to.step] = sh.l_run[tid];
-          at[2 * to.step] = sh.l_sum[tid];
+          to.sums(hb * HB + tid, sh.m_used[tid], sh.l_run[tid], sh.l_sum[tid]);
         }
       }
       tc_fence_before();

@@ -95,10 +95,12 @@ struct LArgs {
   const uint16_t* rope;
   const int32_t* idx;          // selected offsets [n_q][topk], or nullptr
   const int32_t* row_nt;       // selected keys: 64-slot tiles of each row; items: tiles of each
-  const int4* items;           // kItems, and how many there are
-  const int32_t* n_items;
+  const int4* items;           // kItems
+  const int4* shares;          // kItems: {first item, its first tile, tiles} of each group
   float* whole_o;              // kItems: an item that one share holds, by column: [prefix, own][n_q * H][512]
-  float* whole_m;              // [prefix, own][3][n_q * H], as part_m
+  float4* whole_m;             // [prefix, own][n_q * H]: a column's {max in use, rounded, plain sum} (as part_m)
+  float4* item_m;              // [n_grp * 2][part_cols]: the same of partials
+  int2* pieces;                // kItems: the first group of each item, and the one behind its last
   PagedRows pg;
   uint16_t* out;
   float* lse;
@@ -145,6 +147,8 @@ struct Seg {
   bool begins;       // with the row's first tile
   bool whole;        // the row's every tile
   int col0, ncol;    // columns of q and out; kItems: ncol with the item's flags
+  int item;          // kItems
+  bool ends;         // kItems: with the item's last tile
 };
 template <int MODE>
 struct Walk {
@@ -166,6 +170,8 @@ struct Walk {
       const int4 it = gload(a.items + row);
       s.col0 = it.x;
       s.ncol = it.y;
+      s.item = row;
+      s.ends = tile + s.n == T;
       s.row = it.z;
       s.i0 += it.w;
     } else {
@@ -178,27 +184,46 @@ struct Walk {
     return true;
   }
 };
-// Where a segment's unnormalised columns go (the first of `cols`), and where its three numbers a column:
-// at m[0], m[step] and m[2 step].
+// Where a segment's unnormalised columns go: the first's row of O, and (column c) its three numbers.
 template <int MODE>
 struct Partial {
-  float *o, *m;
+  float* o;
+  float* m;
   size_t step;
   __device__ __forceinline__ Partial(const LArgs& a, const Seg& s, int grp) {
     const int cols = MODE == kItems ? a.part_cols : a.H;
-    if (MODE == kItems && s.whole) {
-      const size_t all = static_cast<size_t>(a.n_q) * a.H, own = s.ncol & kItemOwn ? 1 : 0;
-      o = a.whole_o + (own * all + s.col0) * kDv;
-      m = a.whole_m + own * 3 * all + s.col0;
-      step = all;
+    const size_t slot = static_cast<size_t>(grp) * 2 + (s.begins ? 1 : 0);
+    o = a.part_o + slot * cols * kDv;
+    if constexpr (MODE == kItems) {
+      m = reinterpret_cast<float*>(a.item_m + slot * cols);
+      if (s.whole) {
+        const size_t at = (s.ncol & kItemOwn ? static_cast<size_t>(a.n_q) * a.H : 0) + s.col0;
+        o = a.whole_o + at * kDv;
+        m = reinterpret_cast<float*>(a.whole_m + at);
+      }
     } else {
-      const size_t slot = static_cast<size_t>(grp) * 2 + (s.begins ? 1 : 0);
-      o = a.part_o + slot * cols * kDv;
       m = a.part_m + slot * cols;
       step = static_cast<size_t>(a.n_grp) * 2 * cols;
     }
   }
+  __device__ __forceinline__ void sums(int c, float max, float rounded, float plain) const {
+    if constexpr (MODE == kItems) {
+      reinterpret_cast<float4*>(m)[c] = make_float4(max, rounded, plain, 0.f);
+    } else {
+      m[c] = max;
+      m[step + c] = rounded;
+      m[2 * step + c] = plain;
+    }
+  }
 };
+// (one thread of a group, for each of its segments)
+template <int MODE>
+__device__ __forceinline__ void note_piece(const LArgs& a, const Seg& s, int grp) {
+  if constexpr (MODE == kItems) {
+    if (s.begins) a.pieces[s.item].x = grp;
+    if (s.ends) a.pieces[s.item].y = grp + 1;
+  }
+}
 template <int MODE>
 __device__ __forceinline__ bool writes_out(const Seg& s) {
   return s.whole && (MODE != kItems || (s.ncol & kItemSole));
@@ -224,7 +249,7 @@ __device__ __forceinline__ void publish_faults(const LArgs& a, const CtaFaults& 
   w[1] = f.count;
 }
 
-// The share of group `grp`: a scan over the rows' tile counts (the whole block calls it; a block-wide barrier
+// The share of group `grp` (of items: as they were listed): a scan over the rows' tile counts (the whole block calls it; a block-wide barrier
 // is needed behind it before row0 / tile0 are read).
 struct Share {
   long long wsum[32];
@@ -233,30 +258,37 @@ struct Share {
 };
 // Groups in use, and whether they take a row each.
 template <int MODE>
-__device__ __forceinline__ int share_groups(const LArgs& a, int n_rows, long long total, int tallest, bool& by_row) {
+__device__ __forceinline__ int share_groups(int n_grp, int n_hb, int n_rows, long long total, int tallest, bool& by_row) {
   const long long most = min_share(total, n_rows) == 4 ? (total + 3) >> 2 : (total + 1) >> 1;
-  const int groups = static_cast<int>(min(static_cast<long long>(a.n_grp), most));
-  by_row = MODE != kWeights && a.n_hb == 2 && n_rows <= a.n_grp &&
+  const int groups = static_cast<int>(min(static_cast<long long>(n_grp), most));
+  by_row = MODE != kWeights && n_hb == 2 && n_rows <= n_grp &&
            tallest <= share_start(total, 1, max(groups, 1)) + whole_row_extra(groups);
   return by_row ? n_rows : groups;
 }
-__device__ __forceinline__ bool bad_length(const LArgs& a, int row) {
-  const int want = gload(a.pg.seq_len + row);
-  return want < 0 || want > (a.pg.max_pages << kPageShift);
+__device__ __forceinline__ bool bad_length(const PagedRows& pg, int row) {
+  const int want = gload(pg.seq_len + row);
+  return want < 0 || want > (pg.max_pages << kPageShift);
 }
 template <int MODE, int THREADS>
 __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool writes_start, Share& sh, CtaFaults& faults) {
+  if constexpr (MODE == kItems) {
+    const int4 r = gload(a.shares + grp);
+    if (threadIdx.x == 0) {
+      sh.row0 = r.x;
+      sh.tile0 = r.y;
+    }
+    return r.z;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long share = 0;
   int groups;
-  const int n_rows = MODE == kItems ? gload(a.n_items) : a.n_q;
-  if (n_rows <= 32) {
+    if (a.n_q <= 32) {
     // A row a lane, each warp for itself: no barrier, no trip through shared memory (300 keys, 16 heads: 11.6 ->
     // 10.8 us).
-    const int T = lane < n_rows ? row_tiles<MODE>(a, lane) : 0;
+    const int T = lane < a.n_q ? row_tiles<MODE>(a, lane) : 0;
     const uint32_t total = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(T));     // 32 x 2^25 at most
     bool by_row;
-    groups = share_groups<MODE>(a, n_rows, total, __reduce_max_sync(0xffffffffu, T), by_row);
+    groups = share_groups<MODE>(a.n_grp, a.n_hb, a.n_q, total, __reduce_max_sync(0xffffffffu, T), by_row);
     uint32_t pre = T;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -280,13 +312,13 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
       sh.tile0 = tile0;
       if (writes_start && grp < groups) a.start[grp] = make_int2(row0, tile0);
     }
-    if (MODE != kItems && blockIdx.x == 0 && warp == 0) {
+    if (blockIdx.x == 0 && warp == 0) {
       __syncwarp();        // (thread 0 has set faults)
-      if (lane < a.n_q && bad_length(a, lane)) report(faults, DEV_ERR_RANGE);
+      if (lane < a.n_q && bad_length(a.pg, lane)) report(faults, DEV_ERR_RANGE);
     }
   } else {
-    const int per = (n_rows + THREADS - 1) / THREADS;
-    const int ra = min(n_rows, static_cast<int>(threadIdx.x) * per), rb = min(n_rows, ra + per);
+    const int per = (a.n_q + THREADS - 1) / THREADS;
+    const int ra = min(a.n_q, static_cast<int>(threadIdx.x) * per), rb = min(a.n_q, ra + per);
     long long mine = 0;
     int tallest = 0;
     bool bad_len = false;
@@ -295,7 +327,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
       const int T = row_tiles<MODE>(a, r);
       mine += T;
       tallest = max(tallest, T);
-      if (MODE != kItems && blockIdx.x == 0 && bad_length(a, r)) bad_len = true;
+      if (blockIdx.x == 0 && bad_length(a.pg, r)) bad_len = true;
     }
     long long pre = mine;
 #pragma unroll
@@ -317,7 +349,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
       tallest = max(tallest, sh.wmax[w]);
     }
     bool by_row;
-    groups = share_groups<MODE>(a, n_rows, total, tallest, by_row);
+    groups = share_groups<MODE>(a.n_grp, a.n_hb, a.n_q, total, tallest, by_row);
     if (by_row) {
       share = grp < groups ? row_tiles<MODE>(a, grp) : 0;
       if (threadIdx.x == 0 && grp < groups) {
@@ -344,8 +376,8 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
     }
   }
   if (writes_start && threadIdx.x == 0 && grp >= groups) a.start[grp] = make_int2(0x7FFFFFFF, 0);
-  // rows without keys: zeros and -inf (of items: the join's)
-  if constexpr (MODE == kEvery || MODE == kSelected) {
+  // rows without keys: zeros and -inf
+  if constexpr (MODE != kWeights) {
 #pragma unroll 1
     for (int t = blockIdx.x; t < a.n_q; t += gridDim.x) {
       if (row_tiles<MODE>(a, t) != 0) continue;

@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       const int dim0 = (qd >> 1) * 256 + cw * 128;               // this thread's OC dims
       const Partial<MODE> to(a, sg, grp);
       const bool direct = writes_out<MODE>(sg);
+      if (rank == 0 && threadIdx.x == 0) note_piece<MODE>(a, sg, grp);
       const bool live = ghead < columns<MODE>(sg);
       const float inv = l == 0.f ? 0.f : 1.f / l;                // a NaN sum stays NaN; no key: zeros
       uint16_t* orow = a.out + (static_cast<size_t>(sg.col0) + ghead) * kDv + dim0;
@@ -574,9 +575,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
             a.lse[static_cast<size_t>(sg.col0) + ghead] =
                 l2 == 0.f ? -INFINITY : (m_used + log2f(l2)) * 0.69314718055994531f;
         } else {
-          to.m[ghead] = m_used;
-          to.m[to.step + ghead] = l;
-          to.m[2 * to.step + ghead] = l2;
+          to.sums(ghead, m_used, l, l2);
         }
       }
       tc_fence_before();

@@ -13,7 +13,11 @@
 //
 // Which kernel.  Up to 64 columns a group: one launch of the single-CTA kernel takes every item.  More than 64
 // heads: one launch of the CTA-pair kernel (128 columns).  In between two launches, the pair kernel for the
-// prefixes, the single-CTA one for the rows' own keys, which are bound by bytes.
+// prefixes, the single-CTA one for the rows' own keys, which are bound by bytes; where these are few, the pair
+// kernel takes them too and the second launch finds nothing.
+//
+// The line counts an item as a few tiles more than it has, for what it costs by itself (32 rows of 64 heads
+// behind 100K keys, fp8, one walk: the pairs at the line's end had sixteen short items each; 599 -> 525 us).
 //
 // A column's result comes from its prefix item and its own item, each whole or in partials where shares were
 // cut: latent_shared_join_kernel puts them together with one softmax.  A row that is the only thing its columns
@@ -29,51 +33,75 @@
 namespace dsa {
 namespace {
 
-constexpr int kPlanThreads = 1024;
 // A prefix of fewer tiles than this is left to the rows.
 constexpr int kMinShared = 2;
+// What an item costs apart from its tiles, in tiles: its columns of q are loaded and its sums written while the
+// products wait.
+constexpr int kItemCost = 3;
+
+// Up to this many tiles of the rows' own keys go with the prefixes through the pair kernel, which a second walk's
+// launch, fill and partials cost more than: 48 rows behind 8000 keys, own tiles 266, 811, 2121, 5916: bf16, 16 heads, one
+// walk 41, 49, 70, 124 us, two 54, 61, 82, 124; fp8 57, 67, 92, 164 and 65, 73, 87, 130; fp8, 64 heads, 109, 119, 143,
+// 215 and 124, 135, 153, 210.
+constexpr int kMostOwnBf16 = 5000, kMostOwnFp8 = 1500;
 
 struct PlanArgs {
   const int32_t* start;      // [n_groups + 1]
   const int32_t* prefix;     // [n_groups]
   PagedRows pg;
   int n_groups, n_q, H, cols;     // cols: columns of a prefix item
-  bool two;                  // own items in a list of their own
+  bool two;                  // there is a second walk, for own items of more than most_own tiles in all
+  int most_own;
   int32_t* tiles;            // [n_groups]: the shared tiles
   int32_t* table;            // [n_groups]: the row whose table names their pages
-  int32_t* base;             // [n_groups + 1]: first item
+  int32_t* base;             // [n_groups]: first item, and the line before it
+  long long* base_at;
   int32_t* nt[2];
   int4* items[2];
-  int4* rows;                // [n_q]: first prefix item (-1), its first column, own item (-1)
-  int32_t* n_items;          // [2]
+  int4* rows;                // [n_q]: first prefix item (-1), its first column, own item (-1) and its walk
+  long long* at[2];          // the line before each item
+  int4* shares[2];           // [n_grp]
+  int n_grp[2];
+  bool pair[2];
   uint32_t* faults;          // [2]
 };
 
-// Exclusive sum over the block's threads; total: the sum.
-__device__ __forceinline__ int block_excl(int x, int* warp_sum, int& total) {
+struct Count {
+  int items;
+  long long line;
+};
+// Exclusive sums over the block's threads, and the totals.
+template <int kPlanThreads>
+__device__ __forceinline__ Count block_excl(Count x, Count* warp_sum, Count& total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int incl = x;
+  const auto incl = [&](Count c) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int i = __shfl_up_sync(0xffffffffu, c.items, o);
+      const long long t = __shfl_up_sync(0xffffffffu, c.line, o);
+      if (lane >= o) {
+        c.items += i;
+        c.line += t;
+      }
+    }
+    return c;
+  };
+  const Count mine = incl(x);
+  if constexpr (kPlanThreads == 32) {
+    total = Count{__shfl_sync(0xffffffffu, mine.items, 31), __shfl_sync(0xffffffffu, mine.line, 31)};
+    return Count{mine.items - x.items, mine.line - x.line};
   }
   __syncthreads();
-  if (lane == 31) warp_sum[warp] = incl;
+  if (lane == 31) warp_sum[warp] = mine;
   __syncthreads();
-  const int w = warp_sum[lane];
-  int before = w;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
-  }
-  total = __shfl_sync(0xffffffffu, before, 31);
-  before -= w;
-  return __shfl_sync(0xffffffffu, before, warp) + incl - x;
+  const Count w = lane < kPlanThreads / 32 ? warp_sum[lane] : Count{0, 0}, all = incl(w);
+  total = Count{__shfl_sync(0xffffffffu, all.items, 31), __shfl_sync(0xffffffffu, all.line, 31)};
+  return Count{__shfl_sync(0xffffffffu, all.items - w.items, warp) + mine.items - x.items,
+               __shfl_sync(0xffffffffu, all.line - w.line, warp) + mine.line - x.line};
 }
 // The last of the n ascending values at v that is <= x; v[0] <= x.
-__device__ __forceinline__ int last_not_above(const int32_t* v, int n, int x) {
+template <typename T>
+__device__ __forceinline__ int last_not_above(const T* v, int n, T x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -83,12 +111,14 @@ __device__ __forceinline__ int last_not_above(const int32_t* v, int n, int x) {
   return lo;
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_constant__ PlanArgs p) {
-  __shared__ int warp_sum[32];
+  __shared__ Count warp_sum[32];
   __shared__ CtaFaults faults;
+  __shared__ int tallest[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_trigger();
-  if (tid == 0) faults.bits = faults.count = 0;
+  if (tid == 0) faults.bits = faults.count = tallest[0] = tallest[1] = 0;
   grid_wait();
   // groups that do not lie in order within the rows: none is shared
   bool bad = false;
@@ -123,63 +153,133 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   }
   __syncthreads();
   // prefix items
-  int n_pre = 0;
+  Count pre{0, 0};
+  int most_tiles = 0;
   for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
     const int g = g0 + tid;
-    int blocks = 0;
+    Count mine{0, 0};
     if (g < n_groups && p.tiles[g] > 0) {
       const long long cols = static_cast<long long>(gload(p.start + g + 1) - gload(p.start + g)) * p.H;
-      blocks = static_cast<int>((cols + p.cols - 1) / p.cols);
+      mine.items = static_cast<int>((cols + p.cols - 1) / p.cols);
+      mine.line = static_cast<long long>(mine.items) * (p.tiles[g] + kItemCost);
+      most_tiles = max(most_tiles, p.tiles[g]);
     }
-    int total;
-    const int at = n_pre + block_excl(blocks, warp_sum, total);
-    if (g < n_groups) p.base[g] = at;
-    n_pre += total;
+    Count total;
+    const Count before = block_excl<kPlanThreads>(mine, warp_sum, total);
+    if (g < n_groups) {
+      p.base[g] = pre.items + before.items;
+      p.base_at[g] = pre.line + before.line;
+    }
+    pre.items += total.items;
+    pre.line += total.line;
   }
   __syncthreads();
-  for (int i = tid; i < n_pre; i += kPlanThreads) {
+  for (int i = tid; i < pre.items; i += kPlanThreads) {
     const int g = last_not_above(p.base, n_groups, i);       // (the last of equal ones: the one with items)
     const int s = gload(p.start + g), e = gload(p.start + g + 1), b = i - p.base[g];
     p.items[0][i] = make_int4(s * p.H + b * p.cols, min(p.cols, (e - s) * p.H - b * p.cols), p.table[g], 0);
     p.nt[0][i] = p.tiles[g];
+    p.at[0][i] = p.base_at[g] + static_cast<long long>(b) * (p.tiles[g] + kItemCost);
   }
   // the rows' own items
-  const int list = p.two ? 1 : 0;
-  int n_own = p.two ? 0 : n_pre;
   const int first = n_groups > 0 ? gload(p.start) : 0, end = n_groups > 0 ? gload(p.start + n_groups) : 0;
+  const auto own_tiles = [&](int t, int& shared, int4& info) {
+    const int len = row_len(p.pg, t);
+    shared = 0;
+    info = make_int4(-1, 0, -1, 0);
+    if (t >= first && t < end) {
+      const int g = last_not_above(p.start, n_groups, t);
+      if (p.tiles[g] > 0 && len >= p.tiles[g] * kRows) {
+        shared = p.tiles[g];
+        info.x = p.base[g];
+        info.y = gload(p.start + g) * p.H;
+      }
+    }
+    return (len + kRows - 1) / kRows - shared;
+  };
+  int list = 0;
+  if (p.two) {                 // in a walk of their own, where they are many
+    Count mine{0, 0}, total;
+    int shared;
+    int4 info;
+    for (int t = tid; t < p.n_q; t += kPlanThreads) mine.line += own_tiles(t, shared, info);
+    block_excl<kPlanThreads>(mine, warp_sum, total);
+    list = total.line > p.most_own ? 1 : 0;
+  }
+  Count own = list ? Count{0, 0} : pre;
+  int most_own = 0;
   for (int t0 = 0; t0 < p.n_q; t0 += kPlanThreads) {
     const int t = t0 + tid;
     int4 info = make_int4(-1, 0, -1, 0);
-    int own = 0, shared = 0;
+    int tiles = 0, shared = 0;
     if (t < p.n_q) {
-      const int want = gload(p.pg.seq_len + t), len = row_len(p.pg, t);
-      if (want != len) report(faults, DEV_ERR_RANGE);
-      if (t >= first && t < end) {
-        const int g = last_not_above(p.start, n_groups, t);
-        if (p.tiles[g] > 0 && len >= p.tiles[g] * kRows) {
-          shared = p.tiles[g];
-          info.x = p.base[g];
-          info.y = gload(p.start + g) * p.H;
-        }
-      }
-      own = (len + kRows - 1) / kRows - shared;
+      if (bad_length(p.pg, t)) report(faults, DEV_ERR_RANGE);
+      tiles = own_tiles(t, shared, info);
+      info.w = list;
+      most_own = max(most_own, tiles);
     }
-    int total;
-    const int at = n_own + block_excl(own > 0 ? 1 : 0, warp_sum, total);
+    Count total;
+    const Count before = block_excl<kPlanThreads>(tiles > 0 ? Count{1, tiles + kItemCost} : Count{0, 0}, warp_sum, total);
     if (t < p.n_q) {
-      if (own > 0) {
-        info.z = at;
-        p.items[list][at] = make_int4(t * p.H, p.H | kItemOwn | (shared ? 0 : kItemSole), t, shared);
-        p.nt[list][at] = own;
+      if (tiles > 0) {
+        const int i = own.items + before.items;
+        info.z = i;
+        p.items[list][i] = make_int4(t * p.H, p.H | kItemOwn | (shared ? 0 : kItemSole), t, shared);
+        p.nt[list][i] = tiles;
+        p.at[list][i] = own.line + before.line;
       }
       p.rows[t] = info;
     }
-    n_own += total;
+    own.items += total.items;
+    own.line += total.line;
+  }
+  most_tiles = __reduce_max_sync(0xffffffffu, most_tiles);
+  most_own = __reduce_max_sync(0xffffffffu, most_own);
+  if (lane == 0) {
+    atomicMax(&tallest[0], most_tiles);
+    atomicMax(&tallest[list], most_own);
   }
   __syncthreads();
+  // each group's share
+  for (int k = 0; k < (p.two ? 2 : 1); ++k) {
+    const Count c = k == list ? own : list ? pre : Count{0, 0};
+    bool by_row;
+    const int groups = share_groups<kItems>(p.n_grp[k], p.pair[k] ? 2 : 1, c.items, c.line, tallest[k] + kItemCost, by_row);
+    // Where share g begins: an item, and the tiles before it in the item and in the list.  A cut that would leave a
+    // piece of one tile is moved to the item's end or beginning.
+    const auto cut = [&](int g, int& i, int& tile) -> long long {
+      if (g == groups) {
+        i = c.items;
+        tile = 0;
+        return c.line - static_cast<long long>(kItemCost) * c.items;
+      }
+      const long long at = share_start(c.line, g, groups);
+      i = last_not_above(p.at[k], c.items, at);
+      const int nt = p.nt[k][i];
+      const long long before = p.at[k][i] - static_cast<long long>(kItemCost) * i;
+      tile = static_cast<int>(at - p.at[k][i]) - kItemCost;
+      if (tile < 2) {
+        tile = 0;
+      } else if (nt - tile < 2) {
+        ++i;
+        tile = 0;
+        return before + nt;
+      }
+      return before + tile;
+    };
+    for (int g = tid; g < p.n_grp[k]; g += kPlanThreads) {
+      int4 r = make_int4(0, 0, 0, 0);
+      if (g < groups && by_row) {
+        r = make_int4(g, 0, p.nt[k][g], 0);
+      } else if (g < groups) {
+        int i, tile;
+        const long long from = cut(g, r.x, r.y), to = cut(g + 1, i, tile);
+        r.z = static_cast<int>(to - from);
+      }
+      p.shares[k][g] = r;
+    }
+  }
   if (tid == 0) {
-    p.n_items[0] = p.two ? n_pre : n_own;
-    p.n_items[1] = n_own;
     p.faults[0] = faults.bits;
     p.faults[1] = faults.count;
   }
@@ -192,53 +292,37 @@ struct JoinArgs {
   int n_walks, cols;
 };
 
-// The pieces of an item: `n` partials from `o` on, each `pitch` columns behind the one before (the first is in
-// the second slot of its group, the others in the first of theirs), or one, whole.
+// The pieces of an item's column: one, whole, or the partials of groups b .. b + n - 1, of which the first is in the
+// second slot of its group and the others in the first of theirs.
 struct Pieces {
-  const float *o, *m;
-  size_t step, first, next;      // column of the first piece, of the second; the third lies pitch behind that
-  size_t pitch;
+  const float* o;
+  const float4* m;
+  size_t first, next, pitch;
   int n;
   __device__ __forceinline__ size_t at(int k) const { return k == 0 ? first : next + (k - 1) * pitch; }
 };
-__device__ __forceinline__ Pieces find_pieces(const LArgs& a, int item, int col_in_item, size_t col, bool own) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Pieces find_pieces(const LArgs& a, int2 groups, int col_in_item, size_t col) {
   Pieces p{};
-  if (item < 0) return p;
-  uint32_t below = 0;
-#pragma unroll
-  for (int k = 0; k < kMostGroups / 32; ++k) {
-    const int c = lane + 32 * k;
-    if (c >= a.n_grp) continue;
-    const int2 st = gload(a.start + c);
-    below += st.x < item || (st.x == item && st.y == 0) ? 1u : 0u;
-    below += st.x <= item ? 0x10000u : 0u;
-  }
-  below = __reduce_add_sync(0xffffffffu, below);
-  const int b = static_cast<int>(below & 0xFFFFu) - 1, end = static_cast<int>(below >> 16);
-  if (end - b < 2) {
-    const size_t all = static_cast<size_t>(a.n_q) * a.H, k = own ? 1 : 0;
-    p.o = a.whole_o + k * all * kDv;
-    p.m = a.whole_m + k * 3 * all;
-    p.step = all;
+  p.n = groups.y - groups.x;
+  if (p.n == 1) {
+    p.o = a.whole_o;
+    p.m = a.whole_m;
     p.first = col;
-    p.n = 1;
   } else {
     p.o = a.part_o;
-    p.m = a.part_m;
+    p.m = a.item_m;
     p.pitch = 2 * static_cast<size_t>(a.part_cols);
-    p.step = static_cast<size_t>(a.n_grp) * p.pitch;
-    p.first = (static_cast<size_t>(b) * 2 + 1) * a.part_cols + col_in_item;
-    p.next = static_cast<size_t>(b + 1) * 2 * a.part_cols + col_in_item;
-    p.n = end - b;
+    p.first = (static_cast<size_t>(groups.x) * 2 + 1) * a.part_cols + col_in_item;
+    p.next = static_cast<size_t>(groups.x + 1) * p.pitch + col_in_item;
   }
   return p;
 }
 
 // One column's pieces put together, HPB columns a block, 8 / HPB warps each: a warp takes every (8 / HPB)-th
 // piece, a lane 16 dims.  With M the largest of the pieces' maxima m_s and w_s = 2^(m_s - M), out = sum w_s O_s /
-// sum w_s lr_s and lse = ln 2 (M + log2 sum w_s l_s); the order of the sums is fixed.  One block more puts the
-// fault words together.
+// sum w_s lr_s and lse = ln 2 (M + log2 sum w_s l_s); the order of the sums is fixed.  Four trips to L2, one behind
+// the other: the row, its items' groups, the maxima and sums together with the first O rows, the other O rows.
+// One block more puts the fault words together.
 template <int HPB>
 __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_constant__ JoinArgs j) {
   constexpr int kJoinWarps = 8 / HPB;
@@ -247,7 +331,7 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
   __shared__ float weight[8][kMost];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int hw = warp / kJoinWarps, w = warp % kJoinWarps;
-  const LArgs& own_walk = j.walk[j.n_walks - 1];
+  const LArgs& out = j.walk[0];
   grid_trigger();
   grid_wait();
   if (blockIdx.x == gridDim.x - 1) {
@@ -261,14 +345,14 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
     bits = __reduce_or_sync(0xffffffffu, bits);
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) {
-      own_walk.status[0] = bits;
-      own_walk.status[1] = count;
+      out.status[0] = bits;
+      out.status[1] = count;
     }
     return;
   }
-  const int H = own_walk.H;
-  const long long col = static_cast<long long>(blockIdx.x) * HPB + hw;
-  const bool live = col < static_cast<long long>(own_walk.n_q) * H;
+  const int H = out.H;
+  const long long col = static_cast<long long>(blockIdx.x) * HPB + hw, all = static_cast<long long>(out.n_q) * H;
+  const bool live = col < all;
   float M = -INFINITY, lr = 0.f, ls = 0.f;
   float4 acc[4];
 #pragma unroll
@@ -278,19 +362,15 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
     const int t = static_cast<int>(col / H), h = static_cast<int>(col - static_cast<long long>(t) * H);
     const int4 info = gload(j.rows + t);
     const int in_group = static_cast<int>(col - info.y);
-    const Pieces pre = find_pieces(j.walk[0], info.x < 0 ? -1 : info.x + in_group / j.cols, in_group % j.cols, col, false);
-    const Pieces own = find_pieces(own_walk, info.z, h, col, true);
+    int2 pre_groups = make_int2(0, 0), own_groups = make_int2(0, 0);
+    if (info.x >= 0) pre_groups = gload(j.walk[0].pieces + info.x + in_group / j.cols);
+    const LArgs& own_walk = j.walk[info.w];
+    if (info.z >= 0) own_groups = gload(own_walk.pieces + info.z);
+    const Pieces pre = find_pieces(j.walk[0], pre_groups, in_group % j.cols, col);
+    const Pieces own = find_pieces(own_walk, own_groups, h, all + col);
     done = pre.n == 0 && own.n == 1;           // written by the walk
     const int n = done ? 0 : pre.n + own.n;
-    const auto piece = [&](int k, const float*& m, size_t& step) -> const float4* {
-      const bool first = k < pre.n;
-      const size_t at = first ? pre.at(k) : own.at(k - pre.n);
-      m = (first ? pre.m : own.m) + at;
-      step = first ? pre.step : own.step;
-      return reinterpret_cast<const float4*>((first ? pre.o : own.o) + at * kDv) + lane;
-    };
-    const float* pm;
-    size_t step;
+    const auto meta = [&](int k) { return k < pre.n ? gload(pre.m + pre.at(k)) : gload(own.m + own.at(k - pre.n)); };
     constexpr int kAhead = 3;                  // O rows in flight
     bool weighed = false;
 #pragma unroll 1
@@ -300,7 +380,8 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
       for (int u = 0; u < kAhead; ++u) {
         const int k = k0 + u * kJoinWarps;
         if (k < n) {
-          const float4* src = piece(k, pm, step);
+          const float* row = k < pre.n ? pre.o + pre.at(k) * kDv : own.o + own.at(k - pre.n) * kDv;
+          const float4* src = reinterpret_cast<const float4*>(row) + lane;
 #pragma unroll
           for (int v = 0; v < 4; ++v) o[u][v] = gload(src + 32 * v);
         }
@@ -309,20 +390,22 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
         // (while the rows are on their way)  A piece without a key weighs nothing; one whose sum is NaN makes the
         // column NaN even where its maximum says nothing.
         weighed = true;
-        for (int k = lane; k < n; k += 32) {
-          piece(k, pm, step);
-          M = fmaxf(M, gload(pm));
-        }
+        const auto weigh = [&](const float4& m, int k) {
+          const float f = m.x == -INFINITY ? (m.y == m.y ? 0.f : m.y) : exp2f(m.x - M);
+          weight[warp][k] = f;
+          lr += f * m.y;
+          ls += f * m.z;
+        };
+        float4 m[2];                           // (more than 64 pieces are loaded twice)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) m[u] = lane + 32 * u < n ? meta(lane + 32 * u) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        M = fmaxf(m[0].x, m[1].x);
+        for (int k = lane + 64; k < n; k += 32) M = fmaxf(M, meta(k).x);
 #pragma unroll
         for (int e = 16; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, e));
-        for (int k = lane; k < n; k += 32) {
-          piece(k, pm, step);
-          const float m = gload(pm), l1 = gload(pm + step), l2 = gload(pm + 2 * step);
-          const float f = m == -INFINITY ? (l1 == l1 ? 0.f : l1) : exp2f(m - M);
-          weight[warp][k] = f;
-          lr += f * l1;
-          ls += f * l2;
-        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) weigh(m[u], lane + 32 * u);
+        for (int k = lane + 64; k < n; k += 32) weigh(meta(k), k);
         __syncwarp();
       }
 #pragma unroll
@@ -364,21 +447,21 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
     }
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
     const __nv_bfloat162 y = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
-    reinterpret_cast<uint2*>(own_walk.out + static_cast<size_t>(col) * kDv)[lane + 32 * k] =
+    reinterpret_cast<uint2*>(out.out + static_cast<size_t>(col) * kDv)[lane + 32 * k] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
   }
-  if (own_walk.lse && lane == 0) own_walk.lse[col] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+  if (out.lse && lane == 0) out.lse[col] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
 }
 
 struct WalkLayout {
   bool pair;
   int cols, n_grp;
-  size_t off_err, off_start, off_m, off_o, off_ring;
+  size_t off_err, off_shares, off_m, off_o, off_ring;
 };
 struct Layout {
   WalkLayout walk[2];
   int n_walks, n_items[2];
-  size_t off_tiles, off_table, off_base, off_nt[2], off_items[2], off_rows, off_counts, off_whole_m, off_whole_o, total;
+  size_t off_tiles, off_table, off_base, off_base_at, off_nt[2], off_items[2], off_at[2], off_pieces[2], off_rows, off_faults, off_whole_m, off_whole_o, total;
 };
 Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
   Layout L{};
@@ -392,7 +475,7 @@ Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
   L.walk[1].cols = head_block(std::min(n_heads, 64));
   const long long all = static_cast<long long>(n_q) * n_heads;
   const long long pre = all / L.walk[0].cols + n_groups;
-  L.n_items[0] = static_cast<int>(std::min<long long>(pre + (L.n_walks == 1 ? n_q : 0), 0x7FFFFFFF));
+  L.n_items[0] = static_cast<int>(std::min<long long>(pre + n_q, 0x7FFFFFFF));
   L.n_items[1] = L.n_walks == 2 ? n_q : 0;
   size_t o = 0;
   const auto take = [&](size_t bytes) {
@@ -400,23 +483,26 @@ Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
     o += (bytes + 255) & ~size_t(255);
     return at;
   };
-  L.off_counts = take(4 * sizeof(int32_t));
+  L.off_faults = take(2 * sizeof(uint32_t));
   L.off_tiles = take(static_cast<size_t>(n_groups) * sizeof(int32_t));
   L.off_table = take(static_cast<size_t>(n_groups) * sizeof(int32_t));
-  L.off_base = take((static_cast<size_t>(n_groups) + 1) * sizeof(int32_t));
+  L.off_base = take(static_cast<size_t>(n_groups) * sizeof(int32_t));
+  L.off_base_at = take(static_cast<size_t>(n_groups) * sizeof(long long));
   L.off_rows = take(static_cast<size_t>(n_q) * sizeof(int4));
   for (int k = 0; k < L.n_walks; ++k) {
     WalkLayout& w = L.walk[k];
     w.n_grp = std::max(1, std::min(w.pair ? sms / 2 : sms, kMostGroups));
     L.off_nt[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(int32_t));
     L.off_items[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(int4));
+    L.off_pieces[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(int2));
+    L.off_at[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(long long));
     w.off_err = take(static_cast<size_t>(w.n_grp) * 2 * 2 * sizeof(uint32_t));
-    w.off_start = take(static_cast<size_t>(w.n_grp) * sizeof(int2));
-    w.off_m = take(static_cast<size_t>(w.n_grp) * 2 * w.cols * 3 * sizeof(float));
+    w.off_shares = take(static_cast<size_t>(w.n_grp) * sizeof(int4));
+    w.off_m = take(static_cast<size_t>(w.n_grp) * 2 * w.cols * sizeof(float4));
     w.off_o = take(static_cast<size_t>(w.n_grp) * 2 * w.cols * kDv * sizeof(float));
     w.off_ring = w.pair ? take(static_cast<size_t>(w.n_grp) * kRing * kRows * kDqk * sizeof(uint16_t)) : 0;
   }
-  L.off_whole_m = take(static_cast<size_t>(all) * 2 * 3 * sizeof(float));
+  L.off_whole_m = take(static_cast<size_t>(all) * 2 * sizeof(float4));
   L.off_whole_o = take(static_cast<size_t>(all) * 2 * kDv * sizeof(float));
   L.total = o;
   return L;
@@ -458,18 +544,27 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
   p.H = n_heads;
   p.cols = L.walk[0].cols;
   p.two = L.n_walks == 2;
+  p.most_own = c.fp8 ? kMostOwnFp8 : kMostOwnBf16;
   p.tiles = i32(L.off_tiles);
   p.table = i32(L.off_table);
   p.base = i32(L.off_base);
   p.rows = reinterpret_cast<int4*>(base + L.off_rows);
-  p.n_items = i32(L.off_counts);
-  p.faults = reinterpret_cast<uint32_t*>(p.n_items + 2);
+  p.base_at = reinterpret_cast<long long*>(base + L.off_base_at);
+  p.faults = reinterpret_cast<uint32_t*>(base + L.off_faults);
   for (int k = 0; k < L.n_walks; ++k) {
     p.nt[k] = i32(L.off_nt[k]);
     p.items[k] = reinterpret_cast<int4*>(base + L.off_items[k]);
+    p.at[k] = reinterpret_cast<long long*>(base + L.off_at[k]);
+    p.shares[k] = reinterpret_cast<int4*>(base + L.walk[k].off_shares);
+    p.n_grp[k] = L.walk[k].n_grp;
+    p.pair[k] = L.walk[k].pair;
   }
   int ps = prof_begin(kProfAttnPrep, st);
-  cudaError_t e = launch_pdl(latent_plan_kernel, dim3(1), kPlanThreads, 0, st, 1, p);
+  // (fewer threads, fewer and cheaper barriers)
+  const int most = std::max(n_q, 8 * groups.n_groups);
+  cudaError_t e = most <= 64    ? launch_pdl(latent_plan_kernel<32>, dim3(1), 32, 0, st, 1, p)
+                  : most <= 512 ? launch_pdl(latent_plan_kernel<256>, dim3(1), 256, 0, st, 1, p)
+                                : launch_pdl(latent_plan_kernel<1024>, dim3(1), 1024, 0, st, 1, p);
   prof_end(ps, st);
   if (e != cudaSuccess) return e;
   JoinArgs j{};
@@ -486,9 +581,10 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
     a.rope = c.rope;
     a.row_nt = p.nt[k];
     a.items = p.items[k];
-    a.n_items = p.n_items + k;
+    a.shares = p.shares[k];
     a.whole_o = reinterpret_cast<float*>(base + L.off_whole_o);
-    a.whole_m = reinterpret_cast<float*>(base + L.off_whole_m);
+    a.whole_m = reinterpret_cast<float4*>(base + L.off_whole_m);
+    a.pieces = reinterpret_cast<int2*>(base + L.off_pieces[k]);
     a.pg = pg;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
@@ -499,8 +595,7 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
     a.n_cta = w.n_grp * a.n_hb;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = reinterpret_cast<uint32_t*>(base + w.off_err);
-    a.start = reinterpret_cast<int2*>(base + w.off_start);
-    a.part_m = reinterpret_cast<float*>(base + w.off_m);
+    a.item_m = reinterpret_cast<float4*>(base + w.off_m);
     a.part_o = reinterpret_cast<float*>(base + w.off_o);
     a.part_cols = w.cols;
     a.ring = reinterpret_cast<uint16_t*>(base + w.off_ring);
@@ -512,8 +607,11 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
   }
   if (e == cudaSuccess) {
     const long long all = static_cast<long long>(n_q) * n_heads;
-    const int hpb = all <= 1024 ? 1 : 8;
-    e = launch_pdl(hpb == 1 ? latent_shared_join_kernel<1> : latent_shared_join_kernel<8>,
+    // Warps a column by the pieces that it may be in: 64 columns in 40, one column a block 22.0 us, four 26.1, eight
+    // 30.6; 768 in some 13, 54.0, 53.0, 61.3; 8192 in two or three, 378, 353, 349.
+    const long long pieces = static_cast<long long>(L.walk[0].n_grp) * L.walk[0].cols / all;
+    const int hpb = pieces > 32 ? 1 : pieces > 8 ? 4 : 8;
+    e = launch_pdl(hpb == 1 ? latent_shared_join_kernel<1> : hpb == 4 ? latent_shared_join_kernel<4> : latent_shared_join_kernel<8>,
                    dim3(static_cast<unsigned>((all + hpb - 1) / hpb + 1)), 256, 0, st, 1, j);
   }
   prof_end(ps, st);
