@@ -1114,7 +1114,7 @@ dsa_status dsa_latent_key_weights_workspace_size(const dsa_attn_desc* desc, cons
   const dsa_attn_desc d = latent_desc(desc, false);
   const dsa_status s = check_attn_desc(&d);
   if (s != DSA_OK) return s;
-  *bytes = kAlign + align_up(key_weights_ws_bytes(d.n_q, d.n_heads, pages->max_pages));
+  *bytes = kAlign;
   return DSA_OK;
 }
 
@@ -1128,16 +1128,13 @@ dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, cons
   if (s != DSA_OK) return s;
   if (weight_stride < static_cast<long long>(pg.max_pages) * kPageRows)
     return fail(DSA_ERR_ARG, "weight_stride %lld must be at least max_pages * page_rows", static_cast<long long>(weight_stride));
-  if (static_cast<long long>(d.n_q) * pg.max_pages > 0x1FFFFFFFLL)
-    return fail(DSA_ERR_SHAPE, "n_q * max_pages exceeds 2^29 - 1");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d.n_q == 0) return empty_call(ws, ws_bytes, st);
   if (!q || !lse || !weight_out || !ws) return fail(DSA_ERR_ARG, "q, lse, weight_out and ws must be non-NULL");
   if (!aligned16(q)) return fail(DSA_ERR_ARG, "q must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be 256-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
-  const size_t need = kAlign + align_up(key_weights_ws_bytes(d.n_q, d.n_heads, pg.max_pages));
-  if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "key weights workspace too small: %zu < %zu bytes", ws_bytes, need);
+  if (ws_bytes < kAlign) return fail(DSA_ERR_WORKSPACE, "key weights workspace too small: %zu < %zu bytes", ws_bytes, kAlign);
   CUtensorMap tkv, tv, tq;
   std::memset(&tkv, 0, sizeof(tkv));
   std::memset(&tv, 0, sizeof(tv));
@@ -1146,11 +1143,11 @@ dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, cons
     if ((s = tmap_kv_tiles(&tv, c.latent, static_cast<uint64_t>(c.n_rows), 64, 4)) != DSA_OK) return s;
   }
   if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
-                     static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)
+                     static_cast<uint32_t>(key_weights_q_box_rows(d.n_heads)))) != DSA_OK)
     return s;
   const int ps = prof_begin(kProfAttn, st);
   const cudaError_t e = launch_key_weights(c, tkv, tv, tq, pg, d.n_q, d.n_heads, d.softmax_scale, lse, weight_in, weight_out,
-                                           weight_stride, static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st);
+                                           weight_stride, static_cast<uint32_t*>(ws), st);
   prof_end(ps, st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "key weights kernel");
 }

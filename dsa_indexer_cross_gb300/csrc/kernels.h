@@ -301,12 +301,12 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
 
 // w_out[t][j] = w_in[t][j] (nullptr: 0) + sum over heads of exp(scale q . kv_j - lse) of every key of row t, rows of
 // both w_stride apart.  The maps are as for launch_latent_attn with at most 64 heads (tmap_q: boxes of
-// latent_attn_q_box_rows).
-size_t key_weights_ws_bytes(int n_q, int n_heads, int max_pages);
+// key_weights_q_box_rows).
+int key_weights_q_box_rows(int n_heads);
 cudaError_t launch_key_weights(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
                                const CUtensorMap& tmap_q, const PagedRows& pg, int n_q, int n_heads, float scale,
                                const float* lse, const float* w_in, float* w_out, long long w_stride, uint32_t* status,
-                               void* scratch, cudaStream_t st);
+                               cudaStream_t st);
 
 // Rows that share prefixes: group g's are [start[g], start[g + 1]), their common keys [0, prefix[g]); max_rows: a
 // group's rows, at most or thereabouts (it chooses the kernels).

@@ -49,24 +49,27 @@ constexpr int kTileBytes = kKB * kBlkBytes;
 template <int HB, bool FP8, bool WEIGHTS = false>
 struct LCfg {
   static constexpr int Q_BYTES = HB * kDqk * 2;
-  static constexpr int DYN_SMEM = 1024 + 2 * kTileBytes + Q_BYTES;
+  static constexpr int SLOTS = HB > 64 ? 1 : 2;        // tiles in shared memory
+  static constexpr int DYN_SMEM = 1024 + SLOTS * kTileBytes + Q_BYTES;
   // softmax warps (fp8: four, which leaves the converters 128 registers; the keys' weights: each key's
   // columns in one warp)
   static constexpr int SW = HB >= 32 && !FP8 && !WEIGHTS ? 8 : 4;
   static constexpr int SOFT = 32 * SW;
-  static constexpr int NP = FP8 ? 8 : 1;               // producer warps
+  static constexpr int NG = 2;                         // fp8: groups of four converter warps
+  static constexpr int NP = FP8 ? 4 * NG : 1;          // producer warps
   static constexpr int S_WARP = SW + NP;
   static constexpr int PV_WARP = S_WARP + 1;
   static constexpr int THREADS = 32 * (SW + NP + 2);
   static constexpr int CW = HB / (SW / 4);             // columns per softmax warp
   static constexpr int NR = CW / 8;
-  static constexpr uint32_t TMEM_COLS = 6 * HB <= 128 ? 128 : 6 * HB <= 256 ? 256 : 512;
-  static constexpr int S_COL = 4 * HB;
-  static_assert(HB % 16 == 0 && HB <= 64 && CW % 16 == 0, "columns");
+  static constexpr int S_COL = WEIGHTS ? 0 : 4 * HB;
+  static constexpr int COLS = S_COL + 2 * HB;
+  static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static_assert(HB % 16 == 0 && HB <= (WEIGHTS ? 128 : 64) && CW % 16 == 0, "columns");
 };
 
 struct LShared {
-  uint64_t full[2][2], empty[2][2];   // by tile parity and half: latent dims 0 .. 255; 256 .. 511 and the rotary dims
+  uint64_t full[2][2], empty[4][2];   // by slot and half: latent dims 0 .. 255; 256 .. 511 and the rotary dims
   // [2]: by tile parity.  (One p_full for all tiles would not do: the softmax may be two tiles ahead of
   // the PV warp's look, and a barrier two phases on reads as not yet complete.)
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free, mma_done;
@@ -82,6 +85,7 @@ struct LShared {
   alignas(16) float alpha[64];
 };
 static_assert(LCfg<64, true>::DYN_SMEM + sizeof(LShared) <= 232448, "HB = 64 must fit in shared memory");
+static_assert(LCfg<128, true, true>::DYN_SMEM + sizeof(LShared) <= 232448, "HB = 128 must fit in shared memory");
 
 template <int HB, bool FP8, int MODE>
 __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
@@ -95,22 +99,24 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ LShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sT = smem;                        // two tiles
-  uint8_t* sQ = smem + 2 * kTileBytes;       // HB x 576, nine blocks of HB x 128 B
+  uint8_t* sT = smem;                        // the tiles
+  uint8_t* sQ = smem + C::SLOTS * kTileBytes;       // HB x 576, nine blocks of HB x 128 B
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = blockIdx.x / a.n_hb, hb = blockIdx.x - grp * a.n_hb;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       // fp8: each warp of the group (second half: and each thread's copies)
-      mbar_init(&sh.full[s][0], FP8 ? C::NP / 2 : 1);
-      mbar_init(&sh.full[s][1], FP8 ? 33 * (C::NP / 2) : 1);
-      mbar_init(&sh.empty[s][0], 1);
-      mbar_init(&sh.empty[s][1], 1);
+      mbar_init(&sh.full[s][0], FP8 ? 4 : 1);
+      mbar_init(&sh.full[s][1], FP8 ? 33 * 4 : 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], C::SW);
       mbar_init(&sh.p_full[s], C::SW);
       mbar_init(&sh.o_done[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&sh.empty[s][0], 1);
+      mbar_init(&sh.empty[s][1], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
@@ -142,6 +148,13 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
   const uint32_t tmem = sh.tmem_base;
   Walk<MODE> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
+  // Tile g's slot, how many tiles were in it before, and the barrier by which it is freed.  Converters of more
+  // groups than slots may ask for a slot two tiles ahead of its use, so (weights) tiles are freed on four barriers in
+  // turn: the one asked about is then never more than one phase behind.
+  const auto slot = [](uint32_t g) -> uint32_t { return C::SLOTS == 2 ? g & 1 : 0u; };
+  const auto lap = [](uint32_t g) -> uint32_t { return C::SLOTS == 2 ? g >> 1 : g; };
+  const auto freed = [&](uint32_t g, int h) -> uint64_t* { return &sh.empty[MODE == kWeights ? g & 3 : g & 1][h]; };
+  const auto freed_lap = [](uint32_t g) -> uint32_t { return MODE == kWeights ? g >> 2 : g >> 1; };
 
   if (warp >= C::SW && warp < C::S_WARP) {
     // ---------------------------------------------------------------- Q and the rows
@@ -164,12 +177,12 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
             ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
             break;
           }
-          uint8_t* st = sT + (g & 1) * kTileBytes;
+          uint8_t* st = sT + slot(g) * kTileBytes;
           const int row = bad ? 0 : (page << kPageShift) + (i & 1) * kRows;
 #pragma unroll 1
           for (int h = 0; h < 2 && ok; ++h) {
-            uint64_t* full = &sh.full[g & 1][h];
-            if (g >= 2) ok = wait(&sh.empty[g & 1][h], ((g >> 1) - 1) & 1);
+            uint64_t* full = &sh.full[slot(g)][h];
+            if (g >= C::SLOTS) ok = wait(freed(g - C::SLOTS, h), freed_lap(g - C::SLOTS) & 1);
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(full, (4 + h) * kBlkBytes);
               tma_load_3d(st + 4 * h * kBlkBytes, &tmap_v, full, 0, row, 4 * h);
@@ -181,15 +194,15 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       }
     }
     if constexpr (FP8) {
-      // Two groups of four warps take the tiles in turn, so one group's loads are in flight while the
-      // other converts; a warp takes sixteen rows of its group's tiles.  (One group with two tiles in
+      // Groups of four warps take the tiles in turn, so one group's loads are in flight while another
+      // converts; a warp takes sixteen rows of its group's tiles.  (One group with two tiles in
       // flight per warp was slower: a wait for any result also waited for the other tile's loads.)
       // A load instruction takes 256 bytes of two rows, whole 128-byte lines; eight lanes of a store
       // phase cover two rows x every other 16-byte chunk, which the swizzle spreads over all banks.
       // Lane l looks after row l & 15: its offset is found two of the group's tiles ahead, its page
       // one, its codes as soon as the registers are free, across segments.  The rotary dims, which
       // need no conversion, are copied when the slot is free, out of L2.
-      const uint32_t turn = pw >> 2;                                      // tiles with g & 1 == turn, in slot `turn`
+      const uint32_t turn = pw >> 2;                                      // tiles with g % NG == turn
       const int row_base = 16 * (pw & 3), my_row = row_base + (lane & 15);
       const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4 (+ 4), row parity
       uint4 w[16];
@@ -221,8 +234,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         lenx = len0;
         const int s = (as.i0 + ai) * kRows + my_row;
         j0 = !SEL ? s : s < a.topk ? gload(a.idx + static_cast<size_t>(row0) * a.topk + s) : -1;
-        advance();
-        advance();
+#pragma unroll
+        for (int n = 0; n < C::NG; ++n) advance();
       };
       auto page_step = [&]() {
         j2 = j1;
@@ -261,22 +274,23 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         sc = gload(reinterpret_cast<const uint32_t*>(a.scale) + row);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(row) * 64));
       };
-      if (turn) advance();
+      for (uint32_t n = 0; n < turn; ++n) advance();
       offset_step();
       offset_step();
       page_step();
       offset_step();
       fetch_step();
       page_step();
-      const uint32_t tile = smem_u32(sT + turn * kTileBytes);
+      const uint32_t tile0 = smem_u32(sT);
       // the lane's line of row par in block blk4, swizzled for chunk 2 c; row 2 k + par's lies 256 k on, its
       // swizzle differs by 2 k (mod 8)
       const uint32_t lane_line =
-          tile + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
+          tile0 + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
       // one tile: registers -> the bf16 tile, then the registers' next fetch
       auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
-        const uint32_t line = opaque(lane_line);
+        const uint32_t sl = C::SLOTS == C::NG ? turn : slot(g), tile = tile0 + sl * kTileBytes;
+        const uint32_t line = opaque(lane_line + sl * kTileBytes);
         uint32_t rsc[8];                     // scale words of this lane's rows; all ones: no key
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         // previous tile's second product leaves the first half before it is done with the other
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (g >= 2 && !wait(&sh.empty[turn][h], ((g >> 1) - 1) & 1)) return false;
+          if (g >= C::SLOTS && !wait(freed(g - C::SLOTS, h), freed_lap(g - C::SLOTS) & 1)) return false;
           if (h == 1) {
             const uint32_t rl = opaque(tile) + 8 * kBlkBytes + row_base * 128;
 #pragma unroll
@@ -297,10 +311,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
               cp_async_16_zfill(rl + q * 128 + (((lane & 7) ^ (q & 7)) << 4),
                                 a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
             }
-            cp_async_mbar_arrive(&sh.full[turn][1]);
+            cp_async_mbar_arrive(&sh.full[sl][1]);
             if constexpr (SEL) {
               const uint32_t keys = __ballot_sync(0xffffffffu, at >= 0) & 0xFFFFu;
-              if (lane == 0) sh.keys[turn][pw & 3] = keys;
+              if (lane == 0) sh.keys[sl][pw & 3] = keys;
             }
           }
 #pragma unroll
@@ -319,24 +333,25 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[turn][h]);
+          if (lane == 0) mbar_arrive(&sh.full[sl][h]);
         }
         offset_step();
         fetch_step();
         page_step();
         return true;
       };
-      for (g = turn; ok && g < static_cast<uint32_t>(share); g += 2) ok = tile_step();
+      for (g = turn; ok && g < static_cast<uint32_t>(share); g += C::NG) ok = tile_step();
       cp_async_wait<0>();
     }
     // let every copy this CTA started land before its shared memory can be released (a wait that ran out
     // between a tile's halves leaves one more wait here than copies: bounded)
     if constexpr (!FP8) {
       if (lane == 0)
-        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j)
-          for (int h = 0; h < 2; ++h) mbar_drain(&sh.full[j & 1][h], (j >> 1) & 1, 200000000ull);
+        for (uint32_t j = g > C::SLOTS ? g - C::SLOTS : 0; j < g; ++j)
+          for (int h = 0; h < 2; ++h) mbar_drain(&sh.full[slot(j)][h], lap(j) & 1, 200000000ull);
     }
-  } else if (MODE == kWeights && warp < C::SW) {
+  } else if (warp < C::SW) {
+    if constexpr (MODE == kWeights) {
     // ---------------------------------------------------------------- the keys' weights
     // A warp takes sixteen keys of a tile with all of the CTA's columns: a thread holds two keys, two of
     // every eight columns, and four lanes' sums meet by shuffles.
@@ -353,12 +368,12 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       float lse2[2 * NR];
 #pragma unroll
       for (int c = 0; c < 2 * NR; ++c) {
-        const int h = hb * HB + 8 * (c >> 1) + cq + (c & 1);
+        const int h = 8 * (c >> 1) + cq + (c & 1);
         const float l = h < a.H ? gload(a.lse_in + sg.col0 + h) * 1.4426950408889634f : INFINITY;
         lse2[c] = l == -INFINITY ? INFINITY : l;
       }
-      float* to = a.n_hb == 1 ? a.w_out + sg.row * a.w_stride : a.w_part + (static_cast<long long>(hb) * a.n_q + sg.row) * a.w_pitch;
-      const float* from = a.n_hb == 1 && a.w_in ? a.w_in + sg.row * a.w_stride : nullptr;
+      float* to = a.w_out + sg.row * a.w_stride;
+      const float* from = a.w_in ? a.w_in + sg.row * a.w_stride : nullptr;
       for (int n = 0; n < sg.n; ++n, ++g) {
         const int i = sg.i0 + n, sb = g & 1;
         const int nv = tile_rows(a, len, i, gload(bt + (i >> 1)));
@@ -368,17 +383,23 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         ok = wait_bar(&sh.s_full[sb], (g >> 1) & 1, &sh.abort_flag, &sh.faults.bits, a.wait_ns);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        uint32_t v[4 * NR];
-        tmem_ld_16x256b<NR>(tmem + t_lane + C::S_COL + sb * HB, v);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
         float x = 0.f, y = 0.f;
+        constexpr int K = NR < 8 ? NR : 8;               // columns / 8 at a time
 #pragma unroll
-        for (int c = 0; c < 2 * NR; ++c) {
-          x += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + (c & 1)]), a.scale_log2, -lse2[c]));
-          y += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + 2 + (c & 1)]), a.scale_log2, -lse2[c]));
+        for (int k0 = 0; k0 < NR; k0 += K) {
+          uint32_t v[4 * K];
+          tmem_ld_16x256b<K>(tmem + t_lane + C::S_COL + sb * HB + 8 * k0, v);
+          tmem_ld_wait();
+          if (k0 + K == NR) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.s_empty[sb]);
+          }
+#pragma unroll
+          for (int c = 0; c < 2 * K; ++c) {
+            x += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + (c & 1)]), a.scale_log2, -lse2[2 * k0 + c]));
+            y += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + 2 + (c & 1)]), a.scale_log2, -lse2[2 * k0 + c]));
+          }
         }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
@@ -388,7 +409,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         if (mine) to[at] = before + (lane & 1 ? y : x);
       }
     }
-  } else if (MODE != kWeights && warp < C::SW) {
+    } else {
     // ---------------------------------------------------------------- softmax + epilogue
     constexpr int kSoft = C::SOFT;
     const int tid = threadIdx.x;
@@ -638,6 +659,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       if (lane == 0) mbar_arrive(&sh.o_free);
       named_bar_sync(1, kSoft);        // per-column state may be reset now
     }
+    }
   } else {
     // ---------------------------------------------------------------- MMA issuers
     constexpr uint32_t id_qk = idesc_bf16_f32(64, HB, 0, 0);
@@ -669,11 +691,11 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
           int nv = kRows;
           if constexpr (!FP8) nv = tile_rows(a, len, sg.i0 + n, gload(bt + ((sg.i0 + n) >> 1)));
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
-          const uint64_t da = sdesc_sw128(st0 + sb * kTileBytes, 16, 1024);
+          const uint64_t da = sdesc_sw128(st0 + slot(g) * kTileBytes, 16, 1024);
           const uint32_t d_s = tmem + C::S_COL + sb * HB;
 #pragma unroll
           for (int h = 0; h < 2 && ok; ++h) {
-            if (!(ok = wait(&sh.full[sb][h], (g >> 1) & 1))) break;
+            if (!(ok = wait(&sh.full[slot(g)][h], lap(g) & 1))) break;
             if constexpr (FP8) {
               fence_proxy_async_smem();        // the rotary dims' cp.async copies
             } else if (nv < kRows) {
@@ -681,7 +703,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
               // line of its block; their rotary dims only reach masked scores)
 #pragma unroll 1
               for (int kb = 4 * h; kb < 4 * h + 4; ++kb) {
-                const uint32_t blk = st0 + sb * kTileBytes + kb * kBlkBytes;
+                const uint32_t blk = st0 + slot(g) * kTileBytes + kb * kBlkBytes;
 #pragma unroll 1
                 for (uint32_t o = nv * 128 + lane * 16; o < kBlkBytes; o += 512) sts128(blk + o, 0u, 0u, 0u, 0u);
               }
@@ -694,7 +716,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
             for (int kb = 4 * h; kb < 4 + 5 * h; ++kb)
               umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
                                        dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
-            if constexpr (MODE == kWeights) umma_commit_elect(&sh.empty[sb][h]);      // no second product
+            if constexpr (MODE == kWeights) umma_commit_elect(freed(g, h));      // no second product
           }
           if (!ok) break;
           umma_commit_elect(&sh.s_full[sb]);
@@ -962,12 +984,16 @@ cudaError_t launch_t(const CUtensorMap& tkv, const CUtensorMap& tv, const CUtens
   return launch_pdl(latent_attn_kernel<HB, FP8, MODE>, dim3(a.n_cta), C::THREADS, C::DYN_SMEM, st, 1, tkv, tv, tq, a);
 }
 template <int HB>
+cudaError_t launch_weights(bool fp8, const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq, const LArgs& a,
+                           cudaStream_t st) {
+  return fp8 ? launch_t<HB, true, kWeights>(tkv, tv, tq, a, st) : launch_t<HB, false, kWeights>(tkv, tv, tq, a, st);
+}
+template <int HB>
 cudaError_t launch_hb(bool fp8, int mode, const CUtensorMap& tkv, const CUtensorMap& tv, const CUtensorMap& tq,
                       const LArgs& a, cudaStream_t st) {
   switch (mode) {
     case kItems: return fp8 ? launch_t<HB, true, kItems>(tkv, tv, tq, a, st) : launch_t<HB, false, kItems>(tkv, tv, tq, a, st);
-    case kWeights:
-      return fp8 ? launch_t<HB, true, kWeights>(tkv, tv, tq, a, st) : launch_t<HB, false, kWeights>(tkv, tv, tq, a, st);
+    case kWeights: return launch_weights<HB>(fp8, tkv, tv, tq, a, st);
     default: break;
   }
   if (!fp8) return launch_t<HB, false, kEvery>(tkv, tv, tq, a, st);
@@ -999,44 +1025,13 @@ LatentRing latent_attn_ring(int n_q, int n_heads, const PagedRows& pg, bool sele
 
 int latent_attn_q_box_rows(int n_heads) { return head_block(n_heads); }
 
-namespace {
-// More than 64 heads are two blocks of columns on two CTAs; their sums are put together here, in one order.
-constexpr int kSumThreads = 256;
-__global__ void __launch_bounds__(kSumThreads) weights_sum_kernel(const __grid_constant__ LArgs a, int per_row) {
-  grid_trigger();
-  grid_wait();
-  const int t = blockIdx.x / per_row;
-  const uint32_t len = static_cast<uint32_t>(row_len(a.pg, t));
-  const uint32_t j0 = (blockIdx.x - static_cast<uint32_t>(t) * per_row) * (4 * kSumThreads) + threadIdx.x;
-  const float* part = a.w_part + t * a.w_pitch;
-  float x[4], y[4], z[4];
-  bool in[4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const uint32_t j = j0 + u * kSumThreads;
-    in[u] = j < len && static_cast<uint32_t>(gload(a.pg.block_table + static_cast<size_t>(t) * a.pg.max_pages +
-                                                   (j >> kPageShift))) < static_cast<uint32_t>(a.pg.n_pages);
-    if (!in[u]) continue;
-    x[u] = gload(part + j);
-    y[u] = gload(part + static_cast<long long>(a.n_q) * a.w_pitch + j);
-    z[u] = a.w_in ? gload(a.w_in + t * a.w_stride + j) : 0.f;
-  }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    if (in[u]) a.w_out[t * a.w_stride + j0 + u * kSumThreads] = z[u] + (x[u] + y[u]);
-}
-}  // namespace
-
-size_t key_weights_ws_bytes(int n_q, int n_heads, int max_pages) {
-  return n_heads > 64 ? static_cast<size_t>(2) * n_q * max_pages * kPageRows * sizeof(float) : 0;
-}
+int key_weights_q_box_rows(int n_heads) { return n_heads > 64 ? 128 : head_block(n_heads); }
 
 cudaError_t launch_key_weights(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
                                const CUtensorMap& tmap_q, const PagedRows& pg, int n_q, int n_heads, float scale,
                                const float* lse, const float* w_in, float* w_out, long long w_stride, uint32_t* status,
-                               void* scratch, cudaStream_t st) {
+                               cudaStream_t st) {
   const PipelineDebug dbg = pipeline_debug();
-  const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, false, 0));
   LArgs a{};
   a.latent = c.latent;
   a.scale = c.scale;
@@ -1044,26 +1039,23 @@ cudaError_t launch_key_weights(const LatentCache& c, const CUtensorMap& tmap_kv,
   a.pg = pg;
   a.n_q = n_q;
   a.H = n_heads;
-  a.n_grp = L.n_grp;
-  a.n_hb = L.n_hb;
-  a.n_cta = L.n_grp * L.n_hb;
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 152;
+  const long long tiles = n_q * row_tiles_max(pg, false, 0);
+  a.n_grp = a.n_cta = static_cast<int>(std::max(1LL, std::min<long long>(std::min(sms, kMostGroups), (tiles + 1) / 2)));
+  a.n_hb = 1;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.lse_in = lse;
   a.w_in = w_in;
   a.w_out = w_out;
-  a.w_part = static_cast<float*>(scratch);
   a.w_stride = w_stride;
-  a.w_pitch = static_cast<long long>(pg.max_pages) * kPageRows;
   a.status = status;
   a.wait_ns = dbg.wait_ns;
   a.stop_after = dbg.stop_after_tiles;
-  cudaError_t e = clear_status(status, st);
-  if (e == cudaSuccess) e = launch_latent_single(head_block(n_heads), c.fp8, kWeights, tmap_kv, tmap_v, tmap_q, a, st);
-  if (e == cudaSuccess && L.n_hb == 2) {
-    const int per_row = static_cast<int>((a.w_pitch + 4 * kSumThreads - 1) / (4 * kSumThreads));
-    e = launch_pdl(weights_sum_kernel, dim3(static_cast<unsigned>(n_q) * per_row), kSumThreads, 0, st, 1, a, per_row);
-  }
-  return e;
+  const cudaError_t e = clear_status(status, st);
+  if (e != cudaSuccess) return e;
+  if (n_heads > 64) return launch_weights<128>(c.fp8, tmap_kv, tmap_v, tmap_q, a, st);
+  return launch_latent_single(head_block(n_heads), c.fp8, kWeights, tmap_kv, tmap_v, tmap_q, a, st);
 }
 
 size_t latent_attn_ws_bytes(int n_q, int n_heads) {

@@ -114,8 +114,7 @@ struct LArgs {
   const float* lse_in;         // kWeights: [n_q][H]
   const float* w_in;           // [n_q] rows w_stride apart; nullptr: zeros
   float* w_out;
-  float* w_part;               // two blocks of heads: [2][n_q] rows w_pitch apart
-  long long w_stride, w_pitch;
+  long long w_stride;
   uint32_t* status;
   uint32_t* err;               // [CTAs][2]: error bits, bad-index count
   int n_cta;

@@ -570,9 +570,8 @@ dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, cons
  *   apart; weight_in NULL: zeros; it may be weight_out (in place), otherwise the two do not overlap.
  * Elements of weight_out behind a sequence's keys, and those of keys on a page outside the cache (flagged), stay
  * as they were.  desc->topk is not read; desc->n_kv == cache->n_rows.
- * ws: dsa_latent_key_weights_workspace_size bytes: 256, and beyond 64 heads 8 bytes for each row and key of
- * the table.  Errors: those of dsa_latent_attn_paged, DSA_ERR_ARG (weight_stride), DSA_ERR_SHAPE (n_q * max_pages
- * beyond 2^29 - 1). */
+ * ws: dsa_latent_key_weights_workspace_size bytes (256).  Errors: those of dsa_latent_attn_paged, DSA_ERR_ARG
+ * (weight_stride). */
 dsa_status dsa_latent_key_weights_workspace_size(const dsa_attn_desc* desc, const dsa_paged_cache* pages, size_t* bytes);
 dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, const dsa_latent_cache* cache,
                                   const dsa_paged_cache* pages, const float* lse, const float* weight_in,
