@@ -8,7 +8,8 @@
 // weight is found by a radix select on order-preserving 32-bit keys, 11, 11 and 10 bits at a time: a histogram
 // per CTA, summed over the cluster through distributed shared memory, one bin of which goes on.  Then each warp
 // counts the keys above and at the limit, a scan over the cluster's warps says where its own go, and it writes
-// them in order by ballots.  The weights are read four more times, out of L2.
+// them in order by ballots.  A CTA reads its keys once where it can hold them, up to 8192 in registers, up to 24576 in
+// shared memory; of longer sequences they are read again in every pass, out of L2.
 //
 // Copying.  A warp takes eight rows; HBM bounds it.
 #include <cuda_bf16.h>
@@ -25,6 +26,9 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;
 constexpr int kBins = 2048;
+// Where a CTA holds its keys: sixteen a lane in registers, 48 in shared memory, or nowhere.
+enum Hold : int { kRegisters = 0, kShared = 1, kNowhere = 2 };
+constexpr int kHeld = 16, kSharedHeld = 48;
 
 // Larger weights have larger keys, -0 that of 0; a NaN has the smallest.
 __device__ __forceinline__ uint32_t weight_key(float w) { return w == w ? float_key(w) : 0u; }
@@ -65,10 +69,16 @@ __device__ __forceinline__ uint32_t warp_incl(uint32_t x) {
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_constant__ Evict e, int n_cta, uint32_t* status) {
+template <int HOLD>
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_constant__ Evict e, int n_cta, uint32_t* status) {
   __shared__ Smem sh;
+  extern __shared__ float in_shared[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x / n_cta, rank = blockIdx.x - t * n_cta;
+  const auto sync = [&]() {
+    if (n_cta > 1) cluster_sync_all();
+    else __syncthreads();
+  };
   grid_trigger();
   grid_wait();
   const int want = gload(e.from.seq_len + t);
@@ -77,28 +87,52 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   const float* w = e.weight + t * e.weight_stride;
   float* w_out = e.weight_out ? e.weight_out + t * e.weight_out_stride : nullptr;
   int32_t* kept = e.kept + static_cast<long long>(t) * e.n_keep;
+  const bool all = L <= e.n_keep;
+  const int head = all ? L : e.n_first, tail = all ? 0 : e.n_last;
+  const int K = n - head - tail;
+  // the warp's run [lo, hi) of the keys between
+  const int from = head, to = L - tail;
+  const int run = (to - from + n_cta * kWarps - 1) / (n_cta * kWarps);
+  const int lo = min(to, from + (rank * kWarps + warp) * run), hi = K > 0 ? min(to, lo + run) : lo;
+  float held[HOLD == kRegisters ? kHeld : 1];
+  float* mine = in_shared + warp * (32 * kSharedHeld) + lane;
+  if constexpr (HOLD == kRegisters) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) held[u] = lo + 32 * u + lane < hi ? gload(w + lo + 32 * u + lane) : 0.f;
+  } else if constexpr (HOLD == kShared) {
+#pragma unroll 8
+    for (int j = lo + lane; j < hi; j += 32) mine[j - lo - lane] = gload(w + j);
+  }
+  // each(j, weight of key j, whether there is one) for 32 keys after another
+  const auto keys = [&](auto&& each) {
+    if constexpr (HOLD == kRegisters) {
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u)
+        if (lo + 32 * u < hi) each(lo + 32 * u + lane, held[u], lo + 32 * u + lane < hi);
+    } else {
+#pragma unroll 4
+      for (int j0 = lo; j0 < hi; j0 += 32) {
+        const bool there = j0 + lane < hi;
+        const float x = !there ? 0.f : HOLD == kShared ? mine[j0 - lo] : gload(w + j0 + lane);
+        each(j0 + lane, x, there);
+      }
+    }
+  };
   if (rank == 0 && threadIdx.x == 0) {
     if (want != L) report(status, false, DEV_ERR_RANGE);
     e.new_len[t] = n;
   }
+  // those that stay in any case, and the unused end of kept
   const int stride = n_cta * kThreads, me = rank * kThreads + static_cast<int>(threadIdx.x);
   const auto keep = [&](int place, int j) {
     kept[place] = j;
     if (w_out) w_out[place] = gload(w + j);
   };
-  // those that stay in any case, and the unused end of kept
-  const bool all = L <= e.n_keep;
-  const int head = all ? L : e.n_first, tail = all ? 0 : e.n_last;
   for (int i = me; i < head; i += stride) keep(i, i);
   for (int i = me; i < tail; i += stride) keep(n - tail + i, L - tail + i);
   for (int i = n + me; i < e.n_keep; i += stride) kept[i] = -1;
-  const int K = n - head - tail;
   if (K == 0) return;                                          // (the whole cluster)
 
-  // the warp's run [lo, hi) of the keys between
-  const int from = head, to = L - tail;
-  const int run = (to - from + n_cta * kWarps - 1) / (n_cta * kWarps);
-  const int lo = min(to, from + (rank * kWarps + warp) * run), hi = min(to, lo + run);
   uint32_t limit = 0;                // bits of the limit found so far
   uint32_t need = static_cast<uint32_t>(K);
 #pragma unroll 1
@@ -107,34 +141,31 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     const int bits = pass == 2 ? 10 : 11;
     for (int b = threadIdx.x; b < kBins; b += kThreads) sh.mine[b] = 0;
     __syncthreads();
-    constexpr int U = 4;
-#pragma unroll 1
-    for (int j0 = lo + lane; j0 < hi; j0 += 32 * U) {
-      float x[U];
+    keys([&](int, float x, bool there) {
+      const uint32_t key = weight_key(x);
+      if (there && (pass == 0 || (key >> (shift + bits)) == limit)) atomicAdd(&sh.mine[(key >> shift) & ((1u << bits) - 1u)], 1u);
+    });
+    sync();
+    if (n_cta > 1) {
+      // a part of the bins each, summed over the cluster, to every CTA
+      const int part = kBins / n_cta + 1;
+      for (int b = rank * part + static_cast<int>(threadIdx.x); b < min(kBins, (rank + 1) * part); b += kThreads) {
+        uint32_t c[kMostCtas], s = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = j0 + 32 * u < hi ? gload(w + j0 + 32 * u) : 0.f;
+        for (int k = 0; k < kMostCtas; ++k) c[k] = k < n_cta ? load_cta(&sh.mine[b], k) : 0u;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint32_t key = weight_key(x[u]);
-        const bool in = j0 + 32 * u < hi && (pass == 0 || (key >> (shift + bits)) == limit);
-        if (in) atomicAdd(&sh.mine[(key >> shift) & ((1u << bits) - 1u)], 1u);
+        for (int k = 0; k < kMostCtas; ++k) s += c[k];
+        for (int k = 0; k < n_cta; ++k) store_cta(&sh.all[b], k, s);
       }
+      cluster_sync_all();
     }
-    cluster_sync_all();
-    // a part of the bins each, summed over the cluster, to every CTA
-    const int part = kBins / n_cta + 1;
-    for (int b = rank * part + static_cast<int>(threadIdx.x); b < min(kBins, (rank + 1) * part); b += kThreads) {
-      uint32_t s = 0;
-      for (int c = 0; c < n_cta; ++c) s += load_cta(&sh.mine[b], c);
-      for (int c = 0; c < n_cta; ++c) store_cta(&sh.all[b], c, s);
-    }
-    cluster_sync_all();
     // the bin that holds the need-th entry from above: thread i takes the four bins from the top
+    const uint32_t* hist = n_cta > 1 ? sh.all : sh.mine;
     constexpr int PER = kBins / kThreads;
     uint32_t c[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      c[i] = sh.all[kBins - 1 - (static_cast<int>(threadIdx.x) * PER + i)];
+      c[i] = hist[kBins - 1 - (static_cast<int>(threadIdx.x) * PER + i)];
       sum += c[i];
     }
     const uint32_t incl = warp_incl(sum);
@@ -157,19 +188,18 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   }
   // limit: the K-th heaviest weight; need: how many of that weight stay
   uint32_t above = 0, at = 0;
-#pragma unroll 4
-  for (int j = lo + lane; j < hi; j += 32) {
-    const uint32_t key = weight_key(gload(w + j));
-    above += key > limit ? 1u : 0u;
-    at += key == limit ? 1u : 0u;
-  }
+  keys([&](int, float x, bool there) {
+    const uint32_t key = weight_key(x);
+    above += there && key > limit ? 1u : 0u;
+    at += there && key == limit ? 1u : 0u;
+  });
   above = __reduce_add_sync(0xffffffffu, above);
   at = __reduce_add_sync(0xffffffffu, at);
   if (lane < n_cta) {
     store_cta(&sh.above[rank * kWarps + warp], lane, above);
     store_cta(&sh.at[rank * kWarps + warp], lane, at);
   }
-  cluster_sync_all();
+  sync();
   // what the warps before this one hold
   uint32_t above_before = 0, at_before = 0;
   for (int g = lane; g < rank * kWarps + warp; g += 32) {
@@ -178,12 +208,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
   }
   above_before = __reduce_add_sync(0xffffffffu, above_before);
   at_before = __reduce_add_sync(0xffffffffu, at_before);
-#pragma unroll 2
-  for (int j0 = lo; j0 < hi; j0 += 32) {
-    const int j = j0 + lane;
-    const float x = j < hi ? gload(w + j) : 0.f;
+  keys([&](int j, float x, bool there) {
     const uint32_t key = weight_key(x);
-    const uint32_t a = __ballot_sync(0xffffffffu, j < hi && key > limit), q = __ballot_sync(0xffffffffu, j < hi && key == limit);
+    const uint32_t a = __ballot_sync(0xffffffffu, there && key > limit), q = __ballot_sync(0xffffffffu, there && key == limit);
     const uint32_t lower = (1u << lane) - 1u;
     const uint32_t at_here = at_before + __popc(q & lower);
     const bool stays = ((a >> lane) & 1u) || (((q >> lane) & 1u) && at_here < need);
@@ -194,13 +221,12 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const __grid_con
     }
     above_before += __popc(a);
     at_before += __popc(q);
-  }
+  });
 }
 
-// Eight rows a warp: lane l looks row l & 7 up, a trip each for its place and its page, then all rows' loads are in
-// flight before the first store.
-constexpr int kCopyRows = 8;
-template <bool FP8>
+// kCopyRows rows a warp: lane l looks one of them up, a trip each for its place and its page, then all rows' loads
+// are in flight before the first store (bf16: half of them).  Eight rows where there are many, else two.
+template <bool FP8, int kCopyRows>
 __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__ Evict e, const LatentCache src,
                                                          const LatentCache dst, int per_seq, uint32_t* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -225,7 +251,8 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
     }
   }
   if constexpr (FP8) {
-    uint4 v[kCopyRows], r[kCopyRows / 4];
+    constexpr int kRope = (kCopyRows + 3) / 4;       // four rows' rotary dims an instruction
+    uint4 v[kCopyRows], r[kRope];
     uint32_t sc = 0;
 #pragma unroll
     for (int k = 0; k < kCopyRows; ++k) {
@@ -233,9 +260,9 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
       if (row >= 0) v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 512) + lane);
     }
 #pragma unroll
-    for (int k = 0; k < kCopyRows / 4; ++k) {
-      const int row = __shfl_sync(0xffffffffu, from, 4 * k + (lane >> 3));
-      if (row >= 0) r[k] = gload(reinterpret_cast<const uint4*>(src.rope + static_cast<size_t>(row) * 64) + (lane & 7));
+    for (int k = 0; k < kRope; ++k) {
+      const int q = 4 * k + (lane >> 3), row = __shfl_sync(0xffffffffu, from, q);
+      if (q < kCopyRows && row >= 0) r[k] = gload(reinterpret_cast<const uint4*>(src.rope + static_cast<size_t>(row) * 64) + (lane & 7));
     }
     if (lane < kCopyRows && from >= 0) sc = gload(reinterpret_cast<const uint32_t*>(src.scale) + from);
 #pragma unroll
@@ -244,26 +271,26 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
       if (row >= 0) reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 512)[lane] = v[k];
     }
 #pragma unroll
-    for (int k = 0; k < kCopyRows / 4; ++k) {
-      const int row = __shfl_sync(0xffffffffu, to, 4 * k + (lane >> 3));
-      if (row >= 0) reinterpret_cast<uint4*>(dst.rope + static_cast<size_t>(row) * 64)[lane & 7] = r[k];
+    for (int k = 0; k < kRope; ++k) {
+      const int q = 4 * k + (lane >> 3), row = __shfl_sync(0xffffffffu, to, q);
+      if (q < kCopyRows && row >= 0) reinterpret_cast<uint4*>(dst.rope + static_cast<size_t>(row) * 64)[lane & 7] = r[k];
     }
     if (lane < kCopyRows && to >= 0) reinterpret_cast<uint32_t*>(dst.scale)[to] = sc;
   } else {
     // 72 vectors a row
-    constexpr int kVec = 72, kAll = kCopyRows * kVec / 32;
+    constexpr int kVec = 72, kAll = (kCopyRows * kVec + 31) / 32, kPart = kCopyRows > 4 ? (kAll + 1) / 2 : kAll;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint4 v[kAll / 2];
+    for (int h = 0; h < kAll; h += kPart) {
+      uint4 v[kPart];
 #pragma unroll
-      for (int k = 0; k < kAll / 2; ++k) {
-        const int x = (h * (kAll / 2) + k) * 32 + lane, row = __shfl_sync(0xffffffffu, from, x / kVec);
-        if (row >= 0) v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 1152) + x % kVec);
+      for (int k = 0; k < kPart; ++k) {
+        const int x = (h + k) * 32 + lane, row = __shfl_sync(0xffffffffu, from, x / kVec);
+        if (x < kCopyRows * kVec && row >= 0) v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 1152) + x % kVec);
       }
 #pragma unroll
-      for (int k = 0; k < kAll / 2; ++k) {
-        const int x = (h * (kAll / 2) + k) * 32 + lane, row = __shfl_sync(0xffffffffu, to, x / kVec);
-        if (row >= 0) reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 1152)[x % kVec] = v[k];
+      for (int k = 0; k < kPart; ++k) {
+        const int x = (h + k) * 32 + lane, row = __shfl_sync(0xffffffffu, to, x / kVec);
+        if (x < kCopyRows * kVec && row >= 0) reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 1152)[x % kVec] = v[k];
       }
     }
   }
@@ -276,15 +303,32 @@ cudaError_t launch_evict(const Evict& a, const LatentCache& src, const LatentCac
   if (e != cudaSuccess) return e;
   int sms = device_sm_count();
   if (sms <= 0) sms = 152;
-  const int ctas = std::max(1, std::min(kMostCtas, 2 * sms / std::max(1, std::min(a.n_seq, 2 * sms))));
-  e = launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(ctas)), kThreads, 0, st, ctas, a,
-                 ctas, status);
+  // as many CTAs as hold the longest sequence that the table allows in registers, while all are resident at once
+  const int width = a.from.max_pages * kPageRows;
+  const int fit = 2 * sms / std::max(1, std::min(a.n_seq, 2 * sms));
+  const int ctas = std::max(1, std::min({kMostCtas, fit, (width + kHeld * kThreads - 1) / (kHeld * kThreads)}));
+  const dim3 grid(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(ctas));
+  // (a warp's run is the CTA's sixteenth, rounded up)
+  const long long run = (static_cast<long long>(width) + ctas * kWarps - 1) / (ctas * kWarps);
+  if (run <= 32 * kHeld) {
+    e = launch_pdl(evict_select_kernel<kRegisters>, grid, kThreads, 0, st, ctas, a, ctas, status);
+  } else if (run <= 32 * kSharedHeld) {
+    constexpr int kBytes = kThreads * kSharedHeld * static_cast<int>(sizeof(float));
+    if ((e = smem_attr_once<evict_select_kernel<kShared>>(kBytes)) != cudaSuccess) return e;
+    e = launch_pdl(evict_select_kernel<kShared>, grid, kThreads, kBytes, st, ctas, a, ctas, status);
+  } else {
+    e = launch_pdl(evict_select_kernel<kNowhere>, grid, kThreads, 0, st, ctas, a, ctas, status);
+  }
   if (e != cudaSuccess) return e;
-  const int rows = std::min(a.n_keep, a.from.max_pages * kPageRows);
-  const int per_seq = (rows + 8 * kCopyRows - 1) / (8 * kCopyRows);
-  return launch_pdl(src.fp8 ? evict_copy_kernel<true> : evict_copy_kernel<false>,
-                    dim3(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(per_seq)), 256, 0, st, 1, a, src, dst, per_seq,
-                    status);
+  const int rows = std::min(a.n_keep, width);
+  const int each = static_cast<long long>(a.n_seq) * rows > 64LL * sms ? 8 : 2;
+  const int per_seq = (rows + 8 * each - 1) / (8 * each);
+  const auto go = [&](auto kern) {
+    return launch_pdl(kern, dim3(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(per_seq)), 256, 0, st, 1, a, src, dst,
+                      per_seq, status);
+  };
+  if (each == 8) return src.fp8 ? go(evict_copy_kernel<true, 8>) : go(evict_copy_kernel<false, 8>);
+  return src.fp8 ? go(evict_copy_kernel<true, 2>) : go(evict_copy_kernel<false, 2>);
 }
 
 }  // namespace dsa

@@ -117,7 +117,7 @@ def test_edges(keep, first, last, kind, fmt):
 
 @pytest.mark.parametrize("kind", ["spread", "ties", "equal", "close", "odd"])
 @pytest.mark.parametrize("lens,keep", [([70000], 30000), ([40001, 3], 1), ([9000] * 50, 2048), (list(range(0, 800, 2)), 100),
-                                       ([20000, 100, 15000], 14999)])
+                                       ([20000, 100, 15000], 14999), ([250000, 5], 9000), ([14000] * 170, 3000)])
 def test_long_and_many_sequences(lens, keep, kind):
     pc = Paged(lens, "fp8", seed=len(lens))
     w = _weights(pc, 5, kind)
