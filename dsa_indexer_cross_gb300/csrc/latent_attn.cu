@@ -55,8 +55,7 @@ struct LCfg {
   // columns in one warp)
   static constexpr int SW = HB >= 32 && !FP8 && !WEIGHTS ? 8 : 4;
   static constexpr int SOFT = 32 * SW;
-  static constexpr int NG = 2;                         // fp8: groups of four converter warps
-  static constexpr int NP = FP8 ? 4 * NG : 1;          // producer warps
+  static constexpr int NP = FP8 ? 8 : 1;               // producer warps
   static constexpr int S_WARP = SW + NP;
   static constexpr int PV_WARP = S_WARP + 1;
   static constexpr int THREADS = 32 * (SW + NP + 2);
@@ -69,7 +68,7 @@ struct LCfg {
 };
 
 struct LShared {
-  uint64_t full[2][2], empty[4][2];   // by slot and half: latent dims 0 .. 255; 256 .. 511 and the rotary dims
+  uint64_t full[2][2], empty[2][2];   // by slot (empty: tile parity) and half: latent dims 0 .. 255; 256 .. 511 and the rotary dims
   // [2]: by tile parity.  (One p_full for all tiles would not do: the softmax may be two tiles ahead of
   // the PV warp's look, and a barrier two phases on reads as not yet complete.)
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free, mma_done;
@@ -107,16 +106,15 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       // fp8: each warp of the group (second half: and each thread's copies)
-      mbar_init(&sh.full[s][0], FP8 ? 4 : 1);
-      mbar_init(&sh.full[s][1], FP8 ? 33 * 4 : 1);
+      constexpr int kFillers = !FP8 ? 1 : MODE == kWeights ? 8 : 4;       // warps that fill a tile
+      mbar_init(&sh.full[s][0], kFillers);
+      mbar_init(&sh.full[s][1], FP8 ? 33 * kFillers : 1);
+      mbar_init(&sh.empty[s][0], 1);
+      mbar_init(&sh.empty[s][1], 1);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], C::SW);
       mbar_init(&sh.p_full[s], C::SW);
       mbar_init(&sh.o_done[s], 1);
-    }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&sh.empty[s][0], 1);
-      mbar_init(&sh.empty[s][1], 1);
     }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
@@ -148,13 +146,9 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
   const uint32_t tmem = sh.tmem_base;
   Walk<MODE> walk(a, share > 0 ? sh.share.row0 : 0, share > 0 ? sh.share.tile0 : 0, share);
   Seg sg{};
-  // Tile g's slot, how many tiles were in it before, and the barrier by which it is freed.  Converters of more
-  // groups than slots may ask for a slot two tiles ahead of its use, so (weights) tiles are freed on four barriers in
-  // turn: the one asked about is then never more than one phase behind.
+  // Tile g's slot, and how many tiles were in it before.  (Tiles are freed on barriers by their parity.)
   const auto slot = [](uint32_t g) -> uint32_t { return C::SLOTS == 2 ? g & 1 : 0u; };
   const auto lap = [](uint32_t g) -> uint32_t { return C::SLOTS == 2 ? g >> 1 : g; };
-  const auto freed = [&](uint32_t g, int h) -> uint64_t* { return &sh.empty[MODE == kWeights ? g & 3 : g & 1][h]; };
-  const auto freed_lap = [](uint32_t g) -> uint32_t { return MODE == kWeights ? g >> 2 : g >> 1; };
 
   if (warp >= C::SW && warp < C::S_WARP) {
     // ---------------------------------------------------------------- Q and the rows
@@ -182,7 +176,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
 #pragma unroll 1
           for (int h = 0; h < 2 && ok; ++h) {
             uint64_t* full = &sh.full[slot(g)][h];
-            if (g >= C::SLOTS) ok = wait(freed(g - C::SLOTS, h), freed_lap(g - C::SLOTS) & 1);
+            if (g >= C::SLOTS) ok = wait(&sh.empty[(g - C::SLOTS) & 1][h], ((g - C::SLOTS) >> 1) & 1);
             if (ok && lane == 0) {
               mbar_arrive_expect_tx(full, (4 + h) * kBlkBytes);
               tma_load_3d(st + 4 * h * kBlkBytes, &tmap_v, full, 0, row, 4 * h);
@@ -193,16 +187,123 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         }
       }
     }
-    if constexpr (FP8) {
-      // Groups of four warps take the tiles in turn, so one group's loads are in flight while another
-      // converts; a warp takes sixteen rows of its group's tiles.  (One group with two tiles in
+    if constexpr (FP8 && MODE == kWeights) {
+      // All eight warps convert each tile, eight rows a warp, with two tiles' codes in registers: half a tile's are
+      // asked for as soon as the half two tiles before is converted.  (Two groups of four warps that take the tiles
+      // in turn, as for the attention, wait for each other where shared memory has room for one bf16 tile.)  Lane
+      // l looks after row l & 7: its page is found three tiles ahead, its scale word two.
+      const int row_base = 8 * pw, my_row = row_base + (lane & 7);
+      const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4 (+ 4), row parity
+      const uint32_t tile0 = smem_u32(sT);
+      const uint32_t line0 = tile0 + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
+      struct Codes {
+        uint4 w[8];              // rows 2 k + par: w[2 k], of the first half, w[2 k + 1], of the second
+        uint32_t sc;             // scale word of the lane's row
+        int at;                  // its cache row (-1: no key)
+      };
+      Walk<MODE> aw(walk);
+      Seg as;
+      int ai = 0, len = 0;
+      bool alive = aw.next(as);
+      if (alive) len = row_len(a.pg, as.row);
+      int j = -1, jlen = 0, page = -1;         // the next tile's key of this lane, and its page
+      const auto find_page = [&]() {
+        j = -1;
+        if (!alive) return;
+        const int i = as.i0 + ai;
+        j = i * kRows + my_row;
+        jlen = len;
+        page = gload(a.pg.block_table + static_cast<size_t>(as.row) * a.pg.max_pages + (i >> 1));
+        if (++ai == as.n) {
+          ai = 0;
+          alive = aw.next(as);
+          if (alive) len = row_len(a.pg, as.row);
+        }
+      };
+      const uint8_t* next = nullptr;           // this lane's codes of the tile that is asked for
+      const auto ask = [&](Codes& x, int h) {
+        if (h == 0) {
+          const bool in = j >= 0 && static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pg.n_pages);
+          if (!in && j >= 0 && my_row == 0 && lane == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+          const int row = in ? (page << kPageShift) + (j & (kPageRows - 1)) : my_row;     // a row of the cache in any case
+          x.at = in && j < jlen ? row : -1;
+          x.sc = gload(reinterpret_cast<const uint32_t*>(a.scale) + row);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(row) * 64));
+          next = a.latent + static_cast<size_t>(row - (lane & 7) + par) * kDv + blk4 * 64 + c * 16;
+          find_page();
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.w[2 * k + h] = gload_once(next + 2 * k * kDv + 256 * h);
+      };
+      const auto step = [&](Codes& x) -> bool {
+        const uint32_t sl = slot(g) * kTileBytes, line = opaque(line0 + sl), tile = tile0 + sl;
+        uint32_t m[4];                         // scale words of this lane's rows; all ones: no key
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m[k] = __shfl_sync(0xffffffffu, x.sc, 2 * k + par);
+          if (__shfl_sync(0xffffffffu, x.at, 2 * k + par) < 0) m[k] = 0xFFFFFFFFu;
+        }
+        int from[2];                           // rows of its two 16-byte pieces of rotary dims
+#pragma unroll
+        for (int k = 0; k < 2; ++k) from[k] = __shfl_sync(0xffffffffu, x.at, 4 * k + (lane >> 3));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (g >= C::SLOTS && !wait(&sh.empty[(g - C::SLOTS) & 1][h], ((g - C::SLOTS) >> 1) & 1)) return false;
+          if (h == 1) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int q = row_base + 4 * k + (lane >> 3);      // row, 16-byte chunk lane & 7
+              cp_async_16_zfill(tile + 8 * kBlkBytes + q * 128 + (((lane & 7) ^ (q & 7)) << 4),
+                                a.rope + static_cast<size_t>(max(from[k], 0)) * 64 + (lane & 7) * 8, from[k] >= 0);
+            }
+            cp_async_mbar_arrive(&sh.full[slot(g)][1]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t d = (line ^ (static_cast<uint32_t>(2 * k) << 4)) + 256 * k + 4 * h * kBlkBytes;
+            // a row without a key: times zero
+            const uint32_t f = m[k] == 0xFFFFFFFFu ? 0u : fp8_mult((m[k] >> (16 * h + 8 * (blk4 >> 1))) & 0xFFu);
+            const uint4 v = x.w[2 * k + h];
+            uint32_t o[8];
+            fp8x4_to_bf16(v.x, f, o[0], o[1]);
+            fp8x4_to_bf16(v.y, f, o[2], o[3]);
+            fp8x4_to_bf16(v.z, f, o[4], o[5]);
+            fp8x4_to_bf16(v.w, f, o[6], o[7]);
+            sts128(d, o[0], o[1], o[2], o[3]);
+            sts128(d ^ 16u, o[4], o[5], o[6], o[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[slot(g)][h]);
+          ask(x, h);
+        }
+        return true;
+      };
+      const uint32_t n_tiles = a.stop_after >= 0 ? min(static_cast<uint32_t>(share), static_cast<uint32_t>(a.stop_after))
+                                                 : static_cast<uint32_t>(share);       // (test hook)
+      Codes x, y;
+      find_page();
+      ask(x, 0);
+      ask(x, 1);
+      ask(y, 0);
+      ask(y, 1);
+#pragma unroll 1
+      while (g < n_tiles) {
+        if (!step(x)) break;
+        if (++g >= n_tiles || !step(y)) break;
+        ++g;
+      }
+      cp_async_wait<0>();
+    } else if constexpr (FP8) {
+      // Two groups of four warps take the tiles in turn, so one group's loads are in flight while the
+      // other converts; a warp takes sixteen rows of its group's tiles.  (One group with two tiles in
       // flight per warp was slower: a wait for any result also waited for the other tile's loads.)
       // A load instruction takes 256 bytes of two rows, whole 128-byte lines; eight lanes of a store
       // phase cover two rows x every other 16-byte chunk, which the swizzle spreads over all banks.
       // Lane l looks after row l & 15: its offset is found two of the group's tiles ahead, its page
       // one, its codes as soon as the registers are free, across segments.  The rotary dims, which
       // need no conversion, are copied when the slot is free, out of L2.
-      const uint32_t turn = pw >> 2;                                      // tiles with g % NG == turn
+      const uint32_t turn = pw >> 2;                                      // tiles with g & 1 == turn, in slot `turn`
       const int row_base = 16 * (pw & 3), my_row = row_base + (lane & 15);
       const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4 (+ 4), row parity
       uint4 w[16];
@@ -234,8 +335,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         lenx = len0;
         const int s = (as.i0 + ai) * kRows + my_row;
         j0 = !SEL ? s : s < a.topk ? gload(a.idx + static_cast<size_t>(row0) * a.topk + s) : -1;
-#pragma unroll
-        for (int n = 0; n < C::NG; ++n) advance();
+        advance();
+        advance();
       };
       auto page_step = [&]() {
         j2 = j1;
@@ -274,23 +375,22 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         sc = gload(reinterpret_cast<const uint32_t*>(a.scale) + row);
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rope + static_cast<size_t>(row) * 64));
       };
-      for (uint32_t n = 0; n < turn; ++n) advance();
+      if (turn) advance();
       offset_step();
       offset_step();
       page_step();
       offset_step();
       fetch_step();
       page_step();
-      const uint32_t tile0 = smem_u32(sT);
+      const uint32_t tile = smem_u32(sT + turn * kTileBytes);
       // the lane's line of row par in block blk4, swizzled for chunk 2 c; row 2 k + par's lies 256 k on, its
       // swizzle differs by 2 k (mod 8)
       const uint32_t lane_line =
-          tile0 + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
+          tile + blk4 * kBlkBytes + (row_base + par) * 128 + (static_cast<uint32_t>((2 * c) ^ par) << 4);
       // one tile: registers -> the bf16 tile, then the registers' next fetch
       auto tile_step = [&]() -> bool {
         if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) return false;   // test hook
-        const uint32_t sl = C::SLOTS == C::NG ? turn : slot(g), tile = tile0 + sl * kTileBytes;
-        const uint32_t line = opaque(lane_line + sl * kTileBytes);
+        const uint32_t line = opaque(lane_line);
         uint32_t rsc[8];                     // scale words of this lane's rows; all ones: no key
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -301,7 +401,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         // previous tile's second product leaves the first half before it is done with the other
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (g >= C::SLOTS && !wait(freed(g - C::SLOTS, h), freed_lap(g - C::SLOTS) & 1)) return false;
+          if (g >= 2 && !wait(&sh.empty[turn][h], ((g >> 1) - 1) & 1)) return false;
           if (h == 1) {
             const uint32_t rl = opaque(tile) + 8 * kBlkBytes + row_base * 128;
 #pragma unroll
@@ -311,10 +411,10 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
               cp_async_16_zfill(rl + q * 128 + (((lane & 7) ^ (q & 7)) << 4),
                                 a.rope + static_cast<size_t>(max(from, 0)) * 64 + (lane & 7) * 8, from >= 0);
             }
-            cp_async_mbar_arrive(&sh.full[sl][1]);
+            cp_async_mbar_arrive(&sh.full[turn][1]);
             if constexpr (SEL) {
               const uint32_t keys = __ballot_sync(0xffffffffu, at >= 0) & 0xFFFFu;
-              if (lane == 0) sh.keys[sl][pw & 3] = keys;
+              if (lane == 0) sh.keys[turn][pw & 3] = keys;
             }
           }
 #pragma unroll
@@ -333,14 +433,14 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[sl][h]);
+          if (lane == 0) mbar_arrive(&sh.full[turn][h]);
         }
         offset_step();
         fetch_step();
         page_step();
         return true;
       };
-      for (g = turn; ok && g < static_cast<uint32_t>(share); g += C::NG) ok = tile_step();
+      for (g = turn; ok && g < static_cast<uint32_t>(share); g += 2) ok = tile_step();
       cp_async_wait<0>();
     }
     // let every copy this CTA started land before its shared memory can be released (a wait that ran out
@@ -363,15 +463,18 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
     while (ok && walk.next(sg)) {
       const int len = row_len(a.pg, sg.row);
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
-      // log-sum-exps in log2; +inf, which weighs nothing, for columns past the last head and for heads
-      // without any key
+      // log-sum-exps in log2, and the columns that count: not those past the last head (other rows' q, whose
+      // scores of an infinite key would make it NaN) nor heads without any key
       float lse2[2 * NR];
+      uint32_t counts = 0;
 #pragma unroll
       for (int c = 0; c < 2 * NR; ++c) {
         const int h = 8 * (c >> 1) + cq + (c & 1);
-        const float l = h < a.H ? gload(a.lse_in + sg.col0 + h) * 1.4426950408889634f : INFINITY;
-        lse2[c] = l == -INFINITY ? INFINITY : l;
+        const float l = h < a.H ? gload(a.lse_in + sg.col0 + h) * 1.4426950408889634f : -INFINITY;
+        lse2[c] = l == -INFINITY ? 0.f : l;
+        if (l != -INFINITY) counts |= 1u << c;
       }
+      const bool all = __all_sync(0xffffffffu, counts == (NR == 16 ? 0xFFFFFFFFu : (1u << (2 * NR)) - 1u));
       float* to = a.w_out + sg.row * a.w_stride;
       const float* from = a.w_in ? a.w_in + sg.row * a.w_stride : nullptr;
       for (int n = 0; n < sg.n; ++n, ++g) {
@@ -397,8 +500,12 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
           }
 #pragma unroll
           for (int c = 0; c < 2 * K; ++c) {
-            x += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + (c & 1)]), a.scale_log2, -lse2[2 * k0 + c]));
-            y += ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + 2 + (c & 1)]), a.scale_log2, -lse2[2 * k0 + c]));
+            const float p = ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + (c & 1)]), a.scale_log2, -lse2[2 * k0 + c]));
+            const float q = ex2f(fmaf(__uint_as_float(v[4 * (c >> 1) + 2 + (c & 1)]), a.scale_log2, -lse2[2 * k0 + c]));
+            if (all || (counts >> (2 * k0 + c) & 1u)) {
+              x += p;
+              y += q;
+            }
           }
         }
 #pragma unroll
@@ -716,7 +823,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
             for (int kb = 4 * h; kb < 4 + 5 * h; ++kb)
               umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
                                        dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
-            if constexpr (MODE == kWeights) umma_commit_elect(freed(g, h));      // no second product
+            if constexpr (MODE == kWeights) umma_commit_elect(&sh.empty[sb][h]);      // no second product
           }
           if (!ok) break;
           umma_commit_elect(&sh.s_full[sb]);

@@ -115,6 +115,21 @@ def test_heads_without_keys_infinities_and_nan(H):
     assert bool(torch.isnan(out[0, 77])) and int(torch.isnan(out[:, :].float()).sum()) == 1
 
 
+@pytest.mark.parametrize("H", [5, 40, 100])
+def test_other_rows_columns_do_not_count(H):
+    """A key that is -inf in a dim where this row's heads are positive, and the next row's, which lie behind them in
+    q, negative: its scores are -inf, its weight is zero."""
+    pc = Paged([300, 300], "bf16", seed=1)
+    q = randn((2, H, 576), gen(2))
+    q[0, :, 9], q[1, :, 9] = 1.0, -1.0
+    pc.rows[pc.phys[0][77], 9] = -float("inf")
+    _, lse, _ = attend(pc, q)
+    out, ws = _weigh(pc, q, lse)
+    assert D.dsa_workspace_status(ws) == 0
+    assert float(out[0, 77]) == 0.0 and bool(torch.isfinite(out[0, :300]).all())
+    assert abs(float(out[0, :300].double().sum()) - H) <= H * 2.0 ** -9
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
 @pytest.mark.parametrize("H", [16, 100])
 def test_bad_pages_and_lengths(H, fmt):
