@@ -1085,15 +1085,16 @@ dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, cons
   const size_t need = kAlign + align_up(latent_shared_ws_bytes(d.n_q, d.n_heads, groups->n_groups, groups->max_rows));
   if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "shared attention workspace too small: %zu < %zu bytes", ws_bytes, need);
   const SharedWalks walks = latent_shared_walks(d.n_q, d.n_heads, groups->n_groups, groups->max_rows);
-  CUtensorMap tkv[2], tv[2], tq[2];
+  CUtensorMap tkv[3], tv[3], tq[3];
   std::memset(tkv, 0, sizeof(tkv));
   std::memset(tv, 0, sizeof(tv));
   std::memset(tq, 0, sizeof(tq));
-  for (int k = 0; k < walks.n; ++k) {
-    const bool pair = walks.pair[k];
-    if (!c.fp8 || pair) {
-      const void* rows = c.fp8 ? static_cast<const uint8_t*>(ws) + kAlign + walks.ring_offset[k] : c.latent;
-      const uint64_t n = static_cast<uint64_t>(c.fp8 ? walks.ring_rows[k] : c.n_rows);
+  for (int k = 0; k < 3; ++k) {
+    if (!walks.used[k] || (k == 2 && !c.fp8)) continue;
+    const bool pair = walks.pair[k], scratch = c.fp8 && walks.rows[k] > 0;
+    if (!c.fp8 || scratch) {
+      const void* rows = scratch ? static_cast<const uint8_t*>(ws) + kAlign + walks.rows_offset[k] : c.latent;
+      const uint64_t n = static_cast<uint64_t>(scratch ? walks.rows[k] : c.n_rows);
       if ((s = tmap_kv_tiles(&tkv[k], rows, n, pair ? 32 : 64, pair ? 9 : 1)) != DSA_OK) return s;
       if ((s = tmap_kv_tiles(&tv[k], rows, n, 64, 4)) != DSA_OK) return s;
     }

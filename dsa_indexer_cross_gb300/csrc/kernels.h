@@ -315,14 +315,14 @@ struct SharedRows {
   const int32_t* prefix;
   int n_groups, max_rows;
 };
-// The walks (kernel launches) of such a call: whether a walk takes CTA pairs, the box height of its tmap_q, and
-// (pairs) its ring in the scratch; a bf16 cache's maps are as for launch_latent_attn.
+// The walks (kernel launches) of such a call, those that it may have: whether a walk takes CTA pairs, the box height
+// of its tmap_q, and (rows > 0) the bf16 rows in the scratch that its maps cover for an fp8 cache: the pairs' ring, or
+// (walk 2, for an fp8 cache only) the staged prefixes.  Else the maps are as for launch_latent_attn.
 struct SharedWalks {
-  int n;
-  bool pair[2];
-  int q_rows[2];
-  size_t ring_offset[2];
-  int ring_rows[2];
+  bool used[3], pair[3];
+  int q_rows[3];
+  size_t rows_offset[3];
+  int rows[3];
 };
 SharedWalks latent_shared_walks(int n_q, int n_heads, int n_groups, int max_rows);
 size_t latent_shared_ws_bytes(int n_q, int n_heads, int n_groups, int max_rows);

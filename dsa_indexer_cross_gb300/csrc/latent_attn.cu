@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       Seg as;
       int ai = 0, len = 0;
       bool alive = aw.next(as);
-      if (alive) len = row_len(a.pg, as.row);
+      if (alive) len = seg_len<MODE>(a, as);
       int j = -1, jlen = 0, page = -1;         // the next tile's key of this lane, and its page
       const auto find_page = [&]() {
         j = -1;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         if (++ai == as.n) {
           ai = 0;
           alive = aw.next(as);
-          if (alive) len = row_len(a.pg, as.row);
+          if (alive) len = seg_len<MODE>(a, as);
         }
       };
       const uint8_t* next = nullptr;           // this lane's codes of the tile that is asked for
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       Seg as;
       int ai = 0;
       bool alive = aw.next(as);
-      int len0 = alive ? row_len(a.pg, as.row) : 0;
+      int len0 = alive ? seg_len<MODE>(a, as) : 0;
       int j1 = -1, row1 = 0, len1 = 0;       // offset of row lane & 15 known
       int j2 = -1, page2 = -1;               // page known
       bool past2 = false;
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
         if (alive && ++ai == as.n) {
           ai = 0;
           alive = aw.next(as);
-          if (alive) len0 = row_len(a.pg, as.row);
+          if (alive) len0 = seg_len<MODE>(a, as);
         }
       };
       int j0 = -1, row0 = 0, lenx = 0;       // the offset after that, found while w holds nothing
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
     uint32_t g = 0;
     bool ok = true;
     while (ok && walk.next(sg)) {
-      const int len = row_len(a.pg, sg.row);
+      const int len = seg_len<MODE>(a, sg);
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
       // log-sum-exps in log2, and the columns that count: not those past the last head (other rows' q, whose
       // scores of an infinite key would make it NaN) nor heads without any key
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < 2 * NR; ++c) lp[c] = lu[c] = 0.f;
       named_bar_sync(1, kSoft);
-      const int len = row_len(a.pg, sg.row);
+      const int len = seg_len<MODE>(a, sg);
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
       for (int n = 0; n < sg.n; ++n, ++g) {
         const int i = sg.i0 + n;
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
     const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
     while (ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
-        const int len = row_len(a.pg, sg.row);
+        const int len = seg_len<MODE>(a, sg);
         const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
         // the segment's HB rows of q, once the previous ones have been read
         if (it > 0 && !(ok = wait(&sh.q_empty, (it - 1) & 1))) break;

@@ -183,6 +183,12 @@ struct Walk {
     return true;
   }
 };
+// Keys of the row that a segment belongs to.  (A prefix's item has whole tiles, and no length of its own.)
+template <int MODE>
+__device__ __forceinline__ int seg_len(const LArgs& a, const Seg& s) {
+  if (MODE == kItems && !(s.ncol & kItemOwn)) return 0x7FFFFFFF;
+  return row_len(a.pg, s.row);
+}
 // Where a segment's unnormalised columns go: the first's row of O, and (column c) its three numbers.
 template <int MODE>
 struct Partial {

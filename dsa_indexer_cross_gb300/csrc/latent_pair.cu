@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     bool ok = true;
     while (ok && walk.next(sg)) {
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
-      const int len = row_len(a.pg, sg.row);
+      const int len = seg_len<MODE>(a, sg);
       int ahead = FP8 ? 0 : gload(bt + (sg.i0 >> 1));
       for (int n = 0; n < sg.n && ok; ++n, ++g) {
         const int i = sg.i0 + n, page = ahead, sb = g & 1;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     auto find_offset = [&]() {
       j = -1;
       if (!alive) return;
-      len = row_len(a.pg, as.row);
+      len = seg_len<MODE>(a, as);
       const int s = (as.i0 + ai) * kRows + static_cast<int>(32 * rank + my_row);
       j = !SEL ? s : s < a.topk ? gload(a.idx + static_cast<size_t>(as.row) * a.topk + s) : -1;
     };
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     uint32_t g = 0;
     bool stop = false;
     while (!stop && walk.next(sg)) {
-      const int len = row_len(a.pg, sg.row);
+      const int len = seg_len<MODE>(a, sg);
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
       const int32_t* irow = SEL ? a.idx + static_cast<size_t>(sg.row) * a.topk : nullptr;
       float m_used = -INFINITY, lp = 0.f, lu = 0.f;

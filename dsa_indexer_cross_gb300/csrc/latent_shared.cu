@@ -16,6 +16,10 @@
 // prefixes, the single-CTA one for the rows' own keys, which are bound by bytes; where these are few, the pair
 // kernel takes them too and the second launch finds nothing.
 //
+// Staging (fp8).  A walk converts a prefix's codes once for each block of 128 columns.  Where there are many
+// blocks, the prefixes are first brought to bf16 once, in pages of the workspace that stay mostly in L2, and the
+// pair kernel takes them from there as from a bf16 cache, in a walk of its own.
+//
 // The line counts an item as a few tiles more than it has, for what it costs by itself (32 rows of 64 heads
 // behind 100K keys, fp8, one walk: the pairs at the line's end had sixteen short items each; 599 -> 525 us).
 //
@@ -23,7 +27,7 @@
 // cut: latent_shared_join_kernel puts them together with one softmax.  A row that is the only thing its columns
 // come from is written by the walk itself.
 //
-// A group is walked by rows, not shared, where that takes no more items: from 128 heads on.
+// A group is walked by rows, not shared, where that takes no more items (from 128 heads on) and nothing is staged.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -45,6 +49,10 @@ constexpr int kItemCost = 3;
 // 215 and 124, 135, 153, 210.
 constexpr int kMostOwnBf16 = 5000, kMostOwnFp8 = 1500;
 
+// Staging: prefixes of up to this many pages in all (151 MB), walked by this many blocks of columns each and more, on
+// average.  A tile costs some 0.02 us to stage, its walks 0.005 us more each where they convert.
+constexpr int kStagePages = 1024, kStageBlocks = 6, kStageTiles = 64;
+
 struct PlanArgs {
   const int32_t* start;      // [n_groups + 1]
   const int32_t* prefix;     // [n_groups]
@@ -56,14 +64,17 @@ struct PlanArgs {
   int32_t* table;            // [n_groups]: the row whose table names their pages
   int32_t* base;             // [n_groups]: first item, and the line before it
   long long* base_at;
-  int32_t* nt[2];
-  int4* items[2];
-  int4* rows;                // [n_q]: first prefix item (-1), its first column, own item (-1) and its walk
-  long long* at[2];          // the line before each item
-  int4* shares[2];           // [n_grp]
-  int n_grp[2];
-  bool pair[2];
+  int32_t* nt[3];            // by list: 0 prefixes (and own items), 1 own items, 2 staged prefixes
+  int4* items[3];
+  int4* rows;                // [n_q]: first prefix item (-1), its first column, own item (-1), and the lists: of the
+                             // own item + 4 that of the prefix item
+  long long* at[3];          // the line before each item
+  int4* shares[3];           // [n_grp]
+  int n_grp[3];
+  bool pair[3];
   uint32_t* faults;          // [2]
+  int stage_pages;           // room for staged pages, 0: none
+  int32_t* stage_at;         // [n_groups + 1]: first staged page of each group, then their number
 };
 
 struct Count {
@@ -115,10 +126,14 @@ template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_constant__ PlanArgs p) {
   __shared__ Count warp_sum[32];
   __shared__ CtaFaults faults;
-  __shared__ int tallest[2];
+  __shared__ int tallest[3];
+  __shared__ unsigned long long stage_sum[3];      // pages, tiles, and tiles times blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_trigger();
-  if (tid == 0) faults.bits = faults.count = tallest[0] = tallest[1] = 0;
+  if (tid == 0) {
+    faults.bits = faults.count = tallest[0] = tallest[1] = tallest[2] = 0;
+    stage_sum[0] = stage_sum[1] = stage_sum[2] = 0;
+  }
   grid_wait();
   // groups that do not lie in order within the rows: none is shared
   bool bad = false;
@@ -145,13 +160,41 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     if (lane == 0) {
       const long long blocks = (static_cast<long long>(n) * p.H + p.cols - 1) / p.cols;
       int tiles = min(max(want, 0), max(most, 0)) / kRows;
-      if (n < 2 || tiles < kMinShared || blocks >= n) tiles = 0;
+      if (n < 2 || tiles < kMinShared || blocks > n) tiles = 0;
       if (want < 0) report(faults, DEV_ERR_RANGE);
-      p.tiles[g] = tiles;
+      const bool only_staged = blocks >= n;
+      if (only_staged && (p.stage_pages == 0 || blocks < kStageBlocks)) tiles = 0;
+      if (tiles > 0 && p.stage_pages > 0) {
+        atomicAdd(&stage_sum[0], static_cast<unsigned long long>((tiles + 1) >> 1));
+        atomicAdd(&stage_sum[1], static_cast<unsigned long long>(tiles));
+        atomicAdd(&stage_sum[2], static_cast<unsigned long long>(tiles * blocks));
+      }
+      p.tiles[g] = only_staged ? -tiles : tiles;
       p.table[g] = at;
     }
   }
   __syncthreads();
+  const bool staged = p.stage_pages > 0 && stage_sum[0] <= static_cast<unsigned long long>(p.stage_pages) &&
+                      stage_sum[1] >= kStageTiles && stage_sum[2] >= kStageBlocks * stage_sum[1];
+  if (p.stage_pages > 0) {
+    // the tiles that are shared after all, and their pages
+    int pages = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+      const int g = g0 + tid;
+      int tiles = g < n_groups ? p.tiles[g] : 0;
+      tiles = staged ? abs(tiles) : max(tiles, 0);
+      Count total;
+      const Count before = block_excl<kPlanThreads>(Count{staged ? (tiles + 1) >> 1 : 0, 0}, warp_sum, total);
+      if (g < n_groups) {
+        p.tiles[g] = tiles;
+        p.stage_at[g] = pages + before.items;
+      }
+      pages += total.items;
+    }
+    if (tid == 0) p.stage_at[p.n_groups] = pages;
+    __syncthreads();
+  }
+  const int pre_list = staged ? 2 : 0;
   // prefix items
   Count pre{0, 0};
   int most_tiles = 0;
@@ -177,9 +220,9 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   for (int i = tid; i < pre.items; i += kPlanThreads) {
     const int g = last_not_above(p.base, n_groups, i);       // (the last of equal ones: the one with items)
     const int s = gload(p.start + g), e = gload(p.start + g + 1), b = i - p.base[g];
-    p.items[0][i] = make_int4(s * p.H + b * p.cols, min(p.cols, (e - s) * p.H - b * p.cols), p.table[g], 0);
-    p.nt[0][i] = p.tiles[g];
-    p.at[0][i] = p.base_at[g] + static_cast<long long>(b) * (p.tiles[g] + kItemCost);
+    p.items[pre_list][i] = make_int4(s * p.H + b * p.cols, min(p.cols, (e - s) * p.H - b * p.cols), staged ? p.stage_at[g] : p.table[g], 0);
+    p.nt[pre_list][i] = p.tiles[g];
+    p.at[pre_list][i] = p.base_at[g] + static_cast<long long>(b) * (p.tiles[g] + kItemCost);
   }
   // the rows' own items
   const int first = n_groups > 0 ? gload(p.start) : 0, end = n_groups > 0 ? gload(p.start + n_groups) : 0;
@@ -198,7 +241,9 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     return (len + kRows - 1) / kRows - shared;
   };
   int list = 0;
-  if (p.two) {                 // in a walk of their own, where they are many
+  if (p.two && staged) {       // (their prefixes are not in list 0 either)
+    list = 1;
+  } else if (p.two) {          // in a walk of their own, where they are many
     Count mine{0, 0}, total;
     int shared;
     int4 info;
@@ -206,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     block_excl<kPlanThreads>(mine, warp_sum, total);
     list = total.line > p.most_own ? 1 : 0;
   }
-  Count own = list ? Count{0, 0} : pre;
+  Count own = list == pre_list ? pre : Count{0, 0};
   int most_own = 0;
   for (int t0 = 0; t0 < p.n_q; t0 += kPlanThreads) {
     const int t = t0 + tid;
@@ -215,7 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     if (t < p.n_q) {
       if (bad_length(p.pg, t)) report(faults, DEV_ERR_RANGE);
       tiles = own_tiles(t, shared, info);
-      info.w = list;
+      info.w = list + 4 * pre_list;
       most_own = max(most_own, tiles);
     }
     Count total;
@@ -236,13 +281,14 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   most_tiles = __reduce_max_sync(0xffffffffu, most_tiles);
   most_own = __reduce_max_sync(0xffffffffu, most_own);
   if (lane == 0) {
-    atomicMax(&tallest[0], most_tiles);
+    atomicMax(&tallest[pre_list], most_tiles);
     atomicMax(&tallest[list], most_own);
   }
   __syncthreads();
   // each group's share
-  for (int k = 0; k < (p.two ? 2 : 1); ++k) {
-    const Count c = k == list ? own : list ? pre : Count{0, 0};
+  for (int k = 0; k < 3; ++k) {
+    if (p.n_grp[k] == 0) continue;             // no such walk
+    const Count c = k == list ? own : k == pre_list ? pre : Count{0, 0};
     bool by_row;
     const int groups = share_groups<kItems>(p.n_grp[k], p.pair[k] ? 2 : 1, c.items, c.line, tallest[k] + kItemCost, by_row);
     // Where share g begins: an item, and the tiles before it in the item and in the list.  A cut that would leave a
@@ -285,11 +331,54 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   }
 }
 
+// The staged pages: codes of each group's shared tiles to bf16 rows, and the table that names them (-1: a page outside
+// the cache, which the walk reports).  A block takes a page, a warp sixteen rows, four at a time.
+__global__ void __launch_bounds__(256) latent_stage_kernel(const LatentCache c, const PagedRows pg, const int32_t* stage_at,
+                                                           const int32_t* table, int n_groups, uint16_t* rows,
+                                                           int32_t* stage_table) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_trigger();
+  grid_wait();
+  const int pages = gload(stage_at + n_groups);
+#pragma unroll 1
+  for (int p = blockIdx.x; p < pages; p += gridDim.x) {
+    const int g = last_not_above(stage_at, n_groups, p), k = p - gload(stage_at + g);
+    const int page = gload(pg.block_table + static_cast<size_t>(gload(table + g)) * pg.max_pages + k);
+    const bool in = static_cast<uint32_t>(page) < static_cast<uint32_t>(pg.n_pages);
+    if (threadIdx.x == 0) stage_table[p] = in ? p : -1;
+    if (!in) continue;
+#pragma unroll 1
+    for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += 4) {
+      const size_t row = (static_cast<size_t>(page) << kPageShift) + r0;
+      uint4 w[4];
+      uint32_t sc[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        w[u] = gload_once(c.latent + (row + u) * kDv + lane * 16);
+        sc[u] = gload(reinterpret_cast<const uint32_t*>(c.scale) + row + u);
+      }
+      const uint4 rope = gload_once(c.rope + (row + (lane >> 3)) * 64 + (lane & 7) * 8);
+      uint16_t* dst = rows + ((static_cast<size_t>(p) << kPageShift) + r0) * kDqk;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t m = fp8_mult((sc[u] >> (8 * (lane >> 3))) & 0xFFu);
+        uint32_t o[8];
+        fp8x4_to_bf16(w[u].x, m, o[0], o[1]);
+        fp8x4_to_bf16(w[u].y, m, o[2], o[3]);
+        fp8x4_to_bf16(w[u].z, m, o[4], o[5]);
+        fp8x4_to_bf16(w[u].w, m, o[6], o[7]);
+        stg256(dst + u * kDqk + lane * 16, o);
+      }
+      *reinterpret_cast<uint4*>(dst + (lane >> 3) * kDqk + kDv + (lane & 7) * 8) = rope;
+    }
+  }
+}
+
 struct JoinArgs {
-  LArgs walk[2];             // the walks of prefix items and of own items (one launch: the same)
+  LArgs walk[3];             // by list; n_cta 0: no such walk
   const int4* rows;
   const uint32_t* plan_faults;
-  int n_walks, cols;
+  int cols;
 };
 
 // The pieces of an item's column: one, whole, or the partials of groups b .. b + n - 1, of which the first is in the
@@ -337,7 +426,7 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
   if (blockIdx.x == gridDim.x - 1) {
     if (warp != 0) return;
     uint32_t bits = lane == 0 ? j.plan_faults[0] : 0, count = lane == 0 ? j.plan_faults[1] : 0;
-    for (int k = 0; k < j.n_walks; ++k)
+    for (int k = 0; k < 3; ++k)
       for (int i = lane; i < j.walk[k].n_cta; i += 32) {
         bits |= j.walk[k].err[2 * i];
         count += j.walk[k].err[2 * i + 1];
@@ -363,10 +452,10 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
     const int4 info = gload(j.rows + t);
     const int in_group = static_cast<int>(col - info.y);
     int2 pre_groups = make_int2(0, 0), own_groups = make_int2(0, 0);
-    if (info.x >= 0) pre_groups = gload(j.walk[0].pieces + info.x + in_group / j.cols);
-    const LArgs& own_walk = j.walk[info.w];
+    const LArgs &own_walk = j.walk[info.w & 3], &pre_walk = j.walk[info.w >> 2];
+    if (info.x >= 0) pre_groups = gload(pre_walk.pieces + info.x + in_group / j.cols);
     if (info.z >= 0) own_groups = gload(own_walk.pieces + info.z);
-    const Pieces pre = find_pieces(j.walk[0], pre_groups, in_group % j.cols, col);
+    const Pieces pre = find_pieces(pre_walk, pre_groups, in_group % j.cols, col);
     const Pieces own = find_pieces(own_walk, own_groups, h, all + col);
     done = pre.n == 0 && own.n == 1;           // written by the walk
     const int n = done ? 0 : pre.n + own.n;
@@ -454,56 +543,69 @@ __global__ void __launch_bounds__(256) latent_shared_join_kernel(const __grid_co
 }
 
 struct WalkLayout {
-  bool pair;
-  int cols, n_grp;
-  size_t off_err, off_shares, off_m, off_o, off_ring;
+  bool used, pair;
+  int cols, n_grp, n_items;
+  size_t off_nt, off_items, off_at, off_pieces, off_err, off_shares, off_m, off_o, off_ring;
 };
 struct Layout {
-  WalkLayout walk[2];
-  int n_walks, n_items[2];
-  size_t off_tiles, off_table, off_base, off_base_at, off_nt[2], off_items[2], off_at[2], off_pieces[2], off_rows, off_faults, off_whole_m, off_whole_o, total;
+  WalkLayout walk[3];        // by list
+  size_t off_tiles, off_table, off_base, off_base_at, off_rows, off_faults, off_whole_m, off_whole_o, off_stage_at, off_stage_table,
+      off_stage, total;
 };
 Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
   Layout L{};
   int sms = device_sm_count();
   if (sms <= 0) sms = 152;
   const long long group_cols = static_cast<long long>(std::max(1, std::min(max_rows, n_q))) * n_heads;
-  L.n_walks = group_cols > 64 && n_heads <= 64 ? 2 : 1;
-  L.walk[0].pair = group_cols > 64;
-  L.walk[0].cols = group_cols > 64 ? 128 : head_block(static_cast<int>(group_cols));
-  L.walk[1].pair = false;
+  const bool pair = group_cols > 64;
+  L.walk[0].used = true;
+  L.walk[0].pair = pair;
+  L.walk[0].cols = pair ? 128 : head_block(static_cast<int>(group_cols));
+  L.walk[1].used = pair && n_heads <= 64;
   L.walk[1].cols = head_block(std::min(n_heads, 64));
-  const long long all = static_cast<long long>(n_q) * n_heads;
-  const long long pre = all / L.walk[0].cols + n_groups;
-  L.n_items[0] = static_cast<int>(std::min<long long>(pre + n_q, 0x7FFFFFFF));
-  L.n_items[1] = L.n_walks == 2 ? n_q : 0;
+  L.walk[2].used = n_groups > 0 && group_cols > (kStageBlocks - 1) * 128;
+  L.walk[2].pair = true;
+  L.walk[2].cols = 128;
+  const long long all = static_cast<long long>(n_q) * n_heads, pre = all / L.walk[0].cols + n_groups;
+  const auto items = [](long long n) { return static_cast<int>(std::min<long long>(n, 0x7FFFFFFF)); };
+  L.walk[0].n_items = items(pre + n_q);
+  L.walk[1].n_items = n_q;
+  L.walk[2].n_items = items(pre);
   size_t o = 0;
-  const auto take = [&](size_t bytes) {
+  const auto take = [&](size_t n, size_t bytes) {
     const size_t at = o;
-    o += (bytes + 255) & ~size_t(255);
+    o += (n * bytes + 255) & ~size_t(255);
     return at;
   };
-  L.off_faults = take(2 * sizeof(uint32_t));
-  L.off_tiles = take(static_cast<size_t>(n_groups) * sizeof(int32_t));
-  L.off_table = take(static_cast<size_t>(n_groups) * sizeof(int32_t));
-  L.off_base = take(static_cast<size_t>(n_groups) * sizeof(int32_t));
-  L.off_base_at = take(static_cast<size_t>(n_groups) * sizeof(long long));
-  L.off_rows = take(static_cast<size_t>(n_q) * sizeof(int4));
-  for (int k = 0; k < L.n_walks; ++k) {
-    WalkLayout& w = L.walk[k];
+  const size_t groups = static_cast<size_t>(n_groups);
+  L.off_faults = take(2, sizeof(uint32_t));
+  L.off_tiles = take(groups, sizeof(int32_t));
+  L.off_table = take(groups, sizeof(int32_t));
+  L.off_base = take(groups, sizeof(int32_t));
+  L.off_base_at = take(groups, sizeof(long long));
+  L.off_rows = take(n_q, sizeof(int4));
+  for (WalkLayout& w : L.walk) {
+    if (!w.used) continue;
     w.n_grp = std::max(1, std::min(w.pair ? sms / 2 : sms, kMostGroups));
-    L.off_nt[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(int32_t));
-    L.off_items[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(int4));
-    L.off_pieces[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(int2));
-    L.off_at[k] = take(static_cast<size_t>(L.n_items[k]) * sizeof(long long));
-    w.off_err = take(static_cast<size_t>(w.n_grp) * 2 * 2 * sizeof(uint32_t));
-    w.off_shares = take(static_cast<size_t>(w.n_grp) * sizeof(int4));
-    w.off_m = take(static_cast<size_t>(w.n_grp) * 2 * w.cols * sizeof(float4));
-    w.off_o = take(static_cast<size_t>(w.n_grp) * 2 * w.cols * kDv * sizeof(float));
-    w.off_ring = w.pair ? take(static_cast<size_t>(w.n_grp) * kRing * kRows * kDqk * sizeof(uint16_t)) : 0;
+    const size_t n = static_cast<size_t>(w.n_items), slots = static_cast<size_t>(w.n_grp) * 2 * w.cols;
+    w.off_nt = take(n, sizeof(int32_t));
+    w.off_items = take(n, sizeof(int4));
+    w.off_pieces = take(n, sizeof(int2));
+    w.off_at = take(n, sizeof(long long));
+    w.off_err = take(static_cast<size_t>(w.n_grp) * 2, 2 * sizeof(uint32_t));
+    w.off_shares = take(w.n_grp, sizeof(int4));
+    w.off_m = take(slots, sizeof(float4));
+    w.off_o = take(slots, kDv * sizeof(float));
+    if (&w == &L.walk[2]) {
+      L.off_stage_at = take(groups + 1, sizeof(int32_t));
+      L.off_stage_table = take(kStagePages, sizeof(int32_t));
+      L.off_stage = take(static_cast<size_t>(kStagePages) * kPageRows * kDqk, sizeof(uint16_t));
+    } else if (w.pair) {
+      w.off_ring = take(static_cast<size_t>(w.n_grp) * kRing * kRows * kDqk, sizeof(uint16_t));
+    }
   }
-  L.off_whole_m = take(static_cast<size_t>(all) * 2 * sizeof(float4));
-  L.off_whole_o = take(static_cast<size_t>(all) * 2 * kDv * sizeof(float));
+  L.off_whole_m = take(static_cast<size_t>(all) * 2, sizeof(float4));
+  L.off_whole_o = take(static_cast<size_t>(all) * 2 * kDv, sizeof(float));
   L.total = o;
   return L;
 }
@@ -516,15 +618,21 @@ size_t latent_shared_ws_bytes(int n_q, int n_heads, int n_groups, int max_rows) 
 
 SharedWalks latent_shared_walks(int n_q, int n_heads, int n_groups, int max_rows) {
   const Layout L = shared_layout(n_q, n_heads, n_groups, max_rows);
-  SharedWalks w{};
-  w.n = L.n_walks;
-  for (int k = 0; k < L.n_walks; ++k) {
-    w.pair[k] = L.walk[k].pair;
-    w.q_rows[k] = L.walk[k].pair ? 64 : L.walk[k].cols;
-    w.ring_offset[k] = L.walk[k].off_ring;
-    w.ring_rows[k] = L.walk[k].pair ? L.walk[k].n_grp * kRing * kRows : 0;
+  SharedWalks s{};
+  for (int k = 0; k < 3; ++k) {
+    const WalkLayout& w = L.walk[k];
+    s.used[k] = w.used;
+    s.pair[k] = w.pair;
+    s.q_rows[k] = w.pair ? 64 : w.cols;
+    if (k == 2) {
+      s.rows_offset[k] = L.off_stage;
+      s.rows[k] = kStagePages * kPageRows;
+    } else if (w.pair) {
+      s.rows_offset[k] = w.off_ring;
+      s.rows[k] = w.n_grp * kRing * kRows;
+    }
   }
-  return w;
+  return s;
 }
 
 cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_kv, const CUtensorMap* tmap_v,
@@ -535,6 +643,7 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
   uint8_t* base = static_cast<uint8_t*>(scratch);
   const PipelineDebug dbg = pipeline_debug();
   const auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(base + at); };
+  const bool stage = c.fp8 && L.walk[2].used;
   PlanArgs p{};
   p.start = groups.start;
   p.prefix = groups.prefix;
@@ -543,38 +652,29 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
   p.n_q = n_q;
   p.H = n_heads;
   p.cols = L.walk[0].cols;
-  p.two = L.n_walks == 2;
+  p.two = L.walk[1].used;
   p.most_own = c.fp8 ? kMostOwnFp8 : kMostOwnBf16;
   p.tiles = i32(L.off_tiles);
   p.table = i32(L.off_table);
   p.base = i32(L.off_base);
-  p.rows = reinterpret_cast<int4*>(base + L.off_rows);
   p.base_at = reinterpret_cast<long long*>(base + L.off_base_at);
+  p.rows = reinterpret_cast<int4*>(base + L.off_rows);
   p.faults = reinterpret_cast<uint32_t*>(base + L.off_faults);
-  for (int k = 0; k < L.n_walks; ++k) {
-    p.nt[k] = i32(L.off_nt[k]);
-    p.items[k] = reinterpret_cast<int4*>(base + L.off_items[k]);
-    p.at[k] = reinterpret_cast<long long*>(base + L.off_at[k]);
-    p.shares[k] = reinterpret_cast<int4*>(base + L.walk[k].off_shares);
-    p.n_grp[k] = L.walk[k].n_grp;
-    p.pair[k] = L.walk[k].pair;
-  }
-  int ps = prof_begin(kProfAttnPrep, st);
-  // (fewer threads, fewer and cheaper barriers)
-  const int most = std::max(n_q, 8 * groups.n_groups);
-  cudaError_t e = most <= 64    ? launch_pdl(latent_plan_kernel<32>, dim3(1), 32, 0, st, 1, p)
-                  : most <= 512 ? launch_pdl(latent_plan_kernel<256>, dim3(1), 256, 0, st, 1, p)
-                                : launch_pdl(latent_plan_kernel<1024>, dim3(1), 1024, 0, st, 1, p);
-  prof_end(ps, st);
-  if (e != cudaSuccess) return e;
+  p.stage_pages = stage ? kStagePages : 0;
+  p.stage_at = i32(L.off_stage_at);
   JoinArgs j{};
   j.rows = p.rows;
   j.plan_faults = p.faults;
-  j.n_walks = L.n_walks;
   j.cols = p.cols;
-  ps = prof_begin(kProfAttn, st);
-  for (int k = 0; k < L.n_walks && e == cudaSuccess; ++k) {
+  for (int k = 0; k < 3; ++k) {
     const WalkLayout& w = L.walk[k];
+    if (!w.used || (k == 2 && !stage)) continue;
+    p.nt[k] = i32(w.off_nt);
+    p.items[k] = reinterpret_cast<int4*>(base + w.off_items);
+    p.at[k] = reinterpret_cast<long long*>(base + w.off_at);
+    p.shares[k] = reinterpret_cast<int4*>(base + w.off_shares);
+    p.n_grp[k] = w.n_grp;
+    p.pair[k] = w.pair;
     LArgs& a = j.walk[k];
     a.latent = c.latent;
     a.scale = c.scale;
@@ -584,7 +684,7 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
     a.shares = p.shares[k];
     a.whole_o = reinterpret_cast<float*>(base + L.off_whole_o);
     a.whole_m = reinterpret_cast<float4*>(base + L.off_whole_m);
-    a.pieces = reinterpret_cast<int2*>(base + L.off_pieces[k]);
+    a.pieces = reinterpret_cast<int2*>(base + w.off_pieces);
     a.pg = pg;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse;
@@ -602,8 +702,29 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
     a.status = status;
     a.wait_ns = dbg.wait_ns;
     a.stop_after = dbg.stop_after_tiles;
-    e = w.pair ? launch_latent_pair(c.fp8, kItems, tmap_kv[k], tmap_v[k], tmap_q[k], a, st)
-               : launch_latent_single(w.cols, c.fp8, kItems, tmap_kv[k], tmap_v[k], tmap_q[k], a, st);
+  }
+  // a staged prefix's "table row" is its first page: rows of one entry, one behind the other
+  if (stage) j.walk[2].pg = PagedRows{i32(L.off_stage_table), nullptr, 1, kStagePages};
+  int ps = prof_begin(kProfAttnPrep, st);
+  // (fewer threads, fewer and cheaper barriers)
+  const int most = std::max(n_q, 8 * groups.n_groups);
+  cudaError_t e = most <= 64    ? launch_pdl(latent_plan_kernel<32>, dim3(1), 32, 0, st, 1, p)
+                  : most <= 512 ? launch_pdl(latent_plan_kernel<256>, dim3(1), 256, 0, st, 1, p)
+                                : launch_pdl(latent_plan_kernel<1024>, dim3(1), 1024, 0, st, 1, p);
+  if (e == cudaSuccess && stage) {
+    int sms = device_sm_count();
+    if (sms <= 0) sms = 152;
+    e = launch_pdl(latent_stage_kernel, dim3(4 * sms), 256, 0, st, 1, c, pg, p.stage_at, p.table, p.n_groups,
+                   reinterpret_cast<uint16_t*>(base + L.off_stage), i32(L.off_stage_table));
+  }
+  prof_end(ps, st);
+  if (e != cudaSuccess) return e;
+  ps = prof_begin(kProfAttn, st);
+  for (int k = 2; k >= 0 && e == cudaSuccess; --k) {
+    const LArgs& a = j.walk[k];
+    if (a.n_cta == 0) continue;
+    e = L.walk[k].pair ? launch_latent_pair(c.fp8 && k != 2, kItems, tmap_kv[k], tmap_v[k], tmap_q[k], a, st)
+                       : launch_latent_single(L.walk[k].cols, c.fp8, kItems, tmap_kv[k], tmap_v[k], tmap_q[k], a, st);
   }
   if (e == cudaSuccess) {
     const long long all = static_cast<long long>(n_q) * n_heads;

@@ -539,15 +539,17 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
  * for all of their heads.  Rows [group_start[g], group_start[g + 1]) share their first prefix_len[g] keys:
  * their block_table rows name the same pages for these keys, as far as each row has them.  Other rows, and
  * rows shorter than the prefix (a padded batch's empty ones), attend by themselves; the walk takes
- * whole tiles of 64 keys of the prefix, the rows their rest.  Rows of 128 heads gain nothing.
+ * whole tiles of 64 keys of the prefix, the rows their rest.
  *   group_start int32 [n_groups + 1], ascending within [0, n_q] (else no group is shared and the call flags
  *   it; the results are the same); prefix_len int32 [n_groups] (negative: flagged, nothing shared; beyond
  *   the longest row: cut to it).  Device memory, n_groups = 0: may be NULL.  max_rows: rows of the largest
  *   group, or about (it chooses the kernels and the workspace; any value >= 1 gives right results).
- * ws: dsa_latent_attn_shared_workspace_size bytes: up to 85 MB, 4 KB for each row and head, some 50 bytes
- * for each row and group; the size depends on n_groups and max_rows too.  Everything else as
- * dsa_latent_attn_paged.  Errors: those of dsa_latent_attn_paged, DSA_ERR_ARG (the groups), DSA_ERR_SHAPE (n_groups
- * beyond 2^24). */
+ * An fp8 cache's prefixes that many columns share are brought to bf16 in the workspace first (up to 1024 pages of
+ * them, else none).
+ * ws: dsa_latent_attn_shared_workspace_size bytes: 4 KB for each row and head, some 100 bytes for each row and group,
+ * and up to 40 MB where a group's rows and heads are up to 64, 130 MB up to 640 of them, 320 MB beyond.  The size
+ * depends on n_groups and max_rows too.  Everything else as dsa_latent_attn_paged.
+ * Errors: those of dsa_latent_attn_paged, DSA_ERR_ARG (the groups), DSA_ERR_SHAPE (n_groups beyond 2^24). */
 typedef struct dsa_shared_rows {
   const int32_t* group_start;
   const int32_t* prefix_len;

@@ -47,7 +47,7 @@ def test_the_hint_only_chooses_kernels(H, max_rows):
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
 @pytest.mark.parametrize("rows,H,prefix", [(4, 16, 5000), (48, 16, 8000), (2, 1, 700), (8, 64, 20000), (16, 100, 6000),
-                                           (3, 128, 3000), (70, 3, 12345), (130, 8, 1000), (2, 16, 129)])
+                                           (3, 128, 3000), (9, 128, 5000), (70, 3, 12345), (130, 8, 1000), (2, 16, 129)])
 def test_one_group(rows, H, prefix, fmt):
     rng = np.random.default_rng(rows)
     lens = (prefix + rng.integers(0, 700, rows)).tolist()
@@ -183,6 +183,56 @@ def test_two_streams_graphs_and_a_shared_workspace():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     kv = [sp.stored(t)[:300] if t == 2 else sp.stored(t) for t in range(6)]
     check_rows(a[0], a[1], q, kv)
+
+
+def _staged_groups():
+    """Enough columns and tiles that an fp8 cache's prefixes are brought to bf16 first: several groups, odd numbers of
+    tiles and of pages, rows shorter than their prefix, a group and rows that share nothing."""
+    rng = np.random.default_rng(3)
+    lens = lambda p, n: (p + rng.integers(0, 300, n)).tolist()  # noqa: E731
+    return [(0, [100, 0], False), (2100, lens(2100, 9), False), (4000, lens(4000, 12) + [0, 50, 3900], False),
+            (1, [300], False), (1290, [1291 + i for i in range(8)], True), (60, lens(60, 3), False)]
+
+
+@pytest.mark.parametrize("H", [64, 100, 128])
+def test_staged_prefixes(H):
+    groups = _staged_groups()
+    n = sum(len(g[1]) for g in groups)
+    sp, q, out, lse = _check(groups, H, "fp8", seed=H, check=set(range(0, n, 4)) | {12, 23, 24, 25})
+    again, l2, _ = sp.attend(q)
+    assert torch.equal(out, again) and torch.equal(lse, l2)
+    # a page outside the cache: its keys are left out of the rows that walk it
+    rows = list(range(2, 11))
+    keep = sp.bt_d.clone()
+    sp.bt_d[rows, 3] = -1
+    o3, l3, ws = sp.attend(q)
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 2
+    kv = [None] * n
+    for t in (2, 7, 12):
+        w = sp.stored(t)
+        kv[t] = np.concatenate([w[:3 * P], w[4 * P:]]) if t in rows else w
+    check_rows(o3, l3, q, kv)
+    sp.bt_d.copy_(keep)
+    # captured, with other lengths in place: now too short to be shared by most
+    ws = torch.empty_like(ws)
+    g = torch.cuda.CUDAGraph()
+    sp.attend(q, ws=ws)
+    with torch.cuda.graph(g):
+        o4, l4, _ = sp.attend(q, ws=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o4, out) and torch.equal(l4, lse)
+    sp.len_d.clamp_(max=700)
+    g.replay()
+    torch.cuda.synchronize()
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(o4, l4, q, [sp.stored(t)[:700] if t in (0, 2, 12, 25, 30) else None for t in range(n)])
+
+
+def test_prefixes_of_more_pages_than_are_staged():
+    """1100 pages in two groups: they are walked from the cache."""
+    groups = [(70000, [70000 + 10 * i for i in range(14)], True), (70700, [70700 + 5 * i for i in range(13)], True)]
+    _check(groups, 64, "fp8", seed=2, check={0, 26})
 
 
 def test_without_lse_and_empty_calls():
