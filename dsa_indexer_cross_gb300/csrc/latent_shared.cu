@@ -98,10 +98,6 @@ __device__ __forceinline__ Count block_excl(Count x, Count* warp_sum, Count& tot
     return c;
   };
   const Count mine = incl(x);
-  if constexpr (kPlanThreads == 32) {
-    total = Count{__shfl_sync(0xffffffffu, mine.items, 31), __shfl_sync(0xffffffffu, mine.line, 31)};
-    return Count{mine.items - x.items, mine.line - x.line};
-  }
   __syncthreads();
   if (lane == 31) warp_sum[warp] = mine;
   __syncthreads();
@@ -144,22 +140,34 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) report(faults, DEV_ERR_RANGE);
   const int n_groups = bad ? 0 : p.n_groups;
-  // a warp a group: its longest row
-  for (int g = warp; g < n_groups; g += kPlanThreads / 32) {
-    const int s = gload(p.start + g), n = gload(p.start + g + 1) - s, want = gload(p.prefix + g);
-    int longest = -1, at = 0;
-    for (int r = lane; r < n; r += 32) {
-      const int len = row_len(p.pg, s + r);
-      if (len > longest) {
-        longest = len;
-        at = s + r;
+  // A group's longest row: a warp a group, or eight lanes where there are more groups than warps.
+  const int lanes = n_groups > kPlanThreads / 32 ? 8 : 32, sub = lane & (lanes - 1);
+  for (int g0 = warp * (32 / lanes); g0 < n_groups; g0 += kPlanThreads / lanes) {
+    const int g = g0 + lane / lanes;
+    int n = 0, want = 0, longest = -1, at = 0x7FFFFFFF;
+    if (g < n_groups) {
+      const int s = gload(p.start + g);
+      n = gload(p.start + g + 1) - s;
+      want = gload(p.prefix + g);
+      for (int r = sub; r < n; r += lanes) {
+        const int len = row_len(p.pg, s + r);
+        if (len > longest) {
+          longest = len;
+          at = s + r;
+        }
       }
     }
-    const int most = __reduce_max_sync(0xffffffffu, longest);
-    at = __reduce_min_sync(0xffffffffu, longest == most ? at : 0x7FFFFFFF);
-    if (lane == 0) {
+    __syncwarp();
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      const int l = __shfl_xor_sync(0xffffffffu, longest, o), r = __shfl_xor_sync(0xffffffffu, at, o);
+      if (l > longest || (l == longest && r < at)) {
+        longest = l;
+        at = r;
+      }
+    }
+    if (sub == 0 && g < n_groups) {
       const long long blocks = (static_cast<long long>(n) * p.H + p.cols - 1) / p.cols;
-      int tiles = min(max(want, 0), max(most, 0)) / kRows;
+      int tiles = min(max(want, 0), max(longest, 0)) / kRows;
       if (n < 2 || tiles < kMinShared || blocks > n) tiles = 0;
       if (want < 0) report(faults, DEV_ERR_RANGE);
       const bool only_staged = blocks >= n;
@@ -706,11 +714,12 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
   // a staged prefix's "table row" is its first page: rows of one entry, one behind the other
   if (stage) j.walk[2].pg = PagedRows{i32(L.off_stage_table), nullptr, 1, kStagePages};
   int ps = prof_begin(kProfAttnPrep, st);
-  // (fewer threads, fewer and cheaper barriers)
-  const int most = std::max(n_q, 8 * groups.n_groups);
-  cudaError_t e = most <= 64    ? launch_pdl(latent_plan_kernel<32>, dim3(1), 32, 0, st, 1, p)
-                  : most <= 512 ? launch_pdl(latent_plan_kernel<256>, dim3(1), 256, 0, st, 1, p)
-                                : launch_pdl(latent_plan_kernel<1024>, dim3(1), 1024, 0, st, 1, p);
+  // (fewer threads, cheaper barriers: 4 rows 19.2 us with 128, 20.8 with 1024; 200 rows in 40 groups 31.2 with 512, 35.7
+  // with 128; 900 in 300 93 with 1024, 99 with 512)
+  const int most = std::max(n_q, 16 * groups.n_groups);
+  cudaError_t e = most <= 128    ? launch_pdl(latent_plan_kernel<128>, dim3(1), 128, 0, st, 1, p)
+                  : most <= 1024 ? launch_pdl(latent_plan_kernel<512>, dim3(1), 512, 0, st, 1, p)
+                                 : launch_pdl(latent_plan_kernel<1024>, dim3(1), 1024, 0, st, 1, p);
   if (e == cudaSuccess && stage) {
     int sms = device_sm_count();
     if (sms <= 0) sms = 152;
