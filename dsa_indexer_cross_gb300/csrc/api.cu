@@ -972,6 +972,29 @@ dsa_attn_desc latent_desc(const dsa_attn_desc* d, bool selected) {
   if (!selected && c.topk < 1) c.topk = 1;
   return c;
 }
+// Latent attention over every key, or over selected keys of an fp8 cache: arguments checked, the workspace is large
+// enough.  named: groups of rows of a call that shares nothing.
+dsa_status run_latent(const dsa_attn_desc& d, const void* q, const LatentCache& c, const int32_t* idx, const PagedRows& pg,
+                      void* out, float* lse, void* ws, cudaStream_t st, const SharedRows* named) {
+  dsa_status s;
+  CUtensorMap tkv, tv, tq;
+  std::memset(&tkv, 0, sizeof(tkv));
+  std::memset(&tv, 0, sizeof(tv));
+  const LatentRing ring = latent_attn_ring(d.n_q, d.n_heads, pg, idx != nullptr, d.topk);
+  const bool pair = ring.rows > 0;
+  if (!c.fp8 || pair) {
+    const void* rows = c.fp8 ? static_cast<const uint8_t*>(ws) + kAlign + ring.offset : c.latent;
+    const uint64_t n = static_cast<uint64_t>(c.fp8 ? ring.rows : c.n_rows);
+    if ((s = tmap_kv_tiles(&tkv, rows, n, pair ? 32 : 64, pair ? 9 : 1)) != DSA_OK) return s;
+    if ((s = tmap_kv_tiles(&tv, rows, n, 64, 4)) != DSA_OK) return s;
+  }
+  if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
+                     static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)
+    return s;
+  const cudaError_t e = launch_latent_attn(c, tkv, tv, tq, pg, idx, d.n_q, d.n_heads, d.topk, d.softmax_scale, out, lse,
+                         static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st, named);
+  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "latent attention kernel");
+}
 }  // namespace
 
 dsa_status dsa_latent_attn_workspace_size(const dsa_attn_desc* desc, size_t* bytes) {
@@ -1011,23 +1034,7 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
   if ((s = check_device()) != DSA_OK) return s;
   const size_t need = kAlign + align_up(latent_attn_ws_bytes(d.n_q, d.n_heads));
   if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "attention workspace too small: %zu < %zu bytes", ws_bytes, need);
-  CUtensorMap tkv, tv, tq;
-  std::memset(&tkv, 0, sizeof(tkv));
-  std::memset(&tv, 0, sizeof(tv));
-  const LatentRing ring = latent_attn_ring(d.n_q, d.n_heads, pg, idx != nullptr, d.topk);
-  const bool pair = ring.rows > 0;
-  if (!c.fp8 || pair) {
-    const void* rows = c.fp8 ? static_cast<const uint8_t*>(ws) + kAlign + ring.offset : c.latent;
-    const uint64_t n = static_cast<uint64_t>(c.fp8 ? ring.rows : c.n_rows);
-    if ((s = tmap_kv_tiles(&tkv, rows, n, pair ? 32 : 64, pair ? 9 : 1)) != DSA_OK) return s;
-    if ((s = tmap_kv_tiles(&tv, rows, n, 64, 4)) != DSA_OK) return s;
-  }
-  if ((s = tmap_bf16(&tq, q, 576, static_cast<uint64_t>(d.n_q) * d.n_heads,
-                     static_cast<uint32_t>(latent_attn_q_box_rows(d.n_heads)))) != DSA_OK)
-    return s;
-  const cudaError_t e = launch_latent_attn(c, tkv, tv, tq, pg, idx, d.n_q, d.n_heads, d.topk, d.softmax_scale, out, lse,
-                         static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st);
-  return e == cudaSuccess ? DSA_OK : cuda_fail(e, "latent attention kernel");
+  return run_latent(d, q, c, idx, pg, out, lse, ws, st, nullptr);
 }
 
 namespace {
@@ -1055,6 +1062,14 @@ dsa_status check_groups(const dsa_shared_rows* g) {
 }
 }  // namespace
 
+namespace {
+// Enough for the call whether it shares or not.
+size_t latent_shared_need(const dsa_attn_desc* d, const dsa_shared_rows* g) {
+  return kAlign + align_up(std::max(latent_shared_ws_bytes(d->n_q, d->n_heads, g->n_groups, g->max_rows),
+                                    latent_attn_ws_bytes(d->n_q, d->n_heads)));
+}
+}  // namespace
+
 dsa_status dsa_latent_attn_shared_workspace_size(const dsa_attn_desc* desc, const dsa_shared_rows* groups, size_t* bytes) {
   if (!desc) return fail(DSA_ERR_ARG, "attention descriptor is NULL");
   if (!bytes) return fail(DSA_ERR_ARG, "bytes is NULL");
@@ -1063,7 +1078,7 @@ dsa_status dsa_latent_attn_shared_workspace_size(const dsa_attn_desc* desc, cons
   if (s != DSA_OK || (s = check_groups(groups)) != DSA_OK) return s;
   if (static_cast<long long>(d.n_q) * d.n_heads > 0x7FFFFFFFLL)
     return fail(DSA_ERR_SHAPE, "n_q * n_heads exceeds the int32 range");
-  *bytes = kAlign + align_up(latent_shared_ws_bytes(d.n_q, d.n_heads, groups->n_groups, groups->max_rows));
+  *bytes = latent_shared_need(&d, groups);
   return DSA_OK;
 }
 
@@ -1082,8 +1097,11 @@ dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, cons
   if (!aligned16(q) || !aligned16(out)) return fail(DSA_ERR_ARG, "q and out must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(DSA_ERR_ARG, "workspace must be 256-byte aligned");
   if ((s = check_device()) != DSA_OK) return s;
-  const size_t need = kAlign + align_up(latent_shared_ws_bytes(d.n_q, d.n_heads, groups->n_groups, groups->max_rows));
+  const size_t need = latent_shared_need(&d, groups);
   if (ws_bytes < need) return fail(DSA_ERR_WORKSPACE, "shared attention workspace too small: %zu < %zu bytes", ws_bytes, need);
+  const SharedRows rows{groups->group_start, groups->prefix_len, groups->n_groups, groups->max_rows};
+  if (latent_shared_alone(c.fp8, d.n_q, d.n_heads, pg, rows))
+    return run_latent(d, q, c, nullptr, pg, out, lse, ws, st, groups->n_groups > 0 ? &rows : nullptr);
   const SharedWalks walks = latent_shared_walks(d.n_q, d.n_heads, groups->n_groups, groups->max_rows);
   CUtensorMap tkv[3], tv[3], tq[3];
   std::memset(tkv, 0, sizeof(tkv));
@@ -1102,7 +1120,6 @@ dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, cons
         DSA_OK)
       return s;
   }
-  const SharedRows rows{groups->group_start, groups->prefix_len, groups->n_groups, groups->max_rows};
   const cudaError_t e = launch_latent_shared(c, tkv, tv, tq, pg, rows, d.n_q, d.n_heads, d.softmax_scale, out, lse,
                                              static_cast<uint32_t*>(ws), static_cast<uint8_t*>(ws) + kAlign, st);
   return e == cudaSuccess ? DSA_OK : cuda_fail(e, "shared-prefix attention kernel");

@@ -221,6 +221,14 @@ cudaError_t launch_sparse_attn_bwd_dense(int hd, const CUtensorMap& tmap_kv, con
                                          const void* dout, float* dq, float* dkv, uint32_t* status, float* delta,
                                          void* scratch, cudaStream_t st);
 
+// Rows that share prefixes: group g's are [start[g], start[g + 1]), their common keys [0, prefix[g]); max_rows: a
+// group's rows, at most or thereabouts (it chooses the kernels).
+struct SharedRows {
+  const int32_t* start;
+  const int32_t* prefix;
+  int n_groups, max_rows;
+};
+
 // ---------------------------------------------------------------------------- latent cache
 // A launch whose blocks may be scheduled while the previous kernel on the stream ends (as soon as all of
 // its blocks have called grid_trigger or left); every block calls grid_wait before it touches global
@@ -294,10 +302,13 @@ struct LatentRing {
 };
 LatentRing latent_attn_ring(int n_q, int n_heads, const PagedRows& pg, bool selected, int topk);
 int latent_attn_q_box_rows(int n_heads);
+// Whether the call over every key takes more than one CTA, and so a join.
+bool latent_attn_joins(int n_q, int n_heads, const PagedRows& pg);
 size_t latent_attn_ws_bytes(int n_q, int n_heads);
 cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
                                const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads,
-                               int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st);
+                               int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st,
+                               const SharedRows* named = nullptr);
 
 // w_out[t][j] = w_in[t][j] (nullptr: 0) + sum over heads of exp(scale q . kv_j - lse) of every key of row t, rows of
 // both w_stride apart.  The maps are as for launch_latent_attn with at most 64 heads (tmap_q: boxes of
@@ -308,13 +319,6 @@ cudaError_t launch_key_weights(const LatentCache& c, const CUtensorMap& tmap_kv,
                                const float* lse, const float* w_in, float* w_out, long long w_stride, uint32_t* status,
                                cudaStream_t st);
 
-// Rows that share prefixes: group g's are [start[g], start[g + 1]), their common keys [0, prefix[g]); max_rows: a
-// group's rows, at most or thereabouts (it chooses the kernels).
-struct SharedRows {
-  const int32_t* start;
-  const int32_t* prefix;
-  int n_groups, max_rows;
-};
 // The walks (kernel launches) of such a call, those that it may have: whether a walk takes CTA pairs, the box height
 // of its tmap_q, and (rows > 0) the bf16 rows in the scratch that its maps cover for an fp8 cache: the pairs' ring, or
 // (walk 2, for an fp8 cache only) the staged prefixes.  Else the maps are as for launch_latent_attn.
@@ -325,6 +329,9 @@ struct SharedWalks {
   int rows[3];
 };
 SharedWalks latent_shared_walks(int n_q, int n_heads, int n_groups, int max_rows);
+// Whether a call is better off, or no worse, without sharing: then launch_latent_attn takes it (named: the groups, for
+// their checks).
+bool latent_shared_alone(bool fp8, int n_q, int n_heads, const PagedRows& pg, const SharedRows& groups);
 size_t latent_shared_ws_bytes(int n_q, int n_heads, int n_groups, int max_rows);
 cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_kv, const CUtensorMap* tmap_v,
                                  const CUtensorMap* tmap_q, const PagedRows& pg, const SharedRows& groups, int n_q,

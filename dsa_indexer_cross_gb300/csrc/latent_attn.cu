@@ -933,6 +933,12 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const __grid_constant_
       bits |= a.err[2 * i];
       count += a.err[2 * i + 1];
     }
+    if (a.group_start)
+      for (int g = lane; g <= a.n_groups; g += 32) {
+        const uint32_t e = group_errors(a.group_start, a.prefix_len, a.n_groups, a.n_q, g);
+        bits |= e;
+        count += e ? 1u : 0u;
+      }
     bits = __reduce_or_sync(0xffffffffu, bits);
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) {
@@ -1165,6 +1171,11 @@ cudaError_t launch_key_weights(const LatentCache& c, const CUtensorMap& tmap_kv,
   return launch_latent_single(head_block(n_heads), c.fp8, kWeights, tmap_kv, tmap_v, tmap_q, a, st);
 }
 
+bool latent_attn_joins(int n_q, int n_heads, const PagedRows& pg) {
+  const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, false, 0));
+  return L.n_grp * L.n_hb > 1;
+}
+
 size_t latent_attn_ws_bytes(int n_q, int n_heads) {
   // the most groups any block table can ask for
   return latent_layout(n_q, n_heads, 1LL << 24).total;
@@ -1172,7 +1183,8 @@ size_t latent_attn_ws_bytes(int n_q, int n_heads) {
 
 cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv, const CUtensorMap& tmap_v,
                                const CUtensorMap& tmap_q, const PagedRows& pg, const int32_t* idx, int n_q, int n_heads,
-                               int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st) {
+                               int topk, float scale, void* out, float* lse, uint32_t* status, void* scratch, cudaStream_t st,
+                               const SharedRows* named) {
   const bool sel = idx != nullptr;
   const Layout L = latent_layout(n_q, n_heads, row_tiles_max(pg, sel, topk));
   uint8_t* base = static_cast<uint8_t*>(scratch);
@@ -1201,6 +1213,11 @@ cudaError_t launch_latent_attn(const LatentCache& c, const CUtensorMap& tmap_kv,
   a.status = status;
   a.wait_ns = dbg.wait_ns;
   a.stop_after = dbg.stop_after_tiles;
+  if (named) {
+    a.group_start = named->start;
+    a.prefix_len = named->prefix;
+    a.n_groups = named->n_groups;
+  }
   cudaError_t e;
   if (sel) {
     const int ps = prof_begin(kProfAttnPrep, st);

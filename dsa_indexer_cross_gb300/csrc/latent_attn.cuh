@@ -115,6 +115,9 @@ struct LArgs {
   const float* w_in;           // [n_q] rows w_stride apart; nullptr: zeros
   float* w_out;
   long long w_stride;
+  const int32_t* group_start;  // groups of rows that the call names without sharing anything (latent_shared.cu):
+  const int32_t* prefix_len;   // the join checks them; nullptr: none
+  int n_groups;
   uint32_t* status;
   uint32_t* err;               // [CTAs][2]: error bits, bad-index count
   int n_cta;
@@ -236,6 +239,13 @@ __device__ __forceinline__ bool writes_out(const Seg& s) {
 template <int MODE>
 __device__ __forceinline__ int columns(const Seg& s) {
   return MODE == kItems ? s.ncol & 0xFFFF : s.ncol;
+}
+
+// Error bits of entry g of n_groups groups of rows, g <= n_groups: starts ascending within [0, n_q], no prefix below 0.
+__device__ __forceinline__ uint32_t group_errors(const int32_t* start, const int32_t* prefix, int n_groups, int n_q, int g) {
+  const int s = gload(start + g);
+  const bool order = s < 0 || s > n_q || (g < n_groups && gload(start + g + 1) < s);
+  return order || (g < n_groups && gload(prefix + g) < 0) ? DEV_ERR_RANGE : 0u;
 }
 
 // Faults are collected per CTA; the CTAs' words are put together by the join kernel (or, when

@@ -49,6 +49,11 @@ constexpr int kItemCost = 3;
 // 215 and 124, 135, 153, 210.
 constexpr int kMostOwnBf16 = 5000, kMostOwnFp8 = 1500;
 
+// Calls of up to this many tiles, as the table's width allows, share nothing: listing the items and joining them costs
+// more.  Drafts of one sequence, 16 heads, bf16, rows x keys: 4 x 5000 (320 tiles) 19.7 us shared, 14.4 alone; 8 x 8000
+// (1008) 25.5 and 18.1; 16 x 8000 (2016) 26.0 and 25.5; 48 x 8000 and more (7000) 40 and 59.
+constexpr int kAloneTiles = 2000;
+
 // Staging: prefixes of up to this many pages in all (151 MB), walked by this many blocks of columns each and more, on
 // average.  A tile costs some 0.02 us to stage, its walks 0.005 us more each where they convert.
 constexpr int kStagePages = 1024, kStageBlocks = 6, kStageTiles = 64;
@@ -131,14 +136,14 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     stage_sum[0] = stage_sum[1] = stage_sum[2] = 0;
   }
   grid_wait();
-  // groups that do not lie in order within the rows: none is shared
+  // groups that do not lie in order within the rows, or a prefix of less than no key: none is shared
   bool bad = false;
-  for (int g = tid; g <= p.n_groups; g += kPlanThreads) {
-    const int s = gload(p.start + g);
-    bad |= s < 0 || s > p.n_q || (g < p.n_groups && gload(p.start + g + 1) < s);
-  }
+  for (int g = tid; g <= p.n_groups; g += kPlanThreads)
+    if (group_errors(p.start, p.prefix, p.n_groups, p.n_q, g)) {
+      bad = true;
+      report(faults, DEV_ERR_RANGE);
+    }
   bad = __syncthreads_or(bad);
-  if (bad && tid == 0) report(faults, DEV_ERR_RANGE);
   const int n_groups = bad ? 0 : p.n_groups;
   // A group's longest row: a warp a group, or eight lanes where there are more groups than warps.
   const int lanes = n_groups > kPlanThreads / 32 ? 8 : 32, sub = lane & (lanes - 1);
@@ -167,9 +172,8 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     }
     if (sub == 0 && g < n_groups) {
       const long long blocks = (static_cast<long long>(n) * p.H + p.cols - 1) / p.cols;
-      int tiles = min(max(want, 0), max(longest, 0)) / kRows;
+      int tiles = min(want, max(longest, 0)) / kRows;
       if (n < 2 || tiles < kMinShared || blocks > n) tiles = 0;
-      if (want < 0) report(faults, DEV_ERR_RANGE);
       const bool only_staged = blocks >= n;
       if (only_staged && (p.stage_pages == 0 || blocks < kStageBlocks)) tiles = 0;
       if (tiles > 0 && p.stage_pages > 0) {
@@ -619,6 +623,12 @@ Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
 }
 
 }  // namespace
+
+bool latent_shared_alone(bool fp8, int n_q, int n_heads, const PagedRows& pg, const SharedRows& groups) {
+  if (!latent_attn_joins(n_q, n_heads, pg)) return false;
+  if (groups.n_groups == 0 || (n_heads == 128 && !fp8)) return true;       // nothing would be shared
+  return 2LL * n_q * pg.max_pages <= kAloneTiles;
+}
 
 size_t latent_shared_ws_bytes(int n_q, int n_heads, int n_groups, int max_rows) {
   return shared_layout(n_q, n_heads, n_groups, max_rows).total;

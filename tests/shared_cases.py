@@ -12,9 +12,10 @@ from oracle import latent_oracle as LO
 class SharedPaged:
     """groups: [(prefix, [length of each row], drafts)].  The rows of a group hold the same first prefix keys
     (as far as each is long): in common pages where a page lies whole in the prefix (drafts: in every page), in
-    copies where it does not.  Every cache row that nobody uses is NaN, every table entry that nobody uses -7."""
+    copies where it does not.  Every cache row that nobody uses is NaN, every table entry that nobody uses -7.
+    wide: a table so wide that the call cannot know it for one of the small ones that share nothing."""
 
-    def __init__(self, groups, fmt, seed=0, std=1.0):
+    def __init__(self, groups, fmt, seed=0, std=1.0, wide=True):
         g = gen(seed)
         self.fmt, self.lens, self.kv = fmt, [], []
         tables, pages = [], []              # pages: [contents [<= 128, 576]]
@@ -48,6 +49,8 @@ class SharedPaged:
         self.n_pages = len(pages) + 3
         perm = np.random.default_rng(seed).permutation(self.n_pages)
         cols = max([1] + [len(r) for r in tables]) + 1
+        if wide:
+            cols = max(cols, 1001 // max(1, len(tables)) + 1)
         self.bt = np.full((len(tables), cols), -7, dtype=np.int32)
         for t, r in enumerate(tables):
             self.bt[t, :len(r)] = perm[r] if r else []

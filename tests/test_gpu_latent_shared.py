@@ -18,8 +18,8 @@ def _built():
     assert torch.cuda.is_available()
 
 
-def _check(groups, H, fmt, seed=1, check=None, bits=0, **kw):
-    sp = SharedPaged(groups, fmt, seed=seed)
+def _check(groups, H, fmt, seed=1, check=None, bits=0, wide=True, **kw):
+    sp = SharedPaged(groups, fmt, seed=seed, wide=wide)
     q = randn((len(sp.lens), H, 576), gen(seed + 50))
     out, lse, ws = sp.attend(q, **kw)
     assert D.dsa_workspace_status(ws, raise_on_fault=False) == bits
@@ -37,6 +37,29 @@ MIXED = [
 @pytest.mark.parametrize("H", [1, 3, 8, 16, 17, 32, 33, 64, 65, 100, 128])
 def test_groups_of_every_kind(H, fmt):
     _check(MIXED, H, fmt, seed=H)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H", [8, 40, 100, 128])
+def test_small_calls_share_nothing(H, fmt):
+    sp, q, out, lse = _check(MIXED, H, fmt, seed=H, wide=False)
+    # the unshared call's results, bit for bit
+    desc = D.attn_desc(q.shape[0], sp.n_pages * P, H, 0, TAU)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    D.dsa_latent_attn_paged(desc, q, sp.cache, None, sp.pages, o2, l2)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    # and its groups are checked all the same
+    pre = list(sp.prefix)
+    pre[3] = -1
+    for kw in (dict(start=i32([0, 5, 4] + sp.start[3:])), dict(prefix=i32(pre))):
+        o3, l3, ws = sp.attend(q, **kw)
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+        assert torch.equal(out, o3) and torch.equal(lse, l3)
+    sp = SharedPaged([(5, [7], False)], fmt, seed=2, wide=False)       # one row, one CTA
+    q = randn((1, H, 576), gen(3))
+    out, lse, ws = sp.attend(q)
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [sp.stored(0)])
 
 
 @pytest.mark.parametrize("max_rows", [1, 2, 4, 1000])
