@@ -404,6 +404,8 @@ struct Pieces {
 };
 __device__ __forceinline__ Pieces find_pieces(const LArgs& a, int2 groups, int col_in_item, size_t col) {
   Pieces p{};
+  // (a walk whose wait ran out has left items unnoted: what is found there then is any number, and no piece)
+  if (groups.x < 0 || groups.y > a.n_grp || groups.x >= groups.y) return p;
   p.n = groups.y - groups.x;
   if (p.n == 1) {
     p.o = a.whole_o;

@@ -302,3 +302,23 @@ def test_a_wait_that_runs_out_is_reported(H, fmt):
     out, lse, ws = sp.attend(q, ws=ref[2])
     assert D.dsa_workspace_status(ws) == 0
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("fill", [0x7F, 0x00, 0xFF])
+@pytest.mark.parametrize("H,rows", [(8, 6), (40, 6), (100, 6), (100, 9)])
+def test_a_wait_that_runs_out_in_a_workspace_of_anything(H, rows, fill):
+    """The join finds no pieces noted where the walks gave up, whatever the workspace held."""
+    sp = SharedPaged([(9000, [9000 + 50 * i for i in range(rows)], False)], "fp8", seed=3)
+    q = randn((rows, H, 576), gen(4))
+    ref = sp.attend(q)
+    ws = torch.full_like(ref[2], fill)
+    D.dsa_debug_pipeline(0, 1_000_000)
+    try:
+        sp.attend(q, ws=ws)
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) & 1
+    finally:
+        D.dsa_debug_pipeline(-1, 0)
+    ws.fill_(fill)
+    out, lse, ws = sp.attend(q, ws=ws)
+    assert D.dsa_workspace_status(ws) == 0
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
