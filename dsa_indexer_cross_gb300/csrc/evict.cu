@@ -55,7 +55,7 @@ struct Smem {
   uint32_t all[kBins];               // the cluster's
   uint32_t above[kMostCtas * kWarps], at[kMostCtas * kWarps];      // of each warp of the cluster
   uint32_t warp_sum[kWarps];
-  uint32_t bin, before;              // the limit's bin, and the entries above it
+  uint32_t bin, before, count;       // the limit's bin, the entries above it and its own
 };
 
 // Inclusive sum over the lanes.
@@ -118,10 +118,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
       }
     }
   };
-  if (rank == 0 && threadIdx.x == 0) {
-    if (want != L) report(status, false, DEV_ERR_RANGE);
-    e.new_len[t] = n;
-  }
+  if (rank == 0 && threadIdx.x == 0) e.new_len[t] = n;
+  if (blockIdx.x == 0 && threadIdx.x < 2) status[threadIdx.x] = 0u;      // (faults are the next kernel's to report)
   // those that stay in any case, and the unused end of kept
   const int stride = n_cta * kThreads, me = rank * kThreads + static_cast<int>(threadIdx.x);
   const auto keep = [&](int place, int j) {
@@ -133,11 +131,12 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   for (int i = n + me; i < e.n_keep; i += stride) kept[i] = -1;
   if (K == 0) return;                                          // (the whole cluster)
 
-  uint32_t limit = 0;                // bits of the limit found so far
+  uint32_t limit = 0;                // bits of the limit found so far, those from `shift` on
   uint32_t need = static_cast<uint32_t>(K);
+  int shift = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bits = pass == 2 ? 10 : 11;
     for (int b = threadIdx.x; b < kBins; b += kThreads) sh.mine[b] = 0;
     __syncthreads();
@@ -179,17 +178,19 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
       if (before < need && need <= before + c[i]) {
         sh.bin = kBins - 1 - (static_cast<uint32_t>(threadIdx.x) * PER + i);
         sh.before = before;
+        sh.count = c[i];
       }
       before += c[i];
     }
     __syncthreads();
     limit = (limit << bits) | sh.bin;
     need -= sh.before;
+    if (need == sh.count) break;       // the whole bin stays (as a rule one key, after the second pass)
   }
-  // limit: the K-th heaviest weight; need: how many of that weight stay
+  // limit: the K-th heaviest weight, or its upper bits; need: how many with these stay
   uint32_t above = 0, at = 0;
   keys([&](int, float x, bool there) {
-    const uint32_t key = weight_key(x);
+    const uint32_t key = weight_key(x) >> shift;
     above += there && key > limit ? 1u : 0u;
     at += there && key == limit ? 1u : 0u;
   });
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const __grid_
   above_before = __reduce_add_sync(0xffffffffu, above_before);
   at_before = __reduce_add_sync(0xffffffffu, at_before);
   keys([&](int j, float x, bool there) {
-    const uint32_t key = weight_key(x);
+    const uint32_t key = weight_key(x) >> shift;
     const uint32_t a = __ballot_sync(0xffffffffu, there && key > limit), q = __ballot_sync(0xffffffffu, there && key == limit);
     const uint32_t lower = (1u << lane) - 1u;
     const uint32_t at_here = at_before + __popc(q & lower);
@@ -235,6 +236,10 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
   const int t = blockIdx.x / per_seq;
   const int i0 = ((blockIdx.x - t * per_seq) * 8 + warp) * kCopyRows;
   const int n = gload(e.new_len + t);
+  if (i0 == 0 && lane == 0) {
+    const int want = gload(e.from.seq_len + t);
+    if (want < 0 || want > (e.from.max_pages << kPageShift)) report(status, false, DEV_ERR_RANGE);
+  }
   if (i0 >= n) return;
   const int i = i0 + (lane & (kCopyRows - 1));
   int from = -1, to = -1;
@@ -299,8 +304,7 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
 }  // namespace
 
 cudaError_t launch_evict(const Evict& a, const LatentCache& src, const LatentCache& dst, uint32_t* status, cudaStream_t st) {
-  cudaError_t e = clear_status(status, st);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   int sms = device_sm_count();
   if (sms <= 0) sms = 152;
   // as many CTAs as hold the longest sequence that the table allows in registers, while all are resident at once
