@@ -1,5 +1,6 @@
 """GB300-native DSA lightning indexer + causal top-k, IndexShare layer loop and sparse MLA
-attention, and the paged latent cache with the attention that reads it.  The compute runs in
+attention, the paged latent cache with the attention that reads it, and what a decode step needs around
+it (shared prefixes, draft verification, key weights, eviction).  The compute runs in
 libdsa.so (hand-written sm_103a kernels behind a C ABI, include/dsa.h); this package is its ctypes binding plus seeded input generators.
 """
 from ._lib import (AttnDesc, DsaError, IndexCache, IndexerDesc, LayerIO, PagedCache, DSA_IDX_INDEPENDENT_ROWS,

@@ -12,6 +12,12 @@
 // shared memory; of longer sequences they are read again in every pass, out of L2.
 //
 // Copying.  A warp takes eight rows; HBM bounds it.
+//
+// What bounds the call.  24 sequences of 8K to 65K keys cut to 16384, fp8: 95 us, of which the copy moves 490 MB in 72
+// (6.8 TB/s, what a copy reaches), behind some 20 of choosing: three trips to memory and, a pass, two cluster barriers and
+// a scan of 2048 bins.  Two of 3000 to 5000, bf16: 10 us, the same trips without a cluster and one launch more.  Keys
+// read again in every pass: 104 us where they are held (15.4 for the small call); a clearing launch and always three
+// passes: 97 and 11.7.
 #include <cuda_bf16.h>
 
 #include <algorithm>

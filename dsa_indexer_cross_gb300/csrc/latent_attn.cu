@@ -33,6 +33,17 @@
 // through registers and shared memory to its two products, with two tiles under way; how much of it each step
 // takes has not been measured.  Selected keys (2048 of each row): 39 us at 16 heads, 61 at 64: the gathers'
 // latency, the partials and their join.
+//
+// Modes (WalkMode, latent_attn.cuh).  kItems walks what latent_shared.cu lists.  kWeights sums, instead of a second
+// product, each key's weights over the heads, exp(tau q . kv_j - lse), for up to 128 heads a CTA: O and P are not
+// there, so S may have 128 columns, with room for one tile beside 144 KB of q.  The first product's warp frees the
+// tile's halves; four warps take sixteen keys each with every column, so a key's sum is shuffles among four lanes and
+// one store.  fp8 tiles are converted by all eight warps, each with two tiles' codes in registers (see there): 32 rows of 1K
+// to 33K keys, 64 heads, 91 us (3.8 TB/s; floor 54), 16 rows of 8K to 65K, 128 heads, 135 (floor 72).  Measured and not
+// kept: two blocks of 64 heads on two CTAs, whose sums a second kernel adds (240); two groups of converter warps in turn
+// (101 and 152); three groups (118 and 172, spills); sixteen warps (100 and 144); codes copied to shared memory two
+// tiles ahead, in the room of the second tile (89 at 64 heads).  No unit is full (ncu, 64 heads: L1 and shared memory 52 %,
+// issue slots 47, DRAM 40, tensor pipe 34): what is left is the converters' own chain from codes to a tile.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -51,8 +62,8 @@ struct LCfg {
   static constexpr int Q_BYTES = HB * kDqk * 2;
   static constexpr int SLOTS = HB > 64 ? 1 : 2;        // tiles in shared memory
   static constexpr int DYN_SMEM = 1024 + SLOTS * kTileBytes + Q_BYTES;
-  // softmax warps (fp8: four, which leaves the converters 128 registers; the keys' weights: each key's
-  // columns in one warp)
+  // softmax warps (fp8: four, which leaves the converters 128 registers; weights: four, so that a warp has a key's
+  // every column)
   static constexpr int SW = HB >= 32 && !FP8 && !WEIGHTS ? 8 : 4;
   static constexpr int SOFT = 32 * SW;
   static constexpr int NP = FP8 ? 8 : 1;               // producer warps
@@ -191,7 +202,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
       // All eight warps convert each tile, eight rows a warp, with two tiles' codes in registers: half a tile's are
       // asked for as soon as the half two tiles before is converted.  (Two groups of four warps that take the tiles
       // in turn, as for the attention, wait for each other where shared memory has room for one bf16 tile.)  Lane
-      // l looks after row l & 7: its page is found three tiles ahead, its scale word two.
+      // l looks after row l & 7: its page is found three tiles ahead, its scale word two.  As there, a load
+      // instruction takes whole lines and eight lanes of a store phase cover two rows.
       const int row_base = 8 * pw, my_row = row_base + (lane & 7);
       const int c = lane & 3, par = (lane >> 2) & 1, blk4 = lane >> 3;    // codes 16 c .. of block blk4 (+ 4), row parity
       const uint32_t tile0 = smem_u32(sT);
