@@ -586,7 +586,7 @@ dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, cons
  * stay valid for the others, and the caller frees what it no longer needs.
  *   kept int32 [n_seq][n_keep]: old positions, ascending, then -1; new_len int32 [n_seq]: keys that stay (it may
  *   be the seq_len of to_pages, which this call does not read, so that to_pages then describes the result).
- *   weight f32, rows weight_stride >= from_pages->max_pages * page_rows apart; weight_out f32 or NULL, rows
+ *   weight f32, rows weight_stride >= from_pages->max_pages * page_rows apart; weight_out f32 or NULL, no part of weight, rows
  *   weight_out_stride apart (at least the smaller of n_keep and from's keys): the kept keys' weights, in
  *   order; elements behind them stay as they were.
  *   from, to: of one format, the same arrays or others; no page of to_pages is a page of from_pages or of

@@ -195,3 +195,22 @@ def test_steps_of_drafting(fmt, H):
         for x, y in zip(a.state(), b.state()):
             assert torch.equal(x, y)
     assert moved > 0
+
+
+@pytest.mark.parametrize("lens,shares", [([700, 300], False), ([700, 300, 5, 60, 900], True)])
+def test_the_launch_log_names_the_calls(lens, shares):
+    s = Steps(lens, 3, 16, 1000, "fp8", 3)
+    s.feed(1)
+    s.step()
+    want = s.state()
+    s.len.copy_(i32(lens))
+    s.weight.zero_()
+    D.dsa_profile_enable(True)
+    try:
+        s.step()
+        kinds = [k for k, _ in D.dsa_profile_read()]
+    finally:
+        D.dsa_profile_enable(False)
+    # (a small call shares nothing, and lists nothing)
+    assert kinds == ["cache"] + ["attn_prep"] * shares + ["attn", "attn", "verify"]
+    assert all(torch.equal(a, b) for a, b in zip(s.state(), want))
