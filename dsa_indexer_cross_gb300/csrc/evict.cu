@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < kRope; ++k) {
       const int q = 4 * k + (lane >> 3), row = __shfl_sync(0xffffffffu, from, q);
-      if (q < kCopyRows && row >= 0) r[k] = gload(reinterpret_cast<const uint4*>(src.rope + static_cast<size_t>(row) * 64) + (lane & 7));
+      if (q < kCopyRows && row >= 0)
+        r[k] = gload(reinterpret_cast<const uint4*>(src.rope + static_cast<size_t>(row) * 64) + (lane & 7));
     }
     if (lane < kCopyRows && from >= 0) sc = gload(reinterpret_cast<const uint32_t*>(src.scale) + from);
 #pragma unroll
@@ -296,12 +297,14 @@ __global__ void __launch_bounds__(256) evict_copy_kernel(const __grid_constant__
 #pragma unroll
       for (int k = 0; k < kPart; ++k) {
         const int x = (h + k) * 32 + lane, row = __shfl_sync(0xffffffffu, from, x / kVec);
-        if (x < kCopyRows * kVec && row >= 0) v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 1152) + x % kVec);
+        if (x < kCopyRows * kVec && row >= 0)
+          v[k] = gload(reinterpret_cast<const uint4*>(src.latent + static_cast<size_t>(row) * 1152) + x % kVec);
       }
 #pragma unroll
       for (int k = 0; k < kPart; ++k) {
         const int x = (h + k) * 32 + lane, row = __shfl_sync(0xffffffffu, to, x / kVec);
-        if (x < kCopyRows * kVec && row >= 0) reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 1152)[x % kVec] = v[k];
+        if (x < kCopyRows * kVec && row >= 0)
+          reinterpret_cast<uint4*>(dst.latent + static_cast<size_t>(row) * 1152)[x % kVec] = v[k];
       }
     }
   }

@@ -264,8 +264,8 @@ __device__ __forceinline__ void publish_faults(const LArgs& a, const CtaFaults& 
   w[1] = f.count;
 }
 
-// The share of group `grp` (of items: as they were listed): a scan over the rows' tile counts (the whole block calls it; a block-wide barrier
-// is needed behind it before row0 / tile0 are read).
+// The share of group `grp` (of items: as it was listed): a scan over the rows' tile counts (the whole block calls it;
+// a block-wide barrier is needed behind it before row0 / tile0 are read).
 struct Share {
   long long wsum[32];
   int wmax[32];

@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   for (int i = tid; i < pre.items; i += kPlanThreads) {
     const int g = last_not_above(p.base, n_groups, i);       // (the last of equal ones: the one with items)
     const int s = gload(p.start + g), e = gload(p.start + g + 1), b = i - p.base[g];
-    p.items[pre_list][i] = make_int4(s * p.H + b * p.cols, min(p.cols, (e - s) * p.H - b * p.cols), staged ? p.stage_at[g] : p.table[g], 0);
+    p.items[pre_list][i] = make_int4(s * p.H + b * p.cols, min(p.cols, (e - s) * p.H - b * p.cols),
+                                     staged ? p.stage_at[g] : p.table[g], 0);
     p.nt[pre_list][i] = p.tiles[g];
     p.at[pre_list][i] = p.base_at[g] + static_cast<long long>(b) * (p.tiles[g] + kItemCost);
   }
