@@ -151,17 +151,19 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     }
   bad = __syncthreads_or(bad);
   const int n_groups = bad ? 0 : p.n_groups;
-  // A group's longest row: a warp a group, or eight lanes where there are more groups than warps.
+  // A group's longest row, and its second longest, whose keys bound what is shared: a warp a group, or eight lanes
+  // where there are more groups than warps.
   const int lanes = n_groups > kPlanThreads / 32 ? 8 : 32, sub = lane & (lanes - 1);
   for (int g0 = warp * (32 / lanes); g0 < n_groups; g0 += kPlanThreads / lanes) {
     const int g = g0 + lane / lanes;
-    int n = 0, want = 0, longest = -1, at = 0x7FFFFFFF;
+    int n = 0, want = 0, longest = -1, second = -1, at = 0x7FFFFFFF;
     if (g < n_groups) {
       const int s = gload(p.start + g);
       n = gload(p.start + g + 1) - s;
       want = gload(p.prefix + g);
       for (int r = sub; r < n; r += lanes) {
         const int len = row_len(p.pg, s + r);
+        second = max(second, min(len, longest));
         if (len > longest) {
           longest = len;
           at = s + r;
@@ -171,6 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     __syncwarp();
     for (int o = lanes >> 1; o > 0; o >>= 1) {
       const int l = __shfl_xor_sync(0xffffffffu, longest, o), r = __shfl_xor_sync(0xffffffffu, at, o);
+      second = max(max(second, __shfl_xor_sync(0xffffffffu, second, o)), min(longest, l));
       if (l > longest || (l == longest && r < at)) {
         longest = l;
         at = r;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     }
     if (sub == 0 && g < n_groups) {
       const long long blocks = (static_cast<long long>(n) * p.H + p.cols - 1) / p.cols;
-      int tiles = min(want, max(longest, 0)) / kRows;
+      int tiles = min(want, max(second, 0)) / kRows;
       if (n < 2 || tiles < kMinShared || blocks > n) tiles = 0;
       const bool only_staged = blocks >= n;
       if (only_staged && (p.stage_pages == 0 || blocks < kStageBlocks)) tiles = 0;

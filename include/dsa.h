@@ -541,8 +541,8 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
  * rows shorter than the prefix (a padded batch's empty ones), attend by themselves, as all do in calls too small
  * to gain from sharing (n_q * max_pages up to 1000; 128 heads of a bf16 cache); the walk takes
  * whole tiles of 64 keys of the prefix, the rows their rest.
- *   group_start int32 [n_groups + 1], ascending within [0, n_q]; prefix_len int32 [n_groups], >= 0, beyond the longest
- *   row cut to it (groups that break this are flagged and none is shared; the results are the same).  Device memory, n_groups = 0: may be NULL.  max_rows: rows of the largest
+ *   group_start int32 [n_groups + 1], ascending within [0, n_q]; prefix_len int32 [n_groups], >= 0, cut to
+ *   the second longest row (groups that break this are flagged and none is shared; the results are the same).  Device memory, n_groups = 0: may be NULL.  max_rows: rows of the largest
  *   group, or about (it chooses the kernels and the workspace; any value >= 1 gives right results).
  * An fp8 cache's prefixes that many columns share are brought to bf16 in the workspace first (up to 1024 pages of
  * them, else none).
