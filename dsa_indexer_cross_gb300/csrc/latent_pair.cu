@@ -53,12 +53,15 @@ namespace {
 constexpr int kHeads = 64;                       // heads per CTA
 constexpr int kSBlk = 32 * 128, kVBlk = 64 * 128;
 constexpr int kSBytes = kKB * kSBlk, kVBytes = 4 * kVBlk;
-constexpr int kStage = kSBytes + kVBytes;        // 68 KB
-constexpr int kQBytes = kHeads * kDqk * 2;
+constexpr int kSSlots = 3;                       // S parts under way; two V parts
+constexpr int kQBlk = kHeads * 128;
+constexpr int kQB = 6, kQPart = 3;               // the blocks of q that lie in TMEM, and how many of them a slot brings
+constexpr int kQBytes = (kKB - kQB) * kQBlk;     // the others
 constexpr int kPBytes = kHeads * kRows * 2;
-constexpr int kOffStage = kQBytes, kOffP = kQBytes + 2 * kStage, kOffShared = kOffP + 2 * kPBytes;
+constexpr int kOffS = kQBytes, kOffV = kOffS + kSSlots * kSBytes, kOffP = kOffV + 2 * kVBytes, kOffShared = kOffP + 2 * kPBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 256;                       // O: columns 0 .. 255
+constexpr int kQCol = 320;                       // q: 32 columns a block
 
 constexpr int kSW = 8, kSoft = 256;              // softmax warps, threads
 constexpr int kKT = 16, kOC = 128;               // keys of a tile, O columns per softmax thread
@@ -78,7 +81,7 @@ struct PShared {
   // [2]: by tile parity.  full_*: copies have landed (this CTA); ready_*, s_empty, p_full, o_free, q_ready:
   // the leader's, both CTAs arrive; s_full, o_done, q_empty: S, PV, all of a segment's S complete (both CTAs;
   // q_empty where a segment follows); mma_done: every product complete (both CTAs)
-  uint64_t full_s[2], full_v[2], ready_s[2], ready_v[2], q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2],
+  uint64_t full_s[kSSlots], ready_s[kSSlots], s_free[kSSlots], full_v[2], ready_v[2], q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2],
       o_done[2], o_free, mma_done;
   uint64_t ring_full[kRing], ring_empty[kRing];   // fp8: both CTAs arrive on each CTA's
   uint32_t tmem_base, abort_flag, soft_abort;
@@ -89,7 +92,8 @@ struct PShared {
 };
 constexpr int kDynSmem = kOffShared + sizeof(PShared);
 static_assert(kDynSmem <= 232448, "shared memory");
-static_assert(kOffStage % 1024 == 0 && kStage % 1024 == 0 && kSBytes % 1024 == 0, "swizzled blocks");
+static_assert(kOffS % 1024 == 0 && kSBytes % 1024 == 0 && kVBytes % 1024 == 0, "swizzled blocks");
+static_assert(kQPart * kQBlk <= kSBytes && kQB % kQPart == 0, "q through the slots");
 
 // ------------------------------------------------------------------------------- cluster, cta_group::2
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -147,6 +151,31 @@ __device__ __forceinline__ void umma_pair_x4_elect(uint32_t d_tmem, uint64_t ade
       "n"(2 * BSTEP), "n"(3 * BSTEP)
       : "memory");
 }
+// The same with A from TMEM (each CTA's 64 rows in lanes 0 .. 63 and again in 64 .. 127, 8 columns a K step).
+template <int BSTEP>
+__device__ __forceinline__ void umma_pair_ta_x4_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                      uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e, t;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
+      " add.s64 b1, %2, %5;\n add.s64 b2, %2, %6;\n add.s64 b3, %2, %7;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n"
+      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
+      : "memory");
+}
+// 64 rows of 16 bytes in each CTA's shared memory to 4 TMEM columns: rows 0 .. 31 to lanes 0 .. and 64 .., rows
+// 32 .. 63 to lanes 32 .. and 96 ...
+__device__ __forceinline__ void tmem_copy_pair_elect(uint32_t d_tmem, uint64_t sdesc) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.cp.cta_group::2.64x128b.warpx2::02_13 [%0], %1;\n}\n" ::"r"(d_tmem),
+      "l"(sdesc)
+      : "memory");
+}
 // Arrive on this barrier in both CTAs when every product issued so far has completed.
 __device__ __forceinline__ void commit_pair_elect(uint64_t* bar) {
   asm volatile(
@@ -172,14 +201,17 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.full_s[s], 1);
       mbar_init(&sh.full_v[s], 1);
-      mbar_init(&sh.ready_s[s], 2);
       mbar_init(&sh.ready_v[s], 2);
       mbar_init(&sh.s_full[s], 1);
       mbar_init(&sh.s_empty[s], 2 * kSW);
       mbar_init(&sh.p_full[s], 2 * kSW);
       mbar_init(&sh.o_done[s], 1);
+    }
+    for (int s = 0; s < kSSlots; ++s) {
+      mbar_init(&sh.full_s[s], 1);
+      mbar_init(&sh.ready_s[s], 2);
+      mbar_init(&sh.s_free[s], 1);
     }
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&sh.ring_full[s], 8);    // the CTAs' converters, for each quarter of their rows
@@ -219,19 +251,31 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
   };
 
-  // S warps: this CTA's 64 heads of a segment's row, once the previous ones have been read
-  auto load_q = [&](uint32_t it) -> bool {
+  // S warps: this CTA's 64 heads of a segment's row, the blocks that stay in shared memory, once the previous ones
+  // have been read
+  auto start_q = [&](uint32_t it) -> bool {
     if (it > 0 && !wait(&sh.q_empty, (it - 1) & 1)) return false;
     if (lane == 0) {
       mbar_arrive_expect_tx(&sh.q_full, kQBytes);
 #pragma unroll 1
-      for (int kb = 0; kb < kKB; ++kb)
-        tma_load_2d(sQ + kb * (kHeads * 128), &tmap_q, &sh.q_full, kb * 64, sg.col0 + static_cast<int>(rank) * kHeads);
+      for (int kb = kQB; kb < kKB; ++kb)
+        tma_load_2d(sQ + (kb - kQB) * kQBlk, &tmap_q, &sh.q_full, kb * 64, sg.col0 + static_cast<int>(rank) * kHeads);
     }
     __syncwarp();
+    return true;
+  };
+  auto finish_q = [&](uint32_t it) -> bool {
     const bool ok = wait(&sh.q_full, it & 1);
     if (!ok && lane == 0) mbar_drain(&sh.q_full, it & 1, 200000000ull);   // the copy lands before we leave
     return ok;
+  };
+  // the slots of the S parts, in turn: a segment's blocks of q for TMEM, then its tiles
+  uint32_t es = 0, el = 0;
+  auto next_slot = [&]() {
+    if (++es == kSSlots) {
+      es = 0;
+      ++el;
+    }
   };
 
   if (warp >= C::COPY && warp < C::CONV) {
@@ -248,6 +292,21 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
       const int len = seg_len<MODE>(a, sg);
       int ahead = FP8 ? 0 : gload(bt + (sg.i0 >> 1));
+      for (int k = 0; part0 == 0 && k < kQB; k += kQPart, next_slot()) {
+        if (copies) {
+          if (el > 0 && !(ok = wait(&sh.s_free[es], (el - 1) & 1))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.full_s[es], kQPart * kQBlk);
+            for (int u = 0; u < kQPart; ++u)
+              tma_load_2d(smem + kOffS + es * kSBytes + u * kQBlk, &tmap_q, &sh.full_s[es], (k + u) * 64,
+                          sg.col0 + static_cast<int>(rank) * kHeads);
+          }
+          __syncwarp();
+        } else {
+          if (!(ok = wait(&sh.full_s[es], el & 1))) break;
+          if (lane == 0) arrive_cta(&sh.ready_s[es], 0);
+        }
+      }
       for (int n = 0; n < sg.n && ok; ++n, ++g) {
         const int i = sg.i0 + n, page = ahead, sb = g & 1;
         if (!FP8 && n + 1 < sg.n) ahead = gload(bt + ((i + 1) >> 1));
@@ -264,10 +323,12 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
         }
 #pragma unroll 1
         for (int part = part0; part < part1 && ok; ++part) {
-          uint64_t* full = part ? &sh.full_v[sb] : &sh.full_s[sb];
-          uint8_t* st = smem + kOffStage + sb * kStage + (part ? kSBytes : 0);
+          uint64_t* full = part ? &sh.full_v[sb] : &sh.full_s[es];
+          uint8_t* st = smem + (part ? kOffV + sb * kVBytes : kOffS + es * kSBytes);
           if (copies) {
-            if (g >= 2 && !(ok = wait(part ? &sh.o_done[sb] : &sh.s_full[sb], ((g >> 1) - 1) & 1))) break;
+            if (part ? g >= 2 && !(ok = wait(&sh.o_done[sb], ((g >> 1) - 1) & 1))
+                     : el > 0 && !(ok = wait(&sh.s_free[es], (el - 1) & 1)))
+              break;
             if (lane == 0) {
               int row = nv == 0 ? 0 : (page << kPageShift) + (i & 1) * kRows;
               if constexpr (FP8) {
@@ -282,7 +343,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
             }
             __syncwarp();
           } else {
-            if (!(ok = wait(full, (g >> 1) & 1))) break;
+            if (!(ok = wait(full, part ? (g >> 1) & 1 : el & 1))) break;
             if (!FP8 && part && nv < kRows) {
 #pragma unroll 1
               for (int vb = 0; vb < 4; ++vb) {
@@ -293,13 +354,14 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
             }
             __syncwarp();
             if (lane == 0) {
-              arrive_cta(part ? &sh.ready_v[sb] : &sh.ready_s[sb], 0);
+              arrive_cta(part ? &sh.ready_v[sb] : &sh.ready_s[es], 0);
               if constexpr (FP8) {
                 arrive_cta(&sh.ring_empty[slot], rank);
                 if (part) arrive_cta(&sh.ring_empty[slot], rank ^ 1u);
               }
             }
           }
+          if (part == 0) next_slot();
         }
         if (++slot == kRing) {
           slot = 0;
@@ -308,11 +370,17 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
       }
     }
     // let every copy this CTA started land before its shared memory can be released (one more wait than
-    // copies where the last tile's were not both started: bounded)
-    if (copies && lane == 0)
-      for (int part = part0; part < part1; ++part)
-        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j)
-          mbar_drain(part ? &sh.full_v[j & 1] : &sh.full_s[j & 1], (j >> 1) & 1, 200000000ull);
+    // copies where the last tile's V part was not started: bounded)
+    if (copies && lane == 0) {
+      const uint32_t e = el * kSSlots + es;
+      if (part0 == 0)
+        for (uint32_t j = e > kSSlots ? e - kSSlots : 0; j < e; ++j) {
+          mbar_drain(&sh.full_s[j % kSSlots], (j / kSSlots) & 1, 200000000ull);
+          mbar_drain(&sh.s_free[j % kSSlots], (j / kSSlots) & 1, 200000000ull);      // (nobody else waits for these)
+        }
+      if (part1 == 2)
+        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full_v[j & 1], (j >> 1) & 1, 200000000ull);
+    }
   } else if (FP8 && warp >= C::CONV && warp < C::S_WARP) {
     // ---------------------------------------------------------------- fp8: codes -> bf16 rows in the ring
     // Warp w converts the CTA's 32 keys of tiles w, w + kRing, ...: lane l looks up key l of the next tile
@@ -587,7 +655,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     if (warp == C::S_WARP) {
       uint32_t it = 0;
       while (walk.next(sg)) {
-        if (!load_q(it)) break;
+        if (!start_q(it) || !finish_q(it)) break;
         if (lane == 0) arrive_cta(&sh.q_ready, 0);
         ++it;
       }
@@ -601,20 +669,38 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
     while (ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
-        ok = load_q(it) && wait(&sh.q_ready, it & 1);
+        // (start_q: the products that read the previous q have finished)
+        const bool started = ok = start_q(it);
+        for (int k = 0; k < kQB && ok; k += kQPart, next_slot()) {
+          if (!(ok = wait(&sh.ready_s[es], el & 1))) break;
+          tc_fence_after();
+          const uint64_t dp = sdesc_sw128(smem_u32(smem + kOffS + es * kSBytes), 16, 1024);
+#pragma unroll 1
+          for (int c = 0; c < 8 * kQPart; ++c)
+            tmem_copy_pair_elect(tmem + kQCol + 32 * k + 4 * c, dp + static_cast<uint64_t>(((c >> 3) * kQBlk + (c & 7) * 16) >> 4));
+          commit_pair_elect(&sh.s_free[es]);
+        }
+        if (started) ok = finish_q(it) && ok;
+        ok = ok && wait(&sh.q_ready, it & 1);
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
-          if (!(ok = wait(&sh.ready_s[sb], (g >> 1) & 1))) break;
+          if (!(ok = wait(&sh.ready_s[es], el & 1))) break;
           tc_fence_after();
-          const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage), 16, 1024);
+          const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffS + es * kSBytes), 16, 1024);
           // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
           // too slowly for the tensor core: 1913 us where the loop takes 1473)
-#pragma unroll FP8 ? 1 : kKB
-          for (int kb = 0; kb < kKB; ++kb)
-            umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>((kb * kHeads * 128) >> 4),
+#pragma unroll FP8 ? 1 : kQB
+          for (int kb = 0; kb < kQB; ++kb)
+            umma_pair_ta_x4_elect<2>(tmem + kSCol + sb * 32, tmem + kQCol + 32 * kb,
                                      dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
+#pragma unroll FP8 ? 1 : kKB - kQB
+          for (int kb = kQB; kb < kKB; ++kb)
+            umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>(((kb - kQB) * kQBlk) >> 4),
+                                     dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, 1u);
           commit_pair_elect(&sh.s_full[sb]);
+          commit_pair_elect(&sh.s_free[es]);
+          next_slot();
         }
         if (ok && walk.left > 0) commit_pair_elect(&sh.q_empty);
       } else {
@@ -625,7 +711,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const uint64_t dp = sdesc_sw128(smem_u32(smem + kOffP + sb * kPBytes), 16, 1024);
-          const uint64_t dv = sdesc_sw128(smem_u32(smem + kOffStage + sb * kStage + kSBytes), kVBlk, 1024);
+          const uint64_t dv = sdesc_sw128(smem_u32(smem + kOffV + sb * kVBytes), kVBlk, 1024);
 #pragma unroll FP8 ? 1 : 2
           for (int h = 0; h < 2; ++h)
             umma_pair_x4_elect<2, 128>(tmem + h * 128, dp, dv + static_cast<uint64_t>((2 * h * kVBlk) >> 4), id_pv,
