@@ -17,14 +17,19 @@
 //   V part: all 64 keys, its 256 dims   (four 64-dim blocks of 64 rows x 128 B)
 // The two overlap in the values of its keys and dims, which lie in both: each part needs the same place
 // in both CTAs (a descriptor holds for the pair) and its own row order.  They are filled and freed
-// apart: the S part of tile g + 2 as soon as S(g) is complete, the V part once PV(g) is, so the way
+// apart: the S part of tile g + 3 as soon as S(g) is complete, the V part of tile g + 2 once PV(g) is, so the way
 // of a tile from its rows to its product does not limit how often one begins (one barrier for both
-// parts: 1487 us where the two take 1102, 64 rows of 8K to 131K keys, 128 heads, bf16).
+// parts: 1487 us where the two took 1102, 64 rows of 8K to 131K keys, 128 heads, bf16).
 //
 // TMEM.  An M = 128 accumulator of a pair has head h of each CTA in lane h for the first half of the
 // columns and in lane 64 + h for the second half: O is 2 x 128 columns, S 32 columns, double-buffered.
 // A softmax thread owns one head and 16 of a tile's 64 keys, so the running maximum is a register and
 // the slow path (a maximum that grew by more than 2^8) exchanges four values a head.
+// The other 192 columns hold six of q's nine blocks (as operand A, in both halves of the lanes).  They pass through the
+// slots of the S parts, which q then does not take room from: three slots where there were two, and the first product's
+// operand reads fall by 48 KB a tile.  What limits a walk is how soon a slot is filled again (bf16 rows from L2, 32 rows
+// of 64 heads behind 100K keys: two slots 422 us, six blocks in TMEM 406, three slots 377).  The first segment's
+// first three blocks come in where P will be, so that its first two tiles are under way beside q (1.5 us a call).
 //
 // fp8.  The two parts of a tile overlap, so converting into shared memory would convert (or write) the
 // overlap twice.  Instead each CTA converts its 32 keys once, whole rows, into a ring of bf16 tiles in the
@@ -32,13 +37,11 @@
 // their parts from there as they do from a bf16 cache (1900 us and more where converters wrote the parts
 // into shared memory).
 //
-// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 1102 to 1126 us, 1192 TFLOP/s of a measured
-// 1924 and 4.9 TB/s of 6.78: operand reads and copies (224 KB a tile, at 128 bytes a clock) would take 80 %
-// of that, though the counter of L1 and shared memory stands at 51 %, the tensor pipe at 44, DRAM at 54.
-// fp8: 1470 us, 913 TFLOP/s, 2.1 TB/s: the same tiles, with the converters' loads and stores through L1 on
-// top (53 %, 33, 24).  No unit is full in either: the rest is the chain from a tile's rows to S, softmax, P and
-// the second product, two tiles under way, whose steps have not been measured apart.  (Scoring two tiles with
-// one N = 128 product: bf16 1653, fp8 2008 us.)
+// What bounds it (64 rows of 8K to 131K keys, 4.8M in all).  bf16: 956 to 980 us, 1.38 PFLOP/s of a measured 1.93 and 5.7
+// TB/s of 6.78; operand reads and copies are 176 KB a tile, at 128 bytes a clock 70 % of that time.  With neither exponentials
+// nor the barrier of the running maximum a walk takes as long (1 %), without the second product 4 % less: what is left is
+// the S parts' way, L2 to slot to product.  fp8: 1370 to 1385 us: the converters' loads and stores (no codes loaded:
+// 12 % less, nothing stored: 4 %).  (Scoring two tiles with one N = 128 product: bf16 1653, fp8 2008 us, of 1102 and 1470.)
 //
 // The leader (the pair's even CTA) issues every product; the peer's warps signal its barriers.  Every
 // wait is bounded.  The CTAs leave together (a cluster barrier behind the last wait), so no thread
@@ -58,7 +61,8 @@ constexpr int kQBlk = kHeads * 128;
 constexpr int kQB = 6, kQPart = 3;               // the blocks of q that lie in TMEM, and how many of them a slot brings
 constexpr int kQBytes = (kKB - kQB) * kQBlk;     // the others
 constexpr int kPBytes = kHeads * kRows * 2;
-constexpr int kOffS = kQBytes, kOffV = kOffS + kSSlots * kSBytes, kOffP = kOffV + 2 * kVBytes, kOffShared = kOffP + 2 * kPBytes;
+constexpr int kOffS = kQBytes, kOffV = kOffS + kSSlots * kSBytes, kOffP = kOffV + 2 * kVBytes;
+constexpr int kOffShared = kOffP + kQPart * kQBlk;   // (P, and before it the first segment's blocks of q)
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSCol = 256;                       // O: columns 0 .. 255
 constexpr int kQCol = 320;                       // q: 32 columns a block
@@ -78,11 +82,12 @@ struct PCfg {
 };
 
 struct PShared {
-  // [2]: by tile parity.  full_*: copies have landed (this CTA); ready_*, s_empty, p_full, o_free, q_ready:
+  // [2]: by tile parity; [kSSlots]: by slot of the S parts.  full_*: copies have landed (this CTA); s_free: a slot has been
+  // read (both CTAs); ready_*, s_empty, p_full, o_free, q_ready:
   // the leader's, both CTAs arrive; s_full, o_done, q_empty: S, PV, all of a segment's S complete (both CTAs;
   // q_empty where a segment follows); mma_done: every product complete (both CTAs)
-  uint64_t full_s[kSSlots], ready_s[kSSlots], s_free[kSSlots], full_v[2], ready_v[2], q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2],
-      o_done[2], o_free, mma_done;
+  uint64_t full_s[kSSlots], ready_s[kSSlots], s_free[kSSlots], full_v[2], ready_v[2];
+  uint64_t q_full, q_ready, q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_free, mma_done;
   uint64_t ring_full[kRing], ring_empty[kRing];   // fp8: both CTAs arrive on each CTA's
   uint32_t tmem_base, abort_flag, soft_abort;
   CtaFaults faults;
@@ -93,7 +98,7 @@ struct PShared {
 constexpr int kDynSmem = kOffShared + sizeof(PShared);
 static_assert(kDynSmem <= 232448, "shared memory");
 static_assert(kOffS % 1024 == 0 && kSBytes % 1024 == 0 && kVBytes % 1024 == 0, "swizzled blocks");
-static_assert(kQPart * kQBlk <= kSBytes && kQB % kQPart == 0, "q through the slots");
+static_assert(kQPart * kQBlk <= kSBytes && kQB == 2 * kQPart && 2 * kPBytes <= kQPart * kQBlk, "q through the slots");
 
 // ------------------------------------------------------------------------------- cluster, cta_group::2
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -134,53 +139,62 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Four K steps of a pair's product with one election (as umma_bf16_x4_elect).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(one));
+  return one != 0;
+}
+// A shared-memory matrix descriptor's low word; the high word (sdesc_sw128's, SBO = 1024) is the same for all.
+constexpr uint32_t kDescHi = 0x40004040u;
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+// Four K steps of a pair's product, by one thread.  (It is chosen once and issues a tile's products behind one branch: an
+// election before each four of them takes 376 us where this takes 348, 32 rows of 64 heads behind 100K keys.)
 template <int ASTEP, int BSTEP>
-__device__ __forceinline__ void umma_pair_x4_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                   uint32_t accumulate) {
+__device__ __forceinline__ void umma_pair_x4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " add.s64 a1, %1, %5;\n add.s64 a2, %1, %6;\n add.s64 a3, %1, %7;\n"
-      " add.s64 b1, %2, %8;\n add.s64 b2, %2, %9;\n add.s64 b3, %2, %10;\n"
-      " elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(ASTEP), "n"(2 * ASTEP), "n"(3 * ASTEP), "n"(BSTEP),
-      "n"(2 * BSTEP), "n"(3 * BSTEP)
+      "{\n .reg .pred p, t;\n .reg .b32 h, x1, x2, x3, y1, y2, y3;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n mov.b32 h, %11;\n"
+      " add.s32 x1, %1, %5;\n add.s32 x2, %1, %6;\n add.s32 x3, %1, %7;\n"
+      " add.s32 y1, %2, %8;\n add.s32 y2, %2, %9;\n add.s32 y3, %2, %10;\n"
+      " mov.b64 a0, {%1, h};\n mov.b64 a1, {x1, h};\n mov.b64 a2, {x2, h};\n mov.b64 a3, {x3, h};\n"
+      " mov.b64 b0, {%2, h};\n mov.b64 b1, {y1, h};\n mov.b64 b2, {y2, h};\n mov.b64 b3, {y3, h};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a0, b0, %3, p;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(ASTEP), "n"(2 * ASTEP), "n"(3 * ASTEP), "n"(BSTEP),
+      "n"(2 * BSTEP), "n"(3 * BSTEP), "n"(kDescHi)
       : "memory");
 }
 // The same with A from TMEM (each CTA's 64 rows in lanes 0 .. 63 and again in 64 .. 127, 8 columns a K step).
 template <int BSTEP>
-__device__ __forceinline__ void umma_pair_ta_x4_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                      uint32_t accumulate) {
+__device__ __forceinline__ void umma_pair_ta_x4(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                                uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e, t;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      "{\n .reg .pred p, t;\n .reg .b32 h, a1, a2, a3, y1, y2, y3;\n .reg .b64 b0, b1, b2, b3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n mov.b32 h, %8;\n"
       " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
-      " add.s64 b1, %2, %5;\n add.s64 b2, %2, %6;\n add.s64 b3, %2, %7;\n"
-      " elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n"
-      " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP)
+      " add.s32 y1, %2, %5;\n add.s32 y2, %2, %6;\n add.s32 y3, %2, %7;\n"
+      " mov.b64 b0, {%2, h};\n mov.b64 b1, {y1, h};\n mov.b64 b2, {y2, h};\n mov.b64 b3, {y3, h};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b0, %3, p;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, t;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, t;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(BSTEP), "n"(2 * BSTEP), "n"(3 * BSTEP), "n"(kDescHi)
       : "memory");
 }
 // 64 rows of 16 bytes in each CTA's shared memory to 4 TMEM columns: rows 0 .. 31 to lanes 0 .. and 64 .., rows
 // 32 .. 63 to lanes 32 .. and 96 ...
-__device__ __forceinline__ void tmem_copy_pair_elect(uint32_t d_tmem, uint64_t sdesc) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.cp.cta_group::2.64x128b.warpx2::02_13 [%0], %1;\n}\n" ::"r"(d_tmem),
-      "l"(sdesc)
-      : "memory");
+__device__ __forceinline__ void tmem_copy_pair(uint32_t d_tmem, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.64x128b.warpx2::02_13 [%0], %1;" ::"r"(d_tmem), "l"(sdesc) : "memory");
 }
-// Arrive on this barrier in both CTAs when every product issued so far has completed.
-__device__ __forceinline__ void commit_pair_elect(uint64_t* bar) {
+// Arrive on this barrier in both CTAs when every product issued so far has completed (the thread that issued them).
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
   asm volatile(
-      "{\n .reg .pred e;\n .reg .b16 m;\n mov.b16 m, 3;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
+      "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
+      " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(
           smem_u32(bar))
       : "memory");
 }
@@ -252,14 +266,17 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
   };
 
   // S warps: this CTA's 64 heads of a segment's row, the blocks that stay in shared memory, once the previous ones
-  // have been read
+  // have been read; the first segment's also the first blocks for TMEM, where P will be
   auto start_q = [&](uint32_t it) -> bool {
     if (it > 0 && !wait(&sh.q_empty, (it - 1) & 1)) return false;
     if (lane == 0) {
-      mbar_arrive_expect_tx(&sh.q_full, kQBytes);
+      const int col = sg.col0 + static_cast<int>(rank) * kHeads;
+      mbar_arrive_expect_tx(&sh.q_full, it > 0 ? kQBytes : kQBytes + kQPart * kQBlk);
 #pragma unroll 1
-      for (int kb = kQB; kb < kKB; ++kb)
-        tma_load_2d(sQ + (kb - kQB) * kQBlk, &tmap_q, &sh.q_full, kb * 64, sg.col0 + static_cast<int>(rank) * kHeads);
+      for (int kb = it > 0 ? kQB : kQB - kQPart; kb < kKB; ++kb) {
+        const int k = kb < kQB ? kb - (kQB - kQPart) : kb;
+        tma_load_2d(kb < kQB ? smem + kOffP + k * kQBlk : sQ + (kb - kQB) * kQBlk, &tmap_q, &sh.q_full, k * 64, col);
+      }
     }
     __syncwarp();
     return true;
@@ -269,13 +286,12 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     if (!ok && lane == 0) mbar_drain(&sh.q_full, it & 1, 200000000ull);   // the copy lands before we leave
     return ok;
   };
-  // the slots of the S parts, in turn: a segment's blocks of q for TMEM, then its tiles
-  uint32_t es = 0, el = 0;
+  // the slots of the S parts, in turn, from the last: a segment's blocks of q for TMEM, then its tiles.  (So the first
+  // segment's first two tiles need not wait for q to be moved.)
+  uint32_t es = kSSlots - 1, el = 0;
   auto next_slot = [&]() {
-    if (++es == kSSlots) {
-      es = 0;
-      ++el;
-    }
+    if (++es == kSSlots) es = 0;
+    if (es == kSSlots - 1) ++el;
   };
 
   if (warp >= C::COPY && warp < C::CONV) {
@@ -285,14 +301,13 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     // leader.  bf16: two warps for the S part, two for the V part; fp8: one pair for both, in turn.
     const int pw = warp - C::COPY;
     const bool copies = (pw & 1) == 0;
-    const int part0 = FP8 ? 0 : pw >> 1, part1 = FP8 ? 2 : part0 + 1;   // 0: S part, 1: V part
+    const int part0 = FP8 ? 0 : pw >> 1, part1 = FP8 ? 2 : part0 + 1;   // 0: q and S part, 1: V part
     uint32_t g = 0, slot = 0, lap = 0;       // slot, lap: the tile's place in the ring
     bool ok = true;
-    while (ok && walk.next(sg)) {
-      const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
-      const int len = seg_len<MODE>(a, sg);
-      int ahead = FP8 ? 0 : gload(bt + (sg.i0 >> 1));
-      for (int k = 0; part0 == 0 && k < kQB; k += kQPart, next_slot()) {
+    // the segment's blocks of q for TMEM
+    int q_first = kQPart;                    // (start_q brings the first segment's first part)
+    auto move_q = [&]() {
+      for (int k = q_first; k < kQB; k += kQPart, next_slot()) {
         if (copies) {
           if (el > 0 && !(ok = wait(&sh.s_free[es], (el - 1) & 1))) break;
           if (lane == 0) {
@@ -307,22 +322,80 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           if (lane == 0) arrive_cta(&sh.ready_s[es], 0);
         }
       }
-      for (int n = 0; n < sg.n && ok; ++n, ++g) {
-        const int i = sg.i0 + n, page = ahead, sb = g & 1;
-        if (!FP8 && n + 1 < sg.n) ahead = gload(bt + ((i + 1) >> 1));
-        const int nv = FP8 ? kRows : tile_rows(a, len, i, page);
-        if (copies) {
-          if (nv == 0 && lane == 0 && rank == 0 && part0 == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+      q_first = 0;
+    };
+    if constexpr (FP8) {
+      // the S part of a tile, then the V part of the one before it, which is wanted later (1415 us where the tile's own
+      // V part behind its S part takes 1470; a pair of warps for each part, which leaves 88 registers a thread, 1457)
+      sg.n = 0;
+      for (int n = 0; ok; ++n) {
+        bool more = true;
+        if (n == sg.n) {
+          n = 0;
+          if ((more = walk.next(sg))) move_q();
+          if (!ok) break;
+        }
+        if (more && copies) {
           if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
             ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
             break;
           }
-          if constexpr (FP8) {
-            if (!(ok = wait(&sh.ring_full[slot], lap & 1))) break;
-          }
+          if (!(ok = wait(&sh.ring_full[slot], lap & 1))) break;
         }
 #pragma unroll 1
-        for (int part = part0; part < part1 && ok; ++part) {
+        for (int part = more ? 0 : 1; part < (g > 0 ? 2 : 1); ++part) {
+          const uint32_t at = part ? (slot + kRing - 1) % kRing : slot, gv = g - 1, sb = gv & 1;
+          uint64_t* full = part ? &sh.full_v[sb] : &sh.full_s[es];
+          if (copies) {
+            if (part ? gv >= 2 && !(ok = wait(&sh.o_done[sb], ((gv >> 1) - 1) & 1))
+                     : el > 0 && !(ok = wait(&sh.s_free[es], (el - 1) & 1)))
+              break;
+            if (lane == 0) {
+              uint8_t* st = smem + (part ? kOffV + sb * kVBytes : kOffS + es * kSBytes);
+              const int row = (grp * kRing + static_cast<int>(at)) * kRows;
+              fence_proxy_async_global();    // the converters' stores, before the copies that read them
+              mbar_arrive_expect_tx(full, part ? kVBytes : kSBytes);
+              if (part)
+                tma_load_3d(st, &tmap_v, full, 0, row, 4 * static_cast<int>(rank));
+              else
+                tma_load_3d(st, &tmap_s, full, 0, row + 32 * static_cast<int>(rank), 0);
+            }
+            __syncwarp();
+          } else {
+            if (!(ok = wait(full, part ? (gv >> 1) & 1 : el & 1))) break;
+            if (lane == 0) {
+              arrive_cta(part ? &sh.ready_v[sb] : &sh.ready_s[es], 0);
+              arrive_cta(&sh.ring_empty[at], rank);
+              if (part) arrive_cta(&sh.ring_empty[at], rank ^ 1u);
+            }
+          }
+          if (part == 0) next_slot();
+        }
+        if (!more || !ok) break;
+        ++g;
+        if (++slot == kRing) {
+          slot = 0;
+          ++lap;
+        }
+      }
+    } else {
+      while (ok && walk.next(sg)) {
+        const int32_t* bt = a.pg.block_table + static_cast<size_t>(sg.row) * a.pg.max_pages;
+        const int len = seg_len<MODE>(a, sg);
+        int ahead = gload(bt + (sg.i0 >> 1));
+        if (part0 == 0) move_q();
+        for (int n = 0; n < sg.n && ok; ++n, ++g) {
+          const int i = sg.i0 + n, page = ahead, sb = g & 1;
+          if (n + 1 < sg.n) ahead = gload(bt + ((i + 1) >> 1));
+          const int nv = tile_rows(a, len, i, page);
+          if (copies) {
+            if (nv == 0 && lane == 0 && rank == 0 && part0 == 0) report(sh.faults, DEV_ERR_BAD_INDEX);
+            if (a.stop_after >= 0 && g >= static_cast<uint32_t>(a.stop_after)) {
+              ok = false;   // test hook: stop feeding the pipeline; the waits behind it run out
+              break;
+            }
+          }
+          const int part = part0;
           uint64_t* full = part ? &sh.full_v[sb] : &sh.full_s[es];
           uint8_t* st = smem + (part ? kOffV + sb * kVBytes : kOffS + es * kSBytes);
           if (copies) {
@@ -330,11 +403,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
                      : el > 0 && !(ok = wait(&sh.s_free[es], (el - 1) & 1)))
               break;
             if (lane == 0) {
-              int row = nv == 0 ? 0 : (page << kPageShift) + (i & 1) * kRows;
-              if constexpr (FP8) {
-                row = (grp * kRing + static_cast<int>(slot)) * kRows;
-                fence_proxy_async_global();    // the converters' stores, before the copies that read them
-              }
+              const int row = nv == 0 ? 0 : (page << kPageShift) + (i & 1) * kRows;
               mbar_arrive_expect_tx(full, part ? kVBytes : kSBytes);
               if (part)
                 tma_load_3d(st, &tmap_v, full, 0, row, 4 * static_cast<int>(rank));
@@ -344,7 +413,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
             __syncwarp();
           } else {
             if (!(ok = wait(full, part ? (g >> 1) & 1 : el & 1))) break;
-            if (!FP8 && part && nv < kRows) {
+            if (part && nv < kRows) {
 #pragma unroll 1
               for (int vb = 0; vb < 4; ++vb) {
 #pragma unroll 1
@@ -353,33 +422,25 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
               fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) {
-              arrive_cta(part ? &sh.ready_v[sb] : &sh.ready_s[es], 0);
-              if constexpr (FP8) {
-                arrive_cta(&sh.ring_empty[slot], rank);
-                if (part) arrive_cta(&sh.ring_empty[slot], rank ^ 1u);
-              }
-            }
+            if (lane == 0) arrive_cta(part ? &sh.ready_v[sb] : &sh.ready_s[es], 0);
           }
           if (part == 0) next_slot();
         }
-        if (++slot == kRing) {
-          slot = 0;
-          ++lap;
-        }
       }
     }
-    // let every copy this CTA started land before its shared memory can be released (one more wait than
-    // copies where the last tile's V part was not started: bounded)
+    // let every copy this CTA started land before its shared memory can be released (behind a wait that ran out
+    // one more wait than copies: bounded)
     if (copies && lane == 0) {
-      const uint32_t e = el * kSSlots + es;
+      const uint32_t e = el * kSSlots + (es + 1) % kSSlots;      // slots that were filled
       if (part0 == 0)
         for (uint32_t j = e > kSSlots ? e - kSSlots : 0; j < e; ++j) {
-          mbar_drain(&sh.full_s[j % kSSlots], (j / kSSlots) & 1, 200000000ull);
-          mbar_drain(&sh.s_free[j % kSSlots], (j / kSSlots) & 1, 200000000ull);      // (nobody else waits for these)
+          const uint32_t at = (j + kSSlots - 1) % kSSlots, parity = (j / kSSlots) & 1;
+          mbar_drain(&sh.full_s[at], parity, 200000000ull);
+          mbar_drain(&sh.s_free[at], parity, 200000000ull);      // (nobody else waits for these)
         }
       if (part1 == 2)
-        for (uint32_t j = g > 2 ? g - 2 : 0; j < g; ++j) mbar_drain(&sh.full_v[j & 1], (j >> 1) & 1, 200000000ull);
+        for (uint32_t n = ok ? 2 : 3, j = g > n ? g - n : 0; j < g; ++j)
+          mbar_drain(&sh.full_v[j & 1], (j >> 1) & 1, 200000000ull);
     }
   } else if (FP8 && warp >= C::CONV && warp < C::S_WARP) {
     // ---------------------------------------------------------------- fp8: codes -> bf16 rows in the ring
@@ -666,43 +727,50 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     constexpr uint32_t id_pv = idesc_bf16_f32(128, 256, 0, 1);
     uint32_t g = 0, it = 0;
     bool ok = true;
-    const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const bool one = elect_one();
+    const uint32_t dq = sdesc_lo(smem_u32(sQ), 16);
     while (ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
         // (start_q: the products that read the previous q have finished)
         const bool started = ok = start_q(it);
-        for (int k = 0; k < kQB && ok; k += kQPart, next_slot()) {
-          if (!(ok = wait(&sh.ready_s[es], el & 1))) break;
+        for (int k = 0; k < kQB && ok; k += kQPart) {
+          const bool first = it == 0 && k == 0;
+          ok = first ? finish_q(it) && wait(&sh.q_ready, 0) : wait(&sh.ready_s[es], el & 1);
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t dp = sdesc_sw128(smem_u32(smem + kOffS + es * kSBytes), 16, 1024);
-#pragma unroll 1
-          for (int c = 0; c < 8 * kQPart; ++c)
-            tmem_copy_pair_elect(tmem + kQCol + 32 * k + 4 * c, dp + static_cast<uint64_t>(((c >> 3) * kQBlk + (c & 7) * 16) >> 4));
-          commit_pair_elect(&sh.s_free[es]);
+          if (one) {
+            const uint64_t from = sdesc_sw128(smem_u32(smem + (first ? kOffP : kOffS + es * kSBytes)), 16, 1024);
+#pragma unroll 8
+            for (int c = 0; c < 8 * kQPart; ++c)
+              tmem_copy_pair(tmem + kQCol + 32 * k + 4 * c, from + static_cast<uint64_t>(((c >> 3) * kQBlk + (c & 7) * 16) >> 4));
+            if (!first) commit_pair(&sh.s_free[es]);
+          }
+          __syncwarp();
+          if (!first) next_slot();
         }
-        if (started) ok = finish_q(it) && ok;
-        ok = ok && wait(&sh.q_ready, it & 1);
+        if (started && it > 0) ok = finish_q(it) && ok && wait(&sh.q_ready, it & 1);
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
           if (!(ok = wait(&sh.ready_s[es], el & 1))) break;
           tc_fence_after();
-          const uint64_t dk = sdesc_sw128(smem_u32(smem + kOffS + es * kSBytes), 16, 1024);
-          // (fp8: rolled -- 36 products in line, behind the other roles' code, came out of the instruction cache
-          // too slowly for the tensor core: 1913 us where the loop takes 1473)
+          if (one) {
+            const uint32_t dk = sdesc_lo(smem_u32(smem + kOffS + es * kSBytes), 16);
+            // (bf16: in line, 376 us where loops take 439; fp8: rolled, the roles' code has to stay in the instruction caches)
 #pragma unroll FP8 ? 1 : kQB
-          for (int kb = 0; kb < kQB; ++kb)
-            umma_pair_ta_x4_elect<2>(tmem + kSCol + sb * 32, tmem + kQCol + 32 * kb,
-                                     dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
+            for (int kb = 0; kb < kQB; ++kb)
+              umma_pair_ta_x4<2>(tmem + kSCol + sb * 32, tmem + kQCol + 32 * kb, dk + ((kb * kSBlk) >> 4), id_qk, kb ? 1u : 0u);
 #pragma unroll FP8 ? 1 : kKB - kQB
-          for (int kb = kQB; kb < kKB; ++kb)
-            umma_pair_x4_elect<2, 2>(tmem + kSCol + sb * 32, dq + static_cast<uint64_t>(((kb - kQB) * kQBlk) >> 4),
-                                     dk + static_cast<uint64_t>((kb * kSBlk) >> 4), id_qk, 1u);
-          commit_pair_elect(&sh.s_full[sb]);
-          commit_pair_elect(&sh.s_free[es]);
+            for (int kb = kQB; kb < kKB; ++kb)
+              umma_pair_x4<2, 2>(tmem + kSCol + sb * 32, dq + (((kb - kQB) * kQBlk) >> 4), dk + ((kb * kSBlk) >> 4), id_qk, 1u);
+            commit_pair(&sh.s_full[sb]);
+            commit_pair(&sh.s_free[es]);
+          }
+          __syncwarp();
           next_slot();
         }
-        if (ok && walk.left > 0) commit_pair_elect(&sh.q_empty);
+        if (ok && walk.left > 0 && one) commit_pair(&sh.q_empty);
+        __syncwarp();
       } else {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           const int sb = g & 1;
@@ -710,19 +778,22 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
           if (ok && n == 0 && it > 0) ok = wait(&sh.o_free, (it - 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dp = sdesc_sw128(smem_u32(smem + kOffP + sb * kPBytes), 16, 1024);
-          const uint64_t dv = sdesc_sw128(smem_u32(smem + kOffV + sb * kVBytes), kVBlk, 1024);
+          if (one) {
+            const uint32_t dp = sdesc_lo(smem_u32(smem + kOffP + sb * kPBytes), 16);
+            const uint32_t dv = sdesc_lo(smem_u32(smem + kOffV + sb * kVBytes), kVBlk);
 #pragma unroll FP8 ? 1 : 2
-          for (int h = 0; h < 2; ++h)
-            umma_pair_x4_elect<2, 128>(tmem + h * 128, dp, dv + static_cast<uint64_t>((2 * h * kVBlk) >> 4), id_pv,
-                                       n > 0 ? 1u : 0u);
-          commit_pair_elect(&sh.o_done[sb]);
+            for (int h = 0; h < 2; ++h)
+              umma_pair_x4<2, 128>(tmem + h * 128, dp, dv + ((2 * h * kVBlk) >> 4), id_pv, n > 0 ? 1u : 0u);
+            commit_pair(&sh.o_done[sb]);
+          }
+          __syncwarp();
         }
       }
       ++it;
     }
     // every product this warp issued has completed before TMEM is released
-    commit_pair_elect(&sh.mma_done);
+    if (one) commit_pair(&sh.mma_done);
+    __syncwarp();
     mbar_drain(&sh.mma_done, 0, 200000000ull);
   }
   tc_fence_before();
