@@ -54,6 +54,25 @@
 namespace dsa {
 namespace {
 
+// Four K steps of a product, by one thread (descriptors' low words advancing by ASTEP and BSTEP 16-byte units).
+template <int ASTEP, int BSTEP>
+__device__ __forceinline__ void umma_x4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, t;\n .reg .b32 h, x1, x2, x3, y1, y2, y3;\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n mov.b32 h, %11;\n"
+      " add.s32 x1, %1, %5;\n add.s32 x2, %1, %6;\n add.s32 x3, %1, %7;\n"
+      " add.s32 y1, %2, %8;\n add.s32 y2, %2, %9;\n add.s32 y3, %2, %10;\n"
+      " mov.b64 a0, {%1, h};\n mov.b64 a1, {x1, h};\n mov.b64 a2, {x2, h};\n mov.b64 a3, {x3, h};\n"
+      " mov.b64 b0, {%2, h};\n mov.b64 b1, {y1, h};\n mov.b64 b2, {y2, h};\n mov.b64 b3, {y3, h};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %3, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(ASTEP), "n"(2 * ASTEP), "n"(3 * ASTEP), "n"(BSTEP),
+      "n"(2 * BSTEP), "n"(3 * BSTEP), "n"(kDescHi)
+      : "memory");
+}
+
 constexpr int kBlkBytes = kRows * 128;
 constexpr int kTileBytes = kKB * kBlkBytes;
 
@@ -789,7 +808,8 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait_bar(bar, parity, &sh.abort_flag, &sh.faults.bits, a.wait_ns));
     };
-    const uint64_t dq0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const bool one = elect_one();
+    const uint32_t dq0 = sdesc_lo(smem_u32(sQ), 16);
     while (ok && walk.next(sg)) {
       if (warp == C::S_WARP) {
         const int len = seg_len<MODE>(a, sg);
@@ -810,7 +830,7 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
           int nv = kRows;
           if constexpr (!FP8) nv = tile_rows(a, len, sg.i0 + n, gload(bt + ((sg.i0 + n) >> 1)));
           if (g >= 2 && !(ok = wait(&sh.s_empty[sb], ((g >> 1) - 1) & 1))) break;
-          const uint64_t da = sdesc_sw128(st0 + slot(g) * kTileBytes, 16, 1024);
+          const uint32_t da = sdesc_lo(st0 + slot(g) * kTileBytes, 16);
           const uint32_t d_s = tmem + C::S_COL + sb * HB;
 #pragma unroll
           for (int h = 0; h < 2 && ok; ++h) {
@@ -830,17 +850,20 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
               __syncwarp();
             }
             tc_fence_after();
-            // (fp8: rolled, for the instruction cache)
+            if (one) {
+              // (fp8: rolled, for the instruction cache)
 #pragma unroll FP8 ? 1 : 5
-            for (int kb = 4 * h; kb < 4 + 5 * h; ++kb)
-              umma_bf16_x4_elect<2, 2>(d_s, da + static_cast<uint64_t>((kb * kBlkBytes) >> 4),
-                                       dq0 + static_cast<uint64_t>((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
-            if constexpr (MODE == kWeights) umma_commit_elect(&sh.empty[sb][h]);      // no second product
+              for (int kb = 4 * h; kb < 4 + 5 * h; ++kb)
+                umma_x4<2, 2>(d_s, da + ((kb * kBlkBytes) >> 4), dq0 + ((kb * HB * 128) >> 4), id_qk, kb ? 1u : 0u);
+              if constexpr (MODE == kWeights) umma_commit(&sh.empty[sb][h]);      // no second product
+              if (h) umma_commit(&sh.s_full[sb]);
+            }
+            __syncwarp();
           }
           if (!ok) break;
-          umma_commit_elect(&sh.s_full[sb]);
         }
-        if (ok) umma_commit_elect(&sh.q_empty);
+        if (ok && one) umma_commit(&sh.q_empty);
+        __syncwarp();
       } else if constexpr (MODE != kWeights) {
         for (int n = 0; n < sg.n && ok; ++n, ++g) {
           ok = wait(&sh.p_full[g & 1], (g >> 1) & 1);
@@ -849,23 +872,25 @@ __global__ void __launch_bounds__(LCfg<HB, FP8, MODE == kWeights>::THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t tb = st0 + (g & 1u) * kTileBytes;
-          const uint64_t dv = sdesc_sw128(tb, kBlkBytes, 1024);
-          const uint64_t dp = sdesc_sw128(tb + (kKB - 1) * kBlkBytes, kBlkBytes, 1024);
-          const uint32_t acc0 = n > 0 ? 1u : 0u;
+          if (one) {
+            const uint32_t dv = sdesc_lo(tb, kBlkBytes), dp = sdesc_lo(tb + (kKB - 1) * kBlkBytes, kBlkBytes);
+            const uint32_t acc0 = n > 0 ? 1u : 0u;
 #pragma unroll FP8 ? 1 : 4
-          for (int b = 0; b < 4; ++b) {    // four K steps of 16 rows (2048 B)
-            umma_bf16_x4_elect<128, 128>(tmem + b * HB, dv + static_cast<uint64_t>((2 * b * kBlkBytes) >> 4), dp, id_pv,
-                                         acc0);
-            if (b == 1) umma_commit_elect(&sh.empty[g & 1][0]);
+            for (int b = 0; b < 4; ++b) {    // four K steps of 16 rows (2048 B)
+              umma_x4<128, 128>(tmem + b * HB, dv + ((2 * b * kBlkBytes) >> 4), dp, id_pv, acc0);
+              if (b == 1) umma_commit(&sh.empty[g & 1][0]);
+            }
+            umma_commit(&sh.empty[g & 1][1]);
+            umma_commit(&sh.o_done[g & 1]);
           }
-          umma_commit_elect(&sh.empty[g & 1][1]);
-          umma_commit_elect(&sh.o_done[g & 1]);
+          __syncwarp();
         }
       }
       ++it;
     }
     // every MMA this warp issued has completed before TMEM is released
-    umma_commit_elect(&sh.mma_done);
+    if (one) umma_commit(&sh.mma_done);
+    __syncwarp();
     mbar_drain(&sh.mma_done, 0, 200000000ull);
   }
   tc_fence_before();

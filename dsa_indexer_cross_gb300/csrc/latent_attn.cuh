@@ -62,6 +62,17 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+// One thread of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(one));
+  return one != 0;
+}
+// A shared-memory matrix descriptor's low word; the high word (sdesc_sw128's, SBO = 1024) is the same for all.
+constexpr uint32_t kDescHi = 0x40004040u;
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
 // x, as a value the compiler cannot carry around a loop (addresses derived from it are formed where they
 // are used instead of being held in registers).
 __device__ __forceinline__ uint32_t opaque(uint32_t x) {

@@ -139,16 +139,6 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(one));
-  return one != 0;
-}
-// A shared-memory matrix descriptor's low word; the high word (sdesc_sw128's, SBO = 1024) is the same for all.
-constexpr uint32_t kDescHi = 0x40004040u;
-__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo_bytes) {
-  return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
-}
 // Four K steps of a pair's product, by one thread.  (It is chosen once and issues a tile's products behind one branch: an
 // election before each four of them takes 376 us where this takes 348, 32 rows of 64 heads behind 100K keys.)
 template <int ASTEP, int BSTEP>
