@@ -27,11 +27,11 @@
 // cut: latent_shared_join_kernel puts them together with one softmax.  A row that is the only thing its columns
 // come from is written by the walk itself.
 //
-// What bounds it.  32 rows of 64 heads behind 100K keys, fp8, 423 us (the unshared call 663): 327 of them the staged
-// walk, 1.2 PFLOP/s, as the pair kernel reaches over a bf16 cache (latent_pair.cu); 26 staging, HBM; 24 own keys; the rest list
-// and join.  37 rows of 128 heads behind four documents, 319 us (340): 213 staged walk, 48 own keys, 27 staging.  48
-// rows of 16 heads behind 8000 keys, bf16, 41 us (60): 18 tiles a pair, some 26 us with fill and segments' ends, the list 5,
-// the join 7.  Small calls: launches and loads one behind the other, so those that gain nothing are not shared.
+// What bounds it.  32 rows of 64 heads behind 100K keys, fp8, 340 us (the unshared call 640): some 250 of them the staged
+// walk, 1.8 PFLOP/s (latent_pair.cu); 22 staging; 24 own keys; the rest list and join.  37 rows of 128 heads behind four
+// documents, 262 us (318): the staged walk, 45 own keys, 22 staging.  48 rows of 16 heads behind 8000 keys, bf16, 39 us (58): 18
+// tiles a pair, some 24 us with fill and segments' ends, the list 5, the join 7.  Small calls: launches and loads one behind
+// the other, so those that gain nothing are not shared.
 //
 // A group is walked by rows, not shared, where that takes no more items (from 128 heads on) and nothing is staged.
 #include <cuda_bf16.h>
@@ -46,23 +46,26 @@ namespace {
 // A prefix of fewer tiles than this is left to the rows.
 constexpr int kMinShared = 2;
 // What an item costs apart from its tiles, in tiles: its columns of q are loaded and its sums written while the
-// products wait.
-constexpr int kItemCost = 3;
+// products wait.  A pair takes a tile of bf16 rows in less time.  3, 4, 6, 8 tiles: 48 rows of 64 heads behind 8000 keys with
+// 50..150 of their own, bf16, 83, 76, 64, 62 us; 40 groups of 5 behind 5000..8000, 191, 166, 141, 139; the same of 16 heads, fp8,
+// 124, 126, 132, 137.
+constexpr int kItemCost = 3, kItemCostPairBf16 = 6;
 
 // Up to this many tiles of the rows' own keys go with the prefixes through the pair kernel, which a second walk's
-// launch, fill and partials cost more than: 48 rows behind 8000 keys, own tiles 266, 811, 2121, 5916: bf16, 16 heads, one
-// walk 41, 49, 70, 124 us, two 54, 61, 82, 124; fp8 57, 67, 92, 164 and 65, 73, 87, 130; fp8, 64 heads, 109, 119, 143,
-// 215 and 124, 135, 153, 210.
-constexpr int kMostOwnBf16 = 5000, kMostOwnFp8 = 1500;
+// launch, fill and partials cost more than: 48 rows behind 8000 keys, own tiles 266, 811, 2121, 5916, 22575: bf16, 16 heads,
+// one walk 36, 42, 56, 102, 305 us, two 46, 54, 72, 114, 285.  fp8 where nothing is staged: 16 rows of 16 heads, own
+// tiles 16, 802, 3231: 34, 51, 95 and 41, 50, 76; 8 rows of 64 heads, 348, 1404: 37, 70 and 37, 79.
+constexpr int kMostOwnBf16 = 12000, kMostOwnFp8 = 1500;
 
 // Calls of up to this many tiles, as the table's width allows, share nothing: listing the items and joining them costs
-// more.  Drafts of one sequence, 16 heads, bf16, rows x keys: 4 x 5000 (320 tiles) 19.7 us shared, 14.4 alone; 8 x 8000
-// (1008) 25.5 and 18.1; 16 x 8000 (2016) 26.0 and 25.5; 48 x 8000 and more (7000) 40 and 59.
+// more.  Drafts of one sequence, 16 heads, bf16, rows x keys: 4 x 5000 (320 tiles) 19.5 us shared, 13.9 alone; 8 x 8000
+// (1008) 25.0 and 17.7; 16 x 8000 (2016) 25.9 and 25.1; 48 x 8000 and more (7000) 39 and 58.
 constexpr int kAloneTiles = 2000;
 
 // Staging: prefixes of up to this many pages in all (151 MB), walked by this many blocks of columns each and more, on
 // average.  A tile costs some 0.02 us to stage, its walks 0.005 us more each where they convert.
 constexpr int kStagePages = 1024, kStageBlocks = 6, kStageTiles = 64;
+constexpr int kStageParts = 4;         // of a page, a block each
 
 struct PlanArgs {
   const int32_t* start;      // [n_groups + 1]
@@ -83,6 +86,7 @@ struct PlanArgs {
   int4* shares[3];           // [n_grp]
   int n_grp[3];
   bool pair[3];
+  int cost[3];               // what an item costs, in tiles
   uint32_t* faults;          // [2]
   int stage_pages;           // room for staged pages, 0: none
   int32_t* stage_at;         // [n_groups + 1]: first staged page of each group, then their number
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     if (g < n_groups && p.tiles[g] > 0) {
       const long long cols = static_cast<long long>(gload(p.start + g + 1) - gload(p.start + g)) * p.H;
       mine.items = static_cast<int>((cols + p.cols - 1) / p.cols);
-      mine.line = static_cast<long long>(mine.items) * (p.tiles[g] + kItemCost);
+      mine.line = static_cast<long long>(mine.items) * (p.tiles[g] + p.cost[pre_list]);
       most_tiles = max(most_tiles, p.tiles[g]);
     }
     Count total;
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     p.items[pre_list][i] = make_int4(s * p.H + b * p.cols, min(p.cols, (e - s) * p.H - b * p.cols),
                                      staged ? p.stage_at[g] : p.table[g], 0);
     p.nt[pre_list][i] = p.tiles[g];
-    p.at[pre_list][i] = p.base_at[g] + static_cast<long long>(b) * (p.tiles[g] + kItemCost);
+    p.at[pre_list][i] = p.base_at[g] + static_cast<long long>(b) * (p.tiles[g] + p.cost[pre_list]);
   }
   // the rows' own items
   const int first = n_groups > 0 ? gload(p.start) : 0, end = n_groups > 0 ? gload(p.start + n_groups) : 0;
@@ -286,7 +290,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
       most_own = max(most_own, tiles);
     }
     Count total;
-    const Count before = block_excl<kPlanThreads>(tiles > 0 ? Count{1, tiles + kItemCost} : Count{0, 0}, warp_sum, total);
+    const Count before = block_excl<kPlanThreads>(tiles > 0 ? Count{1, tiles + p.cost[list]} : Count{0, 0}, warp_sum, total);
     if (t < p.n_q) {
       if (tiles > 0) {
         const int i = own.items + before.items;
@@ -310,22 +314,23 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
   // each group's share
   for (int k = 0; k < 3; ++k) {
     if (p.n_grp[k] == 0) continue;             // no such walk
+    const int cost = p.cost[k];
     const Count c = k == list ? own : k == pre_list ? pre : Count{0, 0};
     bool by_row;
-    const int groups = share_groups<kItems>(p.n_grp[k], p.pair[k] ? 2 : 1, c.items, c.line, tallest[k] + kItemCost, by_row);
+    const int groups = share_groups<kItems>(p.n_grp[k], p.pair[k] ? 2 : 1, c.items, c.line, tallest[k] + cost, by_row);
     // Where share g begins: an item, and the tiles before it in the item and in the list.  A cut that would leave a
     // piece of one tile is moved to the item's end or beginning.
     const auto cut = [&](int g, int& i, int& tile) -> long long {
       if (g == groups) {
         i = c.items;
         tile = 0;
-        return c.line - static_cast<long long>(kItemCost) * c.items;
+        return c.line - static_cast<long long>(cost) * c.items;
       }
       const long long at = share_start(c.line, g, groups);
       i = last_not_above(p.at[k], c.items, at);
       const int nt = p.nt[k][i];
-      const long long before = p.at[k][i] - static_cast<long long>(kItemCost) * i;
-      tile = static_cast<int>(at - p.at[k][i]) - kItemCost;
+      const long long before = p.at[k][i] - static_cast<long long>(cost) * i;
+      tile = static_cast<int>(at - p.at[k][i]) - cost;
       if (tile < 2) {
         tile = 0;
       } else if (nt - tile < 2) {
@@ -354,23 +359,26 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
 }
 
 // The staged pages: codes of each group's shared tiles to bf16 rows, and the table that names them (-1: a page outside
-// the cache, which the walk reports).  A block takes a page, a warp sixteen rows, four at a time.
+// the cache, which the walk reports).  A block takes a part of a page, a warp four
+// rows of it at a time.  (Whole pages, some blocks two of them and some one: 344 us for a call that takes 340.)
 __global__ void __launch_bounds__(256) latent_stage_kernel(const LatentCache c, const PagedRows pg, const int32_t* stage_at,
                                                            const int32_t* table, int n_groups, uint16_t* rows,
                                                            int32_t* stage_table) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_trigger();
   grid_wait();
-  const int pages = gload(stage_at + n_groups);
+  const int parts = gload(stage_at + n_groups) * kStageParts;
 #pragma unroll 1
-  for (int p = blockIdx.x; p < pages; p += gridDim.x) {
+  for (int u = blockIdx.x; u < parts; u += gridDim.x) {
+    constexpr int kPartRows = kPageRows / kStageParts;
+    const int p = u / kStageParts, part = u % kStageParts;
     const int g = last_not_above(stage_at, n_groups, p), k = p - gload(stage_at + g);
     const int page = gload(pg.block_table + static_cast<size_t>(gload(table + g)) * pg.max_pages + k);
     const bool in = static_cast<uint32_t>(page) < static_cast<uint32_t>(pg.n_pages);
-    if (threadIdx.x == 0) stage_table[p] = in ? p : -1;
+    if (threadIdx.x == 0 && part == 0) stage_table[p] = in ? p : -1;
     if (!in) continue;
 #pragma unroll 1
-    for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += 4) {
+    for (int r0 = part * kPartRows + warp * 4; r0 < (part + 1) * kPartRows; r0 += 32) {
       const size_t row = (static_cast<size_t>(page) << kPageShift) + r0;
       uint4 w[4];
       uint32_t sc[4];
@@ -705,6 +713,7 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
     p.shares[k] = reinterpret_cast<int4*>(base + w.off_shares);
     p.n_grp[k] = w.n_grp;
     p.pair[k] = w.pair;
+    p.cost[k] = w.pair && (!c.fp8 || k == 2) ? kItemCostPairBf16 : kItemCost;
     LArgs& a = j.walk[k];
     a.latent = c.latent;
     a.scale = c.scale;
@@ -745,7 +754,7 @@ cudaError_t launch_latent_shared(const LatentCache& c, const CUtensorMap* tmap_k
   if (e == cudaSuccess && stage) {
     int sms = device_sm_count();
     if (sms <= 0) sms = 152;
-    e = launch_pdl(latent_stage_kernel, dim3(4 * sms), 256, 0, st, 1, c, pg, p.stage_at, p.table, p.n_groups,
+    e = launch_pdl(latent_stage_kernel, dim3(16 * sms), 256, 0, st, 1, c, pg, p.stage_at, p.table, p.n_groups,
                    reinterpret_cast<uint16_t*>(base + L.off_stage), i32(L.off_stage_table));
   }
   prof_end(ps, st);
