@@ -39,7 +39,7 @@
 // there, so S may have 128 columns, with room for one tile beside 144 KB of q.  The first product's warp frees the
 // tile's halves; four warps take sixteen keys each with every column, so a key's sum is shuffles among four lanes and
 // one store.  fp8 tiles are converted by all eight warps, each with two tiles' codes in registers (see there): 32 rows of 1K
-// to 33K keys, 64 heads, 91 us (3.8 TB/s; floor 54), 16 rows of 8K to 65K, 128 heads, 135 (floor 72).  Measured and not
+// to 33K keys, 64 heads, 88 us (3.9 TB/s; floor 54), 16 rows of 8K to 65K, 128 heads, 133 (floor 72).  Measured and not
 // kept: two blocks of 64 heads on two CTAs, whose sums a second kernel adds (240); two groups of converter warps in turn
 // (101 and 152); three groups (118 and 172, spills); sixteen warps (100 and 144); codes copied to shared memory two
 // tiles ahead, in the room of the second tile (89 at 64 heads).  No unit is full (ncu, 64 heads: L1 and shared memory 52 %,

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(PCfg<FP8>::THREADS, 1)
     // out) of each.  The first kRing tiles are spread instead, eight rows of four tiles a warp: the first
     // tile is there after one round of loads, not four (four selections of 2048: 30.8 -> 27.3 us).  The
     // loops stay rolled: the roles' code together has to stay in the instruction caches (all 32 rows
-    // unrolled: 4826 us where this takes 1473).
+    // unrolled: 4826 us where this took 1473).
     const uint32_t slot = warp - C::CONV;
     uint16_t* ring = a.ring + (static_cast<size_t>(grp * kRing) * kRows + 32 * rank) * kDqk;
     const uint32_t quarter = slot & 3, first = slot >> 2;      // spread: these rows of tiles first, first + 2, ...
