@@ -146,9 +146,10 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const __grid_
     stage_sum[0] = stage_sum[1] = stage_sum[2] = 0;
   }
   grid_wait();
-  // groups that do not lie in order within the rows, or a prefix of less than no key: none is shared
+  // groups that do not lie in order within the rows, or a prefix of less than no key: none is shared (a call without
+  // groups does not get here, and may have no arrays of them)
   bool bad = false;
-  for (int g = tid; g <= p.n_groups; g += kPlanThreads)
+  for (int g = tid; p.n_groups > 0 && g <= p.n_groups; g += kPlanThreads)
     if (group_errors(p.start, p.prefix, p.n_groups, p.n_q, g)) {
       bad = true;
       report(faults, DEV_ERR_RANGE);
@@ -645,8 +646,9 @@ Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
 }  // namespace
 
 bool latent_shared_alone(bool fp8, int n_q, int n_heads, const PagedRows& pg, const SharedRows& groups) {
-  if (!latent_attn_joins(n_q, n_heads, pg)) return false;
-  if (groups.n_groups == 0 || (n_heads == 128 && !fp8)) return true;       // nothing would be shared
+  if (groups.n_groups == 0) return true;                                   // no groups to check either
+  if (!latent_attn_joins(n_q, n_heads, pg)) return false;                  // (it is the join that checks them)
+  if (n_heads == 128 && !fp8) return true;                                 // nothing would be shared
   return 2LL * n_q * pg.max_pages <= kAloneTiles;
 }
 

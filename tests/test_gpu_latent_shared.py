@@ -322,3 +322,25 @@ def test_a_wait_that_runs_out_in_a_workspace_of_anything(H, rows, fill):
     out, lse, ws = sp.attend(q, ws=ws)
     assert D.dsa_workspace_status(ws) == 0
     assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("H", [1, 16, 64, 100, 128])
+@pytest.mark.parametrize("lens", [[100], [0], [70, 300], [128] * 40])
+def test_no_groups_need_no_arrays(lens, H, fmt):
+    """n_groups = 0 with NULL arrays, from one row of one page (one CTA, no join) on: the unshared call's results.  What
+    an array of no groups holds is not looked at."""
+    sp = SharedPaged([(0, lens, False)], fmt, seed=H, wide=False)
+    bt = sp.bt_d[:, :max(1, -(-max(lens) // P))].contiguous()
+    pages = D.paged_cache(bt, sp.len_d, sp.n_pages)
+    n = len(lens)
+    q = randn((n, H, 576), gen(5))
+    desc = D.attn_desc(n, sp.n_pages * P, H, 0, TAU)
+    want = torch.empty((n, H, 512), dtype=torch.bfloat16, device=DEV), torch.empty((n, H), device=DEV)
+    D.dsa_latent_attn_paged(desc, q, sp.cache, None, pages, *want)
+    start = i32([-1])
+    for groups in (D.SharedRows(None, None, 0, 1), D.SharedRows(None, None, 0, 1000), D.SharedRows(start.data_ptr(), None, 0, 1)):
+        out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+        ws = D.dsa_latent_attn_shared(desc, q, sp.cache, groups, pages, out, lse)
+        assert D.dsa_workspace_status(ws) == 0
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
