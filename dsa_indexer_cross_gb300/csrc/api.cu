@@ -1259,6 +1259,17 @@ dsa_status dsa_mtp_verify(const dsa_verify_desc* d, const void* target, const vo
   if (reinterpret_cast<uintptr_t>(target) % el || reinterpret_cast<uintptr_t>(draft) % el)
     return fail(DSA_ERR_ARG, "target and draft must be aligned to their elements");
   if ((s = check_device()) != DSA_OK) return s;
+  // A sequence's results are written while other warps still read its drafts.
+  const size_t n = static_cast<size_t>(d->n_seq), k = static_cast<size_t>(d->n_draft);
+  const struct { const void* p; size_t n; } arrays[] = {{tokens_out, n * (k + 1)}, {n_accepted, n}, {tokens, n * k},
+                                                       {draft_len, n}, {u_accept, n * k}, {u_sample, n}};
+  const auto meet = [&](int i, int j) {      // (elements of four bytes)
+    const uintptr_t a = reinterpret_cast<uintptr_t>(arrays[i].p), b = reinterpret_cast<uintptr_t>(arrays[j].p);
+    return a && b && arrays[i].n && arrays[j].n && a < b + 4 * arrays[j].n && b < a + 4 * arrays[i].n;
+  };
+  for (int i = 0; i < 2; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (meet(i, j)) return fail(DSA_ERR_ARG, "tokens_out and n_accepted must not overlap the inputs or each other");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // (without drafts there is no draft distribution to take off)
   const Verify a{target, d->n_draft > 0 ? draft : nullptr, tokens, draft_len, u_accept, u_sample, tokens_out, n_accepted,

@@ -662,6 +662,8 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
  *   tokens int32 [n_seq][n_draft], draft_len int32 [n_seq] (NULL: n_draft each), u_accept f32
  *   [n_seq][n_draft], u_sample f32 [n_seq]; tokens_out int32 [n_seq][n_draft + 1], n_accepted int32
  *   [n_seq].  Entries past a sequence's length are not read.  n_draft = 0: tokens and u_accept may be NULL.
+ *   tokens_out and n_accepted overlap neither an input nor each other (refused for tokens, draft_len, u_accept and
+ *   u_sample).
  * ws: at least 256 bytes.  Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_seq * (n_draft + 1) beyond int32, vocab
  * beyond 2^30), DSA_ERR_WORKSPACE, DSA_ERR_CUDA. */
 typedef struct dsa_verify_desc {

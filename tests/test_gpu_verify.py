@@ -248,3 +248,32 @@ def test_repeated_calls_are_equal():
         again = _run(c)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
     _check(c)
+
+
+def test_results_over_the_inputs_are_refused():
+    """A sequence's lengths and drafts are read by several CTAs, so the results cannot take their place."""
+    c = _case(3, 4, 9000, torch.float32, seed=2)
+    out, acc, ws = _run(c)
+    n, d = 3, 4
+    buf = torch.zeros(64, dtype=torch.int32, device=DEV)
+    f = torch.zeros(64, device=DEV)
+    base = dict(tokens=c["tokens"], draft_len=c["draft_len"], u_accept=c["u_accept"], u_sample=c["u_sample"],
+                out=torch.empty((n, d + 1), dtype=torch.int32, device=DEV), acc=torch.empty(n, dtype=torch.int32, device=DEV))
+    desc = D.verify_desc(c["target"], c["draft"])
+
+    def call(**kw):
+        a = {**base, **kw}
+        D.dsa_mtp_verify(desc, c["target"], c["draft"], a["tokens"], a["draft_len"], a["u_accept"], a["u_sample"], a["out"], a["acc"],
+                         ws=ws)
+        return a
+    for bad in (dict(acc=c["draft_len"]), dict(tokens=buf[:12], out=buf[:15]), dict(tokens=buf[14:26], out=buf[:15]),
+                dict(draft_len=buf[:3], out=buf[2:17]), dict(out=buf[:15], acc=buf[14:17]), dict(tokens=buf[:12], acc=buf[11:14]),
+                dict(u_accept=f[:12], out=f[11:26].view(torch.int32)), dict(u_sample=f[:3], acc=f[:3].view(torch.int32))):
+        with pytest.raises(D.DsaError, match="overlap"):
+            call(**bad)
+    # one behind the other in one buffer: no overlap
+    buf[:12] = c["tokens"].reshape(-1)
+    buf[12:15] = c["draft_len"]
+    a = call(tokens=buf[:12], draft_len=buf[12:15], out=buf[15:30], acc=buf[30:33])
+    assert D.dsa_workspace_status(ws) == 0
+    assert torch.equal(a["out"].view(n, d + 1), out) and torch.equal(a["acc"], acc)
