@@ -57,12 +57,21 @@ __device__ __forceinline__ void store_cta(uint32_t* p, uint32_t rank, uint32_t v
 }
 
 struct Smem {
-  uint32_t mine[kBins];              // this CTA's histogram
-  uint32_t all[kBins];               // the cluster's
-  uint32_t above[kMostCtas * kWarps], at[kMostCtas * kWarps];      // of each warp of the cluster
+  // This CTA's histogram; behind the last pass, where nobody reads it any more, the keys above and at the limit of each
+  // warp of the cluster.  (Beside each other, two CTAs that hold their keys in shared memory did not fit on an SM.)
+  union {
+    uint32_t mine[kBins];
+    struct {
+      uint32_t above[kMostCtas * kWarps], at[kMostCtas * kWarps];
+    };
+  };
+  uint32_t all[kBins];               // the cluster's histogram
   uint32_t warp_sum[kWarps];
   uint32_t bin, before, count;       // the limit's bin, the entries above it and its own
 };
+constexpr int kSharedBytes = kThreads * kSharedHeld * static_cast<int>(sizeof(float));
+// Two CTAs an SM, as the launch counts them: 228 KB, of which each CTA takes 1 KB more than it asks for, in steps of 128 B.
+static_assert(2 * ((sizeof(Smem) + kSharedBytes + 1024 + 127) / 128 * 128) <= 228 * 1024, "two CTAs an SM");
 
 // Inclusive sum over the lanes.
 __device__ __forceinline__ uint32_t warp_incl(uint32_t x) {
@@ -326,9 +335,8 @@ cudaError_t launch_evict(const Evict& a, const LatentCache& src, const LatentCac
   if (run <= 32 * kHeld) {
     e = launch_pdl(evict_select_kernel<kRegisters>, grid, kThreads, 0, st, ctas, a, ctas, status);
   } else if (run <= 32 * kSharedHeld) {
-    constexpr int kBytes = kThreads * kSharedHeld * static_cast<int>(sizeof(float));
-    if ((e = smem_attr_once<evict_select_kernel<kShared>>(kBytes)) != cudaSuccess) return e;
-    e = launch_pdl(evict_select_kernel<kShared>, grid, kThreads, kBytes, st, ctas, a, ctas, status);
+    if ((e = smem_attr_once<evict_select_kernel<kShared>>(kSharedBytes)) != cudaSuccess) return e;
+    e = launch_pdl(evict_select_kernel<kShared>, grid, kThreads, kSharedBytes, st, ctas, a, ctas, status);
   } else {
     e = launch_pdl(evict_select_kernel<kNowhere>, grid, kThreads, 0, st, ctas, a, ctas, status);
   }

@@ -127,6 +127,20 @@ def test_long_and_many_sequences(lens, keep, kind):
     _verify(pc, w, keep, first, last, to, kept, w_out)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+@pytest.mark.parametrize("lens,keep", [([65000, 48000, 30000, 6145, 6144] + list(range(500, 543)), 2048),       # clusters of six
+                                       ([24576, 24575, 5] + [3000] * 149, 1000), ([49152, 49000] + [700] * 98, 4000)])    # of two, of three
+def test_keys_held_in_shared_memory(lens, keep, kind):
+    """Tables so wide, and so many sequences, that a CTA holds its keys in shared memory (up to the most it can)."""
+    pc = Paged(lens, "fp8", seed=len(lens))
+    w = _weights(pc, 6, kind)
+    to, kept, w_out, ws = _evict(pc, w, keep, 4, 64)
+    assert D.dsa_workspace_status(ws) == 0
+    _verify(pc, w, keep, 4, 64, to, kept, w_out)
+    again = _evict(pc, w, keep, 4, 64)
+    assert torch.equal(kept, again[1])
+
+
 def test_strided_weights_and_no_weights_out():
     pc = Paged([900, 300], "bf16", seed=1)
     wide = torch.full((2, pc.bt.shape[1] * P + 5), float("inf"), device=DEV)
