@@ -325,21 +325,28 @@ cudaError_t launch_evict(const Evict& a, const LatentCache& src, const LatentCac
   cudaError_t e;
   int sms = device_sm_count();
   if (sms <= 0) sms = 152;
-  // as many CTAs as hold the longest sequence that the table allows in registers, while all are resident at once
+  // As many CTAs a sequence as hold the longest that the table allows in registers, while all sequences are resident at
+  // once; fewer for that only where their keys are held as before (60000 .. 65536 keys cut to 2048, fp8: 40 sequences,
+  // clusters of seven 64.6 us, of six 54.4; 48, of six 72.9, of five 63.6; 100, of three 122, of two, which hold
+  // nothing, 157).
   const int width = a.from.max_pages * kPageRows;
   const int fit = 2 * sms / std::max(1, std::min(a.n_seq, 2 * sms));
-  const int ctas = std::max(1, std::min({kMostCtas, fit, (width + kHeld * kThreads - 1) / (kHeld * kThreads)}));
-  const dim3 grid(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(ctas));
-  // (a warp's run is the CTA's sixteenth, rounded up)
-  const long long run = (static_cast<long long>(width) + ctas * kWarps - 1) / (ctas * kWarps);
-  if (run <= 32 * kHeld) {
-    e = launch_pdl(evict_select_kernel<kRegisters>, grid, kThreads, 0, st, ctas, a, ctas, status);
-  } else if (run <= 32 * kSharedHeld) {
-    if ((e = smem_attr_once<evict_select_kernel<kShared>>(kSharedBytes)) != cudaSuccess) return e;
-    e = launch_pdl(evict_select_kernel<kShared>, grid, kThreads, kSharedBytes, st, ctas, a, ctas, status);
-  } else {
-    e = launch_pdl(evict_select_kernel<kNowhere>, grid, kThreads, 0, st, ctas, a, ctas, status);
-  }
+  int ctas = std::max(1, std::min({kMostCtas, fit, (width + kHeld * kThreads - 1) / (kHeld * kThreads)}));
+  const auto form = [&](int n) -> Hold {       // (a warp's run is the CTA's sixteenth, rounded up)
+    const long long run = (static_cast<long long>(width) + n * kWarps - 1) / (n * kWarps);
+    return run <= 32 * kHeld ? kRegisters : run <= 32 * kSharedHeld ? kShared : kNowhere;
+  };
+  const Hold hold = form(ctas);
+  if (hold == kShared && (e = smem_attr_once<evict_select_kernel<kShared>>(kSharedBytes)) != cudaSuccess) return e;
+  const auto select = [&](auto kern, int smem) {
+    constexpr auto k = decltype(kern)::value;
+    while (ctas > 1 && form(ctas - 1) == hold && resident_clusters<k>(ctas, kThreads, smem) < a.n_seq) --ctas;
+    const dim3 grid(static_cast<unsigned>(a.n_seq) * static_cast<unsigned>(ctas));
+    return launch_pdl(k, grid, kThreads, static_cast<size_t>(smem), st, ctas, a, ctas, status);
+  };
+  e = hold == kRegisters ? select(Kernel<evict_select_kernel<kRegisters>>{}, 0)
+      : hold == kShared  ? select(Kernel<evict_select_kernel<kShared>>{}, kSharedBytes)
+                         : select(Kernel<evict_select_kernel<kNowhere>>{}, 0);
   if (e != cudaSuccess) return e;
   const int rows = std::min(a.n_keep, width);
   const int each = static_cast<long long>(a.n_seq) * rows > 64LL * sms ? 8 : 2;

@@ -1,6 +1,8 @@
 // Internal launch interface between the C-ABI layer (api.cu) and the kernels.
 #pragma once
 
+#include <atomic>
+#include <climits>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -20,6 +22,40 @@ inline cudaError_t smem_attr_once(int bytes) {
   e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
+}
+
+template <auto K>
+struct Kernel {              // a kernel as an argument, where it has to be a constant
+  static constexpr auto value = K;
+};
+// Clusters of `cluster` <= 8 CTAs of Kern that are resident at once, as the device says: fewer than the SMs' room, as a
+// cluster's CTAs lie in one group of SMs (two 512-thread CTAs an SM, 304 in all: 97 clusters of three, 46 of six, 36 of
+// eight).  Asked once per device and size; no bound where it cannot be told.
+template <auto Kern>
+inline int resident_clusters(int cluster, int threads, int smem) {
+  static std::atomic<int> known[64][9];        // 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return INT_MAX;
+  int n = known[dev][cluster].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(cluster);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, Kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = INT_MAX;
+    }
+    n = n > 0 ? n : 1;
+    known[dev][cluster].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 // Layout of the 256-byte header at the start of every workspace.

@@ -436,14 +436,20 @@ cudaError_t launch_t(const Verify& a, uint32_t* status, cudaStream_t st) {
   const bool sole = static_cast<long long>(a.n_seq) * n <= kSoleMost;
   const cudaError_t e = sole ? cudaSuccess : clear_status(status, st);
   if (e != cudaSuccess) return e;
+  // As many CTAs a sequence as leave all sequences resident at once, so that none waits for another's chain of loads
+  // (131072 values, fp32: 40 sequences, clusters of seven 25.8 us, of six 19.6; 64, of four 23.7, of five 29.8; 100, of
+  // three 37.0, of two 31.9), and 4096 values or more each.
   int sms = device_sm_count();
   if (sms <= 0) sms = 152;
-  // As many CTAs as are resident at once (two an SM), so that no sequence waits for another's chain of loads:
-  // 64 sequences of 131072, 256 CTAs, 15.8 us, 512 20.5; 32 of 32000 9.2 with 8 each, 8.6 with 4.
-  const int ctas = std::max(1, std::min({kMostCtas, 2 * sms / std::max(1, std::min(a.n_seq, 2 * sms)), (a.vocab + 4095) / 4096}));
-  const unsigned grid = (static_cast<unsigned>(a.n_seq) + (sole ? 1u : 0u)) * static_cast<unsigned>(ctas);
-  return launch_pdl(a.draft ? verify_kernel<T, true> : verify_kernel<T, false>, dim3(grid), kThreads, 0, st, ctas, a, ctas,
-                    sole ? a.n_seq * n : 0, status);
+  const int fit = 2 * sms / std::max(1, std::min(a.n_seq, 2 * sms));
+  int ctas = std::max(1, std::min({kMostCtas, fit, (a.vocab + 4095) / 4096}));
+  const auto go = [&](auto kern) {
+    constexpr auto k = decltype(kern)::value;
+    while (ctas > 1 && resident_clusters<k>(ctas, kThreads, 0) < a.n_seq) --ctas;
+    const unsigned grid = (static_cast<unsigned>(a.n_seq) + (sole ? 1u : 0u)) * static_cast<unsigned>(ctas);
+    return launch_pdl(k, dim3(grid), kThreads, 0, st, ctas, a, ctas, sole ? a.n_seq * n : 0, status);
+  };
+  return a.draft ? go(Kernel<verify_kernel<T, true>>{}) : go(Kernel<verify_kernel<T, false>>{});
 }
 
 }  // namespace

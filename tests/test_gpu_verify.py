@@ -83,6 +83,12 @@ def test_sequences_and_drafts(n, d):
     _check(_case(n, d, 1500, torch.float32, d > 0, seed=n + d))
 
 
+@pytest.mark.parametrize("n", [36, 37, 39, 43, 47, 58, 59, 75, 97, 98, 152, 153, 305])
+def test_every_size_of_cluster(n):
+    """Numbers of sequences around those that leave room for another CTA each."""
+    _check(_case(n, 2, 33001, torch.float32, n % 2 == 0, seed=n))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (3, 3), (8, 2), (16, 0), (5, 7)])
 def test_strides_and_alignment(pad, offset, dtype):
