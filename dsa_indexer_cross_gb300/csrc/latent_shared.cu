@@ -33,7 +33,8 @@
 // tiles a pair, some 24 us with fill and segments' ends, the list 5, the join 7.  Small calls: launches and loads one behind
 // the other, so those that gain nothing are not shared.
 //
-// A group is walked by rows, not shared, where that takes no more items (from 128 heads on) and nothing is staged.
+// A group is walked by rows, not shared, where that takes no more items (128 heads, or few rows of more than 64) and
+// nothing is staged; calls that can have no other group run the unshared kernels, as those too small to gain do.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -585,6 +586,8 @@ struct Layout {
   size_t off_tiles, off_table, off_base, off_base_at, off_rows, off_faults, off_whole_m, off_whole_o, off_stage_at, off_stage_table,
       off_stage, total;
 };
+// Whether an fp8 cache's prefixes of groups of that many columns may have enough blocks to be staged.
+bool may_stage(long long group_cols) { return group_cols > (kStageBlocks - 1) * 128; }
 Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
   Layout L{};
   int sms = device_sm_count();
@@ -596,7 +599,7 @@ Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
   L.walk[0].cols = pair ? 128 : head_block(static_cast<int>(group_cols));
   L.walk[1].used = pair && n_heads <= 64;
   L.walk[1].cols = head_block(std::min(n_heads, 64));
-  L.walk[2].used = n_groups > 0 && group_cols > (kStageBlocks - 1) * 128;
+  L.walk[2].used = n_groups > 0 && may_stage(group_cols);
   L.walk[2].pair = true;
   L.walk[2].cols = 128;
   const long long all = static_cast<long long>(n_q) * n_heads, pre = all / L.walk[0].cols + n_groups;
@@ -648,7 +651,11 @@ Layout shared_layout(int n_q, int n_heads, int n_groups, int max_rows) {
 bool latent_shared_alone(bool fp8, int n_q, int n_heads, const PagedRows& pg, const SharedRows& groups) {
   if (groups.n_groups == 0) return true;                                   // no groups to check either
   if (!latent_attn_joins(n_q, n_heads, pg)) return false;                  // (it is the join that checks them)
-  if (n_heads == 128 && !fp8) return true;                                 // nothing would be shared
+  // A group of m rows is walked by rows where its columns fill as many blocks of 128: from 65 heads on, up to that many
+  // rows.  Then only staged prefixes are worth a list.  (128 heads, fp8, with a list that shares
+  // nothing and without, us: 32 sequences of five rows and 8000 keys 421, 413; 512 of 1000 keys 1103, 941.)
+  const long long m = std::max(1, std::min(groups.max_rows, n_q));
+  if (n_heads > 64 && m * (128 - n_heads) < 128 && !(fp8 && may_stage(m * n_heads))) return true;
   return 2LL * n_q * pg.max_pages <= kAloneTiles;
 }
 

@@ -539,8 +539,9 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
  * for all of their heads.  Rows [group_start[g], group_start[g + 1]) share their first prefix_len[g] keys:
  * their block_table rows name the same pages for these keys, as far as each row has them.  Other rows, and
  * rows shorter than the prefix (a padded batch's empty ones), attend by themselves, as all do in calls too small
- * to gain from sharing (n_q * max_pages up to 1000; 128 heads of a bf16 cache); the walk takes
- * whole tiles of 64 keys of the prefix, the rows their rest.
+ * to gain from sharing (n_q * max_pages up to 1000) and in those whose groups fill as many blocks of 128 columns as
+ * they have rows (n_heads > 64 and max_rows * (128 - n_heads) < 128; over an fp8 cache only while max_rows * n_heads
+ * <= 640).  The walk takes whole tiles of 64 keys of the prefix, the rows their rest.
  *   group_start int32 [n_groups + 1], ascending within [0, n_q]; prefix_len int32 [n_groups], >= 0, cut to
  *   the second longest row (groups that break this are flagged and none is shared; the results are the same).  Device memory, n_groups = 0: may be NULL.  max_rows: rows of the largest
  *   group, or about (it chooses the kernels and the workspace; any value >= 1 gives right results).

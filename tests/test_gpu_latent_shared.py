@@ -344,3 +344,33 @@ def test_no_groups_need_no_arrays(lens, H, fmt):
         ws = D.dsa_latent_attn_shared(desc, q, sp.cache, groups, pages, out, lse)
         assert D.dsa_workspace_status(ws) == 0
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("H,rows,fmt,lists", [(128, 5, "fp8", False), (128, 1, "fp8", False), (128, 9, "bf16", False), (100, 4, "fp8", False),
+                                              (100, 4, "bf16", False), (65, 2, "bf16", False), (65, 3, "bf16", True), (126, 63, "bf16", False), (128, 6, "fp8", True),
+                                              (100, 5, "fp8", True), (100, 5, "bf16", True), (64, 2, "fp8", True)])
+def test_calls_that_cannot_share_run_the_unshared_kernels(H, rows, fmt, lists):
+    """Where a group's rows fill as many blocks of columns as there are rows (2 x 65 columns: two of 128; 3 x 65: two), no
+    list is made (the launch log shows it), the results are the unshared call's and the groups are checked all the same."""
+    sp = SharedPaged([(700, [701 + i for i in range(rows)], True)] * 4 + [(0, [900], False)], fmt, seed=H + rows)
+    n = len(sp.lens)
+    q = randn((n, H, 576), gen(3))
+    ref = sp.attend(q)
+    assert D.dsa_workspace_status(ref[2]) == 0
+    D.dsa_profile_enable(True)
+    try:
+        out, lse, ws = sp.attend(q)
+        kinds = [k for k, _ in D.dsa_profile_read()]
+    finally:
+        D.dsa_profile_enable(False)
+    assert kinds == ["attn_prep"] * lists + ["attn"]
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    check_rows(out, lse, q, [sp.stored(t) if t % 5 == 0 or t == n - 1 else None for t in range(n)])
+    if not lists:
+        o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+        D.dsa_latent_attn_paged(D.attn_desc(n, sp.n_pages * P, H, 0, TAU), q, sp.cache, None, sp.pages, o2, l2)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    for kw in (dict(start=i32(sp.start[:-1] + [n + 1])), dict(prefix=i32(sp.prefix[:-1] + [-1]))):
+        o3, l3, ws = sp.attend(q, **kw)
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+        check_rows(o3, l3, q, [sp.stored(t) if t == 0 else None for t in range(n)])
