@@ -254,9 +254,10 @@ __device__ __forceinline__ int columns(const Seg& s) {
 
 // Error bits of entry g of n_groups groups of rows, g <= n_groups: starts ascending within [0, n_q], no prefix below 0.
 __device__ __forceinline__ uint32_t group_errors(const int32_t* start, const int32_t* prefix, int n_groups, int n_q, int g) {
-  const int s = gload(start + g);
-  const bool order = s < 0 || s > n_q || (g < n_groups && gload(start + g + 1) < s);
-  return order || (g < n_groups && gload(prefix + g) < 0) ? DEV_ERR_RANGE : 0u;
+  // (the loads side by side)
+  const bool last = g == n_groups;
+  const int s = gload(start + g), next = last ? s : gload(start + g + 1), len = last ? 0 : gload(prefix + g);
+  return s < 0 || s > n_q || next < s || len < 0 ? DEV_ERR_RANGE : 0u;
 }
 
 // Faults are collected per CTA; the CTAs' words are put together by the join kernel (or, when
@@ -308,7 +309,7 @@ __device__ __forceinline__ long long find_share(const LArgs& a, int grp, bool wr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long share = 0;
   int groups;
-    if (a.n_q <= 32) {
+  if (a.n_q <= 32) {
     // A row a lane, each warp for itself: no barrier, no trip through shared memory (300 keys, 16 heads: 11.6 ->
     // 10.8 us).
     const int T = lane < a.n_q ? row_tiles<MODE>(a, lane) : 0;

@@ -374,3 +374,29 @@ def test_calls_that_cannot_share_run_the_unshared_kernels(H, rows, fmt, lists):
         o3, l3, ws = sp.attend(q, **kw)
         assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
         check_rows(o3, l3, q, [sp.stored(t) if t == 0 else None for t in range(n)])
+
+
+@pytest.mark.parametrize("at", [0, 1, 31, 32, 255, 256, 1023, 1024, 2999, 3000])
+@pytest.mark.parametrize("H,fmt", [(128, "bf16"), (8, "bf16")])
+def test_every_one_of_many_groups_is_checked(H, fmt, at):
+    """3000 groups, most of them empty, of a call that shares nothing (and of one that lists them): a fault in any."""
+    sp = SharedPaged([(200, [210, 220], False), (0, [5], False)], fmt, seed=4)
+    n = 3
+    q = randn((n, H, 576), gen(3))
+    start = np.full(3001, 2, dtype=np.int32)
+    start[0], start[3000] = 0, 3
+    prefix = np.full(3000, 100, dtype=np.int32)
+    out, lse, ws = sp.attend(q, start=i32(start), prefix=i32(prefix))
+    assert D.dsa_workspace_status(ws) == 0
+    check_rows(out, lse, q, [sp.stored(t) for t in range(n)])
+    bad = start.copy()
+    bad[at] = 4 if at else -1          # past the rows, or before them
+    o2, l2, ws = sp.attend(q, start=i32(bad), prefix=i32(prefix))
+    assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+    check_rows(o2, l2, q, [sp.stored(t) for t in range(n)])
+    if at < 3000:
+        bad = prefix.copy()
+        bad[at] = -1
+        o2, l2, ws = sp.attend(q, start=i32(start), prefix=i32(bad))
+        assert D.dsa_workspace_status(ws, raise_on_fault=False) == 8
+        check_rows(o2, l2, q, [sp.stored(t) for t in range(n)])
