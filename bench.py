@@ -221,7 +221,7 @@ def roofline_numbers(w, geo):
 # launch is too long for a full-set capture) and is scaled by the 4096 / 608 units: each
 # group streams the same chunks, so the traffic grows with the number of groups.
 MEASURED_TRAFFIC = {
-    ("indexer", "chunk_1m"): ((1.032666e9 + 0.618700e9) * 4096 / 608, ("indexer.cu", "api.cu"), "0e65661c4d17dfbc",
+    ("indexer", "chunk_1m"): ((1.032536e9 + 0.618336e9) * 4096 / 608, ("indexer.cu", "api.cu"), "372926a39c94a285",
                               "profiles/indexer_chunk_1m.md (608-query slice, scaled by 4096/608)"),
 }
 

@@ -549,7 +549,9 @@ dsa_status dsa_latent_attn_paged(const dsa_attn_desc* desc, const void* q, const
  * them, else none).
  * ws: dsa_latent_attn_shared_workspace_size bytes: 4 KB for each row and head, some 100 bytes for each row and group,
  * and up to 40 MB where a group's rows and heads are up to 64, 130 MB up to 640 of them, 320 MB beyond.  The size
- * depends on n_groups and max_rows too.  Everything else as dsa_latent_attn_paged.
+ * depends on n_groups and max_rows too, not on the cache's format: it is what an fp8 cache needs (a call over a bf16
+ * cache leaves 45 MB of it untouched from 65 rows and heads on, 190 MB more beyond 640).  Everything else as
+ * dsa_latent_attn_paged.
  * Errors: those of dsa_latent_attn_paged, DSA_ERR_ARG (the groups), DSA_ERR_SHAPE (n_groups beyond 2^24). */
 typedef struct dsa_shared_rows {
   const int32_t* group_start;
@@ -568,7 +570,8 @@ dsa_status dsa_latent_attn_shared(const dsa_attn_desc* desc, const void* q, cons
  *   weight_out[t][j] = weight_in[t][j] + sum_h exp(tau q[t, h] . kv_j - lse[t, h])        j < seq_len[t]
  * with the log-sum-exp that the attention of these rows gave (dsa_latent_attn_paged over every key, or
  * dsa_latent_attn_shared; over selected keys the others' weights are what they would have been).  Scores and sums in fp32.
- * A head whose lse is -inf (no key) weighs nothing.  A NaN score or lse makes the key's weight NaN.
+ * A head whose lse is -inf (no key) weighs nothing.  A NaN score or lse makes the key's weight NaN.  Rows of one
+ * sequence (its drafts) each have a row of weights of their own; adding those that count is left to the caller.
  *   lse f32 [n_q][n_heads]; weight_in, weight_out f32 rows weight_stride >= max_pages * page_rows elements
  *   apart; weight_in NULL: zeros; it may be weight_out (in place), otherwise the two do not overlap.
  * Elements of weight_out behind a sequence's keys, and those of keys on a page outside the cache (flagged), stay
@@ -594,6 +597,9 @@ dsa_status dsa_latent_key_weights(const dsa_attn_desc* desc, const void* q, cons
  *   another sequence of to_pages (the rows of such a page become a mixture).  to_pages needs room for what may
  *   stay: the smaller of n_keep and from_pages' max_pages * page_rows.  Rows of `to` that nothing is copied to
  *   stay as they were.  Rotary dims are copied as they are: keys keep the positions they were turned at.
+ *   kept, new_len and weight_out overlap neither an input (but to_pages' seq_len) nor each other.
+ * Only the latent cache's rows move.  An indexer's paged key cache (dsa_indexer_topk_paged) goes by the same positions:
+ * where it is used after an eviction, the caller moves its rows by kept.
  * A length outside [0, max_pages * page_rows] is cut to it and flagged; a row from or to a page outside its
  * cache is not copied and flagged (DSA_ERR_DEVICE).  ws: dsa_latent_cache_evict_workspace_size bytes (256).
  * Errors: DSA_ERR_ARG, DSA_ERR_SHAPE (n_rows != n_pages * page_rows; no room in to_pages; max_pages * page_rows or
@@ -649,8 +655,8 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
  * tokens_out[t] = x_0 .. x_{a-1}, y, then -1 up to n_draft + 1; n_accepted[t] = a.  For u uniform on
  * [0, 1) and x_i drawn from q_i, the tokens follow the target's distribution.  draft NULL: drafts without
  * probabilities (looked up, or a greedy draft): q_i is one at x_i, zero elsewhere.
- * The products are compared exactly; the sums and u_sample times the last are good to some 2^-45
- *, in an order that does not change from call to call.  Only the rows p_a and q_a are read whole.
+ * The products are compared exactly; the sums and u_sample times the last are good to some 2^-45,
+ * in an order that does not change from call to call.  Only the rows p_a and q_a are read whole.
  * Where r has no weight (q_a covers p_a), y is drawn from p_a instead; where that has none either, or a
  * sum is infinite, y = -1.  A NaN or negative difference weighs nothing; a u_sample outside [0, 1)
  * draws the first or the last token of any weight (NaN: the first).
@@ -659,7 +665,8 @@ dsa_status dsa_mtp_indexshare_step(const dsa_indexer_desc* idx_desc, const dsa_a
  * (DSA_ERR_DEVICE).
  *   target [n_seq][n_draft + 1] rows of vocab probabilities, target_stride elements apart; draft
  *   [n_seq][n_draft] rows, draft_stride apart; both of dtype, finite and >= 0, aligned to their elements
- *   (rows on 16-byte boundaries, or target and draft rows equally far behind one, are read in vectors).
+ *   (the draft's rows are read in vectors where they lie as far behind a 16-byte boundary as the target's, else by
+ *   elements: an odd vocabulary's, 64 sequences of 50257, take up to 10 % longer).
  *   tokens int32 [n_seq][n_draft], draft_len int32 [n_seq] (NULL: n_draft each), u_accept f32
  *   [n_seq][n_draft], u_sample f32 [n_seq]; tokens_out int32 [n_seq][n_draft + 1], n_accepted int32
  *   [n_seq].  Entries past a sequence's length are not read.  n_draft = 0: tokens and u_accept may be NULL.
