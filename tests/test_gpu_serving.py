@@ -214,3 +214,48 @@ def test_the_launch_log_names_the_calls(lens, shares):
     # (a small call shares nothing, and lists nothing)
     assert kinds == ["cache"] + ["attn_prep"] * shares + ["attn", "attn", "verify"]
     assert all(torch.equal(a, b) for a, b in zip(s.state(), want))
+
+
+FIRST = """
+import threading, torch
+import dsa_indexer_cross_gb300 as D
+dev = "cuda"
+torch.manual_seed(0)
+n, V, L, keep = 40, 40000, 40000, 300
+t, q = torch.softmax(torch.randn(n, 3, V, device=dev), -1), torch.softmax(torch.randn(n, 2, V, device=dev), -1)
+x = torch.randint(0, V, (n, 2), dtype=torch.int32, device=dev)
+u, us = torch.rand(n, 2, device=dev), torch.rand(n, device=dev)
+pages = (L + 127) // 128
+rows = torch.randn(64 * 128, 576, device=dev).bfloat16()
+bt = torch.randint(0, 8, (n, pages), dtype=torch.int32, device=dev)
+lens = torch.randint(1000, L, (n,), dtype=torch.int32, device=dev)
+w = torch.rand(n, pages * 128, device=dev)
+def outs():
+    dst = torch.zeros(n * 3 * 128, 576, device=dev).bfloat16()
+    return dict(out=torch.zeros(n, 3, dtype=torch.int32, device=dev), acc=torch.zeros(n, dtype=torch.int32, device=dev),
+                kept=torch.zeros(n, keep, dtype=torch.int32, device=dev), new=torch.zeros(n, dtype=torch.int32, device=dev), dst=dst,
+                to=torch.arange(n * 3, dtype=torch.int32, device=dev).view(n, 3), ws=torch.zeros(512, dtype=torch.uint8, device=dev))
+def run(o, stream=None):
+    D.dsa_mtp_verify(D.verify_desc(t, q), t, q, x, None, u, us, o["out"], o["acc"], ws=o["ws"][:256], stream=stream)
+    D.dsa_latent_cache_evict(D.evict_desc(n, keep, 4, 16), D.latent_cache(rows), D.paged_cache(bt, lens, 64), w, D.latent_cache(o["dst"]),
+                             D.paged_cache(o["to"], o["new"], n * 3), o["kept"], None, o["new"], ws=o["ws"][256:], stream=stream)
+def same(a, b):
+    return all(torch.equal(a[k], b[k]) for k in ("out", "acc", "kept", "new", "dst"))
+first, many = outs(), [outs() for _ in range(4)]
+torch.cuda.synchronize()
+"""
+
+
+@pytest.mark.parametrize("how", [
+    "g = torch.cuda.CUDAGraph()\nwith torch.cuda.graph(g):\n    run(first)\ng.replay()\n",
+    "ts = [threading.Thread(target=lambda o=o: [run(o, torch.cuda.Stream()) for _ in range(20)]) for o in many]\n"
+    "[x.start() for x in ts]\n[x.join() for x in ts]\ntorch.cuda.synchronize()\nrun(first)\nassert all(same(first, o) for o in many)\n"])
+def test_a_process_first_calls(how):
+    """What a call finds out about the device at its first use: while a graph is captured, and by four threads at once."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    check = "torch.cuda.synchronize()\nagain = outs()\nrun(again)\nassert same(first, again) and int(again['new'].min()) == 300\nprint('same')\n"
+    r = subprocess.run([sys.executable, "-c", FIRST + how + check], capture_output=True, text=True, timeout=300,
+                       cwd=Path(__file__).resolve().parent.parent)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
